@@ -1,0 +1,81 @@
+/*
+ * atlas_linear.h -- C ABI of the matrix product with bias, activation and
+ * residual in its epilogue: the output projection behind the memory, and both
+ * halves of a feed-forward block.
+ *
+ * The operation, row-major:
+ *
+ *   y = act(x W + bias) + residual      x [M][K], W [K][N], y [M][N]
+ *
+ * Sums, the bias, the activation and the residual's addition are fp32; y is
+ * rounded once.  W has the orientation of atlas_prologue.h's W_in.
+ *
+ * Execution: asynchronous on the given CUDA stream.  bf16 inputs: exact
+ * products, fp32 accumulation.  fp32 inputs: fp32 accuracy.  A handle is not
+ * re-entrant: do not call it from two threads or on two streams at once.
+ *
+ * Errors: the status codes of atlas_mem.h; atlas_linear_last_error gives the
+ * message.  Validation failures return before any CUDA call.
+ */
+#ifndef ATLAS_LINEAR_H
+#define ATLAS_LINEAR_H
+
+#include <stddef.h>
+
+#include "atlas_mem.h"
+#include "atlas_norm.h"   /* ATLAS_ACT_* */
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+typedef struct {
+    int K, N;         /* 1 .. 2^20 */
+    int act;          /* ATLAS_ACT_* */
+    int in_dtype;     /* ATLAS_F32 or ATLAS_BF16: type of x and W */
+    int out_dtype;    /* ATLAS_F32 or ATLAS_BF16: type of residual and y */
+} atlas_linear_config;
+
+typedef struct atlas_linear_handle atlas_linear_handle;
+
+/* Tensors of one call, all DEVICE pointers owned by the caller. */
+typedef struct {
+    int M;                 /* rows, M >= 1 */
+    const void* x;         /* [M][K] in_dtype */
+    const void* W;         /* [K][N] in_dtype */
+    const float* bias;     /* [N]; NULL: 0 */
+    const void* residual;  /* [M][N] out_dtype; NULL: 0 */
+    void* y;               /* [M][N] out_dtype; may be residual itself, not x or W */
+} atlas_linear_io;
+
+/* Validate the config and make a handle (no CUDA call).  INVALID_ARG or
+ * UNSUPPORTED with a message from atlas_linear_last_error(NULL). */
+int atlas_linear_create(const atlas_linear_config* cfg, atlas_linear_handle** out);
+
+/* One call; stream is a cudaStream_t (NULL = the default stream).  Grows the
+ * handle's workspace to atlas_linear_workspace_bytes on first use (cudaMalloc). */
+int atlas_linear_forward(atlas_linear_handle* h, const atlas_linear_io* io, void* stream);
+
+/* Device workspace a call of this size may need. */
+size_t atlas_linear_workspace_bytes(const atlas_linear_handle* h, int M);
+
+/* Wait for the last forward on h and return its device status: ATLAS_OK, or
+ * ATLAS_ERR_TIMEOUT if a bounded wait of the tensor-core kernel gave up (its
+ * outputs are then not valid).  Clears the status word. */
+int atlas_linear_status(atlas_linear_handle* h);
+
+/* How the last forward on h ran: 0 = fp32 tiles, 1 = tensor cores, 2 = few
+ * rows, -1 = none yet. */
+int atlas_linear_last_path(const atlas_linear_handle* h);
+
+/* Message of the last failure on h, or of the last failed create when h is NULL. */
+const char* atlas_linear_last_error(const atlas_linear_handle* h);
+
+/* Free the handle and its workspace (NULL is a no-op). */
+void atlas_linear_destroy(atlas_linear_handle* h);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif

@@ -17,3 +17,4 @@ from .atlas_oracle import (  # noqa: F401
     unit_inputs,
 )
 from .prologue import prologue_row  # noqa: F401,E402
+from . import layer  # noqa: F401,E402

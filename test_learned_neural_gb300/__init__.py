@@ -21,13 +21,24 @@ ATLAS_NS_MOMENTUM, ATLAS_NS_SURPRISE = 0, 1
 ATLAS_UPDATE_PER_TOKEN, ATLAS_UPDATE_CHUNKWISE = 0, 1
 STATUS_NAMES = {0: "OK", 1: "INVALID_ARG", 2: "UNSUPPORTED", 3: "CUDA", 4: "OOM", 5: "TIMEOUT"}
 
-# exported symbols, as declared in include/atlas_mem.h and include/atlas_prologue.h
+ATLAS_LAYOUT_HEADS, ATLAS_LAYOUT_TOKENS = 0, 1
+ATLAS_NORM_CHANNELS_LAST, ATLAS_NORM_HEADS = 0, 1
+ATLAS_ACT_NONE, ATLAS_ACT_SILU, ATLAS_ACT_GELU = 0, 1, 2
+
+# exported symbols, as declared in include/atlas_mem.h, atlas_prologue.h,
+# atlas_decay.h, atlas_norm.h and atlas_linear.h
 EXPORTS = ("atlas_mem_create", "atlas_mem_forward", "atlas_mem_forward_host", "atlas_mem_forward_noalloc",
            "atlas_mem_status",
            "atlas_mem_workspace_bytes", "atlas_mem_last_launches", "atlas_mem_last_error", "atlas_mem_destroy",
            "atlas_prologue_create", "atlas_prologue_forward", "atlas_prologue_workspace_bytes",
            "atlas_prologue_last_error", "atlas_prologue_destroy", "atlas_prologue_status",
-           "atlas_prologue_last_gemm")
+           "atlas_prologue_last_gemm",
+           "atlas_decay_create", "atlas_decay_forward", "atlas_decay_workspace_bytes", "atlas_decay_status",
+           "atlas_decay_last_path", "atlas_decay_last_error", "atlas_decay_destroy",
+           "atlas_norm_create", "atlas_norm_forward", "atlas_norm_workspace_bytes", "atlas_norm_last_error",
+           "atlas_norm_destroy",
+           "atlas_linear_create", "atlas_linear_forward", "atlas_linear_workspace_bytes", "atlas_linear_status",
+           "atlas_linear_last_path", "atlas_linear_last_error", "atlas_linear_destroy")
 
 
 class atlas_mem_config(ctypes.Structure):
@@ -64,6 +75,33 @@ class atlas_prologue_io(ctypes.Structure):
     _fields_ = [("B", ctypes.c_int), ("T", ctypes.c_int)] + [
         (n, _vp) for n in ("x", "W_in", "conv_w", "gate_b", "cache", "q", "k", "v", "theta", "eta", "alpha",
                            "gamma", "cache_out")]
+
+
+class atlas_decay_config(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("H", "d_k", "d_v", "share", "qkv_dtype", "y_dtype", "qkv_layout",
+                                            "y_layout")] + [("scale", ctypes.c_float)]
+
+
+class atlas_decay_io(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("T", ctypes.c_int)] + [
+        (n, _vp) for n in ("q", "k", "v", "decay", "lens", "S0", "y", "S_out")]
+
+
+class atlas_norm_config(ctypes.Structure):
+    _fields_ = [("C", ctypes.c_int), ("groups", ctypes.c_int), ("act", ctypes.c_int), ("eps", ctypes.c_float),
+                ("x_dtype", ctypes.c_int), ("y_dtype", ctypes.c_int), ("layout", ctypes.c_int)]
+
+
+class atlas_norm_io(ctypes.Structure):
+    _fields_ = [("N", ctypes.c_int), ("S", ctypes.c_int)] + [(n, _vp) for n in ("x", "weight", "bias", "y")]
+
+
+class atlas_linear_config(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("K", "N", "act", "in_dtype", "out_dtype")]
+
+
+class atlas_linear_io(ctypes.Structure):
+    _fields_ = [("M", ctypes.c_int)] + [(n, _vp) for n in ("x", "W", "bias", "residual", "y")]
 
 
 class AtlasError(RuntimeError):
@@ -113,6 +151,20 @@ def load(path: str = LIB_PATH):
     lib.atlas_prologue_status.restype = ctypes.c_int
     lib.atlas_prologue_last_gemm.argtypes = [ctypes.c_void_p]
     lib.atlas_prologue_last_gemm.restype = ctypes.c_int
+    for op, cfg, io, sizes in (("decay", atlas_decay_config, atlas_decay_io, 2),
+                               ("norm", atlas_norm_config, atlas_norm_io, 2),
+                               ("linear", atlas_linear_config, atlas_linear_io, 1)):
+        for name, args, res in (
+                ("create", [ctypes.POINTER(cfg), ctypes.POINTER(ctypes.c_void_p)], ctypes.c_int),
+                ("forward", [ctypes.c_void_p, ctypes.POINTER(io), ctypes.c_void_p], ctypes.c_int),
+                ("workspace_bytes", [ctypes.c_void_p] + [ctypes.c_int] * sizes, ctypes.c_size_t),
+                ("last_error", [ctypes.c_void_p], ctypes.c_char_p),
+                ("destroy", [ctypes.c_void_p], None),
+                ("status", [ctypes.c_void_p], ctypes.c_int),
+                ("last_path", [ctypes.c_void_p], ctypes.c_int)):
+            if f"atlas_{op}_{name}" in EXPORTS:
+                fn = getattr(lib, f"atlas_{op}_{name}")
+                fn.argtypes, fn.restype = args, res
     _lib = lib
     return lib
 
@@ -199,6 +251,129 @@ def atlas_prologue_last_gemm(h) -> int:
 
 def atlas_prologue_destroy(h):
     load().atlas_prologue_destroy(h)
+
+
+def _created(fn, last_error, cfg):
+    h = ctypes.c_void_p()
+    rc = fn(ctypes.byref(cfg), ctypes.byref(h))
+    if rc:
+        raise AtlasError(rc, last_error(None).decode())
+    return h
+
+
+def atlas_decay_create(cfg: atlas_decay_config):
+    lib = load()
+    return _created(lib.atlas_decay_create, lib.atlas_decay_last_error, cfg)
+
+
+def atlas_decay_forward(h, io: atlas_decay_io, stream: int = 0):
+    lib = load()
+    rc = lib.atlas_decay_forward(h, ctypes.byref(io), stream)
+    if rc:
+        raise AtlasError(rc, lib.atlas_decay_last_error(h).decode())
+
+
+def atlas_decay_workspace_bytes(h, B, T) -> int:
+    return load().atlas_decay_workspace_bytes(h, B, T)
+
+
+def atlas_decay_status(h) -> int:
+    return load().atlas_decay_status(h)
+
+
+def atlas_decay_last_path(h) -> int:
+    return load().atlas_decay_last_path(h)
+
+
+def atlas_decay_last_error(h) -> str:
+    return load().atlas_decay_last_error(h).decode()
+
+
+def atlas_decay_destroy(h):
+    load().atlas_decay_destroy(h)
+
+
+def atlas_norm_create(cfg: atlas_norm_config):
+    lib = load()
+    return _created(lib.atlas_norm_create, lib.atlas_norm_last_error, cfg)
+
+
+def atlas_norm_forward(h, io: atlas_norm_io, stream: int = 0):
+    lib = load()
+    rc = lib.atlas_norm_forward(h, ctypes.byref(io), stream)
+    if rc:
+        raise AtlasError(rc, lib.atlas_norm_last_error(h).decode())
+
+
+def atlas_norm_workspace_bytes(h, N, S) -> int:
+    return load().atlas_norm_workspace_bytes(h, N, S)
+
+
+def atlas_norm_last_error(h) -> str:
+    return load().atlas_norm_last_error(h).decode()
+
+
+def atlas_norm_destroy(h):
+    load().atlas_norm_destroy(h)
+
+
+def atlas_linear_create(cfg: atlas_linear_config):
+    lib = load()
+    return _created(lib.atlas_linear_create, lib.atlas_linear_last_error, cfg)
+
+
+def atlas_linear_forward(h, io: atlas_linear_io, stream: int = 0):
+    lib = load()
+    rc = lib.atlas_linear_forward(h, ctypes.byref(io), stream)
+    if rc:
+        raise AtlasError(rc, lib.atlas_linear_last_error(h).decode())
+
+
+def atlas_linear_workspace_bytes(h, M) -> int:
+    return load().atlas_linear_workspace_bytes(h, M)
+
+
+def atlas_linear_status(h) -> int:
+    return load().atlas_linear_status(h)
+
+
+def atlas_linear_last_path(h) -> int:
+    return load().atlas_linear_last_path(h)
+
+
+def atlas_linear_last_error(h) -> str:
+    return load().atlas_linear_last_error(h).decode()
+
+
+def atlas_linear_destroy(h):
+    load().atlas_linear_destroy(h)
+
+
+_DTYPES = {"f32": ATLAS_F32, "bf16": ATLAS_BF16}
+_ACTS = {"none": ATLAS_ACT_NONE, "silu": ATLAS_ACT_SILU, "gelu": ATLAS_ACT_GELU}
+_LAYOUTS = {"heads": ATLAS_LAYOUT_HEADS, "tokens": ATLAS_LAYOUT_TOKENS}
+_NORM_LAYOUTS = {"channels_last": ATLAS_NORM_CHANNELS_LAST, "heads": ATLAS_NORM_HEADS}
+
+
+def make_decay_config(H, d_k, d_v, share=1, qkv_dtype="bf16", y_dtype=None, qkv_layout="heads", y_layout="heads",
+                      scale=1.0) -> atlas_decay_config:
+    dt = _DTYPES.get(qkv_dtype, qkv_dtype)
+    yt = dt if y_dtype is None else _DTYPES.get(y_dtype, y_dtype)
+    return atlas_decay_config(H, d_k, d_v, share, dt, yt, _LAYOUTS.get(qkv_layout, qkv_layout),
+                              _LAYOUTS.get(y_layout, y_layout), scale)
+
+
+def make_norm_config(C, groups, act="none", eps=1e-5, x_dtype="bf16", y_dtype=None,
+                     layout="channels_last") -> atlas_norm_config:
+    xt = _DTYPES.get(x_dtype, x_dtype)
+    yt = xt if y_dtype is None else _DTYPES.get(y_dtype, y_dtype)
+    return atlas_norm_config(C, groups, _ACTS.get(act, act), eps, xt, yt, _NORM_LAYOUTS.get(layout, layout))
+
+
+def make_linear_config(K, N, act="none", in_dtype="bf16", out_dtype=None) -> atlas_linear_config:
+    it = _DTYPES.get(in_dtype, in_dtype)
+    ot = it if out_dtype is None else _DTYPES.get(out_dtype, out_dtype)
+    return atlas_linear_config(K, N, _ACTS.get(act, act), it, ot)
 
 
 def make_prologue_config(D, H, d_k, d_v, conv, with_gamma, theta_max, qkv_dtype) -> atlas_prologue_config:

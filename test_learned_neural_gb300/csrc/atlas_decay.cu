@@ -1,0 +1,453 @@
+// Linear attention with a decay for each head: host side, and the kernels
+// that run in fp32 arithmetic (decay_common.cuh has the formulas).
+#include <math.h>
+
+#include <algorithm>
+#include <new>
+
+#include "decay_common.cuh"
+
+using namespace layer;
+using decay::Geom;
+using decay::Ptrs;
+
+namespace {
+
+constexpr int kSlice = 64;         // d_v columns per CTA
+constexpr int kMaxStepTokens = 16; // calls up to this long go token by token
+
+// ------------------------------------------------- token by token
+// A CTA holds kSlice columns of one state in registers: thread (rg, c4) rows
+// rg, rg + 16, ... and columns 4 c4 .. 4 c4 + 3, so the state is read and
+// written once, by 256-byte row segments.
+template <typename TI, typename TO, int RPT, int V>
+__global__ void __launch_bounds__(256) k_decay_step(Geom g, Ptrs p) {
+  constexpr int CL = kSlice / V;             // threads along the columns
+  constexpr int RG = 256 / CL;               // row groups
+  extern __shared__ float sm[];
+  float* qs = sm;                            // [d_k]
+  float* ks = qs + g.d_k;                    // [d_k]
+  float* part = ks + g.d_k;                  // [RG][kSlice]
+  const int unit = blockIdx.x / g.slices, sl = blockIdx.x % g.slices;
+  const int b = unit / g.H, h = unit % g.H, tid = threadIdx.x;
+  const int cl = tid % CL, rg = tid / CL, col = sl * kSlice + cl * V;
+  const bool on = col < g.d_v;
+  const int n = decay::live_tokens(g, p, b);
+  const float gam = p.decay[h];
+  const size_t base = (size_t)unit * g.d_k * g.d_v + col;
+  float S[RPT][V];
+#pragma unroll
+  for (int r = 0; r < RPT; ++r) {
+    const int row = rg + r * RG;
+    if (p.S0 && on && row < g.d_k) {
+      load_vec<V>(p.S0 + base + (size_t)row * g.d_v, S[r]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < V; ++e) S[r][e] = 0.f;
+    }
+  }
+  const TI* q = (const TI*)p.q + b * g.qk_b + (h / g.share) * g.qk_h;
+  const TI* k = (const TI*)p.k + b * g.qk_b + (h / g.share) * g.qk_h;
+  const TI* v = (const TI*)p.v + b * g.v_b + h * g.v_h;
+  TO* y = (TO*)p.y + b * g.y_b + h * g.y_h;
+  for (int t = 0; t < n; ++t) {
+    for (int i = tid; i < g.d_k; i += 256) {
+      qs[i] = to_f32(q[t * g.qk_t + i]);
+      ks[i] = to_f32(k[t * g.qk_t + i]);
+    }
+    float vt[V], acc[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      vt[e] = on && col + e < g.d_v ? to_f32(v[t * g.v_t + col + e]) : 0.f;
+      acc[e] = 0.f;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < RPT; ++r) {
+      const int row = rg + r * RG;
+      const float kr = row < g.d_k ? ks[row] : 0.f, qr = row < g.d_k ? qs[row] : 0.f;
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        S[r][e] = fmaf(gam, S[r][e], kr * vt[e]);
+        acc[e] = fmaf(qr, S[r][e], acc[e]);
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < V; ++e) part[rg * kSlice + cl * V + e] = acc[e];
+    __syncthreads();
+    if (tid < kSlice && sl * kSlice + tid < g.d_v) {
+      float s = 0.f;
+#pragma unroll
+      for (int r = 0; r < RG; ++r) s += part[r * kSlice + tid];
+      y[t * g.y_t + sl * kSlice + tid] = from_f32<TO>(g.scale * s);
+    }
+  }
+  // read-outs past the row's length
+  for (int t = n; t < g.T; ++t)
+    if (tid < kSlice && sl * kSlice + tid < g.d_v) y[t * g.y_t + sl * kSlice + tid] = from_f32<TO>(0.f);
+  if (p.S_out && on) {
+#pragma unroll
+    for (int r = 0; r < RPT; ++r) {
+      const int row = rg + r * RG;
+      if (row < g.d_k) store_vec<V>(p.S_out + base + (size_t)row * g.d_v, S[r]);
+    }
+  }
+}
+
+// ------------------------------------------------------- fp32 chunks
+// One CTA: (segment, column slice, unit), chunks of C tokens in order; every
+// product is a register-tiled fp32 loop over shared-memory tiles.  READ: form
+// the read-outs from the segment-start state; else only the segment's own
+// contribution to the next segment's start.
+template <typename TI, typename TO, int C, bool READ>
+__global__ void __launch_bounds__(256) k_decay_chunk(Geom g, Ptrs p) {
+  extern __shared__ float sm[];
+  const int dk4 = (g.d_k + 3) & ~3, ldk = dk4 + 4;
+  constexpr int LDV = kSlice + 4, LDP = C + 4, NI = C / 16;
+  float* Ks = sm;                   // [C][ldk]
+  float* Vs = Ks + C * ldk;         // [C][LDV]
+  float* Ss = Vs + C * LDV;         // [dk4][LDV]
+  float* pw = Ss + dk4 * LDV;       // g^0 .. g^C, padded to a multiple of 4
+  float* Qs = pw + C + 4;           // [C][ldk]
+  float* Ps = Qs + C * ldk;         // [C][LDP]
+  const int s = blockIdx.x, sl = blockIdx.y, unit = blockIdx.z;
+  const int b = unit / g.H, h = unit % g.H, tid = threadIdx.x, tx = tid % 16, ty = tid / 16;
+  const int live = decay::live_tokens(g, p, b);
+  const int t_lo = s * g.seg, t_hi = min(g.T, t_lo + g.seg), t_live = min(t_hi, max(live, t_lo));
+  const float l2g = log2f(p.decay[h]);
+  const int c0 = sl * kSlice, cols = min(kSlice, g.d_v - c0);
+  const TI* q = (const TI*)p.q + b * g.qk_b + (h / g.share) * g.qk_h;
+  const TI* k = (const TI*)p.k + b * g.qk_b + (h / g.share) * g.qk_h;
+  const TI* v = (const TI*)p.v + b * g.v_b + h * g.v_h + c0;
+  TO* y = (TO*)p.y + b * g.y_b + h * g.y_h + c0;
+  const size_t sq = (size_t)g.d_k * g.d_v;
+  const float* start = nullptr;
+  if constexpr (READ) start = g.nseg > 1 ? p.seg + ((size_t)unit * g.nseg + s) * sq : p.S0 ? p.S0 + unit * sq : nullptr;
+  for (int i = tid; i < dk4 * kSlice; i += 256) {
+    const int r = i / kSlice, c = i % kSlice;
+    Ss[r * LDV + c] = start && r < g.d_k && c < cols ? start[(size_t)r * g.d_v + c0 + c] : 0.f;
+  }
+  for (int i = tid; i <= C; i += 256) pw[i] = decay::power(l2g, i);
+
+  for (int t0 = t_lo; t0 < t_live; t0 += C) {
+    const int n = min(C, t_live - t0);
+    __syncthreads();
+    for (int i = tid; i < C * dk4; i += 256) {
+      const int r = i / dk4, c = i % dk4;
+      const bool in = r < n && c < g.d_k;
+      Ks[r * ldk + c] = in ? to_f32(k[(t0 + r) * g.qk_t + c]) : 0.f;
+      if constexpr (READ) Qs[r * ldk + c] = in ? to_f32(q[(t0 + r) * g.qk_t + c]) : 0.f;
+    }
+    for (int i = tid; i < C * kSlice; i += 256) {
+      const int r = i / kSlice, c = i % kSlice;
+      Vs[r * LDV + c] = r < n && c < cols ? to_f32(v[(t0 + r) * g.v_t + c]) : 0.f;
+    }
+    __syncthreads();
+    if constexpr (READ) {
+      // P = (Q K^T) under the decay mask
+      float a[NI][NI] = {};
+      for (int kk = 0; kk < dk4; kk += 4) {
+        float4 qa[NI], kb[NI];
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+          qa[i] = *reinterpret_cast<const float4*>(Qs + (ty + 16 * i) * ldk + kk);
+          kb[i] = *reinterpret_cast<const float4*>(Ks + (tx + 16 * i) * ldk + kk);
+        }
+#pragma unroll
+        for (int i = 0; i < NI; ++i)
+#pragma unroll
+          for (int j = 0; j < NI; ++j)
+            a[i][j] = fmaf(qa[i].x, kb[j].x, fmaf(qa[i].y, kb[j].y, fmaf(qa[i].z, kb[j].z, fmaf(qa[i].w, kb[j].w, a[i][j]))));
+      }
+#pragma unroll
+      for (int i = 0; i < NI; ++i)
+#pragma unroll
+        for (int j = 0; j < NI; ++j) {
+          const int ri = ty + 16 * i, cj = tx + 16 * j;
+          Ps[ri * LDP + cj] = cj <= ri ? a[i][j] * pw[ri - cj] : 0.f;
+        }
+      __syncthreads();
+      float o[NI][4] = {};
+      for (int kk = 0; kk < dk4; kk += 4) {
+        float4 sv[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sv[e] = *reinterpret_cast<const float4*>(Ss + (kk + e) * LDV + 4 * tx);
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+          const float4 qa = *reinterpret_cast<const float4*>(Qs + (ty + 16 * i) * ldk + kk);
+          o[i][0] = fmaf(qa.x, sv[0].x, fmaf(qa.y, sv[1].x, fmaf(qa.z, sv[2].x, fmaf(qa.w, sv[3].x, o[i][0]))));
+          o[i][1] = fmaf(qa.x, sv[0].y, fmaf(qa.y, sv[1].y, fmaf(qa.z, sv[2].y, fmaf(qa.w, sv[3].y, o[i][1]))));
+          o[i][2] = fmaf(qa.x, sv[0].z, fmaf(qa.y, sv[1].z, fmaf(qa.z, sv[2].z, fmaf(qa.w, sv[3].z, o[i][2]))));
+          o[i][3] = fmaf(qa.x, sv[0].w, fmaf(qa.y, sv[1].w, fmaf(qa.z, sv[2].w, fmaf(qa.w, sv[3].w, o[i][3]))));
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < NI; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[i][e] *= pw[ty + 16 * i + 1];
+      for (int j = 0; j < C; j += 4) {
+        float4 vv[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) vv[e] = *reinterpret_cast<const float4*>(Vs + (j + e) * LDV + 4 * tx);
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+          const float4 pa = *reinterpret_cast<const float4*>(Ps + (ty + 16 * i) * LDP + j);
+          o[i][0] = fmaf(pa.x, vv[0].x, fmaf(pa.y, vv[1].x, fmaf(pa.z, vv[2].x, fmaf(pa.w, vv[3].x, o[i][0]))));
+          o[i][1] = fmaf(pa.x, vv[0].y, fmaf(pa.y, vv[1].y, fmaf(pa.z, vv[2].y, fmaf(pa.w, vv[3].y, o[i][1]))));
+          o[i][2] = fmaf(pa.x, vv[0].z, fmaf(pa.y, vv[1].z, fmaf(pa.z, vv[2].z, fmaf(pa.w, vv[3].z, o[i][2]))));
+          o[i][3] = fmaf(pa.x, vv[0].w, fmaf(pa.y, vv[1].w, fmaf(pa.z, vv[2].w, fmaf(pa.w, vv[3].w, o[i][3]))));
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < NI; ++i) {
+        const int r = ty + 16 * i;
+        if (r < n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (4 * tx + e < cols) y[(t0 + r) * g.y_t + 4 * tx + e] = from_f32<TO>(g.scale * o[i][e]);
+      }
+      __syncthreads();   // every read of the state is done
+    }
+    // S = g^n S + sum_j g^{n-1-j} k_j v_j
+    for (int r0 = 4 * ty; r0 < dk4; r0 += 64) {
+      float a[4][4];
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) a[r][e] = pw[n] * Ss[(r0 + r) * LDV + 4 * tx + e];
+      for (int j = 0; j < n; ++j) {
+        const float w = pw[n - 1 - j];
+        const float4 kr = *reinterpret_cast<const float4*>(Ks + j * ldk + r0);
+        const float4 vv = *reinterpret_cast<const float4*>(Vs + j * LDV + 4 * tx);
+        const float kw[4] = {kr.x * w, kr.y * w, kr.z * w, kr.w * w}, vc[4] = {vv.x, vv.y, vv.z, vv.w};
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) a[r][e] = fmaf(kw[r], vc[e], a[r][e]);
+      }
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        *reinterpret_cast<float4*>(Ss + (r0 + r) * LDV + 4 * tx) = make_float4(a[r][0], a[r][1], a[r][2], a[r][3]);
+    }
+  }
+  __syncthreads();
+  if constexpr (READ) {
+    for (int t = max(t_live, t_lo) + ty; t < t_hi; t += 16)   // read-outs past the row's length
+      for (int c = tx; c < cols; c += 16) y[t * g.y_t + c] = from_f32<TO>(0.f);
+  }
+  float* dst = nullptr;
+  if constexpr (READ) {
+    if (s == g.nseg - 1 && p.S_out) dst = p.S_out + unit * sq;
+  } else {
+    dst = p.seg + ((size_t)unit * g.nseg + s + 1) * sq;
+  }
+  if (dst)
+    for (int i = tid; i < g.d_k * kSlice; i += 256) {
+      const int r = i / kSlice, c = i % kSlice;
+      if (c < cols) dst[(size_t)r * g.d_v + c0 + c] = Ss[r * LDV + c];
+    }
+}
+
+// Segment starts from the segments' own contributions: slot s + 1 holds
+// segment s's; start_0 = S0, start_{s+1} = g^{n_s} start_s + slot_{s+1}.
+__global__ void __launch_bounds__(256) k_decay_scan(Geom g, Ptrs p) {
+  const size_t sq = (size_t)g.d_k * g.d_v;
+  const int unit = blockIdx.y;
+  const size_t e = (size_t)blockIdx.x * 256 + threadIdx.x;
+  if (e >= sq) return;
+  const int live = decay::live_tokens(g, p, unit / g.H);
+  const float l2g = log2f(p.decay[unit % g.H]);
+  float* slot = p.seg + (size_t)unit * g.nseg * sq + e;
+  float run = p.S0 ? p.S0[unit * sq + e] : 0.f;
+  slot[0] = run;
+  const float full = decay::power(l2g, g.seg);
+#pragma unroll 4
+  for (int s = 0; s + 1 < g.nseg; ++s) {
+    const int n = min(g.seg, max(0, live - s * g.seg));
+    run = fmaf(n == g.seg ? full : decay::power(l2g, n), run, slot[(size_t)(s + 1) * sq]);
+    slot[(size_t)(s + 1) * sq] = run;
+  }
+}
+
+size_t step_smem(const Geom& g, int V) { return (size_t)(2 * g.d_k + 256 / (kSlice / V) * kSlice) * sizeof(float); }
+int chunk_tokens(int d_k) { return d_k <= 128 ? 64 : 32; }
+size_t chunk_smem(int d_k, bool read) {
+  const size_t dk4 = (d_k + 3) & ~3, C = chunk_tokens(d_k), ldk = dk4 + 4, ldv = kSlice + 4;
+  return (C * ldk + C * ldv + dk4 * ldv + C + 4 + (read ? C * ldk + C * (C + 4) : 0)) * sizeof(float);
+}
+
+struct Plan {
+  int path, C, slices, nseg, seg;
+};
+
+// A call whose (row, head, slice) triples leave SMs idle is split along the
+// tokens as far as two CTAs per SM, in segments of at least two chunks.
+Plan make_plan(const atlas_decay_config& c, int B, int T) {
+  Plan pl;
+  pl.slices = (c.d_v + kSlice - 1) / kSlice;
+  pl.nseg = 1;
+  pl.seg = T;
+  if (T <= kMaxStepTokens) {
+    pl.path = 0;
+    pl.C = 1;
+    return pl;
+  }
+  pl.path = 1;
+  pl.C = chunk_tokens(c.d_k);
+  const long long ctas = (long long)B * c.H * pl.slices, want = 2LL * sm_count();
+  const long long chunks = (T + pl.C - 1) / pl.C;
+  long long n = ctas >= sm_count() ? 1 : (want + ctas - 1) / ctas;
+  n = std::min(n, std::max(1LL, chunks / 2));
+  const long long per = (chunks + n - 1) / n;
+  pl.seg = (int)(per * pl.C);
+  pl.nseg = (int)((T + pl.seg - 1) / pl.seg);
+  return pl;
+}
+
+}  // namespace
+
+struct atlas_decay_handle : HandleBase {
+  atlas_decay_config cfg;
+  int path = -1;
+};
+
+static thread_local std::string g_create_err;
+
+extern "C" int atlas_decay_create(const atlas_decay_config* cfg, atlas_decay_handle** out) {
+  if (!out || !cfg) {
+    g_create_err = "cfg and out must be non-NULL";
+    if (out) *out = nullptr;
+    return ATLAS_ERR_INVALID_ARG;
+  }
+  *out = nullptr;
+  const atlas_decay_config& c = *cfg;
+  auto bad = [&](int code, const char* why) {
+    g_create_err = why;
+    return code;
+  };
+  if (c.H < 1 || c.d_k < 1 || c.d_v < 1) return bad(ATLAS_ERR_INVALID_ARG, "H, d_k, d_v must be >= 1");
+  if (c.share < 1 || c.H % c.share) return bad(ATLAS_ERR_INVALID_ARG, "share must divide H");
+  if (!dtype_ok(c.qkv_dtype) || !dtype_ok(c.y_dtype))
+    return bad(ATLAS_ERR_INVALID_ARG, "qkv_dtype and y_dtype must be ATLAS_F32 or ATLAS_BF16");
+  auto layout_ok = [](int l) { return l == ATLAS_LAYOUT_HEADS || l == ATLAS_LAYOUT_TOKENS; };
+  if (!layout_ok(c.qkv_layout) || !layout_ok(c.y_layout))
+    return bad(ATLAS_ERR_INVALID_ARG, "qkv_layout and y_layout must be ATLAS_LAYOUT_HEADS or ATLAS_LAYOUT_TOKENS");
+  if (!isfinite(c.scale)) return bad(ATLAS_ERR_INVALID_ARG, "scale must be finite");
+  if (c.d_k > 256 || c.d_v > 1024) return bad(ATLAS_ERR_UNSUPPORTED, "d_k > 256 or d_v > 1024 is not supported");
+  if (c.H > 65535) return bad(ATLAS_ERR_UNSUPPORTED, "H > 65535 is not supported");
+  auto* h = new (std::nothrow) atlas_decay_handle();
+  if (!h) return bad(ATLAS_ERR_OOM, "out of host memory");
+  h->cfg = c;
+  *out = h;
+  return ATLAS_OK;
+}
+
+extern "C" size_t atlas_decay_workspace_bytes(const atlas_decay_handle* h, int B, int T) {
+  if (!h || B < 1 || T < 1) return 0;
+  const Plan pl = make_plan(h->cfg, B, T);
+  return pl.nseg > 1 ? (size_t)B * h->cfg.H * pl.nseg * h->cfg.d_k * h->cfg.d_v * sizeof(float) : 0;
+}
+
+namespace {
+
+template <typename TI, typename TO>
+cudaError_t launch_step(const Geom& g, const Ptrs& p, cudaStream_t st) {
+  // four columns per thread where the state rows are whole 16-byte groups
+  const bool v4 = g.d_v % 4 == 0 && aligned16(p.S0) && aligned16(p.S_out);
+  const int rows = (g.d_k + (v4 ? 15 : 3)) / (v4 ? 16 : 4);
+  const unsigned grid = (unsigned)((size_t)g.B * g.H * g.slices);
+  const size_t smem = step_smem(g, v4 ? 4 : 1);
+  if (v4) {
+    if (rows <= 2) k_decay_step<TI, TO, 2, 4><<<grid, 256, smem, st>>>(g, p);
+    else if (rows <= 4) k_decay_step<TI, TO, 4, 4><<<grid, 256, smem, st>>>(g, p);
+    else if (rows <= 8) k_decay_step<TI, TO, 8, 4><<<grid, 256, smem, st>>>(g, p);
+    else k_decay_step<TI, TO, 16, 4><<<grid, 256, smem, st>>>(g, p);
+  } else {
+    if (rows <= 16) k_decay_step<TI, TO, 16, 1><<<grid, 256, smem, st>>>(g, p);
+    else if (rows <= 32) k_decay_step<TI, TO, 32, 1><<<grid, 256, smem, st>>>(g, p);
+    else k_decay_step<TI, TO, 64, 1><<<grid, 256, smem, st>>>(g, p);
+  }
+  return cudaGetLastError();
+}
+
+template <typename K>
+cudaError_t launch_big(K kern, dim3 grid, size_t smem, const Geom& g, const Ptrs& p, cudaStream_t st) {
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  kern<<<grid, 256, smem, st>>>(g, p);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_scan(const Geom& g, const Ptrs& p, cudaStream_t st) {
+  k_decay_scan<<<dim3((unsigned)(((size_t)g.d_k * g.d_v + 255) / 256), (unsigned)(g.B * g.H)), 256, 0, st>>>(g, p);
+  return cudaGetLastError();
+}
+
+template <typename TI, typename TO, int C>
+cudaError_t launch_chunks(const Geom& g, const Ptrs& p, cudaStream_t st) {
+  const unsigned units = (unsigned)(g.B * g.H);
+  if (g.nseg > 1) {
+    cudaError_t e = launch_big(k_decay_chunk<TI, TO, C, false>, dim3(g.nseg - 1, g.slices, units),
+                               chunk_smem(g.d_k, false), g, p, st);
+    if (e != cudaSuccess) return e;
+    e = launch_scan(g, p, st);
+    if (e != cudaSuccess) return e;
+  }
+  return launch_big(k_decay_chunk<TI, TO, C, true>, dim3(g.nseg, g.slices, units), chunk_smem(g.d_k, true), g, p, st);
+}
+
+template <typename TI, typename TO>
+cudaError_t launch(const Plan& pl, const Geom& g, const Ptrs& p, cudaStream_t st) {
+  if (pl.path == 0) return launch_step<TI, TO>(g, p, st);
+  return pl.C == 64 ? launch_chunks<TI, TO, 64>(g, p, st) : launch_chunks<TI, TO, 32>(g, p, st);
+}
+
+}  // namespace
+
+extern "C" int atlas_decay_forward(atlas_decay_handle* h, const atlas_decay_io* io, void* stream) {
+  if (!h) return ATLAS_ERR_INVALID_ARG;
+  if (!io) return h->fail(ATLAS_ERR_INVALID_ARG, "io must be non-NULL");
+  const atlas_decay_config& c = h->cfg;
+  if (io->B < 1 || io->T < 1) return h->fail(ATLAS_ERR_INVALID_ARG, "B and T must be >= 1");
+  if (!io->q || !io->k || !io->v || !io->decay || !io->y)
+    return h->fail(ATLAS_ERR_INVALID_ARG, "q, k, v, decay, y must be non-NULL");
+  if (io->y == io->q || io->y == io->k || io->y == io->v)
+    return h->fail(ATLAS_ERR_INVALID_ARG, "y must not alias q, k or v");
+  if ((long long)io->B * c.H > 65535 && io->T > kMaxStepTokens)
+    return h->fail(ATLAS_ERR_UNSUPPORTED, "B * H > 65535 is supported for calls of at most %d tokens", kMaxStepTokens);
+  if ((long long)io->B * c.H * ((c.d_v + kSlice - 1) / kSlice) > 0x7fffffffLL)
+    return h->fail(ATLAS_ERR_UNSUPPORTED, "B * H too large for one call");
+  cudaStream_t st = (cudaStream_t)stream;
+  const Plan pl = make_plan(c, io->B, io->T);
+  int rc = h->grow(atlas_decay_workspace_bytes(h, io->B, io->T));
+  if (rc) return rc;
+
+  Geom g;
+  g.B = io->B, g.T = io->T, g.H = c.H, g.share = c.share, g.d_k = c.d_k, g.d_v = c.d_v, g.scale = c.scale;
+  g.slices = pl.slices, g.nseg = pl.nseg, g.seg = pl.seg;
+  const size_t T = io->T, Hq = c.H / c.share;
+  auto strides = [&](int layout, size_t heads, size_t d, size_t& sb, size_t& sh, size_t& stk) {
+    sb = T * heads * d;
+    sh = layout == ATLAS_LAYOUT_HEADS ? T * d : d;
+    stk = layout == ATLAS_LAYOUT_HEADS ? d : heads * d;
+  };
+  strides(c.qkv_layout, Hq, c.d_k, g.qk_b, g.qk_h, g.qk_t);
+  strides(c.qkv_layout, c.H, c.d_v, g.v_b, g.v_h, g.v_t);
+  strides(c.y_layout, c.H, c.d_v, g.y_b, g.y_h, g.y_t);
+  const Ptrs p{io->q, io->k, io->v, io->decay, io->lens, io->S0, io->y, io->S_out, (float*)h->ws};
+  const bool ib = c.qkv_dtype == ATLAS_BF16, ob = c.y_dtype == ATLAS_BF16;
+  const cudaError_t e = ib ? (ob ? launch<bf16, bf16>(pl, g, p, st) : launch<bf16, float>(pl, g, p, st))
+                           : (ob ? launch<float, bf16>(pl, g, p, st) : launch<float, float>(pl, g, p, st));
+  if (e != cudaSuccess) return h->cuda_fail("decay attention launch", e);
+  h->path = pl.path;
+  h->last_stream = st;
+  h->launched = true;
+  return ATLAS_OK;
+}
+
+extern "C" int atlas_decay_status(atlas_decay_handle* h) { return h ? h->read_status() : ATLAS_ERR_INVALID_ARG; }
+extern "C" int atlas_decay_last_path(const atlas_decay_handle* h) { return h ? h->path : -1; }
+extern "C" const char* atlas_decay_last_error(const atlas_decay_handle* h) {
+  return h ? h->err.c_str() : g_create_err.c_str();
+}
+extern "C" void atlas_decay_destroy(atlas_decay_handle* h) { delete h; }

@@ -10,10 +10,15 @@ from __future__ import annotations
 import numpy as np
 import torch
 
-from . import (ATLAS_BF16, ATLAS_F32, atlas_mem_create, atlas_mem_destroy, atlas_mem_forward,
-               atlas_mem_forward_host, atlas_mem_status, atlas_prologue_create, atlas_prologue_destroy,
+from . import (ATLAS_BF16, ATLAS_F32, ATLAS_LAYOUT_HEADS, ATLAS_NORM_HEADS, atlas_decay_create, atlas_decay_destroy,
+               atlas_decay_forward, atlas_decay_io, atlas_decay_last_path, atlas_decay_status, atlas_linear_create,
+               atlas_linear_destroy, atlas_linear_forward, atlas_linear_io, atlas_linear_last_path,
+               atlas_linear_status, atlas_mem_create, atlas_mem_destroy, atlas_mem_forward,
+               atlas_mem_forward_host, atlas_mem_status, atlas_norm_create, atlas_norm_destroy, atlas_norm_forward,
+               atlas_norm_io, atlas_prologue_create, atlas_prologue_destroy,
                atlas_prologue_forward, atlas_prologue_io, atlas_prologue_last_gemm, atlas_prologue_status,
-               current_stream, make_config, make_io, make_prologue_config, AtlasError)
+               current_stream, make_config, make_decay_config, make_io, make_linear_config, make_norm_config,
+               make_prologue_config, AtlasError)
 
 
 def matrix_shapes(cfg):
@@ -178,3 +183,157 @@ def prologue_tensors_from_numpy(inp: dict, device="cuda"):
             return torch.from_numpy(a.view(np.int16)).view(torch.bfloat16).to(device)
         return torch.from_numpy(a).to(device)
     return {k: conv(inp.get(k)) for k in ("x", "W_in", "conv_w", "gate_b", "cache")}
+
+
+def _torch_dtype(t):
+    return torch.bfloat16 if t == ATLAS_BF16 else torch.float32
+
+
+def _check(name, t, dtype, shape):
+    """Device address of a tensor of the layer operators, which must have the
+    type and shape that the configuration and the call's sizes give."""
+    if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous() or not t.is_cuda:
+        raise ValueError(f"{name}: want a contiguous CUDA tensor {dtype} {shape}, got {t.dtype} {tuple(t.shape)} on "
+                         f"{t.device}")
+    return t.data_ptr()
+
+
+class _Layer:
+    """One library handle of a layer operator."""
+    _destroy = None
+    h = None
+
+    def close(self):
+        if self.h is not None:
+            type(self)._destroy(self.h)
+            self.h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+class DecayAttention(_Layer):
+    """Linear attention with a decay for each head (include/atlas_decay.h):
+    S_t = g S_{t-1} + k_t^T v_t, y_t = scale q_t S_t."""
+    _destroy = staticmethod(atlas_decay_destroy)
+
+    def __init__(self, H, d_k, d_v, share=1, qkv_dtype="bf16", y_dtype=None, qkv_layout="heads", y_layout="heads",
+                 scale=1.0):
+        self.cfg = make_decay_config(H, d_k, d_v, share, qkv_dtype, y_dtype, qkv_layout, y_layout, scale)
+        self.h = atlas_decay_create(self.cfg)
+        c = self.cfg
+        self._qkv, self._y = _torch_dtype(c.qkv_dtype), _torch_dtype(c.y_dtype)
+        self._heads_first, self._y_heads_first = c.qkv_layout == ATLAS_LAYOUT_HEADS, c.y_layout == ATLAS_LAYOUT_HEADS
+
+    def _y_shape(self, B, T):
+        c = self.cfg
+        return (B, c.H, T, c.d_v) if self._y_heads_first else (B, T, c.H, c.d_v)
+
+    def alloc_outputs(self, B, T, device):
+        c = self.cfg
+        return dict(y=torch.empty(self._y_shape(B, T), dtype=self._y, device=device),
+                    S=torch.empty((B, c.H, c.d_k, c.d_v), dtype=torch.float32, device=device))
+
+    def forward(self, t, out=None, stream=None):
+        """t: dict of device tensors q, k, v, decay and optional lens (int32
+        [B]) and S0 (fp32 [B, H, d_k, d_v]; may be out["S"]: the state is then
+        continued in place)."""
+        c, q, v = self.cfg, t["q"], t["v"]
+        B, T = (q.shape[0], q.shape[2]) if self._heads_first else q.shape[:2]
+        hq = c.H // c.share
+        qs, vs = ((B, hq, T, c.d_k), (B, c.H, T, c.d_v)) if self._heads_first else (
+            (B, T, hq, c.d_k), (B, T, c.H, c.d_v))
+        if out is None:
+            out = self.alloc_outputs(B, T, q.device)
+        lens, S0, sq, f32 = t.get("lens"), t.get("S0"), (B, c.H, c.d_k, c.d_v), torch.float32
+        io = atlas_decay_io(B, T, _check("q", q, self._qkv, qs), _check("k", t["k"], self._qkv, qs),
+                            _check("v", v, self._qkv, vs), _check("decay", t["decay"], f32, (c.H,)),
+                            None if lens is None else _check("lens", lens, torch.int32, (B,)),
+                            None if S0 is None else _check("S0", S0, f32, sq),
+                            _check("y", out["y"], self._y, self._y_shape(B, T)), _check("S", out["S"], f32, sq))
+        atlas_decay_forward(self.h, io, current_stream() if stream is None else stream)
+        return out
+
+    def status(self):
+        rc = atlas_decay_status(self.h)
+        if rc:
+            raise AtlasError(rc, "device status of the decay attention")
+        return rc
+
+    def last_path(self):
+        """0: token by token, 1: fp32 chunks, 2: tensor-core chunks."""
+        return atlas_decay_last_path(self.h)
+
+
+class GroupNorm(_Layer):
+    """Group norm with an activation, channels last (include/atlas_norm.h).
+    layout "heads": x is a read-out [N, groups, S, C / groups], y [N, S, C]."""
+    _destroy = staticmethod(atlas_norm_destroy)
+
+    def __init__(self, C, groups, act="none", eps=1e-5, x_dtype="bf16", y_dtype=None, layout="channels_last"):
+        self.cfg = make_norm_config(C, groups, act, eps, x_dtype, y_dtype, layout)
+        self.h = atlas_norm_create(self.cfg)
+        self._x, self._y = _torch_dtype(self.cfg.x_dtype), _torch_dtype(self.cfg.y_dtype)
+
+    def alloc_outputs(self, N, S, device):
+        return dict(y=torch.empty((N, S, self.cfg.C), dtype=self._y, device=device))
+
+    def forward(self, t, out=None, stream=None):
+        """t: dict of device tensors x and optional weight, bias (fp32 [C])."""
+        c, x = self.cfg, t["x"]
+        if c.layout == ATLAS_NORM_HEADS:
+            N, S = x.shape[0], x.shape[2]
+            shape = (N, c.groups, S, c.C // c.groups)
+        else:
+            N, S = x.shape[:2]
+            shape = (N, S, c.C)
+        if out is None:
+            out = self.alloc_outputs(N, S, x.device)
+        w, b, f32 = t.get("weight"), t.get("bias"), torch.float32
+        io = atlas_norm_io(N, S, _check("x", x, self._x, shape),
+                           None if w is None else _check("weight", w, f32, (c.C,)),
+                           None if b is None else _check("bias", b, f32, (c.C,)),
+                           _check("y", out["y"], self._y, (N, S, c.C)))
+        atlas_norm_forward(self.h, io, current_stream() if stream is None else stream)
+        return out
+
+
+class Linear(_Layer):
+    """y = act(x W + bias) + residual (include/atlas_linear.h)."""
+    _destroy = staticmethod(atlas_linear_destroy)
+
+    def __init__(self, K, N, act="none", in_dtype="bf16", out_dtype=None):
+        self.cfg = make_linear_config(K, N, act, in_dtype, out_dtype)
+        self.h = atlas_linear_create(self.cfg)
+        self._in, self._out = _torch_dtype(self.cfg.in_dtype), _torch_dtype(self.cfg.out_dtype)
+
+    def alloc_outputs(self, M, device):
+        return dict(y=torch.empty((M, self.cfg.N), dtype=self._out, device=device))
+
+    def forward(self, t, out=None, stream=None):
+        """t: dict of device tensors x [M, K], W [K, N] and optional bias
+        (fp32 [N]) and residual [M, N] (may be out["y"]: added in place)."""
+        c, x = self.cfg, t["x"]
+        M = x.shape[0]
+        if out is None:
+            out = self.alloc_outputs(M, x.device)
+        b, r = t.get("bias"), t.get("residual")
+        io = atlas_linear_io(M, _check("x", x, self._in, (M, c.K)), _check("W", t["W"], self._in, (c.K, c.N)),
+                             None if b is None else _check("bias", b, torch.float32, (c.N,)),
+                             None if r is None else _check("residual", r, self._out, (M, c.N)),
+                             _check("y", out["y"], self._out, (M, c.N)))
+        atlas_linear_forward(self.h, io, current_stream() if stream is None else stream)
+        return out
+
+    def status(self):
+        rc = atlas_linear_status(self.h)
+        if rc:
+            raise AtlasError(rc, "device status of the matrix product")
+        return rc
+
+    def last_path(self):
+        """0: fp32 tiles, 1: tensor cores, 2: few rows."""
+        return atlas_linear_last_path(self.h)

@@ -1,10 +1,9 @@
-// Matrix product with bias, activation and residual: host side and the fp32
-// tiles.
+// Matrix product with bias, activation and residual: host side, the fp32
+// tiles, and the operand planes of the tensor-core kernels.
 #include <algorithm>
 #include <new>
 
-#include "../../include/atlas_linear.h"
-#include "layer_common.cuh"
+#include "linear_common.cuh"
 
 using namespace layer;
 
@@ -50,6 +49,84 @@ __global__ void __launch_bounds__(256) k_linear_f32(int M, int K, int N, const T
       y[(size_t)m * N + n] = from_f32<TO>(v);
     }
 }
+
+// src [R][C] -> bf16 planes [PLANES][Rp][ld], zero past R and C: one plane for
+// bf16 values; three for fp32 ones, the leading 8 bits, the next 8 and the
+// last 8, each cut off (not rounded), so that their sum is the value itself.
+// Infinities and NaN stay in the first plane.
+template <typename TI, int PLANES>
+__global__ void __launch_bounds__(256) k_planes(const TI* __restrict__ src, int R, int C, int Rp, int ld,
+                                                uint16_t* __restrict__ dst) {
+  const int per = ld / 8;
+  const size_t i = (size_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= (size_t)Rp * per) return;
+  const int r = (int)(i / per), c0 = (int)(i % per) * 8;
+  uint32_t w[PLANES][4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    uint32_t half[PLANES][2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int c = c0 + 2 * j + e;
+      const bool in = r < R && c < C;
+      if constexpr (PLANES == 1) {
+        half[0][e] = in ? (uint32_t) reinterpret_cast<const uint16_t*>(src)[(size_t)r * C + c] : 0u;
+      } else {
+        float v = in ? to_f32(src[(size_t)r * C + c]) : 0.f;
+        if (fabsf(v) <= 3.402823466e38f) {
+#pragma unroll
+          for (int k = 0; k < PLANES; ++k) {
+            const uint32_t top = __float_as_uint(v) & 0xffff0000u;
+            half[k][e] = top >> 16;
+            v -= __uint_as_float(top);
+          }
+        } else {
+          half[0][e] = v != v ? 0x7fffu : __float_as_uint(v) >> 16;
+#pragma unroll
+          for (int k = 1; k < PLANES; ++k) half[k][e] = 0u;
+        }
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < PLANES; ++k) w[k][j] = half[k][0] | (half[k][1] << 16);
+  }
+#pragma unroll
+  for (int k = 0; k < PLANES; ++k)
+    *reinterpret_cast<uint4*>(dst + ((size_t)k * Rp + r) * ld + c0) = make_uint4(w[k][0], w[k][1], w[k][2], w[k][3]);
+}
+
+// Where the tensor-core kernels read their operands: the caller's, or planes
+// in the workspace (fp32 values; row strides or addresses off 16 bytes).
+struct Operands {
+  bool copy_x, copy_w;
+  int planes, K, ldx, ldw;   // K: columns of x and rows of W as the kernels see them
+  size_t x_bytes, w_bytes;
+};
+
+Operands make_operands(const atlas_linear_config& c, int M, bool x_ok, bool w_ok) {
+  Operands o;
+  const bool f32 = c.in_dtype == ATLAS_F32;
+  o.planes = f32 ? 3 : 1;
+  o.K = f32 ? (c.K + 63) / 64 * 64 : c.K;
+  o.copy_x = f32 || c.K % 8 || !x_ok;
+  o.copy_w = f32 || c.N % 8 || !w_ok;
+  o.ldx = o.copy_x ? (o.K + 7) / 8 * 8 : c.K;
+  o.ldw = o.copy_w ? (c.N + 7) / 8 * 8 : c.N;
+  o.x_bytes = o.copy_x ? ((size_t)o.planes * M * o.ldx * 2 + 255) / 256 * 256 : 0;
+  o.w_bytes = o.copy_w ? ((size_t)o.planes * o.K * o.ldw * 2 + 255) / 256 * 256 : 0;
+  return o;
+}
+
+cudaError_t planes_launch(bool f32, const void* src, int R, int C, int Rp, int ld, void* dst, cudaStream_t st) {
+  const unsigned grid = (unsigned)(((size_t)Rp * (ld / 8) + 255) / 256);
+  if (f32)
+    k_planes<float, 3><<<grid, 256, 0, st>>>((const float*)src, R, C, Rp, ld, (uint16_t*)dst);
+  else
+    k_planes<bf16, 1><<<grid, 256, 0, st>>>((const bf16*)src, R, C, Rp, ld, (uint16_t*)dst);
+  return cudaGetLastError();
+}
+
+constexpr int kMinTcRows = 17;   // fewer rows go to the fp32 tiles
 
 template <typename TI, typename TO>
 cudaError_t launch(const atlas_linear_config& c, const atlas_linear_io& io, cudaStream_t st) {
@@ -98,8 +175,9 @@ extern "C" int atlas_linear_create(const atlas_linear_config* cfg, atlas_linear_
 }
 
 extern "C" size_t atlas_linear_workspace_bytes(const atlas_linear_handle* h, int M) {
-  (void)h, (void)M;
-  return 0;
+  if (!h || M < kMinTcRows) return 0;
+  const Operands o = make_operands(h->cfg, M, false, false);
+  return o.x_bytes + o.w_bytes;
 }
 
 extern "C" int atlas_linear_forward(atlas_linear_handle* h, const atlas_linear_io* io, void* stream) {
@@ -112,6 +190,27 @@ extern "C" int atlas_linear_forward(atlas_linear_handle* h, const atlas_linear_i
   if (io->M > 65535 * 64) return h->fail(ATLAS_ERR_UNSUPPORTED, "M > %d is not supported", 65535 * 64);
   cudaStream_t st = (cudaStream_t)stream;
   const bool ib = c.in_dtype == ATLAS_BF16, ob = c.out_dtype == ATLAS_BF16;
+  if (io->M >= kMinTcRows) {
+    const Operands o = make_operands(c, io->M, aligned16(io->x), aligned16(io->W));
+    int rc = h->need_status(st);
+    if (!rc) rc = h->grow(o.x_bytes + o.w_bytes);
+    if (rc) return rc;
+    char* ws = (char*)h->ws;
+    cudaError_t e = cudaSuccess;
+    if (o.copy_x) e = planes_launch(!ib, io->x, io->M, c.K, io->M, o.ldx, ws, st);
+    if (e == cudaSuccess && o.copy_w) e = planes_launch(!ib, io->W, c.K, c.N, o.K, o.ldw, ws + o.x_bytes, st);
+    linear::TcCall t;
+    t.M = io->M, t.N = c.N, t.K = o.K, t.planes = o.planes, t.ldx = o.ldx, t.ldw = o.ldw;
+    t.x = o.copy_x ? ws : io->x;
+    t.W = o.copy_w ? ws + o.x_bytes : io->W;
+    t.bias = io->bias, t.residual = io->residual, t.y = io->y, t.act = c.act, t.out_bf16 = ob, t.status = h->status;
+    if (e == cudaSuccess) e = linear::tc_big(t, st);
+    if (e != cudaSuccess) return h->cuda_fail("matrix product launch", e);
+    h->path = 1;
+    h->last_stream = st;
+    h->launched = true;
+    return ATLAS_OK;
+  }
   const cudaError_t e = ib ? (ob ? launch<bf16, bf16>(c, *io, st) : launch<bf16, float>(c, *io, st))
                            : (ob ? launch<float, bf16>(c, *io, st) : launch<float, float>(c, *io, st));
   if (e != cudaSuccess) return h->cuda_fail("matrix product launch", e);

@@ -10,9 +10,11 @@
 //   warp 0     TMA producer; both CTAs' copies complete on the leader's barrier;
 //   warp 1     (leader) MMA issuer; commits release the stage in both CTAs;
 //   warps 2-9  epilogue, two 256-column accumulators in turn: TMEM -> bias,
-//              activation, residual -> one 32-row, 128-byte-wide swizzled block
-//              per warp (two of them alternate) -> TMA store.  The residual's
-//              block comes into the same buffer by TMA one block ahead.
+//              activation, residual -> one 32-row, 64-byte-wide swizzled block
+//              of the warp's four -> TMA store.  The residual's block comes
+//              into the same buffers by TMA, four blocks at a time while the
+//              MMAs fill the tile's accumulator; the accumulator and the bias
+//              are read one block ahead.
 // Where y or the residual cannot be a TMA operand (row stride or address not on
 // 16 bytes) the block leaves by coalesced element stores instead.
 //
@@ -30,13 +32,15 @@ using layer::bf16;
 namespace {
 
 constexpr int BM = 256, BN = 256, BK = 64, STAGES = 5, EPI_WARPS = 8, NTHR = 64 + 32 * EPI_WARPS;
-constexpr int A_BYTES = BM / 2 * BK * 2, B_BYTES = BN / 2 * BK * 2, STAGE_BYTES = A_BYTES + B_BYTES;
-constexpr int BLK_BYTES = 32 * 128;                              // one epilogue block
-constexpr int SMEM = STAGES * STAGE_BYTES + EPI_WARPS * 2 * BLK_BYTES + 1024;
+constexpr int A_BYTES = BM / 2 * BK * 2, B_BYTES = BN / 2 * BK * 2;
+constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
+constexpr int BLK_BYTES = 32 * 64;                               // one epilogue block
+constexpr int NBUF = 4;                                          // epilogue blocks per warp
+constexpr int SMEM = STAGES * STAGE_BYTES + EPI_WARPS * NBUF * BLK_BYTES + 1024;
 constexpr int BAND = 16;                                         // row tiles per band of the tile order
 
 struct Params {
-  int M, N, nk, planes, kw;   // nk: stages of K per plane; kw: W rows per plane
+  int M, N, nk, planes, kw;   // nk: blocks of 64 of K per plane; kw: W rows per plane
   const float* bias;
   const void* residual;
   void* y;
@@ -67,27 +71,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHR, 1)
   extern __shared__ uint8_t smraw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smraw) + 1023) & ~uintptr_t(1023));
   uint8_t* blocks = sm + STAGES * STAGE_BYTES;
-  __shared__ uint64_t full[STAGES], empty[STAGES], acc_full[2], acc_empty[2], res_full[EPI_WARPS][2];
+  __shared__ uint64_t full[STAGES], empty[STAGES], acc_full[2], acc_empty[2], res_full[EPI_WARPS];
   __shared__ uint32_t tbase;
   __shared__ int failed;
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   const uint32_t rank = tc::cluster_rank();
   const int ntm = (p.M + BM - 1) / BM, ntn = (p.N + BN - 1) / BN, ntiles = ntm * ntn;
   const int first = blockIdx.x / 2, step = gridDim.x / 2;
-  const int pairs = p.planes == 1 ? 1 : 6, iters = p.nk * pairs;
+  const int pairs = p.planes == 1 ? 1 : 6;
 
   if (warp == 0) tc::tmem_alloc_pair(&tbase, 2 * BN);
-  if (tid == 0) {
+  if (tid == 32) {
+    tc::prefetch_map(&map_x);
+    tc::prefetch_map(&map_w);
+    if (p.tma_out) tc::prefetch_map(&map_y);
+    if (p.tma_out && p.residual) tc::prefetch_map(&map_r);
     for (int s = 0; s < STAGES; ++s) {
-      tc::mbar_init(&full[s], 1);
-      tc::mbar_init(&empty[s], 1);
+      tc::mbar_init_only(&full[s], 1);
+      tc::mbar_init_only(&empty[s], 1);
     }
     for (int a = 0; a < 2; ++a) {
-      tc::mbar_init(&acc_full[a], 1);
-      tc::mbar_init(&acc_empty[a], 2 * EPI_WARPS);   // every epilogue warp of both CTAs
+      tc::mbar_init_only(&acc_full[a], 1);
+      tc::mbar_init_only(&acc_empty[a], 2 * EPI_WARPS);   // every epilogue warp of both CTAs
     }
     for (int w = 0; w < EPI_WARPS; ++w)
-      for (int b = 0; b < 2; ++b) tc::mbar_init(&res_full[w][b], 1);
+      tc::mbar_init_only(&res_full[w], 1);
+    tc::mbar_init_fence();
     failed = 0;
   }
   tc::fence_before_sync();
@@ -95,177 +104,216 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHR, 1)
   tc::cluster_sync();
   tc::fence_after_sync();
   const uint32_t tacc = tbase;
+  tc::grid_dependency_wait();   // nothing above touched global memory
+  tc::grid_dependents_launch();
 
+  // a ring slot: s counts through the stages, ph flips with every turn
   if (warp == 0) {
-    if (lane == 0) {
-      int it = 0;
-      bool ok = true;
-      for (int t = first; t < ntiles && ok; t += step) {
-        const Tile tl = tile_at(t, ntm, ntn);
-        const int m0 = tl.m0 + (int)rank * (BM / 2), n0 = tl.n0 + (int)rank * (BN / 2);
-        for (int i = 0; i < iters; ++i, ++it) {
-          const int s = it % STAGES;
-          if (it >= STAGES && !(ok = tc::mbar_wait_cluster(&empty[s], ((it / STAGES) - 1) & 1, tc::kWaitCycles))) break;
-          int pa = 0, pb = 0, kt = i;
+    const uint32_t ring = tc::smem_u32(sm), bfull = tc::smem_u32(full), bempty = tc::smem_u32(empty);
+    const uint32_t lead = tc::map_rank(full, 0);   // the leader's barriers
+    uint32_t s = 0, ph = 1;                                  // the first turn finds its slots free
+    bool ok = true;
+    for (int t = first; t < ntiles && ok; t += step) {
+      const Tile tl = tile_at(t, ntm, ntn);
+      const int m0 = tl.m0 + (int)rank * (BM / 2), n0 = tl.n0 + (int)rank * (BN / 2);
+      for (int kt = 0; kt < p.nk && ok; ++kt) {
+        for (int pr = 0; pr < pairs; ++pr) {
+          int row_x = m0, row_w = kt * BK;
           if (pairs > 1) {
-            kt = i / 6;
-            plane_pair(i % 6, pa, pb);
+            int pa, pb;
+            plane_pair(pr, pa, pb);
+            row_x += pa * p.M;
+            row_w += pb * p.kw;
           }
-          uint8_t* a = sm + s * STAGE_BYTES;
-          const uint32_t bar = tc::map_rank(&full[s], 0);
-          if (rank == 0) tc::mbar_expect_tx(&full[s], 2 * STAGE_BYTES);
-          tc::tma_load_2d_pair(a, &map_x, kt * BK, pa * p.M + m0, bar);
-          tc::tma_load_2d_pair(a + A_BYTES, &map_w, n0, pb * p.kw + kt * BK, bar);
-          tc::tma_load_2d_pair(a + A_BYTES + B_BYTES / 2, &map_w, n0 + 64, pb * p.kw + kt * BK, bar);
+          if (!(ok = __all_sync(0xffffffffu, tc::wait(bempty + 8 * s, ph)))) break;
+          if (tc::elect()) {
+            const uint32_t a = ring + s * STAGE_BYTES, b = a + A_BYTES, bar = lead + 8 * s;
+            if (rank == 0) tc::expect_tx(bfull + 8 * s, 2 * STAGE_BYTES);
+            tc::tma_load_2d_pair(a, &map_x, kt * BK, row_x, bar);
+            tc::tma_load_2d_pair(b, &map_w, n0, row_w, bar);
+            tc::tma_load_2d_pair(b + B_BYTES / 2, &map_w, n0 + 64, row_w, bar);
+          }
+          __syncwarp();
+          if (++s == STAGES) s = 0, ph ^= 1;
         }
       }
-      if (!ok) atomicExch(&failed, 1);
     }
+    if (!ok && lane == 0) atomicExch(&failed, 1);
   } else if (warp == 1) {
-    if (lane == 0 && rank == 0) {
+    if (rank == 0) {
       const uint32_t idesc = tc::idesc_f16(BM, BN, 1, 0, 1);
-      int it = 0, n = 0;
+      const uint32_t bfull = tc::smem_u32(full), bempty = tc::smem_u32(empty);
+      const uint64_t ad0 = tc::sdesc_sw128(tc::smem_u32(sm)), bd0 = tc::sdesc_sw128(tc::smem_u32(sm) + A_BYTES, B_BYTES / 2);
+      uint32_t s = 0, ph = 0, n = 0;
       bool ok = true;
       for (int t = first; t < ntiles && ok; t += step, ++n) {
-        const int a = n & 1;
-        if (n >= 2 && !(ok = tc::mbar_wait_cluster(&acc_empty[a], ((n >> 1) - 1) & 1, tc::kWaitCycles))) break;
+        const uint32_t a = n & 1;
+        // the epilogues have read this accumulator's previous tile
+        if (!(ok = __all_sync(0xffffffffu, tc::wait(tc::smem_u32(&acc_empty[a]), ((n >> 1) & 1) ^ 1)))) break;
         tc::fence_after_sync();
-        for (int i = 0; i < iters; ++i, ++it) {
-          const int s = it % STAGES;
-          if (!(ok = tc::mbar_wait_cluster(&full[s], (it / STAGES) & 1, tc::kWaitCycles))) break;
-          tc::fence_after_sync();
-          const uint32_t sa = tc::smem_u32(sm + s * STAGE_BYTES);
-          uint64_t ad = tc::sdesc_sw128(sa), bd = tc::sdesc_sw128(sa + A_BYTES, B_BYTES / 2);
+        for (int kt = 0; kt < p.nk && ok; ++kt) {
+          for (int pr = 0; pr < pairs; ++pr) {
+            if (!(ok = __all_sync(0xffffffffu, tc::wait(bfull + 8 * s, ph)))) break;
+            if (tc::elect()) {
+              const uint64_t ad = ad0 + s * (STAGE_BYTES >> 4), bd = bd0 + s * (STAGE_BYTES >> 4);
+              // K steps: 16 values further inside the swizzled rows of x, 16 rows further in W
 #pragma unroll
-          for (int ks = 0; ks < BK / 16; ++ks) {
-            tc::mma_f16_pair(tacc + a * BN, ad, bd, idesc, (i > 0 || ks > 0) ? 1u : 0u);
-            ad += 32 >> 4;           // 16 values further along K inside the swizzled row
-            bd += (16 * 128) >> 4;   // 16 rows of K further
+              for (int ks = 0; ks < BK / 16; ++ks)
+                tc::mma_f16_pair(tacc + a * BN, ad + ks * (32 >> 4), bd + ks * ((16 * 128) >> 4), idesc,
+                                 (kt > 0 || pr > 0 || ks > 0) ? 1u : 0u);
+              tc::mma_commit_pair(bempty + 8 * s, 3);
+            }
+            __syncwarp();
+            if (++s == STAGES) s = 0, ph ^= 1;
           }
-          tc::mma_commit_pair(&empty[s]);
         }
-        if (ok) tc::mma_commit_pair(&acc_full[a]);
+        if (ok && tc::elect()) tc::mma_commit_pair(tc::smem_u32(&acc_full[a]), 3);
+        __syncwarp();
       }
-      if (!ok) atomicExch(&failed, 1);
+      if (!ok && lane == 0) atomicExch(&failed, 1);
     }
   } else {
-    constexpr int CW = 128 / (int)sizeof(TO);        // columns of a block on the TMA path
+    constexpr int CW = 64 / (int)sizeof(TO);         // columns of a block on the TMA path
     const int e = warp - 2, q = warp & 3, half = e >> 2;
-    uint8_t* buf = blocks + e * 2 * BLK_BYTES;
+    constexpr int NBLK = 128 / CW;                   // blocks of a tile per warp
+    uint8_t* buf = blocks + e * NBUF * BLK_BYTES;
     const uint32_t lane_base = (uint32_t)(32 * q) << 16;
     const uint32_t release[2] = {tc::map_rank(&acc_empty[0], 0), tc::map_rank(&acc_empty[1], 0)};
     const TO* res = (const TO*)p.residual;
     TO* y = (TO*)p.y;
     const bool fetch = p.tma_out && res;
-    int blk = 0, n = 0;
+    uint32_t blk = 0, grp = 0, n = 0;   // blocks, groups of NBUF blocks and tiles so far
     bool ok = true;
-    // asks for the residual's block of (tile, column); the buffer's last store has been read
-    auto ask = [&](int b, int m, int c) {
-      if (lane == 0) {
-        tc::mbar_expect_tx(&res_full[e][b], BLK_BYTES);
-        tc::tma_load_2d(buf + b * BLK_BYTES, &map_r, c, m, &res_full[e][b]);
-      }
+    // the warp's part of tile t: 32 rows from row m, 128 columns from column c
+    auto part_of = [&](int t, int& m, int& c) {
+      const Tile tl = tile_at(t, ntm, ntn);
+      m = tl.m0 + (int)rank * 128 + 32 * q;
+      c = tl.n0 + half * 128;
     };
-    // the first block of this warp at or behind tile t that lies inside y, if any
-    auto ask_first = [&](int b, int t) {
-      for (; t < ntiles; t += step) {
-        const Tile tl = tile_at(t, ntm, ntn);
-        const int m = tl.m0 + (int)rank * 128 + 32 * q, c = tl.n0 + half * 128;
-        if (m < p.M && c < p.N) {
-          ask(b, m, c);
-          return;
-        }
+    // asks for the residual of the next group inside y, at or behind column ac
+    // of tile at: NBUF blocks into the warp's buffers, all of them free
+    auto ask = [&](int at, int ac) {
+      int m, c;
+      for (; at < ntiles; at += step, ac = 0) {
+        part_of(at, m, c);
+        if (m < p.M && ac < 128 && c + ac < p.N) break;
       }
+      if (at < ntiles && tc::elect()) {
+        const int cnt = min(NBUF, (p.N - c - ac + CW - 1) / CW);
+        tc::mbar_expect_tx(&res_full[e], cnt * BLK_BYTES);
+        for (int i = 0; i < cnt; ++i) tc::tma_load_2d(buf + i * BLK_BYTES, &map_r, c + ac + i * CW, m, &res_full[e]);
+      }
+      __syncwarp();
     };
-    if (fetch) ask_first(0, first);
+    auto ask_next = [&](int at, int ac) {
+      if (lane == 0) tc::bulk_wait_read<0>();   // the buffers' stores have been read
+      __syncwarp();
+      ask(at, ac);
+    };
+    if (fetch) ask(first, 0);
     for (int t = first; t < ntiles; t += step, ++n) {
       const int a = n & 1;
-      ok = __all_sync(0xffffffffu, tc::mbar_wait_cluster(&acc_full[a], (n >> 1) & 1, tc::kWaitCycles));
+      ok = __all_sync(0xffffffffu, tc::wait(tc::smem_u32(&acc_full[a]), (n >> 1) & 1));
       if (!ok) break;
       tc::fence_after_sync();
-      const Tile tl = tile_at(t, ntm, ntn);
-      const int m = tl.m0 + (int)rank * 128 + 32 * q, cbeg = tl.n0 + half * 128;
+      int m, cbeg;
+      part_of(t, m, cbeg);
       const uint32_t col0 = tacc + a * BN + lane_base + half * 128;
       if (m < p.M && p.tma_out) {
-#pragma unroll 1
-        for (int c = 0; c < 128; c += CW) {
-          if (cbeg + c >= p.N) break;
-          const int b = blk & 1;
-          float v[CW];
-#pragma unroll
-          for (int j = 0; j < CW; j += 32) tc::tmem_ld32(col0 + c + j, v + j);
-#pragma unroll
-          for (int j = 0; j < CW; j += 32) tc::tmem_ld_wait32(v + j);
+        float v[2][CW], bias[2][CW];
+        auto fetch_block = [&](int c, float* vv, float* bb) {
+          if constexpr (CW == 32)
+            tc::tmem_ld32(col0 + c, vv);
+          else
+            tc::tmem_ld16(col0 + c, vv);
           if (p.bias) {
             const float* bp = p.bias + cbeg + c;
-            const bool whole = cbeg + c + CW <= p.N;
+            if (cbeg + c + CW <= p.N) {
 #pragma unroll
-            for (int j = 0; j < CW; j += 4) {
-              float bv[4];
-              if (whole) {
-                layer::load_vec<4>(bp + j, bv);
-              } else {
+              for (int j = 0; j < CW; j += 4) layer::load_vec<4>(bp + j, bb + j);
+            } else {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) bv[i] = cbeg + c + j + i < p.N ? bp[j + i] : 0.f;
-              }
-#pragma unroll
-              for (int i = 0; i < 4; ++i) v[j + i] += bv[i];
+              for (int j = 0; j < CW; ++j) bb[j] = cbeg + c + j < p.N ? bp[j] : 0.f;
             }
           }
+        };
+        fetch_block(0, v[0], bias[0]);
 #pragma unroll
-          for (int j = 0; j < CW; ++j) v[j] = linear::act_for<ACT, TO>(v[j]);
-          // the other buffer's store has been read: ask for its next block
-          if (lane == 0) tc::bulk_wait_read<0>();
-          if (fetch) {
-            if (c + CW < 128 && cbeg + c + CW < p.N)
-              ask(b ^ 1, m, cbeg + c + CW);
-            else
-              ask_first(b ^ 1, t + step);
-            ok = __all_sync(0xffffffffu, tc::mbar_wait(&res_full[e][b], (blk >> 1) & 1, tc::kWaitCycles));
-            if (!ok) break;
+        for (int i = 0; i < NBLK; ++i) {
+          const int c = i * CW;
+          if (cbeg + c >= p.N) break;
+          float* vv = v[i & 1];
+          float* bb = bias[i & 1];
+          if constexpr (CW == 32)
+            tc::tmem_ld_wait32(vv);
+          else
+            tc::tmem_ld_wait16(vv);
+          if (i + 1 < NBLK) fetch_block(c + CW, v[(i + 1) & 1], bias[(i + 1) & 1]);
+          if (p.bias)
+#pragma unroll
+            for (int j = 0; j < CW; ++j) vv[j] += bb[j];
+#pragma unroll
+          for (int j = 0; j < CW; j += 2) {
+            if constexpr (sizeof(TO) == 2) {
+              linear::activate_fast2<ACT>(vv[j], vv[j + 1]);
+            } else {
+              vv[j] = layer::activate<ACT>(vv[j]);
+              vv[j + 1] = layer::activate<ACT>(vv[j + 1]);
+            }
           }
-          __syncwarp();
-          uint8_t* row = buf + b * BLK_BYTES + lane * 128;
+          const uint32_t b = fetch ? i % NBUF : blk % NBUF;
+          if (fetch) {
+            if (i % NBUF == 0) {
+              if (i > 0) ask_next(t, c);
+              if (!(ok = __all_sync(0xffffffffu, tc::wait(tc::smem_u32(&res_full[e]), grp & 1)))) break;
+              ++grp;
+            }
+          } else {
+            if (lane == 0) tc::bulk_wait_read<NBUF - 1>();
+            __syncwarp();
+          }
+          uint8_t* row = buf + b * BLK_BYTES + lane * 64;
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
+          for (int j = 0; j < 4; ++j) {
             constexpr int PER = 16 / (int)sizeof(TO);
-            TO* at = reinterpret_cast<TO*>(row + ((j ^ (lane & 7)) << 4));
+            TO* at = reinterpret_cast<TO*>(row + ((j ^ ((lane >> 1) & 3)) << 4));
             if (res) {
               float r[PER];
               layer::load_vec<PER>(at, r);
 #pragma unroll
-              for (int i = 0; i < PER; ++i) v[j * PER + i] += r[i];
+              for (int k = 0; k < PER; ++k) vv[j * PER + k] += r[k];
             }
-            layer::store_vec<PER>(at, v + j * PER);
+            layer::store_vec<PER>(at, vv + j * PER);
           }
           tc::fence_smem_to_async();
           __syncwarp();
-          if (lane == 0) {
+          if (lane == 0) {   // always lane 0: it waits for its own stores
             tc::tma_store_2d(&map_y, cbeg + c, m, buf + b * BLK_BYTES);
             tc::bulk_commit();
           }
           ++blk;
         }
+        tc::tmem_ld_wait();
         if (!ok) break;
       } else if (m < p.M) {
-        float* st = reinterpret_cast<float*>(buf);
+        float* st = reinterpret_cast<float*>(buf);   // 32 rows of 16 values, stride 17
 #pragma unroll 1
-        for (int c = 0; c < 128; c += 32) {
+        for (int c = 0; c < 128; c += 16) {
           if (cbeg + c >= p.N) break;
-          float v[32];
-          tc::tmem_ld32(col0 + c, v);
-          tc::tmem_ld_wait32(v);
+          float v[16];
+          tc::tmem_ld16(col0 + c, v);
+          tc::tmem_ld_wait16(v);
 #pragma unroll
-          for (int j = 0; j < 32; ++j) st[lane * 33 + j] = v[j];
+          for (int j = 0; j < 16; ++j) st[lane * 17 + j] = v[j];
           __syncwarp();
-          const int col = cbeg + c + lane;
+          const int col = cbeg + c + lane % 16;
           if (col < p.N) {
             const float bv = p.bias ? p.bias[col] : 0.f;
             const int rows = min(32, p.M - m);
 #pragma unroll 4
-            for (int r = 0; r < rows; ++r) {
+            for (int r = lane / 16; r < rows; r += 2) {
               const size_t at = (size_t)(m + r) * p.N + col;
-              float o = linear::act_for<ACT, TO>(st[r * 33 + lane] + bv);
+              float o = linear::act_for<ACT, TO>(st[r * 17 + lane % 16] + bv);
               if (res) o += layer::to_f32(res[at]);
               y[at] = layer::from_f32<TO>(o);
             }
@@ -277,9 +325,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHR, 1)
       tc::fence_before_sync();
       __syncwarp();
       if (lane == 0) tc::mbar_arrive_remote(release[a]);
+      if (fetch && m < p.M && cbeg < p.N) ask_next(t + step, 0);
     }
     if (!ok && lane == 0) atomicExch(&failed, 1);
-    if (lane == 0) tc::bulk_wait_all();
+    if (lane == 0) tc::bulk_wait_read<0>();
   }
   tc::fence_before_sync();
   __syncthreads();
@@ -302,16 +351,15 @@ cudaError_t launch_pair(const linear::TcCall& c, cudaStream_t st) {
   Params p{c.M, c.N, (c.K + BK - 1) / BK, c.planes, c.K, c.bias, c.residual, c.y, 0, c.status};
   const uint64_t row = (uint64_t)c.N * sizeof(TO);
   p.tma_out = row % 16 == 0 && layer::aligned16(c.y) && layer::aligned16(c.residual) && layer::aligned16(c.bias) &&
-              tc::tensor_map_2d(&my, c.y, sizeof(TO) == 2, c.M, c.N, row, 32) &&
-              tc::tensor_map_2d(&mr, c.residual ? c.residual : c.y, sizeof(TO) == 2, c.M, c.N, row, 32);
+              tc::tensor_map_2d(&my, c.y, sizeof(TO) == 2, c.M, c.N, row, 32, 64) &&
+              tc::tensor_map_2d(&mr, c.residual ? c.residual : c.y, sizeof(TO) == 2, c.M, c.N, row, 32, 64);
   if (!p.tma_out) mr = my = mx;   // not used
   auto kern = k_linear_pair<ACT, TO>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
   if (e != cudaSuccess) return e;
   const long long tiles = (long long)((c.M + BM - 1) / BM) * ((c.N + BN - 1) / BN);
   const int grid = (int)std::min<long long>(tiles, layer::sm_count() / 2) * 2;
-  kern<<<grid, NTHR, SMEM, st>>>(mx, mw, mr, my, p);
-  return cudaGetLastError();
+  return tc::launch_overlapped(kern, dim3(grid), dim3(NTHR), SMEM, st, mx, mw, mr, my, p);
 }
 
 }  // namespace

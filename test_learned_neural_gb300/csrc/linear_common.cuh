@@ -5,23 +5,91 @@
 
 namespace linear {
 
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // Fast activations for results that are rounded to bf16 (errors near 1e-6,
-// the rounding 2^-9).  GELU: erf by Abramowitz and Stegun 7.1.26, |error| <=
-// 1.5e-7.
+// the rounding 2^-9).  GELU: erf by Abramowitz and Stegun 7.1.28, |error| <=
+// 3e-7, one special-function instruction (7.1.26 needs two, and 128 x 256
+// values per tile make that unit the epilogue's limit).
+__device__ __forceinline__ constexpr float erf_coef(int i) {
+  return i == 0   ? 0.0705230784f
+         : i == 1 ? 0.0422820123f
+         : i == 2 ? 0.0092705272f
+         : i == 3 ? 0.0001520143f
+         : i == 4 ? 0.0002765672f
+                  : 0.0000430638f;
+}
 template <int ACT>
 __device__ __forceinline__ float activate_fast(float z) {
-  if constexpr (ACT == ATLAS_ACT_SILU) return __fdividef(z, 1.f + __expf(-z));
+  if constexpr (ACT == ATLAS_ACT_SILU) return z * rcp(1.f + ex2(z * -1.4426950408889634f));
   if constexpr (ACT == ATLAS_ACT_GELU) {
     const float x = fabsf(z) * 0.70710678118654752f;
-    const float t = __fdividef(1.f, fmaf(0.3275911f, x, 1.f));
-    float p = fmaf(1.061405429f, t, -1.453152027f);
-    p = fmaf(p, t, 1.421413741f);
-    p = fmaf(p, t, -0.284496736f);
-    p = fmaf(p, t, 0.254829592f);
-    const float e = 1.f - p * t * __expf(-x * x);   // erf(|z| / sqrt 2)
-    return 0.5f * z * (1.f + copysignf(e, z));
+    float d = fmaf(erf_coef(5), x, erf_coef(4));
+#pragma unroll
+    for (int i = 3; i >= 0; --i) d = fmaf(d, x, erf_coef(i));
+    d = fmaf(d, x, 1.f);
+    d *= d;
+    d *= d;
+    d *= d;
+    d *= d;
+    const float h = 0.5f * z;
+    return fmaf(fabsf(h), 1.f - rcp(d), h);   // z (1 + sign(z) erf(|z| / sqrt 2)) / 2
   }
   return z;
+}
+
+// Pairs of fp32 values: one instruction for two.
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t r, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(r));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+// activate_fast of two values (the scalar formulas, in pairs)
+template <int ACT>
+__device__ __forceinline__ void activate_fast2(float& za, float& zb) {
+  if constexpr (ACT == ATLAS_ACT_GELU) {
+    auto k2 = [](float c) { return pack2(c, c); };
+    const uint64_t h = mul2(pack2(za, zb), k2(0.5f));
+    const uint64_t x = mul2(pack2(fabsf(za), fabsf(zb)), k2(0.70710678118654752f));
+    uint64_t d = fma2(k2(erf_coef(5)), x, k2(erf_coef(4)));
+#pragma unroll
+    for (int i = 3; i >= 0; --i) d = fma2(d, x, k2(erf_coef(i)));
+    d = fma2(d, x, k2(1.f));
+    d = mul2(d, d);
+    d = mul2(d, d);
+    d = mul2(d, d);
+    d = mul2(d, d);
+    float da, db, ha, hb;
+    unpack2(d, da, db);
+    unpack2(h, ha, hb);
+    za = fmaf(fabsf(ha), 1.f - rcp(da), ha);
+    zb = fmaf(fabsf(hb), 1.f - rcp(db), hb);
+  } else {
+    za = activate_fast<ACT>(za);
+    zb = activate_fast<ACT>(zb);
+  }
 }
 
 template <int ACT, typename TO>

@@ -6,6 +6,7 @@
 #include <new>
 
 #include "decay_common.cuh"
+#include "decay_tc.cuh"
 
 using namespace layer;
 using decay::Geom;
@@ -280,9 +281,28 @@ struct Plan {
   int path, C, slices, nseg, seg;
 };
 
-// A call whose (row, head, slice) triples leave SMs idle is split along the
-// tokens as far as two CTAs per SM, in segments of at least two chunks.
-Plan make_plan(const atlas_decay_config& c, int B, int T) {
+// Segments of the tokens for `ctas` (row, head, slice) triples of `chunks`
+// chunks each.  One segment per triple reads every input once; n segments cost
+// another pass over k and v for the states at their starts (`extra` of a
+// chunk's time, measured 0.4) and two more launches (about 3 chunks' time), so
+// n is the one with the least of
+//   waves of the read-out pass + waves of the state pass + launches.
+int best_segments(long long ctas, long long chunks, long long slots) {
+  long long best = 1;
+  double cost = 0;
+  for (long long n = 1; n <= std::min(chunks, 1024LL); ++n) {
+    const long long per = (chunks + n - 1) / n;
+    if (n > 1 && (chunks + per - 1) / per != n) continue;
+    const long long waves = (ctas * n + slots - 1) / slots, before = (ctas * (n - 1) + slots - 1) / slots;
+    const double c = (double)waves * per + (n > 1 ? 0.4 * before * per + 3 : 0);
+    if (n == 1 || c < cost) best = n, cost = c;
+    if (ctas * n > 4 * slots) break;
+  }
+  return (int)best;
+}
+
+// `tc`: the tensors' addresses allow the tensor-core chunks
+Plan make_plan(const atlas_decay_config& c, int B, int T, bool tc) {
   Plan pl;
   pl.slices = (c.d_v + kSlice - 1) / kSlice;
   pl.nseg = 1;
@@ -292,14 +312,14 @@ Plan make_plan(const atlas_decay_config& c, int B, int T) {
     pl.C = 1;
     return pl;
   }
-  pl.path = 1;
-  pl.C = chunk_tokens(c.d_k);
-  const long long ctas = (long long)B * c.H * pl.slices, want = 2LL * sm_count();
+  tc = tc && c.qkv_dtype == ATLAS_BF16 && c.d_k % 8 == 0 && c.d_v % 8 == 0 && c.d_k <= 128;
+  pl.path = tc ? 2 : 1;
+  pl.C = tc ? decay::kTcChunk : chunk_tokens(c.d_k);
+  // CTAs that run at once: two per SM where their shared memory allows it
+  const long long slots = (c.d_k <= 64 ? 2LL : 1LL) * sm_count();
   const long long chunks = (T + pl.C - 1) / pl.C;
-  long long n = ctas >= sm_count() ? 1 : (want + ctas - 1) / ctas;
-  n = std::min(n, std::max(1LL, chunks / 2));
-  const long long per = (chunks + n - 1) / n;
-  pl.seg = (int)(per * pl.C);
+  const long long n = best_segments((long long)B * c.H * pl.slices, chunks, slots);
+  pl.seg = (int)((chunks + n - 1) / n * pl.C);
   pl.nseg = (int)((T + pl.seg - 1) / pl.seg);
   return pl;
 }
@@ -344,8 +364,10 @@ extern "C" int atlas_decay_create(const atlas_decay_config* cfg, atlas_decay_han
 
 extern "C" size_t atlas_decay_workspace_bytes(const atlas_decay_handle* h, int B, int T) {
   if (!h || B < 1 || T < 1) return 0;
-  const Plan pl = make_plan(h->cfg, B, T);
-  return pl.nseg > 1 ? (size_t)B * h->cfg.H * pl.nseg * h->cfg.d_k * h->cfg.d_v * sizeof(float) : 0;
+  // the larger of the two paths': which one runs depends on the tensors' addresses
+  int nseg = 1;
+  for (bool tc : {false, true}) nseg = std::max(nseg, make_plan(h->cfg, B, T, tc).nseg);
+  return nseg > 1 ? (size_t)B * h->cfg.H * nseg * h->cfg.d_k * h->cfg.d_v * sizeof(float) : 0;
 }
 
 namespace {
@@ -378,10 +400,14 @@ cudaError_t launch_big(K kern, dim3 grid, size_t smem, const Geom& g, const Ptrs
   return cudaGetLastError();
 }
 
-cudaError_t launch_scan(const Geom& g, const Ptrs& p, cudaStream_t st) {
+}  // namespace
+
+cudaError_t decay::scan_launch(const Geom& g, const Ptrs& p, cudaStream_t st) {
   k_decay_scan<<<dim3((unsigned)(((size_t)g.d_k * g.d_v + 255) / 256), (unsigned)(g.B * g.H)), 256, 0, st>>>(g, p);
   return cudaGetLastError();
 }
+
+namespace {
 
 template <typename TI, typename TO, int C>
 cudaError_t launch_chunks(const Geom& g, const Ptrs& p, cudaStream_t st) {
@@ -390,7 +416,7 @@ cudaError_t launch_chunks(const Geom& g, const Ptrs& p, cudaStream_t st) {
     cudaError_t e = launch_big(k_decay_chunk<TI, TO, C, false>, dim3(g.nseg - 1, g.slices, units),
                                chunk_smem(g.d_k, false), g, p, st);
     if (e != cudaSuccess) return e;
-    e = launch_scan(g, p, st);
+    e = decay::scan_launch(g, p, st);
     if (e != cudaSuccess) return e;
   }
   return launch_big(k_decay_chunk<TI, TO, C, true>, dim3(g.nseg, g.slices, units), chunk_smem(g.d_k, true), g, p, st);
@@ -418,8 +444,10 @@ extern "C" int atlas_decay_forward(atlas_decay_handle* h, const atlas_decay_io* 
   if ((long long)io->B * c.H * ((c.d_v + kSlice - 1) / kSlice) > 0x7fffffffLL)
     return h->fail(ATLAS_ERR_UNSUPPORTED, "B * H too large for one call");
   cudaStream_t st = (cudaStream_t)stream;
-  const Plan pl = make_plan(c, io->B, io->T);
-  int rc = h->grow(atlas_decay_workspace_bytes(h, io->B, io->T));
+  const Plan pl = make_plan(c, io->B, io->T,
+                            aligned16(io->q) && aligned16(io->k) && aligned16(io->v) && aligned16(io->y));
+  int rc = pl.path == 2 ? h->need_status(st) : ATLAS_OK;
+  if (!rc) rc = h->grow(atlas_decay_workspace_bytes(h, io->B, io->T));
   if (rc) return rc;
 
   Geom g;
@@ -436,7 +464,8 @@ extern "C" int atlas_decay_forward(atlas_decay_handle* h, const atlas_decay_io* 
   strides(c.y_layout, c.H, c.d_v, g.y_b, g.y_h, g.y_t);
   const Ptrs p{io->q, io->k, io->v, io->decay, io->lens, io->S0, io->y, io->S_out, (float*)h->ws};
   const bool ib = c.qkv_dtype == ATLAS_BF16, ob = c.y_dtype == ATLAS_BF16;
-  const cudaError_t e = ib ? (ob ? launch<bf16, bf16>(pl, g, p, st) : launch<bf16, float>(pl, g, p, st))
+  const cudaError_t e = pl.path == 2 ? decay::tc_launch(g, p, ob, h->status, st)
+                        : ib ? (ob ? launch<bf16, bf16>(pl, g, p, st) : launch<bf16, float>(pl, g, p, st))
                            : (ob ? launch<float, bf16>(pl, g, p, st) : launch<float, float>(pl, g, p, st));
   if (e != cudaSuccess) return h->cuda_fail("decay attention launch", e);
   h->path = pl.path;

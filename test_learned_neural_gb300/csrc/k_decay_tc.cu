@@ -1,0 +1,639 @@
+// Decay attention on the tensor cores: bf16 q, k, v, head widths up to 128
+// (d_k) and any d_v in slices of 64 columns, chunks of 128 tokens
+// (decay_common.cuh has the formulas).
+//
+// k_decay_tc, one CTA per (segment, slice, unit), chunks in order.  Per chunk:
+//   scores  Q K^T                      M = 128 tokens, N = 128
+//   inter   Q S                        N = 64, S split into bf16 terms
+//   intra   P V, P = scores * decays   P from TMEM, split into NT terms
+//   state   (w K)^T V, w_j = g^{n-1-j} w K split into three bf16 terms (24
+//           bits), V exact, so the fp32 state keeps fp32 accuracy
+// The decays are applied in fp32 registers; the state lives there too, fp32,
+// for the whole segment.  NT = 1 for bf16 read-outs: P is rounded to bf16 and
+// S to two terms (2^-16), each below the read-out's own rounding.  NT = 3 for
+// fp32 read-outs: three terms of both.
+//
+// TMEM (256 columns, so that two CTAs share an SM where d_k <= 64): scores,
+// then P in place, then the state's product, in 128 columns; inter and intra
+// read-outs 64 columns each.
+//
+// k_decay_tc_state: a segment's own contribution to the state at its end, the
+// same product with weights counted to the segment's end, accumulated in TMEM
+// over the whole segment.
+#include "decay_common.cuh"
+#include "decay_tc.cuh"
+#include "tc2.cuh"
+
+using decay::Geom;
+using decay::Ptrs;
+using layer::bf16;
+
+namespace {
+
+constexpr int C = 128, NTHR = 256, SL = 64;   // tokens per chunk, threads, columns per slice
+constexpr int TILE = C * 128;                 // 128 rows of 64 bf16 values
+
+// 4-D map over [row][head][token][d] in either layout: boxes of 64 bf16 or 32
+// fp32 values x 128 tokens, 128-byte swizzled
+bool map_4d(CUtensorMap* map, const void* base, bool is_bf16, int d, int T, int heads, int B, size_t st, size_t sh,
+            size_t sb) {
+  auto fn = tc::tensor_map_encoder();
+  if (!fn) return false;
+  const size_t es = is_bf16 ? 2 : 4;
+  const cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)T, (cuuint64_t)heads, (cuuint64_t)B};
+  const cuuint64_t strides[3] = {st * es, sh * es, sb * es};
+  const cuuint32_t box[4] = {is_bf16 ? 64u : 32u, (cuuint32_t)C, 1, 1}, estr[4] = {1, 1, 1, 1};
+  return fn(map, is_bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4,
+            const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+__device__ __forceinline__ void load_4d(uint32_t dst, const CUtensorMap* map, int c, int t, int h, int b, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(
+          dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c), "r"(t), "r"(h), "r"(b), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void store_4d(const CUtensorMap* map, int c, int t, int h, int b, uint32_t src) {
+  asm volatile("cp.async.bulk.tensor.4d.global.shared::cta.bulk_group [%0, {%1, %2, %3, %4}], [%5];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(c), "r"(t), "r"(h), "r"(b), "r"(src)
+               : "memory");
+}
+// D (+)= A B^T with A (16-bit, two values of K per column) in TMEM
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// 16 packed columns of this warp's lanes
+__device__ __forceinline__ void tmem_st16u(uint32_t taddr, const uint32_t* v) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
+}
+__device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+__device__ __forceinline__ void lds128(uint32_t addr, uint32_t* w) {
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+               : "r"(addr)
+               : "memory");
+}
+// byte offset of 16-byte chunk j of row r in a 128-byte swizzled tile
+__device__ __forceinline__ uint32_t swz(int r, int j) { return (uint32_t)(r * 128 + ((j ^ (r & 7)) << 4)); }
+
+// Two fp32 values as N packed bf16 pairs whose sums are the values to 8 N
+// bits: each term but the last is the remainder's leading bits cut off, so the
+// subtraction is exact; the last is rounded.
+template <int N>
+__device__ __forceinline__ void split2(float a, float b, uint32_t* w) {
+#pragma unroll
+  for (int i = 0; i + 1 < N; ++i) {
+    const uint32_t ua = __float_as_uint(a), ub = __float_as_uint(b);
+    w[i] = __byte_perm(ua, ub, 0x7632);
+    a -= __uint_as_float(ua & 0xffff0000u);
+    b -= __uint_as_float(ub & 0xffff0000u);
+  }
+  w[N - 1] = layer::pack_bf16(a, b);
+}
+
+// Rows n .. 127 of a tile become zero (a row's tokens past its length: 0 * NaN
+// must not reach the sums).
+__device__ __forceinline__ void zero_rows(uint32_t tile, int n, int tid) {
+  for (int i = tid; i < (C - n) * 8; i += NTHR) sts128(tile + (n + i / 8) * 128 + (i % 8) * 16, 0, 0, 0, 0);
+}
+
+// Token tid % 128's 32 keys of half tid / 128 of a 64-wide tile, times w, in
+// three bf16 terms: term 0 stays packed in k0, terms 1 and 2 go to their tiles.
+__device__ __forceinline__ void scale_keys(uint32_t ktile, uint32_t t1, uint32_t t2, float w, bool live, int tid,
+                                           uint32_t* k0) {
+  const int r = tid & (C - 1), j0 = (tid >> 7) * 4;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    uint32_t x[4], y[4][3];
+    lds128(ktile + swz(r, j0 + j), x);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (!live) x[i] = 0u;
+      split2<3>(__uint_as_float(x[i] << 16) * w, __uint_as_float(x[i] & 0xffff0000u) * w, y[i]);
+      k0[4 * j + i] = y[i][0];
+    }
+    sts128(t1 + swz(r, j0 + j), y[0][1], y[1][1], y[2][1], y[3][1]);
+    sts128(t2 + swz(r, j0 + j), y[0][2], y[1][2], y[2][2], y[3][2]);
+  }
+}
+__device__ __forceinline__ void store_keys(uint32_t tile, int tid, const uint32_t* k0) {
+  const int r = tid & (C - 1), j0 = (tid >> 7) * 4;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) sts128(tile + swz(r, j0 + j), k0[4 * j], k0[4 * j + 1], k0[4 * j + 2], k0[4 * j + 3]);
+}
+
+// (w K)^T V into TMEM at d: three terms of KB 64-wide key tiles, one
+// instruction per 16 tokens; terms at t0, t1, t2 (tiles of a term KB * TILE
+// bytes), M = 64 KB
+template <int KB>
+__device__ __forceinline__ void mma_state(uint32_t d, uint32_t t0, uint32_t t1, uint32_t t2, uint32_t vtile,
+                                          bool accumulate) {
+  const uint32_t idesc = tc::idesc_f16(64 * KB, SL, 1, 1, 1);
+  const uint64_t vd = tc::sdesc_sw128(vtile, TILE);
+  const uint64_t kd[3] = {tc::sdesc_sw128(t0, TILE), tc::sdesc_sw128(t1, TILE), tc::sdesc_sw128(t2, TILE)};
+#pragma unroll
+  for (int i = 2; i >= 0; --i)
+#pragma unroll
+    for (int s = 0; s < C / 16; ++s)
+      tc::mma_f16(d, kd[i] + s * (2048 >> 4), vd + s * (2048 >> 4), idesc, (accumulate || i < 2 || s > 0) ? 1u : 0u);
+}
+
+// The state's product as the threads hold it: KB = 1: M = 64, row 16 q + lane
+// % 16, 16 columns from 32 h + 16 (lane / 16); KB = 2: row 32 q + lane, 32
+// columns from 32 h (warp = q + 4 h).
+template <int KB>
+struct StatePart {
+  static constexpr int N = 16 * KB;
+  int row, col;
+  __device__ StatePart(int warp, int lane) {
+    const int q = warp & 3, h = warp >> 2;
+    row = KB == 1 ? 16 * q + lane % 16 : 32 * q + lane;
+    col = KB == 1 ? 32 * h + 16 * (lane / 16) : 32 * h;
+  }
+  __device__ __forceinline__ void load(uint32_t tmem, int warp, float* v) const {
+    const uint32_t at = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + 32 * (warp >> 2);
+    if constexpr (KB == 1) {
+      tc::tmem_ld16_x2(at, v);
+      tc::tmem_ld_wait16(v);
+    } else {
+      tc::tmem_ld32(at, v);
+      tc::tmem_ld_wait32(v);
+    }
+  }
+};
+
+template <int KB, int NT>
+struct Smem {   // byte offsets from a 1024-byte aligned base
+  static constexpr int q = 0, k = q + KB * TILE, v = k + KB * TILE, k1 = v + TILE, k2 = k1 + KB * TILE,
+                       s = k2 + KB * TILE, NS = NT == 1 ? 2 : 3, s_tile = KB * 64 * 128,
+                       y = NT == 1 ? s + NS * s_tile : q,   // read-outs: a tile of their own, or q's once it is read
+                       pw = NT == 1 ? y + TILE : s + NS * s_tile, bars = pw + (C + 4) * 4, end = bars + 64;
+};
+
+template <int KB, int NT, typename TO>
+__global__ void __launch_bounds__(NTHR, KB == 1 ? 2 : 1)
+    k_decay_tc(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+               const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap my, Geom g, Ptrs p,
+               int* status) {
+  using L = Smem<KB, NT>;
+  extern __shared__ __align__(1024) uint8_t sm[];
+  const uint32_t base = tc::smem_u32(sm);
+  float* pw = reinterpret_cast<float*>(sm + L::pw);   // g^0 .. g^128
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sm + L::bars);
+  // full_q, full_kv, scores, intra, state, tmem base, failed
+  uint32_t* tbase = reinterpret_cast<uint32_t*>(bars + 6);
+  int* failed = reinterpret_cast<int*>(bars + 7);
+  const int s = blockIdx.x, sl = blockIdx.y, unit = blockIdx.z;
+  const int b = unit / g.H, h = unit % g.H, hq = h / g.share;
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, wq = warp & 3, wh = warp >> 2;
+  const uint32_t bq = tc::smem_u32(bars), bkv = bq + 8, bsc = bq + 16, bin = bq + 24, bst = bq + 32;
+  if (warp == 0) tc::tmem_alloc(tbase, 256);
+  if (tid == 32) {
+    for (int i = 0; i < 5; ++i) tc::mbar_init_only(bars + i, 1);
+    tc::mbar_init_fence();
+    *failed = (base & 1023u) ? 1 : 0;   // the swizzled tiles need it; never seen otherwise
+    tc::prefetch_map(&mq);
+    tc::prefetch_map(&mk);
+    tc::prefetch_map(&mv);
+    tc::prefetch_map(&my);
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tm = *tbase;
+  tc::grid_dependency_wait();
+  tc::grid_dependents_launch();
+
+  const int live = decay::live_tokens(g, p, b);
+  const int t_lo = s * g.seg, t_hi = min(g.T, t_lo + g.seg), t_live = min(t_hi, max(live, t_lo));
+  const int c0 = sl * SL, cols = min(SL, g.d_v - c0);
+  const size_t sq = (size_t)g.d_k * g.d_v;
+  bool ok = *failed == 0;
+
+  auto load_q = [&](int t0) {
+    tc::expect_tx(bq, KB * TILE);
+    for (int i = 0; i < KB; ++i) load_4d(base + L::q + i * TILE, &mq, 64 * i, t0, hq, b, bq);
+  };
+  auto load_kv = [&](int t0) {
+    tc::expect_tx(bkv, (KB + 1) * TILE);
+    for (int i = 0; i < KB; ++i) load_4d(base + L::k + i * TILE, &mk, 64 * i, t0, hq, b, bkv);
+    load_4d(base + L::v, &mv, c0, t0, h, b, bkv);
+  };
+  if (ok && t_lo < t_live && warp == 0) {
+    if (tc::elect()) {
+      load_q(t_lo);
+      load_kv(t_lo);
+    }
+    __syncwarp();
+  }
+  const float l2g = log2f(p.decay[h]);
+  for (int i = tid; i <= C; i += NTHR) pw[i] = decay::power(l2g, i);
+
+  // the state, fp32, and its bf16 terms as the operand of Q S: rows d_k, 64
+  // values of d_v
+  const StatePart<KB> part(warp, lane);
+  float S[StatePart<KB>::N];
+  {
+    const float* start = g.nseg > 1 ? p.seg + ((size_t)unit * g.nseg + s) * sq : p.S0 ? p.S0 + unit * sq : nullptr;
+#pragma unroll
+    for (int i = 0; i < StatePart<KB>::N; ++i)
+      S[i] = start && part.row < g.d_k && part.col + i < cols ? start[(size_t)part.row * g.d_v + c0 + part.col + i] : 0.f;
+  }
+  auto state_tiles = [&]() {
+#pragma unroll
+    for (int i = 0; i < StatePart<KB>::N; i += 8) {
+      uint32_t w[4][L::NS];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) split2<L::NS>(S[i + 2 * j], S[i + 2 * j + 1], w[j]);
+#pragma unroll
+      for (int n = 0; n < L::NS; ++n)
+        sts128(base + L::s + n * L::s_tile + swz(part.row, (part.col + i) / 8), w[0][n], w[1][n], w[2][n], w[3][n]);
+    }
+  };
+  state_tiles();
+  tc::fence_smem_to_async();
+  __syncthreads();
+
+  const uint32_t lanes = (uint32_t)(32 * wq) << 16;
+  const int row = 32 * wq + lane;   // token of this thread in the chunk's scores and read-outs
+  uint32_t ph = 0;
+  for (int t0 = t_lo; ok && t0 < t_live; t0 += C, ph ^= 1) {
+    const int n = min(C, t_live - t0);
+    ok &= tc::wait(bq, ph);
+    ok &= tc::wait(bkv, ph);
+    auto mma_inter = [&]() {   // Q S, the smallest terms first
+      const uint32_t idesc = tc::idesc_f16(C, SL, 1, 0, 1);
+#pragma unroll
+      for (int i = L::NS - 1; i >= 0; --i)
+#pragma unroll
+        for (int ks = 0; ks < 4 * KB; ++ks)
+          tc::mma_f16(tm + 128, tc::sdesc_sw128(base + L::q + (ks / 4) * TILE) + (ks % 4) * (32 >> 4),
+                      tc::sdesc_sw128(base + L::s + i * L::s_tile, 8192) + ks * (2048 >> 4), idesc,
+                      (i < L::NS - 1 || ks > 0) ? 1u : 0u);
+    };
+    if (warp == 0) {
+      if (tc::elect()) {
+        const uint32_t idesc = tc::idesc_f16(C, C, 1, 0, 0);
+#pragma unroll
+        for (int ks = 0; ks < 4 * KB; ++ks)
+          tc::mma_f16(tm, tc::sdesc_sw128(base + L::q + (ks / 4) * TILE) + (ks % 4) * (32 >> 4),
+                      tc::sdesc_sw128(base + L::k + (ks / 4) * TILE) + (ks % 4) * (32 >> 4), idesc, ks > 0 ? 1u : 0u);
+        if constexpr (NT == 1) mma_inter();
+        tc::mma_commit(bars + 2);
+      }
+      __syncwarp();
+    }
+    // keys times decays; the first term waits in registers until the scores have read the keys
+    uint32_t k0[KB][16];
+    {
+      const int r = tid & (C - 1);
+      const float w = r < n ? pw[n - 1 - r] : 0.f;
+#pragma unroll
+      for (int i = 0; i < KB; ++i)
+        scale_keys(base + L::k + i * TILE, base + L::k1 + i * TILE, base + L::k2 + i * TILE, w, r < n, tid, k0[i]);
+      if (n < C) zero_rows(base + L::v, n, tid);
+    }
+    ok &= tc::wait(bsc, ph);
+    tc::fence_after_sync();
+#pragma unroll
+    for (int i = 0; i < KB; ++i) store_keys(base + L::k + i * TILE, tid, k0[i]);
+    // P: 32 x 32 blocks, two per warp; full ones below the diagonal
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int blk = wh == 0 ? 3 * u : 1 + u;   // columns 32 blk ..
+      uint32_t w[16][NT];
+      if (blk > wq) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+#pragma unroll
+          for (int k = 0; k < NT; ++k) w[i][k] = 0u;
+      } else {
+        float v[32];
+        tc::tmem_ld32(tm + lanes + 32 * blk, v);
+        tc::tmem_ld_wait32(v);
+        if (blk < wq) {
+          const float f = pw[row - 32 * blk - 31];   // times g^{31 - c}
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            split2<NT>(v[2 * i] * (f * pw[31 - 2 * i]), v[2 * i + 1] * (f * pw[30 - 2 * i]), w[i]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const float a = lane >= 2 * i ? v[2 * i] * pw[max(0, lane - 2 * i)] : 0.f;
+            const float c = lane >= 2 * i + 1 ? v[2 * i + 1] * pw[max(0, lane - 2 * i - 1)] : 0.f;
+            split2<NT>(a, c, w[i]);
+          }
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < NT; ++k) {
+        uint32_t x[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) x[i] = w[i][k];
+        // terms 0 and 1 inside the block's own columns, term 2 where Q S goes later
+        tmem_st16u(tm + lanes + (k < 2 ? 32 * blk + 16 * k : 128 + 16 * blk), x);
+      }
+    }
+    tc::tmem_st_wait();
+    tc::fence_smem_to_async();
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    if (warp == 0) {
+      if (tc::elect()) {
+        if constexpr (NT == 1)
+          if (t0 + C < t_live) load_q(t0 + C);   // scores and Q S have read q
+        const uint32_t idesc = tc::idesc_f16(C, SL, 1, 0, 1);
+        const uint64_t vd = tc::sdesc_sw128(base + L::v, TILE);
+#pragma unroll
+        for (int k = NT - 1; k >= 0; --k)
+#pragma unroll
+          for (int ks = 0; ks < 8; ++ks)
+            mma_ts(tm + 192, tm + (k < 2 ? 32 * (ks / 2) + 16 * k : 128 + 16 * (ks / 2)) + 8 * (ks % 2),
+                   vd + ks * (2048 >> 4), idesc, (k < NT - 1 || ks > 0) ? 1u : 0u);
+        tc::mma_commit(bars + 3);
+      }
+      __syncwarp();
+    }
+    ok &= tc::wait(bin, NT == 3 ? 0 : ph);   // P V done: its columns are free (NT = 3: two phases per chunk)
+    tc::fence_after_sync();
+    if (NT == 3) {
+      if (warp == 0) {
+        if (tc::elect()) {
+          mma_inter();
+          tc::mma_commit(bars + 3);
+        }
+        __syncwarp();
+      }
+    }
+    if (warp == 0) {
+      if (tc::elect()) {
+        mma_state<KB>(tm, base + L::k, base + L::k1, base + L::k2, base + L::v, false);
+        tc::mma_commit(bars + 4);
+      }
+      __syncwarp();
+    }
+    // the read-outs, 32 columns per thread
+    {
+      float yi[32], ya[32];
+      if (NT == 3) {
+        ok &= tc::wait(bin, 1);
+        tc::fence_after_sync();
+      }
+      tc::tmem_ld32(tm + 128 + lanes + 32 * wh, yi);
+      tc::tmem_ld32(tm + 192 + lanes + 32 * wh, ya);
+      tc::tmem_ld_wait32(yi);
+      tc::tmem_ld_wait32(ya);
+      const float f = pw[row + 1] * g.scale;
+#pragma unroll
+      for (int i = 0; i < 32; ++i) ya[i] = row < n ? fmaf(f, yi[i], g.scale * ya[i]) : 0.f;
+      if constexpr (sizeof(TO) == 2) {
+        if (lane == 0 && warp == 0) tc::bulk_wait_read<0>();   // the last chunk's store has been read
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          sts128(base + L::y + swz(row, 4 * wh + j), layer::pack_bf16(ya[8 * j], ya[8 * j + 1]),
+                 layer::pack_bf16(ya[8 * j + 2], ya[8 * j + 3]), layer::pack_bf16(ya[8 * j + 4], ya[8 * j + 5]),
+                 layer::pack_bf16(ya[8 * j + 6], ya[8 * j + 7]));
+        tc::fence_smem_to_async();
+        __syncthreads();
+        if (tid == 0) {
+          store_4d(&my, c0, t0, h, b, base + L::y);
+          tc::bulk_commit();
+        }
+      } else {
+        // 32 columns at a time through one tile
+        for (int half = 0; half < 2; ++half) {
+          if (half == 1 && cols <= 32) break;
+          if (wh == half)
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              sts128(base + L::y + swz(row, j), __float_as_uint(ya[4 * j]), __float_as_uint(ya[4 * j + 1]),
+                     __float_as_uint(ya[4 * j + 2]), __float_as_uint(ya[4 * j + 3]));
+          tc::fence_smem_to_async();
+          __syncthreads();
+          if (tid == 0) {
+            store_4d(&my, c0 + 32 * half, t0, h, b, base + L::y);
+            tc::bulk_commit();
+            tc::bulk_wait_read<0>();
+          }
+          __syncthreads();
+        }
+      }
+    }
+    // the state behind this chunk
+    ok &= tc::wait(bst, ph);
+    tc::fence_after_sync();
+    if (warp == 0 && t0 + C < t_live) {
+      if (tc::elect()) {
+        if constexpr (NT == 3) load_q(t0 + C);
+        load_kv(t0 + C);   // the state's product has read k and v
+      }
+      __syncwarp();
+    }
+    {
+      float d[StatePart<KB>::N];
+      part.load(tm, warp, d);
+      const float f = pw[n];
+#pragma unroll
+      for (int i = 0; i < StatePart<KB>::N; ++i) S[i] = fmaf(f, S[i], d[i]);
+    }
+    if (t0 + C < t_live) state_tiles();
+    tc::fence_smem_to_async();
+    tc::fence_before_sync();
+    ok = __syncthreads_and(ok);
+    tc::fence_after_sync();
+  }
+  if (ok) {
+    // read-outs past the row's length: whole chunks (the last live chunk wrote its own)
+    TO* y = (TO*)p.y + b * g.y_b + h * g.y_h + c0;
+    const int z0 = t_lo + (t_live - t_lo + C - 1) / C * C;
+    for (int t = z0 + tid / 64; t < t_hi; t += NTHR / 64)
+      if (tid % 64 < cols) y[t * g.y_t + tid % 64] = layer::from_f32<TO>(0.f);
+    if (s == g.nseg - 1 && p.S_out) {
+#pragma unroll
+      for (int i = 0; i < StatePart<KB>::N; ++i)
+        if (part.row < g.d_k && part.col + i < cols)
+          p.S_out[unit * sq + (size_t)part.row * g.d_v + c0 + part.col + i] = S[i];
+    }
+  } else if (tid == 0) {
+    // let the copies in flight land before the block's memory is freed
+    tc::wait(bq, ph);
+    tc::wait(bkv, ph);
+    atomicExch(status, ATLAS_ERR_TIMEOUT);
+  }
+  if (tid == 0) tc::bulk_wait_read<0>();
+  tc::fence_before_sync();
+  __syncthreads();
+  if (warp == 0) tc::tmem_dealloc(tm, 256);
+}
+
+// shared memory of k_decay_tc_state: two (k, v) buffers, three terms
+template <int KB>
+struct SmemState {
+  static constexpr int kv_bytes = (KB + 1) * TILE, t0 = 2 * kv_bytes, bars = t0 + 3 * KB * TILE, end = bars + 64;
+};
+
+template <int KB>
+__global__ void __launch_bounds__(NTHR, KB == 1 ? 2 : 1)
+    k_decay_tc_state(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv, Geom g, Ptrs p,
+                     int* status) {
+  using L = SmemState<KB>;
+  extern __shared__ __align__(1024) uint8_t sm[];
+  const uint32_t base = tc::smem_u32(sm);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sm + L::bars);   // full[2], done, tmem base, failed
+  uint32_t* tbase = reinterpret_cast<uint32_t*>(bars + 3);
+  int* failed = reinterpret_cast<int*>(bars + 4);
+  const int s = blockIdx.x, sl = blockIdx.y, unit = blockIdx.z;
+  const int b = unit / g.H, h = unit % g.H, hq = h / g.share;
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+  const uint32_t bfull = tc::smem_u32(bars), bdone = bfull + 16;
+  if (warp == 0) tc::tmem_alloc(tbase, 64);
+  if (tid == 32) {
+    for (int i = 0; i < 3; ++i) tc::mbar_init_only(bars + i, 1);
+    tc::mbar_init_fence();
+    *failed = (base & 1023u) ? 1 : 0;
+    tc::prefetch_map(&mk);
+    tc::prefetch_map(&mv);
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tm = *tbase;
+  tc::grid_dependency_wait();
+  tc::grid_dependents_launch();
+
+  const int live = decay::live_tokens(g, p, b);
+  const int t_lo = s * g.seg, t_hi = min(g.T, t_lo + g.seg), t_live = min(t_hi, max(live, t_lo));
+  const int c0 = sl * SL, cols = min(SL, g.d_v - c0), chunks = (t_live - t_lo + C - 1) / C;
+  bool ok = *failed == 0;
+  auto load = [&](int c) {
+    const uint32_t at = base + (c & 1) * L::kv_bytes, bar = bfull + 8 * (c & 1);
+    const int t0 = t_lo + c * C;
+    tc::expect_tx(bar, (KB + 1) * TILE);
+    for (int i = 0; i < KB; ++i) load_4d(at + i * TILE, &mk, 64 * i, t0, hq, b, bar);
+    load_4d(at + KB * TILE, &mv, c0, t0, h, b, bar);
+  };
+  if (ok && warp == 0) {
+    if (tc::elect())
+      for (int c = 0; c < min(2, chunks); ++c) load(c);
+    __syncwarp();
+  }
+  const float l2g = log2f(p.decay[h]);
+  for (int c = 0; ok && c < chunks; ++c) {
+    const int t0 = t_lo + c * C, n = min(C, t_live - t0);
+    const uint32_t kt = base + (c & 1) * L::kv_bytes, vt = kt + KB * TILE;
+    ok &= tc::wait(bfull + 8 * (c & 1), (c >> 1) & 1);
+    if (c > 0) ok &= tc::wait(bdone, (c - 1) & 1);   // the last product has read the terms
+    const int r = tid & (C - 1);
+    const float w = r < n ? decay::power(l2g, t_live - 1 - t0 - r) : 0.f;
+#pragma unroll
+    for (int i = 0; i < KB; ++i) {
+      uint32_t k0[16];
+      scale_keys(kt + i * TILE, base + L::t0 + (KB + i) * TILE, base + L::t0 + (2 * KB + i) * TILE, w, r < n, tid, k0);
+      store_keys(base + L::t0 + i * TILE, tid, k0);
+    }
+    if (n < C) zero_rows(vt, n, tid);
+    tc::fence_smem_to_async();
+    tc::fence_before_sync();
+    ok = __syncthreads_and(ok);
+    tc::fence_after_sync();
+    if (warp == 0 && ok) {
+      // the buffer of the chunk behind the next: free once its product is done
+      if (c >= 1 && c + 1 < chunks) {
+        if (tc::elect()) load(c + 1);
+        __syncwarp();
+      }
+      if (tc::elect()) {
+        mma_state<KB>(tm, base + L::t0, base + L::t0 + KB * TILE, base + L::t0 + 2 * KB * TILE, vt, c > 0);
+        tc::mma_commit(bars + 2);
+      }
+      __syncwarp();
+    }
+  }
+  if (ok && chunks > 0) ok = tc::wait(bdone, (chunks - 1) & 1);
+  tc::fence_after_sync();
+  ok = __syncthreads_and(ok);
+  if (ok) {
+    const StatePart<KB> part(warp, lane);
+    float d[StatePart<KB>::N];
+    if (chunks > 0) {
+      part.load(tm, warp, d);
+    } else {
+#pragma unroll
+      for (int i = 0; i < StatePart<KB>::N; ++i) d[i] = 0.f;
+    }
+    float* dst = p.seg + ((size_t)unit * g.nseg + s + 1) * ((size_t)g.d_k * g.d_v);
+#pragma unroll
+    for (int i = 0; i < StatePart<KB>::N; ++i)
+      if (part.row < g.d_k && part.col + i < cols) dst[(size_t)part.row * g.d_v + c0 + part.col + i] = d[i];
+  } else if (tid == 0) {
+    tc::wait(bfull, 0);
+    tc::wait(bfull + 8, 0);
+    atomicExch(status, ATLAS_ERR_TIMEOUT);
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  if (warp == 0) tc::tmem_dealloc(tm, 64);
+}
+
+template <int KB, int NT, typename TO>
+cudaError_t launch_out(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const CUtensorMap& my,
+                       const Geom& g, const Ptrs& p, int* status, cudaStream_t st) {
+  auto kern = k_decay_tc<KB, NT, TO>;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<KB, NT>::end);
+  if (e != cudaSuccess) return e;
+  return tc::launch_overlapped(kern, dim3(g.nseg, g.slices, g.B * g.H), dim3(NTHR), Smem<KB, NT>::end, st, mq, mk, mv,
+                               my, g, p, status);
+}
+template <int KB>
+cudaError_t launch_state(const CUtensorMap& mk, const CUtensorMap& mv, const Geom& g, const Ptrs& p, int* status,
+                         cudaStream_t st) {
+  auto kern = k_decay_tc_state<KB>;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SmemState<KB>::end);
+  if (e != cudaSuccess) return e;
+  return tc::launch_overlapped(kern, dim3(g.nseg - 1, g.slices, g.B * g.H), dim3(NTHR), SmemState<KB>::end, st, mk, mv,
+                               g, p, status);
+}
+
+}  // namespace
+
+namespace decay {
+
+cudaError_t tc_launch(const Geom& g, const Ptrs& p, bool y_bf16, int* status, cudaStream_t st) {
+  CUtensorMap mq, mk, mv, my;
+  const int hq = g.H / g.share;
+  if (!map_4d(&mq, p.q, true, g.d_k, g.T, hq, g.B, g.qk_t, g.qk_h, g.qk_b) ||
+      !map_4d(&mk, p.k, true, g.d_k, g.T, hq, g.B, g.qk_t, g.qk_h, g.qk_b) ||
+      !map_4d(&mv, p.v, true, g.d_v, g.T, g.H, g.B, g.v_t, g.v_h, g.v_b) ||
+      !map_4d(&my, p.y, y_bf16, g.d_v, g.T, g.H, g.B, g.y_t, g.y_h, g.y_b))
+    return cudaErrorInvalidValue;
+  if (g.nseg > 1) {
+    cudaError_t e = g.d_k <= 64 ? launch_state<1>(mk, mv, g, p, status, st) : launch_state<2>(mk, mv, g, p, status, st);
+    if (e != cudaSuccess) return e;
+    e = scan_launch(g, p, st);
+    if (e != cudaSuccess) return e;
+  }
+  if (g.d_k <= 64)
+    return y_bf16 ? launch_out<1, 1, bf16>(mq, mk, mv, my, g, p, status, st)
+                  : launch_out<1, 3, float>(mq, mk, mv, my, g, p, status, st);
+  return y_bf16 ? launch_out<2, 1, bf16>(mq, mk, mv, my, g, p, status, st)
+                : launch_out<2, 3, float>(mq, mk, mv, my, g, p, status, st);
+}
+
+}  // namespace decay

@@ -66,7 +66,7 @@ __device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity) {
       : "memory");
   return ok != 0;
 }
-__device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity) {
+static __device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity) {
   const long long t0 = clock64();
   while (!try_wait(bar, parity))
     if (clock64() - t0 > kWaitCycles) return false;

@@ -4,7 +4,8 @@
 #include <algorithm>
 #include <new>
 
-#include "layer_common.cuh"
+#include "linear_common.cuh"
+#include "tc2.cuh"
 
 using namespace layer;
 
@@ -13,158 +14,407 @@ namespace {
 struct Geom {
   int N, S, C, G, Cg;
   float eps;
-  int heads;         // ATLAS_NORM_HEADS
   int rb, rows;      // row blocks per sample and their height (statistics over positions)
+  int gpt, tpr, rl;  // groups per channel tile; threads per row; rows at a time
+  int act;
+  float inv_cg;      // 1 / Cg
 };
+
+// activation (the same for all threads), then V neighbouring results
+template <typename TO, int V>
+__device__ __forceinline__ void store_act(int act, float* z, TO* dst) {
+  if (act == ATLAS_ACT_SILU)
+    linear::act_all<ATLAS_ACT_SILU, TO, V>(z);
+  else if (act == ATLAS_ACT_GELU)
+    linear::act_all<ATLAS_ACT_GELU, TO, V>(z);
+  store_vec<V>(dst, z);
+}
+// V neighbouring channels' weight and bias
+template <int V>
+__device__ __forceinline__ void load_affine(const float* weight, const float* bias, int ch, float* w, float* b) {
+  if (weight) {
+    load_vec<V>(weight + ch, w);
+  } else {
+#pragma unroll
+    for (int e = 0; e < V; ++e) w[e] = 1.f;
+  }
+  if (bias) {
+    load_vec<V>(bias + ch, b);
+  } else {
+#pragma unroll
+    for (int e = 0; e < V; ++e) b[e] = 0.f;
+  }
+}
+__device__ __forceinline__ float inv_std(float var, float eps) { return rsqrtf(var + eps); }   // 2 ulp
 
 // ------------------------------------------- sets of one run of channels
 // A set is Cg neighbouring values (S = 1, or the heads layout): LPG lanes of
 // a warp hold it in registers, I items of V values each; mean, then the
-// centred sum of squares, by shuffles.  Sets are in the order of x.
-template <typename TI, typename TO, int ACT, int V, int LPG, int I>
-__global__ void __launch_bounds__(256) k_norm_run(Geom g, const TI* __restrict__ x, const float* __restrict__ weight,
-                                                  const float* __restrict__ bias, TO* __restrict__ y) {
-  const size_t sets = (size_t)g.N * g.S * g.G;
+// centred sum of squares, by shuffles.  A block takes U x 256 / LPG sets in the
+// order of x, all their loads in flight before the first sum.  heads: the sets
+// of one (sample, head) per blockIdx.y, so the lane's weights are loaded once.
+template <typename TI, typename TO, int V, int LPG, int I, int U, bool HEADS>
+__global__ void __launch_bounds__(256) k_norm_run(Geom g, unsigned sets, const TI* __restrict__ x,
+                                                  const float* __restrict__ weight, const float* __restrict__ bias,
+                                                  TO* __restrict__ y) {
+  constexpr int PER = 256 / LPG;
   const int l = threadIdx.x % LPG;
-  const size_t set = ((size_t)blockIdx.x * 256 + threadIdx.x) / LPG;
-  const bool on = set < sets;
-  const TI* src = x + set * g.Cg;
-  float v[I][V];
-  float s = 0.f;
+  const unsigned s0 = blockIdx.x * (U * PER) + threadIdx.x / LPG;
+  const unsigned grp0 = HEADS ? blockIdx.y % g.G : 0, n = HEADS ? blockIdx.y / g.G : 0;
+  const TI* src = x + (HEADS ? (size_t)blockIdx.y * g.S * g.Cg : 0);
+  TO* dst = y + (HEADS ? (size_t)n * g.S * g.C + (size_t)grp0 * g.Cg : 0);
+  tc::grid_dependency_wait();
+  tc::grid_dependents_launch();
+  float v[U][I][V];
 #pragma unroll
-  for (int i = 0; i < I; ++i) {
-    const int c = (l + i * LPG) * V;
-    if (on && c < g.Cg) {
-      load_vec<V>(src + c, v[i]);
+  for (int u = 0; u < U; ++u)
 #pragma unroll
-      for (int e = 0; e < V; ++e) s += v[i][e];
-    } else {
+    for (int i = 0; i < I; ++i) {
+      const unsigned set = s0 + u * PER;
+      const int c = (l + i * LPG) * V;
+      if (set < sets && c < g.Cg) {
+        load_vec<V>(src + (size_t)set * g.Cg + c, v[u][i]);
+      } else {
 #pragma unroll
-      for (int e = 0; e < V; ++e) v[i][e] = 0.f;
+        for (int e = 0; e < V; ++e) v[u][i][e] = 0.f;
+      }
     }
-  }
+  float w[I][V], b[I][V];
+  auto affine = [&](unsigned grp) {
 #pragma unroll
-  for (int o = LPG / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  const float mean = s / (float)g.Cg;
-  s = 0.f;
-#pragma unroll
-  for (int i = 0; i < I; ++i)
-    if ((l + i * LPG) * V < g.Cg)
-#pragma unroll
-      for (int e = 0; e < V; ++e) s += (v[i][e] - mean) * (v[i][e] - mean);
-#pragma unroll
-  for (int o = LPG / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  if (!on) return;
-  const float r = 1.f / sqrtf(s / (float)g.Cg + g.eps);
-  // position of the set in y: heads layout (n, group, position) -> (n, position, group)
-  size_t grp, row;
-  if (g.heads) {
-    const size_t pos = set % g.S, ng = set / g.S;
-    grp = ng % g.G;
-    row = ng / g.G * g.S + pos;
-  } else {
-    grp = set % g.G;
-    row = set / g.G;
-  }
-  TO* dst = y + row * g.C + grp * g.Cg;
-#pragma unroll
-  for (int i = 0; i < I; ++i) {
-    const int c = (l + i * LPG) * V;
-    if (c >= g.Cg) continue;
-    float o[V];
-#pragma unroll
-    for (int e = 0; e < V; ++e) {
-      const int ch = (int)grp * g.Cg + c + e;
-      const float z = (v[i][e] - mean) * r * (weight ? weight[ch] : 1.f) + (bias ? bias[ch] : 0.f);
-      o[e] = activate<ACT>(z);
+    for (int i = 0; i < I; ++i) {
+      const int c = (l + i * LPG) * V;
+      if (c < g.Cg) load_affine<V>(weight, bias, grp * g.Cg + c, w[i], b[i]);
     }
-    store_vec<V>(dst + c, o);
+  };
+  if constexpr (HEADS) affine(grp0);
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const unsigned set = s0 + u * PER;
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < I; ++i)
+#pragma unroll
+      for (int e = 0; e < V; ++e) s += v[u][i][e];
+#pragma unroll
+    for (int o = LPG / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    const float mean = s * g.inv_cg;
+    s = 0.f;
+#pragma unroll
+    for (int i = 0; i < I; ++i)
+      if ((l + i * LPG) * V < g.Cg)
+#pragma unroll
+        for (int e = 0; e < V; ++e) s += (v[u][i][e] - mean) * (v[u][i][e] - mean);
+#pragma unroll
+    for (int o = LPG / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (set >= sets) continue;
+    const float r = inv_std(s * g.inv_cg, g.eps);
+    if constexpr (!HEADS) affine(set % (unsigned)g.G);
+    // heads: (n, head, position) -> (n, position, head)
+    TO* row = dst + (HEADS ? (size_t)set * g.C : (size_t)set * g.Cg);
+#pragma unroll
+    for (int i = 0; i < I; ++i) {
+      const int c = (l + i * LPG) * V;
+      if (c >= g.Cg) continue;
+      float o[V];
+#pragma unroll
+      for (int e = 0; e < V; ++e)
+        o[e] = fmaf((v[u][i][e] - mean) * r, w[i][e], b[i][e]);
+      store_act<TO, V>(g.act, o, row + c);
+    }
   }
 }
 
 // ------------------------------------------------ statistics over positions
+// A block's channel tile is gpt whole groups (tpr = gpt Cg / V threads per row,
+// rl rows at a time), or one group wider than a block, strided over.
+
 // mean and centred sum of squares of two disjoint parts (Chan, Golub, LeVeque)
 __device__ __forceinline__ void merge(float& n, float& mean, float& m2, float nb, float meanb, float m2b) {
-  if (nb == 0.f) return;
-  const float t = n + nb, d = meanb - mean;
-  mean += d * (nb / t);
-  m2 += m2b + d * d * (n * (nb / t));
+  const float t = n + nb, d = meanb - mean, f = t > 0.f ? __fdividef(nb, t) : 0.f;
+  mean = fmaf(d, f, mean);
+  m2 = fmaf(d * d, n * f, m2 + m2b);
   n = t;
 }
-
-// Elements of one set inside rows [r0, r1) of a sample: row r, then channel.
-// The heads layout keeps a run per position and never comes here, except for
-// runs too wide for k_norm_run, where a position is a sample of one row.
-template <typename TI>
-__global__ void __launch_bounds__(256) k_norm_stats(Geom g, const TI* __restrict__ x, float* __restrict__ part) {
-  const int grp = blockIdx.x, blk = blockIdx.y;
-  const size_t n = blockIdx.z;
-  const int r0 = blk * g.rows, r1 = min(g.S, r0 + g.rows);
-  const TI* src = x + n * g.S * g.C + (size_t)grp * g.Cg;
-  const int cnt = (r1 - r0) * g.Cg;
-  float c = 0.f, mean = 0.f, m2 = 0.f;
-  for (int i = threadIdx.x; i < cnt; i += 256) {
-    const float v = to_f32(src[(size_t)(r0 + i / g.Cg) * g.C + i % g.Cg]);
-    c += 1.f;
-    const float d = v - mean;
-    mean += d / c;
-    m2 += d * (v - mean);
-  }
-  __shared__ float sc[256], sm[256], s2[256];
-  sc[threadIdx.x] = c, sm[threadIdx.x] = mean, s2[threadIdx.x] = m2;
-  for (int o = 128; o > 0; o >>= 1) {
-    __syncthreads();
-    if (threadIdx.x < o) {
-      merge(c, mean, m2, sc[threadIdx.x + o], sm[threadIdx.x + o], s2[threadIdx.x + o]);
-      sc[threadIdx.x] = c, sm[threadIdx.x] = mean, s2[threadIdx.x] = m2;
-    }
-  }
-  if (threadIdx.x == 0) {
-    float* d = part + 3 * ((n * g.G + grp) * g.rb + blk);
-    d[0] = c, d[1] = mean, d[2] = m2;
+// over `lanes` (a power of two) neighbouring lanes, valid in the first of them
+__device__ __forceinline__ void merge_lanes(int lanes, float& n, float& mean, float& m2) {
+  for (int o = 1; o < lanes; o <<= 1) {
+    const float a = __shfl_down_sync(0xffffffffu, n, o), b = __shfl_down_sync(0xffffffffu, mean, o),
+                c = __shfl_down_sync(0xffffffffu, m2, o);
+    merge(n, mean, m2, a, b, c);
   }
 }
 
-template <typename TI, typename TO, int ACT>
-__global__ void __launch_bounds__(256) k_norm_apply(Geom g, const TI* __restrict__ x, const float* __restrict__ weight,
-                                                    const float* __restrict__ bias, const float* __restrict__ part,
-                                                    TO* __restrict__ y) {
-  const int grp = blockIdx.x, blk = blockIdx.y;
-  const size_t n = blockIdx.z;
-  __shared__ float st[2];
-  if (threadIdx.x == 0) {
-    const float* d = part + 3 * (n * g.G + grp) * g.rb;
-    float c = 0.f, mean = 0.f, m2 = 0.f;
-    for (int i = 0; i < g.rb; ++i) merge(c, mean, m2, d[3 * i], d[3 * i + 1], d[3 * i + 2]);
-    st[0] = mean;
-    st[1] = 1.f / sqrtf(m2 / c + g.eps);
+// Where a thread of a position kernel works.
+struct Place {
+  int tile, vecs;    // channel tile; vectors of V per group
+  bool on;
+  int row, vec0, step, cnt;   // row lane; first vector of the thread in the tile, the next ones, how many
+  int ch0;           // first channel of the tile
+  template <int V>
+  __device__ static Place at(const Geom& g, int tile) {
+    Place p;
+    p.tile = tile;
+    p.vecs = g.Cg / V;
+    p.ch0 = tile * g.gpt * g.Cg;
+    p.row = threadIdx.x / g.tpr;
+    p.vec0 = threadIdx.x % g.tpr;
+    p.on = p.row < g.rl && p.ch0 + p.vec0 * V < g.C;
+    p.step = g.tpr;
+    p.cnt = p.vecs > 256 ? (p.vecs - p.vec0 + 255) / 256 : 1;
+    return p;
   }
-  __syncthreads();
-  const float mean = st[0], r = st[1];
-  const int r0 = blk * g.rows, r1 = min(g.S, r0 + g.rows), cnt = (r1 - r0) * g.Cg;
-  const size_t base = n * g.S * g.C + (size_t)grp * g.Cg;
-  for (int i = threadIdx.x; i < cnt; i += 256) {
-    const int ch = i % g.Cg;
-    const size_t at = base + (size_t)(r0 + i / g.Cg) * g.C + ch;
-    const float z = (to_f32(x[at]) - mean) * r * (weight ? weight[grp * g.Cg + ch] : 1.f) +
-                    (bias ? bias[grp * g.Cg + ch] : 0.f);
-    y[at] = from_f32<TO>(activate<ACT>(z));
-  }
-}
-
-constexpr int kMaxRun = 1024;    // widest run held in a warp's registers
-
-struct Plan {
-  bool run;
-  int rb, rows;
 };
 
-Plan make_plan(const atlas_norm_config& c, int N, int S) {
+// sums of d and d^2 with d = x - shift, shift a value of the set near its
+// mean's scale (the thread's first), so a common offset cancels before squares
+struct Sums {
+  float n = 0.f, shift = 0.f, s = 0.f, q = 0.f;
+  template <int V>
+  __device__ __forceinline__ void add(const float* v) {
+    if (n == 0.f) shift = v[0];
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      const float d = v[e] - shift;
+      s += d;
+      q = fmaf(d, d, q);
+    }
+    n += (float)V;
+  }
+  __device__ __forceinline__ void finish(float& mean, float& m2) const {
+    const float m = n > 0.f ? s / n : 0.f;
+    mean = shift + m;
+    m2 = fmaxf(0.f, fmaf(-m, s, q));
+    if (q != q || s != s) m2 = q + s;   // NaN and infinities stay visible
+  }
+};
+
+// the lanes that merge `entries` parts of one group: a power of two, at most 32
+__device__ __forceinline__ int lanes_for(int entries) {
+  return entries >= 32 ? 32 : entries <= 1 ? 1 : 1 << (32 - __clz(entries - 1));
+}
+
+// the block's threads' sums -> (count, mean, m2) per group of the tile, by a
+// few lanes per group in a fixed order; out(group, n, mean, m2) once per group
+template <typename F>
+__device__ __forceinline__ void reduce_groups(const Geom& g, const Place& p, const Sums& sums, float* sh, F out) {
+  float mean, m2;
+  sums.finish(mean, m2);
+  sh[threadIdx.x] = p.on ? sums.n : 0.f;
+  sh[256 + threadIdx.x] = mean;
+  sh[512 + threadIdx.x] = m2;
+  __syncthreads();
+  const int width = min(p.vecs, 256), entries = width * g.rl, lanes = lanes_for(entries), per = 256 / lanes;
+  const int l = threadIdx.x % lanes;
+  for (int k0 = 0; k0 < g.gpt; k0 += per) {
+    const int k = k0 + threadIdx.x / lanes;
+    float n = 0.f, mu = 0.f, q = 0.f;
+    if (k < g.gpt)
+      for (int i = l; i < entries; i += lanes) {
+        const int t = i / width * g.tpr + k * width + i % width;
+        merge(n, mu, q, sh[t], sh[256 + t], sh[512 + t]);
+      }
+    merge_lanes(lanes, n, mu, q);
+    if (l == 0 && k < g.gpt) out(k, n, mu, q);
+  }
+}
+
+constexpr int kAhead = 2;   // rows of a step; two steps in flight per thread
+
+// f(i, values) for the `cnt` rows at src, src + step, ...; kAhead rows' loads
+// are in flight while the kAhead before them are worked on
+template <typename TI, int V, typename F>
+__device__ __forceinline__ void for_rows(const TI* src, size_t step, int cnt, F f) {
+  Words<TI, V> next[kAhead];
+#pragma unroll
+  for (int a = 0; a < kAhead; ++a)
+    if (a < cnt) next[a].load(src + a * step);
+  for (int i = 0; i < cnt; i += kAhead) {
+    Words<TI, V> now[kAhead];
+    src += kAhead * step;
+#pragma unroll
+    for (int a = 0; a < kAhead; ++a) {
+      now[a] = next[a];
+      if (i + kAhead + a < cnt) next[a].load(src + a * step);
+    }
+#pragma unroll
+    for (int a = 0; a < kAhead; ++a)
+      if (i + a < cnt) {
+        float v[V];
+        now[a].values(v);
+        f(i + a, v);
+      }
+  }
+}
+
+template <typename TI, int V>
+__global__ void __launch_bounds__(256, 4) k_norm_stats(Geom g, const TI* __restrict__ x, float* __restrict__ part) {
+  __shared__ float sh[768];
+  const size_t n = blockIdx.x;
+  const int blk = blockIdx.y;
+  const Place p = Place::at<V>(g, blockIdx.z);
+  tc::grid_dependency_wait();
+  tc::grid_dependents_launch();
+  const int r0 = blk * g.rows + p.row, r1 = min(g.S, (blk + 1) * g.rows);
+  Sums sums;
+  if (p.on && r0 < r1) {
+    for (int j = 0; j < p.cnt; ++j) {
+      const TI* src = x + (n * g.S + r0) * g.C + p.ch0 + (p.vec0 + j * p.step) * V;
+      for_rows<TI, V>(src, (size_t)g.rl * g.C, (r1 - r0 + g.rl - 1) / g.rl,
+                      [&](int, const float* v) { sums.add<V>(v); });
+    }
+  }
+  reduce_groups(g, p, sums, sh, [&](int k, float c, float mean, float m2) {
+    const int grp = p.tile * g.gpt + k;
+    if (grp < g.G) {
+      float* d = part + 3 * ((n * g.G + grp) * g.rb + blk);
+      d[0] = c, d[1] = mean, d[2] = m2;
+    }
+  });
+}
+
+// one vector: normalise, affine, activation, store; w: weight times the inverse deviation
+template <typename TO, int V>
+__device__ __forceinline__ void finish_vec(int act, const float* v, float mean, const float* w, const float* b, TO* dst) {
+  float o[V];
+  if constexpr (V == 1) {
+    o[0] = fmaf(v[0] - mean, w[0], b[0]);
+  } else {
+#pragma unroll
+    for (int e = 0; e < V; e += 2) {
+      const uint64_t d = linear::add2(linear::pack2(v[e], v[e + 1]), linear::pack2(-mean, -mean));
+      linear::unpack2(linear::fma2(d, linear::pack2(w[e], w[e + 1]), linear::pack2(b[e], b[e + 1])), o[e], o[e + 1]);
+    }
+  }
+  store_act<TO, V>(act, o, dst);
+}
+
+template <typename TI, typename TO, int V>
+__global__ void __launch_bounds__(256, 4) k_norm_apply(Geom g, const TI* x, const float* __restrict__ weight,
+                                                    const float* __restrict__ bias, const float* __restrict__ part,
+                                                    TO* y) {
+  __shared__ float st[2][256];
+  const size_t n = blockIdx.x;
+  const int blk = blockIdx.y, lane = threadIdx.x % 32;
+  const Place p = Place::at<V>(g, blockIdx.z);
+  tc::grid_dependency_wait();
+  tc::grid_dependents_launch();
+  const int lanes = lanes_for(g.rb), per = 256 / lanes, l = threadIdx.x % lanes;
+  for (int k0 = 0; k0 < g.gpt; k0 += per) {
+    const int k = k0 + threadIdx.x / lanes, grp = p.tile * g.gpt + k;
+    float c = 0.f, mean = 0.f, m2 = 0.f;
+    if (k < g.gpt && grp < g.G)
+      for (int i = l; i < g.rb; i += lanes) {
+        const float* d = part + 3 * ((n * g.G + grp) * g.rb + i);
+        merge(c, mean, m2, d[0], d[1], d[2]);
+      }
+    merge_lanes(lanes, c, mean, m2);
+    if (l == 0 && k < g.gpt) st[0][k] = mean, st[1][k] = inv_std(m2 / c, g.eps);
+  }
+  __syncthreads();
+  if (!p.on) return;
+  const int k = p.vecs > 256 ? 0 : p.vec0 / p.vecs, r0 = blk * g.rows + p.row, r1 = min(g.S, (blk + 1) * g.rows);
+  if (r0 >= r1) return;
+  const size_t step = (size_t)g.rl * g.C;
+  const float mean = st[0][k], rs = st[1][k];
+  for (int j = 0; j < p.cnt; ++j) {
+    const int ch = p.ch0 + (p.vec0 + j * p.step) * V;
+    const size_t base = (n * g.S + r0) * g.C + ch;
+    float w[V], b[V];
+    load_affine<V>(weight, bias, ch, w, b);
+#pragma unroll
+    for (int e = 0; e < V; ++e) w[e] *= rs;
+    TO* dst = y + base;
+    for_rows<TI, V>(x + base, step, (r1 - r0 + g.rl - 1) / g.rl, [&](int, const float* v) {
+      finish_vec<TO, V>(g.act, v, mean, w, b, dst);
+      dst += step;   // rows come in order
+    });
+  }
+}
+
+// Samples whose tile fits shared memory: one block reads it once, keeps it
+// there as it came, and writes the result.
+template <typename TI, typename TO, int V>
+__global__ void __launch_bounds__(256) k_norm_tile(Geom g, const TI* x, const float* __restrict__ weight,
+                                                   const float* __restrict__ bias, TO* y) {
+  extern __shared__ __align__(16) uint8_t raw[];
+  __shared__ float sh[768], st[2][256];
+  TI* keep = reinterpret_cast<TI*>(raw);   // [cnt][S / rl rounded up][256][V]
+  const size_t n = blockIdx.x;
+  const Place p = Place::at<V>(g, blockIdx.z);
+  tc::grid_dependency_wait();
+  tc::grid_dependents_launch();
+  const int per = (g.S + g.rl - 1) / g.rl, rows = (g.S - p.row + g.rl - 1) / g.rl;   // rows per row lane, and of this one
+  const size_t step = (size_t)g.rl * g.C;
+  Sums sums;
+  if (p.on && p.row < g.S) {
+    for (int j = 0; j < p.cnt; ++j) {
+      const TI* src = x + (n * g.S + p.row) * g.C + p.ch0 + (p.vec0 + j * p.step) * V;
+      for_rows<TI, V>(src, step, rows, [&](int i, const float* v) {
+        sums.add<V>(v);
+        store_vec<V>(keep + ((j * per + i) * 256 + threadIdx.x) * V, v);   // exact: v came from TI
+      });
+    }
+  }
+  reduce_groups(g, p, sums, sh, [&](int k, float c, float mean, float m2) {
+    st[0][k] = mean, st[1][k] = inv_std(m2 / c, g.eps);
+  });
+  __syncthreads();
+  if (!p.on) return;
+  const int k = p.vecs > 256 ? 0 : p.vec0 / p.vecs;
+  const float mean = st[0][k], rs = st[1][k];
+  for (int j = 0; j < p.cnt; ++j) {
+    const int ch = p.ch0 + (p.vec0 + j * p.step) * V;
+    float w[V], b[V];
+    load_affine<V>(weight, bias, ch, w, b);
+#pragma unroll
+    for (int e = 0; e < V; ++e) w[e] *= rs;
+    TO* dst = y + (n * g.S + p.row) * g.C + ch;
+#pragma unroll 2
+    for (int i = 0; i < rows; ++i) {
+      float v[V];
+      load_vec<V>(keep + ((j * per + i) * 256 + threadIdx.x) * V, v);
+      finish_vec<TO, V>(g.act, v, mean, w, b, dst + i * step);
+    }
+  }
+}
+
+constexpr int kMaxRun = 1024;             // widest run held in a warp's registers
+constexpr int kTileBytes = 48 * 1024;     // most shared memory of k_norm_tile's block
+
+struct Plan {
+  int kind;              // 0 run, 1 tile, 2 two passes
+  int V, gpt, tpr, rl, tiles, rb, rows, smem;
+};
+
+// `vec`: every run of 8 values starts on a 16-byte boundary
+Plan make_plan(const atlas_norm_config& c, int N, int S, bool vec) {
   const int Cg = c.C / c.groups;
-  Plan p{(S == 1 || c.layout == ATLAS_NORM_HEADS) && Cg <= kMaxRun, 1, S};
-  if (p.run) return p;
-  // blocks of about 8192 values
-  p.rows = std::max(1, std::min(S, 8192 / Cg));
+  Plan p{};
+  p.V = vec && Cg % 8 == 0 ? 8 : 1;
+  p.rb = 1;
+  p.rows = S;
+  if ((S == 1 || c.layout == ATLAS_NORM_HEADS) && Cg <= kMaxRun) return p;
+  const int vecs = Cg / p.V;
+  p.gpt = vecs > 256 ? 1 : std::min(c.groups, 256 / vecs);
+  p.tpr = vecs > 256 ? 256 : p.gpt * vecs;
+  p.rl = 256 / p.tpr;
+  p.tiles = (c.groups + p.gpt - 1) / p.gpt;
+  const long long per = (S + p.rl - 1) / p.rl, cnt = vecs > 256 ? (vecs + 255) / 256 : 1;
+  const long long bytes = cnt * per * 256 * p.V * (long long)dtype_size(c.x_dtype);
+  const long long blocks = (long long)N * p.tiles;
+  // One read instead of two where the tile fits and the blocks fill the SMs
+  // (else two passes with more blocks are faster: their second read is an L2 hit).
+  if (bytes <= kTileBytes && (blocks >= sm_count() || bytes <= 8 * 1024)) {
+    p.kind = 1;
+    p.smem = (int)bytes;
+    return p;
+  }
+  p.kind = 2;
+  // about four blocks per SM, 4 rows per thread at least
+  const long long want = std::max(1LL, 4LL * sm_count() / blocks);
+  p.rows = (int)std::max<long long>((S + want - 1) / want, 4 * p.rl);
+  p.rows = std::max(p.rows, (S + 65534) / 65535);
   p.rb = (S + p.rows - 1) / p.rows;
   return p;
 }
@@ -208,56 +458,56 @@ extern "C" int atlas_norm_create(const atlas_norm_config* cfg, atlas_norm_handle
 
 extern "C" size_t atlas_norm_workspace_bytes(const atlas_norm_handle* h, int N, int S) {
   if (!h || N < 1 || S < 1) return 0;
-  const Plan p = make_plan(h->cfg, N, S);
-  return p.run ? 0 : (size_t)N * h->cfg.groups * p.rb * 3 * sizeof(float);
+  // the larger of the two vector widths': which one runs depends on the tensors' addresses
+  size_t need = 0;
+  for (bool vec : {false, true}) {
+    const Plan p = make_plan(h->cfg, N, S, vec);
+    if (p.kind == 2) need = std::max(need, (size_t)N * h->cfg.groups * p.rb * 3 * sizeof(float));
+  }
+  return need;
 }
 
 namespace {
 
-template <typename TI, typename TO, int ACT, int V>
+template <typename TI, typename TO, int V, bool HEADS>
 cudaError_t launch_run(const Geom& g, const atlas_norm_io& io, cudaStream_t st) {
-  const size_t sets = (size_t)g.N * g.S * g.G;
-  const TI* x = (const TI*)io.x;
-  TO* y = (TO*)io.y;
+  const unsigned sets = HEADS ? g.S : (unsigned)((size_t)g.N * g.S * g.G);
   const int items = (g.Cg + V - 1) / V;   // values of V per set
-  auto go = [&](auto kern, int lpg) {
-    const unsigned grid = (unsigned)((sets * lpg + 255) / 256);
-    kern<<<grid, 256, 0, st>>>(g, x, io.weight, io.bias, y);
+  auto go = [&](auto kern, int per) {
+    const dim3 grid((sets + per - 1) / per, HEADS ? g.N * g.G : 1);
+    return tc::launch_overlapped(kern, grid, dim3(256), 0, st, g, sets, (const TI*)io.x, io.weight, io.bias, (TO*)io.y);
   };
-  if (items <= 2) go(k_norm_run<TI, TO, ACT, V, 2, 1>, 2);
-  else if (items <= 4) go(k_norm_run<TI, TO, ACT, V, 4, 1>, 4);
-  else if (items <= 8) go(k_norm_run<TI, TO, ACT, V, 8, 1>, 8);
-  else if (items <= 16) go(k_norm_run<TI, TO, ACT, V, 16, 1>, 16);
-  else if (items <= 32) go(k_norm_run<TI, TO, ACT, V, 32, 1>, 32);
-  else if (items <= 64) go(k_norm_run<TI, TO, ACT, V, 32, 2>, 32);
-  else if (items <= 128) go(k_norm_run<TI, TO, ACT, V, 32, 4>, 32);
-  else if constexpr (V == 1) {
-    if (items <= 512) go(k_norm_run<TI, TO, ACT, V, 32, 16>, 32);
-    else go(k_norm_run<TI, TO, ACT, V, 32, 32>, 32);
-  }
-  return cudaGetLastError();
+  if (items <= 2) return go(k_norm_run<TI, TO, V, 2, 1, 4, HEADS>, 512);
+  if (items <= 4) return go(k_norm_run<TI, TO, V, 4, 1, 4, HEADS>, 256);
+  if (items <= 8) return go(k_norm_run<TI, TO, V, 8, 1, 4, HEADS>, 128);
+  if (items <= 16) return go(k_norm_run<TI, TO, V, 16, 1, 4, HEADS>, 64);
+  if (items <= 32) return go(k_norm_run<TI, TO, V, 32, 1, 4, HEADS>, 32);
+  if (items <= 128) return go(k_norm_run<TI, TO, V, 32, 4, 1, HEADS>, 8);
+  return go(k_norm_run<TI, TO, V, 32, 32, 1, HEADS>, 8);
 }
 
-template <typename TI, typename TO, int ACT>
-cudaError_t launch(const Plan& pl, const Geom& g, const atlas_norm_io& io, float* part, cudaStream_t st) {
-  if (pl.run) {
-    // eight values a lane where every run starts on a 16-byte boundary
-    const bool v8 = g.Cg % 8 == 0 && aligned16(io.x) && aligned16(io.y);
-    return v8 ? launch_run<TI, TO, ACT, 8>(g, io, st) : launch_run<TI, TO, ACT, 1>(g, io, st);
-  }
-  const dim3 grid(g.G, g.rb, g.N);
-  k_norm_stats<TI><<<grid, 256, 0, st>>>(g, (const TI*)io.x, part);
-  cudaError_t e = cudaGetLastError();
+template <typename TI, typename TO, int V>
+cudaError_t launch_positions(const Plan& pl, const Geom& g, const atlas_norm_io& io, float* part, cudaStream_t st) {
+  const TI* x = (const TI*)io.x;
+  TO* y = (TO*)io.y;
+  if (pl.kind == 1)
+    return tc::launch_overlapped(k_norm_tile<TI, TO, V>, dim3(g.N, 1, pl.tiles), dim3(256), pl.smem, st, g, x,
+                                 io.weight, io.bias, y);
+  const dim3 grid(g.N, g.rb, pl.tiles);
+  const cudaError_t e = tc::launch_overlapped(k_norm_stats<TI, V>, grid, dim3(256), 0, st, g, x, part);
   if (e != cudaSuccess) return e;
-  k_norm_apply<TI, TO, ACT><<<grid, 256, 0, st>>>(g, (const TI*)io.x, io.weight, io.bias, part, (TO*)io.y);
-  return cudaGetLastError();
+  return tc::launch_overlapped(k_norm_apply<TI, TO, V>, grid, dim3(256), 0, st, g, x, io.weight, io.bias,
+                               (const float*)part, y);
 }
 
 template <typename TI, typename TO>
-cudaError_t launch_act(int act, const Plan& pl, const Geom& g, const atlas_norm_io& io, float* part, cudaStream_t st) {
-  if (act == ATLAS_ACT_SILU) return launch<TI, TO, ATLAS_ACT_SILU>(pl, g, io, part, st);
-  if (act == ATLAS_ACT_GELU) return launch<TI, TO, ATLAS_ACT_GELU>(pl, g, io, part, st);
-  return launch<TI, TO, ATLAS_ACT_NONE>(pl, g, io, part, st);
+cudaError_t launch(const Plan& pl, const Geom& g, bool heads, const atlas_norm_io& io, float* part, cudaStream_t st) {
+  if (pl.kind == 0) {
+    if (heads) return pl.V == 8 ? launch_run<TI, TO, 8, true>(g, io, st) : launch_run<TI, TO, 1, true>(g, io, st);
+    return pl.V == 8 ? launch_run<TI, TO, 8, false>(g, io, st) : launch_run<TI, TO, 1, false>(g, io, st);
+  }
+  return pl.V == 8 ? launch_positions<TI, TO, 8>(pl, g, io, part, st)
+                   : launch_positions<TI, TO, 1>(pl, g, io, part, st);
 }
 
 }  // namespace
@@ -270,21 +520,23 @@ extern "C" int atlas_norm_forward(atlas_norm_handle* h, const atlas_norm_io* io,
   if (!io->x || !io->y) return h->fail(ATLAS_ERR_INVALID_ARG, "x and y must be non-NULL");
   if (io->x == io->y && (c.layout == ATLAS_NORM_HEADS || c.x_dtype != c.y_dtype))
     return h->fail(ATLAS_ERR_INVALID_ARG, "y may be x only with channels last and one type");
-  const Plan pl = make_plan(c, io->N, io->S);
-  if ((long long)io->N * io->S * c.groups > (1LL << 33))
-    return h->fail(ATLAS_ERR_UNSUPPORTED, "N * S * groups > 2^33 is not supported");
-  if (!pl.run && (io->N > 65535 || pl.rb > 65535))
-    return h->fail(ATLAS_ERR_UNSUPPORTED, "N or S too large for statistics over positions");
+  const Plan pl = make_plan(c, io->N, io->S, aligned16(io->x) && aligned16(io->y) && aligned16(io->weight) && aligned16(io->bias));
+  const bool heads = c.layout == ATLAS_NORM_HEADS;
+  if ((long long)io->N * io->S * c.groups > 0x40000000LL)
+    return h->fail(ATLAS_ERR_UNSUPPORTED, "N * S * groups > 2^30 is not supported");
+  if (heads && (long long)io->N * c.groups > 65535)
+    return h->fail(ATLAS_ERR_UNSUPPORTED, "N * groups > 65535 is not supported in the heads layout");
+  if (pl.kind && pl.tiles > 65535) return h->fail(ATLAS_ERR_UNSUPPORTED, "too many groups for statistics over positions");
   cudaStream_t st = (cudaStream_t)stream;
-  const int rc = h->grow(atlas_norm_workspace_bytes(h, io->N, io->S));
+  const int rc = h->grow(pl.kind == 2 ? atlas_norm_workspace_bytes(h, io->N, io->S) : 0);
   if (rc) return rc;
-  const Geom g{io->N, io->S, c.C, c.groups, c.C / c.groups, c.eps, c.layout == ATLAS_NORM_HEADS, pl.rb, pl.rows};
+  const Geom g{io->N, io->S, c.C, c.groups, c.C / c.groups, c.eps, pl.rb, pl.rows, pl.gpt, pl.tpr, pl.rl, c.act, 1.f / (float)(c.C / c.groups)};
   const bool ib = c.x_dtype == ATLAS_BF16, ob = c.y_dtype == ATLAS_BF16;
   float* part = (float*)h->ws;
-  const cudaError_t e = ib ? (ob ? launch_act<bf16, bf16>(c.act, pl, g, *io, part, st)
-                                 : launch_act<bf16, float>(c.act, pl, g, *io, part, st))
-                           : (ob ? launch_act<float, bf16>(c.act, pl, g, *io, part, st)
-                                 : launch_act<float, float>(c.act, pl, g, *io, part, st));
+  const cudaError_t e = ib ? (ob ? launch<bf16, bf16>(pl, g, heads, *io, part, st)
+                                 : launch<bf16, float>(pl, g, heads, *io, part, st))
+                           : (ob ? launch<float, bf16>(pl, g, heads, *io, part, st)
+                                 : launch<float, float>(pl, g, heads, *io, part, st));
   if (e != cudaSuccess) return h->cuda_fail("group norm launch", e);
   h->last_stream = st;
   h->launched = true;

@@ -252,15 +252,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHR, 1)
           if (p.bias)
 #pragma unroll
             for (int j = 0; j < CW; ++j) vv[j] += bb[j];
-#pragma unroll
-          for (int j = 0; j < CW; j += 2) {
-            if constexpr (sizeof(TO) == 2) {
-              linear::activate_fast2<ACT>(vv[j], vv[j + 1]);
-            } else {
-              vv[j] = layer::activate<ACT>(vv[j]);
-              vv[j + 1] = layer::activate<ACT>(vv[j + 1]);
-            }
-          }
+          linear::act_all<ACT, TO, CW>(vv);
           const uint32_t b = fetch ? i % NBUF : blk % NBUF;
           if (fetch) {
             if (i % NBUF == 0) {

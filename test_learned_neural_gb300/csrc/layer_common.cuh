@@ -58,6 +58,41 @@ __device__ __forceinline__ void load_vec(const bf16* p, float* v) {
     }
   }
 }
+// The same in two steps: the words as they lie in memory, then their values.
+template <typename T, int V>
+struct Words {
+  static constexpr int N = V * (int)sizeof(T) / 4 > 0 ? V * (int)sizeof(T) / 4 : 1;
+  uint32_t w[N];
+  __device__ __forceinline__ void load(const T* p) {
+    if constexpr (V * sizeof(T) % 16 == 0) {
+#pragma unroll
+      for (int i = 0; i < N; i += 4) {
+        const uint4 u = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint32_t*>(p) + i);
+        w[i] = u.x; w[i + 1] = u.y; w[i + 2] = u.z; w[i + 3] = u.w;
+      }
+    } else if constexpr (sizeof(T) == 2) {
+      static_assert(V == 1, "one value, or whole 16-byte groups");
+      w[0] = *reinterpret_cast<const uint16_t*>(p);
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i) w[i] = reinterpret_cast<const uint32_t*>(p)[i];
+    }
+  }
+  __device__ __forceinline__ void values(float* v) const {
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) v[i] = __uint_as_float(w[i]);
+    } else if constexpr (V == 1) {
+      v[0] = __uint_as_float(w[0] << 16);
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        v[2 * i] = __uint_as_float(w[i] << 16);
+        v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+      }
+    }
+  }
+};
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   const __nv_bfloat162 t = __floats2bfloat162_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&t);

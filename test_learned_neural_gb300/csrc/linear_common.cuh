@@ -61,6 +61,11 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
   return d;
 }
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
 __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
   uint64_t d;
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
@@ -86,9 +91,12 @@ __device__ __forceinline__ void activate_fast2(float& za, float& zb) {
     unpack2(h, ha, hb);
     za = fmaf(fabsf(ha), 1.f - rcp(da), ha);
     zb = fmaf(fabsf(hb), 1.f - rcp(db), hb);
-  } else {
-    za = activate_fast<ACT>(za);
-    zb = activate_fast<ACT>(zb);
+  } else if constexpr (ACT == ATLAS_ACT_SILU) {
+    float ea, eb;
+    const uint64_t z = pack2(za, zb);
+    unpack2(mul2(z, pack2(-1.4426950408889634f, -1.4426950408889634f)), ea, eb);
+    unpack2(add2(pack2(ex2(ea), ex2(eb)), pack2(1.f, 1.f)), ea, eb);
+    unpack2(mul2(z, pack2(rcp(ea), rcp(eb))), za, zb);
   }
 }
 
@@ -96,6 +104,18 @@ template <int ACT, typename TO>
 __device__ __forceinline__ float act_for(float z) {
   if constexpr (sizeof(TO) == 2) return activate_fast<ACT>(z);
   return layer::activate<ACT>(z);
+}
+
+// V neighbouring results, as act_for
+template <int ACT, typename TO, int V>
+__device__ __forceinline__ void act_all(float* z) {
+  if constexpr (sizeof(TO) == 2 && V % 2 == 0) {
+#pragma unroll
+    for (int e = 0; e < V; e += 2) activate_fast2<ACT>(z[e], z[e + 1]);
+  } else {
+#pragma unroll
+    for (int e = 0; e < V; ++e) z[e] = act_for<ACT, TO>(z[e]);
+  }
 }
 
 // One product on the tensor cores: bf16 planes in, epilogue out.

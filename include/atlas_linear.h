@@ -64,8 +64,8 @@ size_t atlas_linear_workspace_bytes(const atlas_linear_handle* h, int M);
  * outputs are then not valid).  Clears the status word. */
 int atlas_linear_status(atlas_linear_handle* h);
 
-/* How the last forward on h ran: 0 = fp32 tiles, 1 = tensor cores, 2 = few
- * rows, -1 = none yet. */
+/* How the last forward on h ran: 1 = tensor cores, 2 = few rows (fp32 sums),
+ * -1 = none yet. */
 int atlas_linear_last_path(const atlas_linear_handle* h);
 
 /* Message of the last failure on h, or of the last failed create when h is NULL. */

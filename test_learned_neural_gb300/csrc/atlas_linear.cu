@@ -1,53 +1,149 @@
-// Matrix product with bias, activation and residual: host side, the fp32
-// tiles, and the operand planes of the tensor-core kernels.
+// Matrix product with bias, activation and residual: host side, the kernel
+// for few rows, and the operand planes of the tensor-core kernel.
 #include <algorithm>
 #include <new>
+#include <type_traits>
 
 #include "linear_common.cuh"
+#include "tc2.cuh"
 
 using namespace layer;
 
 namespace {
 
-// y = act(x W + bias) + residual in 64 x 64 fp32 tiles, 16 x 16 threads with
-// 4 x 4 outputs each, K in steps of 16.
-template <typename TI, typename TO, int ACT>
-__global__ void __launch_bounds__(256) k_linear_f32(int M, int K, int N, const TI* __restrict__ x,
-                                                    const TI* __restrict__ W, const float* __restrict__ bias,
-                                                    const TO* residual, TO* y) {
-  __shared__ float As[16][68], Bs[16][68];   // As[k][m], Bs[k][n]
-  const int m0 = blockIdx.y * 64, n0 = blockIdx.x * 64;
-  const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
-  float acc[4][4] = {};
-  for (int k0 = 0; k0 < K; k0 += 16) {
-    for (int l = threadIdx.x; l < 16 * 64; l += 256) {
-      const int kk = l % 16, mm = l / 16, m = m0 + mm, k = k0 + kk;
-      As[kk][mm] = m < M && k < K ? to_f32(x[(size_t)m * K + k]) : 0.f;
-      const int nn = l % 64, kr = k0 + l / 64, n = n0 + nn;
-      Bs[l / 64][nn] = n < N && kr < K ? to_f32(W[(size_t)kr * N + n]) : 0.f;
-    }
+// ------------------------------------------------------------- few rows
+// MR rows of x against W, every W element read once: a CTA takes 64 columns,
+// its threads V columns of every RL-th row of K; the clusters of S CTAs share
+// the columns and split K.  Sums: over K in registers, over a warp's row lanes
+// by shuffles, over warps and then over the cluster's CTAs through shared
+// memory, always in the same order.
+constexpr int kRowCols = 64, kRowChunk = 1024;   // columns per CTA; rows of K staged at a time
+
+template <typename TI, typename TO, int MR, int V>
+__global__ void __launch_bounds__(256) k_linear_rows(int M, int K, int N, int kper, int act, const TI* __restrict__ x,
+                                                     const TI* __restrict__ W, const float* __restrict__ bias,
+                                                     const TO* residual, TO* y) {
+  constexpr int CL = kRowCols / V, RL = 256 / CL;
+  constexpr int AHEAD = V == 8 ? 8 : 4;
+  __shared__ __align__(16) float xs[MR * kRowChunk];
+  __shared__ float red[8][MR * kRowCols], sum[MR * kRowCols];
+  const int tid = threadIdx.x, cl = tid % CL, rl = tid / CL;
+  const uint32_t rank = tc::cluster_rank();
+  uint32_t S;
+  asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(S));
+  const int col0 = blockIdx.x / S * kRowCols, col = col0 + cl * V, m0 = blockIdx.y * MR;
+  const int k_lo = rank * kper, k_hi = min(K, k_lo + kper);
+  float acc[MR][V] = {};
+  tc::grid_dependency_wait();
+  tc::grid_dependents_launch();
+  for (int k0 = k_lo; k0 < k_hi; k0 += kRowChunk) {
+    const int n = min(kRowChunk, k_hi - k0);
     __syncthreads();
 #pragma unroll
-    for (int kk = 0; kk < 16; ++kk) {
-      const float4 a = *reinterpret_cast<const float4*>(&As[kk][4 * ty]), b = *reinterpret_cast<const float4*>(&Bs[kk][4 * tx]);
-      const float av[4] = {a.x, a.y, a.z, a.w}, bv[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(av[i], bv[j], acc[i][j]);
-    }
+    for (int m = 0; m < MR; ++m)
+      for (int i = tid; i < n; i += 256) xs[m * kRowChunk + i] = m0 + m < M ? to_f32(x[(size_t)(m0 + m) * K + k0 + i]) : 0.f;
     __syncthreads();
+    if (col < N) {
+      const TI* w = W + (size_t)k0 * N + col;
+      for (int r = rl; r < n; r += AHEAD * RL) {
+        Words<TI, V> ws[AHEAD];
+#pragma unroll
+        for (int a = 0; a < AHEAD; ++a)
+          if (r + a * RL < n) ws[a].load(w + (size_t)(r + a * RL) * N);
+#pragma unroll
+        for (int a = 0; a < AHEAD; ++a)
+          if (r + a * RL < n) {
+            float v[V];
+            ws[a].values(v);
+#pragma unroll
+            for (int m = 0; m < MR; ++m) {
+              const float xv = xs[m * kRowChunk + r + a * RL];
+#pragma unroll
+              for (int e = 0; e < V; ++e) acc[m][e] = fmaf(xv, v[e], acc[m][e]);
+            }
+          }
+      }
+    }
   }
+  // row lanes of a warp (V = 8: four of them), then the warps
+  const int warp = tid / 32;
+  if constexpr (V == 8) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+    for (int m = 0; m < MR; ++m)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int m = m0 + 4 * ty + i, n = n0 + 4 * tx + j;
-      if (m >= M || n >= N) continue;
-      float v = activate<ACT>(acc[i][j] + (bias ? bias[n] : 0.f));
-      if (residual) v += to_f32(residual[(size_t)m * N + n]);
-      y[(size_t)m * N + n] = from_f32<TO>(v);
+      for (int e = 0; e < V; ++e) {
+        acc[m][e] += __shfl_xor_sync(0xffffffffu, acc[m][e], 8);
+        acc[m][e] += __shfl_xor_sync(0xffffffffu, acc[m][e], 16);
+        if (tid % 32 < 8) red[warp][m * kRowCols + cl * V + e] = acc[m][e];
+      }
+  } else {
+    // two warps side by side hold a row lane's 64 columns
+#pragma unroll
+    for (int m = 0; m < MR; ++m) red[rl][m * kRowCols + cl] = acc[m][0];
+  }
+  __syncthreads();
+  constexpr int PARTS = V == 8 ? 8 : RL;
+  for (int i = tid; i < MR * kRowCols; i += 256) {
+    float t = 0.f;
+#pragma unroll
+    for (int p = 0; p < PARTS; ++p) t += red[p][i];
+    sum[i] = t;
+  }
+  if (S > 1) tc::cluster_sync();
+  else __syncthreads();
+  // this CTA's share of the columns
+  for (int i = rank * 256 + tid; i < MR * kRowCols; i += S * 256) {
+    const int m = m0 + i / kRowCols, c = col0 + i % kRowCols;
+    if (m >= M || c >= N) continue;
+    float t = 0.f;
+    if (S == 1) {
+      t = sum[i];
+    } else {
+      for (uint32_t p = 0; p < S; ++p) {
+        float v;
+        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(tc::map_rank(&sum[i], p)) : "memory");
+        t += v;
+      }
     }
+    if (bias) t += bias[c];
+    t = act == ATLAS_ACT_SILU ? activate<ATLAS_ACT_SILU>(t) : act == ATLAS_ACT_GELU ? activate<ATLAS_ACT_GELU>(t) : t;
+    if (residual) t += to_f32(residual[(size_t)m * N + c]);
+    y[(size_t)m * N + c] = from_f32<TO>(t);
+  }
+  if (S > 1) tc::cluster_sync();   // no CTA leaves while another reads its sums
+}
+
+template <typename TI, typename TO, int MR, int V>
+cudaError_t launch_rows_v(const atlas_linear_config& c, const atlas_linear_io& io, cudaStream_t st) {
+  const int tiles = (c.N + kRowCols - 1) / kRowCols, groups = (io.M + MR - 1) / MR;
+  // CTAs for every SM, down to 64 rows of K each
+  int S = 1;
+  while (S < 8 && 2 * S * tiles * groups <= 2 * sm_count() && c.K >= 2 * S * 64) S *= 2;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim = {(unsigned)S, 1, 1};
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3((unsigned)(tiles * S), (unsigned)groups);
+  cfg.blockDim = dim3(256);
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, k_linear_rows<TI, TO, MR, V>, io.M, c.K, c.N, (c.K + S - 1) / S, c.act,
+                            (const TI*)io.x, (const TI*)io.W, io.bias, (const TO*)io.residual, (TO*)io.y);
+}
+
+template <typename TI, typename TO>
+cudaError_t launch_rows(const atlas_linear_config& c, const atlas_linear_io& io, cudaStream_t st) {
+  const bool v8 = c.N % 8 == 0 && aligned16(io.W);
+  auto go = [&](auto mr) {
+    constexpr int MR = decltype(mr)::value;
+    return v8 ? launch_rows_v<TI, TO, MR, 8>(c, io, st) : launch_rows_v<TI, TO, MR, 1>(c, io, st);
+  };
+  if (io.M == 1) return go(std::integral_constant<int, 1>());
+  if (io.M == 2) return go(std::integral_constant<int, 2>());
+  return go(std::integral_constant<int, 4>());
 }
 
 // src [R][C] -> bf16 planes [PLANES][Rp][ld], zero past R and C: one plane for
@@ -126,20 +222,7 @@ cudaError_t planes_launch(bool f32, const void* src, int R, int C, int Rp, int l
   return cudaGetLastError();
 }
 
-constexpr int kMinTcRows = 17;   // fewer rows go to the fp32 tiles
-
-template <typename TI, typename TO>
-cudaError_t launch(const atlas_linear_config& c, const atlas_linear_io& io, cudaStream_t st) {
-  const dim3 grid((c.N + 63) / 64, (io.M + 63) / 64);
-  auto go = [&](auto kern) {
-    kern<<<grid, 256, 0, st>>>(io.M, c.K, c.N, (const TI*)io.x, (const TI*)io.W, io.bias, (const TO*)io.residual,
-                               (TO*)io.y);
-    return cudaGetLastError();
-  };
-  if (c.act == ATLAS_ACT_SILU) return go(k_linear_f32<TI, TO, ATLAS_ACT_SILU>);
-  if (c.act == ATLAS_ACT_GELU) return go(k_linear_f32<TI, TO, ATLAS_ACT_GELU>);
-  return go(k_linear_f32<TI, TO, ATLAS_ACT_NONE>);
-}
+constexpr int kMinTcRows = 17;   // fewer rows go to k_linear_rows
 
 }  // namespace
 
@@ -211,10 +294,10 @@ extern "C" int atlas_linear_forward(atlas_linear_handle* h, const atlas_linear_i
     h->launched = true;
     return ATLAS_OK;
   }
-  const cudaError_t e = ib ? (ob ? launch<bf16, bf16>(c, *io, st) : launch<bf16, float>(c, *io, st))
-                           : (ob ? launch<float, bf16>(c, *io, st) : launch<float, float>(c, *io, st));
+  const cudaError_t e = ib ? (ob ? launch_rows<bf16, bf16>(c, *io, st) : launch_rows<bf16, float>(c, *io, st))
+                           : (ob ? launch_rows<float, bf16>(c, *io, st) : launch_rows<float, float>(c, *io, st));
   if (e != cudaSuccess) return h->cuda_fail("matrix product launch", e);
-  h->path = 0;
+  h->path = 2;
   h->last_stream = st;
   h->launched = true;
   return ATLAS_OK;

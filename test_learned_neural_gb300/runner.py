@@ -192,10 +192,16 @@ def _torch_dtype(t):
 def _check(name, t, dtype, shape):
     """Device address of a tensor of the layer operators, which must have the
     type and shape that the configuration and the call's sizes give."""
-    if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous() or not t.is_cuda:
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or not t.is_cuda:
         raise ValueError(f"{name}: want a contiguous CUDA tensor {dtype} {shape}, got {t.dtype} {tuple(t.shape)} on "
                          f"{t.device}")
     return t.data_ptr()
+
+
+# The current stream's handle of a device: torch.cuda.current_stream() builds a
+# Python object for it, 3 us of a serving step's 10 on the host.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 class _Layer:
@@ -254,7 +260,7 @@ class DecayAttention(_Layer):
                             None if lens is None else _check("lens", lens, torch.int32, (B,)),
                             None if S0 is None else _check("S0", S0, f32, sq),
                             _check("y", out["y"], self._y, self._y_shape(B, T)), _check("S", out["S"], f32, sq))
-        atlas_decay_forward(self.h, io, current_stream() if stream is None else stream)
+        atlas_decay_forward(self.h, io, _raw_stream(q.device.index) if stream is None else stream)
         return out
 
     def status(self):
@@ -297,7 +303,7 @@ class GroupNorm(_Layer):
                            None if w is None else _check("weight", w, f32, (c.C,)),
                            None if b is None else _check("bias", b, f32, (c.C,)),
                            _check("y", out["y"], self._y, (N, S, c.C)))
-        atlas_norm_forward(self.h, io, current_stream() if stream is None else stream)
+        atlas_norm_forward(self.h, io, _raw_stream(x.device.index) if stream is None else stream)
         return out
 
 
@@ -325,7 +331,7 @@ class Linear(_Layer):
                              None if b is None else _check("bias", b, torch.float32, (c.N,)),
                              None if r is None else _check("residual", r, self._out, (M, c.N)),
                              _check("y", out["y"], self._out, (M, c.N)))
-        atlas_linear_forward(self.h, io, current_stream() if stream is None else stream)
+        atlas_linear_forward(self.h, io, _raw_stream(x.device.index) if stream is None else stream)
         return out
 
     def status(self):
@@ -335,5 +341,5 @@ class Linear(_Layer):
         return rc
 
     def last_path(self):
-        """0: fp32 tiles, 1: tensor cores, 2: few rows."""
+        """1: tensor cores, 2: few rows."""
         return atlas_linear_last_path(self.h)

@@ -23,10 +23,7 @@ struct Geom {
 // activation (the same for all threads), then V neighbouring results
 template <typename TO, int V>
 __device__ __forceinline__ void store_act(int act, float* z, TO* dst) {
-  if (act == ATLAS_ACT_SILU)
-    linear::act_all<ATLAS_ACT_SILU, TO, V>(z);
-  else if (act == ATLAS_ACT_GELU)
-    linear::act_all<ATLAS_ACT_GELU, TO, V>(z);
+  linear::act_run<TO, V>(act, z);
   store_vec<V>(dst, z);
 }
 // V neighbouring channels' weight and bias

@@ -3,7 +3,7 @@
 // y = act(x W + bias) + residual, x [M][K] bf16 (K-major), W [K][N] bf16 read
 // as it lies (MN-major), fp32 accumulation in TMEM.
 //
-// A pair of CTAs on neighbouring SMs owns a 256 x 256 tile (cta_group::2: the
+// A pair of CTAs on neighbouring SMs owns a 256 x 256 (or 256 x 128) tile (cta_group::2: the
 // leader issues M = 256 MMAs; each CTA stages its 128 rows of x and 128 of the
 // 256 columns of W, so an operand byte in shared memory feeds both tensor
 // cores) and is persistent.  Per CTA: five stages of 32 KB (K = 64), and
@@ -22,7 +22,6 @@
 // 24 bits), six products x0 W0, x0 W1, x1 W0, x0 W2, x2 W0, x1 W1 into one
 // accumulator; the dropped ones are below 2^-23 of the sum of |x W|.
 #include <algorithm>
-#include <type_traits>
 
 #include "linear_common.cuh"
 #include "tc2.cuh"
@@ -31,16 +30,21 @@ using layer::bf16;
 
 namespace {
 
-constexpr int BM = 256, BN = 256, BK = 64, STAGES = 5, EPI_WARPS = 8, NTHR = 64 + 32 * EPI_WARPS;
-constexpr int A_BYTES = BM / 2 * BK * 2, B_BYTES = BN / 2 * BK * 2;
-constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
+constexpr int BM = 256, BK = 64, EPI_WARPS = 8, NTHR = 64 + 32 * EPI_WARPS;
 constexpr int BLK_BYTES = 32 * 64;                               // one epilogue block
 constexpr int NBUF = 4;                                          // epilogue blocks per warp
-constexpr int SMEM = STAGES * STAGE_BYTES + EPI_WARPS * NBUF * BLK_BYTES + 1024;
+template <int BN>
+struct Cfg {
+  static constexpr int A_BYTES = BM / 2 * BK * 2, B_BYTES = BN / 2 * BK * 2, STAGE_BYTES = A_BYTES + B_BYTES;
+  static constexpr int STAGES = 5 * 256 / (128 + BN / 2);        // 160 KB of stages: 5, or 6 for BN = 128
+  static constexpr int SMEM = STAGES * STAGE_BYTES + EPI_WARPS * NBUF * BLK_BYTES + 1024;
+  static constexpr int HALF = BN / 2;                            // columns per epilogue warp
+};
 constexpr int BAND = 16;                                         // row tiles per band of the tile order
 
 struct Params {
-  int M, N, nk, planes, kw;   // nk: blocks of 64 of K per plane; kw: W rows per plane
+  int M, N, nk, kc, planes, kw;   // nk: blocks of 64 of K per plane, kc of them per pass; kw: W rows per plane
+  int act;
   const float* bias;
   const void* residual;
   void* y;
@@ -59,15 +63,18 @@ __device__ __forceinline__ void plane_pair(int i, int& a, int& b) {
 struct Tile {
   int m0, n0;
 };
+template <int BN>
 __device__ __forceinline__ Tile tile_at(int t, int ntm, int ntn) {
   const int width = BAND * ntn, first = t / width * BAND, h = min(BAND, ntm - first), r = t % width;
   return {(first + r % h) * BM, r / h * BN};
 }
 
-template <int ACT, typename TO>
+template <typename TO, int BN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHR, 1)
     k_linear_pair(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
                   const __grid_constant__ CUtensorMap map_r, const __grid_constant__ CUtensorMap map_y, Params p) {
+  using Q = Cfg<BN>;
+  constexpr int STAGES = Q::STAGES, STAGE_BYTES = Q::STAGE_BYTES, A_BYTES = Q::A_BYTES, HALF = Q::HALF;
   extern __shared__ uint8_t smraw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smraw) + 1023) & ~uintptr_t(1023));
   uint8_t* blocks = sm + STAGES * STAGE_BYTES;
@@ -78,7 +85,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHR, 1)
   const uint32_t rank = tc::cluster_rank();
   const int ntm = (p.M + BM - 1) / BM, ntn = (p.N + BN - 1) / BN, ntiles = ntm * ntn;
   const int first = blockIdx.x / 2, step = gridDim.x / 2;
-  const int pairs = p.planes == 1 ? 1 : 6;
+  const int pairs = p.planes == 1 ? 1 : 6, passes = (p.nk + p.kc - 1) / p.kc;
 
   if (warp == 0) tc::tmem_alloc_pair(&tbase, 2 * BN);
   if (tid == 32) {
@@ -114,27 +121,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHR, 1)
     uint32_t s = 0, ph = 1;                                  // the first turn finds its slots free
     bool ok = true;
     for (int t = first; t < ntiles && ok; t += step) {
-      const Tile tl = tile_at(t, ntm, ntn);
+      const Tile tl = tile_at<BN>(t, ntm, ntn);
       const int m0 = tl.m0 + (int)rank * (BM / 2), n0 = tl.n0 + (int)rank * (BN / 2);
-      for (int kt = 0; kt < p.nk && ok; ++kt) {
-        for (int pr = 0; pr < pairs; ++pr) {
-          int row_x = m0, row_w = kt * BK;
+      for (int k0 = 0; k0 < p.nk && ok; k0 += p.kc) {
+        const int k1 = min(p.nk, k0 + p.kc);
+        for (int pr = 0; pr < pairs && ok; ++pr) {
+          int row_x = m0, row_w = 0;
           if (pairs > 1) {
             int pa, pb;
             plane_pair(pr, pa, pb);
             row_x += pa * p.M;
-            row_w += pb * p.kw;
+            row_w = pb * p.kw;
           }
-          if (!(ok = __all_sync(0xffffffffu, tc::wait(bempty + 8 * s, ph)))) break;
-          if (tc::elect()) {
-            const uint32_t a = ring + s * STAGE_BYTES, b = a + A_BYTES, bar = lead + 8 * s;
-            if (rank == 0) tc::expect_tx(bfull + 8 * s, 2 * STAGE_BYTES);
-            tc::tma_load_2d_pair(a, &map_x, kt * BK, row_x, bar);
-            tc::tma_load_2d_pair(b, &map_w, n0, row_w, bar);
-            tc::tma_load_2d_pair(b + B_BYTES / 2, &map_w, n0 + 64, row_w, bar);
+          for (int kt = k0; kt < k1; ++kt) {
+            if (!(ok = __all_sync(0xffffffffu, tc::wait(bempty + 8 * s, ph)))) break;
+            if (tc::elect()) {
+              const uint32_t a = ring + s * STAGE_BYTES, b = a + A_BYTES, bar = lead + 8 * s;
+              if (rank == 0) tc::expect_tx(bfull + 8 * s, 2 * STAGE_BYTES);
+              tc::tma_load_2d_pair(a, &map_x, kt * BK, row_x, bar);
+#pragma unroll
+              for (int i = 0; i < HALF / 64; ++i)
+                tc::tma_load_2d_pair(b + i * 8192, &map_w, n0 + 64 * i, row_w + kt * BK, bar);
+            }
+            __syncwarp();
+            if (++s == STAGES) s = 0, ph ^= 1;
           }
-          __syncwarp();
-          if (++s == STAGES) s = 0, ph ^= 1;
         }
       }
     }
@@ -143,16 +154,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHR, 1)
     if (rank == 0) {
       const uint32_t idesc = tc::idesc_f16(BM, BN, 1, 0, 1);
       const uint32_t bfull = tc::smem_u32(full), bempty = tc::smem_u32(empty);
-      const uint64_t ad0 = tc::sdesc_sw128(tc::smem_u32(sm)), bd0 = tc::sdesc_sw128(tc::smem_u32(sm) + A_BYTES, B_BYTES / 2);
+      const uint64_t ad0 = tc::sdesc_sw128(tc::smem_u32(sm)), bd0 = tc::sdesc_sw128(tc::smem_u32(sm) + A_BYTES, 8192);
       uint32_t s = 0, ph = 0, n = 0;
       bool ok = true;
-      for (int t = first; t < ntiles && ok; t += step, ++n) {
-        const uint32_t a = n & 1;
-        // the epilogues have read this accumulator's previous tile
-        if (!(ok = __all_sync(0xffffffffu, tc::wait(tc::smem_u32(&acc_empty[a]), ((n >> 1) & 1) ^ 1)))) break;
-        tc::fence_after_sync();
-        for (int kt = 0; kt < p.nk && ok; ++kt) {
-          for (int pr = 0; pr < pairs; ++pr) {
+      for (int t = first; t < ntiles && ok; t += step) {
+        for (int k0 = 0; k0 < p.nk && ok; k0 += p.kc, ++n) {
+          const uint32_t a = n & 1;
+          // the epilogues have read this accumulator's last contents
+          if (!(ok = __all_sync(0xffffffffu, tc::wait(tc::smem_u32(&acc_empty[a]), ((n >> 1) & 1) ^ 1)))) break;
+          tc::fence_after_sync();
+          const int stages = (min(p.nk, k0 + p.kc) - k0) * pairs;
+          for (int i = 0; i < stages; ++i) {
             if (!(ok = __all_sync(0xffffffffu, tc::wait(bfull + 8 * s, ph)))) break;
             if (tc::elect()) {
               const uint64_t ad = ad0 + s * (STAGE_BYTES >> 4), bd = bd0 + s * (STAGE_BYTES >> 4);
@@ -160,35 +172,35 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHR, 1)
 #pragma unroll
               for (int ks = 0; ks < BK / 16; ++ks)
                 tc::mma_f16_pair(tacc + a * BN, ad + ks * (32 >> 4), bd + ks * ((16 * 128) >> 4), idesc,
-                                 (kt > 0 || pr > 0 || ks > 0) ? 1u : 0u);
+                                 (i > 0 || ks > 0) ? 1u : 0u);
               tc::mma_commit_pair(bempty + 8 * s, 3);
             }
             __syncwarp();
             if (++s == STAGES) s = 0, ph ^= 1;
           }
+          if (ok && tc::elect()) tc::mma_commit_pair(tc::smem_u32(&acc_full[a]), 3);
+          __syncwarp();
         }
-        if (ok && tc::elect()) tc::mma_commit_pair(tc::smem_u32(&acc_full[a]), 3);
-        __syncwarp();
       }
       if (!ok && lane == 0) atomicExch(&failed, 1);
     }
   } else {
     constexpr int CW = 64 / (int)sizeof(TO);         // columns of a block on the TMA path
     const int e = warp - 2, q = warp & 3, half = e >> 2;
-    constexpr int NBLK = 128 / CW;                   // blocks of a tile per warp
+    constexpr int NBLK = HALF / CW;                  // blocks of a tile per warp
     uint8_t* buf = blocks + e * NBUF * BLK_BYTES;
     const uint32_t lane_base = (uint32_t)(32 * q) << 16;
     const uint32_t release[2] = {tc::map_rank(&acc_empty[0], 0), tc::map_rank(&acc_empty[1], 0)};
     const TO* res = (const TO*)p.residual;
     TO* y = (TO*)p.y;
     const bool fetch = p.tma_out && res;
-    uint32_t blk = 0, grp = 0, n = 0;   // blocks, groups of NBUF blocks and tiles so far
+    uint32_t blk = 0, grp = 0, n = 0;   // blocks, groups of NBUF blocks and accumulators so far
     bool ok = true;
-    // the warp's part of tile t: 32 rows from row m, 128 columns from column c
+    // the warp's part of tile t: 32 rows from row m, HALF columns from column c
     auto part_of = [&](int t, int& m, int& c) {
-      const Tile tl = tile_at(t, ntm, ntn);
+      const Tile tl = tile_at<BN>(t, ntm, ntn);
       m = tl.m0 + (int)rank * 128 + 32 * q;
-      c = tl.n0 + half * 128;
+      c = tl.n0 + half * HALF;
     };
     // asks for the residual of the next group inside y, at or behind column ac
     // of tile at: NBUF blocks into the warp's buffers, all of them free
@@ -196,10 +208,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHR, 1)
       int m, c;
       for (; at < ntiles; at += step, ac = 0) {
         part_of(at, m, c);
-        if (m < p.M && ac < 128 && c + ac < p.N) break;
+        if (m < p.M && ac < HALF && c + ac < p.N) break;
       }
       if (at < ntiles && tc::elect()) {
-        const int cnt = min(NBUF, (p.N - c - ac + CW - 1) / CW);
+        const int cnt = min(min(NBUF, (HALF - ac) / CW), (p.N - c - ac + CW - 1) / CW);
         tc::mbar_expect_tx(&res_full[e], cnt * BLK_BYTES);
         for (int i = 0; i < cnt; ++i) tc::tma_load_2d(buf + i * BLK_BYTES, &map_r, c + ac + i * CW, m, &res_full[e]);
       }
@@ -211,48 +223,99 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHR, 1)
       ask(at, ac);
     };
     if (fetch) ask(first, 0);
+    // fp32 results: the sums of the passes before the tile's last
+    constexpr int NSUM = sizeof(TO) == 4 ? HALF : 1;
+    float sums[NSUM];
     for (int t = first; t < ntiles; t += step, ++n) {
+      int m, cbeg;
+      part_of(t, m, cbeg);
+      if constexpr (sizeof(TO) == 4) {
+#pragma unroll
+        for (int j = 0; j < NSUM; ++j) sums[j] = 0.f;
+        for (int ps = 0; ps + 1 < passes; ++ps, ++n) {
+          const int a = n & 1;
+          ok = __all_sync(0xffffffffu, tc::wait(tc::smem_u32(&acc_full[a]), (n >> 1) & 1));
+          if (!ok) break;
+          tc::fence_after_sync();
+#pragma unroll
+          for (int j = 0; j < HALF; j += 32) {
+            float v[32];
+            tc::tmem_ld32(tacc + a * BN + lane_base + half * HALF + j, v);
+            tc::tmem_ld_wait32(v);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) sums[j + i] += v[i];
+          }
+          tc::fence_before_sync();
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive_remote(release[a]);
+        }
+        if (!ok) break;
+      }
       const int a = n & 1;
       ok = __all_sync(0xffffffffu, tc::wait(tc::smem_u32(&acc_full[a]), (n >> 1) & 1));
       if (!ok) break;
       tc::fence_after_sync();
-      int m, cbeg;
-      part_of(t, m, cbeg);
-      const uint32_t col0 = tacc + a * BN + lane_base + half * 128;
+      const uint32_t col0 = tacc + a * BN + lane_base + half * HALF;
       if (m < p.M && p.tma_out) {
-        float v[2][CW], bias[2][CW];
-        auto fetch_block = [&](int c, float* vv, float* bb) {
+        // bf16: the next block's accumulator and bias are on their way while this
+        // one is worked on; fp32 has no registers left for that
+        constexpr int AHEAD = sizeof(TO) == 2 ? 1 : 0;
+        float v[1 + AHEAD][CW], bias[AHEAD ? CW : 1];
+        auto fetch_block = [&](int c, float* vv) {
           if constexpr (CW == 32)
             tc::tmem_ld32(col0 + c, vv);
           else
             tc::tmem_ld16(col0 + c, vv);
-          if (p.bias) {
-            const float* bp = p.bias + cbeg + c;
-            if (cbeg + c + CW <= p.N) {
+        };
+        // four of the block's bias values (p.bias on a 16-byte boundary here)
+        auto bias4 = [&](int c, float* bb) {
+          if (cbeg + c + 4 <= p.N) {
+            layer::load_vec<4>(p.bias + cbeg + c, bb);
+          } else {
 #pragma unroll
-              for (int j = 0; j < CW; j += 4) layer::load_vec<4>(bp + j, bb + j);
-            } else {
-#pragma unroll
-              for (int j = 0; j < CW; ++j) bb[j] = cbeg + c + j < p.N ? bp[j] : 0.f;
-            }
+            for (int j = 0; j < 4; ++j) bb[j] = cbeg + c + j < p.N ? p.bias[cbeg + c + j] : 0.f;
           }
         };
-        fetch_block(0, v[0], bias[0]);
+        auto fetch_bias = [&](int c, float* bb) {
+          if (p.bias)
+#pragma unroll
+            for (int j = 0; j < CW; j += 4) bias4(c + j, bb + j);
+        };
+        if constexpr (AHEAD == 1) {
+          fetch_bias(0, bias);
+          fetch_block(0, v[0]);
+        }
 #pragma unroll
         for (int i = 0; i < NBLK; ++i) {
           const int c = i * CW;
           if (cbeg + c >= p.N) break;
-          float* vv = v[i & 1];
-          float* bb = bias[i & 1];
+          float* vv = v[i & AHEAD];
+          if constexpr (AHEAD == 0) fetch_block(c, vv);
           if constexpr (CW == 32)
             tc::tmem_ld_wait32(vv);
           else
             tc::tmem_ld_wait16(vv);
-          if (i + 1 < NBLK) fetch_block(c + CW, v[(i + 1) & 1], bias[(i + 1) & 1]);
-          if (p.bias)
+          if constexpr (AHEAD == 1) {
+            if (i + 1 < NBLK) fetch_block(c + CW, v[(i + 1) & 1]);
+          } else {
 #pragma unroll
-            for (int j = 0; j < CW; ++j) vv[j] += bb[j];
-          linear::act_all<ACT, TO, CW>(vv);
+            for (int j = 0; j < CW; ++j) vv[j] += sums[c + j];
+          }
+          if constexpr (AHEAD == 1) {
+            if (p.bias)
+#pragma unroll
+              for (int j = 0; j < CW; ++j) vv[j] += bias[j];
+            if (i + 1 < NBLK) fetch_bias(c + CW, bias);
+          } else if (p.bias) {
+#pragma unroll
+            for (int j = 0; j < CW; j += 4) {
+              float bb[4];
+              bias4(c + j, bb);
+#pragma unroll
+              for (int k = 0; k < 4; ++k) vv[j + k] += bb[k];
+            }
+          }
+          linear::act_run<TO, CW>(p.act, vv);
           const uint32_t b = fetch ? i % NBUF : blk % NBUF;
           if (fetch) {
             if (i % NBUF == 0) {
@@ -289,27 +352,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHR, 1)
         if (!ok) break;
       } else if (m < p.M) {
         float* st = reinterpret_cast<float*>(buf);   // 32 rows of 16 values, stride 17
-#pragma unroll 1
-        for (int c = 0; c < 128; c += 16) {
+        const int rows = min(32, p.M - m), r0 = lane / 16;
+#pragma unroll
+        for (int c = 0; c < HALF; c += 16) {
           if (cbeg + c >= p.N) break;
-          float v[16];
+          const int col = cbeg + c + lane % 16;
+          const size_t at = (size_t)(m + r0) * p.N + col;
+          const bool in = col < p.N;
+          const float bv = p.bias && in ? p.bias[col] : 0.f;
+          float v[16], rv[16];
           tc::tmem_ld16(col0 + c, v);
+          // all 16 rows of the residual in flight at once
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            rv[i] = res && in && r0 + 2 * i < rows ? layer::to_f32(res[at + (size_t)(2 * i) * p.N]) : 0.f;
           tc::tmem_ld_wait16(v);
 #pragma unroll
-          for (int j = 0; j < 16; ++j) st[lane * 17 + j] = v[j];
-          __syncwarp();
-          const int col = cbeg + c + lane % 16;
-          if (col < p.N) {
-            const float bv = p.bias ? p.bias[col] : 0.f;
-            const int rows = min(32, p.M - m);
-#pragma unroll 4
-            for (int r = lane / 16; r < rows; r += 2) {
-              const size_t at = (size_t)(m + r) * p.N + col;
-              float o = linear::act_for<ACT, TO>(st[r * 17 + lane % 16] + bv);
-              if (res) o += layer::to_f32(res[at]);
-              y[at] = layer::from_f32<TO>(o);
-            }
+          for (int j = 0; j < 16; ++j) {
+            if constexpr (sizeof(TO) == 4) v[j] += sums[c + j];
+            st[lane * 17 + j] = v[j];
           }
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 16; ++i) v[i] = st[(r0 + 2 * i) * 17 + lane % 16] + bv;
+          linear::act_run<TO, 16>(p.act, v);
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            if (in && r0 + 2 * i < rows) y[at + (size_t)(2 * i) * p.N] = layer::from_f32<TO>(v[i] + rv[i]);
           __syncwarp();
         }
       }
@@ -334,24 +403,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHR, 1)
   if (warp == 0) tc::tmem_dealloc_pair(tbase, 2 * BN);
 }
 
-template <int ACT, typename TO>
+// How many blocks of 64 of K go into one accumulator.  The tensor cores cut
+// off, they do not round: an fp32 accumulator loses about 1.1e-9 of the result
+// per value of K (measured: 4.8e-7 at K = 517, 9.1e-6 at 8192).  fp32 results
+// take K in passes of 512, added up in registers; three planes in passes of
+// 256, each with its five small products first.  bf16 results round at 2^-9.
+int blocks_per_pass(const linear::TcCall& c, int nk) {
+  return c.out_bf16 && c.planes == 1 ? nk : std::min(nk, c.planes == 1 ? 8 : 4);
+}
+
+template <typename TO, int BN>
 cudaError_t launch_pair(const linear::TcCall& c, cudaStream_t st) {
   CUtensorMap mx, mw, mr, my;
   if (!tc::tensor_map_2d(&mx, c.x, true, (uint64_t)c.planes * c.M, c.K, (uint64_t)c.ldx * 2, BM / 2) ||
       !tc::tensor_map_2d(&mw, c.W, true, (uint64_t)c.planes * c.K, c.N, (uint64_t)c.ldw * 2, BK))
     return cudaErrorInvalidValue;
-  Params p{c.M, c.N, (c.K + BK - 1) / BK, c.planes, c.K, c.bias, c.residual, c.y, 0, c.status};
+  const int nk = (c.K + BK - 1) / BK;
+  Params p{c.M, c.N, nk, blocks_per_pass(c, nk), c.planes, c.K, c.act, c.bias, c.residual, c.y, 0, c.status};
   const uint64_t row = (uint64_t)c.N * sizeof(TO);
   p.tma_out = row % 16 == 0 && layer::aligned16(c.y) && layer::aligned16(c.residual) && layer::aligned16(c.bias) &&
               tc::tensor_map_2d(&my, c.y, sizeof(TO) == 2, c.M, c.N, row, 32, 64) &&
               tc::tensor_map_2d(&mr, c.residual ? c.residual : c.y, sizeof(TO) == 2, c.M, c.N, row, 32, 64);
   if (!p.tma_out) mr = my = mx;   // not used
-  auto kern = k_linear_pair<ACT, TO>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+  auto kern = k_linear_pair<TO, BN>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<BN>::SMEM);
   if (e != cudaSuccess) return e;
   const long long tiles = (long long)((c.M + BM - 1) / BM) * ((c.N + BN - 1) / BN);
   const int grid = (int)std::min<long long>(tiles, layer::sm_count() / 2) * 2;
-  return tc::launch_overlapped(kern, dim3(grid), dim3(NTHR), SMEM, st, mx, mw, mr, my, p);
+  return tc::launch_overlapped(kern, dim3(grid), dim3(NTHR), Cfg<BN>::SMEM, st, mx, mw, mr, my, p);
 }
 
 }  // namespace
@@ -359,13 +438,14 @@ cudaError_t launch_pair(const linear::TcCall& c, cudaStream_t st) {
 namespace linear {
 
 cudaError_t tc_big(const TcCall& c, cudaStream_t st) {
-  auto by_type = [&](auto act) {
-    constexpr int A = decltype(act)::value;
-    return c.out_bf16 ? launch_pair<A, bf16>(c, st) : launch_pair<A, float>(c, st);
-  };
-  if (c.act == ATLAS_ACT_SILU) return by_type(std::integral_constant<int, ATLAS_ACT_SILU>());
-  if (c.act == ATLAS_ACT_GELU) return by_type(std::integral_constant<int, ATLAS_ACT_GELU>());
-  return by_type(std::integral_constant<int, ATLAS_ACT_NONE>());
+  // 128 columns per tile where the last round of tiles then wastes less: time in
+  // units of 128 columns, the narrow tiles 1.3 times as long per column (they
+  // fetch 1.5 times as much: 8192^3 took 816 us with them, 665 with wide ones)
+  const long long pairs = layer::sm_count() / 2, tm = (c.M + BM - 1) / BM;
+  const long long wide = (tm * ((c.N + 255) / 256) + pairs - 1) / pairs * 2,
+                  narrow = (tm * ((c.N + 127) / 128) + pairs - 1) / pairs;
+  if (13 * narrow < 10 * wide) return c.out_bf16 ? launch_pair<bf16, 128>(c, st) : launch_pair<float, 128>(c, st);
+  return c.out_bf16 ? launch_pair<bf16, 256>(c, st) : launch_pair<float, 256>(c, st);
 }
 
 }  // namespace linear

@@ -118,6 +118,15 @@ __device__ __forceinline__ void act_all(float* z) {
   }
 }
 
+// the same for an activation known at run time only (the same for all threads)
+template <typename TO, int V>
+__device__ __forceinline__ void act_run(int act, float* z) {
+  if (act == ATLAS_ACT_SILU)
+    act_all<ATLAS_ACT_SILU, TO, V>(z);
+  else if (act == ATLAS_ACT_GELU)
+    act_all<ATLAS_ACT_GELU, TO, V>(z);
+}
+
 // One product on the tensor cores: bf16 planes in, epilogue out.
 struct TcCall {
   int M, N;

@@ -284,8 +284,9 @@ struct Plan {
 // Segments of the tokens for `ctas` (row, head, slice) triples of `chunks`
 // chunks each.  One segment per triple reads every input once; n segments cost
 // another pass over k and v for the states at their starts (`extra` of a
-// chunk's time, measured 0.4) and two more launches (about 3 chunks' time), so
-// n is the one with the least of
+// chunk's time, measured 0.4) and another launch (about 3 chunks' time), and a
+// block's start and end take about 2 chunks' time, so n is the one with the
+// least of
 //   waves of the read-out pass + waves of the state pass + launches.
 int best_segments(long long ctas, long long chunks, long long slots) {
   long long best = 1;
@@ -294,7 +295,7 @@ int best_segments(long long ctas, long long chunks, long long slots) {
     const long long per = (chunks + n - 1) / n;
     if (n > 1 && (chunks + per - 1) / per != n) continue;
     const long long waves = (ctas * n + slots - 1) / slots, before = (ctas * (n - 1) + slots - 1) / slots;
-    const double c = (double)waves * per + (n > 1 ? 0.4 * before * per + 3 : 0);
+    const double c = (double)waves * (per + 2) + (n > 1 ? 0.4 * before * (per + 2) + 3 : 0);
     if (n == 1 || c < cost) best = n, cost = c;
     if (ctas * n > 4 * slots) break;
   }
@@ -315,8 +316,8 @@ Plan make_plan(const atlas_decay_config& c, int B, int T, bool tc) {
   tc = tc && c.qkv_dtype == ATLAS_BF16 && c.d_k % 8 == 0 && c.d_v % 8 == 0 && c.d_k <= 128;
   pl.path = tc ? 2 : 1;
   pl.C = tc ? decay::kTcChunk : chunk_tokens(c.d_k);
-  // CTAs that run at once: two per SM where their shared memory allows it
-  const long long slots = (c.d_k <= 64 ? 2LL : 1LL) * sm_count();
+  // CTAs that run at once: two per SM for the fp32 chunks where their shared memory allows it
+  const long long slots = (!tc && c.d_k <= 64 ? 2LL : 1LL) * sm_count();
   const long long chunks = (T + pl.C - 1) / pl.C;
   const long long n = best_segments((long long)B * c.H * pl.slices, chunks, slots);
   pl.seg = (int)((chunks + n - 1) / n * pl.C);

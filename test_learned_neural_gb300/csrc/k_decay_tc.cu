@@ -20,91 +20,14 @@
 // k_decay_tc_state: a segment's own contribution to the state at its end, the
 // same product with weights counted to the segment's end, accumulated in TMEM
 // over the whole segment.
-#include "decay_common.cuh"
-#include "decay_tc.cuh"
-#include "tc2.cuh"
+#include "decay_tc_dev.cuh"
 
-using decay::Geom;
-using decay::Ptrs;
+using namespace decay;
 using layer::bf16;
 
 namespace {
 
-constexpr int C = 128, NTHR = 256, SL = 64;   // tokens per chunk, threads, columns per slice
-constexpr int TILE = C * 128;                 // 128 rows of 64 bf16 values
-
-// 4-D map over [row][head][token][d] in either layout: boxes of 64 bf16 or 32
-// fp32 values x 128 tokens, 128-byte swizzled
-bool map_4d(CUtensorMap* map, const void* base, bool is_bf16, int d, int T, int heads, int B, size_t st, size_t sh,
-            size_t sb) {
-  auto fn = tc::tensor_map_encoder();
-  if (!fn) return false;
-  const size_t es = is_bf16 ? 2 : 4;
-  const cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)T, (cuuint64_t)heads, (cuuint64_t)B};
-  const cuuint64_t strides[3] = {st * es, sh * es, sb * es};
-  const cuuint32_t box[4] = {is_bf16 ? 64u : 32u, (cuuint32_t)C, 1, 1}, estr[4] = {1, 1, 1, 1};
-  return fn(map, is_bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4,
-            const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-__device__ __forceinline__ void load_4d(uint32_t dst, const CUtensorMap* map, int c, int t, int h, int b, uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(
-          dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(c), "r"(t), "r"(h), "r"(b), "r"(bar)
-      : "memory");
-}
-__device__ __forceinline__ void store_4d(const CUtensorMap* map, int c, int t, int h, int b, uint32_t src) {
-  asm volatile("cp.async.bulk.tensor.4d.global.shared::cta.bulk_group [%0, {%1, %2, %3, %4}], [%5];" ::"l"(
-                   reinterpret_cast<uint64_t>(map)),
-               "r"(c), "r"(t), "r"(h), "r"(b), "r"(src)
-               : "memory");
-}
-// D (+)= A B^T with A (16-bit, two values of K per column) in TMEM
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(bdesc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-// 16 packed columns of this warp's lanes
-__device__ __forceinline__ void tmem_st16u(uint32_t taddr, const uint32_t* v) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
-      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
-      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
-      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
-      : "memory");
-}
-__device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
-}
-__device__ __forceinline__ void lds128(uint32_t addr, uint32_t* w) {
-  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-               : "r"(addr)
-               : "memory");
-}
-// byte offset of 16-byte chunk j of row r in a 128-byte swizzled tile
-__device__ __forceinline__ uint32_t swz(int r, int j) { return (uint32_t)(r * 128 + ((j ^ (r & 7)) << 4)); }
-
-// Two fp32 values as N packed bf16 pairs whose sums are the values to 8 N
-// bits: each term but the last is the remainder's leading bits cut off, so the
-// subtraction is exact; the last is rounded.
-template <int N>
-__device__ __forceinline__ void split2(float a, float b, uint32_t* w) {
-#pragma unroll
-  for (int i = 0; i + 1 < N; ++i) {
-    const uint32_t ua = __float_as_uint(a), ub = __float_as_uint(b);
-    w[i] = __byte_perm(ua, ub, 0x7632);
-    a -= __uint_as_float(ua & 0xffff0000u);
-    b -= __uint_as_float(ub & 0xffff0000u);
-  }
-  w[N - 1] = layer::pack_bf16(a, b);
-}
+constexpr int NTHR = 256;
 
 // Rows n .. 127 of a tile become zero (a row's tokens past its length: 0 * NaN
 // must not reach the sums).
@@ -135,22 +58,6 @@ __device__ __forceinline__ void store_keys(uint32_t tile, int tid, const uint32_
   const int r = tid & (C - 1), j0 = (tid >> 7) * 4;
 #pragma unroll
   for (int j = 0; j < 4; ++j) sts128(tile + swz(r, j0 + j), k0[4 * j], k0[4 * j + 1], k0[4 * j + 2], k0[4 * j + 3]);
-}
-
-// (w K)^T V into TMEM at d: three terms of KB 64-wide key tiles, one
-// instruction per 16 tokens; terms at t0, t1, t2 (tiles of a term KB * TILE
-// bytes), M = 64 KB
-template <int KB>
-__device__ __forceinline__ void mma_state(uint32_t d, uint32_t t0, uint32_t t1, uint32_t t2, uint32_t vtile,
-                                          bool accumulate) {
-  const uint32_t idesc = tc::idesc_f16(64 * KB, SL, 1, 1, 1);
-  const uint64_t vd = tc::sdesc_sw128(vtile, TILE);
-  const uint64_t kd[3] = {tc::sdesc_sw128(t0, TILE), tc::sdesc_sw128(t1, TILE), tc::sdesc_sw128(t2, TILE)};
-#pragma unroll
-  for (int i = 2; i >= 0; --i)
-#pragma unroll
-    for (int s = 0; s < C / 16; ++s)
-      tc::mma_f16(d, kd[i] + s * (2048 >> 4), vd + s * (2048 >> 4), idesc, (accumulate || i < 2 || s > 0) ? 1u : 0u);
 }
 
 // The state's product as the threads hold it: KB = 1: M = 64, row 16 q + lane
@@ -616,6 +523,7 @@ cudaError_t launch_state(const CUtensorMap& mk, const CUtensorMap& mv, const Geo
 namespace decay {
 
 cudaError_t tc_launch(const Geom& g, const Ptrs& p, bool y_bf16, int* status, cudaStream_t st) {
+  if (g.d_k <= 64) return ws_launch(g, p, y_bf16, status, st);
   CUtensorMap mq, mk, mv, my;
   const int hq = g.H / g.share;
   if (!map_4d(&mq, p.q, true, g.d_k, g.T, hq, g.B, g.qk_t, g.qk_h, g.qk_b) ||

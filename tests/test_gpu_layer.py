@@ -97,6 +97,8 @@ DECAY = [
     (2, 2, 1, 127, 64, 64), (1, 6, 2, 128, 64, 128), (1, 6, 3, 129, 128, 64), (3, 2, 1, 300, 24, 80),
     (1, 2, 1, 200, 3, 130), (1, 2, 1, 150, 136, 72), (1, 1, 1, 257, 256, 65), (1, 1, 1, 2050, 64, 64),
     (2, 1, 1, 1111, 128, 128), (160, 1, 1, 140, 32, 32), (2, 6, 1, 700, 96, 40),
+    # rings of stages that turn more than once: many chunks per block, whole (more rows than SMs) and in segments
+    (160, 1, 1, 900, 64, 64), (40, 1, 1, 2300, 64, 64), (20, 2, 1, 1500, 128, 64),
 ]
 
 

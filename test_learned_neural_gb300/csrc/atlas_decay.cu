@@ -130,18 +130,33 @@ __global__ void __launch_bounds__(256) k_decay_chunk(Geom g, Ptrs p) {
   }
   for (int i = tid; i <= C; i += 256) pw[i] = decay::power(l2g, i);
 
+  // four values at a time where every row starts on their boundary
+  const bool vec = g.d_k % 4 == 0 && g.d_v % 4 == 0 && ((uintptr_t)p.q | (uintptr_t)p.k | (uintptr_t)p.v) % 16 == 0;
+  const bool y_vec = (uintptr_t)p.y % 16 == 0;
   for (int t0 = t_lo; t0 < t_live; t0 += C) {
     const int n = min(C, t_live - t0);
     __syncthreads();
-    for (int i = tid; i < C * dk4; i += 256) {
-      const int r = i / dk4, c = i % dk4;
-      const bool in = r < n && c < g.d_k;
-      Ks[r * ldk + c] = in ? to_f32(k[(t0 + r) * g.qk_t + c]) : 0.f;
-      if constexpr (READ) Qs[r * ldk + c] = in ? to_f32(q[(t0 + r) * g.qk_t + c]) : 0.f;
-    }
-    for (int i = tid; i < C * kSlice; i += 256) {
-      const int r = i / kSlice, c = i % kSlice;
-      Vs[r * LDV + c] = r < n && c < cols ? to_f32(v[(t0 + r) * g.v_t + c]) : 0.f;
+    // 16 threads side by side per token, four values each
+    auto load4 = [&](const TI* src, int c, int width, bool in, float* dst) {
+      float v[4] = {0.f, 0.f, 0.f, 0.f};
+      if (in && vec && c + 4 <= width) {
+        load_vec<4>(src + c, v);
+      } else if (in) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (c + e < width) v[e] = to_f32(src[c + e]);
+      }
+      *reinterpret_cast<float4*>(dst + c) = make_float4(v[0], v[1], v[2], v[3]);
+    };
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      const int r = ty + 16 * i;
+      const size_t at = (size_t)(t0 + r) * g.qk_t;
+      for (int c = 4 * tx; c < dk4; c += 64) {
+        load4(k + at, c, g.d_k, r < n, Ks + r * ldk);
+        if constexpr (READ) load4(q + at, c, g.d_k, r < n, Qs + r * ldk);
+      }
+      load4(v + (size_t)(t0 + r) * g.v_t, 4 * tx, cols, r < n, Vs + r * LDV);
     }
     __syncthreads();
     if constexpr (READ) {
@@ -202,10 +217,17 @@ __global__ void __launch_bounds__(256) k_decay_chunk(Geom g, Ptrs p) {
 #pragma unroll
       for (int i = 0; i < NI; ++i) {
         const int r = ty + 16 * i;
-        if (r < n)
+        if (r >= n) continue;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[i][e] *= g.scale;
+        TO* dst = y + (t0 + r) * g.y_t + 4 * tx;
+        if (vec && y_vec && 4 * tx + 4 <= cols) {
+          store_vec<4>(dst, o[i]);
+        } else {
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            if (4 * tx + e < cols) y[(t0 + r) * g.y_t + 4 * tx + e] = from_f32<TO>(g.scale * o[i][e]);
+            if (4 * tx + e < cols) dst[e] = from_f32<TO>(o[i][e]);
+        }
       }
       __syncthreads();   // every read of the state is done
     }

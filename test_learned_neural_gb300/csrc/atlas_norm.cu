@@ -216,26 +216,28 @@ __device__ __forceinline__ void reduce_groups(const Geom& g, const Place& p, con
   }
 }
 
-constexpr int kAhead = 2;   // rows of a step; two steps in flight per thread
+template <int V>
+constexpr int kAhead = V == 1 ? 8 : 2;   // rows of a step; two steps in flight per thread
 
-// f(i, values) for the `cnt` rows at src, src + step, ...; kAhead rows' loads
-// are in flight while the kAhead before them are worked on
+// f(i, values) for the `cnt` rows at src, src + step, ...; the loads of a step
+// are in flight while the step before it is worked on
 template <typename TI, int V, typename F>
 __device__ __forceinline__ void for_rows(const TI* src, size_t step, int cnt, F f) {
-  Words<TI, V> next[kAhead];
+  constexpr int A = kAhead<V>;
+  Words<TI, V> next[A];
 #pragma unroll
-  for (int a = 0; a < kAhead; ++a)
+  for (int a = 0; a < A; ++a)
     if (a < cnt) next[a].load(src + a * step);
-  for (int i = 0; i < cnt; i += kAhead) {
-    Words<TI, V> now[kAhead];
-    src += kAhead * step;
+  for (int i = 0; i < cnt; i += A) {
+    Words<TI, V> now[A];
+    src += A * step;
 #pragma unroll
-    for (int a = 0; a < kAhead; ++a) {
+    for (int a = 0; a < A; ++a) {
       now[a] = next[a];
-      if (i + kAhead + a < cnt) next[a].load(src + a * step);
+      if (i + A + a < cnt) next[a].load(src + a * step);
     }
 #pragma unroll
-    for (int a = 0; a < kAhead; ++a)
+    for (int a = 0; a < A; ++a)
       if (i + a < cnt) {
         float v[V];
         now[a].values(v);

@@ -11,8 +11,10 @@
 //
 // Only the state warps carry anything from chunk to chunk, so the others run
 // ahead: the scores and keys of chunk c + 1 are formed while chunk c's products
-// run.  TMEM: two score buffers (P in place), inter and intra
-// read-outs, the state's product, and a third term of P for fp32 read-outs.
+// run.  TMEM: two score buffers (P's first two terms in place), inter and intra
+// read-outs, the state's product (transposed, V^T (w K), in as many blocks of
+// columns as there is room for: an MMA of N = 64 takes as long as one of 96),
+// and the third term of P for fp32 read-outs.
 // In lock step (every warp doing each stage in turn, two CTAs per SM) the same
 // work took 6300 cycles per chunk and SM at 1.5 instructions per cycle.
 #include <algorithm>
@@ -43,6 +45,29 @@ __device__ __forceinline__ void scale_chunk(uint32_t src, uint32_t dst, int r, i
   for (int i = 0; i < 4; ++i) split_pair<3>(mul_pair(widen(live ? x[i] : 0u), pair(w, w)), y[i]);
 #pragma unroll
   for (int t = 0; t < 3; ++t) sts128(dst + t * TILE + swz(r, j), y[0][t], y[1][t], y[2][t], y[3][t]);
+}
+// V^T (w K) into TMEM at d, rows d_v, columns d_k, in BLOCKS blocks of 64
+// columns: 3: a block per term, one MMA of N = 192 per 16 tokens; 2: term 0,
+// then terms 1 and 2; 1: all three.  The sum of the blocks is the product.
+template <int BLOCKS>
+__device__ __forceinline__ void mma_state_t(uint32_t d, uint32_t keys, uint32_t vtile, bool accumulate) {
+  const uint64_t vd = tc::sdesc_sw128(vtile, TILE), kd = tc::sdesc_sw128(keys, TILE);
+  const uint32_t wide = tc::idesc_f16(64, 64 * BLOCKS, 1, 1, 1), one = tc::idesc_f16(64, 64, 1, 1, 1);
+  auto term = [&](int t, uint32_t at, uint32_t idesc, bool acc) {
+#pragma unroll
+    for (int s = 0; s < C / 16; ++s)
+      tc::mma_f16(at, vd + s * (2048 >> 4), kd + (t * TILE >> 4) + s * (2048 >> 4), idesc, (acc || s > 0) ? 1u : 0u);
+  };
+  if constexpr (BLOCKS == 3) {
+    term(0, d, wide, accumulate);
+  } else if constexpr (BLOCKS == 2) {
+    term(0, d, wide, accumulate);
+    term(2, d + 64, one, true);
+  } else {
+    term(2, d, one, accumulate);
+    term(1, d, one, true);
+    term(0, d, one, true);
+  }
 }
 __device__ __forceinline__ void zero_row(uint32_t tile, int r) {
 #pragma unroll
@@ -83,7 +108,9 @@ __global__ void __launch_bounds__(NTHR, 1)
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
-  const uint32_t tm = *tbase;
+  // All 512 columns: they start at 0.  As a constant (and not as read back) the
+  // MMAs' operands stay in uniform registers.
+  constexpr uint32_t tm = 0;
   tc::grid_dependency_wait();
   tc::grid_dependents_launch();
 
@@ -96,8 +123,8 @@ __global__ void __launch_bounds__(NTHR, 1)
   for (int i = tid; i <= C; i += NTHR) pw[i] = power(l2g, i);
   if (tid < 32) rev[tid] = power(l2g, 31 - tid);
   __syncthreads();
-  bool ok = *failed == 0;
-  const uint32_t tSC = tm, tY1 = tm + 256, tY2 = tm + 320, tDS = tm + 384, tP2 = tm + 448;
+  bool ok = *failed == 0 && *tbase == tm;
+  constexpr uint32_t tSC = tm, tY1 = tm + 256, tY2 = tm + 320, tDS = tm + 384, tP2 = tm + 448;   // tP2: NT = 3
   auto all_wait = [&](int i, uint32_t parity) { return __all_sync(0xffffffffu, tc::wait(bar(i), parity)); };
   auto arrive = [&](int i) {
     __syncwarp();
@@ -145,33 +172,45 @@ __global__ void __launch_bounds__(NTHR, 1)
     if (ok && chunks > 0) scores(0);
     for (int c = 0; c < chunks && ok; ++c) {
       const uint32_t at = base + (c % STAGES) * STAGE, vt = at + 2 * TILE;
-      // state product: the keys' terms are there, the last product has been taken
-      if (!(ok = all_wait(K, c & 1) && (c == 0 || all_wait(DSFREE, (c - 1) & 1)))) break;
-      tc::fence_after_sync();
-      if (tc::elect()) {
-        mma_state<1>(tDS, base + L::k0, base + L::k0 + TILE, base + L::k0 + 2 * TILE, vt, false);
-        tc::mma_commit(bars + DS);
-      }
-      __syncwarp();
-      // scores of the next chunk: chunk c - 1, which had the same buffer, is done
-      if (c + 1 < chunks) {
-        if (c > 0 && !(ok = all_wait(Y, (c - 1) & 1))) break;
+      // scores of the next chunk, where P of the one before was
+      auto next_scores = [&]() {
+        if (c + 1 >= chunks) return;
+        if (c > 0 && !(ok = all_wait(PV, (c - 1) & 1))) return;
         tc::fence_after_sync();
         scores(c + 1);
-        if (!ok) break;
+      };
+      // state product: the keys' terms are there, the last product has been taken
+      auto state_product = [&]() {
+        if (!(ok = all_wait(K, c & 1) && (c == 0 || all_wait(DSFREE, (c - 1) & 1)))) return;
+        tc::fence_after_sync();
+        if (tc::elect()) {
+          mma_state_t<NT == 1 ? 2 : 1>(tDS, base + L::k0, vt, false);
+          tc::mma_commit(bars + DS);
+        }
+        __syncwarp();
+      };
+      // NT = 3 holds its stages longer, so the next chunk's copies come later:
+      // scores first cost it 3 % (417 against 405 us at 16 x 131072 tokens); NT = 1
+      // waits for the keys instead (36 against 34 us at 32 x 4096 tokens)
+      if constexpr (NT == 1) {
+        next_scores();
+        if (ok) state_product();
+      } else {
+        state_product();
+        if (ok) next_scores();
       }
+      if (!ok) break;
       if (!(ok = all_wait(P + (c & 1), (c >> 1) & 1) && (c == 0 || all_wait(YFREE, (c - 1) & 1)))) break;
       tc::fence_after_sync();
-      const uint32_t idesc = tc::idesc_f16(C, SL, 1, 0, 1);
+      const uint32_t idesc = tc::idesc_f16(C, SL, 1, 0, 1), idesc_s = tc::idesc_f16(C, SL, 1, 0, 0);
       if (tc::elect()) {
-        const uint32_t ps = tSC + 128 * (c & 1);
         const uint64_t vd = tc::sdesc_sw128(vt, TILE);
 #pragma unroll
         for (int k = NT - 1; k >= 0; --k)
 #pragma unroll
           for (int ks = 0; ks < 8; ++ks)
-            mma_ts(tY2, k < 2 ? ps + 16 * ks + 8 * k : tP2 + 8 * ks,
-                   vd + ks * (2048 >> 4), idesc, (k < NT - 1 || ks > 0) ? 1u : 0u);
+            mma_ts(tY2, k < 2 ? tSC + 128 * (c & 1) + 16 * ks + 8 * k : tP2 + 8 * ks, vd + ks * (2048 >> 4), idesc,
+                   (k < NT - 1 || ks > 0) ? 1u : 0u);
         tc::mma_commit(bars + PV);
       }
       __syncwarp();
@@ -181,10 +220,10 @@ __global__ void __launch_bounds__(NTHR, 1)
         const uint64_t qd = tc::sdesc_sw128(at);
 #pragma unroll
         for (int i = L::NS - 1; i >= 0; --i) {   // the smallest terms first
-          const uint64_t sd = tc::sdesc_sw128(base + L::s + i * L::s_tile, 8192);
+          const uint64_t sd = tc::sdesc_sw128(base + L::s + i * L::s_tile);
 #pragma unroll
           for (int ks = 0; ks < 4; ++ks)
-            tc::mma_f16(tY1, qd + ks * (32 >> 4), sd + ks * (2048 >> 4), idesc, (i < L::NS - 1 || ks > 0) ? 1u : 0u);
+            tc::mma_f16(tY1, qd + ks * (32 >> 4), sd + ks * (32 >> 4), idesc_s, (i < L::NS - 1 || ks > 0) ? 1u : 0u);
         }
         tc::mma_commit(bars + Y);
       }
@@ -253,10 +292,9 @@ __global__ void __launch_bounds__(NTHR, 1)
     };
     for (int c = 0; c < chunks; ++c) {
       const uint32_t sc = tSC + 128 * (c & 1) + lanes;
-      if (!(ok = all_wait(SC + (c & 1), (c >> 1) & 1))) break;
+      // the scores; the third term's columns are the last chunk's until its P V is done
+      if (!(ok = all_wait(SC + (c & 1), (c >> 1) & 1) && (NT == 1 || c == 0 || all_wait(PV, (c - 1) & 1)))) break;
       tc::fence_after_sync();
-      // the third term's columns are the last chunk's until its P V is done
-      if (NT == 3 && c > 0 && !(ok = all_wait(PV, (c - 1) & 1))) break;
       // 16 columns a turn: with everything unrolled the kernel's code overran the
       // instruction caches (4.6 of 11 cycles per instruction were spent on that)
 #pragma unroll 1
@@ -296,8 +334,7 @@ __global__ void __launch_bounds__(NTHR, 1)
           uint32_t x[8];
 #pragma unroll
           for (int i = 0; i < 8; ++i) x[i] = w[i][k];
-          // terms 0 and 1 go over the scores just read: into the first and the
-          // second half of this turn's 16 columns
+          // terms 0 and 1 over the halves of the 16 columns just read
           tmem_st8u(k < 2 ? sc + 32 * blk + h0 + 8 * k : tP2 + lanes + 16 * blk + h0 / 2, x);
         }
       }
@@ -318,12 +355,13 @@ __global__ void __launch_bounds__(NTHR, 1)
         if (32 * side + lane < cols) y[t * g.y_t + lane] = layer::from_f32<TO>(0.f);
     }
   } else {
-    // state: rows 16 quarter + lane % 16, columns 16 (lane / 16) + 32 i
+    // state, transposed: column 16 quarter + lane % 16 of d_v, rows 16 (lane /
+    // 16) + 32 i of d_k
     const int row = 16 * quarter + lane % 16, col = 16 * (lane / 16);
     const uint32_t at = tDS + ((uint32_t)(32 * quarter) << 16);
     float st[32];
-    auto element = [&](int i) { return (size_t)row * g.d_v + c0 + col + 32 * (i / 16) + i % 16; };
-    auto inside = [&](int i) { return row < g.d_k && col + 32 * (i / 16) + i % 16 < cols; };
+    auto element = [&](int i) { return (size_t)(col + 32 * (i / 16) + i % 16) * g.d_v + c0 + row; };
+    auto inside = [&](int i) { return row < cols && col + 32 * (i / 16) + i % 16 < g.d_k; };
     {
       const bool add = g.nseg > 1 && inline_scan;   // start = S0 carried over the segments before this one
       const float* d = g.nseg > 1 && !add ? p.seg + ((size_t)unit * g.nseg + s) * sq : p.S0 ? p.S0 + unit * sq : nullptr;
@@ -358,15 +396,23 @@ __global__ void __launch_bounds__(NTHR, 1)
       if (!(ok = all_wait(DS, c & 1))) break;
       tc::fence_after_sync();
       {
-        float d[32];
-        tc::tmem_ld16_x2(at, d);
-        tc::tmem_ld16_x2(at + 32, d + 16);
-        tc::tmem_ld_wait32(d);
-        tc::fence_before_sync();
-        arrive(DSFREE);
         const float f = pw[tokens(c)];
 #pragma unroll
-        for (int i = 0; i < 32; ++i) st[i] = fmaf(f, st[i], d[i]);
+        for (int t = (NT == 1 ? 1 : 0); t >= 0; --t) {   // the product's blocks
+          float d[32];
+          tc::tmem_ld16_x2(at + 64 * t, d);
+          tc::tmem_ld16_x2(at + 64 * t + 32, d + 16);
+          tc::tmem_ld_wait32(d);
+          if (t == (NT == 1 ? 1 : 0)) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) st[i] = fmaf(f, st[i], d[i]);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) st[i] += d[i];
+          }
+        }
+        tc::fence_before_sync();
+        arrive(DSFREE);
       }
       if (c + 1 < chunks) {
         if (!(ok = all_wait(Y, c & 1))) break;   // Q S has read the last terms
@@ -414,7 +460,7 @@ __global__ void __launch_bounds__(NTHR_STATE, 1)
   const int s = blockIdx.x, sl = blockIdx.y, unit = blockIdx.z;
   const int b = unit / g.H, h = unit % g.H, hq = h / g.share;
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, quarter = warp & 3, group = (warp - 2) >> 2;
-  if (warp == 0) tc::tmem_alloc(tbase, 64);
+  if (warp == 0) tc::tmem_alloc(tbase, 256);
   if (tid == 32) {
     for (int i = 0; i < NSBARS; ++i) tc::mbar_init_only(bars + i, i == SK || i == SK + 1 ? 4 : 1);
     tc::mbar_init_fence();
@@ -452,7 +498,7 @@ __global__ void __launch_bounds__(NTHR_STATE, 1)
       tc::fence_after_sync();
       if (tc::elect()) {
         const uint32_t k0 = base + L::k0 + (c & 1) * 3 * TILE;
-        mma_state<1>(tm, k0, k0 + TILE, k0 + 2 * TILE, base + (c % STAGES) * L::stage + TILE, c > 0);
+        mma_state_t<3>(tm, k0, base + (c % STAGES) * L::stage + TILE, c > 0);
         tc::mma_commit(bars + SFREE + (c & 1));
         tc::mma_commit(bars + SEMPTY + c % STAGES);
       }
@@ -483,22 +529,27 @@ __global__ void __launch_bounds__(NTHR_STATE, 1)
       tc::fence_after_sync();
     }
     if (ok && group == (chunks > 0 ? (chunks - 1) & 1 : 0)) {
-      float d[32];
+      float sum[32];
+#pragma unroll
+      for (int i = 0; i < 32; ++i) sum[i] = 0.f;
       if (chunks > 0) {
         const uint32_t ta = tm + ((uint32_t)(32 * quarter) << 16);
-        tc::tmem_ld16_x2(ta, d);
-        tc::tmem_ld16_x2(ta + 32, d + 16);
-        tc::tmem_ld_wait32(d);
-      } else {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) d[i] = 0.f;
+        for (int t = 2; t >= 0; --t) {
+          float d[32];
+          tc::tmem_ld16_x2(ta + 64 * t, d);
+          tc::tmem_ld16_x2(ta + 64 * t + 32, d + 16);
+          tc::tmem_ld_wait32(d);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) sum[i] += d[i];
+        }
       }
-      const int row = 16 * quarter + lane % 16, col = 16 * (lane / 16);
-      float* dst = p.seg + ((size_t)unit * g.nseg + s + 1) * ((size_t)g.d_k * g.d_v) + (size_t)row * g.d_v + c0;
+      const int row = 16 * quarter + lane % 16, col = 16 * (lane / 16);   // column of d_v, rows of d_k
+      float* dst = p.seg + ((size_t)unit * g.nseg + s + 1) * ((size_t)g.d_k * g.d_v) + c0 + row;
 #pragma unroll
       for (int i = 0; i < 32; ++i) {
-        const int cc = col + 32 * (i / 16) + i % 16;
-        if (row < g.d_k && cc < cols) dst[cc] = d[i];
+        const int kk = col + 32 * (i / 16) + i % 16;
+        if (row < cols && kk < g.d_k) dst[(size_t)kk * g.d_v] = sum[i];
       }
     }
   }
@@ -510,7 +561,7 @@ __global__ void __launch_bounds__(NTHR_STATE, 1)
     atomicExch(status, ATLAS_ERR_TIMEOUT);
   }
   __syncthreads();
-  if (warp == 0) tc::tmem_dealloc(tm, 64);
+  if (warp == 0) tc::tmem_dealloc(tm, 256);
 }
 
 template <int NT, typename TO>

@@ -7,6 +7,7 @@
 
 #include "decay_common.cuh"
 #include "decay_tc.cuh"
+#include "tc2.cuh"
 
 using namespace layer;
 using decay::Geom;
@@ -101,7 +102,7 @@ __global__ void __launch_bounds__(256) k_decay_step(Geom g, Ptrs p) {
 // the read-outs from the segment-start state; else only the segment's own
 // contribution to the next segment's start.
 template <typename TI, typename TO, int C, bool READ>
-__global__ void __launch_bounds__(256) k_decay_chunk(Geom g, Ptrs p) {
+__global__ void __launch_bounds__(256, C == 64 ? 3 : 1) k_decay_chunk(Geom g, Ptrs p) {
   extern __shared__ float sm[];
   const int dk4 = (g.d_k + 3) & ~3, ldk = dk4 + 4;
   constexpr int LDV = kSlice + 4, LDP = C + 4, NI = C / 16;
@@ -113,6 +114,8 @@ __global__ void __launch_bounds__(256) k_decay_chunk(Geom g, Ptrs p) {
   float* Ps = Qs + C * ldk;         // [C][LDP]
   const int s = blockIdx.x, sl = blockIdx.y, unit = blockIdx.z;
   const int b = unit / g.H, h = unit % g.H, tid = threadIdx.x, tx = tid % 16, ty = tid / 16;
+  tc::grid_dependency_wait();
+  tc::grid_dependents_launch();
   const int live = decay::live_tokens(g, p, b);
   const int t_lo = s * g.seg, t_hi = min(g.T, t_lo + g.seg), t_live = min(t_hi, max(live, t_lo));
   const float l2g = log2f(p.decay[h]);
@@ -277,6 +280,8 @@ __global__ void __launch_bounds__(256) k_decay_scan(Geom g, Ptrs p) {
   const size_t sq = (size_t)g.d_k * g.d_v;
   const int unit = blockIdx.y;
   const size_t e = (size_t)blockIdx.x * 256 + threadIdx.x;
+  tc::grid_dependency_wait();
+  tc::grid_dependents_launch();
   if (e >= sq) return;
   const int live = decay::live_tokens(g, p, unit / g.H);
   const float l2g = log2f(p.decay[unit % g.H]);
@@ -284,11 +289,18 @@ __global__ void __launch_bounds__(256) k_decay_scan(Geom g, Ptrs p) {
   float run = p.S0 ? p.S0[unit * sq + e] : 0.f;
   slot[0] = run;
   const float full = decay::power(l2g, g.seg);
-#pragma unroll 4
-  for (int s = 0; s + 1 < g.nseg; ++s) {
-    const int n = min(g.seg, max(0, live - s * g.seg));
-    run = fmaf(n == g.seg ? full : decay::power(l2g, n), run, slot[(size_t)(s + 1) * sq]);
-    slot[(size_t)(s + 1) * sq] = run;
+  constexpr int A = 16;   // loads in flight
+  for (int s0 = 0; s0 + 1 < g.nseg; s0 += A) {
+    float v[A];
+#pragma unroll
+    for (int i = 0; i < A; ++i) v[i] = s0 + i + 1 < g.nseg ? slot[(size_t)(s0 + i + 1) * sq] : 0.f;
+#pragma unroll
+    for (int i = 0; i < A; ++i) {
+      const int s = s0 + i, n = min(g.seg, max(0, live - s * g.seg));
+      if (s + 1 >= g.nseg) break;
+      run = fmaf(n == g.seg ? full : decay::power(l2g, n), run, v[i]);
+      slot[(size_t)(s + 1) * sq] = run;
+    }
   }
 }
 
@@ -307,17 +319,17 @@ struct Plan {
 // chunks each.  One segment per triple reads every input once; n segments cost
 // another pass over k and v for the states at their starts (`extra` of a
 // chunk's time, measured 0.4) and another launch (about 3 chunks' time), and a
-// block's start and end take about 2 chunks' time, so n is the one with the
+// block's start and end take `ends` chunks' time, so n is the one with the
 // least of
 //   waves of the read-out pass + waves of the state pass + launches.
-int best_segments(long long ctas, long long chunks, long long slots) {
+int best_segments(long long ctas, long long chunks, long long slots, double ends) {
   long long best = 1;
   double cost = 0;
   for (long long n = 1; n <= std::min(chunks, 1024LL); ++n) {
     const long long per = (chunks + n - 1) / n;
     if (n > 1 && (chunks + per - 1) / per != n) continue;
     const long long waves = (ctas * n + slots - 1) / slots, before = (ctas * (n - 1) + slots - 1) / slots;
-    const double c = (double)waves * (per + 2) + (n > 1 ? 0.4 * before * (per + 2) + 3 : 0);
+    const double c = (double)waves * (per + ends) + (n > 1 ? 0.4 * before * (per + ends) + ends + 1 : 0);
     if (n == 1 || c < cost) best = n, cost = c;
     if (ctas * n > 4 * slots) break;
   }
@@ -338,10 +350,11 @@ Plan make_plan(const atlas_decay_config& c, int B, int T, bool tc) {
   tc = tc && c.qkv_dtype == ATLAS_BF16 && c.d_k % 8 == 0 && c.d_v % 8 == 0 && c.d_k <= 128;
   pl.path = tc ? 2 : 1;
   pl.C = tc ? decay::kTcChunk : chunk_tokens(c.d_k);
-  // CTAs that run at once: two per SM for the fp32 chunks where their shared memory allows it
-  const long long slots = (!tc && c.d_k <= 64 ? 2LL : 1LL) * sm_count();
+  // CTAs that run at once: three per SM for the fp32 chunks where their shared
+  // memory allows it, whose chunks take so long that starts hardly count
+  const long long slots = (tc || c.d_k > 128 ? 1 : c.d_k > 64 ? 2 : 3) * sm_count();
   const long long chunks = (T + pl.C - 1) / pl.C;
-  const long long n = best_segments((long long)B * c.H * pl.slices, chunks, slots);
+  const long long n = best_segments((long long)B * c.H * pl.slices, chunks, slots, tc ? 2 : 0.5);
   pl.seg = (int)((chunks + n - 1) / n * pl.C);
   pl.nseg = (int)((T + pl.seg - 1) / pl.seg);
   return pl;
@@ -419,15 +432,14 @@ template <typename K>
 cudaError_t launch_big(K kern, dim3 grid, size_t smem, const Geom& g, const Ptrs& p, cudaStream_t st) {
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  kern<<<grid, 256, smem, st>>>(g, p);
-  return cudaGetLastError();
+  return tc::launch_overlapped(kern, grid, dim3(256), smem, st, g, p);
 }
 
 }  // namespace
 
 cudaError_t decay::scan_launch(const Geom& g, const Ptrs& p, cudaStream_t st) {
-  k_decay_scan<<<dim3((unsigned)(((size_t)g.d_k * g.d_v + 255) / 256), (unsigned)(g.B * g.H)), 256, 0, st>>>(g, p);
-  return cudaGetLastError();
+  return tc::launch_overlapped(k_decay_scan, dim3((unsigned)(((size_t)g.d_k * g.d_v + 255) / 256), (unsigned)(g.B * g.H)),
+                               dim3(256), 0, st, g, p);
 }
 
 namespace {

@@ -76,8 +76,9 @@ int atlas_decay_create(const atlas_decay_config* cfg, atlas_decay_handle** out);
  * handle's workspace to atlas_decay_workspace_bytes on first use (cudaMalloc). */
 int atlas_decay_forward(atlas_decay_handle* h, const atlas_decay_io* io, void* stream);
 
-/* Device workspace a call of this size needs (states at the segment starts; 0
- * when the call is not split along the tokens). */
+/* Device workspace a call of this size may need: states at the segment starts
+ * of a call that is split along the tokens, and padded copies of q, k, v and y
+ * where bf16 head widths are no multiples of 8 or addresses none of 16. */
 size_t atlas_decay_workspace_bytes(const atlas_decay_handle* h, int B, int T);
 
 /* Wait for the last forward on h and return its device status: ATLAS_OK, or

@@ -304,6 +304,27 @@ __global__ void __launch_bounds__(256) k_decay_scan(Geom g, Ptrs p) {
   }
 }
 
+// rows of `from` values -> rows of `to` values, zero where there are more
+template <typename T>
+__global__ void __launch_bounds__(256) k_decay_rows(const T* __restrict__ src, T* __restrict__ dst, size_t rows, int from,
+                                                    int to) {
+  tc::grid_dependency_wait();
+  tc::grid_dependents_launch();
+  // eight values a thread; `to` or `from` is a multiple of 8, the padded side
+  const int per = (max(from, to) + 7) / 8;
+  const size_t i = (size_t)blockIdx.x * 256 + threadIdx.x, r = i / per;
+  if (r >= rows) return;
+  const int c0 = (int)(i % per) * 8;
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    if (c0 + e < to) dst[r * to + c0 + e] = c0 + e < from ? src[r * from + c0 + e] : from_f32<T>(0.f);
+}
+template <typename T>
+cudaError_t launch_rows(const void* src, void* dst, size_t rows, int from, int to, cudaStream_t st) {
+  const unsigned grid = (unsigned)((rows * ((std::max(from, to) + 7) / 8) + 255) / 256);
+  return tc::launch_overlapped(k_decay_rows<T>, dim3(grid), dim3(256), 0, st, (const T*)src, (T*)dst, rows, from, to);
+}
+
 size_t step_smem(const Geom& g, int V) { return (size_t)(2 * g.d_k + 256 / (kSlice / V) * kSlice) * sizeof(float); }
 int chunk_tokens(int d_k) { return d_k <= 128 ? 64 : 32; }
 size_t chunk_smem(int d_k, bool read) {
@@ -313,7 +334,11 @@ size_t chunk_smem(int d_k, bool read) {
 
 struct Plan {
   int path, C, slices, nseg, seg;
+  bool pad;
+  size_t seg_bytes, q_bytes, v_bytes, y_bytes;   // workspace: segment starts, then padded q, k, v, y
+  size_t bytes() const { return seg_bytes + 2 * q_bytes + v_bytes + y_bytes; }
 };
+size_t round_256(size_t n) { return (n + 255) / 256 * 256; }
 
 // Segments of the tokens for `ctas` (row, head, slice) triples of `chunks`
 // chunks each.  One segment per triple reads every input once; n segments cost
@@ -336,9 +361,11 @@ int best_segments(long long ctas, long long chunks, long long slots, double ends
   return (int)best;
 }
 
-// `tc`: the tensors' addresses allow the tensor-core chunks
-Plan make_plan(const atlas_decay_config& c, int B, int T, bool tc) {
-  Plan pl;
+// bf16 calls with d_k <= 128 take the tensor-core chunks.  Their copies want rows
+// of whole 16-byte groups: other widths (or addresses) go through padded copies
+// of q, k, v and y in the workspace.  `aligned`: the addresses do not ask for it.
+Plan make_plan(const atlas_decay_config& c, int B, int T, bool aligned) {
+  Plan pl{};
   pl.slices = (c.d_v + kSlice - 1) / kSlice;
   pl.nseg = 1;
   pl.seg = T;
@@ -347,7 +374,8 @@ Plan make_plan(const atlas_decay_config& c, int B, int T, bool tc) {
     pl.C = 1;
     return pl;
   }
-  tc = tc && c.qkv_dtype == ATLAS_BF16 && c.d_k % 8 == 0 && c.d_v % 8 == 0 && c.d_k <= 128;
+  const bool tc = c.qkv_dtype == ATLAS_BF16 && c.d_k <= 128;
+  pl.pad = tc && (!aligned || c.d_k % 8 || c.d_v % 8);
   pl.path = tc ? 2 : 1;
   pl.C = tc ? decay::kTcChunk : chunk_tokens(c.d_k);
   // CTAs that run at once: three per SM for the fp32 chunks where their shared
@@ -357,6 +385,13 @@ Plan make_plan(const atlas_decay_config& c, int B, int T, bool tc) {
   const long long n = best_segments((long long)B * c.H * pl.slices, chunks, slots, tc ? 2 : 0.5);
   pl.seg = (int)((chunks + n - 1) / n * pl.C);
   pl.nseg = (int)((T + pl.seg - 1) / pl.seg);
+  if (pl.nseg > 1) pl.seg_bytes = round_256((size_t)B * c.H * pl.nseg * c.d_k * c.d_v * sizeof(float));
+  if (pl.pad) {
+    const size_t rows = (size_t)B * T;
+    pl.q_bytes = round_256(rows * (c.H / c.share) * ((c.d_k + 7) / 8 * 8) * 2);
+    pl.v_bytes = round_256(rows * c.H * ((c.d_v + 7) / 8 * 8) * 2);
+    pl.y_bytes = round_256(rows * c.H * ((c.d_v + 7) / 8 * 8) * dtype_size(c.y_dtype));
+  }
   return pl;
 }
 
@@ -400,10 +435,8 @@ extern "C" int atlas_decay_create(const atlas_decay_config* cfg, atlas_decay_han
 
 extern "C" size_t atlas_decay_workspace_bytes(const atlas_decay_handle* h, int B, int T) {
   if (!h || B < 1 || T < 1) return 0;
-  // the larger of the two paths': which one runs depends on the tensors' addresses
-  int nseg = 1;
-  for (bool tc : {false, true}) nseg = std::max(nseg, make_plan(h->cfg, B, T, tc).nseg);
-  return nseg > 1 ? (size_t)B * h->cfg.H * nseg * h->cfg.d_k * h->cfg.d_v * sizeof(float) : 0;
+  // the most it can be: tensors at addresses that ask for padded copies
+  return make_plan(h->cfg, B, T, false).bytes();
 }
 
 namespace {
@@ -482,26 +515,41 @@ extern "C" int atlas_decay_forward(atlas_decay_handle* h, const atlas_decay_io* 
   const Plan pl = make_plan(c, io->B, io->T,
                             aligned16(io->q) && aligned16(io->k) && aligned16(io->v) && aligned16(io->y));
   int rc = pl.path == 2 ? h->need_status(st) : ATLAS_OK;
-  if (!rc) rc = h->grow(atlas_decay_workspace_bytes(h, io->B, io->T));
+  if (!rc) rc = h->grow(pl.bytes());
   if (rc) return rc;
 
   Geom g;
   g.B = io->B, g.T = io->T, g.H = c.H, g.share = c.share, g.d_k = c.d_k, g.d_v = c.d_v, g.scale = c.scale;
   g.slices = pl.slices, g.nseg = pl.nseg, g.seg = pl.seg;
-  const size_t T = io->T, Hq = c.H / c.share;
+  const size_t T = io->T, Hq = c.H / c.share, rows = (size_t)io->B * T;
+  g.dk_row = pl.pad ? (c.d_k + 7) / 8 * 8 : c.d_k;
+  g.dv_row = pl.pad ? (c.d_v + 7) / 8 * 8 : c.d_v;
   auto strides = [&](int layout, size_t heads, size_t d, size_t& sb, size_t& sh, size_t& stk) {
     sb = T * heads * d;
     sh = layout == ATLAS_LAYOUT_HEADS ? T * d : d;
     stk = layout == ATLAS_LAYOUT_HEADS ? d : heads * d;
   };
-  strides(c.qkv_layout, Hq, c.d_k, g.qk_b, g.qk_h, g.qk_t);
-  strides(c.qkv_layout, c.H, c.d_v, g.v_b, g.v_h, g.v_t);
-  strides(c.y_layout, c.H, c.d_v, g.y_b, g.y_h, g.y_t);
-  const Ptrs p{io->q, io->k, io->v, io->decay, io->lens, io->S0, io->y, io->S_out, (float*)h->ws};
+  strides(c.qkv_layout, Hq, g.dk_row, g.qk_b, g.qk_h, g.qk_t);
+  strides(c.qkv_layout, c.H, g.dv_row, g.v_b, g.v_h, g.v_t);
+  strides(c.y_layout, c.H, g.dv_row, g.y_b, g.y_h, g.y_t);
+  Ptrs p{io->q, io->k, io->v, io->decay, io->lens, io->S0, io->y, io->S_out, (float*)h->ws};
+  if (pl.pad) {
+    char* at = (char*)h->ws + pl.seg_bytes;
+    void *q = at, *k = at + pl.q_bytes, *v = at + 2 * pl.q_bytes;
+    p.y = at + 2 * pl.q_bytes + pl.v_bytes;
+    cudaError_t e = launch_rows<bf16>(io->q, q, rows * Hq, c.d_k, g.dk_row, st);
+    if (e == cudaSuccess) e = launch_rows<bf16>(io->k, k, rows * Hq, c.d_k, g.dk_row, st);
+    if (e == cudaSuccess) e = launch_rows<bf16>(io->v, v, rows * c.H, c.d_v, g.dv_row, st);
+    if (e != cudaSuccess) return h->cuda_fail("decay attention launch", e);
+    p.q = q, p.k = k, p.v = v;
+  }
   const bool ib = c.qkv_dtype == ATLAS_BF16, ob = c.y_dtype == ATLAS_BF16;
-  const cudaError_t e = pl.path == 2 ? decay::tc_launch(g, p, ob, h->status, st)
+  cudaError_t e = pl.path == 2 ? decay::tc_launch(g, p, ob, h->status, st)
                         : ib ? (ob ? launch<bf16, bf16>(pl, g, p, st) : launch<bf16, float>(pl, g, p, st))
                            : (ob ? launch<float, bf16>(pl, g, p, st) : launch<float, float>(pl, g, p, st));
+  if (e == cudaSuccess && pl.pad)
+    e = ob ? launch_rows<bf16>(p.y, io->y, rows * c.H, g.dv_row, c.d_v, st)
+           : launch_rows<float>(p.y, io->y, rows * c.H, g.dv_row, c.d_v, st);
   if (e != cudaSuccess) return h->cuda_fail("decay attention launch", e);
   h->path = pl.path;
   h->last_stream = st;

@@ -48,18 +48,22 @@ __device__ __forceinline__ float inv_std(float var, float eps) { return rsqrtf(v
 // A set is Cg neighbouring values (S = 1, or the heads layout): LPG lanes of
 // a warp hold it in registers, I items of V values each; mean, then the
 // centred sum of squares, by shuffles.  A block takes U x 256 / LPG sets in the
-// order of x, all their loads in flight before the first sum.  heads: the sets
-// of one (sample, head) per blockIdx.y, so the lane's weights are loaded once.
-template <typename TI, typename TO, int V, int LPG, int I, int U, bool HEADS>
-__global__ void __launch_bounds__(256) k_norm_run(Geom g, unsigned sets, const TI* __restrict__ x,
+// order of x, all their loads in flight before the first sum.  Heads layout: a
+// block's sets are of one (sample, head), so the lane's weights are loaded once
+// (HEADS), or, where a head has too few positions to fill a block, of any
+// (SHORT_HEADS).
+enum Sets { CHANNELS, HEADS, SHORT_HEADS };
+template <typename TI, typename TO, int V, int LPG, int I, int U, Sets KIND>
+__global__ void __launch_bounds__(256) k_norm_run(Geom g, unsigned sets, unsigned blocks, const TI* __restrict__ x,
                                                   const float* __restrict__ weight, const float* __restrict__ bias,
                                                   TO* __restrict__ y) {
   constexpr int PER = 256 / LPG;
   const int l = threadIdx.x % LPG;
-  const unsigned s0 = blockIdx.x * (U * PER) + threadIdx.x / LPG;
-  const unsigned grp0 = HEADS ? blockIdx.y % g.G : 0, n = HEADS ? blockIdx.y / g.G : 0;
-  const TI* src = x + (HEADS ? (size_t)blockIdx.y * g.S * g.Cg : 0);
-  TO* dst = y + (HEADS ? (size_t)n * g.S * g.C + (size_t)grp0 * g.Cg : 0);
+  // heads: `blocks` blocks per (sample, head)
+  const unsigned ng = KIND == HEADS ? blockIdx.x / blocks : 0, blk = KIND == HEADS ? blockIdx.x % blocks : blockIdx.x;
+  const unsigned s0 = blk * (U * PER) + threadIdx.x / LPG, grp0 = ng % g.G;
+  const TI* src = x + (size_t)ng * g.S * g.Cg;
+  TO* dst = y + (size_t)(ng / g.G) * g.S * g.C + (size_t)grp0 * g.Cg;
   tc::grid_dependency_wait();
   tc::grid_dependents_launch();
   float v[U][I][V];
@@ -84,7 +88,7 @@ __global__ void __launch_bounds__(256) k_norm_run(Geom g, unsigned sets, const T
       if (c < g.Cg) load_affine<V>(weight, bias, grp * g.Cg + c, w[i], b[i]);
     }
   };
-  if constexpr (HEADS) affine(grp0);
+  if constexpr (KIND == HEADS) affine(grp0);
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     const unsigned set = s0 + u * PER;
@@ -106,9 +110,14 @@ __global__ void __launch_bounds__(256) k_norm_run(Geom g, unsigned sets, const T
     for (int o = LPG / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     if (set >= sets) continue;
     const float r = inv_std(s * g.inv_cg, g.eps);
-    if constexpr (!HEADS) affine(set % (unsigned)g.G);
     // heads: (n, head, position) -> (n, position, head)
-    TO* row = dst + (HEADS ? (size_t)set * g.C : (size_t)set * g.Cg);
+    TO* row = dst + (KIND == HEADS ? (size_t)set * g.C : (size_t)set * g.Cg);
+    if constexpr (KIND == CHANNELS) affine(set % (unsigned)g.G);
+    if constexpr (KIND == SHORT_HEADS) {
+      const unsigned h = set / (unsigned)g.S, pos = set % (unsigned)g.S, grp = h % (unsigned)g.G;
+      affine(grp);
+      row = y + ((size_t)(h / (unsigned)g.G) * g.S + pos) * g.C + (size_t)grp * g.Cg;
+    }
 #pragma unroll
     for (int i = 0; i < I; ++i) {
       const int c = (l + i * LPG) * V;
@@ -468,21 +477,22 @@ extern "C" size_t atlas_norm_workspace_bytes(const atlas_norm_handle* h, int N, 
 
 namespace {
 
-template <typename TI, typename TO, int V, bool HEADS>
+template <typename TI, typename TO, int V, Sets KIND>
 cudaError_t launch_run(const Geom& g, const atlas_norm_io& io, cudaStream_t st) {
-  const unsigned sets = HEADS ? g.S : (unsigned)((size_t)g.N * g.S * g.G);
+  const unsigned sets = KIND == HEADS ? g.S : (unsigned)((size_t)g.N * g.S * g.G);
   const int items = (g.Cg + V - 1) / V;   // values of V per set
   auto go = [&](auto kern, int per) {
-    const dim3 grid((sets + per - 1) / per, HEADS ? g.N * g.G : 1);
-    return tc::launch_overlapped(kern, grid, dim3(256), 0, st, g, sets, (const TI*)io.x, io.weight, io.bias, (TO*)io.y);
+    const unsigned blocks = (sets + per - 1) / per;
+    const dim3 grid(KIND == HEADS ? blocks * (unsigned)(g.N * g.G) : blocks);
+    return tc::launch_overlapped(kern, grid, dim3(256), 0, st, g, sets, blocks, (const TI*)io.x, io.weight, io.bias, (TO*)io.y);
   };
-  if (items <= 2) return go(k_norm_run<TI, TO, V, 2, 1, 4, HEADS>, 512);
-  if (items <= 4) return go(k_norm_run<TI, TO, V, 4, 1, 4, HEADS>, 256);
-  if (items <= 8) return go(k_norm_run<TI, TO, V, 8, 1, 4, HEADS>, 128);
-  if (items <= 16) return go(k_norm_run<TI, TO, V, 16, 1, 4, HEADS>, 64);
-  if (items <= 32) return go(k_norm_run<TI, TO, V, 32, 1, 4, HEADS>, 32);
-  if (items <= 128) return go(k_norm_run<TI, TO, V, 32, 4, 1, HEADS>, 8);
-  return go(k_norm_run<TI, TO, V, 32, 32, 1, HEADS>, 8);
+  if (items <= 2) return go(k_norm_run<TI, TO, V, 2, 1, 4, KIND>, 512);
+  if (items <= 4) return go(k_norm_run<TI, TO, V, 4, 1, 4, KIND>, 256);
+  if (items <= 8) return go(k_norm_run<TI, TO, V, 8, 1, 4, KIND>, 128);
+  if (items <= 16) return go(k_norm_run<TI, TO, V, 16, 1, 4, KIND>, 64);
+  if (items <= 32) return go(k_norm_run<TI, TO, V, 32, 1, 4, KIND>, 32);
+  if (items <= 128) return go(k_norm_run<TI, TO, V, 32, 4, 1, KIND>, 8);
+  return go(k_norm_run<TI, TO, V, 32, 32, 1, KIND>, 8);
 }
 
 template <typename TI, typename TO, int V>
@@ -502,8 +512,12 @@ cudaError_t launch_positions(const Plan& pl, const Geom& g, const atlas_norm_io&
 template <typename TI, typename TO>
 cudaError_t launch(const Plan& pl, const Geom& g, bool heads, const atlas_norm_io& io, float* part, cudaStream_t st) {
   if (pl.kind == 0) {
-    if (heads) return pl.V == 8 ? launch_run<TI, TO, 8, true>(g, io, st) : launch_run<TI, TO, 1, true>(g, io, st);
-    return pl.V == 8 ? launch_run<TI, TO, 8, false>(g, io, st) : launch_run<TI, TO, 1, false>(g, io, st);
+    // (a block holds at most 512 sets, most often 128)
+    if (heads && g.S >= 128)
+      return pl.V == 8 ? launch_run<TI, TO, 8, HEADS>(g, io, st) : launch_run<TI, TO, 1, HEADS>(g, io, st);
+    if (heads)
+      return pl.V == 8 ? launch_run<TI, TO, 8, SHORT_HEADS>(g, io, st) : launch_run<TI, TO, 1, SHORT_HEADS>(g, io, st);
+    return pl.V == 8 ? launch_run<TI, TO, 8, CHANNELS>(g, io, st) : launch_run<TI, TO, 1, CHANNELS>(g, io, st);
   }
   return pl.V == 8 ? launch_positions<TI, TO, 8>(pl, g, io, part, st)
                    : launch_positions<TI, TO, 1>(pl, g, io, part, st);
@@ -523,8 +537,6 @@ extern "C" int atlas_norm_forward(atlas_norm_handle* h, const atlas_norm_io* io,
   const bool heads = c.layout == ATLAS_NORM_HEADS;
   if ((long long)io->N * io->S * c.groups > 0x40000000LL)
     return h->fail(ATLAS_ERR_UNSUPPORTED, "N * S * groups > 2^30 is not supported");
-  if (heads && (long long)io->N * c.groups > 65535)
-    return h->fail(ATLAS_ERR_UNSUPPORTED, "N * groups > 65535 is not supported in the heads layout");
   if (pl.kind && pl.tiles > 65535) return h->fail(ATLAS_ERR_UNSUPPORTED, "too many groups for statistics over positions");
   cudaStream_t st = (cudaStream_t)stream;
   const int rc = h->grow(pl.kind == 2 ? atlas_norm_workspace_bytes(h, io->N, io->S) : 0);

@@ -15,6 +15,7 @@ struct Geom {
   int B, T, H, share, d_k, d_v;
   float scale;
   int slices;        // column slices of d_v, one CTA each
+  int dk_row, dv_row;   // widths of the rows of q, k and of v, y as the kernels see them (padded copies: multiples of 8)
   int nseg, seg;     // segments of the tokens, tokens per segment (a multiple of the chunk)
   // element strides of (row b, head, token) of q/k, of v and of y
   size_t qk_b, qk_h, qk_t, v_b, v_h, v_t, y_b, y_h, y_t;

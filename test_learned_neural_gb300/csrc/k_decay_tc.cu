@@ -526,10 +526,10 @@ cudaError_t tc_launch(const Geom& g, const Ptrs& p, bool y_bf16, int* status, cu
   if (g.d_k <= 64) return ws_launch(g, p, y_bf16, status, st);
   CUtensorMap mq, mk, mv, my;
   const int hq = g.H / g.share;
-  if (!map_4d(&mq, p.q, true, g.d_k, g.T, hq, g.B, g.qk_t, g.qk_h, g.qk_b) ||
-      !map_4d(&mk, p.k, true, g.d_k, g.T, hq, g.B, g.qk_t, g.qk_h, g.qk_b) ||
-      !map_4d(&mv, p.v, true, g.d_v, g.T, g.H, g.B, g.v_t, g.v_h, g.v_b) ||
-      !map_4d(&my, p.y, y_bf16, g.d_v, g.T, g.H, g.B, g.y_t, g.y_h, g.y_b))
+  if (!map_4d(&mq, p.q, true, g.dk_row, g.T, hq, g.B, g.qk_t, g.qk_h, g.qk_b) ||
+      !map_4d(&mk, p.k, true, g.dk_row, g.T, hq, g.B, g.qk_t, g.qk_h, g.qk_b) ||
+      !map_4d(&mv, p.v, true, g.dv_row, g.T, g.H, g.B, g.v_t, g.v_h, g.v_b) ||
+      !map_4d(&my, p.y, y_bf16, g.dv_row, g.T, g.H, g.B, g.y_t, g.y_h, g.y_b))
     return cudaErrorInvalidValue;
   if (g.nseg > 1) {
     cudaError_t e = g.d_k <= 64 ? launch_state<1>(mk, mv, g, p, status, st) : launch_state<2>(mk, mv, g, p, status, st);

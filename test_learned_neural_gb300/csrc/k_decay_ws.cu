@@ -581,10 +581,10 @@ namespace decay {
 cudaError_t ws_launch(const Geom& g, const Ptrs& p, bool y_bf16, int* status, cudaStream_t st) {
   CUtensorMap mq, mk, mv, my;
   const int hq = g.H / g.share;
-  if (!map_4d(&mq, p.q, true, g.d_k, g.T, hq, g.B, g.qk_t, g.qk_h, g.qk_b) ||
-      !map_4d(&mk, p.k, true, g.d_k, g.T, hq, g.B, g.qk_t, g.qk_h, g.qk_b) ||
-      !map_4d(&mv, p.v, true, g.d_v, g.T, g.H, g.B, g.v_t, g.v_h, g.v_b) ||
-      !map_4d(&my, p.y, y_bf16, g.d_v, g.T, g.H, g.B, g.y_t, g.y_h, g.y_b))
+  if (!map_4d(&mq, p.q, true, g.dk_row, g.T, hq, g.B, g.qk_t, g.qk_h, g.qk_b) ||
+      !map_4d(&mk, p.k, true, g.dk_row, g.T, hq, g.B, g.qk_t, g.qk_h, g.qk_b) ||
+      !map_4d(&mv, p.v, true, g.dv_row, g.T, g.H, g.B, g.v_t, g.v_h, g.v_b) ||
+      !map_4d(&my, p.y, y_bf16, g.dv_row, g.T, g.H, g.B, g.y_t, g.y_h, g.y_b))
     return cudaErrorInvalidValue;
   int inline_scan = 1;
   if (g.nseg > 1) {

@@ -216,7 +216,7 @@ def test_norm_parity(gpu_lib, case, act, x_dtype, y_dtype):
     _norm_check(x, C, G, act, x_dtype, y_dtype, "channels_last", affine=C % 3 != 0)
 
 
-@pytest.mark.parametrize("case", [(1, 1, 64, 8), (2, 100, 512, 8), (3, 77, 96, 2), (2, 5, 35, 5), (1, 9, 1500, 2)], ids=str)
+@pytest.mark.parametrize("case", [(1, 1, 64, 8), (2, 100, 512, 8), (3, 77, 96, 2), (2, 5, 35, 5), (1, 9, 1500, 2), (9000, 2, 64, 8)], ids=str)
 @pytest.mark.parametrize("x_dtype,y_dtype", [("f32", "bf16"), ("bf16", "bf16"), ("f32", "f32")])
 def test_norm_heads(gpu_lib, case, x_dtype, y_dtype):
     import torch

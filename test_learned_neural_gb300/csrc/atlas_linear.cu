@@ -150,25 +150,40 @@ cudaError_t launch_rows(const atlas_linear_config& c, const atlas_linear_io& io,
 // bf16 values; three for fp32 ones, the leading 8 bits, the next 8 and the
 // last 8, each cut off (not rounded), so that their sum is the value itself.
 // Infinities and NaN stay in the first plane.
+struct PlaneJob {
+  const void* src;
+  uint16_t* dst;   // NULL: nothing to do
+  int R, C, Rp, ld;
+  unsigned blocks;
+};
+
 template <typename TI, int PLANES>
-__global__ void __launch_bounds__(256) k_planes(const TI* __restrict__ src, int R, int C, int Rp, int ld,
-                                                uint16_t* __restrict__ dst) {
-  const int per = ld / 8;
-  const size_t i = (size_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= (size_t)Rp * per) return;
+__device__ __forceinline__ void planes_of(const PlaneJob& j, unsigned block) {
+  const TI* src = (const TI*)j.src;
+  const int per = j.ld / 8;
+  const size_t i = (size_t)block * 256 + threadIdx.x;
+  if (i >= (size_t)j.Rp * per) return;
   const int r = (int)(i / per), c0 = (int)(i % per) * 8;
+  float f[8];
+  uint32_t raw[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const bool in = r < j.R && c0 + e < j.C;
+    if constexpr (PLANES == 1)
+      raw[e] = in ? (uint32_t) reinterpret_cast<const uint16_t*>(src)[(size_t)r * j.C + c0 + e] : 0u;
+    else
+      f[e] = in ? to_f32(src[(size_t)r * j.C + c0 + e]) : 0.f;
+  }
   uint32_t w[PLANES][4];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
+  for (int q = 0; q < 4; ++q) {
     uint32_t half[PLANES][2];
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      const int c = c0 + 2 * j + e;
-      const bool in = r < R && c < C;
       if constexpr (PLANES == 1) {
-        half[0][e] = in ? (uint32_t) reinterpret_cast<const uint16_t*>(src)[(size_t)r * C + c] : 0u;
+        half[0][e] = raw[2 * q + e];
       } else {
-        float v = in ? to_f32(src[(size_t)r * C + c]) : 0.f;
+        float v = f[2 * q + e];
         if (fabsf(v) <= 3.402823466e38f) {
 #pragma unroll
           for (int k = 0; k < PLANES; ++k) {
@@ -184,11 +199,22 @@ __global__ void __launch_bounds__(256) k_planes(const TI* __restrict__ src, int 
       }
     }
 #pragma unroll
-    for (int k = 0; k < PLANES; ++k) w[k][j] = half[k][0] | (half[k][1] << 16);
+    for (int k = 0; k < PLANES; ++k) w[k][q] = half[k][0] | (half[k][1] << 16);
   }
 #pragma unroll
   for (int k = 0; k < PLANES; ++k)
-    *reinterpret_cast<uint4*>(dst + ((size_t)k * Rp + r) * ld + c0) = make_uint4(w[k][0], w[k][1], w[k][2], w[k][3]);
+    *reinterpret_cast<uint4*>(j.dst + ((size_t)k * j.Rp + r) * j.ld + c0) = make_uint4(w[k][0], w[k][1], w[k][2], w[k][3]);
+}
+
+// x's and W's planes in one launch
+template <typename TI, int PLANES>
+__global__ void __launch_bounds__(256) k_planes(PlaneJob x, PlaneJob w) {
+  tc::grid_dependency_wait();
+  tc::grid_dependents_launch();
+  if (blockIdx.x < x.blocks)
+    planes_of<TI, PLANES>(x, blockIdx.x);
+  else
+    planes_of<TI, PLANES>(w, blockIdx.x - x.blocks);
 }
 
 // Where the tensor-core kernels read their operands: the caller's, or planes
@@ -213,13 +239,8 @@ Operands make_operands(const atlas_linear_config& c, int M, bool x_ok, bool w_ok
   return o;
 }
 
-cudaError_t planes_launch(bool f32, const void* src, int R, int C, int Rp, int ld, void* dst, cudaStream_t st) {
-  const unsigned grid = (unsigned)(((size_t)Rp * (ld / 8) + 255) / 256);
-  if (f32)
-    k_planes<float, 3><<<grid, 256, 0, st>>>((const float*)src, R, C, Rp, ld, (uint16_t*)dst);
-  else
-    k_planes<bf16, 1><<<grid, 256, 0, st>>>((const bf16*)src, R, C, Rp, ld, (uint16_t*)dst);
-  return cudaGetLastError();
+PlaneJob plane_job(const void* src, void* dst, int R, int C, int Rp, int ld) {
+  return PlaneJob{src, (uint16_t*)dst, R, C, Rp, ld, dst ? (unsigned)(((size_t)Rp * (ld / 8) + 255) / 256) : 0u};
 }
 
 // Calls of more rows than this go to the tensor cores.  bf16, W 2048 x 8192
@@ -283,8 +304,11 @@ extern "C" int atlas_linear_forward(atlas_linear_handle* h, const atlas_linear_i
     if (rc) return rc;
     char* ws = (char*)h->ws;
     cudaError_t e = cudaSuccess;
-    if (o.copy_x) e = planes_launch(!ib, io->x, io->M, c.K, io->M, o.ldx, ws, st);
-    if (e == cudaSuccess && o.copy_w) e = planes_launch(!ib, io->W, c.K, c.N, o.K, o.ldw, ws + o.x_bytes, st);
+    const PlaneJob jx = plane_job(io->x, o.copy_x ? ws : nullptr, io->M, c.K, io->M, o.ldx),
+                   jw = plane_job(io->W, o.copy_w ? ws + o.x_bytes : nullptr, c.K, c.N, o.K, o.ldw);
+    if (jx.blocks + jw.blocks)
+      e = tc::launch_overlapped(ib ? k_planes<bf16, 1> : k_planes<float, 3>, dim3(jx.blocks + jw.blocks), dim3(256), 0, st,
+                                jx, jw);
     linear::TcCall t;
     t.M = io->M, t.N = c.N, t.K = o.K, t.planes = o.planes, t.ldx = o.ldx, t.ldw = o.ldw;
     t.x = o.copy_x ? ws : io->x;

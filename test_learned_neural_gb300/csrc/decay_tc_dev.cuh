@@ -119,20 +119,4 @@ __device__ __forceinline__ uint64_t widen(uint32_t x) {
   return pair(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u));
 }
 
-// (w K)^T V into TMEM at d: three terms of KB 64-wide key tiles, one
-// instruction per 16 tokens; terms at t0, t1, t2 (tiles of a term KB * TILE
-// bytes), M = 64 KB
-template <int KB>
-__device__ __forceinline__ void mma_state(uint32_t d, uint32_t t0, uint32_t t1, uint32_t t2, uint32_t vtile,
-                                          bool accumulate) {
-  const uint32_t idesc = tc::idesc_f16(64 * KB, SL, 1, 1, 1);
-  const uint64_t vd = tc::sdesc_sw128(vtile, TILE);
-  const uint64_t kd[3] = {tc::sdesc_sw128(t0, TILE), tc::sdesc_sw128(t1, TILE), tc::sdesc_sw128(t2, TILE)};
-#pragma unroll
-  for (int i = 2; i >= 0; --i)
-#pragma unroll
-    for (int s = 0; s < C / 16; ++s)
-      tc::mma_f16(d, kd[i] + s * (2048 >> 4), vd + s * (2048 >> 4), idesc, (accumulate || i < 2 || s > 0) ? 1u : 0u);
-}
-
 }  // namespace decay

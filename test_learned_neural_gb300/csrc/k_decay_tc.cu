@@ -1,6 +1,7 @@
-// Decay attention on the tensor cores: bf16 q, k, v, head widths up to 128
-// (d_k) and any d_v in slices of 64 columns, chunks of 128 tokens
-// (decay_common.cuh has the formulas).
+// Decay attention on the tensor cores for 64 < d_k <= 128: bf16 q, k, v, any
+// d_v in slices of 64 columns, chunks of 128 tokens (decay_common.cuh has the
+// formulas).  Two 64-wide tiles of q and k and their three terms leave no room
+// for k_decay_ws.cu's ring, so every warp does each stage in turn.
 //
 // k_decay_tc, one CTA per (segment, slice, unit), chunks in order.  Per chunk:
 //   scores  Q K^T                      M = 128 tokens, N = 128
@@ -13,9 +14,8 @@
 // S to two terms (2^-16), each below the read-out's own rounding.  NT = 3 for
 // fp32 read-outs: three terms of both.
 //
-// TMEM (256 columns, so that two CTAs share an SM where d_k <= 64): scores,
-// then P in place, then the state's product, in 128 columns; inter and intra
-// read-outs 64 columns each.
+// TMEM (256 columns): scores, then P in place, then the state's product, in 128
+// columns; inter and intra read-outs 64 columns each.
 //
 // k_decay_tc_state: a segment's own contribution to the state at its end, the
 // same product with weights counted to the segment's end, accumulated in TMEM
@@ -28,6 +28,7 @@ using layer::bf16;
 namespace {
 
 constexpr int NTHR = 256;
+constexpr int KB = 2;   // 64-wide tiles of d_k
 
 // Rows n .. 127 of a tile become zero (a row's tokens past its length: 0 * NaN
 // must not reach the sums).
@@ -60,31 +61,33 @@ __device__ __forceinline__ void store_keys(uint32_t tile, int tid, const uint32_
   for (int j = 0; j < 4; ++j) sts128(tile + swz(r, j0 + j), k0[4 * j], k0[4 * j + 1], k0[4 * j + 2], k0[4 * j + 3]);
 }
 
-// The state's product as the threads hold it: KB = 1: M = 64, row 16 q + lane
-// % 16, 16 columns from 32 h + 16 (lane / 16); KB = 2: row 32 q + lane, 32
-// columns from 32 h (warp = q + 4 h).
-template <int KB>
+// (w K)^T V into TMEM at d, M = 128: three terms of two 64-wide key tiles, one
+// instruction per 16 tokens, the smallest term first; terms at t0, t1, t2
+__device__ __forceinline__ void mma_state(uint32_t d, uint32_t t0, uint32_t t1, uint32_t t2, uint32_t vtile,
+                                          bool accumulate) {
+  const uint32_t idesc = tc::idesc_f16(128, SL, 1, 1, 1);
+  const uint64_t vd = tc::sdesc_sw128(vtile, TILE);
+  const uint64_t kd[3] = {tc::sdesc_sw128(t0, TILE), tc::sdesc_sw128(t1, TILE), tc::sdesc_sw128(t2, TILE)};
+#pragma unroll
+  for (int i = 2; i >= 0; --i)
+#pragma unroll
+    for (int s = 0; s < C / 16; ++s)
+      tc::mma_f16(d, kd[i] + s * (2048 >> 4), vd + s * (2048 >> 4), idesc, (accumulate || i < 2 || s > 0) ? 1u : 0u);
+}
+
+// The state's product as the threads hold it (warp = q + 4 h): row 32 q + lane
+// of d_k, 32 columns from 32 h.
 struct StatePart {
-  static constexpr int N = 16 * KB;
+  static constexpr int N = 32;
   int row, col;
-  __device__ StatePart(int warp, int lane) {
-    const int q = warp & 3, h = warp >> 2;
-    row = KB == 1 ? 16 * q + lane % 16 : 32 * q + lane;
-    col = KB == 1 ? 32 * h + 16 * (lane / 16) : 32 * h;
-  }
+  __device__ StatePart(int warp, int lane) : row(32 * (warp & 3) + lane), col(32 * (warp >> 2)) {}
   __device__ __forceinline__ void load(uint32_t tmem, int warp, float* v) const {
-    const uint32_t at = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + 32 * (warp >> 2);
-    if constexpr (KB == 1) {
-      tc::tmem_ld16_x2(at, v);
-      tc::tmem_ld_wait16(v);
-    } else {
-      tc::tmem_ld32(at, v);
-      tc::tmem_ld_wait32(v);
-    }
+    tc::tmem_ld32(tmem + ((uint32_t)(32 * (warp & 3)) << 16) + 32 * (warp >> 2), v);
+    tc::tmem_ld_wait32(v);
   }
 };
 
-template <int KB, int NT>
+template <int NT>
 struct Smem {   // byte offsets from a 1024-byte aligned base
   static constexpr int q = 0, k = q + KB * TILE, v = k + KB * TILE, k1 = v + TILE, k2 = k1 + KB * TILE,
                        s = k2 + KB * TILE, NS = NT == 1 ? 2 : 3, s_tile = KB * 64 * 128,
@@ -92,12 +95,12 @@ struct Smem {   // byte offsets from a 1024-byte aligned base
                        pw = NT == 1 ? y + TILE : s + NS * s_tile, bars = pw + (C + 4) * 4, end = bars + 64;
 };
 
-template <int KB, int NT, typename TO>
-__global__ void __launch_bounds__(NTHR, KB == 1 ? 2 : 1)
+template <int NT, typename TO>
+__global__ void __launch_bounds__(NTHR, 1)
     k_decay_tc(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap my, Geom g, Ptrs p,
                int* status) {
-  using L = Smem<KB, NT>;
+  using L = Smem<NT>;
   extern __shared__ __align__(1024) uint8_t sm[];
   const uint32_t base = tc::smem_u32(sm);
   float* pw = reinterpret_cast<float*>(sm + L::pw);   // g^0 .. g^128
@@ -153,17 +156,17 @@ __global__ void __launch_bounds__(NTHR, KB == 1 ? 2 : 1)
 
   // the state, fp32, and its bf16 terms as the operand of Q S: rows d_k, 64
   // values of d_v
-  const StatePart<KB> part(warp, lane);
-  float S[StatePart<KB>::N];
+  const StatePart part(warp, lane);
+  float S[StatePart::N];
   {
     const float* start = g.nseg > 1 ? p.seg + ((size_t)unit * g.nseg + s) * sq : p.S0 ? p.S0 + unit * sq : nullptr;
 #pragma unroll
-    for (int i = 0; i < StatePart<KB>::N; ++i)
+    for (int i = 0; i < StatePart::N; ++i)
       S[i] = start && part.row < g.d_k && part.col + i < cols ? start[(size_t)part.row * g.d_v + c0 + part.col + i] : 0.f;
   }
   auto state_tiles = [&]() {
 #pragma unroll
-    for (int i = 0; i < StatePart<KB>::N; i += 8) {
+    for (int i = 0; i < StatePart::N; i += 8) {
       uint32_t w[4][L::NS];
 #pragma unroll
       for (int j = 0; j < 4; ++j) split2<L::NS>(S[i + 2 * j], S[i + 2 * j + 1], w[j]);
@@ -290,7 +293,7 @@ __global__ void __launch_bounds__(NTHR, KB == 1 ? 2 : 1)
     }
     if (warp == 0) {
       if (tc::elect()) {
-        mma_state<KB>(tm, base + L::k, base + L::k1, base + L::k2, base + L::v, false);
+        mma_state(tm, base + L::k, base + L::k1, base + L::k2, base + L::v, false);
         tc::mma_commit(bars + 4);
       }
       __syncwarp();
@@ -354,11 +357,11 @@ __global__ void __launch_bounds__(NTHR, KB == 1 ? 2 : 1)
       __syncwarp();
     }
     {
-      float d[StatePart<KB>::N];
+      float d[StatePart::N];
       part.load(tm, warp, d);
       const float f = pw[n];
 #pragma unroll
-      for (int i = 0; i < StatePart<KB>::N; ++i) S[i] = fmaf(f, S[i], d[i]);
+      for (int i = 0; i < StatePart::N; ++i) S[i] = fmaf(f, S[i], d[i]);
     }
     if (t0 + C < t_live) state_tiles();
     tc::fence_smem_to_async();
@@ -374,7 +377,7 @@ __global__ void __launch_bounds__(NTHR, KB == 1 ? 2 : 1)
       if (tid % 64 < cols) y[t * g.y_t + tid % 64] = layer::from_f32<TO>(0.f);
     if (s == g.nseg - 1 && p.S_out) {
 #pragma unroll
-      for (int i = 0; i < StatePart<KB>::N; ++i)
+      for (int i = 0; i < StatePart::N; ++i)
         if (part.row < g.d_k && part.col + i < cols)
           p.S_out[unit * sq + (size_t)part.row * g.d_v + c0 + part.col + i] = S[i];
     }
@@ -391,16 +394,14 @@ __global__ void __launch_bounds__(NTHR, KB == 1 ? 2 : 1)
 }
 
 // shared memory of k_decay_tc_state: two (k, v) buffers, three terms
-template <int KB>
 struct SmemState {
   static constexpr int kv_bytes = (KB + 1) * TILE, t0 = 2 * kv_bytes, bars = t0 + 3 * KB * TILE, end = bars + 64;
 };
 
-template <int KB>
-__global__ void __launch_bounds__(NTHR, KB == 1 ? 2 : 1)
+__global__ void __launch_bounds__(NTHR, 1)
     k_decay_tc_state(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv, Geom g, Ptrs p,
                      int* status) {
-  using L = SmemState<KB>;
+  using L = SmemState;
   extern __shared__ __align__(1024) uint8_t sm[];
   const uint32_t base = tc::smem_u32(sm);
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + L::bars);   // full[2], done, tmem base, failed
@@ -467,7 +468,7 @@ __global__ void __launch_bounds__(NTHR, KB == 1 ? 2 : 1)
         __syncwarp();
       }
       if (tc::elect()) {
-        mma_state<KB>(tm, base + L::t0, base + L::t0 + KB * TILE, base + L::t0 + 2 * KB * TILE, vt, c > 0);
+        mma_state(tm, base + L::t0, base + L::t0 + KB * TILE, base + L::t0 + 2 * KB * TILE, vt, c > 0);
         tc::mma_commit(bars + 2);
       }
       __syncwarp();
@@ -477,17 +478,17 @@ __global__ void __launch_bounds__(NTHR, KB == 1 ? 2 : 1)
   tc::fence_after_sync();
   ok = __syncthreads_and(ok);
   if (ok) {
-    const StatePart<KB> part(warp, lane);
-    float d[StatePart<KB>::N];
+    const StatePart part(warp, lane);
+    float d[StatePart::N];
     if (chunks > 0) {
       part.load(tm, warp, d);
     } else {
 #pragma unroll
-      for (int i = 0; i < StatePart<KB>::N; ++i) d[i] = 0.f;
+      for (int i = 0; i < StatePart::N; ++i) d[i] = 0.f;
     }
     float* dst = p.seg + ((size_t)unit * g.nseg + s + 1) * ((size_t)g.d_k * g.d_v);
 #pragma unroll
-    for (int i = 0; i < StatePart<KB>::N; ++i)
+    for (int i = 0; i < StatePart::N; ++i)
       if (part.row < g.d_k && part.col + i < cols) dst[(size_t)part.row * g.d_v + c0 + part.col + i] = d[i];
   } else if (tid == 0) {
     tc::wait(bfull, 0);
@@ -499,22 +500,21 @@ __global__ void __launch_bounds__(NTHR, KB == 1 ? 2 : 1)
   if (warp == 0) tc::tmem_dealloc(tm, 64);
 }
 
-template <int KB, int NT, typename TO>
+template <int NT, typename TO>
 cudaError_t launch_out(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const CUtensorMap& my,
                        const Geom& g, const Ptrs& p, int* status, cudaStream_t st) {
-  auto kern = k_decay_tc<KB, NT, TO>;
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<KB, NT>::end);
+  auto kern = k_decay_tc<NT, TO>;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<NT>::end);
   if (e != cudaSuccess) return e;
-  return tc::launch_overlapped(kern, dim3(g.nseg, g.slices, g.B * g.H), dim3(NTHR), Smem<KB, NT>::end, st, mq, mk, mv,
+  return tc::launch_overlapped(kern, dim3(g.nseg, g.slices, g.B * g.H), dim3(NTHR), Smem<NT>::end, st, mq, mk, mv,
                                my, g, p, status);
 }
-template <int KB>
 cudaError_t launch_state(const CUtensorMap& mk, const CUtensorMap& mv, const Geom& g, const Ptrs& p, int* status,
                          cudaStream_t st) {
-  auto kern = k_decay_tc_state<KB>;
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SmemState<KB>::end);
+  auto kern = k_decay_tc_state;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SmemState::end);
   if (e != cudaSuccess) return e;
-  return tc::launch_overlapped(kern, dim3(g.nseg - 1, g.slices, g.B * g.H), dim3(NTHR), SmemState<KB>::end, st, mk, mv,
+  return tc::launch_overlapped(kern, dim3(g.nseg - 1, g.slices, g.B * g.H), dim3(NTHR), SmemState::end, st, mk, mv,
                                g, p, status);
 }
 
@@ -532,16 +532,13 @@ cudaError_t tc_launch(const Geom& g, const Ptrs& p, bool y_bf16, int* status, cu
       !map_4d(&my, p.y, y_bf16, g.dv_row, g.T, g.H, g.B, g.y_t, g.y_h, g.y_b))
     return cudaErrorInvalidValue;
   if (g.nseg > 1) {
-    cudaError_t e = g.d_k <= 64 ? launch_state<1>(mk, mv, g, p, status, st) : launch_state<2>(mk, mv, g, p, status, st);
+    cudaError_t e = launch_state(mk, mv, g, p, status, st);
     if (e != cudaSuccess) return e;
     e = scan_launch(g, p, st);
     if (e != cudaSuccess) return e;
   }
-  if (g.d_k <= 64)
-    return y_bf16 ? launch_out<1, 1, bf16>(mq, mk, mv, my, g, p, status, st)
-                  : launch_out<1, 3, float>(mq, mk, mv, my, g, p, status, st);
-  return y_bf16 ? launch_out<2, 1, bf16>(mq, mk, mv, my, g, p, status, st)
-                : launch_out<2, 3, float>(mq, mk, mv, my, g, p, status, st);
+  return y_bf16 ? launch_out<1, bf16>(mq, mk, mv, my, g, p, status, st)
+                : launch_out<3, float>(mq, mk, mv, my, g, p, status, st);
 }
 
 }  // namespace decay

@@ -327,6 +327,45 @@ def test_linear_large_values(gpu_lib):
         assert bool(torch.isfinite(y).all())
 
 
+# ------------------------------------------------------- graphs and streams
+def test_captured_in_a_graph(gpu_lib):
+    """After one call of a size (which allocates the workspace) the operators
+    can be captured; a replay gives the same bits, on new inputs too."""
+    import torch
+    from test_learned_neural_gb300.runner import DecayAttention, GroupNorm, Linear
+    B, H, T, d = 1, 4, 600, 64
+    t = _decay_inputs(B, H, T, d, d, "bf16", 1, "heads", False, True, seed=6)
+    mix, norm = DecayAttention(H, d, d, y_layout="tokens"), GroupNorm(H * d, H, act="silu")
+    pos, lin = GroupNorm(H * d, H), Linear(H * d, 264)
+    W = (torch.randn(H * d, 264, generator=torch.Generator().manual_seed(3)) / 16).bfloat16().cuda()
+    a, n, p, y = (mix.alloc_outputs(B, T, "cuda"), norm.alloc_outputs(B * T, 1, "cuda"), pos.alloc_outputs(B, T, "cuda"),
+                  lin.alloc_outputs(B * T, "cuda"))
+
+    def run():
+        mix.forward(t, out=a)
+        norm.forward(dict(x=a["y"].view(B * T, 1, H * d)), out=n)
+        pos.forward(dict(x=n["y"].view(B, T, H * d)), out=p)
+        lin.forward(dict(x=p["y"].view(B * T, H * d), W=W), out=y)
+
+    run()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        run()
+    for seed in (7, 8):
+        fresh = _decay_inputs(B, H, T, d, d, "bf16", 1, "heads", False, True, seed=seed)
+        for k in ("q", "k", "v", "S0"):
+            t[k].copy_(fresh[k])
+        run()
+        torch.cuda.synchronize()
+        want = [a["y"].clone(), a["S"].clone(), y["y"].clone()]
+        for o in (a["y"], a["S"], n["y"], p["y"], y["y"]):
+            o.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(u, v) for u, v in zip(want, (a["y"], a["S"], y["y"])))
+
+
 # ------------------------------------------------------------------ chained
 def _layer_reference(la, x):
     """The example layer in 64 bits, nothing rounded in between."""

@@ -222,7 +222,8 @@ __global__ void __launch_bounds__(256) k_planes(PlaneJob x, PlaneJob w) {
 struct Operands {
   bool copy_x, copy_w;
   int planes, K, ldx, ldw;   // K: columns of x and rows of W as the kernels see them
-  size_t x_bytes, w_bytes;
+  int splits;
+  size_t x_bytes, w_bytes, split_bytes;
 };
 
 Operands make_operands(const atlas_linear_config& c, int M, bool x_ok, bool w_ok) {
@@ -236,6 +237,8 @@ Operands make_operands(const atlas_linear_config& c, int M, bool x_ok, bool w_ok
   o.ldw = o.copy_w ? (c.N + 7) / 8 * 8 : c.N;
   o.x_bytes = o.copy_x ? ((size_t)o.planes * M * o.ldx * 2 + 255) / 256 * 256 : 0;
   o.w_bytes = o.copy_w ? ((size_t)o.planes * o.K * o.ldw * 2 + 255) / 256 * 256 : 0;
+  o.splits = linear::tc_splits(M, c.N, o.K, o.planes);
+  o.split_bytes = linear::tc_split_bytes(M, c.N, o.splits);
   return o;
 }
 
@@ -284,7 +287,7 @@ extern "C" int atlas_linear_create(const atlas_linear_config* cfg, atlas_linear_
 extern "C" size_t atlas_linear_workspace_bytes(const atlas_linear_handle* h, int M) {
   if (!h || M <= most_few_rows(h->cfg)) return 0;
   const Operands o = make_operands(h->cfg, M, false, false);
-  return o.x_bytes + o.w_bytes;
+  return o.x_bytes + o.w_bytes + o.split_bytes;
 }
 
 extern "C" int atlas_linear_forward(atlas_linear_handle* h, const atlas_linear_io* io, void* stream) {
@@ -300,7 +303,7 @@ extern "C" int atlas_linear_forward(atlas_linear_handle* h, const atlas_linear_i
   if (io->M > most_few_rows(c)) {
     const Operands o = make_operands(c, io->M, aligned16(io->x), aligned16(io->W));
     int rc = h->need_status(st);
-    if (!rc) rc = h->grow(o.x_bytes + o.w_bytes);
+    if (!rc) rc = h->grow(o.x_bytes + o.w_bytes + o.split_bytes);
     if (rc) return rc;
     char* ws = (char*)h->ws;
     cudaError_t e = cudaSuccess;
@@ -314,6 +317,7 @@ extern "C" int atlas_linear_forward(atlas_linear_handle* h, const atlas_linear_i
     t.x = o.copy_x ? ws : io->x;
     t.W = o.copy_w ? ws + o.x_bytes : io->W;
     t.bias = io->bias, t.residual = io->residual, t.y = io->y, t.act = c.act, t.out_bf16 = ob, t.status = h->status;
+    t.splits = o.splits, t.split_ws = ws + o.x_bytes + o.w_bytes;
     if (e == cudaSuccess) e = linear::tc_big(t, st);
     if (e != cudaSuccess) return h->cuda_fail("matrix product launch", e);
     h->path = 1;

@@ -22,6 +22,7 @@
 // 24 bits), six products x0 W0, x0 W1, x1 W0, x0 W2, x2 W0, x1 W1 into one
 // accumulator; the dropped ones are below 2^-23 of the sum of |x W|.
 #include <algorithm>
+#include <type_traits>
 
 #include "linear_common.cuh"
 #include "tc2.cuh"
@@ -45,6 +46,7 @@ constexpr int BAND = 16;                                         // row tiles pe
 struct Params {
   int M, N, nk, kc, planes, kw;   // nk: blocks of 64 of K per plane, kc of them per pass; kw: W rows per plane
   int act;
+  int kper, split_rows;     // K split: blocks of 64 per split (nk: no split), rows of y per split
   const float* bias;
   const void* residual;
   void* y;
@@ -83,9 +85,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHR, 1)
   __shared__ int failed;
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   const uint32_t rank = tc::cluster_rank();
-  const int ntm = (p.M + BM - 1) / BM, ntn = (p.N + BN - 1) / BN, ntiles = ntm * ntn;
+  const int ntm = (p.M + BM - 1) / BM, ntn = (p.N + BN - 1) / BN, nmn = ntm * ntn;
+  const int ntiles = nmn * ((p.nk + p.kper - 1) / p.kper);   // a split's tiles, then the next split's
   const int first = blockIdx.x / 2, step = gridDim.x / 2;
-  const int pairs = p.planes == 1 ? 1 : 6, passes = (p.nk + p.kc - 1) / p.kc;
+  const int pairs = p.planes == 1 ? 1 : 6;
 
   if (warp == 0) tc::tmem_alloc_pair(&tbase, 2 * BN);
   if (tid == 32) {
@@ -121,10 +124,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHR, 1)
     uint32_t s = 0, ph = 1;                                  // the first turn finds its slots free
     bool ok = true;
     for (int t = first; t < ntiles && ok; t += step) {
-      const Tile tl = tile_at<BN>(t, ntm, ntn);
+      const Tile tl = tile_at<BN>(t % nmn, ntm, ntn);
       const int m0 = tl.m0 + (int)rank * (BM / 2), n0 = tl.n0 + (int)rank * (BN / 2);
-      for (int k0 = 0; k0 < p.nk && ok; k0 += p.kc) {
-        const int k1 = min(p.nk, k0 + p.kc);
+      const int k_lo = t / nmn * p.kper, k_hi = min(p.nk, k_lo + p.kper);
+      for (int k0 = k_lo; k0 < k_hi && ok; k0 += p.kc) {
+        const int k1 = min(k_hi, k0 + p.kc);
         for (int pr = 0; pr < pairs && ok; ++pr) {
           int row_x = m0, row_w = 0;
           if (pairs > 1) {
@@ -158,12 +162,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHR, 1)
       uint32_t s = 0, ph = 0, n = 0;
       bool ok = true;
       for (int t = first; t < ntiles && ok; t += step) {
-        for (int k0 = 0; k0 < p.nk && ok; k0 += p.kc, ++n) {
+        const int k_lo = t / nmn * p.kper, k_hi = min(p.nk, k_lo + p.kper);
+        for (int k0 = k_lo; k0 < k_hi && ok; k0 += p.kc, ++n) {
           const uint32_t a = n & 1;
           // the epilogues have read this accumulator's last contents
           if (!(ok = __all_sync(0xffffffffu, tc::wait(tc::smem_u32(&acc_empty[a]), ((n >> 1) & 1) ^ 1)))) break;
           tc::fence_after_sync();
-          const int stages = (min(p.nk, k0 + p.kc) - k0) * pairs;
+          const int stages = (min(k_hi, k0 + p.kc) - k0) * pairs;
           for (int i = 0; i < stages; ++i) {
             if (!(ok = __all_sync(0xffffffffu, tc::wait(bfull + 8 * s, ph)))) break;
             if (tc::elect()) {
@@ -198,7 +203,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHR, 1)
     bool ok = true;
     // the warp's part of tile t: 32 rows from row m, HALF columns from column c
     auto part_of = [&](int t, int& m, int& c) {
-      const Tile tl = tile_at<BN>(t, ntm, ntn);
+      const Tile tl = tile_at<BN>(t % nmn, ntm, ntn);
       m = tl.m0 + (int)rank * 128 + 32 * q;
       c = tl.n0 + half * HALF;
     };
@@ -232,6 +237,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHR, 1)
       if constexpr (sizeof(TO) == 4) {
 #pragma unroll
         for (int j = 0; j < NSUM; ++j) sums[j] = 0.f;
+        const int k_lo = t / nmn * p.kper, passes = (min(p.kper, p.nk - k_lo) + p.kc - 1) / p.kc;
         for (int ps = 0; ps + 1 < passes; ++ps, ++n) {
           const int a = n & 1;
           ok = __all_sync(0xffffffffu, tc::wait(tc::smem_u32(&acc_full[a]), (n >> 1) & 1));
@@ -343,7 +349,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHR, 1)
           tc::fence_smem_to_async();
           __syncwarp();
           if (lane == 0) {   // always lane 0: it waits for its own stores
-            tc::tma_store_2d(&map_y, cbeg + c, m, buf + b * BLK_BYTES);
+            tc::tma_store_2d(&map_y, cbeg + c, m + t / nmn * p.split_rows, buf + b * BLK_BYTES);
             tc::bulk_commit();
           }
           ++blk;
@@ -403,6 +409,39 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHR, 1)
   if (warp == 0) tc::tmem_dealloc_pair(tbase, 2 * BN);
 }
 
+// y = act(sum of the splits + bias) + residual
+template <typename TO>
+__global__ void __launch_bounds__(256) k_linear_join(const float* __restrict__ part, int splits, int M, int N, int rows,
+                                                     int cols, int act, const float* __restrict__ bias,
+                                                     const TO* residual, TO* y) {
+  tc::grid_dependency_wait();
+  tc::grid_dependents_launch();
+  const size_t i = (size_t)blockIdx.x * 256 + threadIdx.x;
+  const int per = cols / 4, m = (int)(i / per), c = (int)(i % per) * 4;
+  if (m >= M) return;
+  float v[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+  for (int s = 0; s < splits; ++s) {
+    float p[4];
+    layer::load_vec<4>(part + ((size_t)s * rows + m) * cols + c, p);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] += p[e];
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) v[e] += bias && c + e < N ? bias[c + e] : 0.f;
+  linear::act_run<TO, 4>(act, v);
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    if (c + e < N) {
+      const size_t at = (size_t)m * N + c + e;
+      y[at] = layer::from_f32<TO>(residual ? v[e] + layer::to_f32(residual[at]) : v[e]);
+    }
+}
+
+// rows and columns of a split's fp32 product in the workspace
+int split_rows(int M) { return (M + BM - 1) / BM * BM; }
+int split_cols(int N) { return (N + 3) / 4 * 4; }
+
 // How many blocks of 64 of K go into one accumulator.  The tensor cores cut
 // off, they do not round: an fp32 accumulator loses about 1.1e-9 of the result
 // per value of K (measured: 4.8e-7 at K = 517, 9.1e-6 at 8192).  fp32 results
@@ -418,17 +457,23 @@ cudaError_t launch_pair(const linear::TcCall& c, cudaStream_t st) {
   if (!tc::tensor_map_2d(&mx, c.x, true, (uint64_t)c.planes * c.M, c.K, (uint64_t)c.ldx * 2, BM / 2) ||
       !tc::tensor_map_2d(&mw, c.W, true, (uint64_t)c.planes * c.K, c.N, (uint64_t)c.ldw * 2, BK))
     return cudaErrorInvalidValue;
-  const int nk = (c.K + BK - 1) / BK;
-  Params p{c.M, c.N, nk, blocks_per_pass(c, nk), c.planes, c.K, c.act, c.bias, c.residual, c.y, 0, c.status};
-  const uint64_t row = (uint64_t)c.N * sizeof(TO);
+  const int nk = (c.K + BK - 1) / BK, kper = (nk + c.splits - 1) / c.splits;
+  Params p{c.M, c.N, nk, blocks_per_pass(c, nk), c.planes, c.K, c.act, kper, 0, c.bias, c.residual, c.y, 0, c.status};
+  uint64_t rows = c.M;
+  if (c.splits > 1) {
+    p.split_rows = split_rows(c.M);
+    rows = (uint64_t)c.splits * p.split_rows;
+  }
+  const uint64_t row = (uint64_t)(c.splits > 1 ? split_cols(c.N) : c.N) * sizeof(TO);
   p.tma_out = row % 16 == 0 && layer::aligned16(c.y) && layer::aligned16(c.residual) && layer::aligned16(c.bias) &&
-              tc::tensor_map_2d(&my, c.y, sizeof(TO) == 2, c.M, c.N, row, 32, 64) &&
+              tc::tensor_map_2d(&my, c.y, sizeof(TO) == 2, rows, c.N, row, 32, 64) &&
               tc::tensor_map_2d(&mr, c.residual ? c.residual : c.y, sizeof(TO) == 2, c.M, c.N, row, 32, 64);
+  if (c.splits > 1 && !p.tma_out) return cudaErrorInvalidValue;
   if (!p.tma_out) mr = my = mx;   // not used
   auto kern = k_linear_pair<TO, BN>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<BN>::SMEM);
   if (e != cudaSuccess) return e;
-  const long long tiles = (long long)((c.M + BM - 1) / BM) * ((c.N + BN - 1) / BN);
+  const long long tiles = (long long)((c.M + BM - 1) / BM) * ((c.N + BN - 1) / BN) * c.splits;
   const int grid = (int)std::min<long long>(tiles, layer::sm_count() / 2) * 2;
   return tc::launch_overlapped(kern, dim3(grid), dim3(NTHR), Cfg<BN>::SMEM, st, mx, mw, mr, my, p);
 }
@@ -437,7 +482,35 @@ cudaError_t launch_pair(const linear::TcCall& c, cudaStream_t st) {
 
 namespace linear {
 
+// K is split over idle pairs where a tile takes 96 stages or more (7 us) on its
+// own and at least half of the pairs have none: down to 24 stages each.  The
+// splits' fp32 products go through the workspace and are added in order.
+int tc_splits(int M, int N, int K, int planes) {
+  const long long pairs = layer::sm_count() / 2, tiles = (long long)((M + BM - 1) / BM) * ((N + 127) / 128);
+  const long long nk = (K + BK - 1) / BK, stages = nk * (planes == 1 ? 1 : 6);
+  if (stages < 96 || 2 * tiles > pairs) return 1;
+  const long long s = std::min(std::min(pairs / tiles, stages / 24), std::min(nk, 32LL)), per = (nk + s - 1) / s;
+  return (int)((nk + per - 1) / per);   // no empty split
+}
+size_t tc_split_bytes(int M, int N, int splits) {
+  return splits > 1 ? (size_t)splits * split_rows(M) * split_cols(N) * sizeof(float) : 0;
+}
+
 cudaError_t tc_big(const TcCall& c, cudaStream_t st) {
+  if (c.splits > 1) {
+    TcCall part = c;
+    part.bias = nullptr, part.residual = nullptr, part.y = c.split_ws, part.act = ATLAS_ACT_NONE, part.out_bf16 = 0;
+    cudaError_t e = launch_pair<float, 128>(part, st);
+    if (e != cudaSuccess) return e;
+    const int cols = split_cols(c.N);
+    const unsigned grid = (unsigned)(((size_t)c.M * (cols / 4) + 255) / 256);
+    auto join = [&](auto kern, auto* y) {
+      using T = std::remove_pointer_t<decltype(y)>;
+      return tc::launch_overlapped(kern, dim3(grid), dim3(256), 0, st, (const float*)c.split_ws, c.splits, c.M, c.N,
+                                   split_rows(c.M), cols, c.act, c.bias, (const T*)c.residual, (T*)c.y);
+    };
+    return c.out_bf16 ? join(k_linear_join<bf16>, (bf16*)nullptr) : join(k_linear_join<float>, (float*)nullptr);
+  }
   // 128 columns per tile where the last round of tiles then wastes less: time in
   // units of 128 columns, the narrow tiles 1.3 times as long per column (they
   // fetch 1.5 times as much: 8192^3 took 816 us with them, 665 with wide ones)

@@ -139,9 +139,13 @@ struct TcCall {
   const void* residual;
   void* y;
   int act, out_bf16;
+  int splits;        // of K (tc_splits); more than one: through split_ws, tc_split_bytes of it
+  void* split_ws;
   int* status;
 };
 
+int tc_splits(int M, int N, int K, int planes);
+size_t tc_split_bytes(int M, int N, int splits);
 cudaError_t tc_big(const TcCall& c, cudaStream_t st);
 
 }  // namespace linear

@@ -363,8 +363,12 @@ __global__ void __launch_bounds__(NTHR, 1)
     auto element = [&](int i) { return (size_t)(col + 32 * (i / 16) + i % 16) * g.d_v + c0 + row; };
     auto inside = [&](int i) { return row < cols && col + 32 * (i / 16) + i % 16 < g.d_k; };
     {
-      const bool add = g.nseg > 1 && inline_scan;   // start = S0 carried over the segments before this one
-      const float* d = g.nseg > 1 && !add ? p.seg + ((size_t)unit * g.nseg + s) * sq : p.S0 ? p.S0 + unit * sq : nullptr;
+      // start = S0 carried over the segments before this one; S0 from its copy in
+      // the workspace, since the last segment's block may have written S_out, the
+      // same array, by now
+      const bool add = g.nseg > 1 && inline_scan;
+      const float* d = g.nseg == 1 ? (p.S0 ? p.S0 + unit * sq : nullptr)
+                       : add && !p.S0 ? nullptr : p.seg + ((size_t)unit * g.nseg + (add ? 0 : s)) * sq;
 #pragma unroll
       for (int i = 0; i < 32; ++i) st[i] = d && inside(i) ? d[element(i)] : 0.f;
       for (int e = 0; add && e < s; ++e) {
@@ -506,6 +510,10 @@ __global__ void __launch_bounds__(NTHR_STATE, 1)
     }
   } else {
     const int r = 32 * quarter + lane;
+    const int row = 16 * quarter + lane % 16, col = 16 * (lane / 16);   // a thread's column of d_v, rows of d_k
+    auto element = [&](int i) { return col + 32 * (i / 16) + i % 16; };
+    auto inside = [&](int i) { return row < cols && element(i) < g.d_k; };
+    const size_t sq = (size_t)g.d_k * g.d_v;
     const float l2g = log2f(p.decay[h]);
     for (int c = group; c < chunks; c += 2) {
       const int t0 = t_lo + c * C, n = min(C, t_live - t0);
@@ -544,13 +552,19 @@ __global__ void __launch_bounds__(NTHR_STATE, 1)
           for (int i = 0; i < 32; ++i) sum[i] += d[i];
         }
       }
-      const int row = 16 * quarter + lane % 16, col = 16 * (lane / 16);   // column of d_v, rows of d_k
-      float* dst = p.seg + ((size_t)unit * g.nseg + s + 1) * ((size_t)g.d_k * g.d_v) + c0 + row;
+      float* dst = p.seg + ((size_t)unit * g.nseg + s + 1) * sq + c0 + row;
 #pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        const int kk = col + 32 * (i / 16) + i % 16;
-        if (row < cols && kk < g.d_k) dst[(size_t)kk * g.d_v] = sum[i];
-      }
+      for (int i = 0; i < 32; ++i)
+        if (inside(i)) dst[(size_t)element(i) * g.d_v] = sum[i];
+    } else if (ok && s == 0 && p.S0 && g.nseg <= kInlineScan) {   // S0 to slot 0, by the other group
+      const float* src = p.S0 + unit * sq + c0 + row;
+      float* dst = p.seg + (size_t)unit * g.nseg * sq + c0 + row;
+      float v[32];
+#pragma unroll
+      for (int i = 0; i < 32; ++i) v[i] = inside(i) ? src[(size_t)element(i) * g.d_v] : 0.f;
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        if (inside(i)) dst[(size_t)element(i) * g.d_v] = v[i];
     }
   }
   if (!ok && lane == 0) atomicExch(failed, 1);

@@ -138,6 +138,28 @@ def test_decay_extremes(gpu_lib, gammas, T):
     _decay_check(t, 2, 64, 64, "bf16", "f32", 1, "heads", "heads")
 
 
+@pytest.mark.parametrize("dims", [(64, 64), (128, 64), (48, 200)], ids=str)
+@pytest.mark.parametrize("T", [300, 900, 2000, 5000])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_decay_state_in_place_of_split_rows(gpu_lib, dims, T, dtype):
+    """Long rows beside short and empty ones, split along the tokens: S_out in
+    S0's buffer gives the bits that a buffer of its own gives."""
+    import torch
+    from test_learned_neural_gb300.runner import DecayAttention
+    (dk, dv), B, H = dims, 5, 4
+    t = _decay_inputs(B, H, T, dk, dv, dtype, 2, "tokens", False, True, seed=T)
+    t["lens"] = torch.tensor([T, 0, 1, T // 2, T - 1], dtype=torch.int32).cuda()
+    op = DecayAttention(H, dk, dv, 2, dtype, "f32", "tokens", "tokens")
+    own = op.forward(t)
+    S = t["S0"].clone()
+    out = dict(y=torch.empty_like(own["y"]), S=S)
+    op.forward(dict(t, S0=S), out=out)
+    torch.cuda.synchronize()
+    op.status()
+    assert torch.equal(out["y"], own["y"]) and torch.equal(S, own["S"])
+    assert torch.equal(S[1], t["S0"][1])
+
+
 @pytest.mark.parametrize("cuts", [(1,), (40, 41), (64,), (130, 500)], ids=str)
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_decay_continues_in_place(gpu_lib, cuts, dtype):

@@ -25,6 +25,12 @@
  * fp32.  A handle is not re-entrant: do not call it from two threads or on two
  * streams at once.
  *
+ * Inputs: tokens past lens[b] are never used, whatever they hold.  A NaN or an
+ * infinity in a live token reaches nothing but its own row and head (for q and k
+ * the value heads that use them), there the later read-outs and the final state
+ * (0 * NaN is NaN: with a decay of 0 as well) and, in a call that works in
+ * chunks, read-outs up to 127 tokens before it too.
+ *
  * Errors: the status codes of atlas_mem.h; atlas_decay_last_error gives the
  * message.  Validation failures return before any CUDA call.
  */

@@ -11,7 +11,9 @@
  * rounded once.  W has the orientation of atlas_prologue.h's W_in.
  *
  * Execution: asynchronous on the given CUDA stream.  bf16 inputs: exact
- * products, fp32 accumulation.  fp32 inputs: fp32 accuracy.  A handle is not
+ * products, fp32 accumulation.  fp32 inputs: fp32 accuracy (three bf16 planes of
+ * each on the tensor cores; a NaN or an infinity in x makes its row of y
+ * non-finite, not always of the same kind, and no other row).  A handle is not
  * re-entrant: do not call it from two threads or on two streams at once.
  *
  * Errors: the status codes of atlas_mem.h; atlas_linear_last_error gives the

@@ -16,12 +16,13 @@ using decay::Ptrs;
 namespace {
 
 constexpr int kSlice = 64;         // d_v columns per CTA
-constexpr int kMaxStepTokens = 16; // calls up to this long go token by token
 
 // ------------------------------------------------- token by token
 // A CTA holds kSlice columns of one state in registers: thread (rg, c4) rows
 // rg, rg + 16, ... and columns 4 c4 .. 4 c4 + 3, so the state is read and
-// written once, by 256-byte row segments.
+// written once, by 256-byte row segments.  256 rows x 16 heads of 128 x 128, one
+// token: 81 us for 541 MB, 98 % of the copy bandwidth.  8 rows x 8 heads of 64 x 64:
+// 7 us, of which 5 are the host's call.
 template <typename TI, typename TO, int RPT, int V>
 __global__ void __launch_bounds__(256) k_decay_step(Geom g, Ptrs p) {
   constexpr int CL = kSlice / V;             // threads along the columns
@@ -100,7 +101,9 @@ __global__ void __launch_bounds__(256) k_decay_step(Geom g, Ptrs p) {
 // One CTA: (segment, column slice, unit), chunks of C tokens in order; every
 // product is a register-tiled fp32 loop over shared-memory tiles.  READ: form
 // the read-outs from the segment-start state; else only the segment's own
-// contribution to the next segment's start.
+// contribution to the next segment's start.  Bound by the latency of its fp32
+// loops where blocks are few (three per SM at C = 64): 3 rows x 6 heads of ragged
+// lengths to 1501, d 48: 41 us in three overlapped launches (states 15, scan 8, read-outs 32).
 template <typename TI, typename TO, int C, bool READ>
 __global__ void __launch_bounds__(256, C == 64 ? 3 : 1) k_decay_chunk(Geom g, Ptrs p) {
   extern __shared__ float sm[];
@@ -361,6 +364,23 @@ int best_segments(long long ctas, long long chunks, long long slots, double ends
   return (int)best;
 }
 
+// The longest call that goes token by token.  Measured at 8, 64 and 1024 states,
+// token by token against in chunks (us), where the two cross:
+//   8 and 64 states (a block per SM, the chunks' launch and pipeline count)
+//     tensor cores, d_k 64:    5 tokens 10 / 10,   8 tokens  12 / 10
+//     tensor cores, d_k 128:  12 tokens 18 / 18,  16 tokens  21 / 18
+//     fp32, d_k 64:           12 tokens 16 / 17,  16 tokens  21 / 17
+//     fp32, d_k 128:          20 tokens 26 / 29,  32 tokens  39 / 31
+//   1024 states (several blocks per SM: a chunk costs the same at any length)
+//     tensor cores, d_k 64:   20 tokens 49 / 49,  32 tokens  70 / 49
+//     the others: 32 tokens 73 / 92 (fp32, d_k 64), 182 / 205 (tensor cores, d_k
+//     128), 188 / 361 (fp32, d_k 128)
+int most_step_tokens(const atlas_decay_config& c, long long ctas) {
+  const bool tc = c.qkv_dtype == ATLAS_BF16 && c.d_k <= 128;
+  if (ctas > sm_count()) return tc && c.d_k <= 64 ? 20 : 32;
+  return tc && c.d_k <= 64 ? 5 : tc || c.d_k <= 64 ? 12 : 20;
+}
+
 // bf16 calls with d_k <= 128 take the tensor-core chunks.  Their copies want rows
 // of whole 16-byte groups: other widths (or addresses) go through padded copies
 // of q, k, v and y in the workspace.  `aligned`: the addresses do not ask for it.
@@ -369,7 +389,7 @@ Plan make_plan(const atlas_decay_config& c, int B, int T, bool aligned) {
   pl.slices = (c.d_v + kSlice - 1) / kSlice;
   pl.nseg = 1;
   pl.seg = T;
-  if (T <= kMaxStepTokens) {
+  if (T <= most_step_tokens(c, (long long)B * c.H * pl.slices)) {
     pl.path = 0;
     pl.C = 1;
     return pl;
@@ -507,10 +527,11 @@ extern "C" int atlas_decay_forward(atlas_decay_handle* h, const atlas_decay_io* 
     return h->fail(ATLAS_ERR_INVALID_ARG, "q, k, v, decay, y must be non-NULL");
   if (io->y == io->q || io->y == io->k || io->y == io->v)
     return h->fail(ATLAS_ERR_INVALID_ARG, "y must not alias q, k or v");
-  if ((long long)io->B * c.H > 65535 && io->T > kMaxStepTokens)
-    return h->fail(ATLAS_ERR_UNSUPPORTED, "B * H > 65535 is supported for calls of at most %d tokens", kMaxStepTokens);
-  if ((long long)io->B * c.H * ((c.d_v + kSlice - 1) / kSlice) > 0x7fffffffLL)
-    return h->fail(ATLAS_ERR_UNSUPPORTED, "B * H too large for one call");
+  const long long ctas = (long long)io->B * c.H * ((c.d_v + kSlice - 1) / kSlice);
+  if (ctas > 0x7fffffffLL) return h->fail(ATLAS_ERR_UNSUPPORTED, "B * H too large for one call");
+  if ((long long)io->B * c.H > 65535 && io->T > most_step_tokens(c, ctas))
+    return h->fail(ATLAS_ERR_UNSUPPORTED, "B * H > 65535 is supported for calls of at most %d tokens",
+                   most_step_tokens(c, ctas));
   cudaStream_t st = (cudaStream_t)stream;
   const Plan pl = make_plan(c, io->B, io->T,
                             aligned16(io->q) && aligned16(io->k) && aligned16(io->v) && aligned16(io->y));

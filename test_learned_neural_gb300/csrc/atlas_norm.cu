@@ -492,7 +492,9 @@ Plan make_plan(const atlas_norm_config& c, int N, int S, bool vec) {
   if ((S == 1 || c.layout == ATLAS_NORM_HEADS) && Cg <= kMaxRun) return p;
   // A cluster's registers, where they hold the sample's tile (128 bytes or more
   // of a row, whole groups) and the clusters fill the SMs: x is read once.
-  // 8 x 4096 x 1024 bf16: 44 us in two passes.
+  // 8 x 4096 x 1024 bf16, 32 groups: 39 us so, 47 in two passes; 32 x 256 x 512:
+  // 12 / 14.  (Sixteen vectors per thread instead of eight: 51 and 84 -> 90 us for
+  // 4096 rows of fp32, which do not fit eight: too few blocks per SM.)
   const int v16 = 16 / (int)dtype_size(c.x_dtype);
   if (vec && Cg % v16 == 0 && Cg / v16 <= 256) {
     const int vg = Cg / v16;
@@ -518,7 +520,9 @@ Plan make_plan(const atlas_norm_config& c, int N, int S, bool vec) {
   const long long bytes = cnt * per * 256 * p.V * (long long)dtype_size(c.x_dtype);
   const long long blocks = (long long)N * p.tiles;
   // One read instead of two where the tile fits and the blocks fill the SMs
-  // (else two passes with more blocks are faster: their second read is an L2 hit).
+  // (else two passes with more blocks are as fast: their second read is an L2 hit).
+  // 64 x 100 x 96, 3 groups: 8 us so, 10 in two passes; 256 x 100 x 66: 12 / 14;
+  // 2 x 256 x 512 (too few blocks): 10 / 10.
   if (bytes <= kTileBytes && (blocks >= sm_count() || bytes <= 8 * 1024)) {
     p.kind = 1;
     p.smem = (int)bytes;

@@ -15,6 +15,10 @@
 //              into the same buffers by TMA, four blocks at a time while the
 //              MMAs fill the tile's accumulator; the accumulator and the bias
 //              are read one block ahead.
+// 16384 x 2048 x 8192 bf16 with bias and GELU: 338 us = 1.63 PFLOP/s, 93-95 % of
+// the plain library product under the same power cap; a stage's MMAs take 515-525
+// cycles of an ideal 512, tensor pipe 90 % active over the whole launch.  Smaller
+// calls lose to the number of tiles: 16384 x 768 x 768 has 2.5 rounds of 76.
 // Where y or the residual cannot be a TMA operand (row stride or address not on
 // 16 bytes) the block leaves by coalesced element stores instead.
 //
@@ -484,7 +488,9 @@ namespace linear {
 
 // K is split over idle pairs where a tile takes 96 stages or more (7 us) on its
 // own and at least half of the pairs have none: down to 24 stages each.  The
-// splits' fp32 products go through the workspace and are added in order.
+// splits' fp32 products go through the workspace and are added in order.  bf16
+// 64 x 8192 x 1024: 37 us without the split, 21 with it; 40 x 16384 x 136: 64 / 19;
+// fp32 128 x 4096 x 256: 94 / 24; 300 x 1024 x 512 (96 stages): 33 / 22.
 int tc_splits(int M, int N, int K, int planes) {
   const long long pairs = layer::sm_count() / 2, tiles = (long long)((M + BM - 1) / BM) * ((N + 127) / 128);
   const long long nk = (K + BK - 1) / BK, stages = nk * (planes == 1 ? 1 : 6);

@@ -42,7 +42,7 @@ typedef struct atlas_linear_handle atlas_linear_handle;
 
 /* Tensors of one call, all DEVICE pointers owned by the caller. */
 typedef struct {
-    int M;                 /* rows, M >= 1 */
+    int M;                 /* rows, 1 .. 4194240 */
     const void* x;         /* [M][K] in_dtype */
     const void* W;         /* [K][N] in_dtype */
     const float* bias;     /* [N]; NULL: 0 */

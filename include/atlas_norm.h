@@ -56,7 +56,7 @@ typedef struct atlas_norm_handle atlas_norm_handle;
 
 /* Tensors of one call, all DEVICE pointers owned by the caller. */
 typedef struct {
-    int N, S;             /* N >= 1, S >= 1 */
+    int N, S;             /* N >= 1, S >= 1, N * S * groups <= 2^30 */
     const void* x;        /* see layout, x_dtype */
     const float* weight;  /* [C]; NULL: 1 */
     const float* bias;    /* [C]; NULL: 0 */

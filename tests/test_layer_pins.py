@@ -161,6 +161,26 @@ def test_linear_forward_validates_before_any_cuda_call(lib):
     lib.atlas_linear_destroy(None)
 
 
+def test_sizes_beyond_a_call_are_refused(lib):
+    """The documented limits, one past each."""
+    lin = tln.atlas_linear_create(tln.make_linear_config(K=8, N=8))
+    io = tln.atlas_linear_io(4194241)
+    io.x, io.W, io.y = 64, 128, 192
+    _refuses(lib, "linear", lin, io, UNS, "4194240")
+    dec = tln.atlas_decay_create(tln.make_decay_config(H=4, d_k=64, d_v=64))
+    io = tln.atlas_decay_io(1 << 14, 21)
+    io.q = io.k = io.v = io.decay = 64
+    io.y = 128
+    _refuses(lib, "decay", dec, io, UNS, "at most 20 tokens")
+    nrm = tln.atlas_norm_create(tln.make_norm_config(C=12, groups=3))
+    io = tln.atlas_norm_io(1 << 15, 1 << 14)
+    io.x, io.y = 64, 128
+    _refuses(lib, "norm", nrm, io, UNS, "2^30")
+    tln.atlas_linear_destroy(lin)
+    tln.atlas_decay_destroy(dec)
+    tln.atlas_norm_destroy(nrm)
+
+
 def test_runner_refuses_wrong_tensors(lib):
     import torch
     from test_learned_neural_gb300.runner import DecayAttention, GroupNorm, Linear

@@ -486,16 +486,18 @@ cudaError_t launch_pair(const linear::TcCall& c, cudaStream_t st) {
 
 namespace linear {
 
-// K is split over idle pairs where a tile takes 96 stages or more (7 us) on its
-// own and at least half of the pairs have none: down to 24 stages each.  The
-// splits' fp32 products go through the workspace and are added in order.  bf16
-// 64 x 8192 x 1024: 37 us without the split, 21 with it; 40 x 16384 x 136: 64 / 19;
-// fp32 128 x 4096 x 256: 94 / 24; 300 x 1024 x 512 (96 stages): 33 / 22.
+// K is split over idle pairs where a tile takes 32 stages or more on its own and
+// at least half of the pairs have none: down to 8 stages each.  The splits' fp32
+// products go through the workspace and are added in order.  bf16, without the
+// split / with it: 30 x 4864 x 108 (76 stages) 27 / 15 us, 145 x 4864 x 605 31 / 20,
+// 64 x 8192 x 1024 37 / 21, 40 x 16384 x 136 64 / 19, 5 x 2048 x 2048 (32 stages)
+// 16 / 14; fp32 128 x 4096 x 256: 94 / 24, 300 x 1024 x 512 33 / 22.  Splitting
+// where fewer pairs are idle loses: 300 x 4096 x 4096 25 / 35.
 int tc_splits(int M, int N, int K, int planes) {
   const long long pairs = layer::sm_count() / 2, tiles = (long long)((M + BM - 1) / BM) * ((N + 127) / 128);
   const long long nk = (K + BK - 1) / BK, stages = nk * (planes == 1 ? 1 : 6);
-  if (stages < 96 || 2 * tiles > pairs) return 1;
-  const long long s = std::min(std::min(pairs / tiles, stages / 24), std::min(nk, 32LL)), per = (nk + s - 1) / s;
+  if (stages < 32 || 2 * tiles > pairs) return 1;
+  const long long s = std::min(std::min(pairs / tiles, stages / 8), std::min(nk, 32LL)), per = (nk + s - 1) / s;
   return (int)((nk + per - 1) / per);   // no empty split
 }
 size_t tc_split_bytes(int M, int N, int splits) {

@@ -284,7 +284,7 @@ LINEAR = [
     (1, 512, 512), (1, 1, 1), (1, 77, 300), (2, 768, 768), (5, 520, 264), (8, 64, 4096), (17, 512, 136), (33, 1024, 512),
     (64, 256, 512), (100, 51, 67), (127, 192, 128), (128, 64, 256), (129, 100, 72), (300, 768, 200), (700, 96, 1031),
     (1000, 517, 264), (520, 1000, 1160),
-    (40, 8192, 136), (300, 6500, 70),     # K split over the idle blocks (fp32 from about K = 1024)
+    (40, 8192, 136), (300, 6500, 70), (30, 2100, 100), (5, 2048, 2050),     # K split over the idle blocks (fp32 from about K = 1024)
 ]
 
 

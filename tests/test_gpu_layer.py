@@ -208,6 +208,7 @@ def test_decay_other_stream_and_repeat(gpu_lib):
 NORM = [
     (1, 1, 1, 1), (3, 1, 64, 8), (2, 1, 512, 8), (5, 1, 1024, 1), (2, 1, 2048, 1), (3, 1, 70, 7), (2, 1, 768, 16),
     (1, 2, 6, 3), (2, 33, 24, 3), (3, 64, 256, 8), (2, 1000, 64, 4), (1, 4097, 48, 2), (2, 257, 510, 6),
+    (700, 9, 96, 6), (640, 30, 40, 5), (610, 2, 80, 10), (630, 16, 96, 2),   # several groups per tile
     (1, 20000, 16, 2), (4, 7, 5, 5), (2, 50, 8192, 2), (70000, 1, 8, 2), (300, 3, 32, 4), (1, 100, 1030, 2),
 ]
 

@@ -10,9 +10,10 @@
 //   state   (w K)^T V, w_j = g^{n-1-j} w K split into three bf16 terms (24
 //           bits), V exact, so the fp32 state keeps fp32 accuracy
 // The decays are applied in fp32 registers; the state lives there too, fp32,
-// for the whole segment.  NT = 1 for bf16 read-outs: P is rounded to bf16 and
-// S to two terms (2^-16), each below the read-out's own rounding.  NT = 3 for
-// fp32 read-outs: three terms of both.
+// for the whole segment.  NT = 2 for bf16 read-outs: P and S are kept to 16 bits
+// each (2^-16 of a term against the read-out's own rounding of 2^-8; with P in
+// one term, 2^-8 of every term, the read-outs were 1.2 times as far from the
+// exact ones as their rounding alone).  NT = 3 for fp32 read-outs: 24 bits.
 //
 // TMEM (256 columns): scores, then P in place, then the state's product, in 128
 // columns; inter and intra read-outs 64 columns each.
@@ -90,9 +91,9 @@ struct StatePart {
 template <int NT>
 struct Smem {   // byte offsets from a 1024-byte aligned base
   static constexpr int q = 0, k = q + KB * TILE, v = k + KB * TILE, k1 = v + TILE, k2 = k1 + KB * TILE,
-                       s = k2 + KB * TILE, NS = NT == 1 ? 2 : 3, s_tile = KB * 64 * 128,
-                       y = NT == 1 ? s + NS * s_tile : q,   // read-outs: a tile of their own, or q's once it is read
-                       pw = NT == 1 ? y + TILE : s + NS * s_tile, bars = pw + (C + 4) * 4, end = bars + 64;
+                       s = k2 + KB * TILE, NS = NT == 2 ? 2 : 3, s_tile = KB * 64 * 128,
+                       y = NT == 2 ? s + NS * s_tile : q,   // read-outs: a tile of their own, or q's once it is read
+                       pw = NT == 2 ? y + TILE : s + NS * s_tile, bars = pw + (C + 4) * 4, end = bars + 64;
 };
 
 template <int NT, typename TO>
@@ -203,7 +204,7 @@ __global__ void __launch_bounds__(NTHR, 1)
         for (int ks = 0; ks < 4 * KB; ++ks)
           tc::mma_f16(tm, tc::sdesc_sw128(base + L::q + (ks / 4) * TILE) + (ks % 4) * (32 >> 4),
                       tc::sdesc_sw128(base + L::k + (ks / 4) * TILE) + (ks % 4) * (32 >> 4), idesc, ks > 0 ? 1u : 0u);
-        if constexpr (NT == 1) mma_inter();
+        if constexpr (NT == 2) mma_inter();
         tc::mma_commit(bars + 2);
       }
       __syncwarp();
@@ -266,7 +267,7 @@ __global__ void __launch_bounds__(NTHR, 1)
     tc::fence_after_sync();
     if (warp == 0) {
       if (tc::elect()) {
-        if constexpr (NT == 1)
+        if constexpr (NT == 2)
           if (t0 + C < t_live) load_q(t0 + C);   // scores and Q S have read q
         const uint32_t idesc = tc::idesc_f16(C, SL, 1, 0, 1);
         const uint64_t vd = tc::sdesc_sw128(base + L::v, TILE);
@@ -537,7 +538,7 @@ cudaError_t tc_launch(const Geom& g, const Ptrs& p, bool y_bf16, int* status, cu
     e = scan_launch(g, p, st);
     if (e != cudaSuccess) return e;
   }
-  return y_bf16 ? launch_out<1, bf16>(mq, mk, mv, my, g, p, status, st)
+  return y_bf16 ? launch_out<2, bf16>(mq, mk, mv, my, g, p, status, st)
                 : launch_out<3, float>(mq, mk, mv, my, g, p, status, st);
 }
 

@@ -21,7 +21,7 @@
 // scores have to leave TMEM, be weighted and split before P V can start, and the
 // stage is free only when its read-outs, formed in the q and k tiles, have left.
 // 16 x 131072 tokens, d 64, fp32 y: 390 us (state pass 102, scan 7, read-outs
-// 290); 4 x 8 x 4096, bf16: 33 us.
+// 290); 4 x 8 x 4096, bf16: 34 us (33 with P in one term).
 #include <algorithm>
 
 #include "decay_tc_dev.cuh"
@@ -41,7 +41,7 @@ constexpr int kInlineScan = 4;
 
 template <int NT>
 struct Smem {
-  static constexpr int k0 = STAGES * STAGE, s = k0 + 3 * TILE, NS = NT == 1 ? 2 : 3, s_tile = 64 * 128,
+  static constexpr int k0 = STAGES * STAGE, s = k0 + 3 * TILE, NS = NT == 2 ? 2 : 3, s_tile = 64 * 128,
                        pw = s + NS * s_tile, rev = pw + (C + 4) * 4, bars = rev + 32 * 4, end = bars + 24 * 8;
 };
 
@@ -194,15 +194,15 @@ __global__ void __launch_bounds__(NTHR, 1)
         if (!(ok = all_wait(K, c & 1) && (c == 0 || all_wait(DSFREE, (c - 1) & 1)))) return;
         tc::fence_after_sync();
         if (tc::elect()) {
-          mma_state_t<NT == 1 ? 2 : 1>(tDS, base + L::k0, vt, false);
+          mma_state_t<NT == 2 ? 2 : 1>(tDS, base + L::k0, vt, false);
           tc::mma_commit(bars + DS);
         }
         __syncwarp();
       };
       // NT = 3 holds its stages longer, so the next chunk's copies come later:
-      // scores first cost it 3 % (417 against 405 us at 16 x 131072 tokens); NT = 1
+      // scores first cost it 3 % (417 against 405 us at 16 x 131072 tokens); NT = 2
       // waits for the keys instead (36 against 34 us at 32 x 4096 tokens)
-      if constexpr (NT == 1) {
+      if constexpr (NT == 2) {
         next_scores();
         if (ok) state_product();
       } else {
@@ -303,7 +303,7 @@ __global__ void __launch_bounds__(NTHR, 1)
     for (int c = 0; c < chunks; ++c) {
       const uint32_t sc = tSC + 128 * (c & 1) + lanes;
       // the scores; the third term's columns are the last chunk's until its P V is done
-      if (!(ok = all_wait(SC + (c & 1), (c >> 1) & 1) && (NT == 1 || c == 0 || all_wait(PV, (c - 1) & 1)))) break;
+      if (!(ok = all_wait(SC + (c & 1), (c >> 1) & 1) && (NT == 2 || c == 0 || all_wait(PV, (c - 1) & 1)))) break;
       tc::fence_after_sync();
       // 16 columns a turn: with everything unrolled the kernel's code overran the
       // instruction caches (4.6 of 11 cycles per instruction were spent on that)
@@ -412,12 +412,12 @@ __global__ void __launch_bounds__(NTHR, 1)
       {
         const float f = pw[tokens(c)];
 #pragma unroll
-        for (int t = (NT == 1 ? 1 : 0); t >= 0; --t) {   // the product's blocks
+        for (int t = (NT == 2 ? 1 : 0); t >= 0; --t) {   // the product's blocks
           float d[32];
           tc::tmem_ld16_x2(at + 64 * t, d);
           tc::tmem_ld16_x2(at + 64 * t + 32, d + 16);
           tc::tmem_ld_wait32(d);
-          if (t == (NT == 1 ? 1 : 0)) {
+          if (t == (NT == 2 ? 1 : 0)) {
 #pragma unroll
             for (int i = 0; i < 32; ++i) st[i] = fmaf(f, st[i], d[i]);
           } else {
@@ -623,7 +623,7 @@ cudaError_t ws_launch(const Geom& g, const Ptrs& p, bool y_bf16, int* status, cu
       if (e != cudaSuccess) return e;
     }
   }
-  return y_bf16 ? launch_out<1, bf16>(mq, mk, mv, my, g, p, inline_scan, status, st)
+  return y_bf16 ? launch_out<2, bf16>(mq, mk, mv, my, g, p, inline_scan, status, st)
                 : launch_out<3, float>(mq, mk, mv, my, g, p, inline_scan, status, st);
 }
 

@@ -106,7 +106,7 @@ __global__ void __launch_bounds__(256) k_linear_rows(int M, int K, int N, int kp
       }
     }
     if (bias) t += bias[c];
-    t = act == ATLAS_ACT_SILU ? activate<ATLAS_ACT_SILU>(t) : act == ATLAS_ACT_GELU ? activate<ATLAS_ACT_GELU>(t) : t;
+    linear::act_run<TO, 1>(act, &t);
     if (residual) t += to_f32(residual[(size_t)m * N + c]);
     y[(size_t)m * N + c] = from_f32<TO>(t);
   }

@@ -42,3 +42,63 @@ def test_decay_bf16_readouts_carry_only_their_own_rounding(gpu_lib, dims, B, T):
     ours, rounding = _rms(_host(out["y"][:rows]) - y), _rms(_bf16(y) - y)
     print(f"{ours:.3e} rounding {rounding:.3e}")
     assert ours <= 1.02 * rounding
+
+
+# ------------------------------------------------------------- activations
+def _check_tails(y, z, act):
+    """bf16 results of act(z), element by element, so that the tail counts: the
+    formulas are within 4e-4 of the value (GELU to z = -12; SiLU's exponent,
+    rounded to 2^-24 of 115 at z = -80, within 6e-6), and rounding is monotone, so
+    a result lies between the rounded ends of that interval."""
+    import math
+    z = z.double().numpy()
+    want = z * 0.5 * np.vectorize(math.erfc)(-z / math.sqrt(2.0)) if act == "gelu" else z / (1.0 + np.exp(-z))
+    lo, hi = _bf16(want - 4e-4 * np.abs(want)), _bf16(want + 4e-4 * np.abs(want))
+    bad = (y < lo) | (y > hi)
+    at = np.argwhere(bad)
+    assert not bad.any(), [(z[i[-1]], y[tuple(i)], want[i[-1]]) for i in at[:3]]
+
+
+@pytest.mark.parametrize("act,lo", [("gelu", -12.0), ("silu", -80.0)])
+@pytest.mark.parametrize("M", [1, 3, 40])
+def test_linear_activation_tails(gpu_lib, act, lo, M):
+    """z is the bias itself (x is zero)."""
+    import torch
+    from test_learned_neural_gb300.runner import Linear
+    N = 4096
+    z = torch.linspace(lo, 6.0, N)
+    op = Linear(16, N, act)
+    y = op.forward(dict(x=torch.zeros(M, 16, dtype=torch.bfloat16, device="cuda"),
+                        W=torch.ones(16, N, dtype=torch.bfloat16, device="cuda"), bias=z.cuda()))["y"]
+    torch.cuda.synchronize()
+    op.status()
+    _check_tails(_host(y), z, act)
+
+
+@pytest.mark.parametrize("act,lo", [("gelu", -12.0), ("silu", -80.0)])
+@pytest.mark.parametrize("S", [1, 200])
+def test_norm_activation_tails(gpu_lib, act, lo, S):
+    """The same behind the norm: x is zero, so z is the bias."""
+    import torch
+    from test_learned_neural_gb300.runner import GroupNorm
+    C = 4096
+    z = torch.linspace(lo, 6.0, C)
+    op = GroupNorm(C, C // 64, act, x_dtype="f32", y_dtype="bf16")
+    y = op.forward(dict(x=torch.zeros(2, S, C, device="cuda"), bias=z.cuda()))["y"]
+    torch.cuda.synchronize()
+    _check_tails(_host(y).reshape(-1, C), z, act)
+
+
+@pytest.mark.parametrize("act", ["gelu", "silu"])
+@pytest.mark.parametrize("M", [2, 40])
+def test_linear_activation_of_non_finite_values(gpu_lib, act, M):
+    """act(inf) = inf; NaN stays NaN; -inf gives NaN as the formulas do (-inf * 0)."""
+    import torch
+    from test_learned_neural_gb300.runner import Linear
+    z = torch.tensor([float("inf"), float("nan"), float("-inf"), 3e38, -3e38, 0.0, 1.0, -1.0])
+    op = Linear(16, 8, act)
+    y = _host(op.forward(dict(x=torch.zeros(M, 16, dtype=torch.bfloat16, device="cuda"),
+                              W=torch.ones(16, 8, dtype=torch.bfloat16, device="cuda"), bias=z.cuda()))["y"])
+    op.status()
+    assert np.isposinf(y[:, 0]).all() and np.isnan(y[:, 1:3]).all()
+    assert (y[:, 3] > 2.9e38).all() and np.isfinite(y[:, 3]).all() and (y[:, 4] == 0).all() and (y[:, 5] == 0).all()

@@ -75,7 +75,9 @@ __device__ __forceinline__ Tile tile_at(int t, int ntm, int ntn) {
   return {(first + r % h) * BM, r / h * BN};
 }
 
-template <typename TO, int BN>
+// SUM: K in passes, added up in the epilogue's registers (blocks_per_pass); else
+// the whole of K (of a split) in one accumulator.
+template <typename TO, int BN, bool SUM>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHR, 1)
     k_linear_pair(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
                   const __grid_constant__ CUtensorMap map_r, const __grid_constant__ CUtensorMap map_y, Params p) {
@@ -232,13 +234,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHR, 1)
       ask(at, ac);
     };
     if (fetch) ask(first, 0);
-    // fp32 results: the sums of the passes before the tile's last
-    constexpr int NSUM = sizeof(TO) == 4 ? HALF : 1;
+    // the sums of the passes before the tile's last
+    constexpr int NSUM = SUM ? HALF : 1;
     float sums[NSUM];
     for (int t = first; t < ntiles; t += step, ++n) {
       int m, cbeg;
       part_of(t, m, cbeg);
-      if constexpr (sizeof(TO) == 4) {
+      if constexpr (SUM) {
 #pragma unroll
         for (int j = 0; j < NSUM; ++j) sums[j] = 0.f;
         const int k_lo = t / nmn * p.kper, passes = (min(p.kper, p.nk - k_lo) + p.kc - 1) / p.kc;
@@ -267,9 +269,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHR, 1)
       tc::fence_after_sync();
       const uint32_t col0 = tacc + a * BN + lane_base + half * HALF;
       if (m < p.M && p.tma_out) {
-        // bf16: the next block's accumulator and bias are on their way while this
-        // one is worked on; fp32 has no registers left for that
-        constexpr int AHEAD = sizeof(TO) == 2 ? 1 : 0;
+        // the next block's accumulator and bias are on their way while this one is
+        // worked on; the sums leave no registers for that
+        constexpr int AHEAD = SUM ? 0 : 1;
         float v[1 + AHEAD][CW], bias[AHEAD ? CW : 1];
         auto fetch_block = [&](int c, float* vv) {
           if constexpr (CW == 32)
@@ -379,7 +381,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHR, 1)
           tc::tmem_ld_wait16(v);
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
-            if constexpr (sizeof(TO) == 4) v[j] += sums[c + j];
+            if constexpr (SUM) v[j] += sums[c + j];
             st[lane * 17 + j] = v[j];
           }
           __syncwarp();
@@ -449,20 +451,24 @@ int split_cols(int N) { return (N + 3) / 4 * 4; }
 // How many blocks of 64 of K go into one accumulator.  The tensor cores cut
 // off, they do not round: an fp32 accumulator loses about 1.1e-9 of the result
 // per value of K (measured: 4.8e-7 at K = 517, 9.1e-6 at 8192).  fp32 results
-// take K in passes of 512, added up in registers; three planes in passes of
-// 256, each with its five small products first.  bf16 results round at 2^-9.
-int blocks_per_pass(const linear::TcCall& c, int nk) {
-  return c.out_bf16 && c.planes == 1 ? nk : std::min(nk, c.planes == 1 ? 8 : 4);
+// take K in passes of 512, added up in registers; fp32 inputs, whatever the
+// results' type, in passes of 256, each with its five small products first.
+// bf16 inputs with bf16 results, rounded at 2^-9, take all of K at once.
+// Only the kernel with SUM adds passes up: the host and the kernel's template
+// have to agree on this.
+template <bool SUM>
+int blocks_per_pass(int planes, int nk) {
+  return SUM ? std::min(nk, planes == 1 ? 8 : 4) : nk;
 }
 
-template <typename TO, int BN>
+template <typename TO, int BN, bool SUM>
 cudaError_t launch_pair(const linear::TcCall& c, cudaStream_t st) {
   CUtensorMap mx, mw, mr, my;
   if (!tc::tensor_map_2d(&mx, c.x, true, (uint64_t)c.planes * c.M, c.K, (uint64_t)c.ldx * 2, BM / 2) ||
       !tc::tensor_map_2d(&mw, c.W, true, (uint64_t)c.planes * c.K, c.N, (uint64_t)c.ldw * 2, BK))
     return cudaErrorInvalidValue;
   const int nk = (c.K + BK - 1) / BK, kper = (nk + c.splits - 1) / c.splits;
-  Params p{c.M, c.N, nk, blocks_per_pass(c, nk), c.planes, c.K, c.act, kper, 0, c.bias, c.residual, c.y, 0, c.status};
+  Params p{c.M, c.N, nk, blocks_per_pass<SUM>(c.planes, nk), c.planes, c.K, c.act, kper, 0, c.bias, c.residual, c.y, 0, c.status};
   uint64_t rows = c.M;
   if (c.splits > 1) {
     p.split_rows = split_rows(c.M);
@@ -474,7 +480,7 @@ cudaError_t launch_pair(const linear::TcCall& c, cudaStream_t st) {
               tc::tensor_map_2d(&mr, c.residual ? c.residual : c.y, sizeof(TO) == 2, c.M, c.N, row, 32, 64);
   if (c.splits > 1 && !p.tma_out) return cudaErrorInvalidValue;
   if (!p.tma_out) mr = my = mx;   // not used
-  auto kern = k_linear_pair<TO, BN>;
+  auto kern = k_linear_pair<TO, BN, SUM>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<BN>::SMEM);
   if (e != cudaSuccess) return e;
   const long long tiles = (long long)((c.M + BM - 1) / BM) * ((c.N + BN - 1) / BN) * c.splits;
@@ -508,7 +514,7 @@ cudaError_t tc_big(const TcCall& c, cudaStream_t st) {
   if (c.splits > 1) {
     TcCall part = c;
     part.bias = nullptr, part.residual = nullptr, part.y = c.split_ws, part.act = ATLAS_ACT_NONE, part.out_bf16 = 0;
-    cudaError_t e = launch_pair<float, 128>(part, st);
+    cudaError_t e = launch_pair<float, 128, true>(part, st);
     if (e != cudaSuccess) return e;
     const int cols = split_cols(c.N);
     const unsigned grid = (unsigned)(((size_t)c.M * (cols / 4) + 255) / 256);
@@ -525,8 +531,12 @@ cudaError_t tc_big(const TcCall& c, cudaStream_t st) {
   const long long pairs = layer::sm_count() / 2, tm = (c.M + BM - 1) / BM;
   const long long wide = (tm * ((c.N + 255) / 256) + pairs - 1) / pairs * 2,
                   narrow = (tm * ((c.N + 127) / 128) + pairs - 1) / pairs;
-  if (13 * narrow < 10 * wide) return c.out_bf16 ? launch_pair<bf16, 128>(c, st) : launch_pair<float, 128>(c, st);
-  return c.out_bf16 ? launch_pair<bf16, 256>(c, st) : launch_pair<float, 256>(c, st);
+  auto go = [&](auto bn) {
+    constexpr int BN = decltype(bn)::value;
+    if (!c.out_bf16) return launch_pair<float, BN, true>(c, st);
+    return c.planes > 1 ? launch_pair<bf16, BN, true>(c, st) : launch_pair<bf16, BN, false>(c, st);
+  };
+  return 13 * narrow < 10 * wide ? go(std::integral_constant<int, 128>()) : go(std::integral_constant<int, 256>());
 }
 
 }  // namespace linear

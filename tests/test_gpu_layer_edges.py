@@ -102,3 +102,50 @@ def test_linear_activation_of_non_finite_values(gpu_lib, act, M):
     op.status()
     assert np.isposinf(y[:, 0]).all() and np.isnan(y[:, 1:3]).all()
     assert (y[:, 3] > 2.9e38).all() and np.isfinite(y[:, 3]).all() and (y[:, 4] == 0).all() and (y[:, 5] == 0).all()
+
+
+# ---------------------------------------------------------- matrix product
+def _linear_check(M, K, N, act, in_dtype, out_dtype, bias, residual, inplace=False):
+    import torch
+    from test_learned_neural_gb300.runner import Linear
+    g = torch.Generator().manual_seed(31)
+    x = torch.randn(M, K, generator=g).to(_dt(in_dtype)).cuda()
+    W = (torch.randn(K, N, generator=g) / K ** 0.5).to(_dt(in_dtype)).cuda()
+    b = torch.randn(N, generator=g).cuda() if bias else None
+    r = torch.randn(M, N, generator=g).to(_dt(out_dtype)).cuda() if residual else None
+    ref = layer.linear(_host(x), _host(W), _host(b), _host(r), act)
+    op = Linear(K, N, act, in_dtype, out_dtype)
+    y = op.forward(dict(x=x, W=W, bias=b, residual=r), out=dict(y=r) if inplace else None)["y"]
+    torch.cuda.synchronize()
+    op.status()
+    err = maxrel(_host(y), ref)
+    print(f"path {op.last_path()} {err:.2e}")
+    assert err <= TOL[out_dtype], err
+
+
+# few rows; one pass of 256 of K, exactly two, three and a rest; a row length off 16 bytes; one tile per pair and
+# several, narrow and wide; K split over the idle blocks
+F32_TO_BF16 = [
+    (3, 517, 264), (40, 100, 72), (40, 256, 136), (300, 512, 768), (300, 700, 1031), (1999, 517, 1031), (700, 2100, 1160),
+    (4200, 520, 1300), (4200, 600, 2048), (40, 8192, 136), (128, 4096, 256),
+]
+
+
+@pytest.mark.parametrize("case", F32_TO_BF16, ids=str)
+@pytest.mark.parametrize("act,bias,residual", [("none", False, False), ("silu", True, True)])
+def test_linear_fp32_to_bf16(gpu_lib, case, act, bias, residual):
+    _linear_check(*case, act, "f32", "bf16", bias, residual)
+
+
+@pytest.mark.parametrize("T", [1, 7, 300, 2000])
+@pytest.mark.parametrize("dims", [(64, 64), (200, 65)], ids=str)
+def test_decay_fp32_to_bf16(gpu_lib, T, dims):
+    import torch
+    from test_learned_neural_gb300.runner import DecayAttention
+    dk, dv = dims
+    t = _decay_inputs(2, 2, T, dk, dv, "f32", 1, "heads", False, True, seed=22)
+    op = DecayAttention(2, dk, dv, qkv_dtype="f32", y_dtype="bf16")
+    out = op.forward(t)
+    torch.cuda.synchronize()
+    y, S = _decay_ref(t, "heads", "heads")
+    assert maxrel(_host(out["y"]), y) <= TOL["bf16"] and maxrel(_host(out["S"]), S) <= TOL_DECAY["f32"]

@@ -474,7 +474,7 @@ __global__ void __launch_bounds__(256, 4) k_norm_cluster(Geom g, const TI* x, co
 
 constexpr int kMaxRun = 1024;             // widest run held in a warp's registers
 constexpr int kKeep = 8;                  // vectors per thread of k_norm_cluster
-constexpr int kTileBytes = 48 * 1024;     // most shared memory of k_norm_tile's block
+constexpr int kTileBytes = 48 * 1024;     // most dynamic shared memory of k_norm_tile's block
 
 struct Plan {
   int kind;              // 0 run, 1 tile, 2 two passes, 3 cluster
@@ -633,9 +633,13 @@ cudaError_t launch_positions(const Plan& pl, const Geom& g, const atlas_norm_io&
     cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, k_norm_cluster<TI, TO, kKeep>, g, x, io.weight, io.bias, y);
   }
-  if (pl.kind == 1)
-    return tc::launch_overlapped(k_norm_tile<TI, TO, V>, dim3(g.N, 1, pl.tiles), dim3(256), pl.smem, st, g, x,
-                                 io.weight, io.bias, y);
+  if (pl.kind == 1) {
+    auto kern = k_norm_tile<TI, TO, V>;
+    // with the kernel's own 5 KB the largest tiles pass the 48 KB that need no asking
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kTileBytes);
+    if (e != cudaSuccess) return e;
+    return tc::launch_overlapped(kern, dim3(g.N, 1, pl.tiles), dim3(256), pl.smem, st, g, x, io.weight, io.bias, y);
+  }
   const dim3 grid(g.N, g.rb, pl.tiles);
   const cudaError_t e = tc::launch_overlapped(k_norm_stats<TI, V>, grid, dim3(256), 0, st, g, x, part);
   if (e != cudaSuccess) return e;

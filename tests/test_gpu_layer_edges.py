@@ -149,3 +149,26 @@ def test_decay_fp32_to_bf16(gpu_lib, T, dims):
     torch.cuda.synchronize()
     y, S = _decay_ref(t, "heads", "heads")
     assert maxrel(_host(out["y"]), y) <= TOL["bf16"] and maxrel(_host(out["S"]), S) <= TOL_DECAY["f32"]
+
+
+# -------------------------------------------------------------- group norm
+def _norm_check(N, S, C, G, x_dtype, act="none", y_dtype=None, rows=None):
+    import torch
+    from test_learned_neural_gb300.runner import GroupNorm
+    y_dtype = y_dtype or x_dtype
+    g = torch.Generator().manual_seed(41)
+    x = (torch.randn(N, S, C, generator=g) * 1.5 + 0.3).to(_dt(x_dtype)).cuda()
+    w, b = (1 + 0.2 * torch.randn(C, generator=g)).cuda(), (0.2 * torch.randn(C, generator=g)).cuda()
+    y = GroupNorm(C, G, act, x_dtype=x_dtype, y_dtype=y_dtype).forward(dict(x=x, weight=w, bias=b))["y"]
+    torch.cuda.synchronize()
+    pick = slice(None) if rows is None else rows
+    err = maxrel(_host(y[pick]), layer.group_norm(_host(x[pick]), G, _host(w), _host(b), act))
+    print(f"{err:.2e}")
+    assert err <= TOL[y_dtype], err
+
+
+# the one-read tile kernel around 48 KB of shared memory in all, and at its own limit of 48 KB of samples (then two passes)
+@pytest.mark.parametrize("x_dtype,S", [("f32", S) for S in (42, 43, 44, 45, 48, 49)] +
+                         [("bf16", S) for S in (86, 87, 90, 96, 97)])
+def test_norm_tiles_at_the_shared_memory_limits(gpu_lib, x_dtype, S):
+    _norm_check(200, S, 255, 3, x_dtype, rows=slice(0, 200, 40))

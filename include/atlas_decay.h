@@ -25,6 +25,12 @@
  * fp32.  A handle is not re-entrant: do not call it from two threads or on two
  * streams at once.
  *
+ * Capture: calls may be captured in a CUDA graph, the first one of a size too.
+ * A graph uses the handle's workspace: that stays allocated until the handle is
+ * destroyed (a later call that needs more gets a new one beside it), so a graph
+ * may be replayed as long as the handle lives.  A replay counts as a call on it;
+ * wait for its stream before asking for the status.
+ *
  * Inputs: tokens past lens[b] are never used, whatever they hold.  A NaN or an
  * infinity in a live token reaches nothing but its own row and head (for q and k
  * the value heads that use them), there the later read-outs and the final state
@@ -79,7 +85,8 @@ typedef struct {
 int atlas_decay_create(const atlas_decay_config* cfg, atlas_decay_handle** out);
 
 /* One call; stream is a cudaStream_t (NULL = the default stream).  Grows the
- * handle's workspace to atlas_decay_workspace_bytes on first use (cudaMalloc). */
+ * handle's workspace to atlas_decay_workspace_bytes on first use (cudaMalloc);
+ * the stream of the last call on h must still exist then. */
 int atlas_decay_forward(atlas_decay_handle* h, const atlas_decay_io* io, void* stream);
 
 /* Device workspace a call of this size may need: states at the segment starts

@@ -16,6 +16,12 @@
  * non-finite, not always of the same kind, and no other row).  A handle is not
  * re-entrant: do not call it from two threads or on two streams at once.
  *
+ * Capture: calls may be captured in a CUDA graph, the first one of a size too.
+ * A graph uses the handle's workspace: that stays allocated until the handle is
+ * destroyed (a later call that needs more gets a new one beside it), so a graph
+ * may be replayed as long as the handle lives.  A replay counts as a call on it;
+ * wait for its stream before asking for the status.
+ *
  * Errors: the status codes of atlas_mem.h; atlas_linear_last_error gives the
  * message.  Validation failures return before any CUDA call.
  */
@@ -55,7 +61,8 @@ typedef struct {
 int atlas_linear_create(const atlas_linear_config* cfg, atlas_linear_handle** out);
 
 /* One call; stream is a cudaStream_t (NULL = the default stream).  Grows the
- * handle's workspace to atlas_linear_workspace_bytes on first use (cudaMalloc). */
+ * handle's workspace to atlas_linear_workspace_bytes on first use (cudaMalloc);
+ * the stream of the last call on h must still exist then. */
 int atlas_linear_forward(atlas_linear_handle* h, const atlas_linear_io* io, void* stream);
 
 /* Device workspace a call of this size may need. */

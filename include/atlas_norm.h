@@ -20,6 +20,11 @@
  * Execution: asynchronous on the given CUDA stream.  A handle is not
  * re-entrant: do not call it from two threads or on two streams at once.
  *
+ * Capture: calls may be captured in a CUDA graph, the first one of a size too.
+ * A graph uses the handle's workspace: that stays allocated until the handle is
+ * destroyed (a later call that needs more gets a new one beside it), so a graph
+ * may be replayed as long as the handle lives.  A replay counts as a call on it.
+ *
  * Errors: the status codes of atlas_mem.h; atlas_norm_last_error gives the
  * message.  Validation failures return before any CUDA call.
  */
@@ -69,7 +74,8 @@ typedef struct {
 int atlas_norm_create(const atlas_norm_config* cfg, atlas_norm_handle** out);
 
 /* One call; stream is a cudaStream_t (NULL = the default stream).  Grows the
- * handle's workspace to atlas_norm_workspace_bytes on first use (cudaMalloc). */
+ * handle's workspace to atlas_norm_workspace_bytes on first use (cudaMalloc);
+ * the stream of the last call on h must still exist then. */
 int atlas_norm_forward(atlas_norm_handle* h, const atlas_norm_io* io, void* stream);
 
 /* Device workspace a call of this size needs (partial statistics; 0 when a

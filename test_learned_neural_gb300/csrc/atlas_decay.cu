@@ -536,7 +536,7 @@ extern "C" int atlas_decay_forward(atlas_decay_handle* h, const atlas_decay_io* 
   const Plan pl = make_plan(c, io->B, io->T,
                             aligned16(io->q) && aligned16(io->k) && aligned16(io->v) && aligned16(io->y));
   int rc = pl.path == 2 ? h->need_status(st) : ATLAS_OK;
-  if (!rc) rc = h->grow(pl.bytes());
+  if (!rc) rc = h->grow(pl.bytes(), st);
   if (rc) return rc;
 
   Geom g;

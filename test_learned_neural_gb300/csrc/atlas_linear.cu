@@ -303,7 +303,7 @@ extern "C" int atlas_linear_forward(atlas_linear_handle* h, const atlas_linear_i
   if (io->M > most_few_rows(c)) {
     const Operands o = make_operands(c, io->M, aligned16(io->x), aligned16(io->W));
     int rc = h->need_status(st);
-    if (!rc) rc = h->grow(o.x_bytes + o.w_bytes + o.split_bytes);
+    if (!rc) rc = h->grow(o.x_bytes + o.w_bytes + o.split_bytes, st);
     if (rc) return rc;
     char* ws = (char*)h->ws;
     cudaError_t e = cudaSuccess;

@@ -677,7 +677,7 @@ extern "C" int atlas_norm_forward(atlas_norm_handle* h, const atlas_norm_io* io,
     return h->fail(ATLAS_ERR_UNSUPPORTED, "N * S * groups > 2^30 is not supported");
   if (pl.kind && pl.tiles > 65535) return h->fail(ATLAS_ERR_UNSUPPORTED, "too many groups for statistics over positions");
   cudaStream_t st = (cudaStream_t)stream;
-  const int rc = h->grow(pl.kind == 2 ? atlas_norm_workspace_bytes(h, io->N, io->S) : 0);
+  const int rc = h->grow(pl.kind == 2 ? atlas_norm_workspace_bytes(h, io->N, io->S) : 0, st);
   if (rc) return rc;
   const Geom g{io->N, io->S, c.C, c.groups, c.C / c.groups, c.eps, pl.rb, pl.rows, pl.gpt, pl.tpr, pl.rl, c.act, 1.f / (float)(c.C / c.groups)};
   const bool ib = c.x_dtype == ATLAS_BF16, ob = c.y_dtype == ATLAS_BF16;

@@ -9,6 +9,7 @@
 #include <stdio.h>
 
 #include <string>
+#include <vector>
 
 #include "../../include/atlas_norm.h"
 
@@ -129,14 +130,38 @@ inline bool act_ok(int a) { return a == ATLAS_ACT_NONE || a == ATLAS_ACT_SILU ||
 inline size_t dtype_size(int t) { return t == ATLAS_BF16 ? 2 : 4; }
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
-// Message and workspace of a handle.
+// Message and workspace of a handle.  A captured graph holds the workspace's
+// address, so a workspace that a capture has recorded is never freed before the
+// handle: a later call that needs more gets a new one beside it.
 struct HandleBase {
   void* ws = nullptr;
   size_t ws_bytes = 0;
+  bool ws_captured = false;    // a capture has recorded ws
+  std::vector<void*> kept;     // earlier workspaces, freed with the handle
   int* status = nullptr;       // device status word, made with the first call that needs one
   cudaStream_t last_stream = nullptr;
   bool launched = false;
   std::string err;
+
+  // While a capture records, allocations are allowed in the relaxed mode only.
+  struct Relaxed {
+    bool on;
+    cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+    explicit Relaxed(bool capturing) : on(capturing) {
+      if (on) cudaThreadExchangeStreamCaptureMode(&mode);
+    }
+    ~Relaxed() {
+      if (on) cudaThreadExchangeStreamCaptureMode(&mode);
+    }
+  };
+  static bool capturing(cudaStream_t st) {
+    cudaStreamCaptureStatus s = cudaStreamCaptureStatusNone;
+    if (cudaStreamIsCapturing(st, &s) != cudaSuccess) {
+      cudaGetLastError();
+      return false;
+    }
+    return s != cudaStreamCaptureStatusNone;
+  }
 
   int fail(int code, const char* fmt, ...) {
     char buf[512];
@@ -150,35 +175,66 @@ struct HandleBase {
   int cuda_fail(const char* what, cudaError_t e) {
     return fail(ATLAS_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
   }
-  int grow(size_t need) {
-    if (ws_bytes >= need) return ATLAS_OK;
-    if (ws) {
-      // the last call may still read the old one
-      const cudaError_t e = cudaStreamSynchronize(last_stream);
-      if (e != cudaSuccess) return cuda_fail("cudaStreamSynchronize", e);
-      cudaFree(ws);
+  // a workspace of `need` bytes for a call on st
+  int grow(size_t need, cudaStream_t st) {
+    if (need == 0) return ATLAS_OK;
+    const bool cap = capturing(st);
+    if (ws_bytes < need) {
+      if (ws && (ws_captured || cap)) {   // (during a capture nothing can be waited for)
+        try {
+          kept.push_back(ws);
+        } catch (...) {
+          return fail(ATLAS_ERR_OOM, "out of host memory");
+        }
+      } else if (ws) {
+        // the last call may still read the old one
+        const cudaError_t e = cudaStreamSynchronize(last_stream);
+        if (e != cudaSuccess) return cuda_fail("cudaStreamSynchronize", e);
+        cudaFree(ws);
+      }
       ws = nullptr;
       ws_bytes = 0;
+      ws_captured = false;
+      const Relaxed relaxed(cap);
+      const cudaError_t e = cudaMalloc(&ws, need);
+      if (e != cudaSuccess) {
+        cudaGetLastError();
+        ws = nullptr;
+        return fail(ATLAS_ERR_OOM, "cudaMalloc(%zu) failed: %s", need, cudaGetErrorString(e));
+      }
+      ws_bytes = need;
     }
-    const cudaError_t e = cudaMalloc(&ws, need);
-    if (e != cudaSuccess) {
-      cudaGetLastError();
-      ws = nullptr;
-      return fail(ATLAS_ERR_OOM, "cudaMalloc(%zu) failed: %s", need, cudaGetErrorString(e));
-    }
-    ws_bytes = need;
+    ws_captured |= cap;
     return ATLAS_OK;
   }
   int need_status(cudaStream_t st) {
     if (status) return ATLAS_OK;
-    cudaError_t e = cudaMalloc(&status, 256);
+    const bool cap = capturing(st);
+    const Relaxed relaxed(cap);
+    int* made = nullptr;
+    cudaError_t e = cudaMalloc(&made, 256);
     if (e != cudaSuccess) {
       cudaGetLastError();
-      status = nullptr;
       return fail(ATLAS_ERR_OOM, "cudaMalloc(256) failed: %s", cudaGetErrorString(e));
     }
-    e = cudaMemsetAsync(status, 0, 256, st);
-    return e == cudaSuccess ? ATLAS_OK : cuda_fail("cudaMemsetAsync", e);
+    if (cap) {
+      // zero now and not with every replay: on a stream that no capture sees
+      cudaStream_t side = nullptr;
+      e = cudaStreamCreateWithFlags(&side, cudaStreamNonBlocking);
+      if (e == cudaSuccess) {
+        e = cudaMemsetAsync(made, 0, 256, side);
+        if (e == cudaSuccess) e = cudaStreamSynchronize(side);
+        cudaStreamDestroy(side);
+      }
+    } else {
+      e = cudaMemsetAsync(made, 0, 256, st);
+    }
+    if (e != cudaSuccess) {
+      cudaFree(made);
+      return cuda_fail("cudaMemsetAsync", e);
+    }
+    status = made;
+    return ATLAS_OK;
   }
   int read_status() {
     if (!launched || !status) return ATLAS_OK;
@@ -194,6 +250,7 @@ struct HandleBase {
     return ATLAS_OK;
   }
   ~HandleBase() {
+    for (void* p : kept) cudaFree(p);
     if (ws) cudaFree(ws);
     if (status) cudaFree(status);
   }

@@ -172,3 +172,68 @@ def _norm_check(N, S, C, G, x_dtype, act="none", y_dtype=None, rows=None):
                          [("bf16", S) for S in (86, 87, 90, 96, 97)])
 def test_norm_tiles_at_the_shared_memory_limits(gpu_lib, x_dtype, S):
     _norm_check(200, S, 255, 3, x_dtype, rows=slice(0, 200, 40))
+
+
+# ------------------------------------------------------ graphs and workspaces
+def _ops():
+    """(name, handle, a call of a size on fixed tensors): each call needs a workspace."""
+    import torch
+    from test_learned_neural_gb300.runner import DecayAttention, GroupNorm, Linear
+
+    def decay(op, size, seed):
+        t = _decay_inputs(1, 2, 300 * size, 64, 64, "bf16", 1, "heads", False, True, seed=seed)
+        out = op.alloc_outputs(1, 300 * size, "cuda")
+        return lambda: op.forward(t, out=out), [out["y"], out["S"]]
+
+    def norm(op, size, seed):
+        g = torch.Generator().manual_seed(seed)
+        x = torch.randn(1, 700 * size, 66, generator=g).cuda()
+        out = op.alloc_outputs(1, 700 * size, "cuda")
+        return lambda: op.forward(dict(x=x), out=out), [out["y"]]
+
+    def linear(op, size, seed):
+        g = torch.Generator().manual_seed(seed)
+        x, W = torch.randn(50 * size, 600, generator=g).cuda(), torch.randn(600, 200, generator=g).cuda()
+        out = op.alloc_outputs(50 * size, "cuda")
+        return lambda: op.forward(dict(x=x, W=W), out=out), [out["y"]]
+
+    return {"decay": (lambda: DecayAttention(2, 64, 64), decay), "norm": (lambda: GroupNorm(66, 6, x_dtype="f32"), norm),
+            "linear": (lambda: Linear(600, 200, "none", "f32"), linear)}
+
+
+@pytest.mark.parametrize("warm", [True, False], ids=["after_a_call", "first_call_captured"])
+@pytest.mark.parametrize("name", ["decay", "norm", "linear"])
+def test_graph_survives_a_larger_call(gpu_lib, name, warm):
+    """A graph of a small size, then calls of larger sizes on the same handle (and
+    others on another one, which take the memory that is free): its replays still
+    give the direct call's bits, in any order with captures of the larger sizes."""
+    import torch
+    make, call = _ops()[name]
+    op, other = make(), make()
+    cases = [call(op, size, seed=size) for size in (1, 4, 9)]
+    want = []
+    for size, (run, outs) in zip((1, 4, 9), cases):
+        ref = make()                         # a handle of its own: the captured one has not seen the size
+        direct, o = call(ref, size, seed=size)
+        direct()
+        torch.cuda.synchronize()
+        want.append([t.clone() for t in o])
+    graphs = []
+    for run, _ in cases:
+        if warm:
+            run()
+            torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            run()
+        graphs.append(g)
+        call(other, 4, seed=77)[0]()
+    for k in (0, 2, 1, 0):
+        for t in cases[k][1]:
+            t.zero_()
+        call(other, 9, seed=78)[0]()
+        graphs[k].replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(cases[k][1], want[k])), k
+    if name != "norm":
+        op.status()

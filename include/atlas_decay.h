@@ -23,7 +23,8 @@
  * with few (row, head) pairs is also split along the tokens (per-segment
  * states, a scan over them, then the read-outs).  States, sums and decays are
  * fp32.  A handle is not re-entrant: do not call it from two threads or on two
- * streams at once.
+ * streams at once.  Its calls are made on one device, which holds their tensors
+ * and is the current one.
  *
  * Capture: calls may be captured in a CUDA graph, the first one of a size too.
  * A graph uses the handle's workspace: that stays allocated until the handle is

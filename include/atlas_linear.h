@@ -14,7 +14,8 @@
  * products, fp32 accumulation.  fp32 inputs: fp32 accuracy (three bf16 planes of
  * each on the tensor cores; a NaN or an infinity in x makes its row of y
  * non-finite, not always of the same kind, and no other row).  A handle is not
- * re-entrant: do not call it from two threads or on two streams at once.
+ * re-entrant: do not call it from two threads or on two streams at once.  Its
+ * calls are made on one device, which holds their tensors and is the current one.
  *
  * Capture: calls may be captured in a CUDA graph, the first one of a size too.
  * A graph uses the handle's workspace: that stays allocated until the handle is

@@ -18,7 +18,8 @@
  * no digits beyond those x itself lacks).
  *
  * Execution: asynchronous on the given CUDA stream.  A handle is not
- * re-entrant: do not call it from two threads or on two streams at once.
+ * re-entrant: do not call it from two threads or on two streams at once.  Its
+ * calls are made on one device, which holds their tensors and is the current one.
  *
  * Capture: calls may be captured in a CUDA graph, the first one of a size too.
  * A graph uses the handle's workspace: that stays allocated until the handle is

@@ -8,6 +8,7 @@
 #include <stdint.h>
 #include <stdio.h>
 
+#include <atomic>
 #include <string>
 #include <vector>
 
@@ -141,6 +142,7 @@ struct HandleBase {
   int* status = nullptr;       // device status word, made with the first call that needs one
   cudaStream_t last_stream = nullptr;
   bool launched = false;
+  int device = -1;             // of ws and status
   std::string err;
 
   // While a capture records, allocations are allowed in the relaxed mode only.
@@ -175,9 +177,21 @@ struct HandleBase {
   int cuda_fail(const char* what, cudaError_t e) {
     return fail(ATLAS_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
   }
+  // The workspace and the status word lie on the device of the call that made
+  // them: later calls that use them have to be made there.
+  int on_device() {
+    int d = 0;
+    const cudaError_t e = cudaGetDevice(&d);
+    if (e != cudaSuccess) return cuda_fail("cudaGetDevice", e);
+    if (device >= 0 && d != device)
+      return fail(ATLAS_ERR_INVALID_ARG, "the handle's workspace is on device %d, the current device is %d", device, d);
+    device = d;
+    return ATLAS_OK;
+  }
   // a workspace of `need` bytes for a call on st
   int grow(size_t need, cudaStream_t st) {
     if (need == 0) return ATLAS_OK;
+    if (const int rc = on_device()) return rc;
     const bool cap = capturing(st);
     if (ws_bytes < need) {
       if (ws && (ws_captured || cap)) {   // (during a capture nothing can be waited for)
@@ -208,6 +222,7 @@ struct HandleBase {
     return ATLAS_OK;
   }
   int need_status(cudaStream_t st) {
+    if (const int rc = on_device()) return rc;
     if (status) return ATLAS_OK;
     const bool cap = capturing(st);
     const Relaxed relaxed(cap);
@@ -256,17 +271,18 @@ struct HandleBase {
   }
 };
 
+// SMs of a device (the same part wherever the library runs; asked once)
 inline int sm_count() {
-  static int sms = 0;
-  if (sms == 0) {
-    int dev = 0, n = 0;
-    if (cudaGetDevice(&dev) == cudaSuccess &&
-        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess && n > 0)
-      sms = n;
-    else
+  static std::atomic<int> sms{0};
+  int n = sms.load(std::memory_order_relaxed);
+  if (n == 0) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0)
       return 152;
+    sms.store(n, std::memory_order_relaxed);
   }
-  return sms;
+  return n;
 }
 
 }  // namespace layer

@@ -189,12 +189,13 @@ def _torch_dtype(t):
     return torch.bfloat16 if t == ATLAS_BF16 else torch.float32
 
 
-def _check(name, t, dtype, shape):
+def _check(name, t, dtype, shape, device):
     """Device address of a tensor of the layer operators, which must have the
-    type and shape that the configuration and the call's sizes give."""
-    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or not t.is_cuda:
-        raise ValueError(f"{name}: want a contiguous CUDA tensor {dtype} {shape}, got {t.dtype} {tuple(t.shape)} on "
-                         f"{t.device}")
+    type and shape that the configuration and the call's sizes give, and lie
+    on the call's device (its index; -1: host tensors, refused)."""
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != device or device < 0:
+        raise ValueError(f"{name}: want a contiguous CUDA tensor {dtype} {shape} on one device with the others, got "
+                         f"{t.dtype} {tuple(t.shape)} on {t.device}")
     return t.data_ptr()
 
 
@@ -202,6 +203,19 @@ def _check(name, t, dtype, shape):
 # Python object for it, 3 us of a serving step's 10 on the host.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
+def _stream_of(device, stream):
+    """The stream of a call whose tensors are on `device`.  The kernels go to
+    the current device: any other would read the tensors' addresses as its own."""
+    now = _current_device()
+    if now != device:
+        raise ValueError(f"the tensors are on cuda:{device}, the current device is cuda:{now}: make the call under "
+                         f"torch.cuda.device({device})")
+    return _raw_stream(device) if stream is None else stream
 
 
 class _Layer:
@@ -254,13 +268,14 @@ class DecayAttention(_Layer):
             (B, T, hq, c.d_k), (B, T, c.H, c.d_v))
         if out is None:
             out = self.alloc_outputs(B, T, q.device)
-        lens, S0, sq, f32 = t.get("lens"), t.get("S0"), (B, c.H, c.d_k, c.d_v), torch.float32
-        io = atlas_decay_io(B, T, _check("q", q, self._qkv, qs), _check("k", t["k"], self._qkv, qs),
-                            _check("v", v, self._qkv, vs), _check("decay", t["decay"], f32, (c.H,)),
-                            None if lens is None else _check("lens", lens, torch.int32, (B,)),
-                            None if S0 is None else _check("S0", S0, f32, sq),
-                            _check("y", out["y"], self._y, self._y_shape(B, T)), _check("S", out["S"], f32, sq))
-        atlas_decay_forward(self.h, io, _raw_stream(q.device.index) if stream is None else stream)
+        lens, S0, sq, f32, dev = t.get("lens"), t.get("S0"), (B, c.H, c.d_k, c.d_v), torch.float32, q.get_device()
+        io = atlas_decay_io(B, T, _check("q", q, self._qkv, qs, dev), _check("k", t["k"], self._qkv, qs, dev),
+                            _check("v", v, self._qkv, vs, dev), _check("decay", t["decay"], f32, (c.H,), dev),
+                            None if lens is None else _check("lens", lens, torch.int32, (B,), dev),
+                            None if S0 is None else _check("S0", S0, f32, sq, dev),
+                            _check("y", out["y"], self._y, self._y_shape(B, T), dev),
+                            _check("S", out["S"], f32, sq, dev))
+        atlas_decay_forward(self.h, io, _stream_of(dev, stream))
         return out
 
     def status(self):
@@ -298,12 +313,12 @@ class GroupNorm(_Layer):
             shape = (N, S, c.C)
         if out is None:
             out = self.alloc_outputs(N, S, x.device)
-        w, b, f32 = t.get("weight"), t.get("bias"), torch.float32
-        io = atlas_norm_io(N, S, _check("x", x, self._x, shape),
-                           None if w is None else _check("weight", w, f32, (c.C,)),
-                           None if b is None else _check("bias", b, f32, (c.C,)),
-                           _check("y", out["y"], self._y, (N, S, c.C)))
-        atlas_norm_forward(self.h, io, _raw_stream(x.device.index) if stream is None else stream)
+        w, b, f32, dev = t.get("weight"), t.get("bias"), torch.float32, x.get_device()
+        io = atlas_norm_io(N, S, _check("x", x, self._x, shape, dev),
+                           None if w is None else _check("weight", w, f32, (c.C,), dev),
+                           None if b is None else _check("bias", b, f32, (c.C,), dev),
+                           _check("y", out["y"], self._y, (N, S, c.C), dev))
+        atlas_norm_forward(self.h, io, _stream_of(dev, stream))
         return out
 
 
@@ -326,12 +341,12 @@ class Linear(_Layer):
         M = x.shape[0]
         if out is None:
             out = self.alloc_outputs(M, x.device)
-        b, r = t.get("bias"), t.get("residual")
-        io = atlas_linear_io(M, _check("x", x, self._in, (M, c.K)), _check("W", t["W"], self._in, (c.K, c.N)),
-                             None if b is None else _check("bias", b, torch.float32, (c.N,)),
-                             None if r is None else _check("residual", r, self._out, (M, c.N)),
-                             _check("y", out["y"], self._out, (M, c.N)))
-        atlas_linear_forward(self.h, io, _raw_stream(x.device.index) if stream is None else stream)
+        b, r, dev = t.get("bias"), t.get("residual"), x.get_device()
+        io = atlas_linear_io(M, _check("x", x, self._in, (M, c.K), dev), _check("W", t["W"], self._in, (c.K, c.N), dev),
+                             None if b is None else _check("bias", b, torch.float32, (c.N,), dev),
+                             None if r is None else _check("residual", r, self._out, (M, c.N), dev),
+                             _check("y", out["y"], self._out, (M, c.N), dev))
+        atlas_linear_forward(self.h, io, _stream_of(dev, stream))
         return out
 
     def status(self):

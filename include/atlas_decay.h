@@ -70,7 +70,7 @@ typedef struct atlas_decay_handle atlas_decay_handle;
 
 /* Tensors of one call, all DEVICE pointers owned by the caller. */
 typedef struct {
-    int B, T;             /* B >= 1, T >= 1; B * H <= 65535 unless T <= 20 */
+    int B, T;             /* B >= 1, 1 <= T <= 2^30; B * H <= 65535 unless T <= 20 */
     const void* q;        /* H / share heads of d_k, qkv_layout, qkv_dtype */
     const void* k;        /* H / share heads of d_k, qkv_layout, qkv_dtype */
     const void* v;        /* H heads of d_v, qkv_layout, qkv_dtype */

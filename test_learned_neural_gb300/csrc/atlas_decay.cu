@@ -16,6 +16,7 @@ using decay::Ptrs;
 namespace {
 
 constexpr int kSlice = 64;         // d_v columns per CTA
+constexpr int kMostTokens = 1 << 30;
 
 // ------------------------------------------------- token by token
 // A CTA holds kSlice columns of one state in registers: thread (rg, c4) rows
@@ -454,7 +455,7 @@ extern "C" int atlas_decay_create(const atlas_decay_config* cfg, atlas_decay_han
 }
 
 extern "C" size_t atlas_decay_workspace_bytes(const atlas_decay_handle* h, int B, int T) {
-  if (!h || B < 1 || T < 1) return 0;
+  if (!h || B < 1 || T < 1 || T > kMostTokens) return 0;
   // the most it can be: tensors at addresses that ask for padded copies
   return make_plan(h->cfg, B, T, false).bytes();
 }
@@ -527,6 +528,8 @@ extern "C" int atlas_decay_forward(atlas_decay_handle* h, const atlas_decay_io* 
     return h->fail(ATLAS_ERR_INVALID_ARG, "q, k, v, decay, y must be non-NULL");
   if (io->y == io->q || io->y == io->k || io->y == io->v)
     return h->fail(ATLAS_ERR_INVALID_ARG, "y must not alias q, k or v");
+  // (the kernels step over the tokens in ints, a segment or a chunk past the end)
+  if (io->T > kMostTokens) return h->fail(ATLAS_ERR_UNSUPPORTED, "T > 2^30 is not supported");
   const long long ctas = (long long)io->B * c.H * ((c.d_v + kSlice - 1) / kSlice);
   if (ctas > 0x7fffffffLL) return h->fail(ATLAS_ERR_UNSUPPORTED, "B * H too large for one call");
   if ((long long)io->B * c.H > 65535 && io->T > most_step_tokens(c, ctas))

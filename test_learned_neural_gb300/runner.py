@@ -192,8 +192,9 @@ def _torch_dtype(t):
 def _check(name, t, dtype, shape, device):
     """Device address of a tensor of the layer operators, which must have the
     type and shape that the configuration and the call's sizes give, and lie
-    on the call's device (its index; -1: host tensors, refused)."""
-    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != device or device < 0:
+    on the call's device (its index; None: there is only one)."""
+    if (t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or not t.is_cuda
+            or device is not None and t.get_device() != device):
         raise ValueError(f"{name}: want a contiguous CUDA tensor {dtype} {shape} on one device with the others, got "
                          f"{t.dtype} {tuple(t.shape)} on {t.device}")
     return t.data_ptr()
@@ -206,11 +207,23 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
 
 
 _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_devices = None
+
+
+def _device_of(t):
+    """Index of a tensor's device; None where there is only one, so that the
+    checks of a serving step's tensors cost nothing there (else 1 us of 7)."""
+    global _devices
+    if _devices is None:
+        _devices = torch.cuda.device_count()
+    return t.get_device() if _devices > 1 else None
 
 
 def _stream_of(device, stream):
     """The stream of a call whose tensors are on `device`.  The kernels go to
     the current device: any other would read the tensors' addresses as its own."""
+    if device is None:
+        return _raw_stream(0) if stream is None else stream
     now = _current_device()
     if now != device:
         raise ValueError(f"the tensors are on cuda:{device}, the current device is cuda:{now}: make the call under "
@@ -268,7 +281,7 @@ class DecayAttention(_Layer):
             (B, T, hq, c.d_k), (B, T, c.H, c.d_v))
         if out is None:
             out = self.alloc_outputs(B, T, q.device)
-        lens, S0, sq, f32, dev = t.get("lens"), t.get("S0"), (B, c.H, c.d_k, c.d_v), torch.float32, q.get_device()
+        lens, S0, sq, f32, dev = t.get("lens"), t.get("S0"), (B, c.H, c.d_k, c.d_v), torch.float32, _device_of(q)
         io = atlas_decay_io(B, T, _check("q", q, self._qkv, qs, dev), _check("k", t["k"], self._qkv, qs, dev),
                             _check("v", v, self._qkv, vs, dev), _check("decay", t["decay"], f32, (c.H,), dev),
                             None if lens is None else _check("lens", lens, torch.int32, (B,), dev),
@@ -313,7 +326,7 @@ class GroupNorm(_Layer):
             shape = (N, S, c.C)
         if out is None:
             out = self.alloc_outputs(N, S, x.device)
-        w, b, f32, dev = t.get("weight"), t.get("bias"), torch.float32, x.get_device()
+        w, b, f32, dev = t.get("weight"), t.get("bias"), torch.float32, _device_of(x)
         io = atlas_norm_io(N, S, _check("x", x, self._x, shape, dev),
                            None if w is None else _check("weight", w, f32, (c.C,), dev),
                            None if b is None else _check("bias", b, f32, (c.C,), dev),
@@ -341,7 +354,7 @@ class Linear(_Layer):
         M = x.shape[0]
         if out is None:
             out = self.alloc_outputs(M, x.device)
-        b, r, dev = t.get("bias"), t.get("residual"), x.get_device()
+        b, r, dev = t.get("bias"), t.get("residual"), _device_of(x)
         io = atlas_linear_io(M, _check("x", x, self._in, (M, c.K), dev), _check("W", t["W"], self._in, (c.K, c.N), dev),
                              None if b is None else _check("bias", b, torch.float32, (c.N,), dev),
                              None if r is None else _check("residual", r, self._out, (M, c.N), dev),

@@ -45,6 +45,7 @@ def no_calls(monkeypatch):
     for op in ("decay", "norm", "linear"):
         monkeypatch.setattr(runner, f"atlas_{op}_forward", lambda *a, op=op: calls.append((op, a[2])))
     monkeypatch.setattr(runner, "_current_device", lambda: 0, raising=False)
+    monkeypatch.setattr(runner, "_devices", 2, raising=False)
     monkeypatch.setattr(runner, "_raw_stream", lambda index: 100 + index)
     return calls
 
@@ -72,3 +73,20 @@ def test_tensors_of_another_device_are_refused(lib, no_calls, op):  # noqa: F811
     with pytest.raises(ValueError):
         call({"all": -1})
     assert len(no_calls) == 2
+
+
+@pytest.mark.parametrize("op", ["decay", "norm", "linear"])
+def test_host_tensors_are_refused_where_there_is_one_device(lib, no_calls, monkeypatch, op):  # noqa: F811
+    monkeypatch.setattr(runner, "_devices", 1)
+    make, ins, outs = _cases()[op]
+    h = make()
+    for name in (*ins, *outs, None):
+        def at(n):
+            return -1 if n == name else 0
+        t, out = {n: Fake(*ins[n], at(n)) for n in ins}, {n: Fake(*outs[n], at(n)) for n in outs}
+        if name is None:
+            h.forward(t, out=out)
+        else:
+            with pytest.raises(ValueError, match="CUDA"):
+                h.forward(t, out=out)
+    assert no_calls == [(op, 100)]

@@ -46,8 +46,8 @@ __device__ __forceinline__ float inv_std(float var, float eps) { return rsqrtf(v
 
 // ------------------------------------------- sets of one run of channels
 // A set is Cg neighbouring values (S = 1, or the heads layout): LPG lanes of
-// a warp hold it in registers, I items of V values each; mean, then the
-// centred sum of squares, by shuffles.  A block takes U x 256 / LPG sets in the
+// a warp hold it in registers, I items of V values each; mean, then the sums of
+// the centred values and of their squares, by shuffles.  A block takes U x 256 / LPG sets in the
 // order of x, all their loads in flight before the first sum.  Heads layout: a
 // block's sets are of one (sample, head), so the lane's weights are loaded once
 // (HEADS), or, where a head has too few positions to fill a block, of any
@@ -100,16 +100,25 @@ __global__ void __launch_bounds__(256) k_norm_run(Geom g, unsigned sets, unsigne
 #pragma unroll
     for (int o = LPG / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     const float mean = s * g.inv_cg;
-    s = 0.f;
+    // the centred values' own mean, what the rounded one is off by, counts where the spread is no larger
+    float q = s = 0.f;
 #pragma unroll
     for (int i = 0; i < I; ++i)
       if ((l + i * LPG) * V < g.Cg)
 #pragma unroll
-        for (int e = 0; e < V; ++e) s += (v[u][i][e] - mean) * (v[u][i][e] - mean);
+        for (int e = 0; e < V; ++e) {
+          const float d = v[u][i][e] - mean;
+          s += d;
+          q = fmaf(d, d, q);
+        }
 #pragma unroll
-    for (int o = LPG / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    for (int o = LPG / 2; o > 0; o >>= 1) {
+      s += __shfl_xor_sync(0xffffffffu, s, o);
+      q += __shfl_xor_sync(0xffffffffu, q, o);
+    }
     if (set >= sets) continue;
-    const float r = inv_std(s * g.inv_cg, g.eps);
+    const float off = s * g.inv_cg, var = fmaf(q, g.inv_cg, -off * off);
+    const float r = inv_std(var < 0.f ? 0.f : var, g.eps), shift = -off * r;
     // heads: (n, head, position) -> (n, position, head)
     TO* row = dst + (KIND == HEADS ? (size_t)set * g.C : (size_t)set * g.Cg);
     if constexpr (KIND == CHANNELS) affine(set % (unsigned)g.G);
@@ -125,7 +134,7 @@ __global__ void __launch_bounds__(256) k_norm_run(Geom g, unsigned sets, unsigne
       float o[V];
 #pragma unroll
       for (int e = 0; e < V; ++e)
-        o[e] = fmaf((v[u][i][e] - mean) * r, w[i][e], b[i][e]);
+        o[e] = fmaf(fmaf(v[u][i][e] - mean, r, shift), w[i][e], b[i][e]);
       store_act<TO, V>(g.act, o, row + c);
     }
   }
@@ -137,7 +146,8 @@ __global__ void __launch_bounds__(256) k_norm_run(Geom g, unsigned sets, unsigne
 
 // mean and centred sum of squares of two disjoint parts (Chan, Golub, LeVeque)
 __device__ __forceinline__ void merge(float& n, float& mean, float& m2, float nb, float meanb, float m2b) {
-  const float t = n + nb, d = meanb - mean, f = t > 0.f ? __fdividef(nb, t) : 0.f;
+  // (the first part comes in as it is: a quotient of 1 - 2^-24 would move its mean)
+  const float t = n + nb, d = meanb - mean, f = n > 0.f ? __fdividef(nb, t) : 1.f;
   mean = fmaf(d, f, mean);
   m2 = fmaf(d * d, n * f, m2 + m2b);
   n = t;

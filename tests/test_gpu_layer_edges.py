@@ -237,3 +237,29 @@ def test_graph_survives_a_larger_call(gpu_lib, name, warm):
         assert all(torch.equal(a, b) for a, b in zip(cases[k][1], want[k])), k
     if name != "norm":
         op.status()
+
+
+@pytest.mark.parametrize("C,G,S,layout", [(48, 1, 1, "channels_last"), (510, 6, 1, "channels_last"), (2000, 2, 1, "channels_last"),
+                                          (96, 2, 200, "heads"), (85, 1, 7, "heads"), (96, 2, 200, "channels_last"),
+                                          (85, 1, 600, "channels_last")])
+@pytest.mark.parametrize("value", [1000.3, -77777.0])
+def test_norm_of_a_large_common_offset(gpu_lib, C, G, S, layout, value):
+    """A set of one value has variance 0: y is the bias, though 1 / sqrt(eps) = 316
+    stands before every error of the mean.  The rounded mean is off by up to a few
+    units in the last place of the value (0.03 at 77777); the centred values' own
+    mean takes that back to 2^-23 of it, 316 times which is 1.2e-6: 1e-5 allowed.
+    With noise of 1 on the offset the result keeps the digits of x: the mean to a
+    few units in the last place, 6 of them allowed."""
+    import torch
+    from test_learned_neural_gb300.runner import GroupNorm
+    N = 3
+    shape = (N, G, S, C // G) if layout == "heads" else (N, S, C)
+    op = GroupNorm(C, G, x_dtype="f32", layout=layout)
+    bias = torch.randn(C, generator=torch.Generator().manual_seed(3)).cuda()
+    flat = op.forward(dict(x=torch.full(shape, value, device="cuda"), bias=bias))["y"]
+    x = (value + torch.randn(shape, generator=torch.Generator().manual_seed(4))).cuda()
+    noisy = op.forward(dict(x=x))["y"]
+    torch.cuda.synchronize()
+    assert float((flat - bias).abs().max()) <= 1e-5
+    ref = layer.group_norm(_host(x), G, layout=layout)
+    assert np.abs(_host(noisy) - ref).max() <= 6 * np.spacing(np.float32(abs(value)))

@@ -54,9 +54,9 @@ __device__ __forceinline__ float inv_std(float var, float eps) { return rsqrtf(v
 // (SHORT_HEADS).
 enum Sets { CHANNELS, HEADS, SHORT_HEADS };
 template <typename TI, typename TO, int V, int LPG, int I, int U, Sets KIND>
-__global__ void __launch_bounds__(256) k_norm_run(Geom g, unsigned sets, unsigned blocks, const TI* __restrict__ x,
+__global__ void __launch_bounds__(256) k_norm_run(Geom g, unsigned sets, unsigned blocks, const TI* x,
                                                   const float* __restrict__ weight, const float* __restrict__ bias,
-                                                  TO* __restrict__ y) {
+                                                  TO* y) {   // y may be x
   constexpr int PER = 256 / LPG;
   const int l = threadIdx.x % LPG;
   // heads: `blocks` blocks per (sample, head)

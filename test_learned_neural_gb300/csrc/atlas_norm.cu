@@ -500,7 +500,7 @@ Plan make_plan(const atlas_norm_config& c, int N, int S, bool vec) {
   p.rb = 1;
   p.rows = S;
   if ((S == 1 || c.layout == ATLAS_NORM_HEADS) && Cg <= kMaxRun) return p;
-  // A cluster's registers, where they hold the sample's tile (128 bytes or more
+  // A cluster's registers, where they hold the sample's tile (64 bytes or more
   // of a row, whole groups) and the clusters fill the SMs: x is read once.
   // 8 x 4096 x 1024 bf16, 32 groups: 39 us so, 47 in two passes; 32 x 256 x 512:
   // 12 / 14.  (Sixteen vectors per thread instead of eight: 51 and 84 -> 90 us for
@@ -512,7 +512,7 @@ Plan make_plan(const atlas_norm_config& c, int N, int S, bool vec) {
     q.V = v16;
     q.gpt = std::min(c.groups, (3 + vg) / vg);
     // Wider tiles for few positions, while they fit one block and fill the SMs.
-    // bf16, 128-byte tiles / these: 3000 x 32 x 256, 8 groups 178 / 35 us; 2000 x 64 x
+    // bf16, 64-byte tiles / these: 3000 x 32 x 256, 8 groups 178 / 35 us; 2000 x 64 x
     // 1024, 32 groups 502 / 98; 1200 x 5 x 512, 8 groups 74 / 14.
     while (q.gpt < c.groups) {
       const int more = std::min(2 * q.gpt, c.groups);
@@ -621,8 +621,9 @@ cudaError_t launch_run(const Geom& g, const atlas_norm_io& io, cudaStream_t st) 
   if (items <= 8) return go(k_norm_run<TI, TO, V, 8, 1, 4, KIND>, 128);
   if (items <= 16) return go(k_norm_run<TI, TO, V, 16, 1, 4, KIND>, 64);
   if (items <= 32) return go(k_norm_run<TI, TO, V, 32, 1, 4, KIND>, 32);
-  if (items <= 128) return go(k_norm_run<TI, TO, V, 32, 4, 1, KIND>, 8);
-  return go(k_norm_run<TI, TO, V, 32, 32, 1, KIND>, 8);
+  if constexpr (V == 1)   // (of 8 values a widest set has 128)
+    if (items > 128) return go(k_norm_run<TI, TO, V, 32, 32, 1, KIND>, 8);
+  return go(k_norm_run<TI, TO, V, 32, 4, 1, KIND>, 8);
 }
 
 template <typename TI, typename TO, int V>

@@ -103,7 +103,7 @@ __global__ void __launch_bounds__(256) k_decay_step(Geom g, Ptrs p) {
 // product is a register-tiled fp32 loop over shared-memory tiles.  READ: form
 // the read-outs from the segment-start state; else only the segment's own
 // contribution to the next segment's start.  Bound by the latency of its fp32
-// loops where blocks are few (three per SM at C = 64): 3 rows x 6 heads of ragged
+// loops where blocks are few (chunk_blocks has how many an SM holds): 3 rows x 6 heads of ragged
 // lengths to 1501, d 48: 41 us in three overlapped launches (states 15, scan 8, read-outs 32).
 template <typename TI, typename TO, int C, bool READ>
 __global__ void __launch_bounds__(256, C == 64 ? 3 : 1) k_decay_chunk(Geom g, Ptrs p) {
@@ -336,6 +336,19 @@ size_t chunk_smem(int d_k, bool read) {
   return (C * ldk + C * ldv + dk4 * ldv + C + 4 + (read ? C * ldk + C * (C + 4) : 0)) * sizeof(float);
 }
 
+// Blocks of the fp32 chunks that an SM holds: by their shared memory (228 KB an
+// SM, 1 KB of it kept by the system per block), and three (C = 64) or two by
+// registers.  Read-outs: three to d_k = 48, two to 100, one to 128 (C = 64); two
+// to 188, one beyond (C = 32).  State pass: three to 108, two beyond.  With these
+// against 3, 2 and 1 for d_k to 64, 128 and 256 in both passes, fp32: 1 x 2 heads x
+// 32768 tokens of 64 140 us / 157, of 136 432 / 748, of 256 851 / 916; 4 x 8 x 4096 of
+// 96 645 / 724; of 48 and 128 the same; 3 x 6 x 1501 of 64 75 / 71 (12 segments and
+// 24 cost the same by the formula).
+int chunk_blocks(int d_k, bool read) {
+  const size_t fit = (228 * 1024) / (chunk_smem(d_k, read) + 1024);
+  return (int)std::min<size_t>(chunk_tokens(d_k) == 64 ? 3 : 2, fit);
+}
+
 struct Plan {
   int path, C, slices, nseg, seg;
   bool pad;
@@ -351,13 +364,14 @@ size_t round_256(size_t n) { return (n + 255) / 256 * 256; }
 // block's start and end take `ends` chunks' time, so n is the one with the
 // least of
 //   waves of the read-out pass + waves of the state pass + launches.
-int best_segments(long long ctas, long long chunks, long long slots, double ends) {
+// `slots`, `state_slots`: CTAs of either pass that run at once.
+int best_segments(long long ctas, long long chunks, long long slots, long long state_slots, double ends) {
   long long best = 1;
   double cost = 0;
   for (long long n = 1; n <= std::min(chunks, 1024LL); ++n) {
     const long long per = (chunks + n - 1) / n;
     if (n > 1 && (chunks + per - 1) / per != n) continue;
-    const long long waves = (ctas * n + slots - 1) / slots, before = (ctas * (n - 1) + slots - 1) / slots;
+    const long long waves = (ctas * n + slots - 1) / slots, before = (ctas * (n - 1) + state_slots - 1) / state_slots;
     const double c = (double)waves * (per + ends) + (n > 1 ? 0.4 * before * (per + ends) + ends + 1 : 0);
     if (n == 1 || c < cost) best = n, cost = c;
     if (ctas * n > 4 * slots) break;
@@ -399,11 +413,11 @@ Plan make_plan(const atlas_decay_config& c, int B, int T, bool aligned) {
   pl.pad = tc && (!aligned || c.d_k % 8 || c.d_v % 8);
   pl.path = tc ? 2 : 1;
   pl.C = tc ? decay::kTcChunk : chunk_tokens(c.d_k);
-  // CTAs that run at once: three per SM for the fp32 chunks where their shared
-  // memory allows it, whose chunks take so long that starts hardly count
-  const long long slots = (tc || c.d_k > 128 ? 1 : c.d_k > 64 ? 2 : 3) * sm_count();
+  // CTAs that run at once; a fp32 chunk takes so long that starts hardly count
+  const long long slots = (tc ? 1 : chunk_blocks(c.d_k, true)) * sm_count(),
+                  state_slots = (tc ? 1 : chunk_blocks(c.d_k, false)) * sm_count();
   const long long chunks = (T + pl.C - 1) / pl.C;
-  const long long n = best_segments((long long)B * c.H * pl.slices, chunks, slots, tc ? 2 : 0.5);
+  const long long n = best_segments((long long)B * c.H * pl.slices, chunks, slots, state_slots, tc ? 2 : 0.5);
   pl.seg = (int)((chunks + n - 1) / n * pl.C);
   pl.nseg = (int)((T + pl.seg - 1) / pl.seg);
   if (pl.nseg > 1) pl.seg_bytes = round_256((size_t)B * c.H * pl.nseg * c.d_k * c.d_v * sizeof(float));

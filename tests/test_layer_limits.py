@@ -17,3 +17,17 @@ def test_decay_refuses_tokens_past_its_index_range(lib, T, dtype):  # noqa: F811
     assert tln.atlas_decay_workspace_bytes(h, 1, T) == 0
     assert tln.atlas_decay_workspace_bytes(h, 1, 1 << 30) > 0
     tln.atlas_decay_destroy(h)
+
+
+@pytest.mark.parametrize("d,blocks", [(16, 3), (48, 3), (52, 2), (64, 2), (100, 2), (136, 2), (188, 2)])
+def test_decay_fp32_segments_run_at_once(lib, d, blocks):  # noqa: F811
+    """Few long fp32 rows: as many segments as run at once, by the shared memory
+    that a block of the read-out pass takes (228 KB an SM, 152 SMs): no second
+    round of blocks.  (Where an SM holds one block, to d_k = 128, two rounds of half
+    the length are as good: the state pass still runs in one.)  The workspace holds
+    a state per segment."""
+    h = tln.atlas_decay_create(tln.make_decay_config(H=2, d_k=d, d_v=d, qkv_dtype="f32"))
+    segments = tln.atlas_decay_workspace_bytes(h, 1, 32768) // (2 * d * d * 4)
+    slices = -(-d // 64)
+    assert 0.6 * blocks * 152 <= 2 * slices * segments <= blocks * 152
+    tln.atlas_decay_destroy(h)

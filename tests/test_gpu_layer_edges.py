@@ -263,3 +263,72 @@ def test_norm_of_a_large_common_offset(gpu_lib, C, G, S, layout, value):
     assert float((flat - bias).abs().max()) <= 1e-5
     ref = layer.group_norm(_host(x), G, layout=layout)
     assert np.abs(_host(noisy) - ref).max() <= 6 * np.spacing(np.float32(abs(value)))
+
+
+# ------------------------------------------------- the tensor-core kernels' variants
+# fp32 results at fp32 accuracy, on max|gpu - ref| / max|ref|.  An accumulator loses 1.1e-9 of the result per value of K
+# (tensor cores cut off): 5.6e-7 in a pass of 512, fp32 sums of the passes a few 6e-8 more; 2e-6 allowed.  An operand
+# without its third term (2^-17 of each product, signs at random) or K in one accumulator from 4096 on would exceed it.
+FP32 = 2e-6
+
+
+def _product(M, K, N, act, in_dtype, out_dtype, bias=True, residual=True, inplace=False):
+    import torch
+    from test_learned_neural_gb300.runner import Linear
+    g = torch.Generator().manual_seed(51)
+    x = torch.randn(M, K, generator=g).to(_dt(in_dtype)).cuda()
+    W = (torch.randn(K, N, generator=g) / K ** 0.5).to(_dt(in_dtype)).cuda()
+    b = torch.randn(N, generator=g).cuda() if bias else None
+    r = torch.randn(M, N, generator=g).to(_dt(out_dtype)).cuda() if residual else None
+    ref = layer.linear(_host(x), _host(W), _host(b), _host(r), act)
+    op = Linear(K, N, act, in_dtype, out_dtype)
+    y = op.forward(dict(x=x, W=W, bias=b, residual=r), out=dict(y=r) if inplace else None)["y"]
+    torch.cuda.synchronize()
+    op.status()
+    assert op.last_path() == 1
+    err = maxrel(_host(y), ref)
+    print(f"{err:.2e}")
+    assert err <= (FP32 if out_dtype == "f32" else TOL["bf16"]), err
+
+
+# 17 row tiles (a second band of 16) and more tiles than pairs: 256 columns a tile, 128, and rows off 16 bytes
+@pytest.mark.parametrize("M,K,N", [(4200, 96, 2048), (4200, 96, 1300), (4200, 96, 1301), (4097, 200, 2056)], ids=str)
+@pytest.mark.parametrize("in_dtype,out_dtype", [("bf16", "bf16"), ("bf16", "f32"), ("f32", "f32")])
+@pytest.mark.parametrize("residual", ["none", "own", "in place"])
+def test_linear_several_tiles_per_pair(gpu_lib, M, K, N, in_dtype, out_dtype, residual):
+    _product(M, K, N, "none", in_dtype, out_dtype, N % 2 == 0, residual != "none", residual == "in place")
+
+
+# passes of K: one, a whole number and a rest; with and without a split
+@pytest.mark.parametrize("M,K,N", [(300, 8192, 4096), (300, 517, 264), (40, 8192, 136), (700, 2100, 1160)], ids=str)
+@pytest.mark.parametrize("in_dtype", ["bf16", "f32"])
+def test_linear_fp32_accuracy(gpu_lib, M, K, N, in_dtype):
+    _product(M, K, N, "none", in_dtype, "f32")
+
+
+@pytest.mark.parametrize("dims", [(64, 64), (128, 64), (48, 48)], ids=str)
+@pytest.mark.parametrize("B,T", [(2, 2050), (160, 300)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_decay_fp32_accuracy(gpu_lib, dims, B, T, dtype):
+    """As the product: chunks of at most 128 tokens and 128 keys per accumulator."""
+    import torch
+    from test_learned_neural_gb300.runner import DecayAttention
+    (dk, dv), H = dims, 2
+    t = _decay_inputs(B, H, T, dk, dv, dtype, 1, "heads", False, True, seed=52, gammas=[1.0, 0.97])
+    op = DecayAttention(H, dk, dv, qkv_dtype=dtype, y_dtype="f32")
+    out = op.forward(t)
+    torch.cuda.synchronize()
+    op.status()
+    rows = min(B, 3)
+    y, S = _decay_ref({n: v if n == "decay" else v[:rows] for n, v in t.items()}, "heads", "heads")
+    ey, eS = maxrel(_host(out["y"][:rows]), y), maxrel(_host(out["S"][:rows]), S)
+    print(f"y {ey:.2e} S {eS:.2e}")
+    assert ey <= FP32 and eS <= FP32
+
+
+# clusters of 2, 4 and 8 (both types); groups that do not fill the last tile
+@pytest.mark.parametrize("N,S,C,G", [(40, 500, 256, 8), (40, 900, 256, 8), (20, 1900, 256, 8), (20, 4000, 256, 8),
+                                     (60, 1025, 80, 5), (40, 700, 96, 6)], ids=str)
+@pytest.mark.parametrize("x_dtype,y_dtype,act", [("bf16", "bf16", "silu"), ("f32", "f32", "none"), ("f32", "bf16", "gelu")])
+def test_norm_clusters(gpu_lib, N, S, C, G, x_dtype, y_dtype, act):
+    _norm_check(N, S, C, G, x_dtype, act, y_dtype, rows=slice(0, N, N // 3))

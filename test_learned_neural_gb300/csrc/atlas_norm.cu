@@ -182,8 +182,10 @@ struct Place {
   }
 };
 
-// sums of d and d^2 with d = x - shift, shift a value of the set near its
-// mean's scale (the thread's first), so a common offset cancels before squares
+// Sums of d and d^2 with d = x - shift, shift a value of the set near its
+// mean's scale (the first), so a common offset cancels before squares.  A first
+// value far from the others costs digits, about as many times 2^-24 of its own
+// square as there are values, so no more than kFold vectors come under one shift.
 struct Sums {
   float n = 0.f, shift = 0.f, s = 0.f, q = 0.f;
   uint64_t s2 = 0, q2 = 0;   // two of each at a time
@@ -217,20 +219,40 @@ struct Sums {
   }
 };
 
+// count, mean and centred sum of squares of a thread's values, folded in from
+// Sums every kFold vectors.  A thread's 3760 values behind one of 1000 standard
+// deviations: the sum of squares is off by 3e-3 under a single shift, by 9e-6 so.
+template <int V>
+constexpr int kFold = V == 1 ? 32 : 8;
+struct Moments {
+  float n = 0.f, mean = 0.f, m2 = 0.f;
+  __device__ __forceinline__ void fold(Sums& s) {
+    if (s.n == 0.f) return;
+    float mean_s, m2_s;
+    s.finish(mean_s, m2_s);
+    merge(n, mean, m2, s.n, mean_s, m2_s);
+    s = Sums();
+  }
+  // vector i of those that for_rows brings
+  template <int V>
+  __device__ __forceinline__ void add(Sums& s, int i, const float* v) {
+    s.add<V>(v);
+    if (i % kFold<V> == kFold<V> - 1) fold(s);
+  }
+};
+
 // the lanes that merge `entries` parts of one group: a power of two, at most 32
 __device__ __forceinline__ int lanes_for(int entries) {
   return entries >= 32 ? 32 : entries <= 1 ? 1 : 1 << (32 - __clz(entries - 1));
 }
 
-// the block's threads' sums -> (count, mean, m2) per group of the tile, by a
+// the block's threads' moments -> (count, mean, m2) per group of the tile, by a
 // few lanes per group in a fixed order; out(group, n, mean, m2) once per group
 template <typename F>
-__device__ __forceinline__ void reduce_groups(const Geom& g, const Place& p, const Sums& sums, float* sh, F out) {
-  float mean, m2;
-  sums.finish(mean, m2);
-  sh[threadIdx.x] = p.on ? sums.n : 0.f;
-  sh[256 + threadIdx.x] = mean;
-  sh[512 + threadIdx.x] = m2;
+__device__ __forceinline__ void reduce_groups(const Geom& g, const Place& p, const Moments& own, float* sh, F out) {
+  sh[threadIdx.x] = p.on ? own.n : 0.f;
+  sh[256 + threadIdx.x] = own.mean;
+  sh[512 + threadIdx.x] = own.m2;
   __syncthreads();
   const int width = min(p.vecs, 256), entries = width * g.rl, lanes = lanes_for(entries), per = 256 / lanes;
   const int l = threadIdx.x % lanes;
@@ -287,14 +309,16 @@ __global__ void __launch_bounds__(256, 4) k_norm_stats(Geom g, const TI* __restr
   tc::grid_dependents_launch();
   const int r0 = blk * g.rows + p.row, r1 = min(g.S, (blk + 1) * g.rows);
   Sums sums;
+  Moments own;
   if (p.on && r0 < r1) {
     for (int j = 0; j < p.cnt; ++j) {
       const TI* src = x + (n * g.S + r0) * g.C + p.ch0 + (p.vec0 + j * p.step) * V;
       for_rows<TI, V>(src, (size_t)g.rl * g.C, (r1 - r0 + g.rl - 1) / g.rl,
-                      [&](int, const float* v) { sums.add<V>(v); });
+                      [&](int i, const float* v) { own.add<V>(sums, i, v); });
     }
   }
-  reduce_groups(g, p, sums, sh, [&](int k, float c, float mean, float m2) {
+  own.fold(sums);
+  reduce_groups(g, p, own, sh, [&](int k, float c, float mean, float m2) {
     const int grp = p.tile * g.gpt + k;
     if (grp < g.G) {
       float* d = part + 3 * ((n * g.G + grp) * g.rb + blk);
@@ -377,16 +401,18 @@ __global__ void __launch_bounds__(256) k_norm_tile(Geom g, const TI* x, const fl
   const int per = (g.S + g.rl - 1) / g.rl, rows = (g.S - p.row + g.rl - 1) / g.rl;   // rows per row lane, and of this one
   const size_t step = (size_t)g.rl * g.C;
   Sums sums;
+  Moments own;
   if (p.on && p.row < g.S) {
     for (int j = 0; j < p.cnt; ++j) {
       const TI* src = x + (n * g.S + p.row) * g.C + p.ch0 + (p.vec0 + j * p.step) * V;
       for_rows<TI, V>(src, step, rows, [&](int i, const float* v) {
-        sums.add<V>(v);
+        own.add<V>(sums, i, v);
         store_vec<V>(keep + ((j * per + i) * 256 + threadIdx.x) * V, v);   // exact: v came from TI
       });
     }
   }
-  reduce_groups(g, p, sums, sh, [&](int k, float c, float mean, float m2) {
+  own.fold(sums);
+  reduce_groups(g, p, own, sh, [&](int k, float c, float mean, float m2) {
     st[0][k] = mean, st[1][k] = inv_std(m2 / c, g.eps);
   });
   __syncthreads();
@@ -442,7 +468,10 @@ __global__ void __launch_bounds__(256, 4) k_norm_cluster(Geom g, const TI* x, co
       keep[i].values(v);
       sums.add<V>(v);
     }
-  reduce_groups(g, p, sums, sh, [&](int k, float c, float mean, float m2) {
+  Moments own;   // of R <= kFold vectors
+  own.n = sums.n;
+  sums.finish(own.mean, own.m2);
+  reduce_groups(g, p, own, sh, [&](int k, float c, float mean, float m2) {
     part[0][k] = c, part[1][k] = mean, part[2][k] = m2;
   });
   if (cs > 1) tc::cluster_sync();

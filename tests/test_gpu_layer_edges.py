@@ -332,3 +332,28 @@ def test_decay_fp32_accuracy(gpu_lib, dims, B, T, dtype):
 @pytest.mark.parametrize("x_dtype,y_dtype,act", [("bf16", "bf16", "silu"), ("f32", "f32", "none"), ("f32", "bf16", "gelu")])
 def test_norm_clusters(gpu_lib, N, S, C, G, x_dtype, y_dtype, act):
     _norm_check(N, S, C, G, x_dtype, act, y_dtype, rows=slice(0, N, N // 3))
+
+
+@pytest.mark.parametrize("N,S,C,G,dtype", [(320, 60000, 16, 2, "f32"), (320, 20000, 15, 1, "f32"), (200, 47, 255, 3, "f32"),
+                                           (40, 900, 256, 8, "f32"), (1, 30000, 64, 2, "f32"), (320, 60000, 16, 2, "bf16")])
+def test_norm_behind_an_outlier(gpu_lib, N, S, C, G, dtype):
+    """Position 0 of channel 0 is 1000 standard deviations away (a token that
+    attention collects on): the variance keeps its digits.  Squares of 1000 in
+    blocks of up to 64 values under one shift: 64 of them lose a few 2^-24 of 6e7
+    each, 20 of 1e6 and half of that in the inverse deviation, 1e-5.  The
+    largest value is the outlier's own; the others, of order 1 / (1000 / sqrt(S)), are
+    held to 1e-5 of themselves as a whole."""
+    import torch
+    from test_learned_neural_gb300.runner import GroupNorm
+    g = torch.Generator(device="cuda").manual_seed(61)
+    x = torch.randn(N, S, C, generator=g, device="cuda")
+    x[:, 0, 0] = 1000
+    x = x.to(_dt(dtype))
+    y = GroupNorm(C, G, x_dtype=dtype, y_dtype="f32").forward(dict(x=x))["y"]
+    torch.cuda.synchronize()
+    pick = slice(0, N, max(1, N // 3))
+    got, ref = _host(y[pick]), layer.group_norm(_host(x[pick]), G)
+    for part in (np.s_[:, 0], np.s_[:, 1:]):
+        err = _rms(got[part] - ref[part]) / _rms(ref[part])
+        print(f"{err:.2e}")
+        assert err <= 1e-5

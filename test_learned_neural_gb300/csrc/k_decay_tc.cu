@@ -383,9 +383,7 @@ __global__ void __launch_bounds__(NTHR, 1)
           p.S_out[unit * sq + (size_t)part.row * g.d_v + c0 + part.col + i] = S[i];
     }
   } else if (tid == 0) {
-    // let the copies in flight land before the block's memory is freed
-    tc::wait(bq, ph);
-    tc::wait(bkv, ph);
+    tc::settle();
     atomicExch(status, ATLAS_ERR_TIMEOUT);
   }
   if (tid == 0) tc::bulk_wait_read<0>();
@@ -492,8 +490,7 @@ __global__ void __launch_bounds__(NTHR, 1)
     for (int i = 0; i < StatePart::N; ++i)
       if (part.row < g.d_k && part.col + i < cols) dst[(size_t)part.row * g.d_v + c0 + part.col + i] = d[i];
   } else if (tid == 0) {
-    tc::wait(bfull, 0);
-    tc::wait(bfull + 8, 0);
+    tc::settle();
     atomicExch(status, ATLAS_ERR_TIMEOUT);
   }
   tc::fence_before_sync();

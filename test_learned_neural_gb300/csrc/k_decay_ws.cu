@@ -443,8 +443,7 @@ __global__ void __launch_bounds__(NTHR, 1)
   tc::fence_before_sync();
   __syncthreads();
   if (*failed && tid == 0) {
-    // let the copies in flight land before the block's memory is freed
-    for (int i = 0; i < STAGES; ++i) tc::mbar_wait(bars + FULL + i, 0, tc::kWaitCycles / 16);
+    tc::settle();
     atomicExch(status, ATLAS_ERR_TIMEOUT);
   }
   __syncthreads();
@@ -581,7 +580,7 @@ __global__ void __launch_bounds__(NTHR_STATE, 1)
   tc::fence_before_sync();
   __syncthreads();
   if (*failed && tid == 0) {
-    for (int i = 0; i < STAGES; ++i) tc::mbar_wait(bars + SFULL + i, 0, tc::kWaitCycles / 16);
+    tc::settle();
     atomicExch(status, ATLAS_ERR_TIMEOUT);
   }
   __syncthreads();

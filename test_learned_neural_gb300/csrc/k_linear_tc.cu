@@ -406,8 +406,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHR, 1)
   tc::fence_before_sync();
   __syncthreads();
   if (failed && tid == 0) {
-    // let every copy this CTA issued land before its memory is freed
-    for (int s = 0; s < STAGES; ++s) tc::mbar_wait(&full[s], 0, tc::kWaitCycles / 16);
+    tc::settle();
     atomicExch(p.status, ATLAS_ERR_TIMEOUT);
   }
   __syncthreads();

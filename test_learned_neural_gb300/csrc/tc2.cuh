@@ -75,6 +75,13 @@ static __device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity) {
 __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity) {
   return try_wait(bar, parity) || wait_slow(bar, parity);
 }
+// After a wait gave up: time for the copies and MMAs that are in flight to end,
+// before the shared memory and the TMEM they work on are freed.  (A barrier
+// could pass on the parity of an earlier turn.)  2^24 cycles are 8 ms.
+static __device__ __noinline__ void settle() {
+  const long long t0 = clock64();
+  while (clock64() - t0 < (1ll << 24)) __nanosleep(1000);
+}
 __device__ __forceinline__ void expect_tx(uint32_t bar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }

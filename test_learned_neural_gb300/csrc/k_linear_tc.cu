@@ -159,6 +159,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHR, 1)
         }
       }
     }
+    // the commits behind the last stages arrive in both CTAs: none leaves before
+    for (int i = 0; i < STAGES && ok; ++i) {
+      ok = __all_sync(0xffffffffu, tc::wait(bempty + 8 * s, ph));
+      if (++s == STAGES) s = 0, ph ^= 1;
+    }
     if (!ok && lane == 0) atomicExch(&failed, 1);
   } else if (warp == 1) {
     if (rank == 0) {

@@ -357,3 +357,27 @@ def test_norm_behind_an_outlier(gpu_lib, N, S, C, G, dtype):
         err = _rms(got[part] - ref[part]) / _rms(ref[part])
         print(f"{err:.2e}")
         assert err <= 1e-5
+
+
+# ------------------------------------------------------------------ chained
+def test_behind_the_memory_itself(gpu_lib):
+    """The memory's own read-out through the head norm and the output projection:
+    each stage against the oracle on what it was given (2^-8 of the values, as
+    the operators' own tests)."""
+    import torch
+    from harness import WORKLOADS, make_inputs
+    from test_learned_neural_gb300.runner import GroupNorm, Linear, Memory, tensors_from_numpy
+    w = WORKLOADS["titans_mlp"].scaled(B=2, H=4, T=192)
+    mem = Memory(w)
+    y = mem.forward(tensors_from_numpy(make_inputs(w)))["y"]
+    B, H, T, d = y.shape
+    g = torch.Generator().manual_seed(71)
+    weight, W_o = (1 + 0.1 * torch.randn(H * d, generator=g)).cuda(), (torch.randn(H * d, 96, generator=g) / 16).bfloat16().cuda()
+    x = torch.randn(B * T, 96, generator=g).bfloat16().cuda()
+    n = GroupNorm(H * d, H, "silu", x_dtype="f32", y_dtype="bf16", layout="heads").forward(dict(x=y, weight=weight))["y"]
+    out = Linear(H * d, 96).forward(dict(x=n.view(B * T, H * d), W=W_o, residual=x))["y"]
+    torch.cuda.synchronize()
+    mem.status()
+    assert n.shape == (B, T, H * d)
+    assert maxrel(_host(n), layer.group_norm(_host(y), H, _host(weight), None, "silu", layout="heads")) <= TOL["bf16"]
+    assert maxrel(_host(out), layer.linear(_host(n).reshape(B * T, H * d), _host(W_o), residual=_host(x))) <= TOL["bf16"]

@@ -22,7 +22,10 @@
  * state token by token in registers; longer ones work in chunks, and a call
  * with few (row, head) pairs is also split along the tokens (per-segment
  * states, a scan over them, then the read-outs).  States, sums and decays are
- * fp32.  A handle is not re-entrant: do not call it from two threads or on two
+ * fp32; on the tensor cores (bf16 q, k, v, d_k <= 128) the products take the
+ * weighted scores and the state in bf16 terms, 16 bits of them for bf16 read-outs,
+ * which are rounded to 8, and 24 for fp32 ones, and the state's update takes the
+ * weighted keys in 24 bits.  A handle is not re-entrant: do not call it from two threads or on two
  * streams at once.  Its calls are made on one device, which holds their tensors
  * and is the current one.
  *

@@ -11,9 +11,16 @@
  * rounded once.  W has the orientation of atlas_prologue.h's W_in.
  *
  * Execution: asynchronous on the given CUDA stream.  bf16 inputs: exact
- * products, fp32 accumulation.  fp32 inputs: fp32 accuracy (three bf16 planes of
- * each on the tensor cores; a NaN or an infinity in x makes its row of y
- * non-finite, not always of the same kind, and no other row).  A handle is not
+ * products, fp32 accumulation; on the tensor cores an accumulator cuts off and
+ * loses about 1.1e-9 of the result per value of K: fp32 results are added up in
+ * fp32 from pieces of 512 of K, bf16 results take all of K at once (2e-6 at K =
+ * 2048, 1e-5 at 8192, against their rounding of 2^-8).  fp32 inputs: fp32
+ * accuracy whatever y's type (three bf16 planes of each on the tensor cores; a NaN
+ * or an infinity in x makes its row of y non-finite, one in W its column, not
+ * always of the same kind, and no other).  Activations: fp32 y by the formulas of
+ * atlas_norm.h in fp32 (GELU's 1 + erf is exact to 1e-7 of z, not of the result);
+ * bf16 y within 4e-4 of the value before it is rounded, GELU to z = -12.9 and
+ * zero below.  A handle is not
  * re-entrant: do not call it from two threads or on two streams at once.  Its
  * calls are made on one device, which holds their tensors and is the current one.
  *

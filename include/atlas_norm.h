@@ -14,8 +14,9 @@
  *   memory's read-out (N = B, groups = H, S = T), and y is [N][S][C]; a set is
  *   one group (head) of one position.
  *
- * Statistics are fp32, from centred values (a large common offset of x costs
- * no digits beyond those x itself lacks).
+ * Statistics are fp32, from centred values: a large common offset of x costs
+ * no digits beyond those x itself lacks, and a set of one value gives act(bias).
+ * Activations as in atlas_linear.h.
  *
  * Execution: asynchronous on the given CUDA stream.  A handle is not
  * re-entrant: do not call it from two threads or on two streams at once.  Its

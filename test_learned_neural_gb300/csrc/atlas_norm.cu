@@ -531,7 +531,7 @@ Plan make_plan(const atlas_norm_config& c, int N, int S, bool vec) {
   if ((S == 1 || c.layout == ATLAS_NORM_HEADS) && Cg <= kMaxRun) return p;
   // A cluster's registers, where they hold the sample's tile (64 bytes or more
   // of a row, whole groups) and the clusters fill the SMs: x is read once.
-  // 8 x 4096 x 1024 bf16, 32 groups: 39 us so, 47 in two passes; 32 x 256 x 512:
+  // 8 x 4096 x 1024 bf16, 32 groups: 38 us so, 47 in two passes; 32 x 256 x 512:
   // 12 / 14.  (Sixteen vectors per thread instead of eight: 51 and 84 -> 90 us for
   // 4096 rows of fp32, which do not fit eight: too few blocks per SM.)
   const int v16 = 16 / (int)dtype_size(c.x_dtype);

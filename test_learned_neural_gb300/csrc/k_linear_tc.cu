@@ -457,7 +457,7 @@ int split_cols(int N) { return (N + 3) / 4 * 4; }
 // per value of K (measured: 4.8e-7 at K = 517, 9.1e-6 at 8192).  fp32 results
 // take K in passes of 512, added up in registers; fp32 inputs, whatever the
 // results' type, in passes of 256, each with its five small products first.
-// bf16 inputs with bf16 results, rounded at 2^-9, take all of K at once.
+// bf16 inputs with bf16 results, rounded at 2^-8, take all of K at once.
 // Only the kernel with SUM adds passes up: the host and the kernel's template
 // have to agree on this.
 template <bool SUM>

@@ -1,0 +1,118 @@
+/*
+ * atlas_qlinear.h -- C ABI of the matrix product with 4-bit weights for few
+ * rows: the projections of a serving step, whose time is the reading of their
+ * weights.  atlas_linear.h has the same product with 16- and 32-bit ones.
+ *
+ * The operation, row-major:
+ *
+ *   y = act(x W + bias) + residual      x [M][K], W [K][N], y [M][N]
+ *   W[k][n] = scale[k / group][n] * (q[k][n] - zero[k / group][n])
+ *
+ * q is 0 .. 15, the scales are bf16, the zero points 0 .. 15 (8 where the
+ * configuration has none).  x is bf16, fp32, or ATLAS_E4M3 with fp32 scales for
+ * runs of 128 values of a row, or for whole rows, as atlas_rms.h makes them:
+ * the value is then stored x * scale.
+ *
+ * Weights come as q [ceil(K / 2)][N] bytes (the low four bits are row 2 i, the
+ * high ones row 2 i + 1), scales [ceil(K / group)][N] and zeros of the same
+ * shape, a byte each.  atlas_qlinear_quantize makes them from W;
+ * atlas_qlinear_pack lays them out once, in the order in which the kernels read
+ * them, and forward takes what it wrote.
+ *
+ * Execution: asynchronous on the given CUDA stream.  Products of q - zero with x
+ * are exact and summed in fp32 within a group (fp32 x in three bf16 terms, 24
+ * bits); groups are added up in fp32 under their scales.  y is rounded once.
+ * Activations as in atlas_linear.h.  Any M is taken, 64 rows at a time: from about
+ * a hundred rows on the product is bound by its arithmetic, not by its weights.
+ * A handle is not re-entrant: do not call it from two threads or on two streams at
+ * once.  Its calls are made on one device, which holds their tensors and is the
+ * current one.
+ *
+ * Capture: calls may be captured in a CUDA graph, the first one of a size too.
+ * A graph uses the handle's workspace: that stays allocated until the handle is
+ * destroyed (a later call that needs more gets a new one beside it), so a graph
+ * may be replayed as long as the handle lives.  A replay counts as a call on it.
+ *
+ * Inputs: a NaN or an infinity in x makes its row of y non-finite, one in the
+ * scales its column, and no other.
+ *
+ * Errors: the status codes of atlas_mem.h; atlas_qlinear_last_error gives the
+ * message.  Validation failures return before any CUDA call.
+ */
+#ifndef ATLAS_QLINEAR_H
+#define ATLAS_QLINEAR_H
+
+#include <stddef.h>
+#include <stdint.h>
+
+#include "atlas_mem.h"
+#include "atlas_norm.h"   /* ATLAS_ACT_* */
+#include "atlas_rms.h"    /* ATLAS_E4M3 */
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+typedef struct {
+    int K, N;         /* 1 .. 2^20 */
+    int group;        /* rows of W that share a scale: 32, 64 or 128 (the last group may be shorter) */
+    int zeros;        /* 1: zero points for each group and column; 0: all 8 */
+    int act;          /* ATLAS_ACT_* */
+    int x_dtype;      /* ATLAS_F32, ATLAS_BF16 or ATLAS_E4M3 */
+    int x_block;      /* ATLAS_E4M3: 128, or 0 (one scale for a row); else 0 */
+    int out_dtype;    /* ATLAS_F32 or ATLAS_BF16: type of residual and y */
+} atlas_qlinear_config;
+
+typedef struct atlas_qlinear_handle atlas_qlinear_handle;
+
+/* Tensors of one call, all DEVICE pointers owned by the caller. */
+typedef struct {
+    int M;                 /* rows, 1 .. 4194240 */
+    const void* x;         /* [M][K] x_dtype */
+    const float* x_scale;  /* ATLAS_E4M3: [M][ceil(K / 128)], or [M] for x_block 0; else NULL */
+    const void* W;         /* what atlas_qlinear_pack wrote, aligned to 16 bytes */
+    const float* bias;     /* [N]; NULL: 0 */
+    const void* residual;  /* [M][N] out_dtype; NULL: 0 */
+    void* y;               /* [M][N] out_dtype; may be residual itself, overlaps no other tensor */
+} atlas_qlinear_io;
+
+/* Validate the config and make a handle (no CUDA call).  INVALID_ARG or
+ * UNSUPPORTED with a message from atlas_qlinear_last_error(NULL). */
+int atlas_qlinear_create(const atlas_qlinear_config* cfg, atlas_qlinear_handle** out);
+
+/* 4-bit weights of W [K][N] (ATLAS_F32 or ATLAS_BF16, finite): without zero
+ * points scale = largest |W| of a group and column / 7, with them (largest, at
+ * least 0, - smallest, at most 0) / 15 and zero = -smallest / scale; the scale is
+ * rounded to bf16 first, then q and zero to the nearest.  Writes q, scales and (if
+ * the configuration has them, else NULL) zeros. */
+int atlas_qlinear_quantize(atlas_qlinear_handle* h, const void* W, int w_dtype, uint8_t* q, void* scales,
+                           uint8_t* zeros, void* stream);
+
+/* Bytes of the laid out weights. */
+size_t atlas_qlinear_packed_bytes(const atlas_qlinear_handle* h);
+
+/* Lays out q, scales (bf16) and zeros (NULL without zero points) into packed,
+ * atlas_qlinear_packed_bytes long and aligned to 16 bytes. */
+int atlas_qlinear_pack(atlas_qlinear_handle* h, const uint8_t* q, const void* scales, const uint8_t* zeros, void* packed,
+                       void* stream);
+
+/* One call; stream is a cudaStream_t (NULL = the default stream).  Grows the
+ * handle's workspace to atlas_qlinear_workspace_bytes on first use (cudaMalloc);
+ * the stream of the last call on h must still exist then. */
+int atlas_qlinear_forward(atlas_qlinear_handle* h, const atlas_qlinear_io* io, void* stream);
+
+/* Device workspace a call of this size may need: fp32 x in bf16 terms, and
+ * copies of x where its rows are no multiples of 16 bytes. */
+size_t atlas_qlinear_workspace_bytes(const atlas_qlinear_handle* h, int M);
+
+/* Message of the last failure on h, or of the last failed create when h is NULL. */
+const char* atlas_qlinear_last_error(const atlas_qlinear_handle* h);
+
+/* Free the handle and its workspace (NULL is a no-op). */
+void atlas_qlinear_destroy(atlas_qlinear_handle* h);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif

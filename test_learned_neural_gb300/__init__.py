@@ -15,7 +15,7 @@ LIB_PATH = os.path.join(HERE, "_lib", "libatlas_mem.so")
 
 ATLAS_OK, ATLAS_ERR_INVALID_ARG, ATLAS_ERR_UNSUPPORTED, ATLAS_ERR_CUDA, ATLAS_ERR_OOM, ATLAS_ERR_TIMEOUT, \
     ATLAS_ERR_RANGE = range(7)
-ATLAS_F32, ATLAS_BF16 = 0, 1
+ATLAS_F32, ATLAS_BF16, ATLAS_E4M3 = 0, 1, 2
 ATLAS_READOUT_POST, ATLAS_READOUT_PRE = 0, 1
 ATLAS_NS_MOMENTUM, ATLAS_NS_SURPRISE = 0, 1
 ATLAS_UPDATE_PER_TOKEN, ATLAS_UPDATE_CHUNKWISE = 0, 1
@@ -26,7 +26,7 @@ ATLAS_NORM_CHANNELS_LAST, ATLAS_NORM_HEADS = 0, 1
 ATLAS_ACT_NONE, ATLAS_ACT_SILU, ATLAS_ACT_GELU = 0, 1, 2
 
 # exported symbols, as declared in include/atlas_mem.h, atlas_prologue.h,
-# atlas_decay.h, atlas_norm.h and atlas_linear.h
+# atlas_decay.h, atlas_norm.h, atlas_linear.h, atlas_conv.h, atlas_rms.h and atlas_qlinear.h
 EXPORTS = ("atlas_mem_create", "atlas_mem_forward", "atlas_mem_forward_host", "atlas_mem_forward_noalloc",
            "atlas_mem_status",
            "atlas_mem_workspace_bytes", "atlas_mem_last_launches", "atlas_mem_last_error", "atlas_mem_destroy",
@@ -38,7 +38,12 @@ EXPORTS = ("atlas_mem_create", "atlas_mem_forward", "atlas_mem_forward_host", "a
            "atlas_norm_create", "atlas_norm_forward", "atlas_norm_workspace_bytes", "atlas_norm_last_error",
            "atlas_norm_destroy",
            "atlas_linear_create", "atlas_linear_forward", "atlas_linear_workspace_bytes", "atlas_linear_status",
-           "atlas_linear_last_path", "atlas_linear_last_error", "atlas_linear_destroy")
+           "atlas_linear_last_path", "atlas_linear_last_error", "atlas_linear_destroy",
+           "atlas_conv_create", "atlas_conv_forward", "atlas_conv_last_error", "atlas_conv_destroy",
+           "atlas_rms_create", "atlas_rms_forward", "atlas_rms_last_error", "atlas_rms_destroy",
+           "atlas_qlinear_create", "atlas_qlinear_quantize", "atlas_qlinear_packed_bytes", "atlas_qlinear_pack",
+           "atlas_qlinear_forward", "atlas_qlinear_workspace_bytes", "atlas_qlinear_last_error",
+           "atlas_qlinear_destroy")
 
 
 class atlas_mem_config(ctypes.Structure):
@@ -104,6 +109,32 @@ class atlas_linear_io(ctypes.Structure):
     _fields_ = [("M", ctypes.c_int)] + [(n, _vp) for n in ("x", "W", "bias", "residual", "y")]
 
 
+class atlas_conv_config(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("C", "K", "act", "dtype")]
+
+
+class atlas_conv_io(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("B", "T", "ld_x")] + [
+        (n, _vp) for n in ("x", "w", "bias", "cache", "lens", "y", "cache_out")]
+
+
+class atlas_rms_config(ctypes.Structure):
+    _fields_ = [("C", ctypes.c_int), ("eps", ctypes.c_float)] + [
+        (n, ctypes.c_int) for n in ("x_dtype", "residual_dtype", "y_dtype", "block")]
+
+
+class atlas_rms_io(ctypes.Structure):
+    _fields_ = [("M", ctypes.c_int)] + [(n, _vp) for n in ("x", "residual", "weight", "y", "h", "scale")]
+
+
+class atlas_qlinear_config(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("K", "N", "group", "zeros", "act", "x_dtype", "x_block", "out_dtype")]
+
+
+class atlas_qlinear_io(ctypes.Structure):
+    _fields_ = [("M", ctypes.c_int)] + [(n, _vp) for n in ("x", "x_scale", "W", "bias", "residual", "y")]
+
+
 class AtlasError(RuntimeError):
     def __init__(self, code, msg):
         super().__init__(f"{STATUS_NAMES.get(code, code)}: {msg}")
@@ -153,7 +184,10 @@ def load(path: str = LIB_PATH):
     lib.atlas_prologue_last_gemm.restype = ctypes.c_int
     for op, cfg, io, sizes in (("decay", atlas_decay_config, atlas_decay_io, 2),
                                ("norm", atlas_norm_config, atlas_norm_io, 2),
-                               ("linear", atlas_linear_config, atlas_linear_io, 1)):
+                               ("linear", atlas_linear_config, atlas_linear_io, 1),
+                               ("conv", atlas_conv_config, atlas_conv_io, 0),
+                               ("rms", atlas_rms_config, atlas_rms_io, 0),
+                               ("qlinear", atlas_qlinear_config, atlas_qlinear_io, 1)):
         for name, args, res in (
                 ("create", [ctypes.POINTER(cfg), ctypes.POINTER(ctypes.c_void_p)], ctypes.c_int),
                 ("forward", [ctypes.c_void_p, ctypes.POINTER(io), ctypes.c_void_p], ctypes.c_int),
@@ -165,6 +199,12 @@ def load(path: str = LIB_PATH):
             if f"atlas_{op}_{name}" in EXPORTS:
                 fn = getattr(lib, f"atlas_{op}_{name}")
                 fn.argtypes, fn.restype = args, res
+    lib.atlas_qlinear_quantize.argtypes = [_vp, _vp, ctypes.c_int, _vp, _vp, _vp, _vp]
+    lib.atlas_qlinear_quantize.restype = ctypes.c_int
+    lib.atlas_qlinear_packed_bytes.argtypes = [_vp]
+    lib.atlas_qlinear_packed_bytes.restype = ctypes.c_size_t
+    lib.atlas_qlinear_pack.argtypes = [_vp] * 6
+    lib.atlas_qlinear_pack.restype = ctypes.c_int
     _lib = lib
     return lib
 
@@ -349,7 +389,89 @@ def atlas_linear_destroy(h):
     load().atlas_linear_destroy(h)
 
 
-_DTYPES = {"f32": ATLAS_F32, "bf16": ATLAS_BF16}
+def atlas_conv_create(cfg: atlas_conv_config):
+    lib = load()
+    return _created(lib.atlas_conv_create, lib.atlas_conv_last_error, cfg)
+
+
+def atlas_conv_forward(h, io: atlas_conv_io, stream: int = 0):
+    lib = load()
+    rc = lib.atlas_conv_forward(h, ctypes.byref(io), stream)
+    if rc:
+        raise AtlasError(rc, lib.atlas_conv_last_error(h).decode())
+
+
+def atlas_conv_last_error(h) -> str:
+    return load().atlas_conv_last_error(h).decode()
+
+
+def atlas_conv_destroy(h):
+    load().atlas_conv_destroy(h)
+
+
+def atlas_rms_create(cfg: atlas_rms_config):
+    lib = load()
+    return _created(lib.atlas_rms_create, lib.atlas_rms_last_error, cfg)
+
+
+def atlas_rms_forward(h, io: atlas_rms_io, stream: int = 0):
+    lib = load()
+    rc = lib.atlas_rms_forward(h, ctypes.byref(io), stream)
+    if rc:
+        raise AtlasError(rc, lib.atlas_rms_last_error(h).decode())
+
+
+def atlas_rms_last_error(h) -> str:
+    return load().atlas_rms_last_error(h).decode()
+
+
+def atlas_rms_destroy(h):
+    load().atlas_rms_destroy(h)
+
+
+def atlas_qlinear_create(cfg: atlas_qlinear_config):
+    lib = load()
+    return _created(lib.atlas_qlinear_create, lib.atlas_qlinear_last_error, cfg)
+
+
+def atlas_qlinear_forward(h, io: atlas_qlinear_io, stream: int = 0):
+    lib = load()
+    rc = lib.atlas_qlinear_forward(h, ctypes.byref(io), stream)
+    if rc:
+        raise AtlasError(rc, lib.atlas_qlinear_last_error(h).decode())
+
+
+def atlas_qlinear_last_error(h) -> str:
+    return load().atlas_qlinear_last_error(h).decode()
+
+
+def atlas_qlinear_destroy(h):
+    load().atlas_qlinear_destroy(h)
+
+
+def atlas_qlinear_quantize(h, W, w_dtype, q, scales, zeros, stream: int = 0):
+    lib = load()
+    rc = lib.atlas_qlinear_quantize(h, W, w_dtype, q, scales, zeros, stream)
+    if rc:
+        raise AtlasError(rc, lib.atlas_qlinear_last_error(h).decode())
+
+
+def atlas_qlinear_packed_bytes(h) -> int:
+    return load().atlas_qlinear_packed_bytes(h)
+
+
+def atlas_qlinear_pack(h, q, scales, zeros, packed, stream: int = 0):
+    lib = load()
+    rc = lib.atlas_qlinear_pack(h, q, scales, zeros, packed, stream)
+    if rc:
+        raise AtlasError(rc, lib.atlas_qlinear_last_error(h).decode())
+
+
+def atlas_qlinear_workspace_bytes(h, M) -> int:
+    return load().atlas_qlinear_workspace_bytes(h, M)
+
+
+_DTYPES = {"f32": ATLAS_F32, "bf16": ATLAS_BF16, "e4m3": ATLAS_E4M3}
 _ACTS = {"none": ATLAS_ACT_NONE, "silu": ATLAS_ACT_SILU, "gelu": ATLAS_ACT_GELU}
 _LAYOUTS = {"heads": ATLAS_LAYOUT_HEADS, "tokens": ATLAS_LAYOUT_TOKENS}
 _NORM_LAYOUTS = {"channels_last": ATLAS_NORM_CHANNELS_LAST, "heads": ATLAS_NORM_HEADS}
@@ -374,6 +496,23 @@ def make_linear_config(K, N, act="none", in_dtype="bf16", out_dtype=None) -> atl
     it = _DTYPES.get(in_dtype, in_dtype)
     ot = it if out_dtype is None else _DTYPES.get(out_dtype, out_dtype)
     return atlas_linear_config(K, N, _ACTS.get(act, act), it, ot)
+
+
+def make_conv_config(C, K, act="silu", dtype="bf16") -> atlas_conv_config:
+    return atlas_conv_config(C, K, _ACTS.get(act, act), _DTYPES.get(dtype, dtype))
+
+
+def make_rms_config(C, eps=1e-6, x_dtype="bf16", y_dtype=None, residual_dtype=None, block=0) -> atlas_rms_config:
+    xt = _DTYPES.get(x_dtype, x_dtype)
+    yt, rt = (xt if t is None else _DTYPES.get(t, t) for t in (y_dtype, residual_dtype))
+    return atlas_rms_config(C, eps, xt, rt, yt, block)
+
+
+def make_qlinear_config(K, N, group=128, zeros=False, act="none", x_dtype="bf16", x_block=0,
+                        out_dtype=None) -> atlas_qlinear_config:
+    xt = _DTYPES.get(x_dtype, x_dtype)
+    ot = (ATLAS_BF16 if xt == ATLAS_E4M3 else xt) if out_dtype is None else _DTYPES.get(out_dtype, out_dtype)
+    return atlas_qlinear_config(K, N, group, int(zeros), _ACTS.get(act, act), xt, x_block, ot)
 
 
 def make_prologue_config(D, H, d_k, d_v, conv, with_gamma, theta_max, qkv_dtype) -> atlas_prologue_config:

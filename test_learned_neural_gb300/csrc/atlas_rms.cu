@@ -1,0 +1,306 @@
+// Root-mean-square norm with the residual's addition (atlas_rms.h).
+#include "../../include/atlas_rms.h"
+
+#include <cuda_fp8.h>
+#include <math.h>
+
+#include <new>
+#include <type_traits>
+
+#include "layer_common.cuh"
+#include "tc2.cuh"
+
+using namespace layer;
+
+namespace {
+
+constexpr int kMostC = 32768;
+constexpr float kE4m3Max = 448.f, kLeast = 0x1p-100f;
+struct e4m3 {   // 8 bits; stored through pack_e4m3
+  uint8_t bits;
+};
+
+struct Call {
+  int M, C, block, nscale;
+  float eps;
+  const float* weight;
+  float* scale;
+};
+
+__device__ __forceinline__ uint32_t pack_e4m3(float a, float b, float c, float d) {
+  const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3),
+                 hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
+  return lo | (hi << 16);
+}
+// the larger; NaN if one is NaN (fmaxf would drop it)
+__device__ __forceinline__ float max_nan(float a, float b) { return a > b || a != a ? a : b; }
+__device__ __forceinline__ float scale_of(float largest) { return max_nan(largest, kLeast) / kE4m3Max; }
+
+// A row's sum (or largest value) over its threads; all of them get it.
+template <int TPR, bool MAX>
+__device__ __forceinline__ float over_row(float v, float* sh) {
+  auto join = [](float a, float b) { return MAX ? max_nan(a, b) : a + b; };
+#pragma unroll
+  for (int d = 16; d > 0; d /= 2) v = join(v, __shfl_xor_sync(0xffffffffu, v, d));
+  if constexpr (TPR > 32) {
+    constexpr int W = TPR / 32;
+    if (threadIdx.x % 32 == 0) sh[threadIdx.x / 32] = v;
+    __syncthreads();
+    v = sh[0];
+#pragma unroll
+    for (int i = 1; i < W; ++i) v = join(v, sh[i]);
+    __syncthreads();
+  }
+  return v;
+}
+
+// Rows of whole 8-value groups: TPR threads hold a row in registers, VPT groups
+// each, so that x and the residual are read once, with all loads in flight.
+template <typename TX, typename TR, typename TY, int TPR, int VPT>
+__global__ void __launch_bounds__(TPR == 32 ? 128 : TPR) k_rms(Call c, const TX* x, const TR* r, TY* y, TR* h) {
+  constexpr int ROWS = TPR == 32 ? 4 : 1;
+  __shared__ float sh[TPR / 32];
+  const int lane = threadIdx.x % TPR, vecs = c.C / 8;
+  const size_t row = (size_t)blockIdx.x * ROWS + threadIdx.x / TPR;
+  tc::grid_dependency_wait();
+  tc::grid_dependents_launch();
+  if (ROWS > 1 && row >= (size_t)c.M) return;   // whole warps
+  x += row * c.C;
+  y += row * c.C;
+  float v[VPT][8];
+  {
+    Words<TX, 8> xw[VPT];
+#pragma unroll
+    for (int i = 0; i < VPT; ++i)
+      if (lane + i * TPR < vecs) xw[i].load(x + (lane + i * TPR) * 8);
+      else xw[i] = Words<TX, 8>{};
+    if (r) {
+      r += row * c.C;
+      Words<TR, 8> rw[VPT];
+#pragma unroll
+      for (int i = 0; i < VPT; ++i)
+        if (lane + i * TPR < vecs) rw[i].load(r + (lane + i * TPR) * 8);
+        else rw[i] = Words<TR, 8>{};
+#pragma unroll
+      for (int i = 0; i < VPT; ++i) {
+        float a[8];
+        xw[i].values(v[i]);
+        rw[i].values(a);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[i][e] += a[e];
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < VPT; ++i) xw[i].values(v[i]);
+    }
+  }
+  if (h) {
+    h += row * c.C;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i)
+      if (lane + i * TPR < vecs) store_vec<8>(h + (lane + i * TPR) * 8, v[i]);
+  }
+  float ss = 0.f;
+#pragma unroll
+  for (int i = 0; i < VPT; ++i)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) ss = fmaf(v[i][e], v[i][e], ss);
+  const float rs = 1.f / sqrtf(over_row<TPR, false>(ss, sh) / (float)c.C + c.eps);
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    float w[8] = {1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f};
+    if (c.weight && lane + i * TPR < vecs) load_vec<8>(c.weight + (lane + i * TPR) * 8, w);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[i][e] = v[i][e] * rs * w[e];
+  }
+  if constexpr (!std::is_same<TY, e4m3>::value) {
+#pragma unroll
+    for (int i = 0; i < VPT; ++i)
+      if (lane + i * TPR < vecs) store_vec<8>(y + (lane + i * TPR) * 8, v[i]);
+  } else {
+    float top[VPT], all = 0.f;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      top[i] = fabsf(v[i][0]);
+#pragma unroll
+      for (int e = 1; e < 8; ++e) top[i] = max_nan(top[i], fabsf(v[i][e]));
+      all = max_nan(all, top[i]);
+    }
+    if (c.block == 0) {
+      all = over_row<TPR, true>(all, sh);
+    } else {
+      // 16 threads side by side hold a run of 128
+#pragma unroll
+      for (int i = 0; i < VPT; ++i)
+#pragma unroll
+        for (int d = 8; d > 0; d /= 2) top[i] = max_nan(top[i], __shfl_xor_sync(0xffffffffu, top[i], d));
+    }
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int vec = lane + i * TPR;
+      const float s = scale_of(c.block == 0 ? all : top[i]), inv = 1.f / s;
+      if (vec >= vecs) continue;
+      if (c.block == 0 ? vec == 0 : vec % 16 == 0) c.scale[row * c.nscale + (c.block == 0 ? 0 : vec / 16)] = s;
+      *reinterpret_cast<uint2*>(reinterpret_cast<uint8_t*>(y) + vec * 8) =
+          make_uint2(pack_e4m3(v[i][0] * inv, v[i][1] * inv, v[i][2] * inv, v[i][3] * inv),
+                     pack_e4m3(v[i][4] * inv, v[i][5] * inv, v[i][6] * inv, v[i][7] * inv));
+    }
+  }
+}
+
+// Any width and alignment: a block per row, which waits in shared memory.
+template <typename TX, typename TR, typename TY>
+__global__ void __launch_bounds__(256) k_rms_any(Call c, const TX* x, const TR* r, TY* y, TR* h) {
+  extern __shared__ float keep[];
+  __shared__ float sh[8];
+  const int tid = threadIdx.x;
+  tc::grid_dependency_wait();
+  tc::grid_dependents_launch();
+  const size_t at = (size_t)blockIdx.x * c.C;
+  float ss = 0.f;
+#pragma unroll 4
+  for (int i = tid; i < c.C; i += 256) {
+    const float v = to_f32(x[at + i]) + (r ? to_f32(r[at + i]) : 0.f);
+    keep[i] = v;
+    ss = fmaf(v, v, ss);
+  }
+  ss = over_row<256, false>(ss, sh);   // (its barriers also order keep)
+  const float rs = 1.f / sqrtf(ss / (float)c.C + c.eps);
+  if (h)
+    for (int i = tid; i < c.C; i += 256) h[at + i] = from_f32<TR>(keep[i]);
+  if constexpr (!std::is_same<TY, e4m3>::value) {
+    for (int i = tid; i < c.C; i += 256) y[at + i] = from_f32<TY>(keep[i] * rs * (c.weight ? c.weight[i] : 1.f));
+  } else {
+    uint8_t* q = reinterpret_cast<uint8_t*>(y) + at;
+    if (c.block == 0) {
+      float top = 0.f;
+      for (int i = tid; i < c.C; i += 256) {
+        keep[i] = keep[i] * rs * (c.weight ? c.weight[i] : 1.f);   // the thread's own values
+        top = max_nan(top, fabsf(keep[i]));
+      }
+      const float s = scale_of(over_row<256, true>(top, sh)), inv = 1.f / s;
+      if (tid == 0) c.scale[blockIdx.x] = s;
+      for (int i = tid; i < c.C; i += 256) q[i] = (uint8_t)pack_e4m3(keep[i] * inv, 0.f, 0.f, 0.f);
+    } else {
+      for (int blk = tid / 32; blk < c.nscale; blk += 8) {   // a warp per run of 128
+        float v[4], top = 0.f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int i = blk * 128 + e * 32 + tid % 32;
+          v[e] = i < c.C ? keep[i] * rs * (c.weight ? c.weight[i] : 1.f) : 0.f;
+          top = max_nan(top, fabsf(v[e]));
+        }
+        top = over_row<32, true>(top, sh);
+        const float s = scale_of(top), inv = 1.f / s;
+        if (tid % 32 == 0) c.scale[(size_t)blockIdx.x * c.nscale + blk] = s;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int i = blk * 128 + e * 32 + tid % 32;
+          if (i < c.C) q[i] = (uint8_t)pack_e4m3(v[e] * inv, 0.f, 0.f, 0.f);
+        }
+      }
+    }
+  }
+}
+
+template <typename TX, typename TR, typename TY>
+cudaError_t launch(const Call& c, const atlas_rms_io& io, bool vec, cudaStream_t st) {
+  auto go = [&](auto kern, unsigned grid, unsigned threads, size_t smem) {
+    if (smem > 48 * 1024) {
+      const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+      if (e != cudaSuccess) return e;
+    }
+    return tc::launch_overlapped(kern, dim3(grid), dim3(threads), smem, st, c, (const TX*)io.x, (const TR*)io.residual,
+                                 (TY*)io.y, (TR*)io.h);
+  };
+  const unsigned M = (unsigned)io.M;
+  if (!vec) return go(k_rms_any<TX, TR, TY>, M, 256, (size_t)c.C * 4);
+  const int vecs = c.C / 8;
+  if (vecs <= 32) return go(k_rms<TX, TR, TY, 32, 1>, (M + 3) / 4, 128, 0);
+  if (vecs <= 64) return go(k_rms<TX, TR, TY, 32, 2>, (M + 3) / 4, 128, 0);
+  if (vecs <= 128) return go(k_rms<TX, TR, TY, 32, 4>, (M + 3) / 4, 128, 0);
+  if (vecs <= 256) return go(k_rms<TX, TR, TY, 256, 1>, M, 256, 0);
+  if (vecs <= 512) return go(k_rms<TX, TR, TY, 256, 2>, M, 256, 0);
+  if (vecs <= 1024) return go(k_rms<TX, TR, TY, 256, 4>, M, 256, 0);
+  if (vecs <= 2048) return go(k_rms<TX, TR, TY, 512, 4>, M, 512, 0);
+  return go(k_rms<TX, TR, TY, 1024, 4>, M, 1024, 0);
+}
+template <typename TX, typename TR>
+cudaError_t launch_y(const Call& c, const atlas_rms_io& io, int y, bool vec, cudaStream_t st) {
+  return y == ATLAS_F32 ? launch<TX, TR, float>(c, io, vec, st)
+                        : y == ATLAS_BF16 ? launch<TX, TR, bf16>(c, io, vec, st) : launch<TX, TR, e4m3>(c, io, vec, st);
+}
+
+}  // namespace
+
+struct atlas_rms_handle : HandleBase {
+  atlas_rms_config cfg;
+};
+
+static thread_local std::string g_create_err;
+
+extern "C" int atlas_rms_create(const atlas_rms_config* cfg, atlas_rms_handle** out) {
+  if (!out || !cfg) {
+    g_create_err = "cfg and out must be non-NULL";
+    if (out) *out = nullptr;
+    return ATLAS_ERR_INVALID_ARG;
+  }
+  *out = nullptr;
+  const atlas_rms_config& c = *cfg;
+  auto bad = [&](int code, const char* why) {
+    g_create_err = why;
+    return code;
+  };
+  if (c.C < 1) return bad(ATLAS_ERR_INVALID_ARG, "C must be >= 1");
+  if (!(c.eps > 0.f) || !isfinite(c.eps)) return bad(ATLAS_ERR_INVALID_ARG, "eps must be positive and finite");
+  if (!dtype_ok(c.x_dtype) || !dtype_ok(c.residual_dtype))
+    return bad(ATLAS_ERR_INVALID_ARG, "x_dtype and residual_dtype must be ATLAS_F32 or ATLAS_BF16");
+  if (!dtype_ok(c.y_dtype) && c.y_dtype != ATLAS_E4M3)
+    return bad(ATLAS_ERR_INVALID_ARG, "y_dtype must be ATLAS_F32, ATLAS_BF16 or ATLAS_E4M3");
+  if (c.block != 0 && (c.block != 128 || c.y_dtype != ATLAS_E4M3))
+    return bad(ATLAS_ERR_INVALID_ARG, "block must be 0, or 128 with y_dtype ATLAS_E4M3");
+  if (c.C > kMostC) return bad(ATLAS_ERR_UNSUPPORTED, "C > 32768 is not supported");
+  auto* h = new (std::nothrow) atlas_rms_handle();
+  if (!h) return bad(ATLAS_ERR_OOM, "out of host memory");
+  h->cfg = c;
+  *out = h;
+  return ATLAS_OK;
+}
+
+extern "C" int atlas_rms_forward(atlas_rms_handle* h, const atlas_rms_io* io, void* stream) {
+  if (!h) return ATLAS_ERR_INVALID_ARG;
+  if (!io) return h->fail(ATLAS_ERR_INVALID_ARG, "io must be non-NULL");
+  const atlas_rms_config& c = h->cfg;
+  if (io->M < 1) return h->fail(ATLAS_ERR_INVALID_ARG, "M must be >= 1");
+  if (!io->x || !io->y) return h->fail(ATLAS_ERR_INVALID_ARG, "x and y must be non-NULL");
+  const bool q = c.y_dtype == ATLAS_E4M3;
+  if (q != (io->scale != nullptr))
+    return h->fail(ATLAS_ERR_INVALID_ARG, "scale goes with y_dtype ATLAS_E4M3, and only with it");
+  const size_t n = (size_t)io->M * c.C, nscale = c.block ? (c.C + c.block - 1) / c.block : 1;
+  const size_t xb = n * dtype_size(c.x_dtype), rb = n * dtype_size(c.residual_dtype),
+               yb = q ? n : n * dtype_size(c.y_dtype), sb = io->M * nscale * 4;
+  auto same = [](const void* a, const void* b, bool types) { return types && a == b; };
+  // a row is read whole before any of it is written, by the same block: the same tensor is fine, a shifted one is not
+  if ((overlap(io->y, yb, io->x, xb) && !same(io->y, io->x, c.y_dtype == c.x_dtype)) || overlap(io->y, yb, io->residual, rb))
+    return h->fail(ATLAS_ERR_INVALID_ARG, "y may be x itself where the types are the same, else it must not overlap x or residual");
+  if ((overlap(io->h, rb, io->x, xb) && !same(io->h, io->x, c.residual_dtype == c.x_dtype)) ||
+      (overlap(io->h, rb, io->residual, rb) && io->h != io->residual) || overlap(io->h, rb, io->y, yb))
+    return h->fail(ATLAS_ERR_INVALID_ARG, "h may be residual, or x where the types are the same, and must not overlap y");
+  if (overlap(io->scale, sb, io->y, yb) || overlap(io->scale, sb, io->h, rb) || overlap(io->scale, sb, io->x, xb) ||
+      overlap(io->scale, sb, io->residual, rb))
+    return h->fail(ATLAS_ERR_INVALID_ARG, "scale must not overlap another tensor");
+  const bool vec = c.C % 8 == 0 && aligned16(io->x) && aligned16(io->residual) && aligned16(io->y) && aligned16(io->h) &&
+                   aligned16(io->weight);
+  const Call k{io->M, c.C, c.block, (int)nscale, c.eps, io->weight, io->scale};
+  cudaStream_t st = (cudaStream_t)stream;
+  const bool xh = c.x_dtype == ATLAS_BF16, rh = c.residual_dtype == ATLAS_BF16;
+  const cudaError_t e = xh ? (rh ? launch_y<bf16, bf16>(k, *io, c.y_dtype, vec, st) : launch_y<bf16, float>(k, *io, c.y_dtype, vec, st))
+                           : (rh ? launch_y<float, bf16>(k, *io, c.y_dtype, vec, st) : launch_y<float, float>(k, *io, c.y_dtype, vec, st));
+  if (e != cudaSuccess) return h->cuda_fail("root-mean-square norm launch", e);
+  return ATLAS_OK;
+}
+
+extern "C" const char* atlas_rms_last_error(const atlas_rms_handle* h) {
+  return h ? h->err.c_str() : g_create_err.c_str();
+}
+extern "C" void atlas_rms_destroy(atlas_rms_handle* h) { delete h; }

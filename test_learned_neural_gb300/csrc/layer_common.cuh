@@ -80,6 +80,18 @@ struct Words {
       for (int i = 0; i < N; ++i) w[i] = reinterpret_cast<const uint32_t*>(p)[i];
     }
   }
+  __device__ __forceinline__ void store(T* p) const {
+    if constexpr (V * sizeof(T) % 16 == 0) {
+#pragma unroll
+      for (int i = 0; i < N; i += 4)
+        *reinterpret_cast<uint4*>(reinterpret_cast<uint32_t*>(p) + i) = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
+    } else if constexpr (sizeof(T) == 2) {
+      *reinterpret_cast<uint16_t*>(p) = (uint16_t)w[0];
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i) reinterpret_cast<uint32_t*>(p)[i] = w[i];
+    }
+  }
   __device__ __forceinline__ void values(float* v) const {
     if constexpr (sizeof(T) == 4) {
 #pragma unroll
@@ -130,6 +142,11 @@ inline bool dtype_ok(int t) { return t == ATLAS_F32 || t == ATLAS_BF16; }
 inline bool act_ok(int a) { return a == ATLAS_ACT_NONE || a == ATLAS_ACT_SILU || a == ATLAS_ACT_GELU; }
 inline size_t dtype_size(int t) { return t == ATLAS_BF16 ? 2 : 4; }
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+// whether two tensors share a byte (NULL: there is none)
+inline bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a && b && na && nb && x < y + nb && y < x + na;
+}
 
 // Message and workspace of a handle.  A captured graph holds the workspace's
 // address, so a workspace that a capture has recorded is never freed before the

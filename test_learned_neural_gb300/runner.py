@@ -10,15 +10,19 @@ from __future__ import annotations
 import numpy as np
 import torch
 
-from . import (ATLAS_BF16, ATLAS_F32, ATLAS_LAYOUT_HEADS, ATLAS_NORM_HEADS, atlas_decay_create, atlas_decay_destroy,
+from . import (ATLAS_BF16, ATLAS_E4M3, ATLAS_F32, ATLAS_LAYOUT_HEADS, ATLAS_NORM_HEADS, atlas_conv_create,
+               atlas_conv_destroy, atlas_conv_forward, atlas_conv_io, atlas_decay_create, atlas_decay_destroy,
                atlas_decay_forward, atlas_decay_io, atlas_decay_last_path, atlas_decay_status, atlas_linear_create,
                atlas_linear_destroy, atlas_linear_forward, atlas_linear_io, atlas_linear_last_path,
                atlas_linear_status, atlas_mem_create, atlas_mem_destroy, atlas_mem_forward,
                atlas_mem_forward_host, atlas_mem_status, atlas_norm_create, atlas_norm_destroy, atlas_norm_forward,
                atlas_norm_io, atlas_prologue_create, atlas_prologue_destroy,
                atlas_prologue_forward, atlas_prologue_io, atlas_prologue_last_gemm, atlas_prologue_status,
-               current_stream, make_config, make_decay_config, make_io, make_linear_config, make_norm_config,
-               make_prologue_config, AtlasError)
+               atlas_qlinear_create, atlas_qlinear_destroy, atlas_qlinear_forward, atlas_qlinear_io,
+               atlas_qlinear_pack, atlas_qlinear_packed_bytes, atlas_qlinear_quantize, atlas_rms_create,
+               atlas_rms_destroy, atlas_rms_forward, atlas_rms_io, current_stream, make_config, make_conv_config,
+               make_decay_config, make_io, make_linear_config, make_norm_config, make_prologue_config,
+               make_qlinear_config, make_rms_config, AtlasError)
 
 
 def matrix_shapes(cfg):
@@ -186,7 +190,7 @@ def prologue_tensors_from_numpy(inp: dict, device="cuda"):
 
 
 def _torch_dtype(t):
-    return torch.bfloat16 if t == ATLAS_BF16 else torch.float32
+    return {ATLAS_BF16: torch.bfloat16, ATLAS_E4M3: torch.float8_e4m3fn}.get(t, torch.float32)
 
 
 def _check(name, t, dtype, shape, device):
@@ -198,6 +202,30 @@ def _check(name, t, dtype, shape, device):
         raise ValueError(f"{name}: want a contiguous CUDA tensor {dtype} {shape} on one device with the others, got "
                          f"{t.dtype} {tuple(t.shape)} on {t.device}")
     return t.data_ptr()
+
+
+def _check_rows(name, t, dtype, shape, device):
+    """The same for [B, T, ...] whose tokens may lie further apart than their
+    own values (a slice of wider rows, which are themselves contiguous): the
+    address, and the values between neighbouring tokens."""
+    width = 1
+    for n in shape[2:]:
+        width *= n
+    B, T = shape[:2]
+    if t.is_contiguous():
+        return _check(name, t, dtype, shape, device), width
+    st = t.stride()
+    inner, dense = width, len(st) == len(shape)
+    for n, step in zip(shape[2:], st[2:]):
+        inner //= n
+        dense = dense and (n == 1 or step == inner)
+    # the distance of tokens, from that of the batch rows where there is one token each
+    ld = st[1] if T > 1 else st[0] if B > 1 else width
+    if (t.dtype is not dtype or t.shape != shape or not dense or not t.is_cuda or ld < width or ld > 0x7fffffff
+            or B > 1 and st[0] != T * ld or device is not None and t.get_device() != device):
+        raise ValueError(f"{name}: want a CUDA tensor {dtype} {shape} on one device with the others, contiguous or a "
+                         f"slice of contiguous rows, got {t.dtype} {tuple(t.shape)} with strides {st} on {t.device}")
+    return t.data_ptr(), ld
 
 
 # The current stream's handle of a device: torch.cuda.current_stream() builds a
@@ -371,3 +399,142 @@ class Linear(_Layer):
     def last_path(self):
         """1: tensor cores, 2: few rows."""
         return atlas_linear_last_path(self.h)
+
+
+class ShortConv(_Layer):
+    """Causal depthwise convolution over the tokens with bias, activation and a
+    carried cache (include/atlas_conv.h): y_t = act(bias + sum_j w[:, K-1-j] x_{t-j})."""
+    _destroy = staticmethod(atlas_conv_destroy)
+
+    def __init__(self, C, K, act="silu", dtype="bf16"):
+        self.cfg = make_conv_config(C, K, act, dtype)
+        self.h = atlas_conv_create(self.cfg)
+        self._x = _torch_dtype(self.cfg.dtype)
+
+    def alloc_outputs(self, B, T, device):
+        c = self.cfg
+        return dict(y=torch.empty((B, T, c.C), dtype=self._x, device=device),
+                    cache=torch.empty((B, c.K - 1, c.C), dtype=self._x, device=device))
+
+    def forward(self, t, out=None, stream=None):
+        """t: dict of device tensors x [B, T, C] (may be a slice of wider
+        rows), w (fp32 [C, K]) and optional bias (fp32 [C]), lens (int32 [B])
+        and cache [B, K-1, C] (may be out["cache"]: continued in place)."""
+        c, x = self.cfg, t["x"]
+        B, T = x.shape[:2]
+        if out is None:
+            out = self.alloc_outputs(B, T, x.device)
+        b, lens, cache, f32, dev = t.get("bias"), t.get("lens"), t.get("cache"), torch.float32, _device_of(x)
+        sc = (B, c.K - 1, c.C)
+        px, ld = _check_rows("x", x, self._x, (B, T, c.C), dev)
+        io = atlas_conv_io(B, T, ld, px, _check("w", t["w"], f32, (c.C, c.K), dev),
+                           None if b is None else _check("bias", b, f32, (c.C,), dev),
+                           None if cache is None else _check("cache", cache, self._x, sc, dev),
+                           None if lens is None else _check("lens", lens, torch.int32, (B,), dev),
+                           _check("y", out["y"], self._x, (B, T, c.C), dev),
+                           _check("cache", out["cache"], self._x, sc, dev))
+        atlas_conv_forward(self.h, io, _stream_of(dev, stream))
+        return out
+
+
+class RmsNorm(_Layer):
+    """Root-mean-square norm behind the residual's addition (include/atlas_rms.h):
+    h = x + residual, y = h / sqrt(mean h^2 + eps) * weight.  y_dtype "e4m3": with
+    a scale for each 128 values of a row (block = 128) or for a row (block = 0).
+    residual_dtype: of residual and h (None: x's)."""
+    _destroy = staticmethod(atlas_rms_destroy)
+
+    def __init__(self, C, eps=1e-6, x_dtype="bf16", y_dtype=None, residual_dtype=None, block=0):
+        self.cfg = make_rms_config(C, eps, x_dtype, y_dtype, residual_dtype, block)
+        self.h = atlas_rms_create(self.cfg)
+        c = self.cfg
+        self._x, self._y, self._r = (_torch_dtype(d) for d in (c.x_dtype, c.y_dtype, c.residual_dtype))
+        self._scales = -(-c.C // c.block) if c.block else 1
+
+    def alloc_outputs(self, M, device):
+        c = self.cfg
+        out = dict(y=torch.empty((M, c.C), dtype=self._y, device=device),
+                   h=torch.empty((M, c.C), dtype=self._r, device=device))
+        if c.y_dtype == ATLAS_E4M3:
+            out["scale"] = torch.empty((M, self._scales), dtype=torch.float32, device=device)
+        return out
+
+    def forward(self, t, out=None, stream=None):
+        """t: dict of device tensors x [M, C] and optional residual [M, C] (may be
+        out["h"]: added to in place) and weight (fp32 [C]).  out["h"] is written
+        where there is a residual, and is returned with it only."""
+        c, x = self.cfg, t["x"]
+        M = x.shape[0]
+        if out is None:
+            out = self.alloc_outputs(M, x.device)
+        r, w, s, dev, shape = t.get("residual"), t.get("weight"), out.get("scale"), _device_of(x), (M, c.C)
+        io = atlas_rms_io(M, _check("x", x, self._x, shape, dev),
+                          None if r is None else _check("residual", r, self._r, shape, dev),
+                          None if w is None else _check("weight", w, torch.float32, (c.C,), dev),
+                          _check("y", out["y"], self._y, shape, dev),
+                          None if r is None else _check("h", out["h"], self._r, shape, dev),
+                          None if s is None else _check("scale", s, torch.float32, (M, self._scales), dev))
+        atlas_rms_forward(self.h, io, _stream_of(dev, stream))
+        return out if r is not None else {n: a for n, a in out.items() if n != "h"}
+
+
+class QuantLinear(_Layer):
+    """y = act(x W + bias) + residual with 4-bit W and a scale (and a zero point)
+    for each `group` rows of a column (include/atlas_qlinear.h).  x_dtype "e4m3": x
+    comes with its scales, as RmsNorm makes them with the same block."""
+    _destroy = staticmethod(atlas_qlinear_destroy)
+
+    def __init__(self, K, N, group=128, zeros=False, act="none", x_dtype="bf16", x_block=0, out_dtype=None):
+        self.cfg = make_qlinear_config(K, N, group, zeros, act, x_dtype, x_block, out_dtype)
+        self.h = atlas_qlinear_create(self.cfg)
+        c = self.cfg
+        self._x, self._out = _torch_dtype(c.x_dtype), _torch_dtype(c.out_dtype)
+        self._groups, self._bytes = -(-c.K // c.group), atlas_qlinear_packed_bytes(self.h)
+        self._scales = -(-c.K // c.x_block) if c.x_block else 1
+
+    def _check_weights(self, q, scales, zeros, dev):
+        c, sn = self.cfg, (self._groups, self.cfg.N)
+        return (_check("q", q, torch.uint8, ((c.K + 1) // 2, c.N), dev), _check("scales", scales, torch.bfloat16, sn, dev),
+                None if zeros is None else _check("zeros", zeros, torch.uint8, sn, dev))
+
+    def quantize(self, W, stream=None):
+        """W [K, N] (fp32 or bf16) -> q, scales and zeros (None without zero points)."""
+        c, dev, d = self.cfg, _device_of(W), W.device
+        if W.dtype not in (torch.float32, torch.bfloat16):
+            raise ValueError(f"W: want float32 or bfloat16, got {W.dtype}")
+        pw = _check("W", W, W.dtype, (c.K, c.N), dev)
+        q = torch.empty(((c.K + 1) // 2, c.N), dtype=torch.uint8, device=d)
+        scales = torch.empty((self._groups, c.N), dtype=torch.bfloat16, device=d)
+        zeros = torch.empty((self._groups, c.N), dtype=torch.uint8, device=d) if c.zeros else None
+        atlas_qlinear_quantize(self.h, pw, ATLAS_BF16 if W.dtype is torch.bfloat16 else ATLAS_F32,
+                               *self._check_weights(q, scales, zeros, dev), _stream_of(dev, stream))
+        return dict(q=q, scales=scales, zeros=zeros)
+
+    def pack(self, q, scales, zeros=None, stream=None):
+        """The weights as forward takes them, laid out once: q [ceil(K / 2), N]
+        bytes, scales (bf16) and zeros (bytes) [ceil(K / group), N]."""
+        dev = _device_of(q)
+        packed = torch.empty(self._bytes, dtype=torch.uint8, device=q.device)
+        atlas_qlinear_pack(self.h, *self._check_weights(q, scales, zeros, dev), packed.data_ptr(), _stream_of(dev, stream))
+        return packed
+
+    def alloc_outputs(self, M, device):
+        return dict(y=torch.empty((M, self.cfg.N), dtype=self._out, device=device))
+
+    def forward(self, t, out=None, stream=None):
+        """t: dict of device tensors x [M, K], W (from pack), for "e4m3" x_scale
+        (fp32 [M, blocks]), and optional bias (fp32 [N]) and residual [M, N] (may be
+        out["y"]: added in place)."""
+        c, x = self.cfg, t["x"]
+        M = x.shape[0]
+        if out is None:
+            out = self.alloc_outputs(M, x.device)
+        s, b, r, dev = t.get("x_scale"), t.get("bias"), t.get("residual"), _device_of(x)
+        io = atlas_qlinear_io(M, _check("x", x, self._x, (M, c.K), dev),
+                              None if s is None else _check("x_scale", s, torch.float32, (M, self._scales), dev),
+                              _check("W", t["W"], torch.uint8, (self._bytes,), dev),
+                              None if b is None else _check("bias", b, torch.float32, (c.N,), dev),
+                              None if r is None else _check("residual", r, self._out, (M, c.N), dev),
+                              _check("y", out["y"], self._out, (M, c.N), dev))
+        atlas_qlinear_forward(self.h, io, _stream_of(dev, stream))
+        return out

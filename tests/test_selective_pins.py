@@ -1,0 +1,235 @@
+"""CPU checks of the selective layer's operators: the fp64 oracle against closed
+forms and torch, and what the C entry points and the binding refuse before any
+CUDA call."""
+import numpy as np
+import pytest
+
+import test_learned_neural_gb300 as tln
+from oracle import layer
+from tests.test_layer_pins import BAD, UNS, _refuses, lib  # noqa: F401
+
+RNG = np.random.default_rng
+
+
+# --------------------------------------------------------------- the oracle
+@pytest.mark.parametrize("K", [1, 2, 4])
+def test_conv_oracle_is_torchs_convolution(K):
+    import torch
+    import torch.nn.functional as F
+    r = RNG(0)
+    x, w, b = r.normal(size=(2, 9, 5)), r.normal(size=(5, K)), r.normal(size=5)
+    y, keep = layer.short_conv(x, w, b, act="silu")
+    pad = F.pad(torch.tensor(x).transpose(1, 2), (K - 1, 0))
+    want = F.silu(F.conv1d(pad, torch.tensor(w)[:, None], torch.tensor(b), groups=5))
+    np.testing.assert_allclose(y, want.transpose(1, 2).numpy(), rtol=1e-12, atol=1e-12)
+    np.testing.assert_array_equal(keep, x[:, 9 - (K - 1):])
+
+
+def test_conv_oracle_cut_and_lengths():
+    r = RNG(1)
+    x, w, c = r.normal(size=(3, 6, 4)), r.normal(size=(4, 4)), r.normal(size=(3, 3, 4))
+    y, keep = layer.short_conv(x, w, cache=c)
+    y1, k1 = layer.short_conv(x[:, :2], w, cache=c)
+    y2, k2 = layer.short_conv(x[:, 2:], w, cache=k1)
+    np.testing.assert_allclose(np.concatenate([y1, y2], 1), y, rtol=1e-12)
+    np.testing.assert_array_equal(k2, keep)
+    yr, kr = layer.short_conv(x, w, cache=c, lens=[0, 2, 6])
+    np.testing.assert_array_equal(kr[0], c[0])
+    np.testing.assert_array_equal(kr[1], k1[1])
+    assert not yr[0].any() and not yr[1, 2:].any()
+
+
+def test_rms_oracle_and_scales():
+    import torch
+    r = RNG(2)
+    x, res, w = r.normal(size=(4, 300)), r.normal(size=(4, 300)), r.normal(size=300)
+    y, h = layer.rms_norm(x, res, w, 1e-5)
+    want = torch.nn.functional.rms_norm(torch.tensor(x + res), (300,), torch.tensor(w), 1e-5)
+    np.testing.assert_allclose(y, want.numpy(), rtol=1e-12)
+    s = layer.e4m3_scales(y, 128)
+    assert s.shape == (4, 3) and s[2, 2] == np.abs(y[2, 256:]).max() / 448
+    assert layer.e4m3_scales(0 * y, 0).tolist() == [[2.0 ** -100 / 448]] * 4
+
+
+def test_quant_weights_by_hand():
+    q = np.array([[0x1f, 0x80], [0x07, 0x9a]], np.uint8)          # K = 3: the last high half is not looked at
+    W = layer.quant_weights(q, np.array([[0.5, 2.0]]), None, 3, 32)
+    np.testing.assert_array_equal(W, [[3.5, -16.0], [-3.5, 0.0], [-0.5, 4.0]])
+    W = layer.quant_weights(q, np.array([[0.5, 2.0]]), np.array([[15, 0]], np.uint8), 3, 32)
+    np.testing.assert_array_equal(W, [[0.0, 0.0], [-7.0, 16.0], [-4.0, 20.0]])
+    y = layer.quant_linear([[1.0, 2.0, 4.0]], W, [[10.0]], 0)
+    np.testing.assert_array_equal(y, [[10 * (-14 - 16), 10 * (32 + 80)]])
+
+
+@pytest.mark.parametrize("share", [1, 2])
+def test_scan_oracle_is_the_sum_over_past_tokens(share):
+    r = RNG(3)
+    B, H, T, dk, dv = 2, 4, 7, 3, 5
+    q, k = r.normal(size=(2, B, H // share, T, dk))
+    v, S0, D = r.normal(size=(B, H, T, dv)), r.normal(size=(B, H, dk, dv)), r.normal(size=H)
+    s, g = layer.step_gates(r.normal(size=(B, H, T)), r.normal(size=H), -np.exp(r.normal(size=H)))
+    y, S = layer.selective_scan(q, k, v, s, g, D, S0=S0, scale=0.7)
+    for b in range(B):
+        for h in range(H):
+            for t in range(T):
+                past = sum(np.prod(g[b, h, j + 1:t + 1]) * s[b, h, j] * (q[b, h // share, t] @ k[b, h // share, j]) * v[b, h, j]
+                           for j in range(t + 1))
+                past = past + np.prod(g[b, h, :t + 1]) * (q[b, h // share, t] @ S0[b, h])
+                np.testing.assert_allclose(y[b, h, t], 0.7 * past + D[h] * v[b, h, t], rtol=1e-10, atol=1e-12)
+    const = layer.selective_scan(q, k, v, np.ones((B, H, T)), np.full((B, H, T), 0.8))
+    want = layer.decay_attention(q, k, v, np.full(H, 0.8))
+    np.testing.assert_allclose(const[0], want[0], rtol=1e-12)
+    np.testing.assert_allclose(const[1], want[1], rtol=1e-12)
+
+
+# ----------------------------------------------------------------- refusals
+@pytest.mark.parametrize("kw,code", [
+    (dict(C=0), BAD), (dict(K=0), BAD), (dict(act=3), BAD), (dict(dtype=2), BAD), (dict(K=9), UNS), (dict(C=(1 << 20) + 1), UNS)])
+def test_conv_create_rejects(lib, kw, code):  # noqa: F811
+    with pytest.raises(tln.AtlasError) as ei:
+        tln.atlas_conv_create(tln.make_conv_config(**{**dict(C=8, K=4), **kw}))
+    assert ei.value.code == code and tln.atlas_conv_last_error(None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(C=0), BAD), (dict(eps=0.0), BAD), (dict(eps=float("inf")), BAD), (dict(eps=float("nan")), BAD), (dict(x_dtype=2), BAD),
+    (dict(residual_dtype=2), BAD), (dict(y_dtype=3), BAD), (dict(block=128), BAD), (dict(y_dtype="e4m3", block=64), BAD),
+    (dict(C=32769), UNS)])
+def test_rms_create_rejects(lib, kw, code):  # noqa: F811
+    with pytest.raises(tln.AtlasError) as ei:
+        tln.atlas_rms_create(tln.make_rms_config(**{**dict(C=8), **kw}))
+    assert ei.value.code == code and tln.atlas_rms_last_error(None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(K=0), BAD), (dict(N=0), BAD), (dict(group=16), BAD), (dict(group=0), BAD), (dict(zeros=2), BAD), (dict(act=-1), BAD),
+    (dict(x_dtype=3), BAD), (dict(x_block=128), BAD), (dict(x_dtype="e4m3", x_block=32), BAD), (dict(out_dtype=2), BAD),
+    (dict(K=(1 << 20) + 1), UNS), (dict(N=(1 << 20) + 1), UNS)])
+def test_qlinear_create_rejects(lib, kw, code):  # noqa: F811
+    with pytest.raises(tln.AtlasError) as ei:
+        tln.atlas_qlinear_create(tln.make_qlinear_config(**{**dict(K=8, N=8), **kw}))
+    assert ei.value.code == code and tln.atlas_qlinear_last_error(None)
+
+
+def test_conv_forward_validates_before_any_cuda_call(lib):  # noqa: F811
+    h = tln.atlas_conv_create(tln.make_conv_config(8, 4))
+    assert lib.atlas_conv_forward(None, None, None) == BAD and lib.atlas_conv_forward(h, None, None) == BAD
+    io = tln.atlas_conv_io(0, 5)
+    _refuses(lib, "conv", h, io, BAD, "B and T")
+    io.B = 2
+    _refuses(lib, "conv", h, io, BAD, "non-NULL")
+    io.x, io.w, io.y, io.ld_x = 1 << 20, 1 << 10, 1 << 21, 7         # never dereferenced: validation fails first
+    _refuses(lib, "conv", h, io, BAD, "ld_x")
+    io.ld_x = 16
+    io.y = (1 << 20) + (2 * 5 - 1) * 32 + 8                          # inside x's last row
+    _refuses(lib, "conv", h, io, BAD, "overlap")
+    io.y, io.cache, io.cache_out = 1 << 21, 1 << 22, (1 << 22) + 16   # a shifted cache
+    _refuses(lib, "conv", h, io, BAD, "cache itself")
+    io.cache_out = (1 << 21) + 32
+    _refuses(lib, "conv", h, io, BAD, "overlap")
+    io.cache_out, io.T = None, (1 << 30) + 1
+    _refuses(lib, "conv", h, io, UNS, "2^30")
+    tln.atlas_conv_destroy(h)
+    lib.atlas_conv_destroy(None)
+
+
+def test_rms_forward_validates_before_any_cuda_call(lib):  # noqa: F811
+    h = tln.atlas_rms_create(tln.make_rms_config(16, y_dtype="e4m3", block=128))
+    assert lib.atlas_rms_forward(None, None, None) == BAD and lib.atlas_rms_forward(h, None, None) == BAD
+    io = tln.atlas_rms_io(0)
+    _refuses(lib, "rms", h, io, BAD, "M must")
+    io.M = 3
+    _refuses(lib, "rms", h, io, BAD, "non-NULL")
+    io.x, io.y = 1 << 20, 1 << 21
+    _refuses(lib, "rms", h, io, BAD, "scale goes with")
+    io.scale, io.y = 1 << 22, 1 << 20
+    _refuses(lib, "rms", h, io, BAD, "y may be x")
+    io.y, io.h, io.residual = 1 << 21, (1 << 23) + 32, 1 << 23
+    _refuses(lib, "rms", h, io, BAD, "h may be")
+    io.h, io.scale = 1 << 23, (1 << 23) + 4
+    _refuses(lib, "rms", h, io, BAD, "scale must not")
+    tln.atlas_rms_destroy(h)
+    h = tln.atlas_rms_create(tln.make_rms_config(16))
+    _refuses(lib, "rms", h, io, BAD, "scale goes with")
+    tln.atlas_rms_destroy(h)
+    lib.atlas_rms_destroy(None)
+
+
+def test_qlinear_validates_before_any_cuda_call(lib):  # noqa: F811
+    h = tln.atlas_qlinear_create(tln.make_qlinear_config(100, 40, group=32, zeros=True, x_dtype="e4m3"))
+    assert lib.atlas_qlinear_forward(None, None, None) == BAD and lib.atlas_qlinear_forward(h, None, None) == BAD
+    io = tln.atlas_qlinear_io(0)
+    _refuses(lib, "qlinear", h, io, BAD, "M must")
+    io.M = 3
+    _refuses(lib, "qlinear", h, io, BAD, "non-NULL")
+    io.x, io.y, io.W = 1 << 20, 1 << 21, (1 << 22) + 8
+    _refuses(lib, "qlinear", h, io, BAD, "x_scale goes with")
+    io.x_scale = 1 << 23
+    _refuses(lib, "qlinear", h, io, BAD, "aligned")
+    io.W, io.residual = 1 << 22, (1 << 21) + 2
+    _refuses(lib, "qlinear", h, io, BAD, "residual itself")
+    io.residual, io.M = None, 4194241
+    _refuses(lib, "qlinear", h, io, UNS, "4194240")
+    # three 16-column tiles, two steps of 64, four groups: 512 bytes a tile and step, 40 a tile and group
+    assert tln.atlas_qlinear_packed_bytes(h) == 3 * 2 * 512 + 4 * 3 * 40
+    assert tln.atlas_qlinear_workspace_bytes(h, 3) == 3 * 128 and tln.atlas_qlinear_workspace_bytes(h, 0) == 0
+    Q, P = lib.atlas_qlinear_quantize, lib.atlas_qlinear_pack
+    assert Q(None, 64, 0, 64, 64, 64, None) == BAD and P(None, 64, 64, 64, 64, None) == BAD
+    for args in ((None, 0, 64, 1 << 20, 1 << 21), (1 << 30, 2, 64, 1 << 20, 1 << 21), (1 << 30, 0, 64, 1 << 20, None),
+                 (1 << 20, 0, 64, (1 << 20) + 100, 1 << 25)):
+        assert Q(h, *args, None) == BAD and tln.atlas_qlinear_last_error(h)
+    for args in ((64, 1 << 20, 1 << 21, None), (64, 1 << 20, None, 1 << 22), (64, 1 << 20, 1 << 21, (1 << 22) + 4),
+                 (1 << 22, 1 << 20, 1 << 21, 1 << 22)):
+        assert P(h, *args, None) == BAD and tln.atlas_qlinear_last_error(h)
+    tln.atlas_qlinear_destroy(h)
+    lib.atlas_qlinear_destroy(None)
+
+
+def test_runner_refuses_wrong_tensors(lib):  # noqa: F811
+    import torch
+    from test_learned_neural_gb300.runner import QuantLinear, RmsNorm, ShortConv
+    z = torch.zeros
+    with pytest.raises(ValueError):
+        ShortConv(8, 4).forward(dict(x=z(1, 5, 8).bfloat16(), w=z(8, 4)), out=dict(y=z(1, 5, 8).bfloat16(), cache=None))
+    with pytest.raises(ValueError):
+        RmsNorm(8).forward(dict(x=z(3, 9).bfloat16()), out=dict(y=z(3, 8).bfloat16()))
+    with pytest.raises(ValueError):
+        QuantLinear(8, 4).forward(dict(x=z(3, 8).bfloat16(), W=z(10)), out=dict(y=z(3, 4).bfloat16()))
+    with pytest.raises(ValueError):
+        QuantLinear(8, 4).quantize(z(8, 4).half())
+
+
+class Strided:
+    """A tensor on a device that this machine need not have, with strides."""
+
+    def __init__(self, shape, stride):
+        import torch
+        self.shape, self._stride, self.dtype, self.is_cuda, self.device = shape, stride, torch.bfloat16, True, "cuda"
+
+    def is_contiguous(self):
+        return False
+
+    def stride(self):
+        return self._stride
+
+    def data_ptr(self):
+        return 1 << 20
+
+
+@pytest.mark.parametrize("shape,stride,ld", [
+    ((2, 5, 8), (100, 20, 1), 20), ((2, 1, 8), (20, 999, 1), 20), ((1, 5, 8), (7, 20, 1), 20), ((1, 1, 8), (3, 2, 1), 8),
+    ((2, 5, 3, 4), (100, 20, 4, 1), 20), ((2, 5, 1, 4), (100, 20, 77, 1), 20)])
+def test_rows_inside_wider_ones(shape, stride, ld):
+    from test_learned_neural_gb300 import runner
+    import torch
+    assert runner._check_rows("x", Strided(shape, stride), torch.bfloat16, shape, None) == (1 << 20, ld)
+
+
+@pytest.mark.parametrize("shape,stride", [
+    ((2, 5, 8), (100, 20, 2)), ((2, 5, 8), (99, 20, 1)), ((2, 5, 8), (40, 4, 1)), ((2, 5, 3, 4), (100, 20, 5, 1)),
+    ((2, 5, 8), (0, 0, 1)), ((2, 5, 8), (5 << 31, 1 << 31, 1))])
+def test_other_strides_are_refused(shape, stride):
+    from test_learned_neural_gb300 import runner
+    import torch
+    with pytest.raises(ValueError, match="slice"):
+        runner._check_rows("x", Strided(shape, stride), torch.bfloat16, shape, None)

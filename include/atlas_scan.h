@@ -1,0 +1,122 @@
+/*
+ * atlas_scan.h -- C ABI of the selective scan: a plain matrix memory whose
+ * decay and step come with every token, for prompts and single tokens.  It is
+ * atlas_decay.h's attention with the gates of atlas_prologue.h (or those of a
+ * state space layer) in place of a constant decay for each head.
+ *
+ * The operation, per batch row b and value head h, token by token:
+ *
+ *   S_t = g_t S_{t-1} + s_t k_t^T v_t      S: d_k x d_v
+ *   y_t = scale * q_t S_t + D_h v_t        (the memory after token t's update)
+ *
+ * Gates, fp32:
+ *   ATLAS_GATES_MEMORY  s = theta, g = 1 - alpha: the outputs of
+ *                       atlas_prologue.h, alpha in [0, 1], theta any
+ *   ATLAS_GATES_STEP    s = log(1 + exp(dt + dt_bias_h)), g = exp(s A_h): the
+ *                       discretised state space model, A <= 0, dt any
+ * q and k (the model's C and B) have H / share heads: value head h uses
+ * query/key head h / share.  A row with lens[b] tokens stops there: its later
+ * read-outs are zero and its final state is that after token lens[b] - 1 (S0
+ * when lens[b] is 0).  The final state carries a sequence over to the next call,
+ * down to one token per call.
+ *
+ * Layouts: ATLAS_LAYOUT_HEADS  q, k, v [B][heads][T][d], gates [B][H][T]
+ *          ATLAS_LAYOUT_TOKENS q, k, v [B][T][heads][d], gates [B][T][H]; the
+ *                              tokens may lie further apart (ld_qk, ld_v,
+ *                              ld_gates): slices of atlas_conv.h's output, and of
+ *                              a projection's
+ *
+ * Execution, precision, capture: as in atlas_decay.h.  Products of decays are
+ * formed by multiplying the decays themselves, in fp32, so that a decay of 0 (a
+ * reset) is exact.
+ *
+ * Inputs: tokens past lens[b] are never used, whatever they and their gates hold.
+ * A NaN or an infinity in a live token (its gates' products among them) reaches
+ * nothing but its own row and head (for q and k the value heads that use them),
+ * there the later read-outs and the final state and, in a call that works in
+ * chunks, read-outs up to 127 tokens before it too.
+ *
+ * Errors: the status codes of atlas_mem.h; atlas_scan_last_error gives the
+ * message.  Validation failures return before any CUDA call.
+ */
+#ifndef ATLAS_SCAN_H
+#define ATLAS_SCAN_H
+
+#include <stddef.h>
+
+#include "atlas_decay.h"   /* ATLAS_LAYOUT_* */
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+#define ATLAS_GATES_MEMORY 0
+#define ATLAS_GATES_STEP 1
+
+typedef struct {
+    int H;            /* value heads (>= 1) */
+    int d_k, d_v;     /* head widths: 1 <= d_k <= 256, 1 <= d_v <= 1024 */
+    int share;        /* value heads per query/key head; divides H */
+    int gates;        /* ATLAS_GATES_* */
+    int qkv_dtype;    /* ATLAS_F32 or ATLAS_BF16: type of q, k, v */
+    int y_dtype;      /* ATLAS_F32 or ATLAS_BF16: type of y */
+    int qkv_layout;   /* ATLAS_LAYOUT_* of q, k, v and the gates */
+    int y_layout;     /* ATLAS_LAYOUT_* of y */
+    float scale;      /* factor of the read-out, finite */
+} atlas_scan_config;
+
+typedef struct atlas_scan_handle atlas_scan_handle;
+
+/* Tensors of one call, all DEVICE pointers owned by the caller. */
+typedef struct {
+    int B, T;               /* B >= 1, 1 <= T <= 2^30; B * H <= 65535 unless T <= 20 */
+    int ld_qk, ld_v;        /* ATLAS_LAYOUT_TOKENS: values between neighbouring tokens of q and of k, and of v (a batch
+                             * row is T of them); 0: dense */
+    int ld_gates;           /* the same of the gates */
+    const void* q;          /* H / share heads of d_k, qkv_layout, qkv_dtype */
+    const void* k;          /* H / share heads of d_k, qkv_layout, qkv_dtype */
+    const void* v;          /* H heads of d_v, qkv_layout, qkv_dtype */
+    const float* step;      /* theta, or dt */
+    const float* alpha;     /* ATLAS_GATES_MEMORY: alpha, else NULL */
+    const float* A;         /* ATLAS_GATES_STEP: [H], else NULL */
+    const float* dt_bias;   /* ATLAS_GATES_STEP: [H], NULL: 0; else NULL */
+    const float* D;         /* [H]; NULL: 0 */
+    const int* lens;        /* [B] tokens of each row, clamped to [0, T]; NULL: all T */
+    const float* S0;        /* [B][H][d_k][d_v] initial states; NULL: zero */
+    void* y;                /* H heads of d_v, y_layout, y_dtype; overlaps no input */
+    float* S_out;           /* [B][H][d_k][d_v] final states, may be S0 itself; NULL: not wanted */
+} atlas_scan_io;
+
+/* Validate the config and make a handle (no CUDA call).  INVALID_ARG or
+ * UNSUPPORTED with a message from atlas_scan_last_error(NULL). */
+int atlas_scan_create(const atlas_scan_config* cfg, atlas_scan_handle** out);
+
+/* One call; stream is a cudaStream_t (NULL = the default stream).  Grows the
+ * handle's workspace to atlas_scan_workspace_bytes on first use (cudaMalloc);
+ * the stream of the last call on h must still exist then. */
+int atlas_scan_forward(atlas_scan_handle* h, const atlas_scan_io* io, void* stream);
+
+/* Device workspace a call of this size may need: the gates' products, and what
+ * atlas_decay_workspace_bytes counts. */
+size_t atlas_scan_workspace_bytes(const atlas_scan_handle* h, int B, int T);
+
+/* Wait for the last forward on h and return its device status: ATLAS_OK, or
+ * ATLAS_ERR_TIMEOUT if a bounded wait of the tensor-core kernels gave up (the
+ * outputs of that call are then not valid).  Clears the status word. */
+int atlas_scan_status(atlas_scan_handle* h);
+
+/* How the last forward on h ran: 0 = token by token, 1 = fp32 chunks, 2 =
+ * tensor-core chunks, -1 = none yet. */
+int atlas_scan_last_path(const atlas_scan_handle* h);
+
+/* Message of the last failure on h, or of the last failed create when h is NULL. */
+const char* atlas_scan_last_error(const atlas_scan_handle* h);
+
+/* Free the handle and its workspace (NULL is a no-op). */
+void atlas_scan_destroy(atlas_scan_handle* h);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif

@@ -23,10 +23,12 @@ STATUS_NAMES = {0: "OK", 1: "INVALID_ARG", 2: "UNSUPPORTED", 3: "CUDA", 4: "OOM"
 
 ATLAS_LAYOUT_HEADS, ATLAS_LAYOUT_TOKENS = 0, 1
 ATLAS_NORM_CHANNELS_LAST, ATLAS_NORM_HEADS = 0, 1
+ATLAS_GATES_MEMORY, ATLAS_GATES_STEP = 0, 1
 ATLAS_ACT_NONE, ATLAS_ACT_SILU, ATLAS_ACT_GELU = 0, 1, 2
 
 # exported symbols, as declared in include/atlas_mem.h, atlas_prologue.h,
-# atlas_decay.h, atlas_norm.h, atlas_linear.h, atlas_conv.h, atlas_rms.h and atlas_qlinear.h
+# atlas_decay.h, atlas_norm.h, atlas_linear.h, atlas_conv.h, atlas_rms.h, atlas_qlinear.h
+# and atlas_scan.h
 EXPORTS = ("atlas_mem_create", "atlas_mem_forward", "atlas_mem_forward_host", "atlas_mem_forward_noalloc",
            "atlas_mem_status",
            "atlas_mem_workspace_bytes", "atlas_mem_last_launches", "atlas_mem_last_error", "atlas_mem_destroy",
@@ -43,7 +45,9 @@ EXPORTS = ("atlas_mem_create", "atlas_mem_forward", "atlas_mem_forward_host", "a
            "atlas_rms_create", "atlas_rms_forward", "atlas_rms_last_error", "atlas_rms_destroy",
            "atlas_qlinear_create", "atlas_qlinear_quantize", "atlas_qlinear_packed_bytes", "atlas_qlinear_pack",
            "atlas_qlinear_forward", "atlas_qlinear_workspace_bytes", "atlas_qlinear_last_error",
-           "atlas_qlinear_destroy")
+           "atlas_qlinear_destroy",
+           "atlas_scan_create", "atlas_scan_forward", "atlas_scan_workspace_bytes", "atlas_scan_status",
+           "atlas_scan_last_path", "atlas_scan_last_error", "atlas_scan_destroy")
 
 
 class atlas_mem_config(ctypes.Structure):
@@ -135,6 +139,16 @@ class atlas_qlinear_io(ctypes.Structure):
     _fields_ = [("M", ctypes.c_int)] + [(n, _vp) for n in ("x", "x_scale", "W", "bias", "residual", "y")]
 
 
+class atlas_scan_config(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("H", "d_k", "d_v", "share", "gates", "qkv_dtype", "y_dtype", "qkv_layout",
+                                            "y_layout")] + [("scale", ctypes.c_float)]
+
+
+class atlas_scan_io(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("B", "T", "ld_qk", "ld_v", "ld_gates")] + [
+        (n, _vp) for n in ("q", "k", "v", "step", "alpha", "A", "dt_bias", "D", "lens", "S0", "y", "S_out")]
+
+
 class AtlasError(RuntimeError):
     def __init__(self, code, msg):
         super().__init__(f"{STATUS_NAMES.get(code, code)}: {msg}")
@@ -187,7 +201,8 @@ def load(path: str = LIB_PATH):
                                ("linear", atlas_linear_config, atlas_linear_io, 1),
                                ("conv", atlas_conv_config, atlas_conv_io, 0),
                                ("rms", atlas_rms_config, atlas_rms_io, 0),
-                               ("qlinear", atlas_qlinear_config, atlas_qlinear_io, 1)):
+                               ("qlinear", atlas_qlinear_config, atlas_qlinear_io, 1),
+                               ("scan", atlas_scan_config, atlas_scan_io, 2)):
         for name, args, res in (
                 ("create", [ctypes.POINTER(cfg), ctypes.POINTER(ctypes.c_void_p)], ctypes.c_int),
                 ("forward", [ctypes.c_void_p, ctypes.POINTER(io), ctypes.c_void_p], ctypes.c_int),
@@ -471,9 +486,42 @@ def atlas_qlinear_workspace_bytes(h, M) -> int:
     return load().atlas_qlinear_workspace_bytes(h, M)
 
 
+def atlas_scan_create(cfg: atlas_scan_config):
+    lib = load()
+    return _created(lib.atlas_scan_create, lib.atlas_scan_last_error, cfg)
+
+
+def atlas_scan_forward(h, io: atlas_scan_io, stream: int = 0):
+    lib = load()
+    rc = lib.atlas_scan_forward(h, ctypes.byref(io), stream)
+    if rc:
+        raise AtlasError(rc, lib.atlas_scan_last_error(h).decode())
+
+
+def atlas_scan_workspace_bytes(h, B, T) -> int:
+    return load().atlas_scan_workspace_bytes(h, B, T)
+
+
+def atlas_scan_status(h) -> int:
+    return load().atlas_scan_status(h)
+
+
+def atlas_scan_last_path(h) -> int:
+    return load().atlas_scan_last_path(h)
+
+
+def atlas_scan_last_error(h) -> str:
+    return load().atlas_scan_last_error(h).decode()
+
+
+def atlas_scan_destroy(h):
+    load().atlas_scan_destroy(h)
+
+
 _DTYPES = {"f32": ATLAS_F32, "bf16": ATLAS_BF16, "e4m3": ATLAS_E4M3}
 _ACTS = {"none": ATLAS_ACT_NONE, "silu": ATLAS_ACT_SILU, "gelu": ATLAS_ACT_GELU}
 _LAYOUTS = {"heads": ATLAS_LAYOUT_HEADS, "tokens": ATLAS_LAYOUT_TOKENS}
+_GATES = {"memory": ATLAS_GATES_MEMORY, "step": ATLAS_GATES_STEP}
 _NORM_LAYOUTS = {"channels_last": ATLAS_NORM_CHANNELS_LAST, "heads": ATLAS_NORM_HEADS}
 
 
@@ -496,6 +544,14 @@ def make_linear_config(K, N, act="none", in_dtype="bf16", out_dtype=None) -> atl
     it = _DTYPES.get(in_dtype, in_dtype)
     ot = it if out_dtype is None else _DTYPES.get(out_dtype, out_dtype)
     return atlas_linear_config(K, N, _ACTS.get(act, act), it, ot)
+
+
+def make_scan_config(H, d_k, d_v, share=1, gates="memory", qkv_dtype="bf16", y_dtype=None, qkv_layout="heads",
+                     y_layout="heads", scale=1.0) -> atlas_scan_config:
+    dt = _DTYPES.get(qkv_dtype, qkv_dtype)
+    yt = dt if y_dtype is None else _DTYPES.get(y_dtype, y_dtype)
+    return atlas_scan_config(H, d_k, d_v, share, _GATES.get(gates, gates), dt, yt, _LAYOUTS.get(qkv_layout, qkv_layout),
+                             _LAYOUTS.get(y_layout, y_layout), scale)
 
 
 def make_conv_config(C, K, act="silu", dtype="bf16") -> atlas_conv_config:

@@ -1,5 +1,6 @@
-// Linear attention with a decay for each head: host side, and the kernels
-// that run in fp32 arithmetic (decay_common.cuh has the formulas).
+// Linear attention with a decay for each head, and the selective scan (its GATED
+// instances): host side, and the kernels that run in fp32 arithmetic
+// (decay_common.cuh has the formulas).
 #include <math.h>
 
 #include <algorithm>
@@ -10,13 +11,14 @@
 #include "tc2.cuh"
 
 using namespace layer;
+using decay::Gates;
 using decay::Geom;
+using decay::kMostTokens;
 using decay::Ptrs;
 
 namespace {
 
 constexpr int kSlice = 64;         // d_v columns per CTA
-constexpr int kMostTokens = 1 << 30;
 
 // ------------------------------------------------- token by token
 // A CTA holds kSlice columns of one state in registers: thread (rg, c4) rows
@@ -24,8 +26,8 @@ constexpr int kMostTokens = 1 << 30;
 // written once, by 256-byte row segments.  256 rows x 16 heads of 128 x 128, one
 // token: 81 us for 541 MB, 98 % of the copy bandwidth.  8 rows x 8 heads of 64 x 64:
 // 7 us, of which 5 are the host's call.
-template <typename TI, typename TO, int RPT, int V>
-__global__ void __launch_bounds__(256) k_decay_step(Geom g, Ptrs p) {
+template <typename TI, typename TO, int RPT, int V, bool GATED>
+__global__ void __launch_bounds__(256) k_decay_step(Geom g, Ptrs p, Gates gates) {
   constexpr int CL = kSlice / V;             // threads along the columns
   constexpr int RG = 256 / CL;               // row groups
   extern __shared__ float sm[];
@@ -37,7 +39,9 @@ __global__ void __launch_bounds__(256) k_decay_step(Geom g, Ptrs p) {
   const int cl = tid % CL, rg = tid / CL, col = sl * kSlice + cl * V;
   const bool on = col < g.d_v;
   const int n = decay::live_tokens(g, p, b);
-  const float gam = p.decay[h];
+  float gam = 1.f, step = 1.f, skip = 0.f;
+  if constexpr (!GATED) gam = p.decay[h];
+  else if (p.D) skip = p.D[h];
   const size_t base = (size_t)unit * g.d_k * g.d_v + col;
   float S[RPT][V];
 #pragma unroll
@@ -55,9 +59,11 @@ __global__ void __launch_bounds__(256) k_decay_step(Geom g, Ptrs p) {
   const TI* v = (const TI*)p.v + b * g.v_b + h * g.v_h;
   TO* y = (TO*)p.y + b * g.y_b + h * g.y_h;
   for (int t = 0; t < n; ++t) {
+    if constexpr (GATED) decay::gates_of(gates, b, h, t, gam, step);
     for (int i = tid; i < g.d_k; i += 256) {
       qs[i] = to_f32(q[t * g.qk_t + i]);
       ks[i] = to_f32(k[t * g.qk_t + i]);
+      if constexpr (GATED) ks[i] *= step;
     }
     float vt[V], acc[V];
 #pragma unroll
@@ -83,7 +89,9 @@ __global__ void __launch_bounds__(256) k_decay_step(Geom g, Ptrs p) {
       float s = 0.f;
 #pragma unroll
       for (int r = 0; r < RG; ++r) s += part[r * kSlice + tid];
-      y[t * g.y_t + sl * kSlice + tid] = from_f32<TO>(g.scale * s);
+      s *= g.scale;
+      if (GATED && p.D) s = fmaf(skip, to_f32(v[t * g.v_t + sl * kSlice + tid]), s);
+      y[t * g.y_t + sl * kSlice + tid] = from_f32<TO>(s);
     }
   }
   // read-outs past the row's length
@@ -105,7 +113,9 @@ __global__ void __launch_bounds__(256) k_decay_step(Geom g, Ptrs p) {
 // contribution to the next segment's start.  Bound by the latency of its fp32
 // loops where blocks are few (chunk_blocks has how many an SM holds): 3 rows x 6 heads of ragged
 // lengths to 1501, d 48: 41 us in three overlapped launches (states 15, scan 8, read-outs 32).
-template <typename TI, typename TO, int C, bool READ>
+// GATED: pw holds the tokens' products (decay_common.cuh) in place of powers; those
+// of a run's own tokens are formed by each row's threads from the decays.
+template <typename TI, typename TO, int C, bool READ, bool GATED>
 __global__ void __launch_bounds__(256, C == 64 ? 3 : 1) k_decay_chunk(Geom g, Ptrs p) {
   extern __shared__ float sm[];
   const int dk4 = (g.d_k + 3) & ~3, ldk = dk4 + 4;
@@ -113,8 +123,8 @@ __global__ void __launch_bounds__(256, C == 64 ? 3 : 1) k_decay_chunk(Geom g, Pt
   float* Ks = sm;                   // [C][ldk]
   float* Vs = Ks + C * ldk;         // [C][LDV]
   float* Ss = Vs + C * LDV;         // [dk4][LDV]
-  float* pw = Ss + dk4 * LDV;       // g^0 .. g^C, padded to a multiple of 4
-  float* Qs = pw + C + 4;           // [C][ldk]
+  float* pw = Ss + dk4 * LDV;       // g^0 .. g^C, padded to a multiple of 4; GATED: g, s, L, R of C tokens
+  float* Qs = pw + (GATED ? 4 * C : C + 4);   // [C][ldk]
   float* Ps = Qs + C * ldk;         // [C][LDP]
   const int s = blockIdx.x, sl = blockIdx.y, unit = blockIdx.z;
   const int b = unit / g.H, h = unit % g.H, tid = threadIdx.x, tx = tid % 16, ty = tid / 16;
@@ -122,7 +132,9 @@ __global__ void __launch_bounds__(256, C == 64 ? 3 : 1) k_decay_chunk(Geom g, Pt
   tc::grid_dependents_launch();
   const int live = decay::live_tokens(g, p, b);
   const int t_lo = s * g.seg, t_hi = min(g.T, t_lo + g.seg), t_live = min(t_hi, max(live, t_lo));
-  const float l2g = log2f(p.decay[h]);
+  float l2g = 0.f, seg_total = 1.f, skip = 0.f;
+  if constexpr (!GATED) l2g = log2f(p.decay[h]);
+  else if (p.D) skip = p.D[h];
   const int c0 = sl * kSlice, cols = min(kSlice, g.d_v - c0);
   const TI* q = (const TI*)p.q + b * g.qk_b + (h / g.share) * g.qk_h;
   const TI* k = (const TI*)p.k + b * g.qk_b + (h / g.share) * g.qk_h;
@@ -135,10 +147,15 @@ __global__ void __launch_bounds__(256, C == 64 ? 3 : 1) k_decay_chunk(Geom g, Pt
     const int r = i / kSlice, c = i % kSlice;
     Ss[r * LDV + c] = start && r < g.d_k && c < cols ? start[(size_t)r * g.d_v + c0 + c] : 0.f;
   }
-  for (int i = tid; i <= C; i += 256) pw[i] = decay::power(l2g, i);
+  if constexpr (!GATED)
+    for (int i = tid; i <= C; i += 256) pw[i] = decay::power(l2g, i);
+  const float* records = nullptr;
+  if constexpr (GATED)
+    records = p.records + (size_t)unit * ((g.T + decay::kGateTokens - 1) / decay::kGateTokens) * decay::GATE_VALUES;
 
   // four values at a time where every row starts on their boundary
-  const bool vec = g.d_k % 4 == 0 && g.d_v % 4 == 0 && ((uintptr_t)p.q | (uintptr_t)p.k | (uintptr_t)p.v) % 16 == 0;
+  const bool vec = g.d_k % 4 == 0 && g.d_v % 4 == 0 && (g.qk_t | g.v_t) % 4 == 0 &&
+                   ((uintptr_t)p.q | (uintptr_t)p.k | (uintptr_t)p.v) % 16 == 0;
   const bool y_vec = (uintptr_t)p.y % 16 == 0;
   for (int t0 = t_lo; t0 < t_live; t0 += C) {
     const int n = min(C, t_live - t0);
@@ -165,7 +182,14 @@ __global__ void __launch_bounds__(256, C == 64 ? 3 : 1) k_decay_chunk(Geom g, Pt
       }
       load4(v + (size_t)(t0 + r) * g.v_t, 4 * tx, cols, r < n, Vs + r * LDV);
     }
+    if constexpr (GATED) {
+      const float* rec = records + (size_t)(t0 / decay::kGateTokens) * decay::GATE_VALUES + t0 % decay::kGateTokens;
+      for (int i = tid; i < 4 * C; i += 256) pw[i] = rec[i / C * decay::kGateTokens + i % C];
+    }
     __syncthreads();
+    // GATED: the arrays, and the product of g over a run
+    const float *gs = pw, *ss = pw + C, *Ls = pw + 2 * C, *Rs = pw + 3 * C;
+    const float run0 = GATED ? Ls[decay::kRun - 1] : 1.f, run1 = GATED && C == 64 ? Ls[C - 1] : 1.f;
     if constexpr (READ) {
       // P = (Q K^T) under the decay mask
       float a[NI][NI] = {};
@@ -187,9 +211,30 @@ __global__ void __launch_bounds__(256, C == 64 ? 3 : 1) k_decay_chunk(Geom g, Pt
 #pragma unroll
         for (int j = 0; j < NI; ++j) {
           const int ri = ty + 16 * i, cj = tx + 16 * j;
-          Ps[ri * LDP + cj] = cj <= ri ? a[i][j] * pw[ri - cj] : 0.f;
+          if constexpr (!GATED) {
+            Ps[ri * LDP + cj] = cj <= ri ? a[i][j] * pw[ri - cj] : 0.f;
+          } else {
+            const float w = cj / decay::kRun < ri / decay::kRun ? Ls[ri] * Rs[cj] : 1.f;   // (C = 64: the run before)
+            Ps[ri * LDP + cj] = cj <= ri ? a[i][j] * w : 0.f;
+          }
         }
       __syncthreads();
+      if constexpr (GATED) {
+        // a row's own run, eight columns a thread: times s_j and the decays between
+        const int r = tid / 4, lr = r % decay::kRun, lo = 8 * (tid % 4);
+        if (r < C && lo <= lr) {
+          float* row = Ps + r * LDP + r - lr;
+          const float *gr = gs + r - lr, *sr = ss + r - lr;
+          const int hi = min(lr, lo + 7);
+          float w = 1.f;
+          for (int m = lr; m > hi; --m) w *= gr[m];
+          for (int c = hi; c >= lo; --c) {
+            row[c] *= w * sr[c];
+            w *= gr[c];
+          }
+        }
+        __syncthreads();
+      }
       float o[NI][4] = {};
       for (int kk = 0; kk < dk4; kk += 4) {
         float4 sv[4];
@@ -207,7 +252,10 @@ __global__ void __launch_bounds__(256, C == 64 ? 3 : 1) k_decay_chunk(Geom g, Pt
 #pragma unroll
       for (int i = 0; i < NI; ++i)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) o[i][e] *= pw[ty + 16 * i + 1];
+        for (int e = 0; e < 4; ++e) {
+          const int r = ty + 16 * i;
+          o[i][e] *= GATED ? (r < decay::kRun ? 1.f : run0) * Ls[r] : pw[r + 1];
+        }
       for (int j = 0; j < C; j += 4) {
         float4 vv[4];
 #pragma unroll
@@ -226,7 +274,10 @@ __global__ void __launch_bounds__(256, C == 64 ? 3 : 1) k_decay_chunk(Geom g, Pt
         const int r = ty + 16 * i;
         if (r >= n) continue;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) o[i][e] *= g.scale;
+        for (int e = 0; e < 4; ++e) {
+          o[i][e] *= g.scale;
+          if (GATED && p.D) o[i][e] = fmaf(skip, Vs[r * LDV + 4 * tx + e], o[i][e]);
+        }
         TO* dst = y + (t0 + r) * g.y_t + 4 * tx;
         if (vec && y_vec && 4 * tx + 4 <= cols) {
           store_vec<4>(dst, o[i]);
@@ -239,14 +290,16 @@ __global__ void __launch_bounds__(256, C == 64 ? 3 : 1) k_decay_chunk(Geom g, Pt
       __syncthreads();   // every read of the state is done
     }
     // S = g^n S + sum_j g^{n-1-j} k_j v_j
+    const float all = GATED ? run0 * run1 : pw[n];
+    if constexpr (GATED) seg_total *= all;
     for (int r0 = 4 * ty; r0 < dk4; r0 += 64) {
       float a[4][4];
 #pragma unroll
       for (int r = 0; r < 4; ++r)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) a[r][e] = pw[n] * Ss[(r0 + r) * LDV + 4 * tx + e];
+        for (int e = 0; e < 4; ++e) a[r][e] = all * Ss[(r0 + r) * LDV + 4 * tx + e];
       for (int j = 0; j < n; ++j) {
-        const float w = pw[n - 1 - j];
+        const float w = GATED ? Rs[j] * (j < decay::kRun ? run1 : 1.f) : pw[n - 1 - j];
         const float4 kr = *reinterpret_cast<const float4*>(Ks + j * ldk + r0);
         const float4 vv = *reinterpret_cast<const float4*>(Vs + j * LDV + 4 * tx);
         const float kw[4] = {kr.x * w, kr.y * w, kr.z * w, kr.w * w}, vc[4] = {vv.x, vv.y, vv.z, vv.w};
@@ -270,6 +323,7 @@ __global__ void __launch_bounds__(256, C == 64 ? 3 : 1) k_decay_chunk(Geom g, Pt
     if (s == g.nseg - 1 && p.S_out) dst = p.S_out + unit * sq;
   } else {
     dst = p.seg + ((size_t)unit * g.nseg + s + 1) * sq;
+    if (GATED && sl == 0 && tid == 0) p.seg_total[(size_t)unit * g.nseg + s] = seg_total;
   }
   if (dst)
     for (int i = tid; i < g.d_k * kSlice; i += 256) {
@@ -280,6 +334,7 @@ __global__ void __launch_bounds__(256, C == 64 ? 3 : 1) k_decay_chunk(Geom g, Pt
 
 // Segment starts from the segments' own contributions: slot s + 1 holds
 // segment s's; start_0 = S0, start_{s+1} = g^{n_s} start_s + slot_{s+1}.
+template <bool GATED>
 __global__ void __launch_bounds__(256) k_decay_scan(Geom g, Ptrs p) {
   const size_t sq = (size_t)g.d_k * g.d_v;
   const int unit = blockIdx.y;
@@ -288,11 +343,12 @@ __global__ void __launch_bounds__(256) k_decay_scan(Geom g, Ptrs p) {
   tc::grid_dependents_launch();
   if (e >= sq) return;
   const int live = decay::live_tokens(g, p, unit / g.H);
-  const float l2g = log2f(p.decay[unit % g.H]);
+  const float l2g = GATED ? 0.f : log2f(p.decay[unit % g.H]);
   float* slot = p.seg + (size_t)unit * g.nseg * sq + e;
   float run = p.S0 ? p.S0[unit * sq + e] : 0.f;
   slot[0] = run;
-  const float full = decay::power(l2g, g.seg);
+  const float full = GATED ? 1.f : decay::power(l2g, g.seg);
+  const float* total = GATED ? p.seg_total + (size_t)unit * g.nseg : nullptr;
   constexpr int A = 16;   // loads in flight
   for (int s0 = 0; s0 + 1 < g.nseg; s0 += A) {
     float v[A];
@@ -302,10 +358,71 @@ __global__ void __launch_bounds__(256) k_decay_scan(Geom g, Ptrs p) {
     for (int i = 0; i < A; ++i) {
       const int s = s0 + i, n = min(g.seg, max(0, live - s * g.seg));
       if (s + 1 >= g.nseg) break;
-      run = fmaf(n == g.seg ? full : decay::power(l2g, n), run, v[i]);
+      run = fmaf(GATED ? total[s] : n == g.seg ? full : decay::power(l2g, n), run, v[i]);
       slot[(size_t)(s + 1) * sq] = run;
     }
   }
+}
+
+// The selective scan's records: a warp each, four runs of 32 tokens.
+__global__ void __launch_bounds__(256) k_scan_gates(Geom g, Gates gates, const int* lens, float* __restrict__ records,
+                                                    float* __restrict__ totals, size_t n) {
+  const size_t i = (size_t)blockIdx.x * 8 + threadIdx.x / 32;
+  const int lane = threadIdx.x % 32, chunks = (g.T + decay::kGateTokens - 1) / decay::kGateTokens;
+  tc::grid_dependency_wait();
+  tc::grid_dependents_launch();
+  if (i >= n) return;
+  const int unit = (int)(i / chunks), t0 = (int)(i % chunks) * decay::kGateTokens, b = unit / g.H, h = unit % g.H;
+  const int live = lens ? min(max(lens[b], 0), g.T) : g.T;
+  float* rec = records + i * decay::GATE_VALUES + lane;
+  float R[4], all[4];
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    const int t = t0 + r * decay::kRun + lane;
+    float d = 1.f, s = 0.f;
+    if (t < live) decay::gates_of(gates, b, h, t, d, s);
+    float L = d, behind = __shfl_down_sync(0xffffffffu, d, 1);
+    if (lane == 31) behind = 1.f;
+#pragma unroll
+    for (int e = 1; e < 32; e *= 2) {
+      const float x = __shfl_up_sync(0xffffffffu, L, e), y = __shfl_down_sync(0xffffffffu, behind, e);
+      if (lane >= e) L *= x;
+      if (lane + e < 32) behind *= y;
+    }
+    R[r] = s * behind;
+    all[r] = __shfl_sync(0xffffffffu, L, 31);
+    rec[decay::GATE_G + r * decay::kRun] = d;
+    rec[decay::GATE_S + r * decay::kRun] = s;
+    rec[decay::GATE_L + r * decay::kRun] = L;
+    rec[decay::GATE_R + r * decay::kRun] = R[r];
+  }
+  rec[decay::GATE_K] = R[0] * (all[1] * all[2] * all[3]);
+  rec[decay::GATE_K + 32] = R[1] * (all[2] * all[3]);
+  rec[decay::GATE_K + 64] = R[2] * all[3];
+  rec[decay::GATE_K + 96] = R[3];
+  if (lane == 0) totals[i] = all[0] * all[1] * all[2] * all[3];
+}
+
+// rows of `from` values, `heads` to a token and `ld` from token to token -> dense
+// rows of `to` values, zero where there are more
+template <typename T>
+__global__ void __launch_bounds__(256) k_scan_rows(const T* __restrict__ src, T* __restrict__ dst, size_t rows, int heads,
+                                                   int from, size_t ld, int to) {
+  tc::grid_dependency_wait();
+  tc::grid_dependents_launch();
+  const int per = to / 8;
+  const size_t i = (size_t)blockIdx.x * 256 + threadIdx.x, r = i / per;
+  if (r >= rows) return;
+  const int c0 = (int)(i % per) * 8;
+  src += r / heads * ld + r % heads * from;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) dst[r * to + c0 + e] = c0 + e < from ? src[c0 + e] : from_f32<T>(0.f);
+}
+cudaError_t launch_scan_rows(const void* src, void* dst, size_t rows, int heads, int from, size_t ld, int to, cudaStream_t st) {
+  const size_t grid = (rows * (to / 8) + 255) / 256;
+  if (grid > 0x7fffffffull) return cudaErrorInvalidConfiguration;
+  return tc::launch_overlapped(k_scan_rows<bf16>, dim3((unsigned)grid), dim3(256), 0, st, (const bf16*)src, (bf16*)dst, rows, heads,
+                               from, ld, to);
 }
 
 // rows of `from` values -> rows of `to` values, zero where there are more
@@ -331,9 +448,9 @@ cudaError_t launch_rows(const void* src, void* dst, size_t rows, int from, int t
 
 size_t step_smem(const Geom& g, int V) { return (size_t)(2 * g.d_k + 256 / (kSlice / V) * kSlice) * sizeof(float); }
 int chunk_tokens(int d_k) { return d_k <= 128 ? 64 : 32; }
-size_t chunk_smem(int d_k, bool read) {
+size_t chunk_smem(int d_k, bool read, bool gated) {
   const size_t dk4 = (d_k + 3) & ~3, C = chunk_tokens(d_k), ldk = dk4 + 4, ldv = kSlice + 4;
-  return (C * ldk + C * ldv + dk4 * ldv + C + 4 + (read ? C * ldk + C * (C + 4) : 0)) * sizeof(float);
+  return (C * ldk + C * ldv + dk4 * ldv + (gated ? 4 * C : C + 4) + (read ? C * ldk + C * (C + 4) : 0)) * sizeof(float);
 }
 
 // Blocks of the fp32 chunks that an SM holds: by their shared memory (228 KB an
@@ -344,8 +461,8 @@ size_t chunk_smem(int d_k, bool read) {
 // 32768 tokens of 64 140 us / 157, of 136 432 / 748, of 256 851 / 916; 4 x 8 x 4096 of
 // 96 645 / 724; of 48 and 128 the same; 3 x 6 x 1501 of 64 75 / 71 (12 segments and
 // 24 cost the same by the formula).
-int chunk_blocks(int d_k, bool read) {
-  const size_t fit = (228 * 1024) / (chunk_smem(d_k, read) + 1024);
+int chunk_blocks(int d_k, bool read, bool gated) {
+  const size_t fit = (228 * 1024) / (chunk_smem(d_k, read, gated) + 1024);
   return (int)std::min<size_t>(chunk_tokens(d_k) == 64 ? 3 : 2, fit);
 }
 
@@ -353,7 +470,10 @@ struct Plan {
   int path, C, slices, nseg, seg;
   bool pad;
   size_t seg_bytes, q_bytes, v_bytes, y_bytes;   // workspace: segment starts, then padded q, k, v, y
-  size_t bytes() const { return seg_bytes + 2 * q_bytes + v_bytes + y_bytes; }
+  size_t record_bytes, total_bytes, seg_total_bytes;   // then a selective scan's records, their and the segments' products
+  size_t bytes() const {
+    return seg_bytes + 2 * q_bytes + v_bytes + y_bytes + record_bytes + total_bytes + seg_total_bytes;
+  }
 };
 size_t round_256(size_t n) { return (n + 255) / 256 * 256; }
 
@@ -399,7 +519,7 @@ int most_step_tokens(const atlas_decay_config& c, long long ctas) {
 // bf16 calls with d_k <= 128 take the tensor-core chunks.  Their copies want rows
 // of whole 16-byte groups: other widths (or addresses) go through padded copies
 // of q, k, v and y in the workspace.  `aligned`: the addresses do not ask for it.
-Plan make_plan(const atlas_decay_config& c, int B, int T, bool aligned) {
+Plan make_plan(const atlas_decay_config& c, int B, int T, bool aligned, bool gated) {
   Plan pl{};
   pl.slices = (c.d_v + kSlice - 1) / kSlice;
   pl.nseg = 1;
@@ -409,13 +529,13 @@ Plan make_plan(const atlas_decay_config& c, int B, int T, bool aligned) {
     pl.C = 1;
     return pl;
   }
-  const bool tc = c.qkv_dtype == ATLAS_BF16 && c.d_k <= 128;
+  const bool tc = c.qkv_dtype == ATLAS_BF16 && c.d_k <= 128 && !gated;
   pl.pad = tc && (!aligned || c.d_k % 8 || c.d_v % 8);
   pl.path = tc ? 2 : 1;
   pl.C = tc ? decay::kTcChunk : chunk_tokens(c.d_k);
   // CTAs that run at once; a fp32 chunk takes so long that starts hardly count
-  const long long slots = (tc ? 1 : chunk_blocks(c.d_k, true)) * sm_count(),
-                  state_slots = (tc ? 1 : chunk_blocks(c.d_k, false)) * sm_count();
+  const long long slots = (tc ? 1 : chunk_blocks(c.d_k, true, gated)) * sm_count(),
+                  state_slots = (tc ? 1 : chunk_blocks(c.d_k, false, gated)) * sm_count();
   const long long chunks = (T + pl.C - 1) / pl.C;
   const long long n = best_segments((long long)B * c.H * pl.slices, chunks, slots, state_slots, tc ? 2 : 0.5);
   pl.seg = (int)((chunks + n - 1) / n * pl.C);
@@ -426,6 +546,12 @@ Plan make_plan(const atlas_decay_config& c, int B, int T, bool aligned) {
     pl.q_bytes = round_256(rows * (c.H / c.share) * ((c.d_k + 7) / 8 * 8) * 2);
     pl.v_bytes = round_256(rows * c.H * ((c.d_v + 7) / 8 * 8) * 2);
     pl.y_bytes = round_256(rows * c.H * ((c.d_v + 7) / 8 * 8) * dtype_size(c.y_dtype));
+  }
+  if (gated) {
+    const size_t units = (size_t)B * c.H, records = units * ((T + decay::kGateTokens - 1) / decay::kGateTokens);
+    pl.record_bytes = records * decay::GATE_VALUES * sizeof(float);
+    pl.total_bytes = round_256(records * sizeof(float));
+    pl.seg_total_bytes = pl.nseg > 1 ? round_256(units * pl.nseg * sizeof(float)) : 0;
   }
   return pl;
 }
@@ -469,29 +595,34 @@ extern "C" int atlas_decay_create(const atlas_decay_config* cfg, atlas_decay_han
 }
 
 extern "C" size_t atlas_decay_workspace_bytes(const atlas_decay_handle* h, int B, int T) {
-  if (!h || B < 1 || T < 1 || T > kMostTokens) return 0;
+  if (!h) return 0;
+  return decay::workspace_bytes(h->cfg, B, T, false);
+}
+size_t decay::workspace_bytes(const atlas_decay_config& c, int B, int T, bool gated) {
+  if (B < 1 || T < 1 || T > kMostTokens) return 0;
   // the most it can be: tensors at addresses that ask for padded copies
-  return make_plan(h->cfg, B, T, false).bytes();
+  return make_plan(c, B, T, false, gated).bytes();
 }
 
 namespace {
 
-template <typename TI, typename TO>
-cudaError_t launch_step(const Geom& g, const Ptrs& p, cudaStream_t st) {
+template <typename TI, typename TO, bool GATED>
+cudaError_t launch_step(const Geom& g, const Ptrs& p, const Gates& gates, cudaStream_t st) {
   // four columns per thread where the state rows are whole 16-byte groups
   const bool v4 = g.d_v % 4 == 0 && aligned16(p.S0) && aligned16(p.S_out);
   const int rows = (g.d_k + (v4 ? 15 : 3)) / (v4 ? 16 : 4);
   const unsigned grid = (unsigned)((size_t)g.B * g.H * g.slices);
   const size_t smem = step_smem(g, v4 ? 4 : 1);
+  auto go = [&](auto kern) { kern<<<grid, 256, smem, st>>>(g, p, gates); };
   if (v4) {
-    if (rows <= 2) k_decay_step<TI, TO, 2, 4><<<grid, 256, smem, st>>>(g, p);
-    else if (rows <= 4) k_decay_step<TI, TO, 4, 4><<<grid, 256, smem, st>>>(g, p);
-    else if (rows <= 8) k_decay_step<TI, TO, 8, 4><<<grid, 256, smem, st>>>(g, p);
-    else k_decay_step<TI, TO, 16, 4><<<grid, 256, smem, st>>>(g, p);
+    if (rows <= 2) go(k_decay_step<TI, TO, 2, 4, GATED>);
+    else if (rows <= 4) go(k_decay_step<TI, TO, 4, 4, GATED>);
+    else if (rows <= 8) go(k_decay_step<TI, TO, 8, 4, GATED>);
+    else go(k_decay_step<TI, TO, 16, 4, GATED>);
   } else {
-    if (rows <= 16) k_decay_step<TI, TO, 16, 1><<<grid, 256, smem, st>>>(g, p);
-    else if (rows <= 32) k_decay_step<TI, TO, 32, 1><<<grid, 256, smem, st>>>(g, p);
-    else k_decay_step<TI, TO, 64, 1><<<grid, 256, smem, st>>>(g, p);
+    if (rows <= 16) go(k_decay_step<TI, TO, 16, 1, GATED>);
+    else if (rows <= 32) go(k_decay_step<TI, TO, 32, 1, GATED>);
+    else go(k_decay_step<TI, TO, 64, 1, GATED>);
   }
   return cudaGetLastError();
 }
@@ -506,29 +637,38 @@ cudaError_t launch_big(K kern, dim3 grid, size_t smem, const Geom& g, const Ptrs
 }  // namespace
 
 cudaError_t decay::scan_launch(const Geom& g, const Ptrs& p, cudaStream_t st) {
-  return tc::launch_overlapped(k_decay_scan, dim3((unsigned)(((size_t)g.d_k * g.d_v + 255) / 256), (unsigned)(g.B * g.H)),
-                               dim3(256), 0, st, g, p);
+  return tc::launch_overlapped(p.records ? k_decay_scan<true> : k_decay_scan<false>,
+                               dim3((unsigned)(((size_t)g.d_k * g.d_v + 255) / 256), (unsigned)(g.B * g.H)), dim3(256), 0, st, g,
+                               p);
 }
 
 namespace {
 
-template <typename TI, typename TO, int C>
+template <typename TI, typename TO, int C, bool GATED>
 cudaError_t launch_chunks(const Geom& g, const Ptrs& p, cudaStream_t st) {
   const unsigned units = (unsigned)(g.B * g.H);
   if (g.nseg > 1) {
-    cudaError_t e = launch_big(k_decay_chunk<TI, TO, C, false>, dim3(g.nseg - 1, g.slices, units),
-                               chunk_smem(g.d_k, false), g, p, st);
+    cudaError_t e = launch_big(k_decay_chunk<TI, TO, C, false, GATED>, dim3(g.nseg - 1, g.slices, units),
+                               chunk_smem(g.d_k, false, GATED), g, p, st);
     if (e != cudaSuccess) return e;
     e = decay::scan_launch(g, p, st);
     if (e != cudaSuccess) return e;
   }
-  return launch_big(k_decay_chunk<TI, TO, C, true>, dim3(g.nseg, g.slices, units), chunk_smem(g.d_k, true), g, p, st);
+  return launch_big(k_decay_chunk<TI, TO, C, true, GATED>, dim3(g.nseg, g.slices, units), chunk_smem(g.d_k, true, GATED), g, p,
+                    st);
 }
 
-template <typename TI, typename TO>
-cudaError_t launch(const Plan& pl, const Geom& g, const Ptrs& p, cudaStream_t st) {
-  if (pl.path == 0) return launch_step<TI, TO>(g, p, st);
-  return pl.C == 64 ? launch_chunks<TI, TO, 64>(g, p, st) : launch_chunks<TI, TO, 32>(g, p, st);
+template <typename TI, typename TO, bool GATED>
+cudaError_t launch(const Plan& pl, const Geom& g, const Ptrs& p, const Gates& gates, cudaStream_t st) {
+  if (pl.path == 0) return launch_step<TI, TO, GATED>(g, p, gates, st);
+  return pl.C == 64 ? launch_chunks<TI, TO, 64, GATED>(g, p, st) : launch_chunks<TI, TO, 32, GATED>(g, p, st);
+}
+template <bool GATED>
+cudaError_t launch_types(const Plan& pl, const atlas_decay_config& c, const Geom& g, const Ptrs& p, const Gates& gates,
+                         cudaStream_t st) {
+  const bool ib = c.qkv_dtype == ATLAS_BF16, ob = c.y_dtype == ATLAS_BF16;
+  return ib ? (ob ? launch<bf16, bf16, GATED>(pl, g, p, gates, st) : launch<bf16, float, GATED>(pl, g, p, gates, st))
+            : (ob ? launch<float, bf16, GATED>(pl, g, p, gates, st) : launch<float, float, GATED>(pl, g, p, gates, st));
 }
 
 }  // namespace
@@ -542,24 +682,30 @@ extern "C" int atlas_decay_forward(atlas_decay_handle* h, const atlas_decay_io* 
     return h->fail(ATLAS_ERR_INVALID_ARG, "q, k, v, decay, y must be non-NULL");
   if (io->y == io->q || io->y == io->k || io->y == io->v)
     return h->fail(ATLAS_ERR_INVALID_ARG, "y must not alias q, k or v");
-  // (the kernels step over the tokens in ints, a segment or a chunk past the end)
-  if (io->T > kMostTokens) return h->fail(ATLAS_ERR_UNSUPPORTED, "T > 2^30 is not supported");
-  const long long ctas = (long long)io->B * c.H * ((c.d_v + kSlice - 1) / kSlice);
+  return decay::run(h, c, *io, nullptr, (cudaStream_t)stream, &h->path);
+}
+
+int decay::run(HandleBase* h, const atlas_decay_config& c, const atlas_decay_io& io, const Selective* x, cudaStream_t st,
+               int* path) {
+  const char* what = x ? "selective scan launch" : "decay attention launch";
+  if (io.T > kMostTokens) return h->fail(ATLAS_ERR_UNSUPPORTED, "T > 2^30 is not supported");
+  const long long ctas = (long long)io.B * c.H * ((c.d_v + kSlice - 1) / kSlice);
   if (ctas > 0x7fffffffLL) return h->fail(ATLAS_ERR_UNSUPPORTED, "B * H too large for one call");
-  if ((long long)io->B * c.H > 65535 && io->T > most_step_tokens(c, ctas))
+  if ((long long)io.B * c.H > 65535 && io.T > most_step_tokens(c, ctas))
     return h->fail(ATLAS_ERR_UNSUPPORTED, "B * H > 65535 is supported for calls of at most %d tokens",
                    most_step_tokens(c, ctas));
-  cudaStream_t st = (cudaStream_t)stream;
-  const Plan pl = make_plan(c, io->B, io->T,
-                            aligned16(io->q) && aligned16(io->k) && aligned16(io->v) && aligned16(io->y));
+  // rows of wider ones: copies of whole 16-byte groups too
+  const bool strides_ok = !x || (x->ld_qk % 8 == 0 && x->ld_v % 8 == 0);
+  const Plan pl = make_plan(c, io.B, io.T, strides_ok && aligned16(io.q) && aligned16(io.k) && aligned16(io.v) && aligned16(io.y),
+                            x != nullptr);
   int rc = pl.path == 2 ? h->need_status(st) : ATLAS_OK;
   if (!rc) rc = h->grow(pl.bytes(), st);
   if (rc) return rc;
 
   Geom g;
-  g.B = io->B, g.T = io->T, g.H = c.H, g.share = c.share, g.d_k = c.d_k, g.d_v = c.d_v, g.scale = c.scale;
+  g.B = io.B, g.T = io.T, g.H = c.H, g.share = c.share, g.d_k = c.d_k, g.d_v = c.d_v, g.scale = c.scale;
   g.slices = pl.slices, g.nseg = pl.nseg, g.seg = pl.seg;
-  const size_t T = io->T, Hq = c.H / c.share, rows = (size_t)io->B * T;
+  const size_t T = io.T, Hq = c.H / c.share, rows = (size_t)io.B * T;
   g.dk_row = pl.pad ? (c.d_k + 7) / 8 * 8 : c.d_k;
   g.dv_row = pl.pad ? (c.d_v + 7) / 8 * 8 : c.d_v;
   auto strides = [&](int layout, size_t heads, size_t d, size_t& sb, size_t& sh, size_t& stk) {
@@ -570,26 +716,53 @@ extern "C" int atlas_decay_forward(atlas_decay_handle* h, const atlas_decay_io* 
   strides(c.qkv_layout, Hq, g.dk_row, g.qk_b, g.qk_h, g.qk_t);
   strides(c.qkv_layout, c.H, g.dv_row, g.v_b, g.v_h, g.v_t);
   strides(c.y_layout, c.H, g.dv_row, g.y_b, g.y_h, g.y_t);
-  Ptrs p{io->q, io->k, io->v, io->decay, io->lens, io->S0, io->y, io->S_out, (float*)h->ws};
+  const size_t ld_qk = x && x->ld_qk ? x->ld_qk : Hq * c.d_k, ld_v = x && x->ld_v ? x->ld_v : (size_t)c.H * c.d_v;
+  const bool apart = x && (x->ld_qk || x->ld_v);   // (ATLAS_LAYOUT_TOKENS)
+  if (apart && !pl.pad) {
+    g.qk_t = ld_qk, g.qk_b = T * ld_qk;
+    g.v_t = ld_v, g.v_b = T * ld_v;
+  }
+  char* const after = (char*)h->ws + pl.seg_bytes + 2 * pl.q_bytes + pl.v_bytes + pl.y_bytes;
+  Ptrs p{};
+  p.q = io.q, p.k = io.k, p.v = io.v, p.decay = io.decay, p.lens = io.lens, p.S0 = io.S0, p.y = io.y, p.S_out = io.S_out;
+  p.seg = (float*)h->ws;
+  Gates gates{};
+  if (x) {
+    gates = x->gates;
+    p.D = x->D;
+    if (pl.path != 0) {
+      float *records = (float*)after, *totals = (float*)(after + pl.record_bytes);
+      p.records = records, p.totals = totals;
+      p.seg_total = (float*)(after + pl.record_bytes + pl.total_bytes);
+      const size_t n = pl.record_bytes / (decay::GATE_VALUES * sizeof(float)), blocks = (n + 7) / 8;
+      if (blocks > 0x7fffffffull) return h->fail(ATLAS_ERR_UNSUPPORTED, "B * H * T is too large for one call");
+      const cudaError_t e = tc::launch_overlapped(k_scan_gates, dim3((unsigned)blocks), dim3(256), 0, st, g, gates, io.lens, records,
+                                                  totals, n);
+      if (e != cudaSuccess) return h->cuda_fail(what, e);
+    }
+  }
   if (pl.pad) {
     char* at = (char*)h->ws + pl.seg_bytes;
     void *q = at, *k = at + pl.q_bytes, *v = at + 2 * pl.q_bytes;
     p.y = at + 2 * pl.q_bytes + pl.v_bytes;
-    cudaError_t e = launch_rows<bf16>(io->q, q, rows * Hq, c.d_k, g.dk_row, st);
-    if (e == cudaSuccess) e = launch_rows<bf16>(io->k, k, rows * Hq, c.d_k, g.dk_row, st);
-    if (e == cudaSuccess) e = launch_rows<bf16>(io->v, v, rows * c.H, c.d_v, g.dv_row, st);
-    if (e != cudaSuccess) return h->cuda_fail("decay attention launch", e);
+    auto copy = [&](const void* src, void* dst, size_t heads, int from, int to, size_t ld) {
+      return apart ? launch_scan_rows(src, dst, rows * heads, (int)heads, from, ld, to, st)
+                   : launch_rows<bf16>(src, dst, rows * heads, from, to, st);
+    };
+    cudaError_t e = copy(io.q, q, Hq, c.d_k, g.dk_row, ld_qk);
+    if (e == cudaSuccess) e = copy(io.k, k, Hq, c.d_k, g.dk_row, ld_qk);
+    if (e == cudaSuccess) e = copy(io.v, v, c.H, c.d_v, g.dv_row, ld_v);
+    if (e != cudaSuccess) return h->cuda_fail(what, e);
     p.q = q, p.k = k, p.v = v;
   }
-  const bool ib = c.qkv_dtype == ATLAS_BF16, ob = c.y_dtype == ATLAS_BF16;
+  const bool ob = c.y_dtype == ATLAS_BF16;
   cudaError_t e = pl.path == 2 ? decay::tc_launch(g, p, ob, h->status, st)
-                        : ib ? (ob ? launch<bf16, bf16>(pl, g, p, st) : launch<bf16, float>(pl, g, p, st))
-                           : (ob ? launch<float, bf16>(pl, g, p, st) : launch<float, float>(pl, g, p, st));
+                               : x ? launch_types<true>(pl, c, g, p, gates, st) : launch_types<false>(pl, c, g, p, gates, st);
   if (e == cudaSuccess && pl.pad)
-    e = ob ? launch_rows<bf16>(p.y, io->y, rows * c.H, g.dv_row, c.d_v, st)
-           : launch_rows<float>(p.y, io->y, rows * c.H, g.dv_row, c.d_v, st);
-  if (e != cudaSuccess) return h->cuda_fail("decay attention launch", e);
-  h->path = pl.path;
+    e = ob ? launch_rows<bf16>(p.y, io.y, rows * c.H, g.dv_row, c.d_v, st)
+           : launch_rows<float>(p.y, io.y, rows * c.H, g.dv_row, c.d_v, st);
+  if (e != cudaSuccess) return h->cuda_fail(what, e);
+  *path = pl.path;
   h->last_stream = st;
   h->launched = true;
   return ATLAS_OK;

@@ -15,4 +15,16 @@ cudaError_t ws_launch(const Geom& g, const Ptrs& p, bool y_bf16, int* status, cu
 // segment starts from the segments' own contributions (atlas_decay.cu)
 cudaError_t scan_launch(const Geom& g, const Ptrs& p, cudaStream_t st);
 
+// What a selective scan has beside a decay attention's call.
+struct Selective {
+  Gates gates;
+  const float* D;
+  int ld_qk, ld_v;   // values between neighbouring tokens (0: dense)
+};
+// A call of either operator whose arguments have been checked but for its size
+// (atlas_decay.cu): its plan, workspace and launches.  x: NULL for a decay attention.
+int run(layer::HandleBase* h, const atlas_decay_config& c, const atlas_decay_io& io, const Selective* x, cudaStream_t st,
+        int* path);
+size_t workspace_bytes(const atlas_decay_config& c, int B, int T, bool gated);
+
 }  // namespace decay

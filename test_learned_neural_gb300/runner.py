@@ -10,19 +10,22 @@ from __future__ import annotations
 import numpy as np
 import torch
 
-from . import (ATLAS_BF16, ATLAS_E4M3, ATLAS_F32, ATLAS_LAYOUT_HEADS, ATLAS_NORM_HEADS, atlas_conv_create,
-               atlas_conv_destroy, atlas_conv_forward, atlas_conv_io, atlas_decay_create, atlas_decay_destroy,
-               atlas_decay_forward, atlas_decay_io, atlas_decay_last_path, atlas_decay_status, atlas_linear_create,
+from . import (ATLAS_BF16, ATLAS_E4M3, ATLAS_F32, ATLAS_GATES_MEMORY, ATLAS_LAYOUT_HEADS,
+               ATLAS_NORM_HEADS, atlas_conv_create, atlas_conv_destroy, atlas_conv_forward,
+               atlas_conv_io, atlas_decay_create, atlas_decay_destroy, atlas_decay_forward,
+               atlas_decay_io, atlas_decay_last_path, atlas_decay_status, atlas_linear_create,
                atlas_linear_destroy, atlas_linear_forward, atlas_linear_io, atlas_linear_last_path,
                atlas_linear_status, atlas_mem_create, atlas_mem_destroy, atlas_mem_forward,
-               atlas_mem_forward_host, atlas_mem_status, atlas_norm_create, atlas_norm_destroy, atlas_norm_forward,
-               atlas_norm_io, atlas_prologue_create, atlas_prologue_destroy,
-               atlas_prologue_forward, atlas_prologue_io, atlas_prologue_last_gemm, atlas_prologue_status,
-               atlas_qlinear_create, atlas_qlinear_destroy, atlas_qlinear_forward, atlas_qlinear_io,
-               atlas_qlinear_pack, atlas_qlinear_packed_bytes, atlas_qlinear_quantize, atlas_rms_create,
-               atlas_rms_destroy, atlas_rms_forward, atlas_rms_io, current_stream, make_config, make_conv_config,
+               atlas_mem_forward_host, atlas_mem_status, atlas_norm_create, atlas_norm_destroy,
+               atlas_norm_forward, atlas_norm_io, atlas_prologue_create, atlas_prologue_destroy,
+               atlas_prologue_forward, atlas_prologue_io, atlas_prologue_last_gemm,
+               atlas_prologue_status, atlas_qlinear_create, atlas_qlinear_destroy,
+               atlas_qlinear_forward, atlas_qlinear_io, atlas_qlinear_pack, atlas_qlinear_packed_bytes,
+               atlas_qlinear_quantize, atlas_rms_create, atlas_rms_destroy, atlas_rms_forward,
+               atlas_rms_io, atlas_scan_create, atlas_scan_destroy, atlas_scan_forward, atlas_scan_io,
+               atlas_scan_last_path, atlas_scan_status, current_stream, make_config, make_conv_config,
                make_decay_config, make_io, make_linear_config, make_norm_config, make_prologue_config,
-               make_qlinear_config, make_rms_config, AtlasError)
+               make_qlinear_config, make_rms_config, make_scan_config, AtlasError)
 
 
 def matrix_shapes(cfg):
@@ -538,3 +541,82 @@ class QuantLinear(_Layer):
                               _check("y", out["y"], self._out, (M, c.N), dev))
         atlas_qlinear_forward(self.h, io, _stream_of(dev, stream))
         return out
+
+
+class SelectiveScan(_Layer):
+    """The matrix memory whose decay and step come with every token
+    (include/atlas_scan.h): S_t = g_t S_{t-1} + s_t k_t^T v_t, y_t = scale q_t S_t +
+    D v_t.  gates "memory": theta and alpha, as Prologue gives them; "step": dt,
+    A and dt_bias of a state space layer."""
+    _destroy = staticmethod(atlas_scan_destroy)
+
+    def __init__(self, H, d_k, d_v, share=1, gates="memory", qkv_dtype="bf16", y_dtype=None, qkv_layout="heads",
+                 y_layout="heads", scale=1.0):
+        self.cfg = make_scan_config(H, d_k, d_v, share, gates, qkv_dtype, y_dtype, qkv_layout, y_layout, scale)
+        self.h = atlas_scan_create(self.cfg)
+        c = self.cfg
+        self._qkv, self._y = _torch_dtype(c.qkv_dtype), _torch_dtype(c.y_dtype)
+        self._heads_first, self._y_heads_first = c.qkv_layout == ATLAS_LAYOUT_HEADS, c.y_layout == ATLAS_LAYOUT_HEADS
+
+    def _y_shape(self, B, T):
+        c = self.cfg
+        return (B, c.H, T, c.d_v) if self._y_heads_first else (B, T, c.H, c.d_v)
+
+    def alloc_outputs(self, B, T, device):
+        c = self.cfg
+        return dict(y=torch.empty(self._y_shape(B, T), dtype=self._y, device=device),
+                    S=torch.empty((B, c.H, c.d_k, c.d_v), dtype=torch.float32, device=device))
+
+    def forward(self, t, out=None, stream=None):
+        """t: dict of device tensors q, k, v; the gates, fp32 [B, H, T] ([B, T, H]
+        in the layout "tokens"): theta and alpha, or dt with A and optional dt_bias
+        (fp32 [H]); and optional D (fp32 [H]), lens (int32 [B]) and S0 (fp32 [B, H, d_k,
+        d_v]; may be out["S"]: the state is then continued in place).  In the layout
+        "tokens" q and k, v, and the gates may be slices of wider rows."""
+        c, q, v, f32 = self.cfg, t["q"], t["v"], torch.float32
+        hq = c.H // c.share
+        if out is None:
+            out = self.alloc_outputs(*((q.shape[0], q.shape[2]) if self._heads_first else q.shape[:2]), q.device)
+        dev, ld_qk, ld_v, ld_g = _device_of(q), 0, 0, 0
+        memory = c.gates == ATLAS_GATES_MEMORY
+        step, alpha = (t["theta"], t["alpha"]) if memory else (t["dt"], None)
+        if self._heads_first:
+            B, T = q.shape[0], q.shape[2]
+            qs, gs = (B, hq, T, c.d_k), (B, c.H, T)
+            pq, pk, pv = (_check("q", q, self._qkv, qs, dev), _check("k", t["k"], self._qkv, qs, dev),
+                          _check("v", v, self._qkv, (B, c.H, T, c.d_v), dev))
+            ps = _check("step", step, f32, gs, dev)
+            pa = None if alpha is None else _check("alpha", alpha, f32, gs, dev)
+        else:
+            B, T = q.shape[:2]
+            qs, gs = (B, T, hq, c.d_k), (B, T, c.H)
+            pq, ld_qk = _check_rows("q", q, self._qkv, qs, dev)
+            pk, ld_k = _check_rows("k", t["k"], self._qkv, qs, dev)
+            pv, ld_v = _check_rows("v", v, self._qkv, (B, T, c.H, c.d_v), dev)
+            ps, ld_g = _check_rows("step", step, f32, gs, dev)
+            pa, ld_a = (None, ld_g) if alpha is None else _check_rows("alpha", alpha, f32, gs, dev)
+            if ld_k != ld_qk or ld_a != ld_g:
+                raise ValueError("the tokens of q and k, and of theta and alpha, must lie equally far apart")
+        A, bias, D, lens, S0, sq = t.get("A"), t.get("dt_bias"), t.get("D"), t.get("lens"), t.get("S0"), (B, c.H, c.d_k, c.d_v)
+
+        def head(name, a):
+            return None if a is None else _check(name, a, f32, (c.H,), dev)
+
+        io = atlas_scan_io(B, T, ld_qk, ld_v, ld_g, pq, pk, pv, ps, pa, None if memory else head("A", A),
+                           None if memory else head("dt_bias", bias), head("D", D),
+                           None if lens is None else _check("lens", lens, torch.int32, (B,), dev),
+                           None if S0 is None else _check("S0", S0, f32, sq, dev),
+                           _check("y", out["y"], self._y, self._y_shape(B, T), dev),
+                           _check("S", out["S"], f32, sq, dev))
+        atlas_scan_forward(self.h, io, _stream_of(dev, stream))
+        return out
+
+    def status(self):
+        rc = atlas_scan_status(self.h)
+        if rc:
+            raise AtlasError(rc, "device status of the selective scan")
+        return rc
+
+    def last_path(self):
+        """0: token by token, 1: fp32 chunks, 2: tensor-core chunks."""
+        return atlas_scan_last_path(self.h)

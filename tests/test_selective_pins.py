@@ -233,3 +233,56 @@ def test_other_strides_are_refused(shape, stride):
     import torch
     with pytest.raises(ValueError, match="slice"):
         runner._check_rows("x", Strided(shape, stride), torch.bfloat16, shape, None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(H=0), BAD), (dict(d_k=0), BAD), (dict(d_v=-1), BAD), (dict(share=3), BAD), (dict(gates=2), BAD), (dict(qkv_dtype=2), BAD),
+    (dict(y_dtype=2), BAD), (dict(qkv_layout=2), BAD), (dict(y_layout=-1), BAD), (dict(scale=float("nan")), BAD), (dict(d_k=257), UNS),
+    (dict(d_v=1025), UNS), (dict(H=65536), UNS)])
+def test_scan_create_rejects(lib, kw, code):  # noqa: F811
+    with pytest.raises(tln.AtlasError) as ei:
+        tln.atlas_scan_create(tln.make_scan_config(**{**dict(H=4, d_k=8, d_v=8), **kw}))
+    assert ei.value.code == code and tln.atlas_scan_last_error(None)
+
+
+def test_scan_forward_validates_before_any_cuda_call(lib):  # noqa: F811
+    h = tln.atlas_scan_create(tln.make_scan_config(4, 8, 8, gates="memory", qkv_layout="tokens"))
+    assert lib.atlas_scan_forward(None, None, None) == BAD and lib.atlas_scan_forward(h, None, None) == BAD
+    io = tln.atlas_scan_io(0, 5)
+    _refuses(lib, "scan", h, io, BAD, "B and T")
+    io.B = 2
+    _refuses(lib, "scan", h, io, BAD, "non-NULL")
+    io.q, io.k, io.v, io.step, io.y = (i << 20 for i in range(1, 6))     # never dereferenced: validation fails first
+    _refuses(lib, "scan", h, io, BAD, "takes alpha")
+    io.alpha = io.A = 6 << 20
+    _refuses(lib, "scan", h, io, BAD, "takes alpha")
+    io.A = None
+    for name, value in (("ld_qk", 31), ("ld_v", 31), ("ld_gates", 3)):
+        setattr(io, name, value)
+        _refuses(lib, "scan", h, io, BAD, "at least")
+        setattr(io, name, 0)
+    io.ld_v, io.y = 100, (3 << 20) + 9 * 200 + 60                        # the last token's values
+    _refuses(lib, "scan", h, io, BAD, "y must not")
+    io.y, io.S_out = 5 << 20, 6 << 20
+    _refuses(lib, "scan", h, io, BAD, "S_out")
+    io.S0, io.S_out = 7 << 20, (7 << 20) + 4
+    _refuses(lib, "scan", h, io, BAD, "S_out")
+    io.S_out, io.T = None, (1 << 30) + 1
+    _refuses(lib, "scan", h, io, UNS, "2^30")
+    io.T, io.B, io.S0 = 50, 1 << 14, None
+    for i, n in enumerate(("q", "k", "v", "step", "alpha", "y")):
+        setattr(io, n, (i + 1) << 40)
+    _refuses(lib, "scan", h, io, UNS, "65535")
+    assert tln.atlas_scan_last_path(h) == -1 and tln.atlas_scan_status(h) == tln.ATLAS_OK
+    assert tln.atlas_scan_workspace_bytes(h, 1, 1) == 0 and tln.atlas_scan_workspace_bytes(h, 0, 1) == 0
+    assert tln.atlas_scan_workspace_bytes(h, 1, 1000) >= 4 * 8 * 640 * 4
+    tln.atlas_scan_destroy(h)
+    h = tln.atlas_scan_create(tln.make_scan_config(4, 8, 8, gates="step"))
+    io = tln.atlas_scan_io(1, 5)
+    io.q, io.k, io.v, io.step, io.y = (i << 20 for i in range(1, 6))
+    _refuses(lib, "scan", h, io, BAD, "ATLAS_GATES_STEP A")
+    io.A, io.ld_qk = 6 << 20, 40
+    _refuses(lib, "scan", h, io, BAD, "ATLAS_LAYOUT_TOKENS")
+    tln.atlas_scan_destroy(h)
+    lib.atlas_scan_destroy(None)
+    assert lib.atlas_scan_status(None) == BAD

@@ -529,7 +529,7 @@ Plan make_plan(const atlas_decay_config& c, int B, int T, bool aligned, bool gat
     pl.C = 1;
     return pl;
   }
-  const bool tc = c.qkv_dtype == ATLAS_BF16 && c.d_k <= 128 && !gated;
+  const bool tc = c.qkv_dtype == ATLAS_BF16 && c.d_k <= 128;
   pl.pad = tc && (!aligned || c.d_k % 8 || c.d_v % 8);
   pl.path = tc ? 2 : 1;
   pl.C = tc ? decay::kTcChunk : chunk_tokens(c.d_k);

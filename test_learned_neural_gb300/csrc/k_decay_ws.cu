@@ -39,11 +39,14 @@ constexpr int NTHR = 18 * 32, STAGES = 3, STAGE = 3 * TILE;
 // 4096 tokens) 35 / 28.
 constexpr int kInlineScan = 4;
 
-template <int NT>
+constexpr int RECORD = GATE_VALUES * 4;   // bytes of a chunk's gates (GATED), a ring of stages too
+template <int NT, bool GATED>
 struct Smem {
   static constexpr int k0 = STAGES * STAGE, s = k0 + 3 * TILE, NS = NT == 2 ? 2 : 3, s_tile = 64 * 128,
-                       pw = s + NS * s_tile, rev = pw + (C + 4) * 4, bars = rev + 32 * 4, end = bars + 24 * 8;
+                       pw = s + NS * s_tile, rev = pw + (GATED ? STAGES * RECORD : (C + 4) * 4),
+                       bars = rev + (GATED ? 0 : 32 * 4), end = bars + 24 * 8;
 };
+static_assert(kGateTokens == C && Smem<3, true>::end <= 227 * 1024, "a record for each chunk, a block on each SM");
 
 enum Bar { FULL = 0, SC = 3, P = 5, K = 7, DS, DSFREE, S, PV, Y, YFREE, OUT, NBARS };
 
@@ -84,15 +87,15 @@ __device__ __forceinline__ void zero_row(uint32_t tile, int r) {
   for (int j = 0; j < 8; ++j) sts128(tile + r * 128 + 16 * j, 0, 0, 0, 0);
 }
 
-template <int NT, typename TO>
+template <int NT, typename TO, bool GATED>
 __global__ void __launch_bounds__(NTHR, 1)
     k_decay_ws(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap my, Geom g, Ptrs p,
                int inline_scan, int* status) {
-  using L = Smem<NT>;
+  using L = Smem<NT, GATED>;
   extern __shared__ __align__(1024) uint8_t sm[];
   const uint32_t base = tc::smem_u32(sm);
-  float* pw = reinterpret_cast<float*>(sm + L::pw);      // g^0 .. g^128
+  float* pw = reinterpret_cast<float*>(sm + L::pw);      // g^0 .. g^128; GATED: the stages' records
   float* rev = reinterpret_cast<float*>(sm + L::rev);    // g^31 .. g^0
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + L::bars);
   uint32_t* tbase = reinterpret_cast<uint32_t*>(bars + NBARS);
@@ -129,9 +132,12 @@ __global__ void __launch_bounds__(NTHR, 1)
   const int chunks = (t_live - t_lo + C - 1) / C;
   const int c0 = sl * SL, cols = min(SL, g.d_v - c0);
   const size_t sq = (size_t)g.d_k * g.d_v;
-  const float l2g = log2f(p.decay[h]);
-  for (int i = tid; i <= C; i += NTHR) pw[i] = power(l2g, i);
-  if (tid < 32) rev[tid] = power(l2g, 31 - tid);
+  float l2g = 0.f;
+  if constexpr (!GATED) {
+    l2g = log2f(p.decay[h]);
+    for (int i = tid; i <= C; i += NTHR) pw[i] = power(l2g, i);
+    if (tid < 32) rev[tid] = power(l2g, 31 - tid);
+  }
   __syncthreads();
   bool ok = *failed == 0 && *tbase == tm;
   constexpr uint32_t tSC = tm, tY1 = tm + 256, tY2 = tm + 320, tDS = tm + 384, tP2 = tm + 448;   // tP2: NT = 3
@@ -141,12 +147,18 @@ __global__ void __launch_bounds__(NTHR, 1)
     if (lane == 0) tc::mbar_arrive(bars + i);
   };
   auto tokens = [&](int c) { return min(C, t_live - t_lo - c * C); };
+  auto record = [&](int c) { return pw + (c % STAGES) * GATE_VALUES; };
+  // product of g over run r of a chunk
+  auto run_of = [&](const float* rec, int r) { return rec[GATE_L + kRun * r + kRun - 1]; };
 
   if (warp == 0) {
     auto load = [&](int c) {
       const uint32_t at = base + (c % STAGES) * STAGE, full = bar(FULL + c % STAGES);
       const int t0 = t_lo + c * C;
-      tc::expect_tx(full, STAGE);
+      tc::expect_tx(full, STAGE + (GATED ? RECORD : 0));
+      if constexpr (GATED)
+        load_bytes(base + L::pw + (c % STAGES) * RECORD,
+                   p.records + ((size_t)unit * ((g.T + C - 1) / C) + t0 / C) * GATE_VALUES, RECORD, full);
       load_4d(at, &mq, 0, t0, hq, b, full);
       load_4d(at + TILE, &mk, 0, t0, hq, b, full);
       load_4d(at + 2 * TILE, &mv, c0, t0, h, b, full);
@@ -245,8 +257,9 @@ __global__ void __launch_bounds__(NTHR, 1)
     for (int c = 0; c < chunks; ++c) {
       const uint32_t at = base + (c % STAGES) * STAGE;
       const int n = tokens(c);
-      const float w = r < n ? pw[n - 1 - r] : 0.f;
+      float w = !GATED && r < n ? pw[n - 1 - r] : 0.f;
       if (!(ok = all_wait(FULL + c % STAGES, (c / STAGES) & 1) && (c == 0 || all_wait(DS, (c - 1) & 1)))) break;
+      if constexpr (GATED) w = record(c)[GATE_K + r];   // (0 past the row's length)
 #pragma unroll 2
       for (int j = 0; j < 8; ++j) scale_chunk(at + TILE, base + L::k0, r, j, w, r < n);
       // a token past the row's length: 0 * NaN must not reach the sums
@@ -258,11 +271,20 @@ __global__ void __launch_bounds__(NTHR, 1)
     // probs: 32 x 32 blocks of a warp's 32 rows, 0 and 3 or 1 and 2 of the four
     const uint32_t lanes = (uint32_t)(32 * quarter) << 16;
     const int row = 32 * quarter + lane, side = group - 1;
+    const float skip = GATED && p.D ? p.D[h] : 0.f;
     // the read-outs of chunk c, this warp's 32 tokens and half of the columns
     auto reads = [&](int c) {
       if (!(ok = all_wait(Y, c & 1))) return;
       tc::fence_after_sync();
-      const float f = pw[row + 1] * g.scale, sc = g.scale;
+      const float sc = g.scale;
+      float f = sc;
+      if constexpr (GATED) {
+        const float* rec = record(c);
+        f *= rec[GATE_L + row];
+        for (int r = 0; r < quarter; ++r) f *= run_of(rec, r);
+      } else {
+        f *= pw[row + 1];
+      }
       const bool dead = row >= tokens(c);
       const uint32_t out = base + (c % STAGES) * STAGE;
 #pragma unroll 1
@@ -280,6 +302,18 @@ __global__ void __launch_bounds__(NTHR, 1)
         for (int i = 0; i < 16; i += 2)
           unpair(fma_pair(pair(yi[i], yi[i + 1]), pair(f, f), mul_pair(pair(ya[i], ya[i + 1]), pair(sc, sc))), ya[i],
                  ya[i + 1]);
+        if (GATED && p.D) {   // D v, from the stage's own tile
+          uint32_t x[4];
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            lds128(out + 2 * TILE + swz(row, 4 * side + 2 * part + j), x);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              float &a = ya[8 * j + 2 * i], &b2 = ya[8 * j + 2 * i + 1];
+              unpair(fma_pair(widen(x[i]), pair(skip, skip), pair(a, b2)), a, b2);
+            }
+          }
+        }
         if (dead) {
 #pragma unroll
           for (int i = 0; i < 16; ++i) ya[i] = 0.f;
@@ -304,12 +338,18 @@ __global__ void __launch_bounds__(NTHR, 1)
       const uint32_t sc = tSC + 128 * (c & 1) + lanes;
       // the scores; the third term's columns are the last chunk's until its P V is done
       if (!(ok = all_wait(SC + (c & 1), (c >> 1) & 1) && (NT == 2 || c == 0 || all_wait(PV, (c - 1) & 1)))) break;
+      // the stage's own barrier, for its record and v: it stays at this phase until these warps' read-outs of the chunk
+      if (GATED && !(ok = all_wait(FULL + c % STAGES, (c / STAGES) & 1))) break;
       tc::fence_after_sync();
+      // GATED: a row's weights in its own run, from the row backwards: s_j times the decays between
+      const float* rec = GATED ? record(c) : nullptr;
+      float own = 0.f;
       // 16 columns a turn: with everything unrolled the kernel's code overran the
       // instruction caches (4.6 of 11 cycles per instruction were spent on that)
 #pragma unroll 1
       for (int u = 0; u < 4; ++u) {
-        const int blk = side == 0 ? 3 * (u >> 1) : 1 + (u >> 1), h0 = 16 * (u & 1);   // columns 32 blk + h0 ..
+        // columns 32 blk + h0 .. (GATED: the later half first)
+        const int blk = side == 0 ? 3 * (u >> 1) : 1 + (u >> 1), h0 = 16 * (GATED ? 1 - (u & 1) : u & 1);
         uint32_t w[8][NT];
         if (blk > quarter) {
 #pragma unroll
@@ -321,12 +361,36 @@ __global__ void __launch_bounds__(NTHR, 1)
           tc::tmem_ld16(sc + 32 * blk + h0, v);
           tc::tmem_ld_wait16(v);
           if (blk < quarter) {
-            const float f = pw[row - 32 * blk - 31];   // times g^{31 - column}
+            float f;
+            if constexpr (GATED) {   // the runs between, times what the record has to the run's end
+              f = rec[GATE_L + row];
+              for (int r = blk + 1; r < quarter; ++r) f *= run_of(rec, r);
+            } else {
+              f = pw[row - 32 * blk - 31];   // times g^{31 - column}
+            }
+            const float* behind = GATED ? rec + GATE_R + 32 * blk : rev;
 #pragma unroll
             for (int i = 0; i < 8; i += 2) {
-              const float4 d = *reinterpret_cast<const float4*>(rev + h0 + 2 * i);
+              const float4 d = *reinterpret_cast<const float4*>(behind + h0 + 2 * i);
               split_pair<NT>(mul_pair(pair(v[2 * i], v[2 * i + 1]), mul_pair(pair(d.x, d.y), pair(f, f))), w[i]);
               split_pair<NT>(mul_pair(pair(v[2 * i + 2], v[2 * i + 3]), mul_pair(pair(d.z, d.w), pair(f, f))), w[i + 1]);
+            }
+          } else if constexpr (GATED) {
+            const float *gr = rec + GATE_G + 32 * blk + h0, *sr = rec + GATE_S + 32 * blk + h0;
+#pragma unroll
+            for (int i = 12; i >= 0; i -= 4) {
+              const float4 d = *reinterpret_cast<const float4*>(gr + i), st = *reinterpret_cast<const float4*>(sr + i);
+              const float ds[4] = {d.x, d.y, d.z, d.w}, ss[4] = {st.x, st.y, st.z, st.w};
+              float x[4];
+#pragma unroll
+              for (int e = 3; e >= 0; --e) {
+                const int col = h0 + i + e;
+                if (col == lane) own = 1.f;
+                x[e] = col <= lane ? v[i + e] * (own * ss[e]) : 0.f;
+                if (col <= lane) own *= ds[e];
+              }
+              split2<NT>(x[0], x[1], w[i / 2]);
+              split2<NT>(x[2], x[3], w[i / 2 + 1]);
             }
           } else {
             const int gap = lane - h0;
@@ -382,7 +446,7 @@ __global__ void __launch_bounds__(NTHR, 1)
 #pragma unroll
       for (int i = 0; i < 32; ++i) st[i] = d && inside(i) ? d[element(i)] : 0.f;
       for (int e = 0; add && e < s; ++e) {
-        const float f = power(l2g, min(g.seg, max(0, live - e * g.seg)));
+        const float f = GATED ? p.seg_total[(size_t)unit * g.nseg + e] : power(l2g, min(g.seg, max(0, live - e * g.seg)));
         const float* x = p.seg + ((size_t)unit * g.nseg + e + 1) * sq;
         float v[32];
 #pragma unroll
@@ -405,12 +469,22 @@ __global__ void __launch_bounds__(NTHR, 1)
       tc::fence_smem_to_async();
       arrive(S);
     };
-    if (chunks > 0) tiles();
-    for (int c = 0; c < chunks; ++c) {
+    // GATED: a chunk's product of g, taken before its read-outs can be made (they wait
+    // for these tiles), so that the stage's record is still the chunk's
+    float all = 1.f;
+    auto product = [&](int c) {
+      if (!all_wait(FULL + c % STAGES, (c / STAGES) & 1)) return false;
+      const float* rec = record(c);
+      all = run_of(rec, 0) * run_of(rec, 1) * (run_of(rec, 2) * run_of(rec, 3));
+      return true;
+    };
+    if (GATED && ok && chunks > 0) ok = product(0);
+    if (ok && chunks > 0) tiles();
+    for (int c = 0; c < chunks && ok; ++c) {
       if (!(ok = all_wait(DS, c & 1))) break;
       tc::fence_after_sync();
       {
-        const float f = pw[tokens(c)];
+        const float f = GATED ? all : pw[tokens(c)];
 #pragma unroll
         for (int t = (NT == 2 ? 1 : 0); t >= 0; --t) {   // the product's blocks
           float d[32];
@@ -430,6 +504,7 @@ __global__ void __launch_bounds__(NTHR, 1)
       }
       if (c + 1 < chunks) {
         if (!(ok = all_wait(Y, c & 1))) break;   // Q S has read the last terms
+        if (GATED && !(ok = product(c + 1))) break;
         tiles();
       }
     }
@@ -459,6 +534,9 @@ struct SmemState {
 constexpr int NTHR_STATE = 10 * 32;
 enum BarState { SFULL = 0, SEMPTY = 3, SK = 6, SFREE = 8, NSBARS = 10 };
 
+// GATED: the chunks in reverse, so that the product of the decays behind a chunk
+// comes by multiplying the chunks' own.
+template <bool GATED>
 __global__ void __launch_bounds__(NTHR_STATE, 1)
     k_decay_ws_state(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv, Geom g, Ptrs p,
                      int* status) {
@@ -491,6 +569,8 @@ __global__ void __launch_bounds__(NTHR_STATE, 1)
   const int live = live_tokens(g, p, b);
   const int t_lo = s * g.seg, t_hi = min(g.T, t_lo + g.seg), t_live = min(t_hi, max(live, t_lo));
   const int c0 = sl * SL, cols = min(SL, g.d_v - c0), chunks = (t_live - t_lo + C - 1) / C;
+  // the token that the c-th chunk to be worked on begins with
+  auto first = [&](int c) { return t_lo + (GATED ? chunks - 1 - c : c) * C; };
   bool ok = *failed == 0;
   auto all_wait = [&](int i, uint32_t parity) { return __all_sync(0xffffffffu, tc::wait(bar(i), parity)); };
   if (warp == 0) {
@@ -500,8 +580,8 @@ __global__ void __launch_bounds__(NTHR_STATE, 1)
       if (tc::elect()) {
         const uint32_t at = base + st * L::stage, full = bar(SFULL + st);
         tc::expect_tx(full, L::stage);
-        load_4d(at, &mk, 0, t_lo + c * C, hq, b, full);
-        load_4d(at + TILE, &mv, c0, t_lo + c * C, h, b, full);
+        load_4d(at, &mk, 0, first(c), hq, b, full);
+        load_4d(at + TILE, &mv, c0, first(c), h, b, full);
       }
       __syncwarp();
     }
@@ -523,11 +603,18 @@ __global__ void __launch_bounds__(NTHR_STATE, 1)
     auto element = [&](int i) { return col + 32 * (i / 16) + i % 16; };
     auto inside = [&](int i) { return row < cols && element(i) < g.d_k; };
     const size_t sq = (size_t)g.d_k * g.d_v;
-    const float l2g = log2f(p.decay[h]);
+    const float l2g = GATED ? 0.f : log2f(p.decay[h]);
+    const size_t unit_chunk = (size_t)unit * ((g.T + C - 1) / C);
+    auto total = [&](int c) { return c < chunks ? p.totals[unit_chunk + first(c) / C] : 1.f; };
+    float behind = GATED && group == 1 ? total(0) : 1.f;   // the chunks that come behind this one
     for (int c = group; c < chunks; c += 2) {
-      const int t0 = t_lo + c * C, n = min(C, t_live - t0);
+      const int t0 = first(c), n = min(C, t_live - t0);
       const uint32_t at = base + (c % STAGES) * L::stage, k0 = base + L::k0 + (c & 1) * 3 * TILE;
-      const float w = r < n ? power(l2g, t_live - 1 - t0 - r) : 0.f;
+      float w = !GATED && r < n ? power(l2g, t_live - 1 - t0 - r) : 0.f;
+      if constexpr (GATED) {
+        w = p.records[(unit_chunk + t0 / C) * GATE_VALUES + GATE_K + r] * behind;   // (0 past the row's length)
+        behind *= total(c) * total(c + 1);
+      }
       // the terms' buffer first: chunk c - 2's product done means that the loads
       // up to chunk c - 2 have landed, so the stage's parity below is the one of
       // this chunk's load or the one before it
@@ -540,6 +627,8 @@ __global__ void __launch_bounds__(NTHR_STATE, 1)
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(bars + SK + (c & 1));
     }
+    if (GATED && ok && group == 0 && quarter == 0 && lane == 0 && sl == 0)
+      p.seg_total[(size_t)unit * g.nseg + s] = behind;   // all chunks by now
     // the sums, by the group of the last chunk
     if (ok && chunks > 0 && group == ((chunks - 1) & 1)) {
       ok = all_wait(SFREE + ((chunks - 1) & 1), ((chunks - 1) >> 1) & 1);
@@ -587,14 +676,36 @@ __global__ void __launch_bounds__(NTHR_STATE, 1)
   if (warp == 0) tc::tmem_dealloc(tm, 256);
 }
 
-template <int NT, typename TO>
+template <int NT, typename TO, bool GATED>
 cudaError_t launch_out(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const CUtensorMap& my,
                        const Geom& g, const Ptrs& p, int inline_scan, int* status, cudaStream_t st) {
-  auto kern = k_decay_ws<NT, TO>;
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<NT>::end);
+  auto kern = k_decay_ws<NT, TO, GATED>;
+  constexpr int smem = Smem<NT, GATED>::end;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  return tc::launch_overlapped(kern, dim3(g.nseg, g.slices, g.B * g.H), dim3(NTHR), Smem<NT>::end, st, mq, mk, mv, my,
-                               g, p, inline_scan, status);
+  return tc::launch_overlapped(kern, dim3(g.nseg, g.slices, g.B * g.H), dim3(NTHR), smem, st, mq, mk, mv, my, g, p, inline_scan,
+                               status);
+}
+
+template <bool GATED>
+cudaError_t launch_all(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const CUtensorMap& my,
+                       const Geom& g, const Ptrs& p, bool y_bf16, int* status, cudaStream_t st) {
+  int inline_scan = 1;
+  if (g.nseg > 1) {
+    auto kern = k_decay_ws_state<GATED>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SmemState::end);
+    if (e != cudaSuccess) return e;
+    e = tc::launch_overlapped(kern, dim3(g.nseg - 1, g.slices, g.B * g.H), dim3(NTHR_STATE), SmemState::end, st, mk, mv, g, p,
+                              status);
+    if (e != cudaSuccess) return e;
+    if (g.nseg > kInlineScan) {
+      inline_scan = 0;
+      e = scan_launch(g, p, st);
+      if (e != cudaSuccess) return e;
+    }
+  }
+  return y_bf16 ? launch_out<2, bf16, GATED>(mq, mk, mv, my, g, p, inline_scan, status, st)
+                : launch_out<3, float, GATED>(mq, mk, mv, my, g, p, inline_scan, status, st);
 }
 
 }  // namespace
@@ -609,21 +720,8 @@ cudaError_t ws_launch(const Geom& g, const Ptrs& p, bool y_bf16, int* status, cu
       !map_4d(&mv, p.v, true, g.dv_row, g.T, g.H, g.B, g.v_t, g.v_h, g.v_b) ||
       !map_4d(&my, p.y, y_bf16, g.dv_row, g.T, g.H, g.B, g.y_t, g.y_h, g.y_b))
     return cudaErrorInvalidValue;
-  int inline_scan = 1;
-  if (g.nseg > 1) {
-    cudaError_t e = cudaFuncSetAttribute(k_decay_ws_state, cudaFuncAttributeMaxDynamicSharedMemorySize, SmemState::end);
-    if (e != cudaSuccess) return e;
-    e = tc::launch_overlapped(k_decay_ws_state, dim3(g.nseg - 1, g.slices, g.B * g.H), dim3(NTHR_STATE), SmemState::end,
-                              st, mk, mv, g, p, status);
-    if (e != cudaSuccess) return e;
-    if (g.nseg > kInlineScan) {
-      inline_scan = 0;
-      e = scan_launch(g, p, st);
-      if (e != cudaSuccess) return e;
-    }
-  }
-  return y_bf16 ? launch_out<2, bf16>(mq, mk, mv, my, g, p, inline_scan, status, st)
-                : launch_out<3, float>(mq, mk, mv, my, g, p, inline_scan, status, st);
+  return p.records ? launch_all<true>(mq, mk, mv, my, g, p, y_bf16, status, st)
+                   : launch_all<false>(mq, mk, mv, my, g, p, y_bf16, status, st);
 }
 
 }  // namespace decay

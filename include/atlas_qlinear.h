@@ -101,8 +101,9 @@ int atlas_qlinear_pack(atlas_qlinear_handle* h, const uint8_t* q, const void* sc
  * the stream of the last call on h must still exist then. */
 int atlas_qlinear_forward(atlas_qlinear_handle* h, const atlas_qlinear_io* io, void* stream);
 
-/* Device workspace a call of this size may need: fp32 x in bf16 terms, and
- * copies of x where its rows are no multiples of 16 bytes. */
+/* Device workspace a call of this size may need: a copy of x in the order in
+ * which the kernels read it, in 16 bits (fp32 x in three terms; bf16 x where K is
+ * no multiple of 64 or x not aligned to 16 bytes). */
 size_t atlas_qlinear_workspace_bytes(const atlas_qlinear_handle* h, int M);
 
 /* Message of the last failure on h, or of the last failed create when h is NULL. */

@@ -3,6 +3,7 @@
 
 #include <algorithm>
 #include <new>
+#include <type_traits>
 
 #include "linear_common.cuh"
 #include "tc2.cuh"
@@ -22,16 +23,18 @@ struct Call {
 
 // A thread takes V neighbouring channels of `run` tokens in order: the K - 1 rows
 // before the current one stay in registers, so x is read once but for the K - 1
-// rows in front of a run.  Every tap's product is formed for existing rows only,
-// or for zeros: an infinity K tokens back meets no padded tap.
+// rows in front of a run, and A rows are in flight at a time.  Taps are a template
+// parameter, not padded with zeros: an infinity K tokens back would meet them.
+// Bound by memory: four channels a thread leave room for four blocks on an SM and
+// their loads (eight: 150 registers, one block, 42 us for 4 x 4096 x 1536 bf16).
 //
 // The thread of a sequence's first run is the only one that reads the cache (a
 // run is K - 1 tokens at least), and it writes the next one, so that one may be
 // the other.
-template <typename T, int K, int V>
-__global__ void __launch_bounds__(256) k_conv(Call c, const T* __restrict__ x, const T* cache, T* __restrict__ y,
-                                              T* cache_out) {
-  constexpr int A = V == 1 ? 8 : 4;   // rows in flight
+template <typename T, int K, int V, int ACT>
+__global__ void __launch_bounds__(256, K <= 4 ? 3 : 2) k_conv(Call c, const T* __restrict__ x, const T* cache,
+                                                              T* __restrict__ y, T* cache_out) {
+  constexpr int A = sizeof(T) == 2 ? 8 : 4;   // 64 bytes of a thread
   tc::grid_dependency_wait();
   tc::grid_dependents_launch();
   const size_t item = (size_t)blockIdx.x * 256 + threadIdx.x, rest = item / c.vecs;
@@ -42,12 +45,8 @@ __global__ void __launch_bounds__(256) k_conv(Call c, const T* __restrict__ x, c
   const int t0 = seg * c.run, t1 = min(c.T, t0 + c.run), t_live = min(t1, live);
   const T* xb = x + b * c.T * c.ld_x + ch;
   const T* cb = cache ? cache + b * (K - 1) * c.C + ch : nullptr;
-  T* yb = y + b * c.T * c.C + ch;
+  T* yb = y + (b * c.T + t0) * c.C + ch;
   if (t0 < t_live) {
-    Words<T, V> now[A];
-#pragma unroll
-    for (int a = 0; a < A; ++a)
-      if (t0 + a < t_live) now[a].load(xb + (size_t)(t0 + a) * c.ld_x);
     float w[V * K], bias[V], win[K][V];
     load_vec<(V == 1 ? 1 : V * K)>(c.w + (size_t)ch * K, w);
     if constexpr (V == 1) {
@@ -71,36 +70,44 @@ __global__ void __launch_bounds__(256) k_conv(Call c, const T* __restrict__ x, c
         for (int e = 0; e < V; ++e) win[i][e] = 0.f;
       }
     }
+    const T* src = xb + (size_t)t0 * c.ld_x;
     for (int t = t0; t < t_live; t += A) {
-      Words<T, V> next[A];
+      Words<T, V> rows[A];
 #pragma unroll
       for (int a = 0; a < A; ++a)
-        if (t + A + a < t_live) next[a].load(xb + (size_t)(t + A + a) * c.ld_x);
+        if (t + a < t_live) rows[a].load(src + a * c.ld_x);
+      src += A * c.ld_x;
 #pragma unroll
       for (int a = 0; a < A; ++a) {
         if (t + a >= t_live) break;
-        now[a].values(win[K - 1]);
+        rows[a].values(win[K - 1]);
         float o[V];
+        if constexpr (V == 1) {
+          o[0] = bias[0];
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-          float s = bias[e];
+          for (int i = 0; i < K; ++i) o[0] = fmaf(w[i], win[i][0], o[0]);
+        } else {   // pairs of channels, one instruction for two
 #pragma unroll
-          for (int i = 0; i < K; ++i) s = fmaf(w[e * K + i], win[i][e], s);
-          o[e] = s;
+          for (int e = 0; e < V; e += 2) {
+            uint64_t s = linear::pack2(bias[e], bias[e + 1]);
+#pragma unroll
+            for (int i = 0; i < K; ++i)
+              s = linear::fma2(linear::pack2(w[e * K + i], w[(e + 1) * K + i]), linear::pack2(win[i][e], win[i][e + 1]), s);
+            linear::unpack2(s, o[e], o[e + 1]);
+          }
         }
-        linear::act_run<T, V>(c.act, o);
-        store_vec<V>(yb + (size_t)(t + a) * c.C, o);
+        linear::act_all<ACT, T, V>(o);
+        store_vec<V>(yb, o);
+        yb += c.C;
 #pragma unroll
         for (int i = 0; i + 1 < K; ++i)
 #pragma unroll
           for (int e = 0; e < V; ++e) win[i][e] = win[i + 1][e];
       }
-#pragma unroll
-      for (int a = 0; a < A; ++a) now[a] = next[a];
     }
   }
   float zero[V] = {};
-  for (int t = max(t0, t_live); t < t1; ++t) store_vec<V>(yb + (size_t)t * c.C, zero);
+  for (int t = max(t0, t_live); t < t1; ++t, yb += c.C) store_vec<V>(yb, zero);
   if (K > 1 && seg == 0 && cache_out) {
     // rows live .. live + K - 2 of [cache, x]
     Words<T, V> keep[K];
@@ -119,14 +126,22 @@ __global__ void __launch_bounds__(256) k_conv(Call c, const T* __restrict__ x, c
 
 template <typename T, int K>
 cudaError_t launch(Call c, const atlas_conv_io& io, bool vec, cudaStream_t st) {
-  constexpr int V = 16 / sizeof(T);
+  constexpr int V = 4;
   c.vecs = vec ? c.C / V : c.C;
   c.run = std::min(c.T, std::max(16, K - 1));
   c.nseg = (c.T + c.run - 1) / c.run;
   const size_t blocks = ((size_t)c.B * c.nseg * c.vecs + 255) / 256;
   if (blocks > 0x7fffffffull) return cudaErrorInvalidConfiguration;
-  return tc::launch_overlapped(vec ? k_conv<T, K, V> : k_conv<T, K, 1>, dim3((unsigned)blocks), dim3(256), 0, st, c,
-                               (const T*)io.x, (const T*)io.cache, (T*)io.y, (T*)io.cache_out);
+  auto go = [&](auto kern) {
+    return tc::launch_overlapped(kern, dim3((unsigned)blocks), dim3(256), 0, st, c, (const T*)io.x, (const T*)io.cache, (T*)io.y,
+                                 (T*)io.cache_out);
+  };
+  auto act = [&](auto v) {
+    constexpr int W = decltype(v)::value;
+    return c.act == ATLAS_ACT_SILU ? go(k_conv<T, K, W, ATLAS_ACT_SILU>)
+           : c.act == ATLAS_ACT_GELU ? go(k_conv<T, K, W, ATLAS_ACT_GELU>) : go(k_conv<T, K, W, ATLAS_ACT_NONE>);
+  };
+  return vec ? act(std::integral_constant<int, V>()) : act(std::integral_constant<int, 1>());
 }
 template <typename T>
 cudaError_t launch_k(const Call& c, const atlas_conv_io& io, int K, bool vec, cudaStream_t st) {
@@ -193,8 +208,7 @@ extern "C" int atlas_conv_forward(atlas_conv_handle* h, const atlas_conv_io* io,
   if (overlap(io->cache_out, cache_bytes, io->x, x_bytes) ||
       (io->cache_out != io->cache && overlap(io->cache_out, cache_bytes, io->cache, cache_bytes)))
     return h->fail(ATLAS_ERR_INVALID_ARG, "cache_out may be cache itself, else it must not overlap x or cache");
-  const size_t V = 16 / es;
-  const bool vec = c.C % V == 0 && ld % V == 0 && aligned16(io->x) && aligned16(io->y) && aligned16(io->cache) &&
+  const bool vec = c.C % 4 == 0 && ld % 4 == 0 && aligned16(io->x) && aligned16(io->y) && aligned16(io->cache) &&
                    aligned16(io->cache_out) && aligned16(io->w) && aligned16(io->bias);
   Call k{io->B, io->T, c.C, c.act, 0, 0, 0, ld, io->w, io->bias, io->lens};
   cudaStream_t st = (cudaStream_t)stream;

@@ -35,7 +35,11 @@ constexpr int kWarps = 8, kThreads = 32 * kWarps;
 constexpr int kStep = 64;       // of K, a packed 16 bytes of each lane
 constexpr int kMostRows = 65535 * 64;
 
-enum { X_BF16, X_PLANES, X_E4M3 };   // how the kernel gets x; planes: three bf16 terms of fp32 values
+// How the kernel gets x: bf16 rows as the caller has them (whole steps of K), or,
+// from a pass in front, as fragments: [8 rows][step][lane][2] of 16 bytes, bf16,
+// fp16 (e4m3 values, exactly), or three planes of bf16 (fp32 values).  Converting
+// e4m3 in every block instead took a third of the product's instructions.
+enum { X_ROWS, X_BF16, X_F16, X_PLANES };
 
 struct Shape {
   int K, N, group, groups, tiles, steps;
@@ -49,40 +53,57 @@ Shape make_shape(const atlas_qlinear_config& c) {
 struct Call {
   Shape s;
   int M, act, zeros, x_block, xblocks, per;   // per: steps of a warp
-  size_t ldx, plane;                          // row stride of x and distance of its planes, in values
-  const void* x;
+  bool early;                                 // the pass in front is this call's own
+  size_t plane;                               // 16-byte groups of a plane of x
+  const uint4* x;
   const float* x_scale;
   const uint8_t* W;
   const float* bias;
 };
 
-// D (16 x 8) += A (16 x 16) B (16 x 8)
-template <bool HALF>
+// D (16 x 8) = A (16 x 16) B (16 x 8) + D, or + 0
+template <bool HALF, bool FIRST>
 __device__ __forceinline__ void mma(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
-  if constexpr (HALF)
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-  else
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, "
-        "%3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+#define ATLAS_MMA(T, C, ...)                                                                                          \
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32." T "." T ".f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, " C ";" \
+               : __VA_ARGS__                                                                                          \
+               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f))
+  if constexpr (FIRST) {
+    if constexpr (HALF) ATLAS_MMA("f16", "{%10, %10, %10, %10}", "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3]));
+    else ATLAS_MMA("bf16", "{%10, %10, %10, %10}", "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3]));
+  } else {
+    if constexpr (HALF) ATLAS_MMA("f16", "{%0, %1, %2, %3}", "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3]));
+    else ATLAS_MMA("bf16", "{%0, %1, %2, %3}", "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3]));
+  }
+#undef ATLAS_MMA
 }
-// pair i of a packed word, less the offset (both halves)
+// A packed word's pairs, q - zero.  bf16: 128 + q less 128 + zero.  fp16 has room
+// for bits 4 to 7 as well: 1024 + q less 1024 + zero, and (1024 + 16 q) / 16 less 64 +
+// zero, which saves two shifts.  All exact.
+struct Offset {
+  uint32_t low, high;   // 128 + zero; fp16: 1024 + zero and -(64 + zero)
+};
 template <bool HALF>
-__device__ __forceinline__ uint32_t weights(uint32_t word, int i, uint32_t offset) {
-  const uint32_t v = ((word >> (4 * i)) & 0x000f000fu) | (HALF ? 0x64006400u : 0x43004300u);
-  uint32_t d;
-  if constexpr (HALF) asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(v), "r"(offset));
-  else asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(v), "r"(offset));
-  return d;
+__device__ __forceinline__ void weights(uint32_t word, const Offset* off, uint32_t* q) {
+  constexpr uint32_t magic = HALF ? 0x64006400u : 0x43004300u, sixteenth = 0x2c002c00u;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (HALF) {
+      const uint32_t w = i < 2 ? word : word >> 8;
+      if (i % 2 == 0) asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(q[i]) : "r"((w & 0x000f000fu) | magic), "r"(off[0].low));
+      else asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(q[i]) : "r"((w & 0x00f000f0u) | magic), "r"(sixteenth), "r"(off[1].high));
+    } else {
+      const uint32_t v = ((word >> (4 * i)) & 0x000f000fu) | magic;
+      asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(q[i]) : "r"(v), "r"(off[i % 2].low));
+    }
+  }
 }
 template <bool HALF>
-__device__ __forceinline__ uint32_t offset_of(uint32_t zero) {
-  return ((HALF ? 0x6400u : 0x4300u) + zero) * 0x00010001u;
+__device__ __forceinline__ Offset offset_of(uint32_t zero) {
+  Offset o;
+  o.low = ((HALF ? 0x6400u : 0x4300u) + zero) * 0x00010001u;
+  o.high = HALF ? (0xd400u + 16 * zero) * 0x00010001u : 0u;   // fp16: 64 + zero has a step of 1/16
+  return o;
 }
 __device__ __forceinline__ uint32_t two_halves(uint32_t e4m3x2) {
   const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)e4m3x2, __NV_E4M3);
@@ -93,9 +114,11 @@ __device__ __forceinline__ uint32_t two_halves(uint32_t e4m3x2) {
 // which its warps split.  Sums over the warps, then over the cluster's blocks,
 // through shared memory and always in the same order.
 template <int X, int MT, int NT, typename TO>
-__global__ void __launch_bounds__(kThreads) k_qlinear(Call c, const TO* residual, TO* y) {
-  constexpr bool HALF = X == X_E4M3;
-  constexpr int PLANES = X == X_PLANES ? 3 : 1, COLS = 16 * NT, ROWS = 8 * MT, LD = COLS + 4, AHEAD = NT * MT <= 4 ? 4 : 2;
+__global__ void __launch_bounds__(kThreads, 2) k_qlinear(Call c, const TO* residual, TO* y) {
+  constexpr bool HALF = X == X_F16;
+  constexpr int PLANES = X == X_PLANES ? 3 : 1, COLS = 16 * NT, ROWS = 8 * MT, LD = COLS + 4;
+  constexpr int AHEAD = NT * MT <= 2 ? 4 : 2;      // steps of weights in flight
+  constexpr bool X_AHEAD = MT * PLANES <= 2;       // x a step ahead too
   extern __shared__ float red[];               // [kWarps][ROWS][LD], the sums in the first
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, gr = lane / 4, ln = lane % 4;
   const uint32_t rank = tc::cluster_rank();
@@ -104,50 +127,76 @@ __global__ void __launch_bounds__(kThreads) k_qlinear(Call c, const TO* residual
   const int tile0 = blockIdx.x / S * NT, m0 = blockIdx.y * ROWS;
   const Shape& s = c.s;
   const int s_lo = min(s.steps, (int)(rank * kWarps + warp) * c.per), s_hi = min(s.steps, s_lo + c.per);
-  const uint4* wt[NT];
-  const uint32_t* sc[NT];
-  const uint8_t* ze[NT];
+  const int mask = s.group - 1;
+  // one address each, and small offsets from it: a register instead of two
+  const size_t group0 = (size_t)(s_lo * kStep / s.group) * s.tiles * 8 + (size_t)tile0 * 8 + gr;
+  const uint4* wt = reinterpret_cast<const uint4*>(c.W) + ((size_t)tile0 * s.steps + s_lo) * 32 + lane;
+  const uint32_t* sc = reinterpret_cast<const uint32_t*>(c.W + s.scale_at()) + group0;
+  const uint8_t* ze = c.W + s.zero_at() + group0;
+  uint32_t tile[NT], row[MT], xs_row[MT][2];
 #pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    const int tile = min(tile0 + n, s.tiles - 1);   // columns past the last: any, they are not stored
-    wt[n] = reinterpret_cast<const uint4*>(c.W) + (size_t)tile * s.steps * 32 + lane;
-    sc[n] = reinterpret_cast<const uint32_t*>(c.W + s.scale_at()) + (size_t)tile * 8 + gr;
-    ze[n] = c.W + s.zero_at() + (size_t)tile * 8 + gr;
+  for (int n = 0; n < NT; ++n) tile[n] = min(n, s.tiles - 1 - tile0);   // columns past the last: any, they are not stored
+  // x: 16-byte groups; rows past the last: any row's values or zeros, they are not stored
+  const uint4* xr = c.x + (X == X_ROWS ? (size_t)m0 * (s.K / 8) + s_lo * (kStep / 8) + ln
+                                       : ((size_t)(m0 / 8) * s.steps + s_lo) * 64 + lane * 2);
+  const float* xsr = c.x_scale + (size_t)m0 * c.xblocks;
+#pragma unroll
+  for (int m = 0; m < MT; ++m) {
+    row[m] = X == X_ROWS ? (uint32_t)min(8 * m + gr, c.M - 1 - m0) * (s.K / 8)
+                         : (uint32_t)min(m, (c.M - 1 - m0) / 8) * s.steps * 64;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) xs_row[m][e] = (uint32_t)min(8 * m + 2 * ln + e, c.M - 1 - m0) * c.xblocks;
   }
   uint4 w[AHEAD][NT];
+  auto first_weights = [&]() {
+#pragma unroll
+    for (int a = 0; a < AHEAD; ++a)
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+        if (s_lo + a < s_hi) w[a][n] = __ldg(wt + (tile[n] * (uint32_t)s.steps + a) * 32);
+  };
+  // Behind the call's own pass over x the weights need not wait for it: that pass
+  // let this kernel start only after all work in front of it was done.
+  if (c.early) first_weights();
   tc::grid_dependency_wait();
   tc::grid_dependents_launch();
+  if (!c.early) first_weights();
+  struct Frag {   // of half a step
+    uint4 v[MT][PLANES];
+  };
+  auto load_x = [&](int at, int h, Frag& f) {   // the at-th of the warp's steps
 #pragma unroll
-  for (int a = 0; a < AHEAD; ++a)
+    for (int m = 0; m < MT; ++m)
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
-      if (s_lo + a < s_hi) w[a][n] = __ldg(wt[n] + (size_t)(s_lo + a) * 32);
+      for (int p = 0; p < PLANES; ++p)
+        f.v[m][p] = X == X_ROWS ? __ldg(xr + (row[m] + at * (kStep / 8) + 4 * h)) : __ldg(xr + p * c.plane + (row[m] + at * 64 + h));
+  };
+  Frag x[2][2];   // X_AHEAD: by step parity and half
+  if (X_AHEAD && s_lo < s_hi) load_x(0, 0, x[0][0]), load_x(0, 1, x[0][1]);
 
-  // rows past the last: any row's values, they are not stored
-  const char* xr[MT];
-  constexpr int ES = X == X_E4M3 ? 1 : 2;
-#pragma unroll
-  for (int m = 0; m < MT; ++m)
-    xr[m] = (const char*)c.x + ((size_t)min(m0 + 8 * m + gr, c.M - 1) * c.ldx + 8 * ln) * ES;
-
-  float tot[NT][MT][4] = {}, acc[NT][MT][4] = {};
-  uint32_t scale[NT], off[NT][2];
+  float tot[NT][MT][4] = {}, acc[NT][MT][4];
+  uint32_t scale[NT];
+  Offset off[NT][2];
   float xs[MT][2];
+#pragma unroll
+  for (int n = 0; n < NT; ++n) off[n][0] = off[n][1] = offset_of<HALF>(8);
   auto open = [&](int k) {   // a group begins, or the warp's part of one
-    const int grp = k / s.group;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      scale[n] = sc[n][(size_t)grp * s.tiles * 8];
-      const uint32_t z = c.zeros ? ze[n][(size_t)grp * s.tiles * 8] : 0x88u;
-      off[n][0] = offset_of<HALF>(z & 15u);
-      off[n][1] = offset_of<HALF>(z >> 4);
+      scale[n] = __ldg(sc + tile[n] * 8);
+      if (c.zeros) {
+        const uint32_t z = __ldg(ze + tile[n] * 8);
+        off[n][0] = offset_of<HALF>(z & 15u);
+        off[n][1] = offset_of<HALF>(z >> 4);
+      }
     }
-    if constexpr (X == X_E4M3) {
+    sc += s.tiles * 8;
+    ze += s.tiles * 8;
+    if constexpr (X == X_F16) {
 #pragma unroll
       for (int m = 0; m < MT; ++m)
 #pragma unroll
-        for (int e = 0; e < 2; ++e)
-          xs[m][e] = c.x_block ? c.x_scale[(size_t)min(m0 + 8 * m + 2 * ln + e, c.M - 1) * c.xblocks + k / 128] : 1.f;
+        for (int e = 0; e < 2; ++e) xs[m][e] = c.x_block ? __ldg(xsr + (xs_row[m][e] + k / 128)) : 1.f;
     }
   };
   auto close = [&]() {
@@ -159,10 +208,29 @@ __global__ void __launch_bounds__(kThreads) k_qlinear(Call c, const TO* residual
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           float f = e < 2 ? a : b;
-          if constexpr (X == X_E4M3) f *= xs[m][e & 1];
+          if constexpr (X == X_F16) f *= xs[m][e & 1];
           tot[n][m][e] = fmaf(acc[n][m][e], f, tot[n][m][e]);
-          acc[n][m][e] = 0.f;
         }
+    }
+  };
+  // half a step: 32 of K; FIRST: of a group
+  auto half = [&](auto first, const Frag& f, const uint4* words, int h) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const uint32_t word[2] = {h ? words[n].z : words[n].x, h ? words[n].w : words[n].y};
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        uint32_t q[4];
+        weights<HALF>(word[j], off[n], q);
+#pragma unroll
+        for (int p = PLANES - 1; p >= 0; --p)   // the smallest terms first
+#pragma unroll
+          for (int m = 0; m < MT; ++m) {
+            const uint4& v = f.v[m][p];
+            if (decltype(first)::value && j == 0 && p == PLANES - 1) mma<HALF, true>(acc[n][m], q, v.x, v.y);
+            else mma<HALF, false>(acc[n][m], q, j ? v.z : v.x, j ? v.w : v.y);
+          }
+      }
     }
   };
   for (int st0 = s_lo; st0 < s_hi; st0 += AHEAD) {
@@ -170,59 +238,29 @@ __global__ void __launch_bounds__(kThreads) k_qlinear(Call c, const TO* residual
     for (int a = 0; a < AHEAD; ++a) {
       const int st = st0 + a;
       if (st >= s_hi) break;
-      uint32_t x[2][MT][PLANES][4];
+      if (X_AHEAD && st + 1 < s_hi) load_x(st + 1 - s_lo, 0, x[(a + 1) & 1][0]), load_x(st + 1 - s_lo, 1, x[(a + 1) & 1][1]);
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const int k = st * kStep + 32 * h;
-        const bool in = k + 8 * ln < s.K;   // (rows are whole groups of eight, or padded with zeros to a step)
-#pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-          for (int p = 0; p < PLANES; ++p) {
-            if constexpr (X == X_E4M3) {
-              const uint2 u = in ? *reinterpret_cast<const uint2*>(xr[m] + k) : make_uint2(0u, 0u);
-              x[h][m][p][0] = u.x, x[h][m][p][1] = u.y;
-            } else {
-              const uint4 u = in ? *reinterpret_cast<const uint4*>(xr[m] + (k + p * c.plane) * 2) : make_uint4(0u, 0u, 0u, 0u);
-              x[h][m][p][0] = u.x, x[h][m][p][1] = u.y, x[h][m][p][2] = u.z, x[h][m][p][3] = u.w;
-            }
-          }
-      }
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int k = st * kStep + 32 * h;
-        if (k >= s.K) break;
-        if (k % s.group == 0 || (h == 0 && st == s_lo)) open(k);
-        if constexpr (X == X_E4M3) {
-#pragma unroll
-          for (int m = 0; m < MT; ++m) {
-            const uint32_t u = x[h][m][0][0], v = x[h][m][0][1];
-            x[h][m][0][0] = two_halves(u & 0xffffu), x[h][m][0][1] = two_halves(u >> 16);
-            x[h][m][0][2] = two_halves(v & 0xffffu), x[h][m][0][3] = two_halves(v >> 16);
-          }
+        if (h == 1 && k >= s.K) break;
+        Frag& f = x[X_AHEAD ? a & 1 : 0][X_AHEAD ? h : 0];
+        if constexpr (!X_AHEAD) load_x(st - s_lo, h, f);
+        if ((k & mask) == 0 || (h == 0 && st == s_lo)) {
+          open(k);
+          half(std::true_type(), f, w[a], h);
+        } else {
+          half(std::false_type(), f, w[a], h);
         }
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          const uint32_t word[2] = {h ? w[a][n].z : w[a][n].x, h ? w[a][n].w : w[a][n].y};
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            uint32_t f[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) f[i] = weights<HALF>(word[j], i, off[n][i & 1]);
-#pragma unroll
-            for (int p = PLANES - 1; p >= 0; --p)   // the smallest terms first
-#pragma unroll
-              for (int m = 0; m < MT; ++m) mma<HALF>(acc[n][m], f, x[h][m][p][2 * j], x[h][m][p][2 * j + 1]);
-          }
-        }
-        if ((k + 32) % s.group == 0) close();
+        if (((k + 32) & mask) == 0) close();
       }
 #pragma unroll
       for (int n = 0; n < NT; ++n)
-        if (st + AHEAD < s_hi) w[a][n] = __ldg(wt[n] + (size_t)(st + AHEAD) * 32);
+        if (st + AHEAD < s_hi) w[a][n] = __ldg(wt + (tile[n] * (uint32_t)s.steps + a + AHEAD) * 32);
     }
+    wt += AHEAD * 32;
   }
-  if (s_lo < s_hi) close();   // a part of a group (or zeros)
+  // a part of a group: K's last, or one that ends with the warp's steps
+  if (s_lo < s_hi && (min((s.K + 31) / 32 * 32, s_hi * kStep) & mask) != 0) close();
 
 #pragma unroll
   for (int n = 0; n < NT; ++n)
@@ -256,7 +294,7 @@ __global__ void __launch_bounds__(kThreads) k_qlinear(Call c, const TO* residual
         t += v;
       }
     }
-    if (X == X_E4M3 && c.x_block == 0) t *= c.x_scale[m];
+    if (X == X_F16 && c.x_block == 0) t *= c.x_scale[m];
     if (c.bias) t += c.bias[col];
     linear::act_run<TO, 1>(c.act, &t);
     if (residual) t += to_f32(residual[(size_t)m * s.N + col]);
@@ -265,31 +303,49 @@ __global__ void __launch_bounds__(kThreads) k_qlinear(Call c, const TO* residual
   if (S > 1) tc::cluster_sync();   // no block leaves while another reads its sums
 }
 
-// x as the kernel wants it: rows of ld values, a multiple of a step, zeros past
-// K; fp32 values as three bf16 planes, the leading 8 bits, the next 8 and the last
-// 8, each cut off, so that their sum is the value itself (infinities and NaN stay
-// in the first)
-template <typename TI, int PLANES>
-__global__ void __launch_bounds__(256) k_rows_of(const TI* __restrict__ x, uint16_t* __restrict__ dst, int M, int K, int ld) {
+// x as fragments: a thread writes 16 bytes of each plane, eight values of a row,
+// zeros past K and M.  fp32 values as three bf16 planes, the leading 8 bits, the next 8 and the
+// last 8, each cut off, so that their sum is the value itself (infinities and NaN
+// stay in the first).
+template <typename TI, int X>
+__global__ void __launch_bounds__(256) k_fragments(const TI* __restrict__ x, uint4* __restrict__ dst, int M, int K, int steps,
+                                                   size_t plane) {
   tc::grid_dependency_wait();
   tc::grid_dependents_launch();
-  const size_t i = (size_t)blockIdx.x * 256 + threadIdx.x, r = i / ld;
-  const int k = (int)(i % ld);
-  if (r >= (size_t)M) return;
-  if constexpr (PLANES == 1) {
-    if constexpr (sizeof(TI) == 1) reinterpret_cast<uint8_t*>(dst)[i] = k < K ? x[r * K + k] : 0;
-    else dst[i] = k < K ? x[r * K + k] : 0;
-  } else {
-    float v = k < K ? x[r * K + k] : 0.f;
-    const bool finite = fabsf(v) <= 3.402823466e38f;
+  const size_t i = (size_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= plane) return;
+  const int h = (int)(i % 2), lane = (int)(i / 2 % 32), step = (int)(i / 64 % steps);
+  const size_t r = i / 64 / steps * 8 + lane / 4;
+  const int k = step * kStep + 32 * h + 8 * (lane % 4);
+  constexpr int PLANES = X == X_PLANES ? 3 : 1;
+  uint32_t out[PLANES][4];
 #pragma unroll
-    for (int p = 0; p < PLANES; ++p) {
-      uint32_t top = __float_as_uint(v) & 0xffff0000u;
-      if (!finite) top = p > 0 ? 0u : v != v ? 0x7fff0000u : top;
-      dst[(size_t)p * M * ld + i] = (uint16_t)(top >> 16);
-      if (finite) v -= __uint_as_float(top);
+  for (int e = 0; e < 8; e += 2) {
+    uint32_t half[PLANES][2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const bool in = r < (size_t)M && k + e + j < K;
+      const TI v = in ? x[r * K + k + e + j] : TI(0);
+      if constexpr (X == X_PLANES) {
+        float rest = v;
+        const bool finite = fabsf(rest) <= 3.402823466e38f;
+#pragma unroll
+        for (int p = 0; p < PLANES; ++p) {
+          uint32_t top = __float_as_uint(rest) & 0xffff0000u;
+          if (!finite) top = p > 0 ? 0u : rest != rest ? 0x7fff0000u : top;
+          half[p][j] = top >> 16;
+          if (finite) rest -= __uint_as_float(top);
+        }
+      } else {
+        half[0][j] = v;
+      }
     }
+#pragma unroll
+    for (int p = 0; p < PLANES; ++p)
+      out[p][e / 2] = X == X_F16 ? two_halves(half[p][0] | (half[p][1] << 8)) : half[p][0] | (half[p][1] << 16);
   }
+#pragma unroll
+  for (int p = 0; p < PLANES; ++p) dst[p * plane + i] = make_uint4(out[p][0], out[p][1], out[p][2], out[p][3]);
 }
 
 // a thread: a word of the laid out weights, or of the scales
@@ -362,27 +418,32 @@ __global__ void __launch_bounds__(256) k_quantize(Shape s, const T* __restrict__
   }
 }
 
-// What x goes through before the product: nothing, or a copy in the workspace.
+// What x goes through before the product: nothing, or a copy as fragments in the workspace.
 struct Operand {
-  bool copy;
-  size_t ld, plane, bytes;
+  int kind;
+  size_t plane, bytes;
 };
 Operand make_operand(const atlas_qlinear_config& c, int M, bool aligned) {
   Operand o;
-  const size_t es = c.x_dtype == ATLAS_E4M3 ? 1 : 2, planes = c.x_dtype == ATLAS_F32 ? 3 : 1;
-  o.copy = c.x_dtype == ATLAS_F32 || c.K % 8 || !aligned;
-  o.ld = o.copy ? (size_t)(c.K + kStep - 1) / kStep * kStep : c.K;
-  o.plane = o.ld * M;
-  o.bytes = o.copy ? planes * o.plane * es : 0;
+  const size_t planes = c.x_dtype == ATLAS_F32 ? 3 : 1;
+  o.kind = c.x_dtype == ATLAS_F32 ? X_PLANES : c.x_dtype == ATLAS_E4M3 ? X_F16 : c.K % kStep || !aligned ? X_BF16 : X_ROWS;
+  o.plane = (size_t)(M + 7) / 8 * ((c.K + kStep - 1) / kStep) * 64;
+  o.bytes = o.kind == X_ROWS ? 0 : planes * o.plane * 16;
   return o;
 }
 
 template <int X, int MT, int NT, typename TO>
 cudaError_t launch(Call c, const atlas_qlinear_io& io, cudaStream_t st) {
   const int cols = (c.s.tiles + NT - 1) / NT, rows = (c.M + 8 * MT - 1) / (8 * MT);
-  // blocks for every SM, down to a step for each warp
+  // Blocks of a cluster that share K: as few steps of a warp, and rounds of blocks
+  // (two on an SM), as possible; a block's start and end take about four steps' time.
   int S = 1;
-  while (S < 8 && (long long)S * cols * rows < sm_count() && c.s.steps >= 2 * S * kWarps) S *= 2;
+  long long cost = 0;
+  for (int n = 1; n <= 8 && (n == 1 || c.s.steps >= n * kWarps); n *= 2) {
+    const long long rounds = ((long long)n * cols * rows + 2 * sm_count() - 1) / (2 * sm_count()),
+                    now = rounds * ((c.s.steps + n * kWarps - 1) / (n * kWarps) + 4 + (n > 1));
+    if (n == 1 || now < cost) S = n, cost = now;
+  }
   c.per = (c.s.steps + S * kWarps - 1) / (S * kWarps);
   const size_t smem = (size_t)kWarps * 8 * MT * (16 * NT + 4) * sizeof(float);
   auto kern = k_qlinear<X, MT, NT, TO>;
@@ -409,7 +470,7 @@ cudaError_t launch_rows(const Call& c, const atlas_qlinear_io& io, cudaStream_t 
   if (c.M <= 8) return launch<X, 1, 2, TO>(c, io, st);
   if (c.M <= 16) return launch<X, 2, 2, TO>(c, io, st);
   if constexpr (X == X_PLANES) {
-    return launch<X, 4, 1, TO>(c, io, st);   // (three terms of eight rows would not fit the registers)
+    return launch<X, 4, 1, TO>(c, io, st);   // (three terms of more rows would not fit the registers)
   } else {
     if (c.M <= 32) return launch<X, 4, 2, TO>(c, io, st);
     return launch<X, 8, 1, TO>(c, io, st);
@@ -526,27 +587,29 @@ extern "C" int atlas_qlinear_forward(atlas_qlinear_handle* h, const atlas_qlinea
       (io->y != io->residual && overlap(io->y, yb, io->residual, yb)))
     return h->fail(ATLAS_ERR_INVALID_ARG, "y may be residual itself, else it must not overlap an input");
   cudaStream_t st = (cudaStream_t)stream;
-  // (e4m3 rows are read eight bytes at a time, bf16 ones sixteen)
   const Operand o = make_operand(c, io->M, aligned16(io->x));
   if (const int rc = h->grow(o.bytes, st)) return rc;
   Call k;
   k.s = make_shape(c);
   k.M = io->M, k.act = c.act, k.zeros = c.zeros, k.x_block = c.x_block, k.xblocks = (int)xblocks, k.per = 0;
-  k.ldx = o.ld, k.plane = o.plane, k.x = o.copy ? h->ws : io->x, k.x_scale = io->x_scale;
+  k.early = o.kind != X_ROWS;
+  k.plane = o.plane, k.x = (const uint4*)(o.kind == X_ROWS ? io->x : h->ws), k.x_scale = io->x_scale;
   k.W = (const uint8_t*)io->W, k.bias = io->bias;
   cudaError_t e = cudaSuccess;
-  if (o.copy) {
+  if (o.kind != X_ROWS) {
     const size_t blocks = (o.plane + 255) / 256;
     if (blocks > 0x7fffffffull) return h->fail(ATLAS_ERR_UNSUPPORTED, "M * K is too large");
-    auto rows = [&](auto kern, auto* x) {
-      return tc::launch_overlapped(kern, dim3((unsigned)blocks), dim3(256), 0, st, x, (uint16_t*)h->ws, io->M, c.K, (int)o.ld);
+    auto pass = [&](auto kern, auto* x) {
+      return tc::launch_overlapped(kern, dim3((unsigned)blocks), dim3(256), 0, st, x, (uint4*)h->ws, io->M, c.K, k.s.steps, o.plane);
     };
-    e = c.x_dtype == ATLAS_F32 ? rows(k_rows_of<float, 3>, (const float*)io->x)
-        : q ? rows(k_rows_of<uint8_t, 1>, (const uint8_t*)io->x) : rows(k_rows_of<uint16_t, 1>, (const uint16_t*)io->x);
+    e = o.kind == X_PLANES ? pass(k_fragments<float, X_PLANES>, (const float*)io->x)
+        : o.kind == X_F16  ? pass(k_fragments<uint8_t, X_F16>, (const uint8_t*)io->x)
+                           : pass(k_fragments<uint16_t, X_BF16>, (const uint16_t*)io->x);
   }
   if (e == cudaSuccess)
-    e = c.x_dtype == ATLAS_F32 ? launch_out<X_PLANES>(k, *io, c.out_dtype, st)
-        : q ? launch_out<X_E4M3>(k, *io, c.out_dtype, st) : launch_out<X_BF16>(k, *io, c.out_dtype, st);
+    e = o.kind == X_PLANES ? launch_out<X_PLANES>(k, *io, c.out_dtype, st)
+        : o.kind == X_F16  ? launch_out<X_F16>(k, *io, c.out_dtype, st)
+        : o.kind == X_BF16 ? launch_out<X_BF16>(k, *io, c.out_dtype, st) : launch_out<X_ROWS>(k, *io, c.out_dtype, st);
   if (e != cudaSuccess) return h->cuda_fail("4-bit matrix product launch", e);
   h->last_stream = st;
   h->launched = true;

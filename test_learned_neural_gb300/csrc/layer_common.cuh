@@ -72,8 +72,11 @@ struct Words {
         const uint4 u = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint32_t*>(p) + i);
         w[i] = u.x; w[i + 1] = u.y; w[i + 2] = u.z; w[i + 3] = u.w;
       }
+    } else if constexpr (V * sizeof(T) == 8) {
+      const uint2 u = *reinterpret_cast<const uint2*>(p);
+      w[0] = u.x; w[1] = u.y;
     } else if constexpr (sizeof(T) == 2) {
-      static_assert(V == 1, "one value, or whole 16-byte groups");
+      static_assert(V == 1, "one value, or whole 8- or 16-byte groups");
       w[0] = *reinterpret_cast<const uint16_t*>(p);
     } else {
 #pragma unroll
@@ -85,6 +88,8 @@ struct Words {
 #pragma unroll
       for (int i = 0; i < N; i += 4)
         *reinterpret_cast<uint4*>(reinterpret_cast<uint32_t*>(p) + i) = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
+    } else if constexpr (V * sizeof(T) == 8) {
+      *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
     } else if constexpr (sizeof(T) == 2) {
       *reinterpret_cast<uint16_t*>(p) = (uint16_t)w[0];
     } else {

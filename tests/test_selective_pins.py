@@ -172,7 +172,7 @@ def test_qlinear_validates_before_any_cuda_call(lib):  # noqa: F811
     _refuses(lib, "qlinear", h, io, UNS, "4194240")
     # three 16-column tiles, two steps of 64, four groups: 512 bytes a tile and step, 40 a tile and group
     assert tln.atlas_qlinear_packed_bytes(h) == 3 * 2 * 512 + 4 * 3 * 40
-    assert tln.atlas_qlinear_workspace_bytes(h, 3) == 3 * 128 and tln.atlas_qlinear_workspace_bytes(h, 0) == 0
+    assert tln.atlas_qlinear_workspace_bytes(h, 3) == 8 * 128 * 2 and tln.atlas_qlinear_workspace_bytes(h, 0) == 0
     Q, P = lib.atlas_qlinear_quantize, lib.atlas_qlinear_pack
     assert Q(None, 64, 0, 64, 64, 64, None) == BAD and P(None, 64, 64, 64, 64, None) == BAD
     for args in ((None, 0, 64, 1 << 20, 1 << 21), (1 << 30, 2, 64, 1 << 20, 1 << 21), (1 << 30, 0, 64, 1 << 20, None),

@@ -31,7 +31,8 @@
  * Capture: calls may be captured in a CUDA graph, the first one of a size too.
  * A graph uses the handle's workspace: that stays allocated until the handle is
  * destroyed (a later call that needs more gets a new one beside it), so a graph
- * may be replayed as long as the handle lives.  A replay counts as a call on it.
+ * may be replayed as long as the handle lives.  A replay counts as a call on it;
+ * wait for its stream before asking for the status.
  *
  * Inputs: a NaN or an infinity in x makes its row of y non-finite, one in the
  * scales its column, and no other.
@@ -102,9 +103,14 @@ int atlas_qlinear_pack(atlas_qlinear_handle* h, const uint8_t* q, const void* sc
 int atlas_qlinear_forward(atlas_qlinear_handle* h, const atlas_qlinear_io* io, void* stream);
 
 /* Device workspace a call of this size may need: a copy of x in the order in
- * which the kernels read it, in 16 bits (fp32 x in three terms; bf16 x where K is
- * no multiple of 64 or x not aligned to 16 bytes). */
+ * which the kernels read it, in 16 bits (fp32 x in three terms; bf16 x of more than
+ * eight rows, or where K is no multiple of 128 or x not aligned to 16 bytes). */
 size_t atlas_qlinear_workspace_bytes(const atlas_qlinear_handle* h, int M);
+
+/* Wait for the last forward on h and return its device status: ATLAS_OK, or
+ * ATLAS_ERR_TIMEOUT if a bounded wait of the kernel gave up (its outputs are then
+ * not valid).  Clears the status word. */
+int atlas_qlinear_status(atlas_qlinear_handle* h);
 
 /* Message of the last failure on h, or of the last failed create when h is NULL. */
 const char* atlas_qlinear_last_error(const atlas_qlinear_handle* h);

@@ -44,7 +44,7 @@ EXPORTS = ("atlas_mem_create", "atlas_mem_forward", "atlas_mem_forward_host", "a
            "atlas_conv_create", "atlas_conv_forward", "atlas_conv_last_error", "atlas_conv_destroy",
            "atlas_rms_create", "atlas_rms_forward", "atlas_rms_last_error", "atlas_rms_destroy",
            "atlas_qlinear_create", "atlas_qlinear_quantize", "atlas_qlinear_packed_bytes", "atlas_qlinear_pack",
-           "atlas_qlinear_forward", "atlas_qlinear_workspace_bytes", "atlas_qlinear_last_error",
+           "atlas_qlinear_forward", "atlas_qlinear_workspace_bytes", "atlas_qlinear_status", "atlas_qlinear_last_error",
            "atlas_qlinear_destroy",
            "atlas_scan_create", "atlas_scan_forward", "atlas_scan_workspace_bytes", "atlas_scan_status",
            "atlas_scan_last_path", "atlas_scan_last_error", "atlas_scan_destroy")
@@ -484,6 +484,10 @@ def atlas_qlinear_pack(h, q, scales, zeros, packed, stream: int = 0):
 
 def atlas_qlinear_workspace_bytes(h, M) -> int:
     return load().atlas_qlinear_workspace_bytes(h, M)
+
+
+def atlas_qlinear_status(h) -> int:
+    return load().atlas_qlinear_status(h)
 
 
 def atlas_scan_create(cfg: atlas_scan_config):

@@ -4,17 +4,20 @@
 // 16 of K), x the second (16 of K by 8 rows): one instruction uses 256 weights
 // for eight rows, so that up to about 16 rows the weights' way from memory and
 // their unpacking set the time.  K may come in any order within a group, so a
-// lane takes eight neighbouring values of its row of x (16 bytes of bf16) per
-// 32 of K, and the weights are packed to match:
+// lane takes eight neighbouring values of its row of x (16 bytes) per 32 of K, and
+// the weights are packed to match.
 //
-//   tile (16 columns), step (64 of K): 32 lanes x 16 bytes, 512 in a row.
-//   Word m of a lane (g = lane / 4, c = lane % 4) has, with k = 64 step + 32 (m /
-//   2) + 8 c + 4 (m % 2), from its lowest four bits up, q of
+// The laid out weights are blocks of 128 columns by 128 of K, each in one piece
+// that one bulk copy brings: codes [8 tiles of 16 columns][2 steps of 64 of K][32
+// lanes][16 bytes], scales [128 / group][8 tiles][8], a word each, zero points
+// [128 / group][8 tiles][8], a byte each.
+//   Word m of a lane (g = lane / 4, c = lane % 4) of a step has, with k = 32 (m /
+//   2) + 8 c + 4 (m % 2) in the step, from its lowest four bits up, q of
 //   (k, g) (k, g + 8) (k + 2, g) (k + 2, g + 8) (k + 1, g) (k + 1, g + 8) (k + 3, g) (k + 3, g + 8)
-//
-// so that (word >> 4 i) & 0x000f000f is a pair of neighbours in K.  Or-ed into
-// the mantissa of 128 (bf16) or 1024 (fp16) it is 128 + q, and less 128 + zero
-// it is q - zero, exactly.
+// so that (word >> 4 i) & 0x000f000f is a pair of neighbours in K.  Or-ed into the
+// mantissa of 128 (bf16) or 1024 (fp16) it is 128 + q, and less 128 + zero it is
+// q - zero, exactly.  A scale's word and a zero point's byte are of columns g and
+// g + 8.
 #include "../../include/atlas_qlinear.h"
 
 #include <cuda_fp16.h>
@@ -31,42 +34,47 @@ using namespace layer;
 
 namespace {
 
-constexpr int kWarps = 8, kThreads = 32 * kWarps;
-constexpr int kStep = 64;       // of K, a packed 16 bytes of each lane
+constexpr int kWarps = 8, kThreads = 32 * (kWarps + 1);   // eight work, one loads
+constexpr int kCols = 128, kChunk = 128, kCodes = kCols * kChunk / 2;
+constexpr int kRowBytes = 320;   // of a chunk of a row of x in shared memory: 256, and no two rows of a pair in the same banks
+constexpr int kMostStages = 4;
 constexpr int kMostRows = 65535 * 64;
 
-// How the kernel gets x: bf16 rows as the caller has them (whole steps of K), or,
-// from a pass in front, as fragments: [8 rows][step][lane][2] of 16 bytes, bf16,
-// fp16 (e4m3 values, exactly), or three planes of bf16 (fp32 values).  Converting
-// e4m3 in every block instead took a third of the product's instructions.
+// How the kernel gets x: bf16 rows as the caller has them (whole chunks of K, eight
+// rows), or, from a pass in front, as fragments: [row block][chunk][plane][8 rows][4
+// times 32 of K][32 lanes] of 16 bytes, bf16, fp16 (e4m3 values, exactly), or three
+// planes of bf16 (fp32 values).  Converting e4m3 in every block instead took a third
+// of the product's instructions.
 enum { X_ROWS, X_BF16, X_F16, X_PLANES };
+__host__ __device__ constexpr int planes_of(int x) { return x == X_PLANES ? 3 : 1; }
 
 struct Shape {
-  int K, N, group, groups, tiles, steps;
-  __host__ __device__ size_t scale_at() const { return (size_t)tiles * steps * 512; }
-  __host__ __device__ size_t zero_at() const { return scale_at() + (size_t)groups * tiles * 32; }
+  int K, N, group, zeros, blocks, chunks;   // blocks of columns, chunks of K
+  __host__ __device__ int groups() const { return kChunk / group; }   // of a chunk
+  __host__ __device__ int block_bytes() const { return kCodes + groups() * (zeros ? 320 : 256); }
 };
 Shape make_shape(const atlas_qlinear_config& c) {
-  return Shape{c.K, c.N, c.group, (c.K + c.group - 1) / c.group, (c.N + 15) / 16, (c.K + kStep - 1) / kStep};
+  return Shape{c.K, c.N, c.group, c.zeros, (c.N + kCols - 1) / kCols, (c.K + kChunk - 1) / kChunk};
 }
 
 struct Call {
   Shape s;
-  int M, act, zeros, x_block, xblocks, per;   // per: steps of a warp
-  bool early;                                 // the pass in front is this call's own
-  size_t plane;                               // 16-byte groups of a plane of x
-  const uint4* x;
+  int M, act, out_bf16, x_block, xblocks;
+  int turns, stages;       // chunks of each K group; stages of the ring
+  bool early;              // the pass in front is this call's own
+  const uint8_t* x;
   const float* x_scale;
   const uint8_t* W;
   const float* bias;
+  int* status;
 };
 
 // D (16 x 8) = A (16 x 16) B (16 x 8) + D, or + 0
 template <bool HALF, bool FIRST>
 __device__ __forceinline__ void mma(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
-#define ATLAS_MMA(T, C, ...)                                                                                          \
+#define ATLAS_MMA(T, C, ...)                                                                                            \
   asm volatile("mma.sync.aligned.m16n8k16.row.col.f32." T "." T ".f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, " C ";" \
-               : __VA_ARGS__                                                                                          \
+               : __VA_ARGS__                                                                                            \
                : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f))
   if constexpr (FIRST) {
     if constexpr (HALF) ATLAS_MMA("f16", "{%10, %10, %10, %10}", "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3]));
@@ -84,17 +92,25 @@ struct Offset {
   uint32_t low, high;   // 128 + zero; fp16: 1024 + zero and -(64 + zero)
 };
 template <bool HALF>
-__device__ __forceinline__ void weights(uint32_t word, const Offset* off, uint32_t* q) {
-  constexpr uint32_t magic = HALF ? 0x64006400u : 0x43004300u, sixteenth = 0x2c002c00u;
+__device__ __forceinline__ constexpr uint32_t magic_of() { return HALF ? 0x64006400u : 0x43004300u; }
+// (a & mask) | magic in one instruction: that takes the magic from a register (two
+// constants make two instructions of the pipe that is busiest)
+__device__ __forceinline__ uint32_t pick(uint32_t a, uint32_t mask, uint32_t magic) {
+  uint32_t d;
+  asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(d) : "r"(a), "r"(mask), "r"(magic));
+  return d;
+}
+template <bool HALF>
+__device__ __forceinline__ void weights(uint32_t word, const Offset* off, uint32_t magic, uint32_t* q) {
+  constexpr uint32_t sixteenth = 0x2c002c00u;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     if constexpr (HALF) {
       const uint32_t w = i < 2 ? word : word >> 8;
-      if (i % 2 == 0) asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(q[i]) : "r"((w & 0x000f000fu) | magic), "r"(off[0].low));
-      else asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(q[i]) : "r"((w & 0x00f000f0u) | magic), "r"(sixteenth), "r"(off[1].high));
+      if (i % 2 == 0) asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(q[i]) : "r"(pick(w, 0x000f000fu, magic)), "r"(off[0].low));
+      else asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(q[i]) : "r"(pick(w, 0x00f000f0u, magic)), "r"(sixteenth), "r"(off[1].high));
     } else {
-      const uint32_t v = ((word >> (4 * i)) & 0x000f000fu) | magic;
-      asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(q[i]) : "r"(v), "r"(off[i % 2].low));
+      asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(q[i]) : "r"(pick(word >> (4 * i), 0x000f000fu, magic)), "r"(off[i % 2].low));
     }
   }
 }
@@ -110,180 +126,239 @@ __device__ __forceinline__ uint32_t two_halves(uint32_t e4m3x2) {
   return (uint32_t)h.x | ((uint32_t)h.y << 16);
 }
 
-// A block: 16 NT columns, 8 MT rows, all or (as one of a cluster) a part of K,
-// which its warps split.  Sums over the warps, then over the cluster's blocks,
-// through shared memory and always in the same order.
-template <int X, int MT, int NT, typename TO>
-__global__ void __launch_bounds__(kThreads, 2) k_qlinear(Call c, const TO* residual, TO* y) {
+// plain bytes; addresses and size multiples of 16
+__device__ __forceinline__ void load_bytes(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(__cvta_generic_to_global(src)), "r"(bytes), "r"(bar)
+               : "memory");
+}
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+  return v;
+}
+
+template <int X, int MT, int WK>
+struct Stage {   // bytes: WK blocks of weights, then WK pieces of x
+  static constexpr int x = X == X_ROWS ? 8 * kRowBytes : planes_of(X) * MT * 2048;
+  __host__ __device__ static int bytes(const Shape& s) { return WK * (s.block_bytes() + x); }
+};
+
+// by registers: two sums of 16 or 32 columns by 8 MT rows in a warp
+constexpr int blocks_per_sm(int mt) { return mt >= 4 ? 1 : 2; }
+
+// A block of the grid: 128 columns, 8 MT rows, all or (as one of a cluster) a part
+// of K.  Its ninth warp keeps a ring of stages full by bulk copies; the others are
+// WN sets of 16 NT columns times WK parts of a stage's K.  What bounds it: the
+// unpacking (about 20 instructions for eight weights of a lane, nine of them of the
+// pipe for logic that takes one in two cycles): 31 GB/s of codes an SM with
+// two blocks, 4.8 TB/s in all.  1 x 8192 x 8192: 11.0 us (33.5 MB), 16 rows in e4m3 16.3;
+// 1 x 2048 x 8192 5.0, most of it start and end.  Sums over the WK
+// parts, then over the cluster's blocks, through shared memory and always in the
+// same order.
+template <int X, int MT, int NT, int GROUPS>
+__global__ void __launch_bounds__(kThreads, blocks_per_sm(MT)) k_qlinear(Call c, const void* residual, void* y) {
   constexpr bool HALF = X == X_F16;
-  constexpr int PLANES = X == X_PLANES ? 3 : 1, COLS = 16 * NT, ROWS = 8 * MT, LD = COLS + 4;
-  constexpr int AHEAD = NT * MT <= 2 ? 4 : 2;      // steps of weights in flight
-  constexpr bool X_AHEAD = MT * PLANES <= 2;       // x a step ahead too
-  extern __shared__ float red[];               // [kWarps][ROWS][LD], the sums in the first
+  constexpr int PLANES = planes_of(X), WN = kCols / 16 / NT, WK = kWarps / WN, ROWS = 8 * MT, LD = kCols + 4;
+  using L = Stage<X, MT, WK>;
+  extern __shared__ __align__(128) uint8_t sm[];   // the ring; then [WK][ROWS][LD] sums
+  __shared__ uint64_t bars[2 * kMostStages];       // full, empty
+  __shared__ int failed;
+  float* red = reinterpret_cast<float*>(sm);
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, gr = lane / 4, ln = lane % 4;
   const uint32_t rank = tc::cluster_rank();
   uint32_t S;
   asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(S));
-  const int tile0 = blockIdx.x / S * NT, m0 = blockIdx.y * ROWS;
   const Shape& s = c.s;
-  const int s_lo = min(s.steps, (int)(rank * kWarps + warp) * c.per), s_hi = min(s.steps, s_lo + c.per);
-  const int mask = s.group - 1;
-  // one address each, and small offsets from it: a register instead of two
-  const size_t group0 = (size_t)(s_lo * kStep / s.group) * s.tiles * 8 + (size_t)tile0 * 8 + gr;
-  const uint4* wt = reinterpret_cast<const uint4*>(c.W) + ((size_t)tile0 * s.steps + s_lo) * 32 + lane;
-  const uint32_t* sc = reinterpret_cast<const uint32_t*>(c.W + s.scale_at()) + group0;
-  const uint8_t* ze = c.W + s.zero_at() + group0;
-  uint32_t tile[NT], row[MT], xs_row[MT][2];
-#pragma unroll
-  for (int n = 0; n < NT; ++n) tile[n] = min(n, s.tiles - 1 - tile0);   // columns past the last: any, they are not stored
-  // x: 16-byte groups; rows past the last: any row's values or zeros, they are not stored
-  const uint4* xr = c.x + (X == X_ROWS ? (size_t)m0 * (s.K / 8) + s_lo * (kStep / 8) + ln
-                                       : ((size_t)(m0 / 8) * s.steps + s_lo) * 64 + lane * 2);
-  const float* xsr = c.x_scale + (size_t)m0 * c.xblocks;
-#pragma unroll
-  for (int m = 0; m < MT; ++m) {
-    row[m] = X == X_ROWS ? (uint32_t)min(8 * m + gr, c.M - 1 - m0) * (s.K / 8)
-                         : (uint32_t)min(m, (c.M - 1 - m0) / 8) * s.steps * 64;
-#pragma unroll
-    for (int e = 0; e < 2; ++e) xs_row[m][e] = (uint32_t)min(8 * m + 2 * ln + e, c.M - 1 - m0) * c.xblocks;
+  const int block = blockIdx.x / S, m0 = blockIdx.y * ROWS, block_bytes = s.block_bytes(), stage_bytes = L::bytes(s);
+  const uint32_t base = tc::smem_u32(sm), full = tc::smem_u32(bars), empty = full + 8 * kMostStages;
+  if (tid == 0) {
+    for (int i = 0; i < kMostStages; ++i) tc::mbar_init_only(bars + i, 1), tc::mbar_init_only(bars + kMostStages + i, kWarps);
+    tc::mbar_init_fence();
+    failed = 0;
   }
-  uint4 w[AHEAD][NT];
-  auto first_weights = [&]() {
-#pragma unroll
-    for (int a = 0; a < AHEAD; ++a)
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-        if (s_lo + a < s_hi) w[a][n] = __ldg(wt + (tile[n] * (uint32_t)s.steps + a) * 32);
-  };
-  // Behind the call's own pass over x the weights need not wait for it: that pass
-  // let this kernel start only after all work in front of it was done.
-  if (c.early) first_weights();
-  tc::grid_dependency_wait();
-  tc::grid_dependents_launch();
-  if (!c.early) first_weights();
-  struct Frag {   // of half a step
-    uint4 v[MT][PLANES];
-  };
-  auto load_x = [&](int at, int h, Frag& f) {   // the at-th of the warp's steps
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-      for (int p = 0; p < PLANES; ++p)
-        f.v[m][p] = X == X_ROWS ? __ldg(xr + (row[m] + at * (kStep / 8) + 4 * h)) : __ldg(xr + p * c.plane + (row[m] + at * 64 + h));
-  };
-  Frag x[2][2];   // X_AHEAD: by step parity and half
-  if (X_AHEAD && s_lo < s_hi) load_x(0, 0, x[0][0]), load_x(0, 1, x[0][1]);
-
-  float tot[NT][MT][4] = {}, acc[NT][MT][4];
-  uint32_t scale[NT];
-  Offset off[NT][2];
-  float xs[MT][2];
-#pragma unroll
-  for (int n = 0; n < NT; ++n) off[n][0] = off[n][1] = offset_of<HALF>(8);
-  auto open = [&](int k) {   // a group begins, or the warp's part of one
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      scale[n] = __ldg(sc + tile[n] * 8);
-      if (c.zeros) {
-        const uint32_t z = __ldg(ze + tile[n] * 8);
-        off[n][0] = offset_of<HALF>(z & 15u);
-        off[n][1] = offset_of<HALF>(z >> 4);
-      }
-    }
-    sc += s.tiles * 8;
-    ze += s.tiles * 8;
-    if constexpr (X == X_F16) {
-#pragma unroll
-      for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) xs[m][e] = c.x_block ? __ldg(xsr + (xs_row[m][e] + k / 128)) : 1.f;
-    }
-  };
-  auto close = [&]() {
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      const float a = __uint_as_float(scale[n] << 16), b = __uint_as_float(scale[n] & 0xffff0000u);
-#pragma unroll
-      for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          float f = e < 2 ? a : b;
-          if constexpr (X == X_F16) f *= xs[m][e & 1];
-          tot[n][m][e] = fmaf(acc[n][m][e], f, tot[n][m][e]);
-        }
-    }
-  };
-  // half a step: 32 of K; FIRST: of a group
-  auto half = [&](auto first, const Frag& f, const uint4* words, int h) {
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      const uint32_t word[2] = {h ? words[n].z : words[n].x, h ? words[n].w : words[n].y};
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        uint32_t q[4];
-        weights<HALF>(word[j], off[n], q);
-#pragma unroll
-        for (int p = PLANES - 1; p >= 0; --p)   // the smallest terms first
-#pragma unroll
-          for (int m = 0; m < MT; ++m) {
-            const uint4& v = f.v[m][p];
-            if (decltype(first)::value && j == 0 && p == PLANES - 1) mma<HALF, true>(acc[n][m], q, v.x, v.y);
-            else mma<HALF, false>(acc[n][m], q, j ? v.z : v.x, j ? v.w : v.y);
-          }
-      }
-    }
-  };
-  for (int st0 = s_lo; st0 < s_hi; st0 += AHEAD) {
-#pragma unroll
-    for (int a = 0; a < AHEAD; ++a) {
-      const int st = st0 + a;
-      if (st >= s_hi) break;
-      if (X_AHEAD && st + 1 < s_hi) load_x(st + 1 - s_lo, 0, x[(a + 1) & 1][0]), load_x(st + 1 - s_lo, 1, x[(a + 1) & 1][1]);
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int k = st * kStep + 32 * h;
-        if (h == 1 && k >= s.K) break;
-        Frag& f = x[X_AHEAD ? a & 1 : 0][X_AHEAD ? h : 0];
-        if constexpr (!X_AHEAD) load_x(st - s_lo, h, f);
-        if ((k & mask) == 0 || (h == 0 && st == s_lo)) {
-          open(k);
-          half(std::true_type(), f, w[a], h);
-        } else {
-          half(std::false_type(), f, w[a], h);
-        }
-        if (((k + 32) & mask) == 0) close();
-      }
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-        if (st + AHEAD < s_hi) w[a][n] = __ldg(wt + (tile[n] * (uint32_t)s.steps + a + AHEAD) * 32);
-    }
-    wt += AHEAD * 32;
-  }
-  // a part of a group: K's last, or one that ends with the warp's steps
-  if (s_lo < s_hi && (min((s.K + 31) / 32 * 32, s_hi * kStep) & mask) != 0) close();
-
-#pragma unroll
-  for (int n = 0; n < NT; ++n)
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        red[(warp * ROWS + 8 * m + 2 * ln + (e & 1)) * LD + 16 * n + gr + 8 * (e >> 1)] = tot[n][m][e];
   __syncthreads();
-  for (int i = tid; i < ROWS * COLS; i += kThreads) {
-    const int at = i / COLS * LD + i % COLS;
-    float t = red[at];
+  // the chunk that K group kg works on in a turn; none past the last
+  auto chunk_of = [&](int turn, int kg) { return (turn * (int)S + (int)rank) * WK + kg; };
+  bool ok = true;
+  // a turn's stage, and the parity of its round of the ring
+  struct Place {
+    int stage = 0;
+    uint32_t parity = 0;
+    __device__ __forceinline__ void next(int stages) {
+      if (++stage == stages) stage = 0, parity ^= 1;
+    }
+  };
+  if (warp == kWarps) {
+    const uint8_t* W = c.W + (size_t)block * s.chunks * block_bytes;
+    const int rows = min(8, c.M - m0);   // X_ROWS
+    const uint8_t* x = X == X_ROWS ? c.x + (size_t)m0 * s.K * 2 : c.x + (size_t)blockIdx.y * s.chunks * L::x;
+    // the lanes side by side: one a block of weights, then one a piece (or row) of x
+    auto weights_of = [&](int turn, int stage) {
+      const uint32_t bar = full + 8 * stage, at = base + stage * stage_bytes;
+      if (lane == 0) {
+        int live = 0;
 #pragma unroll
-    for (int p = 1; p < kWarps; ++p) t += red[p * ROWS * LD + at];
-    red[at] = t;   // the thread's own place
+        for (int kg = 0; kg < WK; ++kg) live += chunk_of(turn, kg) < s.chunks;
+        tc::expect_tx(bar, live * (block_bytes + (X == X_ROWS ? rows * kChunk * 2 : L::x)));
+      }
+      __syncwarp();
+      if (lane < WK && chunk_of(turn, lane) < s.chunks)
+        load_bytes(at + lane * block_bytes, W + (size_t)chunk_of(turn, lane) * block_bytes, block_bytes, bar);
+    };
+    auto x_of = [&](int turn, int stage) {
+      const uint32_t bar = full + 8 * stage, at = base + stage * stage_bytes + WK * block_bytes;
+      const int kg = X == X_ROWS ? lane / 8 : lane, r = lane % 8;
+      if (kg >= WK || chunk_of(turn, kg) >= s.chunks) return;
+      if constexpr (X == X_ROWS) {
+        if (r < rows)
+          load_bytes(at + kg * L::x + r * kRowBytes, x + ((size_t)r * s.K + chunk_of(turn, kg) * kChunk) * 2, kChunk * 2, bar);
+      } else {
+        load_bytes(at + kg * L::x, x + (size_t)chunk_of(turn, kg) * L::x, L::x, bar);
+      }
+    };
+    const int first = min(c.turns, c.stages);
+    // Behind the call's own pass over x the weights need not wait for it: that pass
+    // let this kernel start only after all work in front of it was done.
+    if (c.early)
+      for (int t = 0; t < first; ++t) weights_of(t, t);
+    tc::grid_dependency_wait();
+    tc::grid_dependents_launch();
+    for (int t = 0; t < first; ++t) {
+      if (!c.early) weights_of(t, t);
+      x_of(t, t);
+    }
+    Place p;
+    for (int t = first; t < c.turns; ++t, p.next(c.stages)) {
+      ok = __all_sync(0xffffffffu, tc::wait(empty + 8 * p.stage, p.parity));
+      if (!ok) break;
+      weights_of(t, p.stage);
+      x_of(t, p.stage);
+    }
+  } else {
+    const int kg = warp / WN, tile0 = warp % WN * NT;   // the warp's tiles of the block
+    tc::grid_dependency_wait();
+    tc::grid_dependents_launch();
+    const uint32_t x_lane = X == X_ROWS ? min(gr, c.M - 1 - m0) * kRowBytes + 16 * ln : lane * 16;
+    float tot[NT][MT][4] = {}, acc[NT][MT][4];
+    const float* xsr = c.x_scale;
+    uint32_t xs_row[MT][2];   // rows past the last: any row's
+    if constexpr (X == X_F16) {
+      xsr += (size_t)m0 * c.xblocks;
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) xs_row[m][e] = (uint32_t)min(8 * m + 2 * ln + e, c.M - 1 - m0) * c.xblocks;
+    }
+    const uint32_t w_lane = kg * block_bytes + tile0 * 1024 + lane * 16, s_lane = kg * block_bytes + kCodes + (tile0 * 8 + gr) * 4,
+                   z_lane = kg * block_bytes + kCodes + GROUPS * 256 + tile0 * 8 + gr,
+                   x_at = WK * block_bytes + kg * L::x + x_lane;
+    const uint32_t magic = magic_of<HALF>() | (uint32_t)(c.M >> 31);   // (M > 0; a value that is not known when compiling)
+    int chunk = chunk_of(0, kg);
+    Place p;
+    for (int t = 0; t < c.turns; ++t, p.next(c.stages), chunk += (int)S * WK) {
+      const bool live = chunk < s.chunks;
+      float xs[MT][2];
+      if constexpr (X == X_F16) {   // a chunk is a run of the scales
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) xs[m][e] = c.x_block && live ? __ldg(xsr + (xs_row[m][e] + chunk)) : 1.f;
+      }
+      if (!(ok = __all_sync(0xffffffffu, tc::wait(full + 8 * p.stage, p.parity)))) break;
+      if (live) {
+        const uint32_t at = base + p.stage * stage_bytes;
+        Offset off[NT][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) off[n][0] = off[n][1] = offset_of<HALF>(8);
+        uint4 w[NT];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {   // 32 of K each
+          uint4 x[MT][PLANES];
+#pragma unroll
+          for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int q = 0; q < PLANES; ++q) x[m][q] = lds128(at + x_at + (X == X_ROWS ? 64 * i : ((q * MT + m) * 4 + i) * 512));
+          if (i % 2 == 0)
+#pragma unroll
+            for (int n = 0; n < NT; ++n) w[n] = lds128(at + w_lane + n * 1024 + i * 256);
+          constexpr int kHalves = 4 / GROUPS;   // 32 of K, of a group
+          if (i % kHalves == 0 && s.zeros) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+              uint32_t v;
+              asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(at + z_lane + i / kHalves * 64 + n * 8));
+              off[n][0] = offset_of<HALF>(v & 15u);
+              off[n][1] = offset_of<HALF>(v >> 4);
+            }
+          }
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            const uint32_t word[2] = {i % 2 ? w[n].z : w[n].x, i % 2 ? w[n].w : w[n].y};
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              uint32_t v[4];
+              weights<HALF>(word[j], off[n], magic, v);
+#pragma unroll
+              for (int q = PLANES - 1; q >= 0; --q)   // the smallest terms first
+#pragma unroll
+                for (int m = 0; m < MT; ++m) {
+                  if (i % kHalves == 0 && j == 0 && q == PLANES - 1) mma<HALF, true>(acc[n][m], v, x[m][q].x, x[m][q].y);
+                  else mma<HALF, false>(acc[n][m], v, j ? x[m][q].z : x[m][q].x, j ? x[m][q].w : x[m][q].y);
+                }
+            }
+          }
+          if ((i + 1) % kHalves == 0) {   // a group ends
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+              uint32_t v;
+              asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(at + s_lane + i / kHalves * 256 + n * 32));
+              const float scale[2] = {__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u)};
+#pragma unroll
+              for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  float f = scale[e >> 1];
+                  if constexpr (X == X_F16) f *= xs[m][e & 1];
+                  tot[n][m][e] = fmaf(acc[n][m][e], f, tot[n][m][e]);
+                }
+            }
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(bars + kMostStages + p.stage);
+    }
+    // every copy has landed and been read (or a wait gave up): the ring becomes the sums
+    if (!ok && lane == 0) atomicExch(&failed, 1);
+    asm volatile("bar.sync 1, %0;" ::"n"(32 * kWarps) : "memory");
+    if (failed) tc::settle();
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          red[(kg * ROWS + 8 * m + 2 * ln + (e & 1)) * LD + 16 * (tile0 + n) + gr + 8 * (e >> 1)] = tot[n][m][e];
+    asm volatile("bar.sync 1, %0;" ::"n"(32 * kWarps) : "memory");
+    if (WK > 1)
+      for (int i = tid; i < ROWS * kCols; i += 32 * kWarps) {
+        const int at = i / kCols * LD + i % kCols;
+        float t = red[at];
+#pragma unroll
+        for (int p = 1; p < WK; ++p) t += red[p * ROWS * LD + at];
+        red[at] = t;   // the thread's own place
+      }
   }
+  if (!ok && lane == 0) atomicExch(c.status, ATLAS_ERR_TIMEOUT);
   if (S > 1) tc::cluster_sync();
   else __syncthreads();
   // this block's share of the results
-  for (int i = rank * kThreads + tid; i < ROWS * COLS; i += S * kThreads) {
-    const int m = m0 + i / COLS, col = tile0 * 16 + i % COLS;
+  const int col0 = block * kCols;
+  for (int i = rank * kThreads + tid; i < ROWS * kCols; i += S * kThreads) {
+    const int m = m0 + i / kCols, col = col0 + i % kCols;
     if (m >= c.M || col >= s.N) continue;
-    const float* from = red + i / COLS * LD + i % COLS;
+    const float* from = red + i / kCols * LD + i % kCols;
     float t = 0.f;
     if (S == 1) {
       t = *from;
@@ -296,28 +371,36 @@ __global__ void __launch_bounds__(kThreads, 2) k_qlinear(Call c, const TO* resid
     }
     if (X == X_F16 && c.x_block == 0) t *= c.x_scale[m];
     if (c.bias) t += c.bias[col];
-    linear::act_run<TO, 1>(c.act, &t);
-    if (residual) t += to_f32(residual[(size_t)m * s.N + col]);
-    y[(size_t)m * s.N + col] = from_f32<TO>(t);
+    const size_t at = (size_t)m * s.N + col;
+    if (c.out_bf16) {
+      linear::act_run<bf16, 1>(c.act, &t);
+      if (residual) t += to_f32(reinterpret_cast<const bf16*>(residual)[at]);
+      reinterpret_cast<bf16*>(y)[at] = from_f32<bf16>(t);
+    } else {
+      linear::act_run<float, 1>(c.act, &t);
+      if (residual) t += reinterpret_cast<const float*>(residual)[at];
+      reinterpret_cast<float*>(y)[at] = t;
+    }
   }
   if (S > 1) tc::cluster_sync();   // no block leaves while another reads its sums
 }
 
 // x as fragments: a thread writes 16 bytes of each plane, eight values of a row,
-// zeros past K and M.  fp32 values as three bf16 planes, the leading 8 bits, the next 8 and the
-// last 8, each cut off, so that their sum is the value itself (infinities and NaN
-// stay in the first).
+// zeros past K and M.  fp32 values as three bf16 planes, the leading 8 bits, the
+// next 8 and the last 8, each cut off, so that their sum is the value itself
+// (infinities and NaN stay in the first).
 template <typename TI, int X>
-__global__ void __launch_bounds__(256) k_fragments(const TI* __restrict__ x, uint4* __restrict__ dst, int M, int K, int steps,
-                                                   size_t plane) {
+__global__ void __launch_bounds__(256) k_fragments(const TI* __restrict__ x, uint4* __restrict__ dst, int M, int K, int chunks,
+                                                   int tiles, size_t n) {
   tc::grid_dependency_wait();
   tc::grid_dependents_launch();
   const size_t i = (size_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= plane) return;
-  const int h = (int)(i % 2), lane = (int)(i / 2 % 32), step = (int)(i / 64 % steps);
-  const size_t r = i / 64 / steps * 8 + lane / 4;
-  const int k = step * kStep + 32 * h + 8 * (lane % 4);
-  constexpr int PLANES = X == X_PLANES ? 3 : 1;
+  if (i >= n) return;
+  constexpr int PLANES = planes_of(X);
+  // 128 pieces of 16 bytes for eight rows of a chunk; `tiles` times eight rows of a row block
+  const int lane = (int)(i % 32), part = (int)(i / 32 % 4), tile = (int)(i / 128 % tiles), chunk = (int)(i / 128 / tiles % chunks);
+  const size_t block = i / 128 / tiles / chunks, r = (block * tiles + tile) * 8 + lane / 4;
+  const int k = chunk * kChunk + 32 * part + 8 * (lane % 4);
   uint32_t out[PLANES][4];
 #pragma unroll
   for (int e = 0; e < 8; e += 2) {
@@ -344,43 +427,44 @@ __global__ void __launch_bounds__(256) k_fragments(const TI* __restrict__ x, uin
     for (int p = 0; p < PLANES; ++p)
       out[p][e / 2] = X == X_F16 ? two_halves(half[p][0] | (half[p][1] << 8)) : half[p][0] | (half[p][1] << 16);
   }
+  uint4* at = dst + ((block * chunks + chunk) * PLANES * tiles + tile) * 128 + part * 32 + lane;
 #pragma unroll
-  for (int p = 0; p < PLANES; ++p) dst[p * plane + i] = make_uint4(out[p][0], out[p][1], out[p][2], out[p][3]);
+  for (int p = 0; p < PLANES; ++p) at[p * tiles * 128] = make_uint4(out[p][0], out[p][1], out[p][2], out[p][3]);
 }
 
-// a thread: a word of the laid out weights, or of the scales
+// a thread: four bytes of a block
 __global__ void __launch_bounds__(256) k_pack(Shape s, const uint8_t* __restrict__ q, const uint16_t* __restrict__ scales,
                                               const uint8_t* __restrict__ zeros, uint8_t* __restrict__ out) {
-  const size_t i = (size_t)blockIdx.x * 256 + threadIdx.x, words = (size_t)s.tiles * s.steps * 128;
-  if (i < words) {
-    const int m = (int)(i % 4), lane = (int)(i / 4 % 32), g = lane / 4, c = lane % 4;
-    const size_t rest = i / 128;
-    const int step = (int)(rest % s.steps), tile = (int)(rest / s.steps);
-    const int k0 = step * kStep + 32 * (m / 2) + 8 * c + 4 * (m % 2);
-    uint32_t word = 0;
+  const int per = s.block_bytes() / 4, groups = s.groups(), all = (s.K + s.group - 1) / s.group;
+  const size_t i = (size_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= (size_t)s.blocks * s.chunks * per) return;
+  const int at = (int)(i % per), chunk = (int)(i / per % s.chunks), col0 = (int)(i / per / s.chunks) * kCols;
+  auto zero = [&](int grp, int n) {   // past K and N: weights of 0
+    return zeros && n < s.N ? zeros[(size_t)min(grp, all - 1) * s.N + n] & 15u : 8u;
+  };
+  uint32_t word = 0;
+  if (at < kCodes / 4) {
+    const int m = at % 4, lane = at / 4 % 32, g = lane / 4, c = lane % 4, step = at / 128 % 2, tile = at / 256;
+    const int k0 = chunk * kChunk + 64 * step + 32 * (m / 2) + 8 * c + 4 * (m % 2);
 #pragma unroll
     for (int e = 0; e < 8; ++e) {   // four bits each, from the lowest
-      const int n = tile * 16 + g + 8 * (e & 1), k = k0 + 2 * ((e >> 1) & 1) + (e >> 2);
-      uint32_t v = 8;
-      if (n < s.N) {
-        if (k < s.K) v = (q[(size_t)(k / 2) * s.N + n] >> (4 * (k & 1))) & 15u;
-        else if (zeros) v = zeros[(size_t)(s.groups - 1) * s.N + n] & 15u;   // past K: a weight of 0
-      }
+      const int n = col0 + tile * 16 + g + 8 * (e & 1), k = k0 + 2 * ((e >> 1) & 1) + (e >> 2);
+      const uint32_t v = n < s.N && k < s.K ? (q[(size_t)(k / 2) * s.N + n] >> (4 * (k & 1))) & 15u : zero(k / s.group, n);
       word |= v << (4 * e);
     }
-    reinterpret_cast<uint32_t*>(out)[i] = word;
-    return;
+  } else if (at < kCodes / 4 + groups * 64) {
+    const int j = at - kCodes / 4, n = col0 + j / 8 % 8 * 16 + j % 8, grp = chunk * groups + j / 64;
+    auto scale = [&](int col) { return col < s.N && grp < all ? (uint32_t)scales[(size_t)grp * s.N + col] : 0u; };
+    word = scale(n) | (scale(n + 8) << 16);
+  } else {
+    const int j = (at - kCodes / 4 - groups * 64) * 4, grp = chunk * groups + j / 64;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int n = col0 + (j + e) / 8 % 8 * 16 + (j + e) % 8;
+      word |= (zero(grp, n) | (zero(grp, n + 8) << 4)) << (8 * e);
+    }
   }
-  const size_t j = i - words;
-  if (j >= (size_t)s.groups * s.tiles * 8) return;
-  const int g = (int)(j % 8), tile = (int)(j / 8 % s.tiles), grp = (int)(j / 8 / s.tiles);
-  const int n = tile * 16 + g;
-  auto scale = [&](int col) { return col < s.N ? (uint32_t)scales[(size_t)grp * s.N + col] : 0u; };
-  reinterpret_cast<uint32_t*>(out + s.scale_at())[j] = scale(n) | (scale(n + 8) << 16);
-  if (zeros) {
-    auto zero = [&](int col) { return col < s.N ? zeros[(size_t)grp * s.N + col] & 15u : 8u; };
-    out[s.zero_at() + j] = (uint8_t)(zero(n) | (zero(n + 8) << 4));
-  }
+  reinterpret_cast<uint32_t*>(out)[i] = word;
 }
 
 // a thread: a column of a group
@@ -388,7 +472,7 @@ template <typename T>
 __global__ void __launch_bounds__(256) k_quantize(Shape s, const T* __restrict__ W, uint8_t* __restrict__ q,
                                                   bf16* __restrict__ scales, uint8_t* __restrict__ zeros) {
   const size_t i = (size_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= (size_t)s.groups * s.N) return;
+  if (i >= (size_t)((s.K + s.group - 1) / s.group) * s.N) return;
   const int n = (int)(i % s.N), grp = (int)(i / s.N), k0 = grp * s.group, k1 = min(s.K, k0 + s.group);
   float lo = 0.f, hi = 0.f;
   for (int k = k0; k < k1; ++k) {
@@ -418,69 +502,79 @@ __global__ void __launch_bounds__(256) k_quantize(Shape s, const T* __restrict__
   }
 }
 
+// Rows of a block: of x as fragments too
+int row_tiles(int M, int x_dtype) { return M <= 8 ? 1 : M <= 16 ? 2 : M <= 32 || x_dtype == ATLAS_F32 ? 4 : 8; }
+
 // What x goes through before the product: nothing, or a copy as fragments in the workspace.
 struct Operand {
-  int kind;
-  size_t plane, bytes;
+  int kind, tiles;
+  size_t pieces, bytes;   // pieces: of 16 bytes, of one plane
 };
 Operand make_operand(const atlas_qlinear_config& c, int M, bool aligned) {
   Operand o;
-  const size_t planes = c.x_dtype == ATLAS_F32 ? 3 : 1;
-  o.kind = c.x_dtype == ATLAS_F32 ? X_PLANES : c.x_dtype == ATLAS_E4M3 ? X_F16 : c.K % kStep || !aligned ? X_BF16 : X_ROWS;
-  o.plane = (size_t)(M + 7) / 8 * ((c.K + kStep - 1) / kStep) * 64;
-  o.bytes = o.kind == X_ROWS ? 0 : planes * o.plane * 16;
+  o.tiles = row_tiles(M, c.x_dtype);
+  o.kind = c.x_dtype == ATLAS_F32    ? X_PLANES
+           : c.x_dtype == ATLAS_E4M3 ? X_F16 : c.K % kChunk || !aligned || M > 8 ? X_BF16 : X_ROWS;
+  o.pieces = (size_t)(M + 8 * o.tiles - 1) / (8 * o.tiles) * o.tiles * ((c.K + kChunk - 1) / kChunk) * 128;
+  o.bytes = o.kind == X_ROWS ? 0 : planes_of(o.kind) * o.pieces * 16;
   return o;
 }
 
-template <int X, int MT, int NT, typename TO>
+template <int X, int MT, int NT>
 cudaError_t launch(Call c, const atlas_qlinear_io& io, cudaStream_t st) {
-  const int cols = (c.s.tiles + NT - 1) / NT, rows = (c.M + 8 * MT - 1) / (8 * MT);
-  // Blocks of a cluster that share K: as few steps of a warp, and rounds of blocks
-  // (two on an SM), as possible; a block's start and end take about four steps' time.
+  constexpr int WN = kCols / 16 / NT, WK = kWarps / WN;
+  const int rows = (c.M + 8 * MT - 1) / (8 * MT);
+  const size_t stage = Stage<X, MT, WK>::bytes(c.s), sums = (size_t)WK * 8 * MT * (kCols + 4) * sizeof(float);
+  // Stages: as many as leave room for the blocks of an SM, two at least.
+  int stages = kMostStages, per_sm = blocks_per_sm(MT);
+  while (stages > 2 && stages * stage > 224 * 1024 / per_sm) --stages;
+  if (stages * stage > 224 * 1024 / per_sm) per_sm = 1;
+  // Blocks of a cluster that share K.  Time, as measured (us): about 2.5 for a block's
+  // start and end and 0.63 a turn where every block has an SM of its own, 3.5 and 0.95
+  // where two share one, for each round of blocks.  1 x 2048 x 8192: clusters of 1, 2, 4,
+  // 8 take 6.7, 5.0, 6.0, 8.1; 1 x 8192 x 8192 21.6, 12.5, 11.0, 14.2; 4 x 4096 x 4096
+  // 14.7, 8.5, 5.3, 6.4; 37 x 1031 x 2517 in fp32 of 1, 2, 3, 4 17.8, 13.9, 11.9, 16.7.  Many
+  // rows' sums make clusters of 8 slow (64 x 2048 x 2048: 4 10.4, 8 13.5).
   int S = 1;
-  long long cost = 0;
-  for (int n = 1; n <= 8 && (n == 1 || c.s.steps >= n * kWarps); n *= 2) {
-    const long long rounds = ((long long)n * cols * rows + 2 * sm_count() - 1) / (2 * sm_count()),
-                    now = rounds * ((c.s.steps + n * kWarps - 1) / (n * kWarps) + 4 + (n > 1));
+  double cost = 0;
+  for (int n = 1; n <= (MT >= 4 ? 4 : 8) && (n == 1 || n * WK <= c.s.chunks); n += n < 4 ? 1 : 4) {
+    const long long blocks = (long long)n * c.s.blocks * rows, slots = per_sm * sm_count();
+    const int turns = (c.s.chunks + n * WK - 1) / (n * WK);
+    const double now = blocks <= sm_count() ? 2.5 + 0.63 * turns : (double)((blocks + slots - 1) / slots) * (3.5 + 0.95 * turns);
     if (n == 1 || now < cost) S = n, cost = now;
   }
-  c.per = (c.s.steps + S * kWarps - 1) / (S * kWarps);
-  const size_t smem = (size_t)kWarps * 8 * MT * (16 * NT + 4) * sizeof(float);
-  auto kern = k_qlinear<X, MT, NT, TO>;
-  if (smem > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-  }
+  c.turns = (c.s.chunks + S * WK - 1) / (S * WK);
+  c.stages = std::min(stages, c.turns);
+  const size_t smem = std::max(c.stages * stage, sums);
+  auto kern = c.s.group == 128 ? k_qlinear<X, MT, NT, 1> : c.s.group == 64 ? k_qlinear<X, MT, NT, 2> : k_qlinear<X, MT, NT, 4>;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim = {(unsigned)S, 1, 1};
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = dim3((unsigned)(cols * S), (unsigned)rows);
+  cfg.gridDim = dim3((unsigned)(c.s.blocks * S), (unsigned)rows);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, kern, c, (const TO*)io.residual, (TO*)io.y);
-}
-template <int X, typename TO>
-cudaError_t launch_rows(const Call& c, const atlas_qlinear_io& io, cudaStream_t st) {
-  if (c.M <= 8) return launch<X, 1, 2, TO>(c, io, st);
-  if (c.M <= 16) return launch<X, 2, 2, TO>(c, io, st);
-  if constexpr (X == X_PLANES) {
-    return launch<X, 4, 1, TO>(c, io, st);   // (three terms of more rows would not fit the registers)
-  } else {
-    if (c.M <= 32) return launch<X, 4, 2, TO>(c, io, st);
-    return launch<X, 8, 1, TO>(c, io, st);
-  }
+  return cudaLaunchKernelEx(&cfg, kern, c, io.residual, io.y);
 }
 template <int X>
-cudaError_t launch_out(const Call& c, const atlas_qlinear_io& io, int out, cudaStream_t st) {
-  return out == ATLAS_BF16 ? launch_rows<X, bf16>(c, io, st) : launch_rows<X, float>(c, io, st);
+cudaError_t launch_rows(const Call& c, const atlas_qlinear_io& io, int tiles, cudaStream_t st) {
+  if constexpr (X == X_ROWS) {
+    return launch<X, 1, 2>(c, io, st);
+  } else {
+    if (tiles == 1) return launch<X, 1, 2>(c, io, st);
+    if (tiles == 2) return launch<X, 2, 2>(c, io, st);
+    if (tiles == 4) return launch<X, 4, 2>(c, io, st);
+    if constexpr (X == X_PLANES) return cudaErrorInvalidValue;
+    else return launch<X, 8, 1>(c, io, st);
+  }
 }
-
 }  // namespace
 
 struct atlas_qlinear_handle : HandleBase {
@@ -521,7 +615,7 @@ extern "C" int atlas_qlinear_create(const atlas_qlinear_config* cfg, atlas_qline
 extern "C" size_t atlas_qlinear_packed_bytes(const atlas_qlinear_handle* h) {
   if (!h) return 0;
   const Shape s = make_shape(h->cfg);
-  return (s.zero_at() + (h->cfg.zeros ? (size_t)s.groups * s.tiles * 8 : 0) + 15) / 16 * 16;
+  return (size_t)s.blocks * s.chunks * s.block_bytes();
 }
 
 extern "C" int atlas_qlinear_quantize(atlas_qlinear_handle* h, const void* W, int w_dtype, uint8_t* q, void* scales,
@@ -532,7 +626,7 @@ extern "C" int atlas_qlinear_quantize(atlas_qlinear_handle* h, const void* W, in
   if ((zeros != nullptr) != (h->cfg.zeros != 0))
     return h->fail(ATLAS_ERR_INVALID_ARG, "zeros goes with a configuration that has zero points, and only with it");
   const Shape s = make_shape(h->cfg);
-  const size_t sn = (size_t)s.groups * s.N, qn = (size_t)((s.K + 1) / 2) * s.N, wn = (size_t)s.K * s.N * dtype_size(w_dtype);
+  const size_t sn = (size_t)((s.K + s.group - 1) / s.group) * s.N, qn = (size_t)((s.K + 1) / 2) * s.N, wn = (size_t)s.K * s.N * dtype_size(w_dtype);
   if (overlap(q, qn, W, wn) || overlap(scales, sn * 2, W, wn) || overlap(zeros, sn, W, wn) || overlap(q, qn, scales, sn * 2) ||
       overlap(q, qn, zeros, sn) || overlap(scales, sn * 2, zeros, sn))
     return h->fail(ATLAS_ERR_INVALID_ARG, "W, q, scales and zeros must not overlap");
@@ -553,10 +647,10 @@ extern "C" int atlas_qlinear_pack(atlas_qlinear_handle* h, const uint8_t* q, con
     return h->fail(ATLAS_ERR_INVALID_ARG, "zeros goes with a configuration that has zero points, and only with it");
   if (!aligned16(packed)) return h->fail(ATLAS_ERR_INVALID_ARG, "packed must be aligned to 16 bytes");
   const Shape s = make_shape(h->cfg);
-  const size_t sn = (size_t)s.groups * s.N, pn = atlas_qlinear_packed_bytes(h);
+  const size_t sn = (size_t)((s.K + s.group - 1) / s.group) * s.N, pn = atlas_qlinear_packed_bytes(h);
   if (overlap(packed, pn, q, (size_t)((s.K + 1) / 2) * s.N) || overlap(packed, pn, scales, sn * 2) || overlap(packed, pn, zeros, sn))
     return h->fail(ATLAS_ERR_INVALID_ARG, "packed must not overlap q, scales or zeros");
-  const size_t threads = (size_t)s.tiles * s.steps * 128 + (size_t)s.groups * s.tiles * 8, blocks = (threads + 255) / 256;
+  const size_t blocks = (pn / 4 + 255) / 256;
   if (blocks > 0x7fffffffull) return h->fail(ATLAS_ERR_UNSUPPORTED, "K * N is too large");
   k_pack<<<(unsigned)blocks, 256, 0, (cudaStream_t)stream>>>(s, q, (const uint16_t*)scales, zeros, (uint8_t*)packed);
   const cudaError_t e = cudaGetLastError();
@@ -588,34 +682,39 @@ extern "C" int atlas_qlinear_forward(atlas_qlinear_handle* h, const atlas_qlinea
     return h->fail(ATLAS_ERR_INVALID_ARG, "y may be residual itself, else it must not overlap an input");
   cudaStream_t st = (cudaStream_t)stream;
   const Operand o = make_operand(c, io->M, aligned16(io->x));
-  if (const int rc = h->grow(o.bytes, st)) return rc;
+  int rc = h->need_status(st);
+  if (!rc) rc = h->grow(o.bytes, st);
+  if (rc) return rc;
   Call k;
   k.s = make_shape(c);
-  k.M = io->M, k.act = c.act, k.zeros = c.zeros, k.x_block = c.x_block, k.xblocks = (int)xblocks, k.per = 0;
+  k.M = io->M, k.act = c.act, k.out_bf16 = c.out_dtype == ATLAS_BF16, k.x_block = c.x_block, k.xblocks = (int)xblocks, k.turns = k.stages = 0;
   k.early = o.kind != X_ROWS;
-  k.plane = o.plane, k.x = (const uint4*)(o.kind == X_ROWS ? io->x : h->ws), k.x_scale = io->x_scale;
-  k.W = (const uint8_t*)io->W, k.bias = io->bias;
+  k.x = (const uint8_t*)(o.kind == X_ROWS ? io->x : h->ws), k.x_scale = io->x_scale;
+  k.W = (const uint8_t*)io->W, k.bias = io->bias, k.status = h->status;
   cudaError_t e = cudaSuccess;
   if (o.kind != X_ROWS) {
-    const size_t blocks = (o.plane + 255) / 256;
+    const size_t blocks = (o.pieces + 255) / 256;
     if (blocks > 0x7fffffffull) return h->fail(ATLAS_ERR_UNSUPPORTED, "M * K is too large");
     auto pass = [&](auto kern, auto* x) {
-      return tc::launch_overlapped(kern, dim3((unsigned)blocks), dim3(256), 0, st, x, (uint4*)h->ws, io->M, c.K, k.s.steps, o.plane);
+      return tc::launch_overlapped(kern, dim3((unsigned)blocks), dim3(256), 0, st, x, (uint4*)h->ws, io->M, c.K, k.s.chunks, o.tiles,
+                                   o.pieces);
     };
     e = o.kind == X_PLANES ? pass(k_fragments<float, X_PLANES>, (const float*)io->x)
         : o.kind == X_F16  ? pass(k_fragments<uint8_t, X_F16>, (const uint8_t*)io->x)
                            : pass(k_fragments<uint16_t, X_BF16>, (const uint16_t*)io->x);
   }
   if (e == cudaSuccess)
-    e = o.kind == X_PLANES ? launch_out<X_PLANES>(k, *io, c.out_dtype, st)
-        : o.kind == X_F16  ? launch_out<X_F16>(k, *io, c.out_dtype, st)
-        : o.kind == X_BF16 ? launch_out<X_BF16>(k, *io, c.out_dtype, st) : launch_out<X_ROWS>(k, *io, c.out_dtype, st);
+    e = o.kind == X_PLANES ? launch_rows<X_PLANES>(k, *io, o.tiles, st)
+        : o.kind == X_F16  ? launch_rows<X_F16>(k, *io, o.tiles, st)
+        : o.kind == X_BF16 ? launch_rows<X_BF16>(k, *io, o.tiles, st)
+                           : launch_rows<X_ROWS>(k, *io, o.tiles, st);
   if (e != cudaSuccess) return h->cuda_fail("4-bit matrix product launch", e);
   h->last_stream = st;
   h->launched = true;
   return ATLAS_OK;
 }
 
+extern "C" int atlas_qlinear_status(atlas_qlinear_handle* h) { return h ? h->read_status() : ATLAS_ERR_INVALID_ARG; }
 extern "C" const char* atlas_qlinear_last_error(const atlas_qlinear_handle* h) {
   return h ? h->err.c_str() : g_create_err.c_str();
 }

@@ -21,7 +21,7 @@ from . import (ATLAS_BF16, ATLAS_E4M3, ATLAS_F32, ATLAS_GATES_MEMORY, ATLAS_LAYO
                atlas_prologue_forward, atlas_prologue_io, atlas_prologue_last_gemm,
                atlas_prologue_status, atlas_qlinear_create, atlas_qlinear_destroy,
                atlas_qlinear_forward, atlas_qlinear_io, atlas_qlinear_pack, atlas_qlinear_packed_bytes,
-               atlas_qlinear_quantize, atlas_rms_create, atlas_rms_destroy, atlas_rms_forward,
+               atlas_qlinear_quantize, atlas_qlinear_status, atlas_rms_create, atlas_rms_destroy, atlas_rms_forward,
                atlas_rms_io, atlas_scan_create, atlas_scan_destroy, atlas_scan_forward, atlas_scan_io,
                atlas_scan_last_path, atlas_scan_status, current_stream, make_config, make_conv_config,
                make_decay_config, make_io, make_linear_config, make_norm_config, make_prologue_config,
@@ -541,6 +541,12 @@ class QuantLinear(_Layer):
                               _check("y", out["y"], self._out, (M, c.N), dev))
         atlas_qlinear_forward(self.h, io, _stream_of(dev, stream))
         return out
+
+    def status(self):
+        rc = atlas_qlinear_status(self.h)
+        if rc:
+            raise AtlasError(rc, "device status of the 4-bit matrix product")
+        return rc
 
 
 class SelectiveScan(_Layer):

@@ -170,8 +170,8 @@ def test_qlinear_validates_before_any_cuda_call(lib):  # noqa: F811
     _refuses(lib, "qlinear", h, io, BAD, "residual itself")
     io.residual, io.M = None, 4194241
     _refuses(lib, "qlinear", h, io, UNS, "4194240")
-    # three 16-column tiles, two steps of 64, four groups: 512 bytes a tile and step, 40 a tile and group
-    assert tln.atlas_qlinear_packed_bytes(h) == 3 * 2 * 512 + 4 * 3 * 40
+    # a block of 128 columns by 128 of K: codes, four groups of scales and zero points
+    assert tln.atlas_qlinear_packed_bytes(h) == 128 * 64 + 4 * 128 * 2 + 4 * 64
     assert tln.atlas_qlinear_workspace_bytes(h, 3) == 8 * 128 * 2 and tln.atlas_qlinear_workspace_bytes(h, 0) == 0
     Q, P = lib.atlas_qlinear_quantize, lib.atlas_qlinear_pack
     assert Q(None, 64, 0, 64, 64, 64, None) == BAD and P(None, 64, 64, 64, 64, None) == BAD
@@ -181,6 +181,7 @@ def test_qlinear_validates_before_any_cuda_call(lib):  # noqa: F811
     for args in ((64, 1 << 20, 1 << 21, None), (64, 1 << 20, None, 1 << 22), (64, 1 << 20, 1 << 21, (1 << 22) + 4),
                  (1 << 22, 1 << 20, 1 << 21, 1 << 22)):
         assert P(h, *args, None) == BAD and tln.atlas_qlinear_last_error(h)
+    assert tln.atlas_qlinear_status(h) == tln.ATLAS_OK and lib.atlas_qlinear_status(None) == BAD
     tln.atlas_qlinear_destroy(h)
     lib.atlas_qlinear_destroy(None)
 

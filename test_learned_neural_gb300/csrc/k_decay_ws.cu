@@ -48,7 +48,7 @@ struct Smem {
 };
 static_assert(kGateTokens == C && Smem<3, true>::end <= 227 * 1024, "a record for each chunk, a block on each SM");
 
-enum Bar { FULL = 0, SC = 3, P = 5, K = 7, DS, DSFREE, S, PV, Y, YFREE, OUT, NBARS };
+enum Bar { FULL = 0, SC = 3, P = 5, K = 7, DS, DSFREE, S, PV, Y, YFREE, OUT, NBARS = OUT + STAGES };
 
 // 8 of a token's keys (16-byte chunk j of row r), times w, in three terms
 __device__ __forceinline__ void scale_chunk(uint32_t src, uint32_t dst, int r, int j, float w, bool live) {
@@ -108,7 +108,7 @@ __global__ void __launch_bounds__(NTHR, 1)
   if (warp == 0) tc::tmem_alloc(tbase, 512);
   if (tid == 32) {
     for (int i = 0; i < NBARS; ++i) {
-      const bool four = i == K || i == DSFREE || i == S, eight = i == P || i == P + 1 || i == YFREE || i == OUT;
+      const bool four = i == K || i == DSFREE || i == S, eight = i == P || i == P + 1 || i == YFREE || i >= OUT;
       tc::mbar_init_only(bars + i, eight ? 8 : four ? 4 : 1);
     }
     tc::mbar_init_fence();
@@ -167,7 +167,7 @@ __global__ void __launch_bounds__(NTHR, 1)
       for (int c = 0; c < min(chunks, STAGES); ++c) load(c);
     __syncwarp();
     for (int c = 0; c < chunks && ok; ++c) {
-      if (!(ok = all_wait(OUT, c & 1))) break;
+      if (!(ok = all_wait(OUT + c % STAGES, (c / STAGES) & 1))) break;
       if (tc::elect()) {
         const uint32_t at = base + (c % STAGES) * STAGE;
         store_4d(&my, c0, t_lo + c * C, h, b, at);
@@ -332,7 +332,7 @@ __global__ void __launch_bounds__(NTHR, 1)
         }
       }
       tc::fence_smem_to_async();
-      arrive(OUT);
+      arrive(OUT + c % STAGES);
     };
     for (int c = 0; c < chunks; ++c) {
       const uint32_t sc = tSC + 128 * (c & 1) + lanes;

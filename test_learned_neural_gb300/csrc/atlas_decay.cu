@@ -27,7 +27,7 @@ constexpr int kSlice = 64;         // d_v columns per CTA
 // token: 81 us for 541 MB, 98 % of the copy bandwidth.  8 rows x 8 heads of 64 x 64:
 // 7 us, of which 5 are the host's call.
 template <typename TI, typename TO, int RPT, int V, bool GATED>
-__global__ void __launch_bounds__(256) k_decay_step(Geom g, Ptrs p, Gates gates) {
+__global__ void __launch_bounds__(256) k_decay_step(Geom g, Ptrs p) {
   constexpr int CL = kSlice / V;             // threads along the columns
   constexpr int RG = 256 / CL;               // row groups
   extern __shared__ float sm[];
@@ -42,6 +42,7 @@ __global__ void __launch_bounds__(256) k_decay_step(Geom g, Ptrs p, Gates gates)
   float gam = 1.f, step = 1.f, skip = 0.f;
   if constexpr (!GATED) gam = p.decay[h];
   else if (p.D) skip = p.D[h];
+  const decay::HeadGates head(GATED ? p.gates : Gates{nullptr, p.decay}, h);
   const size_t base = (size_t)unit * g.d_k * g.d_v + col;
   float S[RPT][V];
 #pragma unroll
@@ -59,7 +60,11 @@ __global__ void __launch_bounds__(256) k_decay_step(Geom g, Ptrs p, Gates gates)
   const TI* v = (const TI*)p.v + b * g.v_b + h * g.v_h;
   TO* y = (TO*)p.y + b * g.y_b + h * g.y_h;
   for (int t = 0; t < n; ++t) {
-    if constexpr (GATED) decay::gates_of(gates, b, h, t, gam, step);
+    if constexpr (GATED) {
+      decay::RawGates raw;
+      raw.load(p.gates, b, h, t);
+      raw.values(p.gates, head.bias, head.A, gam, step);
+    }
     for (int i = tid; i < g.d_k; i += 256) {
       qs[i] = to_f32(q[t * g.qk_t + i]);
       ks[i] = to_f32(k[t * g.qk_t + i]);
@@ -113,8 +118,9 @@ __global__ void __launch_bounds__(256) k_decay_step(Geom g, Ptrs p, Gates gates)
 // contribution to the next segment's start.  Bound by the latency of its fp32
 // loops where blocks are few (chunk_blocks has how many an SM holds): 3 rows x 6 heads of ragged
 // lengths to 1501, d 48: 41 us in three overlapped launches (states 15, scan 8, read-outs 32).
-// GATED: pw holds the tokens' products (decay_common.cuh) in place of powers; those
-// of a run's own tokens are formed by each row's threads from the decays.
+// GATED: pw holds the tokens' products (decay_common.cuh) in place of powers, which
+// a warp for each run forms; those of a run's own tokens are formed by each row's
+// threads from the decays.
 template <typename TI, typename TO, int C, bool READ, bool GATED>
 __global__ void __launch_bounds__(256, C == 64 ? 3 : 1) k_decay_chunk(Geom g, Ptrs p) {
   extern __shared__ float sm[];
@@ -149,9 +155,9 @@ __global__ void __launch_bounds__(256, C == 64 ? 3 : 1) k_decay_chunk(Geom g, Pt
   }
   if constexpr (!GATED)
     for (int i = tid; i <= C; i += 256) pw[i] = decay::power(l2g, i);
-  const float* records = nullptr;
-  if constexpr (GATED)
-    records = p.records + (size_t)unit * ((g.T + decay::kGateTokens - 1) / decay::kGateTokens) * decay::GATE_VALUES;
+  const decay::HeadGates head(GATED ? p.gates : Gates{nullptr, p.decay}, h);
+  decay::RawGates ahead;   // of this thread's token of the next chunk
+  if (GATED && tid < C && t_lo + tid < t_live) ahead.load(p.gates, b, h, t_lo + tid);
 
   // four values at a time where every row starts on their boundary
   const bool vec = g.d_k % 4 == 0 && g.d_v % 4 == 0 && (g.qk_t | g.v_t) % 4 == 0 &&
@@ -182,9 +188,12 @@ __global__ void __launch_bounds__(256, C == 64 ? 3 : 1) k_decay_chunk(Geom g, Pt
       }
       load4(v + (size_t)(t0 + r) * g.v_t, 4 * tx, cols, r < n, Vs + r * LDV);
     }
-    if constexpr (GATED) {
-      const float* rec = records + (size_t)(t0 / decay::kGateTokens) * decay::GATE_VALUES + t0 % decay::kGateTokens;
-      for (int i = tid; i < 4 * C; i += 256) pw[i] = rec[i / C * decay::kGateTokens + i % C];
+    if (GATED && tid < C) {   // whole warps
+      float d = 1.f, s = 0.f, L, R;
+      if (tid < n) ahead.values(p.gates, head.bias, head.A, d, s);
+      decay::run_products(d, s, L, R);
+      pw[tid] = d, pw[C + tid] = s, pw[2 * C + tid] = L, pw[3 * C + tid] = R;
+      if (t0 + C + tid < t_live) ahead.load(p.gates, b, h, t0 + C + tid);
     }
     __syncthreads();
     // GATED: the arrays, and the product of g over a run
@@ -364,45 +373,6 @@ __global__ void __launch_bounds__(256) k_decay_scan(Geom g, Ptrs p) {
   }
 }
 
-// The selective scan's records: a warp each, four runs of 32 tokens.
-__global__ void __launch_bounds__(256) k_scan_gates(Geom g, Gates gates, const int* lens, float* __restrict__ records,
-                                                    float* __restrict__ totals, size_t n) {
-  const size_t i = (size_t)blockIdx.x * 8 + threadIdx.x / 32;
-  const int lane = threadIdx.x % 32, chunks = (g.T + decay::kGateTokens - 1) / decay::kGateTokens;
-  tc::grid_dependency_wait();
-  tc::grid_dependents_launch();
-  if (i >= n) return;
-  const int unit = (int)(i / chunks), t0 = (int)(i % chunks) * decay::kGateTokens, b = unit / g.H, h = unit % g.H;
-  const int live = lens ? min(max(lens[b], 0), g.T) : g.T;
-  float* rec = records + i * decay::GATE_VALUES + lane;
-  float R[4], all[4];
-#pragma unroll
-  for (int r = 0; r < 4; ++r) {
-    const int t = t0 + r * decay::kRun + lane;
-    float d = 1.f, s = 0.f;
-    if (t < live) decay::gates_of(gates, b, h, t, d, s);
-    float L = d, behind = __shfl_down_sync(0xffffffffu, d, 1);
-    if (lane == 31) behind = 1.f;
-#pragma unroll
-    for (int e = 1; e < 32; e *= 2) {
-      const float x = __shfl_up_sync(0xffffffffu, L, e), y = __shfl_down_sync(0xffffffffu, behind, e);
-      if (lane >= e) L *= x;
-      if (lane + e < 32) behind *= y;
-    }
-    R[r] = s * behind;
-    all[r] = __shfl_sync(0xffffffffu, L, 31);
-    rec[decay::GATE_G + r * decay::kRun] = d;
-    rec[decay::GATE_S + r * decay::kRun] = s;
-    rec[decay::GATE_L + r * decay::kRun] = L;
-    rec[decay::GATE_R + r * decay::kRun] = R[r];
-  }
-  rec[decay::GATE_K] = R[0] * (all[1] * all[2] * all[3]);
-  rec[decay::GATE_K + 32] = R[1] * (all[2] * all[3]);
-  rec[decay::GATE_K + 64] = R[2] * all[3];
-  rec[decay::GATE_K + 96] = R[3];
-  if (lane == 0) totals[i] = all[0] * all[1] * all[2] * all[3];
-}
-
 // rows of `from` values, `heads` to a token and `ld` from token to token -> dense
 // rows of `to` values, zero where there are more
 template <typename T>
@@ -470,10 +440,8 @@ struct Plan {
   int path, C, slices, nseg, seg;
   bool pad;
   size_t seg_bytes, q_bytes, v_bytes, y_bytes;   // workspace: segment starts, then padded q, k, v, y
-  size_t record_bytes, total_bytes, seg_total_bytes;   // then a selective scan's records, their and the segments' products
-  size_t bytes() const {
-    return seg_bytes + 2 * q_bytes + v_bytes + y_bytes + record_bytes + total_bytes + seg_total_bytes;
-  }
+  size_t seg_total_bytes;   // then a selective scan's products of g over the segments
+  size_t bytes() const { return seg_bytes + 2 * q_bytes + v_bytes + y_bytes + seg_total_bytes; }
 };
 size_t round_256(size_t n) { return (n + 255) / 256 * 256; }
 
@@ -519,7 +487,7 @@ int most_step_tokens(const atlas_decay_config& c, long long ctas) {
 // bf16 calls with d_k <= 128 take the tensor-core chunks.  Their copies want rows
 // of whole 16-byte groups: other widths (or addresses) go through padded copies
 // of q, k, v and y in the workspace.  `aligned`: the addresses do not ask for it.
-Plan make_plan(const atlas_decay_config& c, int B, int T, bool aligned, bool gated) {
+Plan make_plan(const atlas_decay_config& c, int B, int T, bool aligned, bool gated, bool ragged) {
   Plan pl{};
   pl.slices = (c.d_v + kSlice - 1) / kSlice;
   pl.nseg = 1;
@@ -534,8 +502,10 @@ Plan make_plan(const atlas_decay_config& c, int B, int T, bool aligned, bool gat
   pl.path = tc ? 2 : 1;
   pl.C = tc ? decay::kTcChunk : chunk_tokens(c.d_k);
   // CTAs that run at once; a fp32 chunk takes so long that starts hardly count
-  const long long slots = (tc ? 1 : chunk_blocks(c.d_k, true, gated)) * sm_count(),
-                  state_slots = (tc ? 1 : chunk_blocks(c.d_k, false, gated)) * sm_count();
+  // (twice as many in a selective scan's ragged batch: half of the segments lie past their rows' lengths,
+  // as a rule, and end at once; 2 x 16 rows and heads of 0 and 8192 tokens, 128 x 64: 4 segments 143 us, 8 108)
+  const long long more = gated && ragged ? 2 : 1, slots = more * (tc ? 1 : chunk_blocks(c.d_k, true, gated)) * sm_count(),
+                  state_slots = more * (tc ? 1 : chunk_blocks(c.d_k, false, gated)) * sm_count();
   const long long chunks = (T + pl.C - 1) / pl.C;
   const long long n = best_segments((long long)B * c.H * pl.slices, chunks, slots, state_slots, tc ? 2 : 0.5);
   pl.seg = (int)((chunks + n - 1) / n * pl.C);
@@ -547,12 +517,7 @@ Plan make_plan(const atlas_decay_config& c, int B, int T, bool aligned, bool gat
     pl.v_bytes = round_256(rows * c.H * ((c.d_v + 7) / 8 * 8) * 2);
     pl.y_bytes = round_256(rows * c.H * ((c.d_v + 7) / 8 * 8) * dtype_size(c.y_dtype));
   }
-  if (gated) {
-    const size_t units = (size_t)B * c.H, records = units * ((T + decay::kGateTokens - 1) / decay::kGateTokens);
-    pl.record_bytes = records * decay::GATE_VALUES * sizeof(float);
-    pl.total_bytes = round_256(records * sizeof(float));
-    pl.seg_total_bytes = pl.nseg > 1 ? round_256(units * pl.nseg * sizeof(float)) : 0;
-  }
+  if (gated && pl.nseg > 1) pl.seg_total_bytes = round_256((size_t)B * c.H * pl.nseg * sizeof(float));
   return pl;
 }
 
@@ -601,19 +566,19 @@ extern "C" size_t atlas_decay_workspace_bytes(const atlas_decay_handle* h, int B
 size_t decay::workspace_bytes(const atlas_decay_config& c, int B, int T, bool gated) {
   if (B < 1 || T < 1 || T > kMostTokens) return 0;
   // the most it can be: tensors at addresses that ask for padded copies
-  return make_plan(c, B, T, false, gated).bytes();
+  return std::max(make_plan(c, B, T, false, gated, false).bytes(), make_plan(c, B, T, false, gated, true).bytes());
 }
 
 namespace {
 
 template <typename TI, typename TO, bool GATED>
-cudaError_t launch_step(const Geom& g, const Ptrs& p, const Gates& gates, cudaStream_t st) {
+cudaError_t launch_step(const Geom& g, const Ptrs& p, cudaStream_t st) {
   // four columns per thread where the state rows are whole 16-byte groups
   const bool v4 = g.d_v % 4 == 0 && aligned16(p.S0) && aligned16(p.S_out);
   const int rows = (g.d_k + (v4 ? 15 : 3)) / (v4 ? 16 : 4);
   const unsigned grid = (unsigned)((size_t)g.B * g.H * g.slices);
   const size_t smem = step_smem(g, v4 ? 4 : 1);
-  auto go = [&](auto kern) { kern<<<grid, 256, smem, st>>>(g, p, gates); };
+  auto go = [&](auto kern) { kern<<<grid, 256, smem, st>>>(g, p); };
   if (v4) {
     if (rows <= 2) go(k_decay_step<TI, TO, 2, 4, GATED>);
     else if (rows <= 4) go(k_decay_step<TI, TO, 4, 4, GATED>);
@@ -637,7 +602,7 @@ cudaError_t launch_big(K kern, dim3 grid, size_t smem, const Geom& g, const Ptrs
 }  // namespace
 
 cudaError_t decay::scan_launch(const Geom& g, const Ptrs& p, cudaStream_t st) {
-  return tc::launch_overlapped(p.records ? k_decay_scan<true> : k_decay_scan<false>,
+  return tc::launch_overlapped(p.gated ? k_decay_scan<true> : k_decay_scan<false>,
                                dim3((unsigned)(((size_t)g.d_k * g.d_v + 255) / 256), (unsigned)(g.B * g.H)), dim3(256), 0, st, g,
                                p);
 }
@@ -659,16 +624,15 @@ cudaError_t launch_chunks(const Geom& g, const Ptrs& p, cudaStream_t st) {
 }
 
 template <typename TI, typename TO, bool GATED>
-cudaError_t launch(const Plan& pl, const Geom& g, const Ptrs& p, const Gates& gates, cudaStream_t st) {
-  if (pl.path == 0) return launch_step<TI, TO, GATED>(g, p, gates, st);
+cudaError_t launch(const Plan& pl, const Geom& g, const Ptrs& p, cudaStream_t st) {
+  if (pl.path == 0) return launch_step<TI, TO, GATED>(g, p, st);
   return pl.C == 64 ? launch_chunks<TI, TO, 64, GATED>(g, p, st) : launch_chunks<TI, TO, 32, GATED>(g, p, st);
 }
 template <bool GATED>
-cudaError_t launch_types(const Plan& pl, const atlas_decay_config& c, const Geom& g, const Ptrs& p, const Gates& gates,
-                         cudaStream_t st) {
+cudaError_t launch_types(const Plan& pl, const atlas_decay_config& c, const Geom& g, const Ptrs& p, cudaStream_t st) {
   const bool ib = c.qkv_dtype == ATLAS_BF16, ob = c.y_dtype == ATLAS_BF16;
-  return ib ? (ob ? launch<bf16, bf16, GATED>(pl, g, p, gates, st) : launch<bf16, float, GATED>(pl, g, p, gates, st))
-            : (ob ? launch<float, bf16, GATED>(pl, g, p, gates, st) : launch<float, float, GATED>(pl, g, p, gates, st));
+  return ib ? (ob ? launch<bf16, bf16, GATED>(pl, g, p, st) : launch<bf16, float, GATED>(pl, g, p, st))
+            : (ob ? launch<float, bf16, GATED>(pl, g, p, st) : launch<float, float, GATED>(pl, g, p, st));
 }
 
 }  // namespace
@@ -697,7 +661,7 @@ int decay::run(HandleBase* h, const atlas_decay_config& c, const atlas_decay_io&
   // rows of wider ones: copies of whole 16-byte groups too
   const bool strides_ok = !x || (x->ld_qk % 8 == 0 && x->ld_v % 8 == 0);
   const Plan pl = make_plan(c, io.B, io.T, strides_ok && aligned16(io.q) && aligned16(io.k) && aligned16(io.v) && aligned16(io.y),
-                            x != nullptr);
+                            x != nullptr, io.lens != nullptr);
   int rc = pl.path == 2 ? h->need_status(st) : ATLAS_OK;
   if (!rc) rc = h->grow(pl.bytes(), st);
   if (rc) return rc;
@@ -722,24 +686,14 @@ int decay::run(HandleBase* h, const atlas_decay_config& c, const atlas_decay_io&
     g.qk_t = ld_qk, g.qk_b = T * ld_qk;
     g.v_t = ld_v, g.v_b = T * ld_v;
   }
-  char* const after = (char*)h->ws + pl.seg_bytes + 2 * pl.q_bytes + pl.v_bytes + pl.y_bytes;
   Ptrs p{};
   p.q = io.q, p.k = io.k, p.v = io.v, p.decay = io.decay, p.lens = io.lens, p.S0 = io.S0, p.y = io.y, p.S_out = io.S_out;
   p.seg = (float*)h->ws;
-  Gates gates{};
   if (x) {
-    gates = x->gates;
+    p.gated = true;
+    p.gates = x->gates;
     p.D = x->D;
-    if (pl.path != 0) {
-      float *records = (float*)after, *totals = (float*)(after + pl.record_bytes);
-      p.records = records, p.totals = totals;
-      p.seg_total = (float*)(after + pl.record_bytes + pl.total_bytes);
-      const size_t n = pl.record_bytes / (decay::GATE_VALUES * sizeof(float)), blocks = (n + 7) / 8;
-      if (blocks > 0x7fffffffull) return h->fail(ATLAS_ERR_UNSUPPORTED, "B * H * T is too large for one call");
-      const cudaError_t e = tc::launch_overlapped(k_scan_gates, dim3((unsigned)blocks), dim3(256), 0, st, g, gates, io.lens, records,
-                                                  totals, n);
-      if (e != cudaSuccess) return h->cuda_fail(what, e);
-    }
+    p.seg_total = (float*)((char*)h->ws + pl.seg_bytes + 2 * pl.q_bytes + pl.v_bytes + pl.y_bytes);
   }
   if (pl.pad) {
     char* at = (char*)h->ws + pl.seg_bytes;
@@ -757,7 +711,7 @@ int decay::run(HandleBase* h, const atlas_decay_config& c, const atlas_decay_io&
   }
   const bool ob = c.y_dtype == ATLAS_BF16;
   cudaError_t e = pl.path == 2 ? decay::tc_launch(g, p, ob, h->status, st)
-                               : x ? launch_types<true>(pl, c, g, p, gates, st) : launch_types<false>(pl, c, g, p, gates, st);
+                               : x ? launch_types<true>(pl, c, g, p, st) : launch_types<false>(pl, c, g, p, st);
   if (e == cudaSuccess && pl.pad)
     e = ob ? launch_rows<bf16>(p.y, io.y, rows * c.H, g.dv_row, c.d_v, st)
            : launch_rows<float>(p.y, io.y, rows * c.H, g.dv_row, c.d_v, st);

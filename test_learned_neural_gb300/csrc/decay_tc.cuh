@@ -12,6 +12,9 @@ cudaError_t tc_launch(const Geom& g, const Ptrs& p, bool y_bf16, int* status, cu
 // the same for d_k <= 64 (k_decay_ws.cu)
 cudaError_t ws_launch(const Geom& g, const Ptrs& p, bool y_bf16, int* status, cudaStream_t st);
 
+// a selective scan with 64 < d_k <= 128 (k_scan_wide.cu)
+cudaError_t wide_launch(const Geom& g, const Ptrs& p, bool y_bf16, int* status, cudaStream_t st);
+
 // segment starts from the segments' own contributions (atlas_decay.cu)
 cudaError_t scan_launch(const Geom& g, const Ptrs& p, cudaStream_t st);
 

@@ -88,24 +88,23 @@ struct StatePart {
   }
 };
 
-template <int NT, bool GATED>
+template <int NT>
 struct Smem {   // byte offsets from a 1024-byte aligned base
   static constexpr int q = 0, k = q + KB * TILE, v = k + KB * TILE, k1 = v + TILE, k2 = k1 + KB * TILE,
                        s = k2 + KB * TILE, NS = NT == 2 ? 2 : 3, s_tile = KB * 64 * 128,
                        y = NT == 2 ? s + NS * s_tile : q,   // read-outs: a tile of their own, or q's once it is read
-                       pw = NT == 2 ? y + TILE : s + NS * s_tile, bars = pw + (GATED ? GATE_VALUES : C + 4) * 4,
-                       end = bars + 64;
+                       pw = NT == 2 ? y + TILE : s + NS * s_tile, bars = pw + (C + 4) * 4, end = bars + 64;
 };
 
-template <int NT, typename TO, bool GATED>
+template <int NT, typename TO>
 __global__ void __launch_bounds__(NTHR, 1)
     k_decay_tc(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap my, Geom g, Ptrs p,
                int* status) {
-  using L = Smem<NT, GATED>;
+  using L = Smem<NT>;
   extern __shared__ __align__(1024) uint8_t sm[];
   const uint32_t base = tc::smem_u32(sm);
-  float* pw = reinterpret_cast<float*>(sm + L::pw);   // g^0 .. g^128; GATED: the chunk's record
+  float* pw = reinterpret_cast<float*>(sm + L::pw);   // g^0 .. g^128
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + L::bars);
   // full_q, full_kv, scores, intra, state, tmem base, failed
   uint32_t* tbase = reinterpret_cast<uint32_t*>(bars + 6);
@@ -153,17 +152,8 @@ __global__ void __launch_bounds__(NTHR, 1)
     }
     __syncwarp();
   }
-  if constexpr (!GATED) {
-    const float l2g = log2f(p.decay[h]);
-    for (int i = tid; i <= C; i += NTHR) pw[i] = decay::power(l2g, i);
-  }
-  // GATED: a record comes through registers, a chunk ahead
-  const float4* records =
-      reinterpret_cast<const float4*>(p.records) + (size_t)unit * ((g.T + C - 1) / C) * (GATE_VALUES / 4) + tid;
-  float4 ahead;
-  if (GATED && tid < GATE_VALUES / 4 && t_lo < t_live) ahead = records[(size_t)(t_lo / C) * (GATE_VALUES / 4)];
-  auto run_of = [&](int r) { return pw[GATE_L + kRun * r + kRun - 1]; };   // product of g over run r
-  const float skip = GATED && p.D ? p.D[h] : 0.f;
+  const float l2g = log2f(p.decay[h]);
+  for (int i = tid; i <= C; i += NTHR) pw[i] = decay::power(l2g, i);
 
   // the state, fp32, and its bf16 terms as the operand of Q S: rows d_k, 64
   // values of d_v
@@ -195,13 +185,6 @@ __global__ void __launch_bounds__(NTHR, 1)
   uint32_t ph = 0;
   for (int t0 = t_lo; ok && t0 < t_live; t0 += C, ph ^= 1) {
     const int n = min(C, t_live - t0);
-    if constexpr (GATED) {
-      if (tid < GATE_VALUES / 4) {   // (the last chunk's readers are behind its closing barrier)
-        reinterpret_cast<float4*>(pw)[tid] = ahead;
-        if (t0 + C < t_live) ahead = records[(size_t)(t0 / C + 1) * (GATE_VALUES / 4)];
-      }
-      __syncthreads();
-    }
     ok &= tc::wait(bq, ph);
     ok &= tc::wait(bkv, ph);
     auto mma_inter = [&]() {   // Q S, the smallest terms first
@@ -230,9 +213,7 @@ __global__ void __launch_bounds__(NTHR, 1)
     uint32_t k0[KB][16];
     {
       const int r = tid & (C - 1);
-      float w;
-      if constexpr (GATED) w = pw[GATE_K + r];   // (0 past the row's length)
-      else w = r < n ? pw[n - 1 - r] : 0.f;
+      const float w = r < n ? pw[n - 1 - r] : 0.f;
 #pragma unroll
       for (int i = 0; i < KB; ++i)
         scale_keys(base + L::k + i * TILE, base + L::k1 + i * TILE, base + L::k2 + i * TILE, w, r < n, tid, k0[i]);
@@ -256,29 +237,7 @@ __global__ void __launch_bounds__(NTHR, 1)
         float v[32];
         tc::tmem_ld32(tm + lanes + 32 * blk, v);
         tc::tmem_ld_wait32(v);
-        if (GATED && blk < wq) {
-          float f = pw[GATE_L + row];   // the runs between, times what the record has to the run's end
-          for (int r = blk + 1; r < wq; ++r) f *= run_of(r);
-          const float* behind = pw + GATE_R + 32 * blk;
-#pragma unroll
-          for (int i = 0; i < 16; ++i) split2<NT>(v[2 * i] * (f * behind[2 * i]), v[2 * i + 1] * (f * behind[2 * i + 1]), w[i]);
-        } else if (GATED) {
-          // a row's own run, from the row backwards: s_j times the decays between
-          const float *gr = pw + GATE_G + 32 * blk, *sr = pw + GATE_S + 32 * blk;
-          float own = 0.f;
-#pragma unroll
-          for (int i = 15; i >= 0; --i) {
-            float x[2];
-#pragma unroll
-            for (int e = 1; e >= 0; --e) {
-              const int c = 2 * i + e;
-              if (c == lane) own = 1.f;
-              x[e] = c <= lane ? v[c] * (own * sr[c]) : 0.f;
-              if (c <= lane) own *= gr[c];
-            }
-            split2<NT>(x[0], x[1], w[i]);
-          }
-        } else if (blk < wq) {
+        if (blk < wq) {
           const float f = pw[row - 32 * blk - 31];   // times g^{31 - c}
 #pragma unroll
           for (int i = 0; i < 16; ++i)
@@ -351,26 +310,9 @@ __global__ void __launch_bounds__(NTHR, 1)
       tc::tmem_ld32(tm + 192 + lanes + 32 * wh, ya);
       tc::tmem_ld_wait32(yi);
       tc::tmem_ld_wait32(ya);
-      float f = g.scale;
-      if constexpr (GATED) {
-        f *= pw[GATE_L + row];
-        for (int r = 0; r < wq; ++r) f *= run_of(r);
-      } else {
-        f *= pw[row + 1];
-      }
+      const float f = pw[row + 1] * g.scale;
 #pragma unroll
       for (int i = 0; i < 32; ++i) ya[i] = row < n ? fmaf(f, yi[i], g.scale * ya[i]) : 0.f;
-      if (GATED && p.D && row < n) {   // D v, from the chunk's own tile (its next load waits for the state's product)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          uint32_t x[4];
-          lds128(base + L::v + swz(row, 4 * wh + j), x);
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            unpair(fma_pair(widen(x[i]), pair(skip, skip), pair(ya[8 * j + 2 * i], ya[8 * j + 2 * i + 1])), ya[8 * j + 2 * i],
-                   ya[8 * j + 2 * i + 1]);
-        }
-      }
       if constexpr (sizeof(TO) == 2) {
         if (lane == 0 && warp == 0) tc::bulk_wait_read<0>();   // the last chunk's store has been read
         __syncthreads();
@@ -418,7 +360,7 @@ __global__ void __launch_bounds__(NTHR, 1)
     {
       float d[StatePart::N];
       part.load(tm, warp, d);
-      const float f = GATED ? run_of(0) * run_of(1) * (run_of(2) * run_of(3)) : pw[n];
+      const float f = pw[n];
 #pragma unroll
       for (int i = 0; i < StatePart::N; ++i) S[i] = fmaf(f, S[i], d[i]);
     }
@@ -455,9 +397,6 @@ struct SmemState {
   static constexpr int kv_bytes = (KB + 1) * TILE, t0 = 2 * kv_bytes, bars = t0 + 3 * KB * TILE, end = bars + 64;
 };
 
-// GATED: the chunks in reverse, so that the product of the decays behind a chunk
-// comes by multiplying the chunks' own.
-template <bool GATED>
 __global__ void __launch_bounds__(NTHR, 1)
     k_decay_tc_state(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv, Geom g, Ptrs p,
                      int* status) {
@@ -489,12 +428,10 @@ __global__ void __launch_bounds__(NTHR, 1)
   const int live = decay::live_tokens(g, p, b);
   const int t_lo = s * g.seg, t_hi = min(g.T, t_lo + g.seg), t_live = min(t_hi, max(live, t_lo));
   const int c0 = sl * SL, cols = min(SL, g.d_v - c0), chunks = (t_live - t_lo + C - 1) / C;
-  // the token that the c-th chunk to be worked on begins with
-  auto first = [&](int c) { return t_lo + (GATED ? chunks - 1 - c : c) * C; };
   bool ok = *failed == 0;
   auto load = [&](int c) {
     const uint32_t at = base + (c & 1) * L::kv_bytes, bar = bfull + 8 * (c & 1);
-    const int t0 = first(c);
+    const int t0 = t_lo + c * C;
     tc::expect_tx(bar, (KB + 1) * TILE);
     for (int i = 0; i < KB; ++i) load_4d(at + i * TILE, &mk, 64 * i, t0, hq, b, bar);
     load_4d(at + KB * TILE, &mv, c0, t0, h, b, bar);
@@ -504,22 +441,14 @@ __global__ void __launch_bounds__(NTHR, 1)
       for (int c = 0; c < min(2, chunks); ++c) load(c);
     __syncwarp();
   }
-  const float l2g = GATED ? 0.f : log2f(p.decay[h]);
-  const size_t unit_chunk = (size_t)unit * ((g.T + C - 1) / C);
-  float behind = 1.f;   // GATED: the product of g over the chunks that come behind
+  const float l2g = log2f(p.decay[h]);
   for (int c = 0; ok && c < chunks; ++c) {
-    const int t0 = first(c), n = min(C, t_live - t0);
+    const int t0 = t_lo + c * C, n = min(C, t_live - t0);
     const uint32_t kt = base + (c & 1) * L::kv_bytes, vt = kt + KB * TILE;
     ok &= tc::wait(bfull + 8 * (c & 1), (c >> 1) & 1);
     if (c > 0) ok &= tc::wait(bdone, (c - 1) & 1);   // the last product has read the terms
     const int r = tid & (C - 1);
-    float w;
-    if constexpr (GATED) {
-      w = p.records[(unit_chunk + t0 / C) * GATE_VALUES + GATE_K + r] * behind;   // (0 past the row's length)
-      behind *= p.totals[unit_chunk + t0 / C];
-    } else {
-      w = r < n ? decay::power(l2g, t_live - 1 - t0 - r) : 0.f;
-    }
+    const float w = r < n ? decay::power(l2g, t_live - 1 - t0 - r) : 0.f;
 #pragma unroll
     for (int i = 0; i < KB; ++i) {
       uint32_t k0[16];
@@ -556,7 +485,6 @@ __global__ void __launch_bounds__(NTHR, 1)
 #pragma unroll
       for (int i = 0; i < StatePart::N; ++i) d[i] = 0.f;
     }
-    if (GATED && sl == 0 && tid == 0) p.seg_total[(size_t)unit * g.nseg + s] = behind;
     float* dst = p.seg + ((size_t)unit * g.nseg + s + 1) * ((size_t)g.d_k * g.d_v);
 #pragma unroll
     for (int i = 0; i < StatePart::N; ++i)
@@ -570,29 +498,22 @@ __global__ void __launch_bounds__(NTHR, 1)
   if (warp == 0) tc::tmem_dealloc(tm, 64);
 }
 
-template <int NT, typename TO, bool GATED>
+template <int NT, typename TO>
 cudaError_t launch_out(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const CUtensorMap& my,
                        const Geom& g, const Ptrs& p, int* status, cudaStream_t st) {
-  auto kern = k_decay_tc<NT, TO, GATED>;
-  constexpr int smem = Smem<NT, GATED>::end;
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  auto kern = k_decay_tc<NT, TO>;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<NT>::end);
   if (e != cudaSuccess) return e;
-  return tc::launch_overlapped(kern, dim3(g.nseg, g.slices, g.B * g.H), dim3(NTHR), smem, st, mq, mk, mv, my, g, p, status);
+  return tc::launch_overlapped(kern, dim3(g.nseg, g.slices, g.B * g.H), dim3(NTHR), Smem<NT>::end, st, mq, mk, mv,
+                               my, g, p, status);
 }
-template <bool GATED>
-cudaError_t launch_all(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const CUtensorMap& my,
-                       const Geom& g, const Ptrs& p, bool y_bf16, int* status, cudaStream_t st) {
-  if (g.nseg > 1) {
-    auto kern = k_decay_tc_state<GATED>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SmemState::end);
-    if (e != cudaSuccess) return e;
-    e = tc::launch_overlapped(kern, dim3(g.nseg - 1, g.slices, g.B * g.H), dim3(NTHR), SmemState::end, st, mk, mv, g, p, status);
-    if (e != cudaSuccess) return e;
-    e = scan_launch(g, p, st);
-    if (e != cudaSuccess) return e;
-  }
-  return y_bf16 ? launch_out<2, bf16, GATED>(mq, mk, mv, my, g, p, status, st)
-                : launch_out<3, float, GATED>(mq, mk, mv, my, g, p, status, st);
+cudaError_t launch_state(const CUtensorMap& mk, const CUtensorMap& mv, const Geom& g, const Ptrs& p, int* status,
+                         cudaStream_t st) {
+  auto kern = k_decay_tc_state;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SmemState::end);
+  if (e != cudaSuccess) return e;
+  return tc::launch_overlapped(kern, dim3(g.nseg - 1, g.slices, g.B * g.H), dim3(NTHR), SmemState::end, st, mk, mv,
+                               g, p, status);
 }
 
 }  // namespace
@@ -601,6 +522,7 @@ namespace decay {
 
 cudaError_t tc_launch(const Geom& g, const Ptrs& p, bool y_bf16, int* status, cudaStream_t st) {
   if (g.d_k <= 64) return ws_launch(g, p, y_bf16, status, st);
+  if (p.gated) return wide_launch(g, p, y_bf16, status, st);
   CUtensorMap mq, mk, mv, my;
   const int hq = g.H / g.share;
   if (!map_4d(&mq, p.q, true, g.dk_row, g.T, hq, g.B, g.qk_t, g.qk_h, g.qk_b) ||
@@ -608,8 +530,14 @@ cudaError_t tc_launch(const Geom& g, const Ptrs& p, bool y_bf16, int* status, cu
       !map_4d(&mv, p.v, true, g.dv_row, g.T, g.H, g.B, g.v_t, g.v_h, g.v_b) ||
       !map_4d(&my, p.y, y_bf16, g.dv_row, g.T, g.H, g.B, g.y_t, g.y_h, g.y_b))
     return cudaErrorInvalidValue;
-  return p.records ? launch_all<true>(mq, mk, mv, my, g, p, y_bf16, status, st)
-                   : launch_all<false>(mq, mk, mv, my, g, p, y_bf16, status, st);
+  if (g.nseg > 1) {
+    cudaError_t e = launch_state(mk, mv, g, p, status, st);
+    if (e != cudaSuccess) return e;
+    e = scan_launch(g, p, st);
+    if (e != cudaSuccess) return e;
+  }
+  return y_bf16 ? launch_out<2, bf16>(mq, mk, mv, my, g, p, status, st)
+                : launch_out<3, float>(mq, mk, mv, my, g, p, status, st);
 }
 
 }  // namespace decay

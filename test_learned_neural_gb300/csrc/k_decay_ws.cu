@@ -31,6 +31,7 @@ using layer::bf16;
 
 namespace {
 
+// GATED: a warp more, for the chunks' records
 constexpr int NTHR = 18 * 32, STAGES = 3, STAGE = 3 * TILE;
 // Most segments whose starts the read-out pass adds up itself.  It saves a launch,
 // but a block waits for the sums of every segment before its own, one after the
@@ -40,6 +41,7 @@ constexpr int NTHR = 18 * 32, STAGES = 3, STAGE = 3 * TILE;
 constexpr int kInlineScan = 4;
 
 constexpr int RECORD = GATE_VALUES * 4;   // bytes of a chunk's gates (GATED), a ring of stages too
+constexpr int threads_of(bool gated) { return NTHR + (gated ? 32 : 0); }
 template <int NT, bool GATED>
 struct Smem {
   static constexpr int k0 = STAGES * STAGE, s = k0 + 3 * TILE, NS = NT == 2 ? 2 : 3, s_tile = 64 * 128,
@@ -88,7 +90,7 @@ __device__ __forceinline__ void zero_row(uint32_t tile, int r) {
 }
 
 template <int NT, typename TO, bool GATED>
-__global__ void __launch_bounds__(NTHR, 1)
+__global__ void __launch_bounds__(threads_of(GATED), 1)
     k_decay_ws(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap my, Geom g, Ptrs p,
                int inline_scan, int* status) {
@@ -109,7 +111,7 @@ __global__ void __launch_bounds__(NTHR, 1)
   if (tid == 32) {
     for (int i = 0; i < NBARS; ++i) {
       const bool four = i == K || i == DSFREE || i == S, eight = i == P || i == P + 1 || i == YFREE || i >= OUT;
-      tc::mbar_init_only(bars + i, eight ? 8 : four ? 4 : 1);
+      tc::mbar_init_only(bars + i, eight ? 8 : four ? 4 : GATED && i < SC ? 2 : 1);   // GATED: copies and record
     }
     tc::mbar_init_fence();
     *failed = (base & 1023u) ? 1 : 0;   // the swizzled tiles need it; never seen otherwise
@@ -155,10 +157,7 @@ __global__ void __launch_bounds__(NTHR, 1)
     auto load = [&](int c) {
       const uint32_t at = base + (c % STAGES) * STAGE, full = bar(FULL + c % STAGES);
       const int t0 = t_lo + c * C;
-      tc::expect_tx(full, STAGE + (GATED ? RECORD : 0));
-      if constexpr (GATED)
-        load_bytes(base + L::pw + (c % STAGES) * RECORD,
-                   p.records + ((size_t)unit * ((g.T + C - 1) / C) + t0 / C) * GATE_VALUES, RECORD, full);
+      tc::expect_tx(full, STAGE);
       load_4d(at, &mq, 0, t0, hq, b, full);
       load_4d(at + TILE, &mk, 0, t0, hq, b, full);
       load_4d(at + 2 * TILE, &mv, c0, t0, h, b, full);
@@ -250,6 +249,18 @@ __global__ void __launch_bounds__(NTHR, 1)
         tc::mma_commit(bars + Y);
       }
       __syncwarp();
+    }
+  } else if (GATED && group == 4) {
+    // records, the gates of the next one in flight
+    const HeadGates head(p.gates, h);
+    RecordMaker next;
+    if (chunks > 0) next.load(p.gates, b, h, t_lo, t_live);
+    for (int c = 0; c < chunks; ++c) {
+      const RecordMaker now = next;
+      if (c + 1 < chunks) next.load(p.gates, b, h, t_lo + (c + 1) * C, t_live);
+      if (c >= STAGES && !(ok = all_wait(OUT + c % STAGES, (c / STAGES - 1) & 1))) break;
+      now.write<true>(p.gates, head, t_lo + c * C, t_live, 1.f, record(c));
+      arrive(FULL + c % STAGES);
     }
   } else if (group == 0) {
     // keys: one token per thread
@@ -529,20 +540,22 @@ __global__ void __launch_bounds__(NTHR, 1)
 // that end, the product accumulated in TMEM over the whole segment.  Two groups
 // of four key warps take chunks in turn, each with its own terms.
 struct SmemState {
-  static constexpr int stage = 2 * TILE, k0 = STAGES * stage, bars = k0 + 6 * TILE, end = bars + 16 * 8;
+  static constexpr int stage = 2 * TILE, k0 = STAGES * stage, kw = k0 + 6 * TILE, bars = kw + STAGES * C * 4, end = bars + 16 * 8;
 };
 constexpr int NTHR_STATE = 10 * 32;
+constexpr int state_threads_of(bool gated) { return NTHR_STATE + (gated ? 32 : 0); }
 enum BarState { SFULL = 0, SEMPTY = 3, SK = 6, SFREE = 8, NSBARS = 10 };
 
 // GATED: the chunks in reverse, so that the product of the decays behind a chunk
 // comes by multiplying the chunks' own.
 template <bool GATED>
-__global__ void __launch_bounds__(NTHR_STATE, 1)
+__global__ void __launch_bounds__(state_threads_of(GATED), 1)
     k_decay_ws_state(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv, Geom g, Ptrs p,
                      int* status) {
   using L = SmemState;
   extern __shared__ __align__(1024) uint8_t sm[];
   const uint32_t base = tc::smem_u32(sm);
+  float* kw = reinterpret_cast<float*>(sm + L::kw);   // GATED: the stages' weights
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + L::bars);
   uint32_t* tbase = reinterpret_cast<uint32_t*>(bars + NSBARS);
   int* failed = reinterpret_cast<int*>(bars + NSBARS + 1);
@@ -553,7 +566,8 @@ __global__ void __launch_bounds__(NTHR_STATE, 1)
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, quarter = warp & 3, group = (warp - 2) >> 2;
   if (warp == 0) tc::tmem_alloc(tbase, 256);
   if (tid == 32) {
-    for (int i = 0; i < NSBARS; ++i) tc::mbar_init_only(bars + i, i == SK || i == SK + 1 ? 4 : 1);
+    for (int i = 0; i < NSBARS; ++i)
+      tc::mbar_init_only(bars + i, i == SK || i == SK + 1 ? 4 : GATED && i < SEMPTY ? 2 : 1);   // GATED: copies and weights
     tc::mbar_init_fence();
     *failed = (base & 1023u) ? 1 : 0;
     tc::prefetch_map(&mk);
@@ -597,6 +611,21 @@ __global__ void __launch_bounds__(NTHR_STATE, 1)
       }
       __syncwarp();
     }
+  } else if (GATED && group == 2) {
+    // the tokens' weights to the segment's end, the gates of the next chunk in flight
+    const HeadGates head(p.gates, h);
+    RecordMaker next;
+    float behind = 1.f;   // the product of g over the chunks that come behind
+    if (chunks > 0) next.load(p.gates, b, h, first(0), t_live);
+    for (int c = 0; c < chunks; ++c) {
+      const RecordMaker now = next;
+      if (c + 1 < chunks) next.load(p.gates, b, h, first(c + 1), t_live);
+      if (c >= STAGES && !(ok = all_wait(SEMPTY + c % STAGES, (c / STAGES - 1) & 1))) break;
+      behind *= now.write<false>(p.gates, head, first(c), t_live, behind, kw + (c % STAGES) * C);
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(bars + SFULL + c % STAGES);
+    }
+    if (sl == 0 && lane == 0) p.seg_total[(size_t)unit * g.nseg + s] = behind;
   } else {
     const int r = 32 * quarter + lane;
     const int row = 16 * quarter + lane % 16, col = 16 * (lane / 16);   // a thread's column of d_v, rows of d_k
@@ -604,22 +633,16 @@ __global__ void __launch_bounds__(NTHR_STATE, 1)
     auto inside = [&](int i) { return row < cols && element(i) < g.d_k; };
     const size_t sq = (size_t)g.d_k * g.d_v;
     const float l2g = GATED ? 0.f : log2f(p.decay[h]);
-    const size_t unit_chunk = (size_t)unit * ((g.T + C - 1) / C);
-    auto total = [&](int c) { return c < chunks ? p.totals[unit_chunk + first(c) / C] : 1.f; };
-    float behind = GATED && group == 1 ? total(0) : 1.f;   // the chunks that come behind this one
     for (int c = group; c < chunks; c += 2) {
       const int t0 = first(c), n = min(C, t_live - t0);
       const uint32_t at = base + (c % STAGES) * L::stage, k0 = base + L::k0 + (c & 1) * 3 * TILE;
       float w = !GATED && r < n ? power(l2g, t_live - 1 - t0 - r) : 0.f;
-      if constexpr (GATED) {
-        w = p.records[(unit_chunk + t0 / C) * GATE_VALUES + GATE_K + r] * behind;   // (0 past the row's length)
-        behind *= total(c) * total(c + 1);
-      }
       // the terms' buffer first: chunk c - 2's product done means that the loads
       // up to chunk c - 2 have landed, so the stage's parity below is the one of
       // this chunk's load or the one before it
       if (!(ok = (c < 2 || all_wait(SFREE + (c & 1), ((c >> 1) - 1) & 1)) && all_wait(SFULL + c % STAGES, (c / STAGES) & 1)))
         break;
+      if constexpr (GATED) w = kw[(c % STAGES) * C + r];   // (0 past the row's length)
 #pragma unroll 2
       for (int j = 0; j < 8; ++j) scale_chunk(at, k0, r, j, w, r < n);
       if (r >= n) zero_row(at + TILE, r);
@@ -627,8 +650,6 @@ __global__ void __launch_bounds__(NTHR_STATE, 1)
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(bars + SK + (c & 1));
     }
-    if (GATED && ok && group == 0 && quarter == 0 && lane == 0 && sl == 0)
-      p.seg_total[(size_t)unit * g.nseg + s] = behind;   // all chunks by now
     // the sums, by the group of the last chunk
     if (ok && chunks > 0 && group == ((chunks - 1) & 1)) {
       ok = all_wait(SFREE + ((chunks - 1) & 1), ((chunks - 1) >> 1) & 1);
@@ -683,7 +704,7 @@ cudaError_t launch_out(const CUtensorMap& mq, const CUtensorMap& mk, const CUten
   constexpr int smem = Smem<NT, GATED>::end;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  return tc::launch_overlapped(kern, dim3(g.nseg, g.slices, g.B * g.H), dim3(NTHR), smem, st, mq, mk, mv, my, g, p, inline_scan,
+  return tc::launch_overlapped(kern, dim3(g.nseg, g.slices, g.B * g.H), dim3(threads_of(GATED)), smem, st, mq, mk, mv, my, g, p, inline_scan,
                                status);
 }
 
@@ -695,7 +716,7 @@ cudaError_t launch_all(const CUtensorMap& mq, const CUtensorMap& mk, const CUten
     auto kern = k_decay_ws_state<GATED>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SmemState::end);
     if (e != cudaSuccess) return e;
-    e = tc::launch_overlapped(kern, dim3(g.nseg - 1, g.slices, g.B * g.H), dim3(NTHR_STATE), SmemState::end, st, mk, mv, g, p,
+    e = tc::launch_overlapped(kern, dim3(g.nseg - 1, g.slices, g.B * g.H), dim3(state_threads_of(GATED)), SmemState::end, st, mk, mv, g, p,
                               status);
     if (e != cudaSuccess) return e;
     if (g.nseg > kInlineScan) {
@@ -720,7 +741,7 @@ cudaError_t ws_launch(const Geom& g, const Ptrs& p, bool y_bf16, int* status, cu
       !map_4d(&mv, p.v, true, g.dv_row, g.T, g.H, g.B, g.v_t, g.v_h, g.v_b) ||
       !map_4d(&my, p.y, y_bf16, g.dv_row, g.T, g.H, g.B, g.y_t, g.y_h, g.y_b))
     return cudaErrorInvalidValue;
-  return p.records ? launch_all<true>(mq, mk, mv, my, g, p, y_bf16, status, st)
+  return p.gated ? launch_all<true>(mq, mk, mv, my, g, p, y_bf16, status, st)
                    : launch_all<false>(mq, mk, mv, my, g, p, y_bf16, status, st);
 }
 

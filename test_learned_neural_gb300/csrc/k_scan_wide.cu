@@ -1,0 +1,636 @@
+// Selective scan on the tensor cores for 64 < d_k <= 128: bf16 q, k, v, any d_v in
+// slices of 64 columns, chunks of 128 tokens (decay_common.cuh has the formulas).
+// A pipeline of specialised warps, one CTA per SM:
+//
+//   warp 0       TMA: q of a chunk (32 KB, one buffer), once Q S of the one before is done
+//   warp 1       MMAs, per chunk c: Q S c, state product c, P V c, scores c + 1
+//   values (4)   V tile times the tokens' weights -> three bf16 terms (w V)
+//   probs (8)    scores of chunk c -> weights -> bf16 terms in TMEM; then the
+//                read-outs of chunk c - 1: TMEM -> the stage's own k tiles
+//   state (4)    the state in fp32 registers, a row of 64 values a thread; its terms
+//                as the operand of Q S
+//   warp 18      the chunks' records (products of the gates)
+//   warp 19      TMA: k, v of a chunk (48 KB) into a ring of two stages; a chunk's
+//                read-outs out of its stage before the next load into it
+//
+// The weights go into V and not into K (k_decay_ws.cu): V is the narrower of the
+// two here, and half as much has to be split into terms and held.
+// TMEM (512 columns): two score buffers (P's first two terms in place), P V, the
+// state's product, and for bf16 read-outs two buffers of Q S, so that Q S need not wait
+// for the read-outs of the chunk before; for fp32 ones, one, and P's third term.
+#include "decay_tc_dev.cuh"
+
+using namespace decay;
+using layer::bf16;
+
+namespace {
+
+constexpr int NTHR = 20 * 32, KB = 2, KV = (KB + 1) * TILE;   // KB: 64-wide tiles of d_k
+constexpr int RECORD = GATE_VALUES * 4;
+
+template <int NT>
+struct Smem {   // byte offsets from a 1024-byte aligned base
+  static constexpr int q = 2 * KV, w = q + KB * TILE, NS = NT == 2 ? 2 : 3, s = w + 3 * TILE, slots = NT == 2 ? 2 : 1,
+                       rec = s + NS * TILE, bars = rec + slots * RECORD, end = bars + 28 * 8;
+};
+static_assert(kGateTokens == C && Smem<2>::end <= 227 * 1024 && Smem<3>::end <= 227 * 1024, "a block on each SM");
+
+// SC, P, KVF, OUT: a barrier for each parity of the chunk; G, GE: for each slot of the records
+enum Bar { KVF = 0, OUT = 2, SC = 4, P = 6, G = 8, GE = 10, QFULL = 12, QFREE, WV, DS, DSFREE, S, PV, YFREE, NBARS };
+
+// 8 of a token's values (16-byte chunk j of row r), times w, in three terms
+__device__ __forceinline__ void scale_chunk(uint32_t src, uint32_t dst, int r, int j, float w, bool live) {
+  uint32_t x[4], y[4][3];
+  lds128(src + swz(r, j), x);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) split_pair<3>(mul_pair(widen(live ? x[i] : 0u), pair(w, w)), y[i]);
+#pragma unroll
+  for (int t = 0; t < 3; ++t) sts128(dst + t * TILE + swz(r, j), y[0][t], y[1][t], y[2][t], y[3][t]);
+}
+__device__ __forceinline__ void zero_row(uint32_t tile, int r) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) sts128(tile + r * 128 + 16 * j, 0, 0, 0, 0);
+}
+// K^T (w V), M = 128 rows of d_k, 64 columns, the three terms one after the other, the smallest first
+__device__ __forceinline__ void mma_state(uint32_t d, uint32_t ktile, uint32_t wtile) {
+  const uint32_t idesc = tc::idesc_f16(128, SL, 1, 1, 1);
+  const uint64_t kd = tc::sdesc_sw128(ktile, TILE);
+#pragma unroll
+  for (int t = 2; t >= 0; --t) {
+    const uint64_t vd = tc::sdesc_sw128(wtile + t * TILE, TILE);
+#pragma unroll
+    for (int s = 0; s < C / 16; ++s) tc::mma_f16(d, kd + s * (2048 >> 4), vd + s * (2048 >> 4), idesc, (t < 2 || s > 0) ? 1u : 0u);
+  }
+}
+
+template <int NT, typename TO>
+__global__ void __launch_bounds__(NTHR, 1)
+    k_scan_wide(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+                const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap my, Geom g, Ptrs p, int* status) {
+  using L = Smem<NT>;
+  extern __shared__ __align__(1024) uint8_t sm[];
+  const uint32_t base = tc::smem_u32(sm);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sm + L::bars);
+  uint32_t* tbase = reinterpret_cast<uint32_t*>(bars + NBARS);
+  int* failed = reinterpret_cast<int*>(bars + NBARS + 1);
+  const uint32_t bar0 = tc::smem_u32(bars);
+  auto bar = [&](int i) { return bar0 + 8 * i; };
+  const int s = blockIdx.x, sl = blockIdx.y, unit = blockIdx.z;
+  const int b = unit / g.H, h = unit % g.H, hq = h / g.share;
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, quarter = warp & 3, group = (warp - 2) >> 2;
+  if (warp == 0) tc::tmem_alloc(tbase, 512);
+  if (tid == 32) {
+    for (int i = 0; i < NBARS; ++i) {
+      const bool four = i == WV || i == DSFREE || i == S, eight = i == OUT || i == OUT + 1 || i == P || i == P + 1 || i == YFREE;
+      tc::mbar_init_only(bars + i, i == GE || i == GE + 1 ? 16 : eight ? 8 : four ? 4 : 1);
+    }
+    tc::mbar_init_fence();
+    *failed = (base & 1023u) ? 1 : 0;   // the swizzled tiles need it; never seen otherwise
+    tc::prefetch_map(&mq);
+    tc::prefetch_map(&mk);
+    tc::prefetch_map(&mv);
+    tc::prefetch_map(&my);
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  constexpr uint32_t tm = 0;   // all 512 columns: they start at 0 (checked below)
+  tc::grid_dependency_wait();
+  tc::grid_dependents_launch();
+
+  const int live = live_tokens(g, p, b);
+  const int t_lo = s * g.seg, t_hi = min(g.T, t_lo + g.seg), t_live = min(t_hi, max(live, t_lo));
+  const int chunks = (t_live - t_lo + C - 1) / C;
+  const int c0 = sl * SL, cols = min(SL, g.d_v - c0);
+  const size_t sq = (size_t)g.d_k * g.d_v;
+  bool ok = *failed == 0 && *tbase == tm;
+  constexpr uint32_t tSC = tm, tY2 = tm + 256, tDS = tm + 320, tY1 = tm + 384, tP2 = tm + 448;   // Y1: two (NT = 2) or one
+  auto all_wait = [&](int i, uint32_t parity) { return __all_sync(0xffffffffu, tc::wait(bar(i), parity)); };
+  auto arrive = [&](int i) {
+    __syncwarp();
+    if (lane == 0) tc::mbar_arrive(bars + i);
+  };
+  auto tokens = [&](int c) { return min(C, t_live - t_lo - c * C); };
+  auto stage = [&](int c) { return base + (c & 1) * KV; };
+  auto half = [](int c) { return (uint32_t)(c >> 1) & 1; };   // parity of a barrier that there are two of
+  auto rec_slot = [](int c) { return c % L::slots; };
+  auto rec_turn = [](int c) { return (uint32_t)(c / L::slots) & 1; };
+  auto record = [&](int c) { return reinterpret_cast<float*>(sm + L::rec) + rec_slot(c) * GATE_VALUES; };
+  auto run_of = [&](const float* rec, int r) { return rec[GATE_L + kRun * r + kRun - 1]; };   // product of g over run r
+
+  if (warp == 0) {
+    for (int c = 0; c < chunks && ok; ++c) {
+      if (c > 0 && !(ok = all_wait(QFREE, (c - 1) & 1))) break;
+      if (tc::elect()) {
+        tc::expect_tx(bar(QFULL), KB * TILE);
+        for (int i = 0; i < KB; ++i) load_4d(base + L::q + i * TILE, &mq, 64 * i, t_lo + c * C, hq, b, bar(QFULL));
+      }
+      __syncwarp();
+    }
+  } else if (warp == 19) {
+    auto load = [&](int c) {
+      tc::expect_tx(bar(KVF + (c & 1)), KV);
+      for (int i = 0; i < KB; ++i) load_4d(stage(c) + i * TILE, &mk, 64 * i, t_lo + c * C, hq, b, bar(KVF + (c & 1)));
+      load_4d(stage(c) + KB * TILE, &mv, c0, t_lo + c * C, h, b, bar(KVF + (c & 1)));
+    };
+    if (ok && tc::elect())
+      for (int c = 0; c < min(chunks, 2); ++c) load(c);
+    __syncwarp();
+    for (int c = 0; c < chunks && ok; ++c) {
+      if (!(ok = all_wait(OUT + (c & 1), half(c)))) break;
+      if (tc::elect()) {
+        store_4d(&my, c0, t_lo + c * C, h, b, stage(c));
+        if (sizeof(TO) == 4 && cols > 32) store_4d(&my, c0 + 32, t_lo + c * C, h, b, stage(c) + TILE);
+        tc::bulk_commit();
+        tc::bulk_wait_read<0>();
+        if (c + 2 < chunks) load(c + 2);
+      }
+      __syncwarp();
+    }
+  } else if (warp == 18) {
+    // records, the gates of the next one in flight
+    const HeadGates head(p.gates, h);
+    RecordMaker next;
+    if (chunks > 0) next.load(p.gates, b, h, t_lo, t_live);
+    for (int c = 0; c < chunks && ok; ++c) {
+      const RecordMaker now = next;
+      if (c + 1 < chunks) next.load(p.gates, b, h, t_lo + (c + 1) * C, t_live);
+      if (c >= L::slots && !(ok = all_wait(GE + rec_slot(c), rec_turn(c) ^ 1))) break;
+      now.write<true>(p.gates, head, t_lo + c * C, t_live, 1.f, record(c));
+      arrive(G + rec_slot(c));
+    }
+  } else if (warp == 1) {
+    const uint32_t idesc_p = tc::idesc_f16(C, SL, 1, 0, 1);
+    // Where P of the chunk before the last was: its P V is done, since that of the last
+    // one has waited for its read-outs.  (No wait for it here: the barrier may have gone
+    // on by a phase, and a wait for the earlier one would not end.)
+    auto scores = [&](int c) {
+      if (!(ok = all_wait(QFULL, c & 1) && all_wait(KVF + (c & 1), half(c)))) return;
+      tc::fence_after_sync();
+      if (tc::elect()) {
+        const uint32_t idesc = tc::idesc_f16(C, C, 1, 0, 0);
+#pragma unroll
+        for (int ks = 0; ks < 4 * KB; ++ks)
+          tc::mma_f16(tSC + 128 * (c & 1), tc::sdesc_sw128(base + L::q + (ks / 4) * TILE) + (ks % 4) * (32 >> 4),
+                      tc::sdesc_sw128(stage(c) + (ks / 4) * TILE) + (ks % 4) * (32 >> 4), idesc, ks > 0 ? 1u : 0u);
+        tc::mma_commit(bars + SC + (c & 1));
+      }
+      __syncwarp();
+    };
+    // Q S: the smallest terms first.  Its columns are free: the read-outs that used them are done, since P V of
+    // the last chunk (NT = 2, two buffers) or of this one (NT = 3) has waited for them.
+    auto inter = [&](int c) {
+      if (!(ok = all_wait(S, c & 1))) return;
+      tc::fence_after_sync();
+      if (tc::elect()) {
+#pragma unroll
+        for (int i = L::NS - 1; i >= 0; --i)
+#pragma unroll
+          for (int ks = 0; ks < 4 * KB; ++ks)
+            tc::mma_f16(tY1 + (NT == 2 ? 64 * (c & 1) : 0), tc::sdesc_sw128(base + L::q + (ks / 4) * TILE) + (ks % 4) * (32 >> 4),
+                        tc::sdesc_sw128(base + L::s + i * TILE, 8192) + ks * (2048 >> 4), idesc_p,
+                        (i < L::NS - 1 || ks > 0) ? 1u : 0u);
+        tc::mma_commit(bars + QFREE);
+      }
+      __syncwarp();
+    };
+    auto state_product = [&](int c) {
+      if (!(ok = all_wait(WV, c & 1) && (c == 0 || all_wait(DSFREE, (c - 1) & 1)))) return;
+      tc::fence_after_sync();
+      if (tc::elect()) {
+        mma_state(tDS, stage(c), base + L::w);
+        tc::mma_commit(bars + DS);
+      }
+      __syncwarp();
+    };
+    auto intra = [&](int c) {   // P V
+      if (!(ok = all_wait(P + (c & 1), half(c)) && (c == 0 || all_wait(YFREE, (c - 1) & 1)))) return;
+      tc::fence_after_sync();
+      if (tc::elect()) {
+        const uint64_t vd = tc::sdesc_sw128(stage(c) + KB * TILE, TILE);
+#pragma unroll
+        for (int k = NT - 1; k >= 0; --k)
+#pragma unroll
+          for (int ks = 0; ks < 8; ++ks)
+            mma_ts(tY2, k < 2 ? tSC + 128 * (c & 1) + 16 * ks + 8 * k : tP2 + 8 * ks, vd + ks * (2048 >> 4), idesc_p,
+                   (k < NT - 1 || ks > 0) ? 1u : 0u);
+        tc::mma_commit(bars + PV);
+      }
+      __syncwarp();
+    };
+    if (ok && chunks > 0) scores(0);
+    for (int c = 0; c < chunks && ok; ++c) {
+      if constexpr (NT == 2) {
+        inter(c);
+        if (ok) state_product(c);
+        if (ok) intra(c);
+      } else {
+        state_product(c);
+        if (ok) intra(c);
+        if (ok) inter(c);
+      }
+      if (ok && c + 1 < chunks) scores(c + 1);
+    }
+  } else if (group == 0) {
+    // values: one token per thread
+    const int r = 32 * quarter + lane;
+    for (int c = 0; c < chunks; ++c) {
+      const uint32_t kt = stage(c), vt = kt + KB * TILE;
+      const int n = tokens(c);
+      if (!(ok = all_wait(G + rec_slot(c), rec_turn(c)))) break;
+      const float w = record(c)[GATE_K + r];   // (0 past the row's length)
+      arrive(GE + rec_slot(c));
+      if (!(ok = all_wait(KVF + (c & 1), half(c)) && (c == 0 || all_wait(DS, (c - 1) & 1)))) break;
+#pragma unroll 2
+      for (int j = 0; j < 8; ++j) scale_chunk(vt, base + L::w, r, j, w, r < n);
+      // a token past the row's length: 0 * NaN must not reach the sums
+      if (r >= n) {
+        zero_row(vt, r);
+        for (int i = 0; i < KB; ++i) zero_row(kt + i * TILE, r);
+      }
+      tc::fence_smem_to_async();
+      arrive(WV);
+    }
+  } else if (group <= 2) {
+    // probs: 32 x 32 blocks of a warp's 32 rows, 0 and 3 or 1 and 2 of the four
+    const uint32_t lanes = (uint32_t)(32 * quarter) << 16;
+    const int row = 32 * quarter + lane, side = group - 1;
+    const float skip = p.D ? p.D[h] : 0.f;
+    float before = 0.f, now = 0.f;   // product of g from a chunk's start to the row's token
+    // the read-outs of chunk c, this warp's 32 tokens and half of the columns; f: times Q S.  The last product
+    // issued for them also stands behind the others that read the stage: P V behind the state's product.
+    auto reads = [&](int c, float f) {
+      if (!(ok = NT == 2 ? all_wait(PV, c & 1) : all_wait(QFREE, c & 1))) return;
+      tc::fence_after_sync();
+      const float sc = g.scale;
+      const bool dead = row >= tokens(c);
+      const uint32_t out = stage(c), y1 = tY1 + (NT == 2 ? 64 * (c & 1) : 0) + lanes + 32 * side;
+      f *= sc;
+#pragma unroll 1
+      for (int part = 0; part < 2; ++part) {   // 16 columns at a time
+        float yi[16], ya[16];
+        tc::tmem_ld16(y1 + 16 * part, yi);
+        tc::tmem_ld16(tY2 + lanes + 32 * side + 16 * part, ya);
+        tc::tmem_ld_wait16(yi);
+        tc::tmem_ld_wait16(ya);
+        if (part == 1) {
+          tc::fence_before_sync();
+          arrive(YFREE);
+        }
+#pragma unroll
+        for (int i = 0; i < 16; i += 2)
+          unpair(fma_pair(pair(yi[i], yi[i + 1]), pair(f, f), mul_pair(pair(ya[i], ya[i + 1]), pair(sc, sc))), ya[i],
+                 ya[i + 1]);
+        if (p.D) {   // D v, from the stage's own tile
+          uint32_t x[4];
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            lds128(out + KB * TILE + swz(row, 4 * side + 2 * part + j), x);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              float &u = ya[8 * j + 2 * i], &v = ya[8 * j + 2 * i + 1];
+              unpair(fma_pair(widen(x[i]), pair(skip, skip), pair(u, v)), u, v);
+            }
+          }
+        }
+        if (dead) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) ya[i] = 0.f;
+        }
+        if constexpr (sizeof(TO) == 2) {
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+            sts128(out + swz(row, 4 * side + 2 * part + j), layer::pack_bf16(ya[8 * j], ya[8 * j + 1]),
+                   layer::pack_bf16(ya[8 * j + 2], ya[8 * j + 3]), layer::pack_bf16(ya[8 * j + 4], ya[8 * j + 5]),
+                   layer::pack_bf16(ya[8 * j + 6], ya[8 * j + 7]));
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            sts128(out + side * TILE + swz(row, 4 * part + j), __float_as_uint(ya[4 * j]),
+                   __float_as_uint(ya[4 * j + 1]), __float_as_uint(ya[4 * j + 2]), __float_as_uint(ya[4 * j + 3]));
+        }
+      }
+      tc::fence_smem_to_async();
+      arrive(OUT + (c & 1));
+    };
+    for (int c = 0; c < chunks; ++c) {
+      const uint32_t sc = tSC + 128 * (c & 1) + lanes;
+      // the scores; the record; the stage's own barrier, for v; the third term's columns are the last chunk's
+      // until its P V is done
+      if (!(ok = all_wait(G + rec_slot(c), rec_turn(c)) && all_wait(KVF + (c & 1), half(c)) &&
+                 all_wait(SC + (c & 1), half(c)) && (NT == 2 || c == 0 || all_wait(PV, (c - 1) & 1))))
+        break;
+      tc::fence_after_sync();
+      const float* rec = record(c);
+      before = now;
+      now = rec[GATE_L + row];
+      for (int r = 0; r < quarter; ++r) now *= run_of(rec, r);
+      // a row's weights in its own run, from the row backwards: s_j times the decays between
+      float own = 0.f;
+#pragma unroll 1
+      for (int u = 0; u < 4; ++u) {
+        // columns 32 blk + h0 .., the later half first
+        const int blk = side == 0 ? 3 * (u >> 1) : 1 + (u >> 1), h0 = 16 * (1 - (u & 1));
+        uint32_t w[8][NT];
+        if (blk > quarter) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+#pragma unroll
+            for (int k = 0; k < NT; ++k) w[i][k] = 0u;
+        } else {
+          float v[16];
+          tc::tmem_ld16(sc + 32 * blk + h0, v);
+          tc::tmem_ld_wait16(v);
+          if (blk < quarter) {
+            float f = rec[GATE_L + row];   // the runs between, times what the record has to the run's end
+            for (int r = blk + 1; r < quarter; ++r) f *= run_of(rec, r);
+            const float* behind = rec + GATE_R + 32 * blk + h0;
+#pragma unroll
+            for (int i = 0; i < 8; i += 2) {
+              const float4 d = *reinterpret_cast<const float4*>(behind + 2 * i);
+              split_pair<NT>(mul_pair(pair(v[2 * i], v[2 * i + 1]), mul_pair(pair(d.x, d.y), pair(f, f))), w[i]);
+              split_pair<NT>(mul_pair(pair(v[2 * i + 2], v[2 * i + 3]), mul_pair(pair(d.z, d.w), pair(f, f))), w[i + 1]);
+            }
+          } else {
+            const float *gr = rec + GATE_G + 32 * blk + h0, *sr = rec + GATE_S + 32 * blk + h0;
+#pragma unroll
+            for (int i = 12; i >= 0; i -= 4) {
+              const float4 d = *reinterpret_cast<const float4*>(gr + i), st = *reinterpret_cast<const float4*>(sr + i);
+              const float ds[4] = {d.x, d.y, d.z, d.w}, ss[4] = {st.x, st.y, st.z, st.w};
+              float x[4];
+#pragma unroll
+              for (int e = 3; e >= 0; --e) {
+                const int col = h0 + i + e;
+                if (col == lane) own = 1.f;
+                x[e] = col <= lane ? v[i + e] * (own * ss[e]) : 0.f;
+                if (col <= lane) own *= ds[e];
+              }
+              split2<NT>(x[0], x[1], w[i / 2]);
+              split2<NT>(x[2], x[3], w[i / 2 + 1]);
+            }
+          }
+        }
+        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < NT; ++k) {
+          uint32_t x[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) x[i] = w[i][k];
+          // terms 0 and 1 over the halves of the 16 columns just read
+          tmem_st8u(k < 2 ? sc + 32 * blk + h0 + 8 * k : tP2 + lanes + 16 * blk + h0 / 2, x);
+        }
+      }
+      arrive(GE + rec_slot(c));
+      tc::tmem_st_wait();
+      tc::fence_before_sync();
+      arrive(P + (c & 1));
+      if (c > 0) {
+        reads(c - 1, before);
+        if (!ok) break;
+      }
+    }
+    if (ok && chunks > 0) reads(chunks - 1, now);
+    if (ok) {
+      // read-outs past the row's length: whole chunks (the last live chunk wrote its own)
+      TO* y = (TO*)p.y + b * g.y_b + h * g.y_h + c0 + 32 * side;
+      for (int t = t_lo + chunks * C + row / 32; t < t_hi; t += 4)
+        if (32 * side + lane < cols) y[t * g.y_t + lane] = layer::from_f32<TO>(0.f);
+    }
+  } else {
+    // state: row 32 quarter + lane of d_k
+    const int row = 32 * quarter + lane;
+    const uint32_t at = tDS + ((uint32_t)(32 * quarter) << 16);
+    float st[SL];
+    {
+      const float* start = g.nseg > 1 ? p.seg + ((size_t)unit * g.nseg + s) * sq : p.S0 ? p.S0 + unit * sq : nullptr;
+#pragma unroll
+      for (int i = 0; i < SL; ++i) st[i] = start && row < g.d_k && i < cols ? start[(size_t)row * g.d_v + c0 + i] : 0.f;
+    }
+    auto tiles = [&]() {
+#pragma unroll
+      for (int i = 0; i < SL; i += 8) {
+        uint32_t w[4][L::NS];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) split2<L::NS>(st[i + 2 * j], st[i + 2 * j + 1], w[j]);
+#pragma unroll
+        for (int n = 0; n < L::NS; ++n)
+          sts128(base + L::s + n * TILE + swz(row, i / 8), w[0][n], w[1][n], w[2][n], w[3][n]);
+      }
+      tc::fence_smem_to_async();
+      arrive(S);
+    };
+    if (ok && chunks > 0) tiles();
+    for (int c = 0; c < chunks && ok; ++c) {
+      if (!(ok = all_wait(G + rec_slot(c), rec_turn(c)))) break;
+      const float* rec = record(c);
+      const float all = run_of(rec, 0) * run_of(rec, 1) * (run_of(rec, 2) * run_of(rec, 3));
+      arrive(GE + rec_slot(c));
+      if (!(ok = all_wait(DS, c & 1))) break;
+      tc::fence_after_sync();
+#pragma unroll
+      for (int i = 0; i < SL; i += 16) {
+        float d[16];
+        tc::tmem_ld16(at + i, d);
+        tc::tmem_ld_wait16(d);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) st[i + e] = fmaf(all, st[i + e], d[e]);
+      }
+      tc::fence_before_sync();
+      arrive(DSFREE);
+      if (c + 1 < chunks) {
+        if (!(ok = all_wait(QFREE, c & 1))) break;   // Q S has read the last terms
+        tiles();
+      }
+    }
+    if (ok && s == g.nseg - 1 && p.S_out) {
+#pragma unroll
+      for (int i = 0; i < SL; ++i)
+        if (row < g.d_k && i < cols) p.S_out[unit * sq + (size_t)row * g.d_v + c0 + i] = st[i];
+    }
+  }
+  if (!ok && lane == 0) atomicExch(failed, 1);
+  tc::fence_before_sync();
+  __syncthreads();
+  if (*failed && tid == 0) {
+    tc::settle();
+    atomicExch(status, ATLAS_ERR_TIMEOUT);
+  }
+  __syncthreads();
+  if (warp == 0) tc::tmem_dealloc(tm, 512);
+}
+
+// A segment's own contribution to the state at its end: weights counted to that
+// end, the product accumulated in TMEM over the whole segment, a block of 64 columns
+// for each term (one MMA of N = 192).  The chunks in reverse, so that the product of
+// the decays behind a chunk comes by multiplying the chunks' own.  Two groups of
+// four value warps take chunks in turn, each with its own stage and terms.
+struct SmemState {
+  static constexpr int w = 2 * KV, kw = w + 6 * TILE, bars = kw + 2 * C * 4, end = bars + 8 * 8;
+};
+constexpr int NTHR_STATE = 11 * 32;
+enum BarState { SFULL = 0, SK = 2, SFREE = 4, NSBARS = 6 };
+
+__global__ void __launch_bounds__(NTHR_STATE, 1)
+    k_scan_wide_state(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv, Geom g, Ptrs p, int* status) {
+  using L = SmemState;
+  extern __shared__ __align__(1024) uint8_t sm[];
+  const uint32_t base = tc::smem_u32(sm);
+  float* kw = reinterpret_cast<float*>(sm + L::kw);   // the stages' weights
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sm + L::bars);
+  uint32_t* tbase = reinterpret_cast<uint32_t*>(bars + NSBARS);
+  int* failed = reinterpret_cast<int*>(bars + NSBARS + 1);
+  const uint32_t bar0 = tc::smem_u32(bars);
+  auto bar = [&](int i) { return bar0 + 8 * i; };
+  const int s = blockIdx.x, sl = blockIdx.y, unit = blockIdx.z;
+  const int b = unit / g.H, h = unit % g.H, hq = h / g.share;
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, quarter = warp & 3, group = (warp - 2) >> 2;
+  if (warp == 0) tc::tmem_alloc(tbase, 256);
+  if (tid == 32) {
+    for (int i = 0; i < NSBARS; ++i) tc::mbar_init_only(bars + i, i < SK ? 2 : i < SFREE ? 4 : 1);   // SFULL: copies and weights
+    tc::mbar_init_fence();
+    *failed = (base & 1023u) ? 1 : 0;
+    tc::prefetch_map(&mk);
+    tc::prefetch_map(&mv);
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tm = *tbase;
+  tc::grid_dependency_wait();
+  tc::grid_dependents_launch();
+
+  const int live = live_tokens(g, p, b);
+  const int t_lo = s * g.seg, t_hi = min(g.T, t_lo + g.seg), t_live = min(t_hi, max(live, t_lo));
+  const int c0 = sl * SL, cols = min(SL, g.d_v - c0), chunks = (t_live - t_lo + C - 1) / C;
+  auto first = [&](int c) { return t_lo + (chunks - 1 - c) * C; };   // of the c-th chunk to be worked on
+  bool ok = *failed == 0;
+  auto all_wait = [&](int i, uint32_t parity) { return __all_sync(0xffffffffu, tc::wait(bar(i), parity)); };
+  auto free_of = [&](int c) { return c < 2 || all_wait(SFREE + (c & 1), ((c >> 1) - 1) & 1); };   // chunk c - 2's product is done
+  if (warp == 0) {
+    for (int c = 0; c < chunks && ok; ++c) {
+      if (!(ok = free_of(c))) break;
+      if (tc::elect()) {
+        const uint32_t at = base + (c & 1) * KV, full = bar(SFULL + (c & 1));
+        tc::expect_tx(full, KV);
+        for (int i = 0; i < KB; ++i) load_4d(at + i * TILE, &mk, 64 * i, first(c), hq, b, full);
+        load_4d(at + KB * TILE, &mv, c0, first(c), h, b, full);
+      }
+      __syncwarp();
+    }
+  } else if (warp == 1) {
+    const uint32_t idesc = tc::idesc_f16(128, 3 * SL, 1, 1, 1);
+    for (int c = 0; c < chunks; ++c) {
+      if (!(ok = all_wait(SK + (c & 1), (c >> 1) & 1))) break;
+      tc::fence_after_sync();
+      if (tc::elect()) {
+        const uint64_t kd = tc::sdesc_sw128(base + (c & 1) * KV, TILE), vd = tc::sdesc_sw128(base + L::w + (c & 1) * 3 * TILE, TILE);
+#pragma unroll
+        for (int i = 0; i < C / 16; ++i)
+          tc::mma_f16(tm, kd + i * (2048 >> 4), vd + i * (2048 >> 4), idesc, (c > 0 || i > 0) ? 1u : 0u);
+        tc::mma_commit(bars + SFREE + (c & 1));
+      }
+      __syncwarp();
+    }
+  } else if (warp == 10) {
+    // the tokens' weights to the segment's end, the gates of the next chunk in flight
+    const HeadGates head(p.gates, h);
+    RecordMaker next;
+    float behind = 1.f;   // the product of g over the chunks that come behind
+    if (chunks > 0) next.load(p.gates, b, h, first(0), t_live);
+    for (int c = 0; c < chunks; ++c) {
+      const RecordMaker now = next;
+      if (c + 1 < chunks) next.load(p.gates, b, h, first(c + 1), t_live);
+      if (!(ok = free_of(c))) break;
+      behind *= now.write<false>(p.gates, head, first(c), t_live, behind, kw + (c & 1) * C);
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(bars + SFULL + (c & 1));
+    }
+    if (sl == 0 && lane == 0) p.seg_total[(size_t)unit * g.nseg + s] = behind;
+  } else {
+    const int r = 32 * quarter + lane;   // a token; at the end a row of d_k
+    for (int c = group; c < chunks; c += 2) {
+      const int n = min(C, t_live - first(c));
+      const uint32_t kt = base + (c & 1) * KV, vt = kt + KB * TILE, w0 = base + L::w + (c & 1) * 3 * TILE;
+      if (!(ok = free_of(c) && all_wait(SFULL + (c & 1), (c >> 1) & 1))) break;
+      const float w = kw[(c & 1) * C + r];   // (0 past the row's length)
+#pragma unroll 2
+      for (int j = 0; j < 8; ++j) scale_chunk(vt, w0, r, j, w, r < n);
+      if (r >= n)
+        for (int i = 0; i < KB; ++i) zero_row(kt + i * TILE, r);
+      tc::fence_smem_to_async();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(bars + SK + (c & 1));
+    }
+    // the sums, by the group of the last chunk
+    const int last = chunks > 0 ? (chunks - 1) & 1 : 0;
+    if (ok && chunks > 0 && group == last) {
+      ok = all_wait(SFREE + last, ((chunks - 1) >> 1) & 1);
+      tc::fence_after_sync();
+    }
+    if (ok && group == last) {
+      float* dst = p.seg + ((size_t)unit * g.nseg + s + 1) * ((size_t)g.d_k * g.d_v) + (size_t)r * g.d_v + c0;
+      const uint32_t ta = tm + ((uint32_t)(32 * quarter) << 16);
+#pragma unroll 1
+      for (int i = 0; i < SL; i += 16) {
+        float sum[16] = {};
+        if (chunks > 0) {
+#pragma unroll
+          for (int t = 2; t >= 0; --t) {
+            float d[16];
+            tc::tmem_ld16(ta + 64 * t + i, d);
+            tc::tmem_ld_wait16(d);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) sum[e] += d[e];
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          if (r < g.d_k && i + e < cols) dst[i + e] = sum[e];
+      }
+    }
+  }
+  if (!ok && lane == 0) atomicExch(failed, 1);
+  tc::fence_before_sync();
+  __syncthreads();
+  if (*failed && tid == 0) {
+    tc::settle();
+    atomicExch(status, ATLAS_ERR_TIMEOUT);
+  }
+  __syncthreads();
+  if (warp == 0) tc::tmem_dealloc(tm, 256);
+}
+
+template <int NT, typename TO>
+cudaError_t launch_out(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const CUtensorMap& my,
+                       const Geom& g, const Ptrs& p, int* status, cudaStream_t st) {
+  auto kern = k_scan_wide<NT, TO>;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<NT>::end);
+  if (e != cudaSuccess) return e;
+  return tc::launch_overlapped(kern, dim3(g.nseg, g.slices, g.B * g.H), dim3(NTHR), Smem<NT>::end, st, mq, mk, mv, my, g, p, status);
+}
+
+}  // namespace
+
+namespace decay {
+
+cudaError_t wide_launch(const Geom& g, const Ptrs& p, bool y_bf16, int* status, cudaStream_t st) {
+  CUtensorMap mq, mk, mv, my;
+  const int hq = g.H / g.share;
+  if (!map_4d(&mq, p.q, true, g.dk_row, g.T, hq, g.B, g.qk_t, g.qk_h, g.qk_b) ||
+      !map_4d(&mk, p.k, true, g.dk_row, g.T, hq, g.B, g.qk_t, g.qk_h, g.qk_b) ||
+      !map_4d(&mv, p.v, true, g.dv_row, g.T, g.H, g.B, g.v_t, g.v_h, g.v_b) ||
+      !map_4d(&my, p.y, y_bf16, g.dv_row, g.T, g.H, g.B, g.y_t, g.y_h, g.y_b))
+    return cudaErrorInvalidValue;
+  if (g.nseg > 1) {
+    auto kern = k_scan_wide_state;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SmemState::end);
+    if (e != cudaSuccess) return e;
+    e = tc::launch_overlapped(kern, dim3(g.nseg - 1, g.slices, g.B * g.H), dim3(NTHR_STATE), SmemState::end, st, mk, mv, g, p, status);
+    if (e != cudaSuccess) return e;
+    e = scan_launch(g, p, st);
+    if (e != cudaSuccess) return e;
+  }
+  return y_bf16 ? launch_out<2, bf16>(mq, mk, mv, my, g, p, status, st) : launch_out<3, float>(mq, mk, mv, my, g, p, status, st);
+}
+
+}  // namespace decay

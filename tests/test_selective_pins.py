@@ -276,7 +276,7 @@ def test_scan_forward_validates_before_any_cuda_call(lib):  # noqa: F811
     _refuses(lib, "scan", h, io, UNS, "65535")
     assert tln.atlas_scan_last_path(h) == -1 and tln.atlas_scan_status(h) == tln.ATLAS_OK
     assert tln.atlas_scan_workspace_bytes(h, 1, 1) == 0 and tln.atlas_scan_workspace_bytes(h, 0, 1) == 0
-    assert tln.atlas_scan_workspace_bytes(h, 1, 1000) >= 4 * 8 * 640 * 4
+    assert tln.atlas_scan_workspace_bytes(h, 1, 100000) >= 4 * 2 * 8 * 8 * 4      # states at the segments' starts
     tln.atlas_scan_destroy(h)
     h = tln.atlas_scan_create(tln.make_scan_config(4, 8, 8, gates="step"))
     io = tln.atlas_scan_io(1, 5)

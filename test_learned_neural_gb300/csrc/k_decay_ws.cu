@@ -283,19 +283,12 @@ __global__ void __launch_bounds__(threads_of(GATED), 1)
     const uint32_t lanes = (uint32_t)(32 * quarter) << 16;
     const int row = 32 * quarter + lane, side = group - 1;
     const float skip = GATED && p.D ? p.D[h] : 0.f;
+    float before = 0.f, from_start = 0.f;   // GATED: product of g from a chunk's start to the row's token
     // the read-outs of chunk c, this warp's 32 tokens and half of the columns
-    auto reads = [&](int c) {
+    auto reads = [&](int c, float gated) {
       if (!(ok = all_wait(Y, c & 1))) return;
       tc::fence_after_sync();
-      const float sc = g.scale;
-      float f = sc;
-      if constexpr (GATED) {
-        const float* rec = record(c);
-        f *= rec[GATE_L + row];
-        for (int r = 0; r < quarter; ++r) f *= run_of(rec, r);
-      } else {
-        f *= pw[row + 1];
-      }
+      const float f = (GATED ? gated : pw[row + 1]) * g.scale, sc = g.scale;
       const bool dead = row >= tokens(c);
       const uint32_t out = base + (c % STAGES) * STAGE;
 #pragma unroll 1
@@ -347,13 +340,25 @@ __global__ void __launch_bounds__(threads_of(GATED), 1)
     };
     for (int c = 0; c < chunks; ++c) {
       const uint32_t sc = tSC + 128 * (c & 1) + lanes;
+      const float* rec = GATED ? record(c) : nullptr;
+      float to_first = 1.f, to_second = 1.f;
+      if constexpr (GATED) {
+        // the stage's own barrier, for its record and v: it stays at this phase until these warps' read-outs of the
+        // chunk.  The products of g to the row's token, while the scores are on their way: from the chunk's start, and from
+        // the ends of the runs `side` and `side` + 1.
+        if (!(ok = all_wait(FULL + c % STAGES, (c / STAGES) & 1))) break;
+        before = from_start;
+        to_first = to_second = from_start = rec[GATE_L + row];
+        for (int r = 0; r < quarter; ++r) {
+          const float x = run_of(rec, r);
+          from_start *= x;
+          if (r > side) to_first *= x;
+        }
+      }
       // the scores; the third term's columns are the last chunk's until its P V is done
       if (!(ok = all_wait(SC + (c & 1), (c >> 1) & 1) && (NT == 2 || c == 0 || all_wait(PV, (c - 1) & 1)))) break;
-      // the stage's own barrier, for its record and v: it stays at this phase until these warps' read-outs of the chunk
-      if (GATED && !(ok = all_wait(FULL + c % STAGES, (c / STAGES) & 1))) break;
       tc::fence_after_sync();
       // GATED: a row's weights in its own run, from the row backwards: s_j times the decays between
-      const float* rec = GATED ? record(c) : nullptr;
       float own = 0.f;
       // 16 columns a turn: with everything unrolled the kernel's code overran the
       // instruction caches (4.6 of 11 cycles per instruction were spent on that)
@@ -372,13 +377,8 @@ __global__ void __launch_bounds__(threads_of(GATED), 1)
           tc::tmem_ld16(sc + 32 * blk + h0, v);
           tc::tmem_ld_wait16(v);
           if (blk < quarter) {
-            float f;
-            if constexpr (GATED) {   // the runs between, times what the record has to the run's end
-              f = rec[GATE_L + row];
-              for (int r = blk + 1; r < quarter; ++r) f *= run_of(rec, r);
-            } else {
-              f = pw[row - 32 * blk - 31];   // times g^{31 - column}
-            }
+            // GATED: times what the record has to the run's end, else times g^{31 - column}
+            const float f = GATED ? (u < 2 ? to_first : to_second) : pw[row - 32 * blk - 31];
             const float* behind = GATED ? rec + GATE_R + 32 * blk : rev;
 #pragma unroll
             for (int i = 0; i < 8; i += 2) {
@@ -396,9 +396,9 @@ __global__ void __launch_bounds__(threads_of(GATED), 1)
 #pragma unroll
               for (int e = 3; e >= 0; --e) {
                 const int col = h0 + i + e;
-                if (col == lane) own = 1.f;
+                own = col == lane ? 1.f : own;   // 0 before that: past the row's token
                 x[e] = col <= lane ? v[i + e] * (own * ss[e]) : 0.f;
-                if (col <= lane) own *= ds[e];
+                own *= ds[e];
               }
               split2<NT>(x[0], x[1], w[i / 2]);
               split2<NT>(x[2], x[3], w[i / 2 + 1]);
@@ -428,11 +428,11 @@ __global__ void __launch_bounds__(threads_of(GATED), 1)
       tc::fence_before_sync();
       arrive(P + (c & 1));
       if (c > 0) {
-        reads(c - 1);
+        reads(c - 1, before);
         if (!ok) break;
       }
     }
-    if (ok && chunks > 0) reads(chunks - 1);
+    if (ok && chunks > 0) reads(chunks - 1, from_start);
     if (ok) {
       // read-outs past the row's length: whole chunks (the last live chunk wrote its own)
       TO* y = (TO*)p.y + b * g.y_b + h * g.y_h + c0 + 32 * side;

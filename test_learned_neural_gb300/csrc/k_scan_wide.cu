@@ -315,16 +315,23 @@ __global__ void __launch_bounds__(NTHR, 1)
     };
     for (int c = 0; c < chunks; ++c) {
       const uint32_t sc = tSC + 128 * (c & 1) + lanes;
-      // the scores; the record; the stage's own barrier, for v; the third term's columns are the last chunk's
-      // until its P V is done
-      if (!(ok = all_wait(G + rec_slot(c), rec_turn(c)) && all_wait(KVF + (c & 1), half(c)) &&
-                 all_wait(SC + (c & 1), half(c)) && (NT == 2 || c == 0 || all_wait(PV, (c - 1) & 1))))
-        break;
-      tc::fence_after_sync();
+      // the record; the stage's own barrier, for v
+      if (!(ok = all_wait(G + rec_slot(c), rec_turn(c)) && all_wait(KVF + (c & 1), half(c)))) break;
+      // The products of g to the row's token, while the scores are on their way: from the chunk's start, and from the
+      // ends of the runs `side` and `side` + 1.
       const float* rec = record(c);
       before = now;
-      now = rec[GATE_L + row];
-      for (int r = 0; r < quarter; ++r) now *= run_of(rec, r);
+      float to_first = rec[GATE_L + row];
+      const float to_second = to_first;
+      now = to_first;
+      for (int r = 0; r < quarter; ++r) {
+        const float x = run_of(rec, r);
+        now *= x;
+        if (r > side) to_first *= x;
+      }
+      // the scores; the third term's columns are the last chunk's until its P V is done
+      if (!(ok = all_wait(SC + (c & 1), half(c)) && (NT == 2 || c == 0 || all_wait(PV, (c - 1) & 1)))) break;
+      tc::fence_after_sync();
       // a row's weights in its own run, from the row backwards: s_j times the decays between
       float own = 0.f;
 #pragma unroll 1
@@ -342,8 +349,7 @@ __global__ void __launch_bounds__(NTHR, 1)
           tc::tmem_ld16(sc + 32 * blk + h0, v);
           tc::tmem_ld_wait16(v);
           if (blk < quarter) {
-            float f = rec[GATE_L + row];   // the runs between, times what the record has to the run's end
-            for (int r = blk + 1; r < quarter; ++r) f *= run_of(rec, r);
+            const float f = u < 2 ? to_first : to_second;   // times what the record has to the run's end
             const float* behind = rec + GATE_R + 32 * blk + h0;
 #pragma unroll
             for (int i = 0; i < 8; i += 2) {
@@ -361,9 +367,9 @@ __global__ void __launch_bounds__(NTHR, 1)
 #pragma unroll
               for (int e = 3; e >= 0; --e) {
                 const int col = h0 + i + e;
-                if (col == lane) own = 1.f;
+                own = col == lane ? 1.f : own;   // 0 before that: past the row's token
                 x[e] = col <= lane ? v[i + e] * (own * ss[e]) : 0.f;
-                if (col <= lane) own *= ds[e];
+                own *= ds[e];
               }
               split2<NT>(x[0], x[1], w[i / 2]);
               split2<NT>(x[2], x[3], w[i / 2 + 1]);

@@ -2,22 +2,24 @@
 // slices of 64 columns, chunks of 128 tokens (decay_common.cuh has the formulas).
 // A pipeline of specialised warps, one CTA per SM:
 //
-//   warp 0       TMA: q of a chunk (32 KB, one buffer), once Q S of the one before is done
-//   warp 1       MMAs, per chunk c: Q S c, state product c, P V c, scores c + 1
+//   warp 0       TMA: q of a chunk (32 KB, one buffer), once Q S of the one before is
+//                done; k, v (48 KB) into a ring of two stages
+//   warp 1       MMAs, per chunk c: Q S c, state product c, scores c + 1, P V c
 //   values (4)   V tile times the tokens' weights -> three bf16 terms (w V)
-//   probs (8)    scores of chunk c -> weights -> bf16 terms in TMEM; then the
-//                read-outs of chunk c - 1: TMEM -> the stage's own k tiles
+//   probs (8)    scores of chunk c -> weights -> bf16 terms in TMEM (D on P's
+//                diagonal); then the read-outs of chunk c - 1: TMEM -> a tile of theirs
 //   state (4)    the state in fp32 registers, a row of 64 values a thread; its terms
 //                as the operand of Q S
 //   warp 18      the chunks' records (products of the gates)
-//   warp 19      TMA: k, v of a chunk (48 KB) into a ring of two stages; a chunk's
-//                read-outs out of its stage before the next load into it
+//   warp 19      TMA: read-outs to memory
 //
 // The weights go into V and not into K (k_decay_ws.cu): V is the narrower of the
 // two here, and half as much has to be split into terms and held.
 // TMEM (512 columns): two score buffers (P's first two terms in place), P V, the
 // state's product, and for bf16 read-outs two buffers of Q S, so that Q S need not wait
 // for the read-outs of the chunk before; for fp32 ones, one, and P's third term.
+// fp32 read-outs (32 KB) find no room of their own: they are formed in the stage's k
+// tiles, and the stage is free when they have left.
 #include "decay_tc_dev.cuh"
 
 using namespace decay;
@@ -30,13 +32,13 @@ constexpr int RECORD = GATE_VALUES * 4;
 
 template <int NT>
 struct Smem {   // byte offsets from a 1024-byte aligned base
-  static constexpr int q = 2 * KV, w = q + KB * TILE, NS = NT == 2 ? 2 : 3, s = w + 3 * TILE, slots = NT == 2 ? 2 : 1,
-                       rec = s + NS * TILE, bars = rec + slots * RECORD, end = bars + 28 * 8;
+  static constexpr int q = 2 * KV, w = q + KB * TILE, NS = NT == 2 ? 2 : 3, s = w + 3 * TILE,
+                       y = s + NS * TILE /* NT = 2 */, rec = y + (NT == 2 ? TILE : 0), bars = rec + RECORD, end = bars + 28 * 8;
 };
 static_assert(kGateTokens == C && Smem<2>::end <= 227 * 1024 && Smem<3>::end <= 227 * 1024, "a block on each SM");
 
-// SC, P, KVF, OUT: a barrier for each parity of the chunk; G, GE: for each slot of the records
-enum Bar { KVF = 0, OUT = 2, SC = 4, P = 6, G = 8, GE = 10, QFULL = 12, QFREE, WV, DS, DSFREE, S, PV, YFREE, NBARS };
+// KVF, KVE, OUT, SC, P: a barrier for each parity of the chunk
+enum Bar { KVF = 0, KVE = 2, OUT = 4, SC = 6, P = 8, G = 10, GE, QFULL, QFREE, WV, DS, DSFREE, S, PV, YFREE, YOUT, NBARS };
 
 // 8 of a token's values (16-byte chunk j of row r), times w, in three terms
 __device__ __forceinline__ void scale_chunk(uint32_t src, uint32_t dst, int r, int j, float w, bool live) {
@@ -82,7 +84,7 @@ __global__ void __launch_bounds__(NTHR, 1)
   if (tid == 32) {
     for (int i = 0; i < NBARS; ++i) {
       const bool four = i == WV || i == DSFREE || i == S, eight = i == OUT || i == OUT + 1 || i == P || i == P + 1 || i == YFREE;
-      tc::mbar_init_only(bars + i, i == GE || i == GE + 1 ? 16 : eight ? 8 : four ? 4 : 1);
+      tc::mbar_init_only(bars + i, i == GE ? 16 : eight ? 8 : four ? 4 : 1);
     }
     tc::mbar_init_fence();
     *failed = (base & 1023u) ? 1 : 0;   // the swizzled tiles need it; never seen otherwise
@@ -113,13 +115,20 @@ __global__ void __launch_bounds__(NTHR, 1)
   auto tokens = [&](int c) { return min(C, t_live - t_lo - c * C); };
   auto stage = [&](int c) { return base + (c & 1) * KV; };
   auto half = [](int c) { return (uint32_t)(c >> 1) & 1; };   // parity of a barrier that there are two of
-  auto rec_slot = [](int c) { return c % L::slots; };
-  auto rec_turn = [](int c) { return (uint32_t)(c / L::slots) & 1; };
-  auto record = [&](int c) { return reinterpret_cast<float*>(sm + L::rec) + rec_slot(c) * GATE_VALUES; };
-  auto run_of = [&](const float* rec, int r) { return rec[GATE_L + kRun * r + kRun - 1]; };   // product of g over run r
+  float* const rec = reinterpret_cast<float*>(sm + L::rec);   // of a chunk, until all have taken what they need of it
+  auto run_of = [&](int r) { return rec[GATE_L + kRun * r + kRun - 1]; };   // product of g over run r
 
+  auto load_kv = [&](int c) {
+    tc::expect_tx(bar(KVF + (c & 1)), KV);
+    for (int i = 0; i < KB; ++i) load_4d(stage(c) + i * TILE, &mk, 64 * i, t_lo + c * C, hq, b, bar(KVF + (c & 1)));
+    load_4d(stage(c) + KB * TILE, &mv, c0, t_lo + c * C, h, b, bar(KVF + (c & 1)));
+  };
   if (warp == 0) {
     for (int c = 0; c < chunks && ok; ++c) {
+      // the stage is free behind P V of the chunk before the last (NT = 3: when its read-outs have left, warp 19)
+      if (NT == 2 && c > 1 && !(ok = all_wait(KVE + (c & 1), half(c) ^ 1))) break;
+      if ((NT == 2 || c < 2) && tc::elect()) load_kv(c);
+      __syncwarp();
       if (c > 0 && !(ok = all_wait(QFREE, (c - 1) & 1))) break;
       if (tc::elect()) {
         tc::expect_tx(bar(QFULL), KB * TILE);
@@ -128,22 +137,16 @@ __global__ void __launch_bounds__(NTHR, 1)
       __syncwarp();
     }
   } else if (warp == 19) {
-    auto load = [&](int c) {
-      tc::expect_tx(bar(KVF + (c & 1)), KV);
-      for (int i = 0; i < KB; ++i) load_4d(stage(c) + i * TILE, &mk, 64 * i, t_lo + c * C, hq, b, bar(KVF + (c & 1)));
-      load_4d(stage(c) + KB * TILE, &mv, c0, t_lo + c * C, h, b, bar(KVF + (c & 1)));
-    };
-    if (ok && tc::elect())
-      for (int c = 0; c < min(chunks, 2); ++c) load(c);
-    __syncwarp();
     for (int c = 0; c < chunks && ok; ++c) {
       if (!(ok = all_wait(OUT + (c & 1), half(c)))) break;
       if (tc::elect()) {
-        store_4d(&my, c0, t_lo + c * C, h, b, stage(c));
-        if (sizeof(TO) == 4 && cols > 32) store_4d(&my, c0 + 32, t_lo + c * C, h, b, stage(c) + TILE);
+        const uint32_t from = NT == 2 ? base + L::y : stage(c);
+        store_4d(&my, c0, t_lo + c * C, h, b, from);
+        if (sizeof(TO) == 4 && cols > 32) store_4d(&my, c0 + 32, t_lo + c * C, h, b, from + TILE);
         tc::bulk_commit();
         tc::bulk_wait_read<0>();
-        if (c + 2 < chunks) load(c + 2);
+        if constexpr (NT == 2) tc::mbar_arrive(bars + YOUT);
+        else if (c + 2 < chunks) load_kv(c + 2);
       }
       __syncwarp();
     }
@@ -155,16 +158,17 @@ __global__ void __launch_bounds__(NTHR, 1)
     for (int c = 0; c < chunks && ok; ++c) {
       const RecordMaker now = next;
       if (c + 1 < chunks) next.load(p.gates, b, h, t_lo + (c + 1) * C, t_live);
-      if (c >= L::slots && !(ok = all_wait(GE + rec_slot(c), rec_turn(c) ^ 1))) break;
-      now.write<true>(p.gates, head, t_lo + c * C, t_live, 1.f, record(c));
-      arrive(G + rec_slot(c));
+      if (c > 0 && !(ok = all_wait(GE, (c - 1) & 1))) break;
+      now.write<true>(p.gates, head, t_lo + c * C, t_live, 1.f, rec);
+      arrive(G);
     }
   } else if (warp == 1) {
     const uint32_t idesc_p = tc::idesc_f16(C, SL, 1, 0, 1);
-    // Where P of the chunk before the last was: its P V is done, since that of the last
-    // one has waited for its read-outs.  (No wait for it here: the barrier may have gone
-    // on by a phase, and a wait for the earlier one would not end.)
+    // Where P of the chunk before the last was.  NT = 3: its P V is done, since that of
+    // the last one has waited for its read-outs (and no wait for it: the barrier may have
+    // gone on by a phase, and a wait for the earlier one would not end).
     auto scores = [&](int c) {
+      if (NT == 2 && c > 1 && !(ok = all_wait(PV, c & 1))) return;
       if (!(ok = all_wait(QFULL, c & 1) && all_wait(KVF + (c & 1), half(c)))) return;
       tc::fence_after_sync();
       if (tc::elect()) {
@@ -177,8 +181,9 @@ __global__ void __launch_bounds__(NTHR, 1)
       }
       __syncwarp();
     };
-    // Q S: the smallest terms first.  Its columns are free: the read-outs that used them are done, since P V of
-    // the last chunk (NT = 2, two buffers) or of this one (NT = 3) has waited for them.
+    // Q S: the smallest terms first.  Its columns are free: the read-outs that used them
+    // are done, since P V of the last chunk (NT = 2, two buffers) or of this one (NT = 3)
+    // has waited for them.
     auto inter = [&](int c) {
       if (!(ok = all_wait(S, c & 1))) return;
       tc::fence_after_sync();
@@ -215,21 +220,27 @@ __global__ void __launch_bounds__(NTHR, 1)
             mma_ts(tY2, k < 2 ? tSC + 128 * (c & 1) + 16 * ks + 8 * k : tP2 + 8 * ks, vd + ks * (2048 >> 4), idesc_p,
                    (k < NT - 1 || ks > 0) ? 1u : 0u);
         tc::mma_commit(bars + PV);
+        if constexpr (NT == 2) tc::mma_commit(bars + KVE + (c & 1));   // the stage is free
       }
       __syncwarp();
     };
     if (ok && chunks > 0) scores(0);
     for (int c = 0; c < chunks && ok; ++c) {
+      // The probs warps set the pace, so the next scores are to be there when they have
+      // made this chunk's P and the last one's read-outs: in front of P V, which waits for
+      // both.  NT = 3 has one buffer for Q S,
+      // free after those read-outs, and q is free after Q S.
       if constexpr (NT == 2) {
         inter(c);
         if (ok) state_product(c);
+        if (ok && c + 1 < chunks) scores(c + 1);
         if (ok) intra(c);
       } else {
         state_product(c);
         if (ok) intra(c);
         if (ok) inter(c);
+        if (ok && c + 1 < chunks) scores(c + 1);
       }
-      if (ok && c + 1 < chunks) scores(c + 1);
     }
   } else if (group == 0) {
     // values: one token per thread
@@ -237,9 +248,9 @@ __global__ void __launch_bounds__(NTHR, 1)
     for (int c = 0; c < chunks; ++c) {
       const uint32_t kt = stage(c), vt = kt + KB * TILE;
       const int n = tokens(c);
-      if (!(ok = all_wait(G + rec_slot(c), rec_turn(c)))) break;
-      const float w = record(c)[GATE_K + r];   // (0 past the row's length)
-      arrive(GE + rec_slot(c));
+      if (!(ok = all_wait(G, c & 1))) break;
+      const float w = rec[GATE_K + r];   // (0 past the row's length)
+      arrive(GE);
       if (!(ok = all_wait(KVF + (c & 1), half(c)) && (c == 0 || all_wait(DS, (c - 1) & 1)))) break;
 #pragma unroll 2
       for (int j = 0; j < 8; ++j) scale_chunk(vt, base + L::w, r, j, w, r < n);
@@ -255,17 +266,16 @@ __global__ void __launch_bounds__(NTHR, 1)
     // probs: 32 x 32 blocks of a warp's 32 rows, 0 and 3 or 1 and 2 of the four
     const uint32_t lanes = (uint32_t)(32 * quarter) << 16;
     const int row = 32 * quarter + lane, side = group - 1;
-    const float skip = p.D ? p.D[h] : 0.f;
+    const float skip = p.D ? p.D[h] : 0.f, sc = g.scale;
     float before = 0.f, now = 0.f;   // product of g from a chunk's start to the row's token
-    // the read-outs of chunk c, this warp's 32 tokens and half of the columns; f: times Q S.  The last product
-    // issued for them also stands behind the others that read the stage: P V behind the state's product.
+    // the read-outs of chunk c, this warp's 32 tokens and half of the columns; f: times Q S.
+    // (NT = 3: Q S is the last product that was issued for them, and the others that
+    // read the k tiles are in front of it.)
     auto reads = [&](int c, float f) {
-      if (!(ok = NT == 2 ? all_wait(PV, c & 1) : all_wait(QFREE, c & 1))) return;
+      if (!(ok = NT == 2 ? all_wait(PV, c & 1) && (c == 0 || all_wait(YOUT, (c - 1) & 1)) : all_wait(QFREE, c & 1))) return;
       tc::fence_after_sync();
-      const float sc = g.scale;
       const bool dead = row >= tokens(c);
-      const uint32_t out = stage(c), y1 = tY1 + (NT == 2 ? 64 * (c & 1) : 0) + lanes + 32 * side;
-      f *= sc;
+      const uint32_t out = NT == 2 ? base + L::y : stage(c), y1 = tY1 + (NT == 2 ? 64 * (c & 1) : 0) + lanes + 32 * side;
 #pragma unroll 1
       for (int part = 0; part < 2; ++part) {   // 16 columns at a time
         float yi[16], ya[16];
@@ -279,20 +289,7 @@ __global__ void __launch_bounds__(NTHR, 1)
         }
 #pragma unroll
         for (int i = 0; i < 16; i += 2)
-          unpair(fma_pair(pair(yi[i], yi[i + 1]), pair(f, f), mul_pair(pair(ya[i], ya[i + 1]), pair(sc, sc))), ya[i],
-                 ya[i + 1]);
-        if (p.D) {   // D v, from the stage's own tile
-          uint32_t x[4];
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            lds128(out + KB * TILE + swz(row, 4 * side + 2 * part + j), x);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              float &u = ya[8 * j + 2 * i], &v = ya[8 * j + 2 * i + 1];
-              unpair(fma_pair(widen(x[i]), pair(skip, skip), pair(u, v)), u, v);
-            }
-          }
-        }
+          unpair(fma_pair(pair(yi[i], yi[i + 1]), pair(f, f), pair(ya[i], ya[i + 1])), ya[i], ya[i + 1]);
         if (dead) {
 #pragma unroll
           for (int i = 0; i < 16; ++i) ya[i] = 0.f;
@@ -314,18 +311,17 @@ __global__ void __launch_bounds__(NTHR, 1)
       arrive(OUT + (c & 1));
     };
     for (int c = 0; c < chunks; ++c) {
-      const uint32_t sc = tSC + 128 * (c & 1) + lanes;
-      // the record; the stage's own barrier, for v
-      if (!(ok = all_wait(G + rec_slot(c), rec_turn(c)) && all_wait(KVF + (c & 1), half(c)))) break;
-      // The products of g to the row's token, while the scores are on their way: from the chunk's start, and from the
-      // ends of the runs `side` and `side` + 1.
-      const float* rec = record(c);
+      const uint32_t at = tSC + 128 * (c & 1) + lanes;
+      if (!(ok = all_wait(G, c & 1))) break;
+      // The products of g to the row's token, times the read-outs' factor, while the scores
+      // are on their way: from the chunk's start, and from the ends of the runs `side` and
+      // `side` + 1.
       before = now;
-      float to_first = rec[GATE_L + row];
+      float to_first = rec[GATE_L + row] * sc;
       const float to_second = to_first;
       now = to_first;
       for (int r = 0; r < quarter; ++r) {
-        const float x = run_of(rec, r);
+        const float x = run_of(r);
         now *= x;
         if (r > side) to_first *= x;
       }
@@ -346,7 +342,7 @@ __global__ void __launch_bounds__(NTHR, 1)
             for (int k = 0; k < NT; ++k) w[i][k] = 0u;
         } else {
           float v[16];
-          tc::tmem_ld16(sc + 32 * blk + h0, v);
+          tc::tmem_ld16(at + 32 * blk + h0, v);
           tc::tmem_ld_wait16(v);
           if (blk < quarter) {
             const float f = u < 2 ? to_first : to_second;   // times what the record has to the run's end
@@ -367,8 +363,8 @@ __global__ void __launch_bounds__(NTHR, 1)
 #pragma unroll
               for (int e = 3; e >= 0; --e) {
                 const int col = h0 + i + e;
-                own = col == lane ? 1.f : own;   // 0 before that: past the row's token
-                x[e] = col <= lane ? v[i + e] * (own * ss[e]) : 0.f;
+                own = col == lane ? sc : own;   // 0 before that: past the row's token
+                x[e] = col <= lane ? fmaf(v[i + e], own * ss[e], col == lane ? skip : 0.f) : 0.f;
                 own *= ds[e];
               }
               split2<NT>(x[0], x[1], w[i / 2]);
@@ -383,10 +379,10 @@ __global__ void __launch_bounds__(NTHR, 1)
 #pragma unroll
           for (int i = 0; i < 8; ++i) x[i] = w[i][k];
           // terms 0 and 1 over the halves of the 16 columns just read
-          tmem_st8u(k < 2 ? sc + 32 * blk + h0 + 8 * k : tP2 + lanes + 16 * blk + h0 / 2, x);
+          tmem_st8u(k < 2 ? at + 32 * blk + h0 + 8 * k : tP2 + lanes + 16 * blk + h0 / 2, x);
         }
       }
-      arrive(GE + rec_slot(c));
+      arrive(GE);
       tc::tmem_st_wait();
       tc::fence_before_sync();
       arrive(P + (c & 1));
@@ -409,8 +405,16 @@ __global__ void __launch_bounds__(NTHR, 1)
     float st[SL];
     {
       const float* start = g.nseg > 1 ? p.seg + ((size_t)unit * g.nseg + s) * sq : p.S0 ? p.S0 + unit * sq : nullptr;
+      const float* at = start + (size_t)row * g.d_v + c0;
+      if (!start || row >= g.d_k) {
 #pragma unroll
-      for (int i = 0; i < SL; ++i) st[i] = start && row < g.d_k && i < cols ? start[(size_t)row * g.d_v + c0 + i] : 0.f;
+        for (int i = 0; i < SL; ++i) st[i] = 0.f;
+      } else if (cols == SL && g.d_v % 4 == 0 && (uintptr_t)start % 16 == 0) {
+        layer::load_vec<SL>(at, st);
+      } else {
+#pragma unroll
+        for (int i = 0; i < SL; ++i) st[i] = i < cols ? at[i] : 0.f;
+      }
     }
     auto tiles = [&]() {
 #pragma unroll
@@ -427,10 +431,9 @@ __global__ void __launch_bounds__(NTHR, 1)
     };
     if (ok && chunks > 0) tiles();
     for (int c = 0; c < chunks && ok; ++c) {
-      if (!(ok = all_wait(G + rec_slot(c), rec_turn(c)))) break;
-      const float* rec = record(c);
-      const float all = run_of(rec, 0) * run_of(rec, 1) * (run_of(rec, 2) * run_of(rec, 3));
-      arrive(GE + rec_slot(c));
+      if (!(ok = all_wait(G, c & 1))) break;
+      const float all = run_of(0) * run_of(1) * (run_of(2) * run_of(3));
+      arrive(GE);
       if (!(ok = all_wait(DS, c & 1))) break;
       tc::fence_after_sync();
 #pragma unroll
@@ -449,9 +452,14 @@ __global__ void __launch_bounds__(NTHR, 1)
       }
     }
     if (ok && s == g.nseg - 1 && p.S_out) {
+      float* to = p.S_out + unit * sq + (size_t)row * g.d_v + c0;
+      if (row < g.d_k && cols == SL && g.d_v % 4 == 0 && (uintptr_t)p.S_out % 16 == 0) {
+        layer::store_vec<SL>(to, st);
+      } else {
 #pragma unroll
-      for (int i = 0; i < SL; ++i)
-        if (row < g.d_k && i < cols) p.S_out[unit * sq + (size_t)row * g.d_v + c0 + i] = st[i];
+        for (int i = 0; i < SL; ++i)
+          if (row < g.d_k && i < cols) to[i] = st[i];
+      }
     }
   }
   if (!ok && lane == 0) atomicExch(failed, 1);
@@ -589,9 +597,13 @@ __global__ void __launch_bounds__(NTHR_STATE, 1)
             for (int e = 0; e < 16; ++e) sum[e] += d[e];
           }
         }
+        if (r < g.d_k && cols == SL && g.d_v % 4 == 0) {   // (the workspace's states start on 16 bytes then)
+          layer::store_vec<16>(dst + i, sum);
+        } else {
 #pragma unroll
-        for (int e = 0; e < 16; ++e)
-          if (r < g.d_k && i + e < cols) dst[i + e] = sum[e];
+          for (int e = 0; e < 16; ++e)
+            if (r < g.d_k && i + e < cols) dst[i + e] = sum[e];
+        }
       }
     }
   }

@@ -38,11 +38,33 @@ __global__ void __launch_bounds__(256) k_decay_step(Geom g, Ptrs p) {
   const int b = unit / g.H, h = unit % g.H, tid = threadIdx.x;
   const int cl = tid % CL, rg = tid / CL, col = sl * kSlice + cl * V;
   const bool on = col < g.d_v;
+  tc::grid_dependency_wait();
+  tc::grid_dependents_launch();
   const int n = decay::live_tokens(g, p, b);
+  const TI* q = (const TI*)p.q + b * g.qk_b + (h / g.share) * g.qk_h;
+  const TI* k = (const TI*)p.k + b * g.qk_b + (h / g.share) * g.qk_h;
+  const TI* v = (const TI*)p.v + b * g.v_b + h * g.v_h;
+  TO* y = (TO*)p.y + b * g.y_b + h * g.y_h;
   float gam = 1.f, step = 1.f, skip = 0.f;
   if constexpr (!GATED) gam = p.decay[h];
   else if (p.D) skip = p.D[h];
   const decay::HeadGates head(GATED ? p.gates : Gates{nullptr, p.decay}, h);
+  // a token's values, a token ahead: the first one's in front of the state, so that
+  // its gates are there when the state comes (256 x 16 states of 128 x 64, one token: 48.7 us
+  // behind it and launched on its own, 42.5 so and overlapped)
+  decay::RawGates raw;
+  float qn = 0.f, kn = 0.f, vn[V] = {};
+  auto fetch = [&](int t) {
+    if constexpr (GATED) raw.load(p.gates, b, h, t);
+    if (tid < g.d_k) {   // (d_k <= 256)
+      qn = to_f32(q[t * g.qk_t + tid]);
+      kn = to_f32(k[t * g.qk_t + tid]);
+    }
+#pragma unroll
+    for (int e = 0; e < V; ++e)
+      if (on && col + e < g.d_v) vn[e] = to_f32(v[t * g.v_t + col + e]);
+  };
+  if (n > 0) fetch(0);
   const size_t base = (size_t)unit * g.d_k * g.d_v + col;
   float S[RPT][V];
 #pragma unroll
@@ -55,27 +77,13 @@ __global__ void __launch_bounds__(256) k_decay_step(Geom g, Ptrs p) {
       for (int e = 0; e < V; ++e) S[r][e] = 0.f;
     }
   }
-  const TI* q = (const TI*)p.q + b * g.qk_b + (h / g.share) * g.qk_h;
-  const TI* k = (const TI*)p.k + b * g.qk_b + (h / g.share) * g.qk_h;
-  const TI* v = (const TI*)p.v + b * g.v_b + h * g.v_h;
-  TO* y = (TO*)p.y + b * g.y_b + h * g.y_h;
   for (int t = 0; t < n; ++t) {
-    if constexpr (GATED) {
-      decay::RawGates raw;
-      raw.load(p.gates, b, h, t);
-      raw.values(p.gates, head.bias, head.A, gam, step);
-    }
-    for (int i = tid; i < g.d_k; i += 256) {
-      qs[i] = to_f32(q[t * g.qk_t + i]);
-      ks[i] = to_f32(k[t * g.qk_t + i]);
-      if constexpr (GATED) ks[i] *= step;
-    }
+    if constexpr (GATED) raw.values(p.gates, head.bias, head.A, gam, step);
+    if (tid < g.d_k) qs[tid] = qn, ks[tid] = GATED ? kn * step : kn;
     float vt[V], acc[V];
 #pragma unroll
-    for (int e = 0; e < V; ++e) {
-      vt[e] = on && col + e < g.d_v ? to_f32(v[t * g.v_t + col + e]) : 0.f;
-      acc[e] = 0.f;
-    }
+    for (int e = 0; e < V; ++e) vt[e] = vn[e], acc[e] = 0.f;
+    if (t + 1 < n) fetch(t + 1);
     __syncthreads();
 #pragma unroll
     for (int r = 0; r < RPT; ++r) {
@@ -578,18 +586,16 @@ cudaError_t launch_step(const Geom& g, const Ptrs& p, cudaStream_t st) {
   const int rows = (g.d_k + (v4 ? 15 : 3)) / (v4 ? 16 : 4);
   const unsigned grid = (unsigned)((size_t)g.B * g.H * g.slices);
   const size_t smem = step_smem(g, v4 ? 4 : 1);
-  auto go = [&](auto kern) { kern<<<grid, 256, smem, st>>>(g, p); };
+  auto go = [&](auto kern) { return tc::launch_overlapped(kern, dim3(grid), dim3(256), smem, st, g, p); };
   if (v4) {
-    if (rows <= 2) go(k_decay_step<TI, TO, 2, 4, GATED>);
-    else if (rows <= 4) go(k_decay_step<TI, TO, 4, 4, GATED>);
-    else if (rows <= 8) go(k_decay_step<TI, TO, 8, 4, GATED>);
-    else go(k_decay_step<TI, TO, 16, 4, GATED>);
-  } else {
-    if (rows <= 16) go(k_decay_step<TI, TO, 16, 1, GATED>);
-    else if (rows <= 32) go(k_decay_step<TI, TO, 32, 1, GATED>);
-    else go(k_decay_step<TI, TO, 64, 1, GATED>);
+    if (rows <= 2) return go(k_decay_step<TI, TO, 2, 4, GATED>);
+    if (rows <= 4) return go(k_decay_step<TI, TO, 4, 4, GATED>);
+    if (rows <= 8) return go(k_decay_step<TI, TO, 8, 4, GATED>);
+    return go(k_decay_step<TI, TO, 16, 4, GATED>);
   }
-  return cudaGetLastError();
+  if (rows <= 16) return go(k_decay_step<TI, TO, 16, 1, GATED>);
+  if (rows <= 32) return go(k_decay_step<TI, TO, 32, 1, GATED>);
+  return go(k_decay_step<TI, TO, 64, 1, GATED>);
 }
 
 template <typename K>

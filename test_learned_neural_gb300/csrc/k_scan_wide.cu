@@ -477,19 +477,21 @@ __global__ void __launch_bounds__(NTHR, 1)
 // end, the product accumulated in TMEM over the whole segment, a block of 64 columns
 // for each term (one MMA of N = 192).  The chunks in reverse, so that the product of
 // the decays behind a chunk comes by multiplying the chunks' own.  Two groups of
-// four value warps take chunks in turn, each with its own stage and terms.
+// four value warps take chunks in turn, each with its own terms.  V is free as soon as
+// it has been split, K behind the product: rings of two and three stages (one ring of
+// two for both waited for every load, 3.5 us a chunk).
 struct SmemState {
-  static constexpr int w = 2 * KV, kw = w + 6 * TILE, bars = kw + 2 * C * 4, end = bars + 8 * 8;
+  static constexpr int v = 3 * KB * TILE, w = v + 2 * TILE, kw = w + 6 * TILE, bars = kw + 2 * C * 4, end = bars + 16 * 8;
 };
 constexpr int NTHR_STATE = 11 * 32;
-enum BarState { SFULL = 0, SK = 2, SFREE = 4, NSBARS = 6 };
+enum BarState { KFULL = 0, KFREE = 3, VFULL = 6, VFREE = 8, SK = 10, SFREE = 12, NSBARS = 14 };
 
 __global__ void __launch_bounds__(NTHR_STATE, 1)
     k_scan_wide_state(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv, Geom g, Ptrs p, int* status) {
   using L = SmemState;
   extern __shared__ __align__(1024) uint8_t sm[];
   const uint32_t base = tc::smem_u32(sm);
-  float* kw = reinterpret_cast<float*>(sm + L::kw);   // the stages' weights
+  float* kw = reinterpret_cast<float*>(sm + L::kw);   // the chunks' weights
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + L::bars);
   uint32_t* tbase = reinterpret_cast<uint32_t*>(bars + NSBARS);
   int* failed = reinterpret_cast<int*>(bars + NSBARS + 1);
@@ -500,7 +502,8 @@ __global__ void __launch_bounds__(NTHR_STATE, 1)
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, quarter = warp & 3, group = (warp - 2) >> 2;
   if (warp == 0) tc::tmem_alloc(tbase, 256);
   if (tid == 32) {
-    for (int i = 0; i < NSBARS; ++i) tc::mbar_init_only(bars + i, i < SK ? 2 : i < SFREE ? 4 : 1);   // SFULL: copies and weights
+    for (int i = 0; i < NSBARS; ++i)   // VFULL: copies and weights; VFREE, SK: four warps
+      tc::mbar_init_only(bars + i, i >= VFULL && i < VFREE ? 2 : i >= VFREE && i < SFREE ? 4 : 1);
     tc::mbar_init_fence();
     *failed = (base & 1023u) ? 1 : 0;
     tc::prefetch_map(&mk);
@@ -519,29 +522,37 @@ __global__ void __launch_bounds__(NTHR_STATE, 1)
   auto first = [&](int c) { return t_lo + (chunks - 1 - c) * C; };   // of the c-th chunk to be worked on
   bool ok = *failed == 0;
   auto all_wait = [&](int i, uint32_t parity) { return __all_sync(0xffffffffu, tc::wait(bar(i), parity)); };
-  auto free_of = [&](int c) { return c < 2 || all_wait(SFREE + (c & 1), ((c >> 1) - 1) & 1); };   // chunk c - 2's product is done
+  auto turn3 = [](int c) { return (uint32_t)(c / 3) & 1; };   // parity of a barrier that there are three of
+  auto turn2 = [](int c) { return (uint32_t)(c >> 1) & 1; };
+  auto ktile = [&](int c) { return base + (c % 3) * KB * TILE; };
+  auto vtile = [&](int c) { return base + L::v + (c & 1) * TILE; };
   if (warp == 0) {
     for (int c = 0; c < chunks && ok; ++c) {
-      if (!(ok = free_of(c))) break;
+      if (c > 1 && !(ok = all_wait(VFREE + (c & 1), turn2(c) ^ 1))) break;
       if (tc::elect()) {
-        const uint32_t at = base + (c & 1) * KV, full = bar(SFULL + (c & 1));
-        tc::expect_tx(full, KV);
-        for (int i = 0; i < KB; ++i) load_4d(at + i * TILE, &mk, 64 * i, first(c), hq, b, full);
-        load_4d(at + KB * TILE, &mv, c0, first(c), h, b, full);
+        tc::expect_tx(bar(VFULL + (c & 1)), TILE);
+        load_4d(vtile(c), &mv, c0, first(c), h, b, bar(VFULL + (c & 1)));
+      }
+      __syncwarp();
+      if (c > 2 && !(ok = all_wait(KFREE + c % 3, turn3(c) ^ 1))) break;
+      if (tc::elect()) {
+        tc::expect_tx(bar(KFULL + c % 3), KB * TILE);
+        for (int i = 0; i < KB; ++i) load_4d(ktile(c) + i * TILE, &mk, 64 * i, first(c), hq, b, bar(KFULL + c % 3));
       }
       __syncwarp();
     }
   } else if (warp == 1) {
     const uint32_t idesc = tc::idesc_f16(128, 3 * SL, 1, 1, 1);
     for (int c = 0; c < chunks; ++c) {
-      if (!(ok = all_wait(SK + (c & 1), (c >> 1) & 1))) break;
+      if (!(ok = all_wait(SK + (c & 1), turn2(c)) && all_wait(KFULL + c % 3, turn3(c)))) break;
       tc::fence_after_sync();
       if (tc::elect()) {
-        const uint64_t kd = tc::sdesc_sw128(base + (c & 1) * KV, TILE), vd = tc::sdesc_sw128(base + L::w + (c & 1) * 3 * TILE, TILE);
+        const uint64_t kd = tc::sdesc_sw128(ktile(c), TILE), vd = tc::sdesc_sw128(base + L::w + (c & 1) * 3 * TILE, TILE);
 #pragma unroll
         for (int i = 0; i < C / 16; ++i)
           tc::mma_f16(tm, kd + i * (2048 >> 4), vd + i * (2048 >> 4), idesc, (c > 0 || i > 0) ? 1u : 0u);
         tc::mma_commit(bars + SFREE + (c & 1));
+        tc::mma_commit(bars + KFREE + c % 3);
       }
       __syncwarp();
     }
@@ -554,23 +565,29 @@ __global__ void __launch_bounds__(NTHR_STATE, 1)
     for (int c = 0; c < chunks; ++c) {
       const RecordMaker now = next;
       if (c + 1 < chunks) next.load(p.gates, b, h, first(c + 1), t_live);
-      if (!(ok = free_of(c))) break;
+      if (c > 1 && !(ok = all_wait(VFREE + (c & 1), turn2(c) ^ 1))) break;
       behind *= now.write<false>(p.gates, head, first(c), t_live, behind, kw + (c & 1) * C);
       __syncwarp();
-      if (lane == 0) tc::mbar_arrive(bars + SFULL + (c & 1));
+      if (lane == 0) tc::mbar_arrive(bars + VFULL + (c & 1));
     }
     if (sl == 0 && lane == 0) p.seg_total[(size_t)unit * g.nseg + s] = behind;
   } else {
     const int r = 32 * quarter + lane;   // a token; at the end a row of d_k
     for (int c = group; c < chunks; c += 2) {
       const int n = min(C, t_live - first(c));
-      const uint32_t kt = base + (c & 1) * KV, vt = kt + KB * TILE, w0 = base + L::w + (c & 1) * 3 * TILE;
-      if (!(ok = free_of(c) && all_wait(SFULL + (c & 1), (c >> 1) & 1))) break;
+      const uint32_t w0 = base + L::w + (c & 1) * 3 * TILE;
+      // the terms' buffer first: chunk c - 2's product has read it
+      if (!(ok = (c < 2 || all_wait(SFREE + (c & 1), turn2(c) ^ 1)) && all_wait(VFULL + (c & 1), turn2(c)))) break;
       const float w = kw[(c & 1) * C + r];   // (0 past the row's length)
 #pragma unroll 2
-      for (int j = 0; j < 8; ++j) scale_chunk(vt, w0, r, j, w, r < n);
-      if (r >= n)
-        for (int i = 0; i < KB; ++i) zero_row(kt + i * TILE, r);
+      for (int j = 0; j < 8; ++j) scale_chunk(vtile(c), w0, r, j, w, r < n);
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(bars + VFREE + (c & 1));
+      if (n < C) {   // tokens past the row's length (the first chunk): 0 * NaN must not reach the sums
+        if (!(ok = all_wait(KFULL + c % 3, turn3(c)))) break;
+        if (r >= n)
+          for (int i = 0; i < KB; ++i) zero_row(ktile(c) + i * TILE, r);
+      }
       tc::fence_smem_to_async();
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(bars + SK + (c & 1));
@@ -578,7 +595,7 @@ __global__ void __launch_bounds__(NTHR_STATE, 1)
     // the sums, by the group of the last chunk
     const int last = chunks > 0 ? (chunks - 1) & 1 : 0;
     if (ok && chunks > 0 && group == last) {
-      ok = all_wait(SFREE + last, ((chunks - 1) >> 1) & 1);
+      ok = all_wait(SFREE + last, turn2(chunks - 1));
       tc::fence_after_sync();
     }
     if (ok && group == last) {

@@ -68,7 +68,7 @@ typedef struct atlas_qlinear_handle atlas_qlinear_handle;
 
 /* Tensors of one call, all DEVICE pointers owned by the caller. */
 typedef struct {
-    int M;                 /* rows, 1 .. 4194240 */
+    int M;                 /* rows, 1 .. 4194240 (fp32 x: 2097120) */
     const void* x;         /* [M][K] x_dtype */
     const float* x_scale;  /* ATLAS_E4M3: [M][ceil(K / 128)], or [M] for x_block 0; else NULL */
     const void* W;         /* what atlas_qlinear_pack wrote, aligned to 16 bytes */

@@ -38,7 +38,8 @@ constexpr int kWarps = 8, kThreads = 32 * (kWarps + 1);   // eight work, one loa
 constexpr int kCols = 128, kChunk = 128, kCodes = kCols * kChunk / 2;
 constexpr int kRowBytes = 320;   // of a chunk of a row of x in shared memory: 256, and no two rows of a pair in the same banks
 constexpr int kMostStages = 4;
-constexpr int kMostRows = 65535 * 64;
+// rows of a call: row blocks are the grid's second dimension
+int most_rows(int x_dtype) { return 65535 * (x_dtype == ATLAS_F32 ? 32 : 64); }
 
 // How the kernel gets x: bf16 rows as the caller has them (whole chunks of K, eight
 // rows), or, from a pass in front, as fragments: [row block][chunk][plane][8 rows][4
@@ -479,7 +480,7 @@ __global__ void __launch_bounds__(256) k_quantize(Shape s, const T* __restrict__
     const float v = to_f32(W[(size_t)k * s.N + n]);
     lo = fminf(lo, v), hi = fmaxf(hi, v);
   }
-  const bf16 sb = from_f32<bf16>(zeros ? (hi - lo) / 15.f : fmaxf(hi, -lo) / 7.f);
+  const bf16 sb = from_f32<bf16>(zeros ? hi / 15.f - lo / 15.f : fmaxf(hi, -lo) / 7.f);
   const float sc = to_f32(sb);
   int zero = 8;
   if (zeros) {
@@ -673,7 +674,7 @@ extern "C" int atlas_qlinear_forward(atlas_qlinear_handle* h, const atlas_qlinea
   if (q != (io->x_scale != nullptr))
     return h->fail(ATLAS_ERR_INVALID_ARG, "x_scale goes with x_dtype ATLAS_E4M3, and only with it");
   if (!aligned16(io->W)) return h->fail(ATLAS_ERR_INVALID_ARG, "W must be aligned to 16 bytes");
-  if (io->M > kMostRows) return h->fail(ATLAS_ERR_UNSUPPORTED, "M > %d is not supported", kMostRows);
+  if (io->M > most_rows(c.x_dtype)) return h->fail(ATLAS_ERR_UNSUPPORTED, "M > %d is not supported", most_rows(c.x_dtype));
   const size_t M = io->M, xblocks = c.x_block ? (c.K + c.x_block - 1) / c.x_block : 1;
   const size_t yb = M * c.N * dtype_size(c.out_dtype);
   if (overlap(io->y, yb, io->x, M * c.K * (q ? 1 : dtype_size(c.x_dtype))) || overlap(io->y, yb, io->W, atlas_qlinear_packed_bytes(h)) ||

@@ -178,6 +178,11 @@ def test_qlinear_validates_before_any_cuda_call(lib):  # noqa: F811
     for args in ((None, 0, 64, 1 << 20, 1 << 21), (1 << 30, 2, 64, 1 << 20, 1 << 21), (1 << 30, 0, 64, 1 << 20, None),
                  (1 << 20, 0, 64, (1 << 20) + 100, 1 << 25)):
         assert Q(h, *args, None) == BAD and tln.atlas_qlinear_last_error(h)
+    f32 = tln.atlas_qlinear_create(tln.make_qlinear_config(100, 40, x_dtype="f32"))
+    io = tln.atlas_qlinear_io(2097121)
+    io.x, io.y, io.W = 1 << 40, 1 << 41, 1 << 42
+    _refuses(lib, "qlinear", f32, io, UNS, "2097120")
+    tln.atlas_qlinear_destroy(f32)
     for args in ((64, 1 << 20, 1 << 21, None), (64, 1 << 20, None, 1 << 22), (64, 1 << 20, 1 << 21, (1 << 22) + 4),
                  (1 << 22, 1 << 20, 1 << 21, 1 << 22)):
         assert P(h, *args, None) == BAD and tln.atlas_qlinear_last_error(h)

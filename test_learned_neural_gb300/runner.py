@@ -211,21 +211,14 @@ def _check_rows(name, t, dtype, shape, device):
     """The same for [B, T, ...] whose tokens may lie further apart than their
     own values (a slice of wider rows, which are themselves contiguous): the
     address, and the values between neighbouring tokens."""
-    width = 1
-    for n in shape[2:]:
-        width *= n
-    B, T = shape[:2]
-    if t.is_contiguous():
-        return _check(name, t, dtype, shape, device), width
     st = t.stride()
-    inner, dense = width, len(st) == len(shape)
-    for n, step in zip(shape[2:], st[2:]):
-        inner //= n
-        dense = dense and (n == 1 or step == inner)
+    width, inner = (shape[2] * shape[3], (shape[3], 1)) if len(shape) == 4 else (shape[2], (1,))
     # the distance of tokens, from that of the batch rows where there is one token each
-    ld = st[1] if T > 1 else st[0] if B > 1 else width
-    if (t.dtype is not dtype or t.shape != shape or not dense or not t.is_cuda or ld < width or ld > 0x7fffffff
-            or B > 1 and st[0] != T * ld or device is not None and t.get_device() != device):
+    ld = st[1] if shape[1] > 1 else st[0] if shape[0] > 1 else width
+    if (t.dtype is not dtype or t.shape != shape or not t.is_cuda or not width <= ld <= 0x7fffffff
+            or shape[0] > 1 and st[0] != shape[1] * ld
+            or st[2:] != inner and any(n > 1 and a != b for n, a, b in zip(shape[2:], st[2:], inner))
+            or device is not None and t.get_device() != device):
         raise ValueError(f"{name}: want a CUDA tensor {dtype} {shape} on one device with the others, contiguous or a "
                          f"slice of contiguous rows, got {t.dtype} {tuple(t.shape)} with strides {st} on {t.device}")
     return t.data_ptr(), ld
@@ -561,7 +554,7 @@ class SelectiveScan(_Layer):
         self.cfg = make_scan_config(H, d_k, d_v, share, gates, qkv_dtype, y_dtype, qkv_layout, y_layout, scale)
         self.h = atlas_scan_create(self.cfg)
         c = self.cfg
-        self._qkv, self._y = _torch_dtype(c.qkv_dtype), _torch_dtype(c.y_dtype)
+        self._qkv, self._y, self._memory = _torch_dtype(c.qkv_dtype), _torch_dtype(c.y_dtype), c.gates == ATLAS_GATES_MEMORY
         self._heads_first, self._y_heads_first = c.qkv_layout == ATLAS_LAYOUT_HEADS, c.y_layout == ATLAS_LAYOUT_HEADS
 
     def _y_shape(self, B, T):
@@ -579,40 +572,41 @@ class SelectiveScan(_Layer):
         (fp32 [H]); and optional D (fp32 [H]), lens (int32 [B]) and S0 (fp32 [B, H, d_k,
         d_v]; may be out["S"]: the state is then continued in place).  In the layout
         "tokens" q and k, v, and the gates may be slices of wider rows."""
-        c, q, v, f32 = self.cfg, t["q"], t["v"], torch.float32
-        hq = c.H // c.share
-        if out is None:
-            out = self.alloc_outputs(*((q.shape[0], q.shape[2]) if self._heads_first else q.shape[:2]), q.device)
-        dev, ld_qk, ld_v, ld_g = _device_of(q), 0, 0, 0
-        memory = c.gates == ATLAS_GATES_MEMORY
-        step, alpha = (t["theta"], t["alpha"]) if memory else (t["dt"], None)
+        c, q, f32 = self.cfg, t["q"], torch.float32
+        H, dk, dv, memory = c.H, c.d_k, c.d_v, self._memory
+        hq, dev = H // c.share, _device_of(q)
+        A = bias = pa = None
+        if memory:
+            step, alpha = t["theta"], t["alpha"]
+        else:
+            step, alpha, A, bias = t["dt"], None, _check("A", t["A"], f32, (H,), dev), t.get("dt_bias")
+            if bias is not None:
+                bias = _check("dt_bias", bias, f32, (H,), dev)
         if self._heads_first:
             B, T = q.shape[0], q.shape[2]
-            qs, gs = (B, hq, T, c.d_k), (B, c.H, T)
-            pq, pk, pv = (_check("q", q, self._qkv, qs, dev), _check("k", t["k"], self._qkv, qs, dev),
-                          _check("v", v, self._qkv, (B, c.H, T, c.d_v), dev))
-            ps = _check("step", step, f32, gs, dev)
-            pa = None if alpha is None else _check("alpha", alpha, f32, gs, dev)
+            qs, gs, ld_qk, ld_v, ld_g = (B, hq, T, dk), (B, H, T), 0, 0, 0
+            pq, pk = _check("q", q, self._qkv, qs, dev), _check("k", t["k"], self._qkv, qs, dev)
+            pv, ps = _check("v", t["v"], self._qkv, (B, H, T, dv), dev), _check("step", step, f32, gs, dev)
+            if memory:
+                pa = _check("alpha", alpha, f32, gs, dev)
         else:
             B, T = q.shape[:2]
-            qs, gs = (B, T, hq, c.d_k), (B, T, c.H)
+            qs, gs = (B, T, hq, dk), (B, T, H)
             pq, ld_qk = _check_rows("q", q, self._qkv, qs, dev)
             pk, ld_k = _check_rows("k", t["k"], self._qkv, qs, dev)
-            pv, ld_v = _check_rows("v", v, self._qkv, (B, T, c.H, c.d_v), dev)
+            pv, ld_v = _check_rows("v", t["v"], self._qkv, (B, T, H, dv), dev)
             ps, ld_g = _check_rows("step", step, f32, gs, dev)
-            pa, ld_a = (None, ld_g) if alpha is None else _check_rows("alpha", alpha, f32, gs, dev)
+            pa, ld_a = _check_rows("alpha", alpha, f32, gs, dev) if memory else (None, ld_g)
             if ld_k != ld_qk or ld_a != ld_g:
                 raise ValueError("the tokens of q and k, and of theta and alpha, must lie equally far apart")
-        A, bias, D, lens, S0, sq = t.get("A"), t.get("dt_bias"), t.get("D"), t.get("lens"), t.get("S0"), (B, c.H, c.d_k, c.d_v)
-
-        def head(name, a):
-            return None if a is None else _check(name, a, f32, (c.H,), dev)
-
-        io = atlas_scan_io(B, T, ld_qk, ld_v, ld_g, pq, pk, pv, ps, pa, None if memory else head("A", A),
-                           None if memory else head("dt_bias", bias), head("D", D),
+        if out is None:
+            out = self.alloc_outputs(B, T, q.device)
+        D, lens, S0, sq = t.get("D"), t.get("lens"), t.get("S0"), (B, H, dk, dv)
+        io = atlas_scan_io(B, T, ld_qk, ld_v, ld_g, pq, pk, pv, ps, pa, A, bias,
+                           None if D is None else _check("D", D, f32, (H,), dev),
                            None if lens is None else _check("lens", lens, torch.int32, (B,), dev),
                            None if S0 is None else _check("S0", S0, f32, sq, dev),
-                           _check("y", out["y"], self._y, self._y_shape(B, T), dev),
+                           _check("y", out["y"], self._y, (B, H, T, dv) if self._y_heads_first else (B, T, H, dv), dev),
                            _check("S", out["S"], f32, sq, dev))
         atlas_scan_forward(self.h, io, _stream_of(dev, stream))
         return out

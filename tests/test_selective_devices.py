@@ -4,8 +4,13 @@ import pytest
 import torch
 
 from test_learned_neural_gb300 import runner
-from tests.test_layer_devices import Fake
+from tests.test_layer_devices import Fake as Plain
 from tests.test_layer_pins import lib  # noqa: F401
+
+
+class Fake(Plain):
+    def stride(self):
+        return torch.empty(self.shape, device="meta").stride()
 
 
 def _cases():

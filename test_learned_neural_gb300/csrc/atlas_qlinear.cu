@@ -74,7 +74,7 @@ struct Call {
 template <bool HALF, bool FIRST>
 __device__ __forceinline__ void mma(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
 #define ATLAS_MMA(T, C, ...)                                                                                            \
-  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32." T "." T ".f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, " C ";" \
+  asm("mma.sync.aligned.m16n8k16.row.col.f32." T "." T ".f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, " C ";" \
                : __VA_ARGS__                                                                                            \
                : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f))
   if constexpr (FIRST) {
@@ -133,12 +133,6 @@ __device__ __forceinline__ void load_bytes(uint32_t dst, const void* src, uint32
                "l"(__cvta_generic_to_global(src)), "r"(bytes), "r"(bar)
                : "memory");
 }
-__device__ __forceinline__ uint4 lds128(uint32_t addr) {
-  uint4 v;
-  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
-  return v;
-}
-
 template <int X, int MT, int WK>
 struct Stage {   // bytes: WK blocks of weights, then WK pieces of x
   static constexpr int x = X == X_ROWS ? 8 * kRowBytes : planes_of(X) * MT * 2048;
@@ -268,7 +262,8 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(MT)) k_qlinear(Call c,
       }
       if (!(ok = __all_sync(0xffffffffu, tc::wait(full + 8 * p.stage, p.parity)))) break;
       if (live) {
-        const uint32_t at = base + p.stage * stage_bytes;
+        // (plain loads and products: the compiler may move them, so that the next ones are in flight)
+        const uint8_t* at = sm + p.stage * stage_bytes;
         Offset off[NT][2];
 #pragma unroll
         for (int n = 0; n < NT; ++n) off[n][0] = off[n][1] = offset_of<HALF>(8);
@@ -279,16 +274,15 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(MT)) k_qlinear(Call c,
 #pragma unroll
           for (int m = 0; m < MT; ++m)
 #pragma unroll
-            for (int q = 0; q < PLANES; ++q) x[m][q] = lds128(at + x_at + (X == X_ROWS ? 64 * i : ((q * MT + m) * 4 + i) * 512));
+            for (int q = 0; q < PLANES; ++q) x[m][q] = *reinterpret_cast<const uint4*>(at + x_at + (X == X_ROWS ? 64 * i : ((q * MT + m) * 4 + i) * 512));
           if (i % 2 == 0)
 #pragma unroll
-            for (int n = 0; n < NT; ++n) w[n] = lds128(at + w_lane + n * 1024 + i * 256);
+            for (int n = 0; n < NT; ++n) w[n] = *reinterpret_cast<const uint4*>(at + w_lane + n * 1024 + i * 256);
           constexpr int kHalves = 4 / GROUPS;   // 32 of K, of a group
           if (i % kHalves == 0 && s.zeros) {
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-              uint32_t v;
-              asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(at + z_lane + i / kHalves * 64 + n * 8));
+              const uint32_t v = at[z_lane + i / kHalves * 64 + n * 8];
               off[n][0] = offset_of<HALF>(v & 15u);
               off[n][1] = offset_of<HALF>(v >> 4);
             }
@@ -312,8 +306,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(MT)) k_qlinear(Call c,
           if ((i + 1) % kHalves == 0) {   // a group ends
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-              uint32_t v;
-              asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(at + s_lane + i / kHalves * 256 + n * 32));
+              const uint32_t v = *reinterpret_cast<const uint32_t*>(at + s_lane + i / kHalves * 256 + n * 32);
               const float scale[2] = {__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u)};
 #pragma unroll
               for (int m = 0; m < MT; ++m)

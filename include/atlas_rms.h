@@ -18,9 +18,8 @@
  *
  * Execution: asynchronous on the given CUDA stream, one kernel, no workspace.
  * The sum and y are fp32 and come from the sum x + residual before it is
- * rounded to h; h and y are rounded once.  Squares are summed in fp32: a row with
- * |h| of 1e19 or more gives zeros.  A NaN makes its row of y (and its scales)
- * NaN, an infinity a NaN in its own place (in 8 bits: in its run, and the run's
+ * rounded to h; h and y are rounded once.  A NaN makes its row of y (and its
+ * scales) NaN, an infinity a NaN in its own place (in 8 bits: in its run, and the run's
  * scale) and zeros in the others; no other row is touched.  Calls are made on one
  * device, which holds their tensors and is the current one.  Calls may be captured
  * in a CUDA graph.

@@ -417,3 +417,19 @@ def test_graph_behind_a_larger_call(gpu_lib):
     torch.cuda.synchronize()
     assert torch.equal(out["y"], ref)
     _q4_check(w, t, out["y"], 200, 128, "none", 0, "f32")
+
+
+@pytest.mark.parametrize("C", [512, 515, 2560, 16384])
+@pytest.mark.parametrize("y", ["f32", "e4m3"])
+def test_rms_rows_whose_squares_leave_the_range(gpu_lib, C, y):
+    """Values to the largest of fp32, beside ordinary rows: the sum of squares does not overflow."""
+    import torch
+    from test_learned_neural_gb300.runner import RmsNorm
+    t = _rms_case(6, C, x="f32", r=None)
+    x = t["x"]
+    x[1] *= 1e18
+    x[2] *= 3e30
+    x[3, 3] = 3e38
+    x[4, C - 1] = -2e19
+    block = 128 if y == "e4m3" else 0
+    _rms_check(t, RmsNorm(C, x_dtype="f32", y_dtype=y, block=block).forward(t), "f32", None, y, block)

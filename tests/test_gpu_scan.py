@@ -257,3 +257,48 @@ def test_scan_takes_the_stage_in_fronts_outputs(gpu_lib):
                                    conv_w=n(cfg.Nc, 4).cuda(), gate_b=n(3, H).cuda()))
     t = {m: p[m] for m in ("q", "k", "v", "theta", "alpha")}
     _check(t, H, d, d, "bf16", "bf16")
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.25])
+@pytest.mark.parametrize("dtype,y_dtype,dk,T", [("bf16", "bf16", 64, 300), ("bf16", "f32", 64, 300), ("bf16", "bf16", 128, 300),
+                                                ("bf16", "f32", 128, 300), ("f32", "f32", 48, 300), ("bf16", "f32", 64, 2)])
+def test_scan_scale_is_not_of_the_skip_term(gpu_lib, scale, dtype, y_dtype, dk, T):
+    """A factor of 0 leaves D v; a negative one turns the read-outs alone."""
+    t = _inputs(2, 2, T, dk, 64, dtype, "step", skip=True, seed=3)
+    _check(t, 2, dk, 64, dtype, y_dtype, scale=scale)
+
+
+def test_scan_steps_that_vanish_or_saturate(gpu_lib):
+    """dt of -inf (a token that is left out), of 80 and of 1e4 with A = 0 and A far below 0."""
+    import torch
+    for T, dtype in ((4, "f32"), (300, "bf16"), (300, "f32")):
+        t = _inputs(1, 3, T, 64, 32, dtype, "step", seed=4)
+        t["dt_bias"].zero_()
+        t["A"].copy_(torch.tensor([0.0, -1.0, -1e30]))
+        t["dt"][0, :, 1::3] = -float("inf")
+        t["dt"][0, 1, 2::7] = 80.0
+        t["dt"][0, 2, 2::11] = 1e4
+        y, S = _ref(t)
+        out = _op(t, 3, 64, 32, dtype, "f32").forward(t)
+        for h in range(3):
+            assert maxrel(_host(out["y"])[:, h], y[:, h]) <= 1e-5 and maxrel(_host(out["S"])[:, h], S[:, h]) <= 1e-5, (T, dtype, h)
+
+
+def test_scans_of_two_handles_on_two_streams_at_once(gpu_lib):
+    import torch
+    calls = []
+    for i, (dk, T) in enumerate(((64, 900), (128, 700))):
+        t = _inputs(2, 4, T, dk, 64, "bf16", skip=True, seed=6 + i)
+        op = _op(t, 4, dk, 64, "bf16", "f32")
+        calls.append((op, t, {n: a.clone() for n, a in op.forward(t).items()}, torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    outs = [[], []]
+    for _ in range(10):
+        for i, (op, t, _, st) in enumerate(calls):
+            with torch.cuda.stream(st):
+                outs[i].append(op.forward(t))
+    torch.cuda.synchronize()
+    for (op, _, ref, _), many in zip(calls, outs):
+        op.status()
+        for out in many:
+            assert all(torch.equal(out[n], ref[n]) for n in ref)

@@ -433,3 +433,39 @@ def test_rms_rows_whose_squares_leave_the_range(gpu_lib, C, y):
     x[4, C - 1] = -2e19
     block = 128 if y == "e4m3" else 0
     _rms_check(t, RmsNorm(C, x_dtype="f32", y_dtype=y, block=block).forward(t), "f32", None, y, block)
+
+
+@pytest.mark.parametrize("C", [96, 2048, 333])
+def test_rms_sum_in_place_of_x(gpu_lib, C):
+    """h written over x, the residual left alone."""
+    import torch
+    from test_learned_neural_gb300.runner import RmsNorm
+    t = _rms_case(7, C, x="bf16", r="bf16")
+    op = RmsNorm(C)
+    ref = {n: a.clone() for n, a in op.forward(t).items()}
+    kept = t["residual"].clone()
+    out = op.forward(t, out=dict(y=torch.empty_like(ref["y"]), h=t["x"]))
+    assert torch.equal(out["y"], ref["y"]) and torch.equal(t["x"], ref["h"]) and torch.equal(t["residual"], kept)
+
+
+def test_products_of_two_handles_on_two_streams_at_once(gpu_lib):
+    """Each with its own fragments of x in its own workspace."""
+    import torch
+    from test_learned_neural_gb300.runner import QuantLinear
+    calls = []
+    for K, N, M in ((1024, 512, 40), (768, 1024, 33)):
+        op = QuantLinear(K, N, 64)
+        g = torch.Generator().manual_seed(K)
+        W = op.quantize((torch.randn(K, N, generator=g) / K ** 0.5).cuda())
+        t = dict(x=torch.randn(M, K, generator=g).bfloat16().cuda(), W=op.pack(**W))
+        calls.append((op, t, op.forward(t)["y"].clone(), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    outs = [[], []]
+    for _ in range(20):
+        for i, (op, t, _, st) in enumerate(calls):
+            with torch.cuda.stream(st):
+                outs[i].append(op.forward(t)["y"])
+    torch.cuda.synchronize()
+    for (op, _, ref, _), many in zip(calls, outs):
+        op.status()
+        assert all(torch.equal(y, ref) for y in many)

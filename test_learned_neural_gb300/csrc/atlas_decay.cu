@@ -1,6 +1,6 @@
-// Linear attention with a decay for each head, and the selective scan (its GATED
-// instances): host side, and the kernels that run in fp32 arithmetic
-// (decay_common.cuh has the formulas).
+// Linear attention with a decay for each head, and the selective scan (GATED
+// instances): host side, the token-by-token form, the segments' starts, and the
+// decay attention's chunks in fp32 arithmetic (decay_common.cuh has the formulas).
 #include <math.h>
 
 #include <algorithm>
@@ -126,10 +126,7 @@ __global__ void __launch_bounds__(256) k_decay_step(Geom g, Ptrs p) {
 // contribution to the next segment's start.  Bound by the latency of its fp32
 // loops where blocks are few (chunk_blocks has how many an SM holds): 3 rows x 6 heads of ragged
 // lengths to 1501, d 48: 41 us in three overlapped launches (states 15, scan 8, read-outs 32).
-// GATED: pw holds the tokens' products (decay_common.cuh) in place of powers, which
-// a warp for each run forms; those of a run's own tokens are formed by each row's
-// threads from the decays.
-template <typename TI, typename TO, int C, bool READ, bool GATED>
+template <typename TI, typename TO, int C, bool READ>
 __global__ void __launch_bounds__(256, C == 64 ? 3 : 1) k_decay_chunk(Geom g, Ptrs p) {
   extern __shared__ float sm[];
   const int dk4 = (g.d_k + 3) & ~3, ldk = dk4 + 4;
@@ -137,8 +134,8 @@ __global__ void __launch_bounds__(256, C == 64 ? 3 : 1) k_decay_chunk(Geom g, Pt
   float* Ks = sm;                   // [C][ldk]
   float* Vs = Ks + C * ldk;         // [C][LDV]
   float* Ss = Vs + C * LDV;         // [dk4][LDV]
-  float* pw = Ss + dk4 * LDV;       // g^0 .. g^C, padded to a multiple of 4; GATED: g, s, L, R of C tokens
-  float* Qs = pw + (GATED ? 4 * C : C + 4);   // [C][ldk]
+  float* pw = Ss + dk4 * LDV;       // g^0 .. g^C, padded to a multiple of 4
+  float* Qs = pw + C + 4;           // [C][ldk]
   float* Ps = Qs + C * ldk;         // [C][LDP]
   const int s = blockIdx.x, sl = blockIdx.y, unit = blockIdx.z;
   const int b = unit / g.H, h = unit % g.H, tid = threadIdx.x, tx = tid % 16, ty = tid / 16;
@@ -146,9 +143,7 @@ __global__ void __launch_bounds__(256, C == 64 ? 3 : 1) k_decay_chunk(Geom g, Pt
   tc::grid_dependents_launch();
   const int live = decay::live_tokens(g, p, b);
   const int t_lo = s * g.seg, t_hi = min(g.T, t_lo + g.seg), t_live = min(t_hi, max(live, t_lo));
-  float l2g = 0.f, seg_total = 1.f, skip = 0.f;
-  if constexpr (!GATED) l2g = log2f(p.decay[h]);
-  else if (p.D) skip = p.D[h];
+  const float l2g = log2f(p.decay[h]);
   const int c0 = sl * kSlice, cols = min(kSlice, g.d_v - c0);
   const TI* q = (const TI*)p.q + b * g.qk_b + (h / g.share) * g.qk_h;
   const TI* k = (const TI*)p.k + b * g.qk_b + (h / g.share) * g.qk_h;
@@ -161,15 +156,10 @@ __global__ void __launch_bounds__(256, C == 64 ? 3 : 1) k_decay_chunk(Geom g, Pt
     const int r = i / kSlice, c = i % kSlice;
     Ss[r * LDV + c] = start && r < g.d_k && c < cols ? start[(size_t)r * g.d_v + c0 + c] : 0.f;
   }
-  if constexpr (!GATED)
-    for (int i = tid; i <= C; i += 256) pw[i] = decay::power(l2g, i);
-  const decay::HeadGates head(GATED ? p.gates : Gates{nullptr, p.decay}, h);
-  decay::RawGates ahead;   // of this thread's token of the next chunk
-  if (GATED && tid < C && t_lo + tid < t_live) ahead.load(p.gates, b, h, t_lo + tid);
+  for (int i = tid; i <= C; i += 256) pw[i] = decay::power(l2g, i);
 
   // four values at a time where every row starts on their boundary
-  const bool vec = g.d_k % 4 == 0 && g.d_v % 4 == 0 && (g.qk_t | g.v_t) % 4 == 0 &&
-                   ((uintptr_t)p.q | (uintptr_t)p.k | (uintptr_t)p.v) % 16 == 0;
+  const bool vec = g.d_k % 4 == 0 && g.d_v % 4 == 0 && ((uintptr_t)p.q | (uintptr_t)p.k | (uintptr_t)p.v) % 16 == 0;
   const bool y_vec = (uintptr_t)p.y % 16 == 0;
   for (int t0 = t_lo; t0 < t_live; t0 += C) {
     const int n = min(C, t_live - t0);
@@ -196,17 +186,7 @@ __global__ void __launch_bounds__(256, C == 64 ? 3 : 1) k_decay_chunk(Geom g, Pt
       }
       load4(v + (size_t)(t0 + r) * g.v_t, 4 * tx, cols, r < n, Vs + r * LDV);
     }
-    if (GATED && tid < C) {   // whole warps
-      float d = 1.f, s = 0.f, L, R;
-      if (tid < n) ahead.values(p.gates, head.bias, head.A, d, s);
-      decay::run_products(d, s, L, R);
-      pw[tid] = d, pw[C + tid] = s, pw[2 * C + tid] = L, pw[3 * C + tid] = R;
-      if (t0 + C + tid < t_live) ahead.load(p.gates, b, h, t0 + C + tid);
-    }
     __syncthreads();
-    // GATED: the arrays, and the product of g over a run
-    const float *gs = pw, *ss = pw + C, *Ls = pw + 2 * C, *Rs = pw + 3 * C;
-    const float run0 = GATED ? Ls[decay::kRun - 1] : 1.f, run1 = GATED && C == 64 ? Ls[C - 1] : 1.f;
     if constexpr (READ) {
       // P = (Q K^T) under the decay mask
       float a[NI][NI] = {};
@@ -228,30 +208,9 @@ __global__ void __launch_bounds__(256, C == 64 ? 3 : 1) k_decay_chunk(Geom g, Pt
 #pragma unroll
         for (int j = 0; j < NI; ++j) {
           const int ri = ty + 16 * i, cj = tx + 16 * j;
-          if constexpr (!GATED) {
-            Ps[ri * LDP + cj] = cj <= ri ? a[i][j] * pw[ri - cj] : 0.f;
-          } else {
-            const float w = cj / decay::kRun < ri / decay::kRun ? Ls[ri] * Rs[cj] : 1.f;   // (C = 64: the run before)
-            Ps[ri * LDP + cj] = cj <= ri ? a[i][j] * w : 0.f;
-          }
+          Ps[ri * LDP + cj] = cj <= ri ? a[i][j] * pw[ri - cj] : 0.f;
         }
       __syncthreads();
-      if constexpr (GATED) {
-        // a row's own run, eight columns a thread: times s_j and the decays between
-        const int r = tid / 4, lr = r % decay::kRun, lo = 8 * (tid % 4);
-        if (r < C && lo <= lr) {
-          float* row = Ps + r * LDP + r - lr;
-          const float *gr = gs + r - lr, *sr = ss + r - lr;
-          const int hi = min(lr, lo + 7);
-          float w = 1.f;
-          for (int m = lr; m > hi; --m) w *= gr[m];
-          for (int c = hi; c >= lo; --c) {
-            row[c] *= w * sr[c];
-            w *= gr[c];
-          }
-        }
-        __syncthreads();
-      }
       float o[NI][4] = {};
       for (int kk = 0; kk < dk4; kk += 4) {
         float4 sv[4];
@@ -269,10 +228,7 @@ __global__ void __launch_bounds__(256, C == 64 ? 3 : 1) k_decay_chunk(Geom g, Pt
 #pragma unroll
       for (int i = 0; i < NI; ++i)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int r = ty + 16 * i;
-          o[i][e] *= GATED ? (r < decay::kRun ? 1.f : run0) * Ls[r] : pw[r + 1];
-        }
+        for (int e = 0; e < 4; ++e) o[i][e] *= pw[ty + 16 * i + 1];
       for (int j = 0; j < C; j += 4) {
         float4 vv[4];
 #pragma unroll
@@ -291,10 +247,7 @@ __global__ void __launch_bounds__(256, C == 64 ? 3 : 1) k_decay_chunk(Geom g, Pt
         const int r = ty + 16 * i;
         if (r >= n) continue;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          o[i][e] *= g.scale;
-          if (GATED && p.D) o[i][e] = fmaf(skip, Vs[r * LDV + 4 * tx + e], o[i][e]);
-        }
+        for (int e = 0; e < 4; ++e) o[i][e] *= g.scale;
         TO* dst = y + (t0 + r) * g.y_t + 4 * tx;
         if (vec && y_vec && 4 * tx + 4 <= cols) {
           store_vec<4>(dst, o[i]);
@@ -307,16 +260,14 @@ __global__ void __launch_bounds__(256, C == 64 ? 3 : 1) k_decay_chunk(Geom g, Pt
       __syncthreads();   // every read of the state is done
     }
     // S = g^n S + sum_j g^{n-1-j} k_j v_j
-    const float all = GATED ? run0 * run1 : pw[n];
-    if constexpr (GATED) seg_total *= all;
     for (int r0 = 4 * ty; r0 < dk4; r0 += 64) {
       float a[4][4];
 #pragma unroll
       for (int r = 0; r < 4; ++r)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) a[r][e] = all * Ss[(r0 + r) * LDV + 4 * tx + e];
+        for (int e = 0; e < 4; ++e) a[r][e] = pw[n] * Ss[(r0 + r) * LDV + 4 * tx + e];
       for (int j = 0; j < n; ++j) {
-        const float w = GATED ? Rs[j] * (j < decay::kRun ? run1 : 1.f) : pw[n - 1 - j];
+        const float w = pw[n - 1 - j];
         const float4 kr = *reinterpret_cast<const float4*>(Ks + j * ldk + r0);
         const float4 vv = *reinterpret_cast<const float4*>(Vs + j * LDV + 4 * tx);
         const float kw[4] = {kr.x * w, kr.y * w, kr.z * w, kr.w * w}, vc[4] = {vv.x, vv.y, vv.z, vv.w};
@@ -340,7 +291,6 @@ __global__ void __launch_bounds__(256, C == 64 ? 3 : 1) k_decay_chunk(Geom g, Pt
     if (s == g.nseg - 1 && p.S_out) dst = p.S_out + unit * sq;
   } else {
     dst = p.seg + ((size_t)unit * g.nseg + s + 1) * sq;
-    if (GATED && sl == 0 && tid == 0) p.seg_total[(size_t)unit * g.nseg + s] = seg_total;
   }
   if (dst)
     for (int i = tid; i < g.d_k * kSlice; i += 256) {
@@ -426,9 +376,9 @@ cudaError_t launch_rows(const void* src, void* dst, size_t rows, int from, int t
 
 size_t step_smem(const Geom& g, int V) { return (size_t)(2 * g.d_k + 256 / (kSlice / V) * kSlice) * sizeof(float); }
 int chunk_tokens(int d_k) { return d_k <= 128 ? 64 : 32; }
-size_t chunk_smem(int d_k, bool read, bool gated) {
+size_t chunk_smem(int d_k, bool read) {
   const size_t dk4 = (d_k + 3) & ~3, C = chunk_tokens(d_k), ldk = dk4 + 4, ldv = kSlice + 4;
-  return (C * ldk + C * ldv + dk4 * ldv + (gated ? 4 * C : C + 4) + (read ? C * ldk + C * (C + 4) : 0)) * sizeof(float);
+  return (C * ldk + C * ldv + dk4 * ldv + C + 4 + (read ? C * ldk + C * (C + 4) : 0)) * sizeof(float);
 }
 
 // Blocks of the fp32 chunks that an SM holds: by their shared memory (228 KB an
@@ -440,8 +390,9 @@ size_t chunk_smem(int d_k, bool read, bool gated) {
 // 96 645 / 724; of 48 and 128 the same; 3 x 6 x 1501 of 64 75 / 71 (12 segments and
 // 24 cost the same by the formula).
 int chunk_blocks(int d_k, bool read, bool gated) {
-  const size_t fit = (228 * 1024) / (chunk_smem(d_k, read, gated) + 1024);
-  return (int)std::min<size_t>(chunk_tokens(d_k) == 64 ? 3 : 2, fit);
+  const size_t fit = (228 * 1024) / ((gated ? decay::split_smem(d_k, read) : chunk_smem(d_k, read)) + 1024);
+  const size_t by_registers = gated ? decay::split_blocks(d_k, read) : chunk_tokens(d_k) == 64 ? 3 : 2;
+  return (int)std::min(by_registers, fit);
 }
 
 struct Plan {
@@ -508,7 +459,7 @@ Plan make_plan(const atlas_decay_config& c, int B, int T, bool aligned, bool gat
   const bool tc = c.qkv_dtype == ATLAS_BF16 && c.d_k <= 128;
   pl.pad = tc && (!aligned || c.d_k % 8 || c.d_v % 8);
   pl.path = tc ? 2 : 1;
-  pl.C = tc ? decay::kTcChunk : chunk_tokens(c.d_k);
+  pl.C = tc ? decay::kTcChunk : gated ? decay::split_tokens(c.d_k) : chunk_tokens(c.d_k);
   // CTAs that run at once; a fp32 chunk takes so long that starts hardly count
   // (twice as many in a selective scan's ragged batch: half of the segments lie past their rows' lengths,
   // as a rule, and end at once; 2 x 16 rows and heads of 0 and 8192 tokens, 128 x 64: 4 segments 143 us, 8 108)
@@ -615,30 +566,29 @@ cudaError_t decay::scan_launch(const Geom& g, const Ptrs& p, cudaStream_t st) {
 
 namespace {
 
-template <typename TI, typename TO, int C, bool GATED>
+template <typename TI, typename TO, int C>
 cudaError_t launch_chunks(const Geom& g, const Ptrs& p, cudaStream_t st) {
   const unsigned units = (unsigned)(g.B * g.H);
   if (g.nseg > 1) {
-    cudaError_t e = launch_big(k_decay_chunk<TI, TO, C, false, GATED>, dim3(g.nseg - 1, g.slices, units),
-                               chunk_smem(g.d_k, false, GATED), g, p, st);
+    cudaError_t e = launch_big(k_decay_chunk<TI, TO, C, false>, dim3(g.nseg - 1, g.slices, units),
+                               chunk_smem(g.d_k, false), g, p, st);
     if (e != cudaSuccess) return e;
     e = decay::scan_launch(g, p, st);
     if (e != cudaSuccess) return e;
   }
-  return launch_big(k_decay_chunk<TI, TO, C, true, GATED>, dim3(g.nseg, g.slices, units), chunk_smem(g.d_k, true, GATED), g, p,
-                    st);
+  return launch_big(k_decay_chunk<TI, TO, C, true>, dim3(g.nseg, g.slices, units), chunk_smem(g.d_k, true), g, p, st);
 }
 
-template <typename TI, typename TO, bool GATED>
+template <typename TI, typename TO>
 cudaError_t launch(const Plan& pl, const Geom& g, const Ptrs& p, cudaStream_t st) {
-  if (pl.path == 0) return launch_step<TI, TO, GATED>(g, p, st);
-  return pl.C == 64 ? launch_chunks<TI, TO, 64, GATED>(g, p, st) : launch_chunks<TI, TO, 32, GATED>(g, p, st);
+  if (pl.path == 0) return p.gated ? launch_step<TI, TO, true>(g, p, st) : launch_step<TI, TO, false>(g, p, st);
+  if (p.gated) return decay::split_launch(g, p, sizeof(TI) == 2, sizeof(TO) == 2, st);
+  return pl.C == 64 ? launch_chunks<TI, TO, 64>(g, p, st) : launch_chunks<TI, TO, 32>(g, p, st);
 }
-template <bool GATED>
 cudaError_t launch_types(const Plan& pl, const atlas_decay_config& c, const Geom& g, const Ptrs& p, cudaStream_t st) {
   const bool ib = c.qkv_dtype == ATLAS_BF16, ob = c.y_dtype == ATLAS_BF16;
-  return ib ? (ob ? launch<bf16, bf16, GATED>(pl, g, p, st) : launch<bf16, float, GATED>(pl, g, p, st))
-            : (ob ? launch<float, bf16, GATED>(pl, g, p, st) : launch<float, float, GATED>(pl, g, p, st));
+  return ib ? (ob ? launch<bf16, bf16>(pl, g, p, st) : launch<bf16, float>(pl, g, p, st))
+            : (ob ? launch<float, bf16>(pl, g, p, st) : launch<float, float>(pl, g, p, st));
 }
 
 }  // namespace
@@ -717,7 +667,7 @@ int decay::run(HandleBase* h, const atlas_decay_config& c, const atlas_decay_io&
   }
   const bool ob = c.y_dtype == ATLAS_BF16;
   cudaError_t e = pl.path == 2 ? decay::tc_launch(g, p, ob, h->status, st)
-                               : x ? launch_types<true>(pl, c, g, p, st) : launch_types<false>(pl, c, g, p, st);
+                               : launch_types(pl, c, g, p, st);
   if (e == cudaSuccess && pl.pad)
     e = ob ? launch_rows<bf16>(p.y, io.y, rows * c.H, g.dv_row, c.d_v, st)
            : launch_rows<float>(p.y, io.y, rows * c.H, g.dv_row, c.d_v, st);

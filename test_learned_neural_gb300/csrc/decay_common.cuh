@@ -80,16 +80,18 @@ struct HeadGates {
   }
 };
 // A run's products, by a warp, lane by lane: L, and R = s times the product behind
+// (RUN = 8: of four runs of 8)
+template <int RUN = kRun>
 __device__ __forceinline__ void run_products(float decay, float step, float& L, float& R) {
-  const int lane = threadIdx.x % 32;
+  const int lane = threadIdx.x % RUN;
   float behind = __shfl_down_sync(0xffffffffu, decay, 1);
   L = decay;
-  if (lane == 31) behind = 1.f;
+  if (lane == RUN - 1) behind = 1.f;
 #pragma unroll
-  for (int e = 1; e < 32; e *= 2) {
+  for (int e = 1; e < RUN; e *= 2) {
     const float x = __shfl_up_sync(0xffffffffu, L, e), y = __shfl_down_sync(0xffffffffu, behind, e);
     if (lane >= e) L *= x;
-    if (lane + e < 32) behind *= y;
+    if (lane + e < RUN) behind *= y;
   }
   R = step * behind;
 }

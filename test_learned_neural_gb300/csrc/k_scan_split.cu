@@ -1,0 +1,382 @@
+// Selective scan in chunks from fp32 q, k, v, and from bf16 ones with d_k > 128
+// (decay_common.cuh has the formulas): the products run on the tensor cores from
+// split operands.
+//
+// A value is the sum of its leading 11 bits and the next 11, both tf32 (mma.sync
+// takes those from registers); a product of two values is three products, the small
+// ones first, and what is left out is below 2^-20 of it.  bf16 values are one part.
+// The fp32 pipes give 116 multiply-adds a clock of an SM, the tensor cores 497 of tf32, so
+// 166 of these, and a fragment feeds more of them: the fp32 loops in front of
+// this (the decay attention's) reach a third of their pipes.
+//
+// One CTA: (segment, 64 columns of d_v, unit), chunks of C tokens in order.  Eight
+// warps in C / 16 row groups share the columns of the chunk's products; for the
+// state a warp holds rows 16 (w % 4 + 4 i) .. and 32 columns, in registers for the
+// whole segment (a copy in shared memory is the operand of Q S).  Row strides of
+// the tiles are 8 or 24 words (mod 32) where fragments lie along the row in pairs,
+// 4 where they lie across it, so that no load meets a bank twice.
+// READ: form the read-outs from the segment-start state; else only the segment's own
+// contribution to the next segment's start.
+#include <type_traits>
+
+#include "decay_common.cuh"
+#include "decay_tc.cuh"
+#include "tc2.cuh"
+
+using namespace layer;
+using decay::Geom;
+using decay::Ptrs;
+
+namespace {
+
+constexpr int SL = 64, LDV = SL + 8, LDS = SL + 4;
+
+__host__ __device__ constexpr int rows_of(int d_k) { return (d_k + 15) & ~15; }   // d_k in whole 16-row tiles
+
+// value = hi + lo; ONE: a bf16 value, hi alone
+template <bool ONE>
+struct Part {
+  uint32_t hi, lo;
+  __device__ __forceinline__ Part() {}
+  __device__ __forceinline__ Part(float x) {
+    hi = __float_as_uint(x);
+    if constexpr (!ONE) {
+      hi &= 0xffffe000u;
+      lo = __float_as_uint(x - __uint_as_float(hi)) & 0xffffe000u;
+    }
+  }
+};
+__device__ __forceinline__ void mma8(float* d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// d[n] += a b[n], N tiles of 16 x 8 with 8 of the inner axis
+template <int N, bool A1, bool B1>
+__device__ __forceinline__ void products(float (*d)[4], const Part<A1>* a, const Part<B1> (*b)[2], int n_on) {
+  if constexpr (!A1) {
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+      if (n < n_on) mma8(d[n], a[0].lo, a[1].lo, a[2].lo, a[3].lo, b[n][0].hi, b[n][1].hi);
+  }
+  if constexpr (!B1) {
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+      if (n < n_on) mma8(d[n], a[0].hi, a[1].hi, a[2].hi, a[3].hi, b[n][0].lo, b[n][1].lo);
+  }
+#pragma unroll
+  for (int n = 0; n < N; ++n)
+    if (n < n_on) mma8(d[n], a[0].hi, a[1].hi, a[2].hi, a[3].hi, b[n][0].hi, b[n][1].hi);
+}
+
+// Tiles, in words from the start of shared memory.  K twice and for the state pass V
+// as well, so that the next chunk's copies run under this one's products; else V
+// arrives under the scores, and Q when they are done.
+template <int C, bool READ>
+struct Tiles {
+  int k, v, gates, s, q, p, end;   // k: C ldk apart
+  __host__ __device__ Tiles(int d_k) {
+    const int dk16 = rows_of(d_k), ldk = dk16 + 8;
+    k = 0;
+    v = 2 * C * ldk;
+    gates = v + (READ ? 1 : 2) * C * LDV;
+    s = gates + 6 * C;
+    q = s + (READ ? dk16 * LDS : 0);
+    p = q + (READ ? C * ldk : 0);
+    end = p + (READ ? C * (C + 4) : 0);
+  }
+};
+
+// MI: 16-row tiles of the state a warp (d_k <= 64 MI)
+template <typename TI, typename TO, int C, int MI, bool READ>
+__global__ void __launch_bounds__(256, MI <= 2 ? 2 : 1) k_scan_split(Geom g, Ptrs p) {
+  constexpr bool ONE = sizeof(TI) == 2;
+  constexpr int LDP = C + 4, MT = C / 16, NG = 8 / MT, NQ = C / 8 / NG, NO = SL / 8 / NG;
+  extern __shared__ __align__(16) float sm[];
+  const Tiles<C, READ> at(g.d_k);
+  const int dk16 = rows_of(g.d_k), ldk = dk16 + 8;
+  // of C tokens: g, s; products to and behind a token in its run of 32 (L, R) and in its run of 8
+  float* const gates = sm + at.gates;
+  const float *gs = gates, *ss = gates + C, *Ls = gates + 2 * C, *Rs = gates + 3 * C, *L8 = gates + 4 * C, *R8 = gates + 5 * C;
+  float *const Ss = sm + at.s, *const Ps = sm + at.p;
+  const int s = blockIdx.x, sl = blockIdx.y, unit = blockIdx.z;
+  const int b = unit / g.H, h = unit % g.H, tid = threadIdx.x, warp = tid / 32, q8 = tid % 32 / 4, t4 = tid % 4;
+  tc::grid_dependency_wait();
+  tc::grid_dependents_launch();
+  const int live = decay::live_tokens(g, p, b);
+  const int t_lo = s * g.seg, t_hi = min(g.T, t_lo + g.seg), t_live = min(t_hi, max(live, t_lo));
+  const float skip = p.D ? p.D[h] : 0.f;
+  float seg_total = 1.f;
+  const int c0 = sl * SL, cols = min(SL, g.d_v - c0);
+  const TI* q = (const TI*)p.q + b * g.qk_b + (h / g.share) * g.qk_h;
+  const TI* k = (const TI*)p.k + b * g.qk_b + (h / g.share) * g.qk_h;
+  const TI* v = (const TI*)p.v + b * g.v_b + h * g.v_h + c0;
+  TO* y = (TO*)p.y + b * g.y_b + h * g.y_h + c0;
+  const size_t sq = (size_t)g.d_k * g.d_v;
+
+  // A tile's C rows, 16 threads side by side per token, four values each; zeros past
+  // the row's length and width.  fp32 rows that start on four values go by copies
+  // that this thread waits for later (copies_left), others are there at once.
+  const bool vec = g.d_k % 4 == 0 && g.d_v % 4 == 0 && (g.qk_t | g.v_t) % 4 == 0 &&
+                   ((uintptr_t)p.q | (uintptr_t)p.k | (uintptr_t)p.v) % 16 == 0;
+  auto fetch = [&](const TI* src, size_t stride, int t0, int width, int padded, float* dst, int ld) {
+    const int tx = tid % 16, ty = tid / 16, n = min(C, t_live - t0);
+    if (n > 0) {
+#pragma unroll
+      for (int i = 0; i < C / 16; ++i) {
+        const int r = ty + 16 * i;
+        const TI* row = src + (t0 + r) * stride;
+        for (int c = 4 * tx; c < padded; c += 64) {
+          float* to = dst + r * ld + c;
+          const bool in = r < n && c < width;
+          if (sizeof(TI) == 4 && vec) {
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(tc::smem_u32(to)), "l"(in ? row + c : src), "r"(in ? 16 : 0)
+                         : "memory");
+            continue;
+          }
+          float x[4] = {0.f, 0.f, 0.f, 0.f};
+          if (in && vec) {
+            load_vec<4>(row + c, x);
+          } else if (in) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (c + e < width) x[e] = to_f32(row[c + e]);
+          }
+          *reinterpret_cast<float4*>(to) = make_float4(x[0], x[1], x[2], x[3]);
+        }
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  auto copies_left = [](auto n) { asm volatile("cp.async.wait_group %0;" ::"n"(decltype(n)::value) : "memory"); };
+  auto k_tile = [&](int c) { return sm + at.k + (c & 1) * C * ldk; };
+  auto v_tile = [&](int c) { return sm + at.v + (READ ? 0 : (c & 1) * C * LDV); };
+  auto fetch_k = [&](int c) { fetch(k, g.qk_t, t_lo + c * C, g.d_k, dk16, k_tile(c), ldk); };
+  auto fetch_q = [&](int c) { fetch(q, g.qk_t, t_lo + c * C, g.d_k, dk16, sm + at.q, ldk); };
+  auto fetch_v = [&](int c) { fetch(v, g.v_t, t_lo + c * C, cols, SL, v_tile(c), LDV); };
+  fetch_k(0);
+  if constexpr (READ) fetch_q(0);
+  else fetch_v(0);
+
+  // the state: rows 16 (warp % 4 + 4 i) + q8 (+ 8), columns 32 (warp / 4) + 8 n + 2 t4 (+ 1)
+  const int srow = 16 * (warp % 4), scol = 32 * (warp / 4);
+  float st[MI][4][4] = {};
+  auto each_state = [&](auto f) {   // f(value, row, column)
+#pragma unroll
+    for (int i = 0; i < MI; ++i)
+#pragma unroll
+      for (int n = 0; n < 4; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) f(st[i][n][e], srow + 64 * i + q8 + 8 * (e / 2), scol + 8 * n + 2 * t4 + e % 2);
+  };
+  auto publish = [&] { each_state([&](float& x, int r, int c) { if (r < dk16) Ss[r * LDS + c] = x; }); };
+  const decay::HeadGates head(p.gates, h);
+  decay::RawGates ahead;   // of this thread's token of the next chunk
+  if (tid < C && t_lo + tid < t_live) ahead.load(p.gates, b, h, t_lo + tid);
+  if constexpr (READ) {
+    const float* start = g.nseg > 1 ? p.seg + ((size_t)unit * g.nseg + s) * sq : p.S0 ? p.S0 + unit * sq : nullptr;
+    if (start)
+      each_state([&](float& x, int r, int c) { x = r < g.d_k && c < cols ? start[(size_t)r * g.d_v + c0 + c] : 0.f; });
+    publish();
+  }
+
+  const bool pairs = g.d_v % 2 == 0 && (uintptr_t)p.y % 8 == 0;   // (y's strides are multiples of d_v)
+  for (int c = 0, t0 = t_lo; t0 < t_live; ++c, t0 += C) {
+    const int n = min(C, t_live - t0);
+    __syncthreads();   // the last chunk's products are done, the state is in Ss
+    if constexpr (READ) fetch_v(c);
+    fetch_k(c + 1);
+    if constexpr (!READ) fetch_v(c + 1);
+    if (tid < C) {   // whole warps
+      float d = 1.f, w = 0.f, L, R;
+      if (tid < n) ahead.values(p.gates, head.bias, head.A, d, w);
+      gates[tid] = d, gates[C + tid] = w;
+      decay::run_products(d, w, L, R);
+      gates[2 * C + tid] = L, gates[3 * C + tid] = R;
+      if constexpr (READ) {
+        decay::run_products<8>(d, w, L, R);
+        gates[4 * C + tid] = L, gates[5 * C + tid] = R;
+      }
+      if (t0 + C + tid < t_live) ahead.load(p.gates, b, h, t0 + C + tid);
+    }
+    copies_left(std::integral_constant<int, 2>());   // (this chunk's K, and Q or V, are older)
+    __syncthreads();
+    const float *Ks = k_tile(c), *Vs = v_tile(c), *Qs = sm + at.q;
+    const float run0 = Ls[decay::kRun - 1], run1 = C == 64 ? Ls[C - 1] : 1.f;   // products of g over the runs
+    if constexpr (READ) {
+      const int m0 = 16 * (warp % MT), part = warp / MT, r0 = m0 + q8, i0 = m0 / 8;   // i0: the rows' run of 8
+      const int n_on = min(NQ, max(0, i0 + 2 - part * NQ));   // score tiles that are not wholly above the diagonal
+      float a[NQ][4] = {}, o[NO][4] = {};
+      const float *qa = Qs + r0 * ldk + 2 * t4, *kb = Ks + (8 * NQ * part + q8) * ldk + 2 * t4,
+                  *sb = Ss + 2 * t4 * LDS + 8 * NO * part + q8;
+      for (int kk = 0; kk < dk16; kk += 8) {
+        const float2 x0 = *reinterpret_cast<const float2*>(qa + kk), x1 = *reinterpret_cast<const float2*>(qa + 8 * ldk + kk);
+        const Part<ONE> qf[4] = {x0.x, x1.x, x0.y, x1.y};
+        Part<ONE> kf[NQ][2];
+#pragma unroll
+        for (int i = 0; i < NQ; ++i) {
+          const float2 w = *reinterpret_cast<const float2*>(kb + 8 * i * ldk + kk);
+          kf[i][0] = w.x, kf[i][1] = w.y;
+        }
+        products<NQ>(a, qf, kf, n_on);
+        Part<false> sf[NO][2];
+#pragma unroll
+        for (int i = 0; i < NO; ++i) sf[i][0] = sb[kk * LDS + 8 * i], sf[i][1] = sb[(kk + 1) * LDS + 8 * i];
+        products<NO>(o, qf, sf, NO);
+      }
+      // The weights, tile by tile from the diagonal backwards: a run of 8 is a tile's columns and half of its
+      // rows, so between runs a weight is L of the row, the products of the runs between and R of the column.
+      {
+        auto total = [&](int m) { return L8[8 * m + 7]; };
+        float f0 = L8[r0], f1 = L8[r0 + 8] * total(i0);
+        const float f1_near = L8[r0 + 8];
+        for (int m = i0 - 1; m >= NQ * (part + 1); --m) f0 *= total(m), f1 *= total(m);
+        // a run's own tile: s of the column times the decays between
+        auto own = [&](int run, float& x0, float& x1) {
+          float w0 = ss[8 * run + 2 * t4], w1 = ss[8 * run + 2 * t4 + 1];
+#pragma unroll
+          for (int m = 1; m < 8; ++m) {
+            const float d = gs[8 * run + m];
+            w0 *= m > 2 * t4 && m <= q8 ? d : 1.f;
+            w1 *= m > 2 * t4 + 1 && m <= q8 ? d : 1.f;
+          }
+          x0 = 2 * t4 <= q8 ? x0 * w0 : 0.f;
+          x1 = 2 * t4 + 1 <= q8 ? x1 * w1 : 0.f;
+        };
+#pragma unroll
+        for (int i = NQ - 1; i >= 0; --i) {
+          const int run = NQ * part + i;
+          if (run > i0 + 1) continue;
+          const float z0 = R8[8 * run + 2 * t4], z1 = R8[8 * run + 2 * t4 + 1];
+          if (run == i0 + 1) {
+            a[i][0] = a[i][1] = 0.f;
+            own(run, a[i][2], a[i][3]);
+          } else if (run == i0) {
+            own(run, a[i][0], a[i][1]);
+            a[i][2] *= f1_near * z0, a[i][3] *= f1_near * z1;
+          } else {
+            a[i][0] *= f0 * z0, a[i][1] *= f0 * z1, a[i][2] *= f1 * z0, a[i][3] *= f1 * z1;
+            f0 *= total(run), f1 *= total(run);
+          }
+          float* to = Ps + r0 * LDP + 8 * run + 2 * t4;
+          *reinterpret_cast<float2*>(to) = make_float2(a[i][0], a[i][1]);
+          *reinterpret_cast<float2*>(to + 8 * LDP) = make_float2(a[i][2], a[i][3]);
+        }
+      }
+      copies_left(std::integral_constant<int, 1>());   // V
+      __syncthreads();
+      fetch_q(c + 1);
+      const float f0 = (r0 < decay::kRun ? 1.f : run0) * Ls[r0], f1 = (r0 + 8 < decay::kRun ? 1.f : run0) * Ls[r0 + 8];
+#pragma unroll
+      for (int i = 0; i < NO; ++i) o[i][0] *= f0, o[i][1] *= f0, o[i][2] *= f1, o[i][3] *= f1;
+      const float *pa = Ps + r0 * LDP + t4, *vb = Vs + t4 * LDV + 8 * NO * part + q8;
+      for (int j = 0; j < m0 + 16; j += 8) {
+        const Part<false> pf[4] = {pa[j], pa[8 * LDP + j], pa[j + 4], pa[8 * LDP + j + 4]};
+        Part<ONE> vf[NO][2];
+#pragma unroll
+        for (int i = 0; i < NO; ++i) vf[i][0] = vb[j * LDV + 8 * i], vf[i][1] = vb[(j + 4) * LDV + 8 * i];
+        products<NO>(o, pf, vf, NO);
+      }
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const int r = r0 + 8 * half;
+        if (r >= n) continue;
+        TO* dst = y + (t0 + r) * g.y_t;
+#pragma unroll
+        for (int i = 0; i < NO; ++i) {
+          const int col = 8 * (NO * part + i) + 2 * t4;
+          float x0 = o[i][2 * half] * g.scale, x1 = o[i][2 * half + 1] * g.scale;
+          if (p.D) x0 = fmaf(skip, Vs[r * LDV + col], x0), x1 = fmaf(skip, Vs[r * LDV + col + 1], x1);
+          if (pairs && col < cols) {
+            if constexpr (sizeof(TO) == 4) *reinterpret_cast<float2*>(dst + col) = make_float2(x0, x1);
+            else *reinterpret_cast<uint32_t*>(dst + col) = pack_bf16(x0, x1);
+          } else {
+            if (col < cols) dst[col] = from_f32<TO>(x0);
+            if (col + 1 < cols) dst[col + 1] = from_f32<TO>(x1);
+          }
+        }
+      }
+    }
+    // S = (products of g) S + sum_j (weights to the chunk's end) k_j v_j
+    const float all = run0 * run1;
+    seg_total *= all;
+#pragma unroll
+    for (int i = 0; i < MI; ++i)
+#pragma unroll
+      for (int m = 0; m < 4; ++m)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) st[i][m][e] *= all;
+    const float *ka = Ks + t4 * ldk + srow + q8, *vb = Vs + t4 * LDV + scol + q8;
+#pragma unroll 2
+    for (int j = 0; j < C; j += 8) {
+      const float to_end = j < decay::kRun ? run1 : 1.f, w0 = Rs[j + t4] * to_end, w1 = Rs[j + t4 + 4] * to_end;
+      Part<ONE> vf[4][2];
+#pragma unroll
+      for (int m = 0; m < 4; ++m) vf[m][0] = vb[j * LDV + 8 * m], vf[m][1] = vb[(j + 4) * LDV + 8 * m];
+#pragma unroll
+      for (int i = 0; i < MI; ++i) {
+        if (srow + 64 * i >= dk16) continue;   // (a whole warp's)
+        const float* kr = ka + j * ldk + 64 * i;
+        const Part<false> kf[4] = {kr[0] * w0, kr[8] * w0, kr[4 * ldk] * w1, kr[4 * ldk + 8] * w1};
+        products<4>(st[i], kf, vf, 4);
+      }
+    }
+    if constexpr (READ)
+      if (t0 + C < t_live) publish();   // (Q S of this chunk is behind a barrier)
+  }
+  copies_left(std::integral_constant<int, 0>());
+  if constexpr (READ) {
+    for (int t = max(t_live, t_lo) + warp; t < t_hi; t += 8)   // read-outs past the row's length
+      for (int c = tid % 32; c < cols; c += 32) y[t * g.y_t + c] = from_f32<TO>(0.f);
+  }
+  float* dst = nullptr;
+  if constexpr (READ) {
+    if (s == g.nseg - 1 && p.S_out) dst = p.S_out + unit * sq;
+  } else {
+    dst = p.seg + ((size_t)unit * g.nseg + s + 1) * sq;
+    if (sl == 0 && tid == 0) p.seg_total[(size_t)unit * g.nseg + s] = seg_total;
+  }
+  if (dst) each_state([&](float& x, int r, int c) { if (r < g.d_k && c < cols) dst[(size_t)r * g.d_v + c0 + c] = x; });
+}
+
+template <typename TI, typename TO, int C, int MI>
+cudaError_t launch_split(const Geom& g, const Ptrs& p, cudaStream_t st) {
+  const unsigned units = (unsigned)(g.B * g.H);
+  auto go = [&](auto kern, int segments, bool read) {
+    const size_t smem = decay::split_smem(g.d_k, read);
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    return tc::launch_overlapped(kern, dim3(segments, g.slices, units), dim3(256), smem, st, g, p);
+  };
+  if (g.nseg > 1) {
+    cudaError_t e = go(k_scan_split<TI, TO, C, MI, false>, g.nseg - 1, false);
+    if (e == cudaSuccess) e = decay::scan_launch(g, p, st);
+    if (e != cudaSuccess) return e;
+  }
+  return go(k_scan_split<TI, TO, C, MI, true>, g.nseg, true);
+}
+template <typename TI, typename TO>
+cudaError_t launch_width(const Geom& g, const Ptrs& p, cudaStream_t st) {
+  static_assert(decay::split_tokens(64) == 64 && decay::split_tokens(128) == 32 && decay::split_tokens(256) == 32, "as launched");
+  if constexpr (sizeof(TI) == 4) {   // (bf16 keys up to 128 take the bf16 chunks)
+    if (g.d_k <= 64) return launch_split<TI, TO, 64, 1>(g, p, st);
+    if (g.d_k <= 128) return launch_split<TI, TO, 32, 2>(g, p, st);
+  }
+  return launch_split<TI, TO, 32, 4>(g, p, st);
+}
+
+}  // namespace
+
+namespace decay {
+
+size_t split_smem(int d_k, bool read) {
+  auto words = [&](auto c) { constexpr int C = decltype(c)::value; return read ? Tiles<C, true>(d_k).end : Tiles<C, false>(d_k).end; };
+  return (split_tokens(d_k) == 64 ? words(std::integral_constant<int, 64>()) : words(std::integral_constant<int, 32>())) * sizeof(float);
+}
+int split_blocks(int d_k, bool read) { return d_k <= 128 ? 2 : 1; }
+cudaError_t split_launch(const Geom& g, const Ptrs& p, bool bf16_in, bool bf16_out, cudaStream_t st) {
+  return bf16_in ? (bf16_out ? launch_width<bf16, bf16>(g, p, st) : launch_width<bf16, float>(g, p, st))
+                 : (bf16_out ? launch_width<float, bf16>(g, p, st) : launch_width<float, float>(g, p, st));
+}
+
+}  // namespace decay

@@ -80,7 +80,7 @@ struct Tiles {
     k = 0;
     v = 2 * C * ldk;
     gates = v + (READ ? 1 : 2) * C * LDV;
-    s = gates + 6 * C;
+    s = gates + (READ ? 6 : 4) * C;
     q = s + (READ ? dk16 * LDS : 0);
     p = q + (READ ? C * ldk : 0);
     end = p + (READ ? C * (C + 4) : 0);
@@ -89,7 +89,7 @@ struct Tiles {
 
 // MI: 16-row tiles of the state a warp (d_k <= 64 MI)
 template <typename TI, typename TO, int C, int MI, bool READ>
-__global__ void __launch_bounds__(256, MI <= 2 ? 2 : 1) k_scan_split(Geom g, Ptrs p) {
+__global__ void __launch_bounds__(256, MI == 1 && !READ ? 3 : MI <= 2 ? 2 : 1) k_scan_split(Geom g, Ptrs p) {
   constexpr bool ONE = sizeof(TI) == 2;
   constexpr int LDP = C + 4, MT = C / 16, NG = 8 / MT, NQ = C / 8 / NG, NO = SL / 8 / NG;
   extern __shared__ __align__(16) float sm[];
@@ -204,7 +204,8 @@ __global__ void __launch_bounds__(256, MI <= 2 ? 2 : 1) k_scan_split(Geom g, Ptr
     const float *Ks = k_tile(c), *Vs = v_tile(c), *Qs = sm + at.q;
     const float run0 = Ls[decay::kRun - 1], run1 = C == 64 ? Ls[C - 1] : 1.f;   // products of g over the runs
     if constexpr (READ) {
-      const int m0 = 16 * (warp % MT), part = warp / MT, r0 = m0 + q8, i0 = m0 / 8;   // i0: the rows' run of 8
+      // (the later rows have more score tiles and more of P V: a scheduler's two warps get rows from either end)
+      const int m0 = 16 * (warp < 4 ? warp % MT : MT - 1 - warp % MT), part = warp / MT, r0 = m0 + q8, i0 = m0 / 8;   // i0: the rows' run of 8
       const int n_on = min(NQ, max(0, i0 + 2 - part * NQ));   // score tiles that are not wholly above the diagonal
       float a[NQ][4] = {}, o[NO][4] = {};
       const float *qa = Qs + r0 * ldk + 2 * t4, *kb = Ks + (8 * NQ * part + q8) * ldk + 2 * t4,
@@ -373,7 +374,7 @@ size_t split_smem(int d_k, bool read) {
   auto words = [&](auto c) { constexpr int C = decltype(c)::value; return read ? Tiles<C, true>(d_k).end : Tiles<C, false>(d_k).end; };
   return (split_tokens(d_k) == 64 ? words(std::integral_constant<int, 64>()) : words(std::integral_constant<int, 32>())) * sizeof(float);
 }
-int split_blocks(int d_k, bool read) { return d_k <= 128 ? 2 : 1; }
+int split_blocks(int d_k, bool read) { return d_k <= 64 && !read ? 3 : d_k <= 128 ? 2 : 1; }
 cudaError_t split_launch(const Geom& g, const Ptrs& p, bool bf16_in, bool bf16_out, cudaStream_t st) {
   return bf16_in ? (bf16_out ? launch_width<bf16, bf16>(g, p, st) : launch_width<bf16, float>(g, p, st))
                  : (bf16_out ? launch_width<float, bf16>(g, p, st) : launch_width<float, float>(g, p, st));

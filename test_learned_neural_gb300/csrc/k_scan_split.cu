@@ -53,20 +53,17 @@ __device__ __forceinline__ void mma8(float* d, uint32_t a0, uint32_t a1, uint32_
 }
 // d[n] += a b[n], N tiles of 16 x 8 with 8 of the inner axis
 template <int N, bool A1, bool B1>
-__device__ __forceinline__ void products(float (*d)[4], const Part<A1>* a, const Part<B1> (*b)[2], int n_on) {
+__device__ __forceinline__ void products(float (*d)[4], const Part<A1>* a, const Part<B1> (*b)[2]) {
   if constexpr (!A1) {
 #pragma unroll
-    for (int n = 0; n < N; ++n)
-      if (n < n_on) mma8(d[n], a[0].lo, a[1].lo, a[2].lo, a[3].lo, b[n][0].hi, b[n][1].hi);
+    for (int n = 0; n < N; ++n) mma8(d[n], a[0].lo, a[1].lo, a[2].lo, a[3].lo, b[n][0].hi, b[n][1].hi);
   }
   if constexpr (!B1) {
 #pragma unroll
-    for (int n = 0; n < N; ++n)
-      if (n < n_on) mma8(d[n], a[0].hi, a[1].hi, a[2].hi, a[3].hi, b[n][0].lo, b[n][1].lo);
+    for (int n = 0; n < N; ++n) mma8(d[n], a[0].hi, a[1].hi, a[2].hi, a[3].hi, b[n][0].lo, b[n][1].lo);
   }
 #pragma unroll
-  for (int n = 0; n < N; ++n)
-    if (n < n_on) mma8(d[n], a[0].hi, a[1].hi, a[2].hi, a[3].hi, b[n][0].hi, b[n][1].hi);
+  for (int n = 0; n < N; ++n) mma8(d[n], a[0].hi, a[1].hi, a[2].hi, a[3].hi, b[n][0].hi, b[n][1].hi);
 }
 
 // Tiles, in words from the start of shared memory.  K twice and for the state pass V
@@ -80,7 +77,7 @@ struct Tiles {
     k = 0;
     v = 2 * C * ldk;
     gates = v + (READ ? 1 : 2) * C * LDV;
-    s = gates + (READ ? 6 : 4) * C;
+    s = gates + 2 * (READ ? 6 : 4) * C;
     q = s + (READ ? dk16 * LDS : 0);
     p = q + (READ ? C * ldk : 0);
     end = p + (READ ? C * (C + 4) : 0);
@@ -95,9 +92,6 @@ __global__ void __launch_bounds__(256, MI == 1 && !READ ? 3 : MI <= 2 ? 2 : 1) k
   extern __shared__ __align__(16) float sm[];
   const Tiles<C, READ> at(g.d_k);
   const int dk16 = rows_of(g.d_k), ldk = dk16 + 8;
-  // of C tokens: g, s; products to and behind a token in its run of 32 (L, R) and in its run of 8
-  float* const gates = sm + at.gates;
-  const float *gs = gates, *ss = gates + C, *Ls = gates + 2 * C, *Rs = gates + 3 * C, *L8 = gates + 4 * C, *R8 = gates + 5 * C;
   float *const Ss = sm + at.s, *const Ps = sm + at.p;
   const int s = blockIdx.x, sl = blockIdx.y, unit = blockIdx.z;
   const int b = unit / g.H, h = unit % g.H, tid = threadIdx.x, warp = tid / 32, q8 = tid % 32 / 4, t4 = tid % 4;
@@ -171,8 +165,26 @@ __global__ void __launch_bounds__(256, MI == 1 && !READ ? 3 : MI <= 2 ? 2 : 1) k
   };
   auto publish = [&] { each_state([&](float& x, int r, int c) { if (r < dk16) Ss[r * LDS + c] = x; }); };
   const decay::HeadGates head(p.gates, h);
-  decay::RawGates ahead;   // of this thread's token of the next chunk
+  // A chunk's arrays of C values: g, s, products to and behind a token in its run of 32 (L, R), the
+  // same in its run of 8.  By the first warps, a chunk ahead, the next one's gates in flight.
+  decay::RawGates ahead;
   if (tid < C && t_lo + tid < t_live) ahead.load(p.gates, b, h, t_lo + tid);
+  auto gates_of = [&](int c) { return sm + at.gates + (c & 1) * (READ ? 6 : 4) * C; };
+  auto make_gates = [&](int c) {
+    if (tid >= C) return;   // (whole warps)
+    const int t = t_lo + c * C + tid;
+    float *to = gates_of(c) + tid, d = 1.f, w = 0.f, L, R;
+    if (t < t_live) ahead.values(p.gates, head.bias, head.A, d, w);
+    to[0] = d, to[C] = w;
+    decay::run_products(d, w, L, R);
+    to[2 * C] = L, to[3 * C] = R;
+    if constexpr (READ) {
+      decay::run_products<8>(d, w, L, R);
+      to[4 * C] = L, to[5 * C] = R;
+    }
+    if (t + C < t_live) ahead.load(p.gates, b, h, t + C);
+  };
+  make_gates(0);
   if constexpr (READ) {
     const float* start = g.nseg > 1 ? p.seg + ((size_t)unit * g.nseg + s) * sq : p.S0 ? p.S0 + unit * sq : nullptr;
     if (start)
@@ -183,48 +195,42 @@ __global__ void __launch_bounds__(256, MI == 1 && !READ ? 3 : MI <= 2 ? 2 : 1) k
   const bool pairs = g.d_v % 2 == 0 && (uintptr_t)p.y % 8 == 0;   // (y's strides are multiples of d_v)
   for (int c = 0, t0 = t_lo; t0 < t_live; ++c, t0 += C) {
     const int n = min(C, t_live - t0);
-    __syncthreads();   // the last chunk's products are done, the state is in Ss
+    copies_left(std::integral_constant<int, 0>());
+    __syncthreads();   // this chunk's K, Q (V), gates and Ss are there, the last one's products are done
     if constexpr (READ) fetch_v(c);
     fetch_k(c + 1);
-    if constexpr (!READ) fetch_v(c + 1);
-    if (tid < C) {   // whole warps
-      float d = 1.f, w = 0.f, L, R;
-      if (tid < n) ahead.values(p.gates, head.bias, head.A, d, w);
-      gates[tid] = d, gates[C + tid] = w;
-      decay::run_products(d, w, L, R);
-      gates[2 * C + tid] = L, gates[3 * C + tid] = R;
-      if constexpr (READ) {
-        decay::run_products<8>(d, w, L, R);
-        gates[4 * C + tid] = L, gates[5 * C + tid] = R;
-      }
-      if (t0 + C + tid < t_live) ahead.load(p.gates, b, h, t0 + C + tid);
-    }
-    copies_left(std::integral_constant<int, 2>());   // (this chunk's K, and Q or V, are older)
-    __syncthreads();
+    if constexpr (!READ) fetch_v(c + 1), make_gates(c + 1);
+    const float *gs = gates_of(c), *ss = gs + C, *Ls = gs + 2 * C, *Rs = gs + 3 * C, *L8 = gs + 4 * C, *R8 = gs + 5 * C;
     const float *Ks = k_tile(c), *Vs = v_tile(c), *Qs = sm + at.q;
     const float run0 = Ls[decay::kRun - 1], run1 = C == 64 ? Ls[C - 1] : 1.f;   // products of g over the runs
     if constexpr (READ) {
       // (the later rows have more score tiles and more of P V: a scheduler's two warps get rows from either end)
       const int m0 = 16 * (warp < 4 ? warp % MT : MT - 1 - warp % MT), part = warp / MT, r0 = m0 + q8, i0 = m0 / 8;   // i0: the rows' run of 8
-      const int n_on = min(NQ, max(0, i0 + 2 - part * NQ));   // score tiles that are not wholly above the diagonal
+      const bool scores = NQ * part < i0 + 2;   // else this warp's lie above the diagonal
       float a[NQ][4] = {}, o[NO][4] = {};
       const float *qa = Qs + r0 * ldk + 2 * t4, *kb = Ks + (8 * NQ * part + q8) * ldk + 2 * t4,
                   *sb = Ss + 2 * t4 * LDS + 8 * NO * part + q8;
+      auto inner = [&](auto with_scores) {
       for (int kk = 0; kk < dk16; kk += 8) {
         const float2 x0 = *reinterpret_cast<const float2*>(qa + kk), x1 = *reinterpret_cast<const float2*>(qa + 8 * ldk + kk);
         const Part<ONE> qf[4] = {x0.x, x1.x, x0.y, x1.y};
+        if constexpr (decltype(with_scores)::value) {
         Part<ONE> kf[NQ][2];
 #pragma unroll
         for (int i = 0; i < NQ; ++i) {
           const float2 w = *reinterpret_cast<const float2*>(kb + 8 * i * ldk + kk);
           kf[i][0] = w.x, kf[i][1] = w.y;
         }
-        products<NQ>(a, qf, kf, n_on);
+        products<NQ>(a, qf, kf);
+        }
         Part<false> sf[NO][2];
 #pragma unroll
         for (int i = 0; i < NO; ++i) sf[i][0] = sb[kk * LDS + 8 * i], sf[i][1] = sb[(kk + 1) * LDS + 8 * i];
-        products<NO>(o, qf, sf, NO);
+        products<NO>(o, qf, sf);
       }
+      };
+      if (scores) inner(std::true_type());
+      else inner(std::false_type());
       // The weights, tile by tile from the diagonal backwards: a run of 8 is a tile's columns and half of its
       // rows, so between runs a weight is L of the row, the products of the runs between and R of the column.
       {
@@ -267,6 +273,7 @@ __global__ void __launch_bounds__(256, MI == 1 && !READ ? 3 : MI <= 2 ? 2 : 1) k
       copies_left(std::integral_constant<int, 1>());   // V
       __syncthreads();
       fetch_q(c + 1);
+      make_gates(c + 1);
       const float f0 = (r0 < decay::kRun ? 1.f : run0) * Ls[r0], f1 = (r0 + 8 < decay::kRun ? 1.f : run0) * Ls[r0 + 8];
 #pragma unroll
       for (int i = 0; i < NO; ++i) o[i][0] *= f0, o[i][1] *= f0, o[i][2] *= f1, o[i][3] *= f1;
@@ -276,7 +283,7 @@ __global__ void __launch_bounds__(256, MI == 1 && !READ ? 3 : MI <= 2 ? 2 : 1) k
         Part<ONE> vf[NO][2];
 #pragma unroll
         for (int i = 0; i < NO; ++i) vf[i][0] = vb[j * LDV + 8 * i], vf[i][1] = vb[(j + 4) * LDV + 8 * i];
-        products<NO>(o, pf, vf, NO);
+        products<NO>(o, pf, vf);
       }
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
@@ -319,7 +326,7 @@ __global__ void __launch_bounds__(256, MI == 1 && !READ ? 3 : MI <= 2 ? 2 : 1) k
         if (srow + 64 * i >= dk16) continue;   // (a whole warp's)
         const float* kr = ka + j * ldk + 64 * i;
         const Part<false> kf[4] = {kr[0] * w0, kr[8] * w0, kr[4 * ldk] * w1, kr[4 * ldk + 8] * w1};
-        products<4>(st[i], kf, vf, 4);
+        products<4>(st[i], kf, vf);
       }
     }
     if constexpr (READ)

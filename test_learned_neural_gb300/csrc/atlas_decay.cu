@@ -389,10 +389,9 @@ size_t chunk_smem(int d_k, bool read) {
 // 32768 tokens of 64 140 us / 157, of 136 432 / 748, of 256 851 / 916; 4 x 8 x 4096 of
 // 96 645 / 724; of 48 and 128 the same; 3 x 6 x 1501 of 64 75 / 71 (12 segments and
 // 24 cost the same by the formula).
-int chunk_blocks(int d_k, bool read, bool gated) {
-  const size_t fit = (228 * 1024) / ((gated ? decay::split_smem(d_k, read) : chunk_smem(d_k, read)) + 1024);
-  const size_t by_registers = gated ? decay::split_blocks(d_k, read) : chunk_tokens(d_k) == 64 ? 3 : 2;
-  return (int)std::min(by_registers, fit);
+int chunk_blocks(int d_k, bool read) {
+  const size_t fit = (228 * 1024) / (chunk_smem(d_k, read) + 1024);
+  return (int)std::min<size_t>(chunk_tokens(d_k) == 64 ? 3 : 2, fit);
 }
 
 struct Plan {
@@ -426,6 +425,31 @@ int best_segments(long long ctas, long long chunks, long long slots, long long s
   return (int)best;
 }
 
+// The same for the selective scan's split chunks (k_scan_split.cu), whose blocks share
+// an SM's tensor cores: `blocks` (`state_blocks`) on an SM at once, fewer of them
+// at (r + a fifth) / (1 + a fifth) of their rate; a state pass's chunk is 0.3 of one, the last chunk of a
+// segment but the row's last does without its state product (0.25), a block's start
+// and end take 0.25, the other two launches 0.7.  1 x 16 x 8192 of 64: 19 segments 123 us, 32 126, 64 120, 128 129;
+// 4 x 16 x 600: 1 70, 4 57, 10 47; 16 x 16 x 1024 of 128: 1 497, 2 573, 4 615.
+int split_segments(long long ctas, long long chunks, int blocks, int state_blocks, int more) {
+  const long long sms = (long long)more * sm_count();
+  auto waves = [&](long long n, int at_once) {
+    const long long b = (n + sms - 1) / sms, rest = b % at_once;
+    return (double)(b / at_once) + (rest ? (rest + 0.2 * at_once) / (1.2 * at_once) : 0.0);
+  };
+  long long best = 1;
+  double cost = 0;
+  for (long long n = 1; n <= std::min(chunks, 1024LL); ++n) {
+    const long long per = (chunks + n - 1) / n;
+    if (n > 1 && (chunks + per - 1) / per != n) continue;
+    const double c = n == 1 ? waves(ctas, blocks) * (per + 0.25)
+                            : waves(ctas * n, blocks) * per + 0.3 * waves(ctas * (n - 1), state_blocks) * (per + 0.25) + 0.7;
+    if (n == 1 || c < cost) best = n, cost = c;
+    if (ctas * n > 8 * blocks * sms) break;
+  }
+  return (int)best;
+}
+
 // The longest call that goes token by token.  Measured at 8, 64 and 1024 states,
 // token by token against in chunks (us), where the two cross:
 //   8 and 64 states (a block per SM, the chunks' launch and pipeline count)
@@ -437,7 +461,15 @@ int best_segments(long long ctas, long long chunks, long long slots, long long s
 //     tensor cores, d_k 64:   20 tokens 49 / 49,  32 tokens  70 / 49
 //     the others: 32 tokens 73 / 92 (fp32, d_k 64), 182 / 205 (tensor cores, d_k
 //     128), 188 / 361 (fp32, d_k 128)
-int most_step_tokens(const atlas_decay_config& c, long long ctas) {
+// The selective scan's split chunks (fp32; 8 to 1024 states): d_k 32 and 64 20 tokens 9-10 / 9-11 and
+// from 1024 states on 32 tokens 36-49 / 39-48; 96 and 128 8 tokens 9 / 9-10, 12 tokens 11-84 / 9-90;
+// 200 20 tokens 16-292 / 13-315.
+int most_step_tokens(const atlas_decay_config& c, long long units, bool gated) {
+  const long long ctas = units * ((c.d_v + kSlice - 1) / kSlice);
+  if (gated && (c.qkv_dtype == ATLAS_F32 || c.d_k > 128)) {
+    if (units > 65535) return 20;   // (the chunks' grid)
+    return c.d_k <= 64 ? (ctas > 4 * sm_count() ? 32 : 20) : c.d_k <= 128 ? 11 : 20;
+  }
   const bool tc = c.qkv_dtype == ATLAS_BF16 && c.d_k <= 128;
   if (ctas > sm_count()) return tc && c.d_k <= 64 ? 20 : 32;
   return tc && c.d_k <= 64 ? 5 : tc || c.d_k <= 64 ? 12 : 20;
@@ -451,7 +483,7 @@ Plan make_plan(const atlas_decay_config& c, int B, int T, bool aligned, bool gat
   pl.slices = (c.d_v + kSlice - 1) / kSlice;
   pl.nseg = 1;
   pl.seg = T;
-  if (T <= most_step_tokens(c, (long long)B * c.H * pl.slices)) {
+  if (T <= most_step_tokens(c, (long long)B * c.H, gated)) {
     pl.path = 0;
     pl.C = 1;
     return pl;
@@ -463,10 +495,13 @@ Plan make_plan(const atlas_decay_config& c, int B, int T, bool aligned, bool gat
   // CTAs that run at once; a fp32 chunk takes so long that starts hardly count
   // (twice as many in a selective scan's ragged batch: half of the segments lie past their rows' lengths,
   // as a rule, and end at once; 2 x 16 rows and heads of 0 and 8192 tokens, 128 x 64: 4 segments 143 us, 8 108)
-  const long long more = gated && ragged ? 2 : 1, slots = more * (tc ? 1 : chunk_blocks(c.d_k, true, gated)) * sm_count(),
-                  state_slots = more * (tc ? 1 : chunk_blocks(c.d_k, false, gated)) * sm_count();
-  const long long chunks = (T + pl.C - 1) / pl.C;
-  const long long n = best_segments((long long)B * c.H * pl.slices, chunks, slots, state_slots, tc ? 2 : 0.5);
+  const int more = gated && ragged ? 2 : 1;
+  const long long slots = (long long)more * (tc ? 1 : chunk_blocks(c.d_k, true)) * sm_count(),
+                  state_slots = (long long)more * (tc ? 1 : chunk_blocks(c.d_k, false)) * sm_count();
+  const long long ctas = (long long)B * c.H * pl.slices, chunks = (T + pl.C - 1) / pl.C;
+  const long long n = gated && !tc ? split_segments(ctas, chunks, decay::split_blocks(c.d_k, true),
+                                                    decay::split_blocks(c.d_k, false), more)
+                                   : best_segments(ctas, chunks, slots, state_slots, tc ? 2 : 0.5);
   pl.seg = (int)((chunks + n - 1) / n * pl.C);
   pl.nseg = (int)((T + pl.seg - 1) / pl.seg);
   if (pl.nseg > 1) pl.seg_bytes = round_256((size_t)B * c.H * pl.nseg * c.d_k * c.d_v * sizeof(float));
@@ -611,9 +646,9 @@ int decay::run(HandleBase* h, const atlas_decay_config& c, const atlas_decay_io&
   if (io.T > kMostTokens) return h->fail(ATLAS_ERR_UNSUPPORTED, "T > 2^30 is not supported");
   const long long ctas = (long long)io.B * c.H * ((c.d_v + kSlice - 1) / kSlice);
   if (ctas > 0x7fffffffLL) return h->fail(ATLAS_ERR_UNSUPPORTED, "B * H too large for one call");
-  if ((long long)io.B * c.H > 65535 && io.T > most_step_tokens(c, ctas))
-    return h->fail(ATLAS_ERR_UNSUPPORTED, "B * H > 65535 is supported for calls of at most %d tokens",
-                   most_step_tokens(c, ctas));
+  const int steps = most_step_tokens(c, (long long)io.B * c.H, x != nullptr);
+  if ((long long)io.B * c.H > 65535 && io.T > steps)
+    return h->fail(ATLAS_ERR_UNSUPPORTED, "B * H > 65535 is supported for calls of at most %d tokens", steps);
   // rows of wider ones: copies of whole 16-byte groups too
   const bool strides_ok = !x || (x->ld_qk % 8 == 0 && x->ld_v % 8 == 0);
   const Plan pl = make_plan(c, io.B, io.T, strides_ok && aligned16(io.q) && aligned16(io.k) && aligned16(io.v) && aligned16(io.y),

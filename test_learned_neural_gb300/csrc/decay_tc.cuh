@@ -15,11 +15,10 @@ cudaError_t ws_launch(const Geom& g, const Ptrs& p, bool y_bf16, int* status, cu
 // a selective scan with 64 < d_k <= 128 (k_scan_wide.cu)
 cudaError_t wide_launch(const Geom& g, const Ptrs& p, bool y_bf16, int* status, cudaStream_t st);
 
-// a selective scan's other chunks (k_scan_split.cu): their tokens, a block's shared
-// memory, and the launches; d_k <= 256
+// a selective scan's other chunks (k_scan_split.cu): their tokens, the blocks that an
+// SM holds, and the launches; d_k <= 256
 constexpr int split_tokens(int d_k) { return d_k <= 64 ? 64 : 32; }
-size_t split_smem(int d_k, bool read);
-int split_blocks(int d_k, bool read);   // that an SM has registers for
+int split_blocks(int d_k, bool read);
 cudaError_t split_launch(const Geom& g, const Ptrs& p, bool bf16_in, bool bf16_out, cudaStream_t st);
 
 // segment starts from the segments' own contributions (atlas_decay.cu)

@@ -2,9 +2,11 @@
 // (decay_common.cuh has the formulas): the products run on the tensor cores from
 // split operands.
 //
-// A value is the sum of its leading 11 bits and the next 11, both tf32 (mma.sync
-// takes those from registers); a product of two values is three products, the small
-// ones first, and what is left out is below 2^-20 of it.  bf16 values are one part.
+// A value is the sum of its leading 11 bits, rounded, and of the next 11, both tf32 (mma.sync
+// takes those from registers): all but its last bit.  A product of two values is three
+// products, the small ones first; what is left out, of either sign, is at most 2^-21 of it.
+// (Cutting the leading bits off instead leaves out up to 2^-19, always of the same sign: 2.5e-6
+// of sums of positive values.)  bf16 values are one part.
 // The fp32 pipes give 116 multiply-adds a clock of an SM, the tensor cores 497 of tf32, so
 // 166 of these, and a fragment feeds more of them: the fp32 loops in front of
 // this (the decay attention's) reach a third of their pipes.
@@ -41,7 +43,7 @@ struct Part {
   __device__ __forceinline__ Part(float x) {
     hi = __float_as_uint(x);
     if constexpr (!ONE) {
-      hi &= 0xffffe000u;
+      hi = (hi + 0x1000u) & 0xffffe000u;   // (a NaN stays one in lo at least)
       lo = __float_as_uint(x - __uint_as_float(hi)) & 0xffffe000u;
     }
   }
@@ -64,6 +66,27 @@ __device__ __forceinline__ void products(float (*d)[4], const Part<A1>* a, const
   }
 #pragma unroll
   for (int n = 0; n < N; ++n) mma8(d[n], a[0].hi, a[1].hi, a[2].hi, a[3].hi, b[n][0].hi, b[n][1].hi);
+}
+
+// Both at once, so that a sum's three products lie far apart.  dl, el: where the small
+// ones go.
+template <int N, int M, bool ONE>
+__device__ __forceinline__ void products(float (*d)[4], float (*e)[4], float (*dl)[4], float (*el)[4], const Part<ONE>* a,
+                                         const Part<ONE> (*b)[2], const Part<false> (*c)[2]) {
+  if constexpr (!ONE) {
+#pragma unroll
+    for (int n = 0; n < N; ++n) mma8(dl[n], a[0].lo, a[1].lo, a[2].lo, a[3].lo, b[n][0].hi, b[n][1].hi);
+#pragma unroll
+    for (int n = 0; n < M; ++n) mma8(el[n], a[0].lo, a[1].lo, a[2].lo, a[3].lo, c[n][0].hi, c[n][1].hi);
+#pragma unroll
+    for (int n = 0; n < N; ++n) mma8(dl[n], a[0].hi, a[1].hi, a[2].hi, a[3].hi, b[n][0].lo, b[n][1].lo);
+  }
+#pragma unroll
+  for (int n = 0; n < M; ++n) mma8(el[n], a[0].hi, a[1].hi, a[2].hi, a[3].hi, c[n][0].lo, c[n][1].lo);
+#pragma unroll
+  for (int n = 0; n < N; ++n) mma8(d[n], a[0].hi, a[1].hi, a[2].hi, a[3].hi, b[n][0].hi, b[n][1].hi);
+#pragma unroll
+  for (int n = 0; n < M; ++n) mma8(e[n], a[0].hi, a[1].hi, a[2].hi, a[3].hi, c[n][0].hi, c[n][1].hi);
 }
 
 // Tiles, in words from the start of shared memory.  K twice and for the state pass V
@@ -107,6 +130,7 @@ __global__ void __launch_bounds__(256, MI == 1 && !READ ? 3 : MI <= 2 ? 2 : 1) k
   const TI* v = (const TI*)p.v + b * g.v_b + h * g.v_h + c0;
   TO* y = (TO*)p.y + b * g.y_b + h * g.y_h + c0;
   const size_t sq = (size_t)g.d_k * g.d_v;
+  float* const S_out = READ && s == g.nseg - 1 && p.S_out ? p.S_out + unit * sq : nullptr;
 
   // A tile's C rows, 16 threads side by side per token, four values each; zeros past
   // the row's length and width.  fp32 rows that start on four values go by copies
@@ -207,30 +231,41 @@ __global__ void __launch_bounds__(256, MI == 1 && !READ ? 3 : MI <= 2 ? 2 : 1) k
       // (the later rows have more score tiles and more of P V: a scheduler's two warps get rows from either end)
       const int m0 = 16 * (warp < 4 ? warp % MT : MT - 1 - warp % MT), part = warp / MT, r0 = m0 + q8, i0 = m0 / 8;   // i0: the rows' run of 8
       const bool scores = NQ * part < i0 + 2;   // else this warp's lie above the diagonal
-      float a[NQ][4] = {}, o[NO][4] = {};
+      // An accumulator's additions cut the sum off, 2^-25 of it each time on average: for d_k
+      // > 128, of a long row of them, the small products have their own.
+      constexpr bool APART = MI == 4;
+      float a[NQ][4] = {}, o[NO][4] = {}, a_low[NQ][4] = {}, o_low[NO][4] = {};
       const float *qa = Qs + r0 * ldk + 2 * t4, *kb = Ks + (8 * NQ * part + q8) * ldk + 2 * t4,
                   *sb = Ss + 2 * t4 * LDS + 8 * NO * part + q8;
       auto inner = [&](auto with_scores) {
-      for (int kk = 0; kk < dk16; kk += 8) {
-        const float2 x0 = *reinterpret_cast<const float2*>(qa + kk), x1 = *reinterpret_cast<const float2*>(qa + 8 * ldk + kk);
-        const Part<ONE> qf[4] = {x0.x, x1.x, x0.y, x1.y};
-        if constexpr (decltype(with_scores)::value) {
-        Part<ONE> kf[NQ][2];
+        constexpr int N = decltype(with_scores)::value ? NQ : 0;
+        for (int kk = 0; kk < dk16; kk += 8) {
+          const float2 x0 = *reinterpret_cast<const float2*>(qa + kk), x1 = *reinterpret_cast<const float2*>(qa + 8 * ldk + kk);
+          const Part<ONE> qf[4] = {x0.x, x1.x, x0.y, x1.y};
+          Part<ONE> kf[NQ][2];
 #pragma unroll
-        for (int i = 0; i < NQ; ++i) {
-          const float2 w = *reinterpret_cast<const float2*>(kb + 8 * i * ldk + kk);
-          kf[i][0] = w.x, kf[i][1] = w.y;
-        }
-        products<NQ>(a, qf, kf);
-        }
-        Part<false> sf[NO][2];
+          for (int i = 0; i < N; ++i) {
+            const float2 w = *reinterpret_cast<const float2*>(kb + 8 * i * ldk + kk);
+            kf[i][0] = w.x, kf[i][1] = w.y;
+          }
+          Part<false> sf[NO][2];
 #pragma unroll
-        for (int i = 0; i < NO; ++i) sf[i][0] = sb[kk * LDS + 8 * i], sf[i][1] = sb[(kk + 1) * LDS + 8 * i];
-        products<NO>(o, qf, sf);
-      }
+          for (int i = 0; i < NO; ++i) sf[i][0] = sb[kk * LDS + 8 * i], sf[i][1] = sb[(kk + 1) * LDS + 8 * i];
+          if constexpr (APART) products<N, NO, ONE>(a, o, a_low, o_low, qf, kf, sf);
+          else products<N, NO, ONE>(a, o, a, o, qf, kf, sf);
+        }
       };
       if (scores) inner(std::true_type());
       else inner(std::false_type());
+      if constexpr (APART) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+#pragma unroll
+          for (int i = 0; i < NQ; ++i) a[i][e] += a_low[i][e];
+#pragma unroll
+          for (int i = 0; i < NO; ++i) o[i][e] += o_low[i][e];
+        }
+      }
       // The weights, tile by tile from the diagonal backwards: a run of 8 is a tile's columns and half of its
       // rows, so between runs a weight is L of the row, the products of the runs between and R of the column.
       {
@@ -278,6 +313,7 @@ __global__ void __launch_bounds__(256, MI == 1 && !READ ? 3 : MI <= 2 ? 2 : 1) k
 #pragma unroll
       for (int i = 0; i < NO; ++i) o[i][0] *= f0, o[i][1] *= f0, o[i][2] *= f1, o[i][3] *= f1;
       const float *pa = Ps + r0 * LDP + t4, *vb = Vs + t4 * LDV + 8 * NO * part + q8;
+#pragma unroll 2
       for (int j = 0; j < m0 + 16; j += 8) {
         const Part<false> pf[4] = {pa[j], pa[8 * LDP + j], pa[j + 4], pa[8 * LDP + j + 4]};
         Part<ONE> vf[NO][2];
@@ -305,6 +341,7 @@ __global__ void __launch_bounds__(256, MI == 1 && !READ ? 3 : MI <= 2 ? 2 : 1) k
         }
       }
     }
+    if (READ && t0 + C >= t_live && !S_out) break;   // no one takes the state at this segment's end
     // S = (products of g) S + sum_j (weights to the chunk's end) k_j v_j
     const float all = run0 * run1;
     seg_total *= all;
@@ -315,7 +352,7 @@ __global__ void __launch_bounds__(256, MI == 1 && !READ ? 3 : MI <= 2 ? 2 : 1) k
 #pragma unroll
         for (int e = 0; e < 4; ++e) st[i][m][e] *= all;
     const float *ka = Ks + t4 * ldk + srow + q8, *vb = Vs + t4 * LDV + scol + q8;
-#pragma unroll 2
+#pragma unroll 4
     for (int j = 0; j < C; j += 8) {
       const float to_end = j < decay::kRun ? run1 : 1.f, w0 = Rs[j + t4] * to_end, w1 = Rs[j + t4 + 4] * to_end;
       Part<ONE> vf[4][2];
@@ -337,21 +374,24 @@ __global__ void __launch_bounds__(256, MI == 1 && !READ ? 3 : MI <= 2 ? 2 : 1) k
     for (int t = max(t_live, t_lo) + warp; t < t_hi; t += 8)   // read-outs past the row's length
       for (int c = tid % 32; c < cols; c += 32) y[t * g.y_t + c] = from_f32<TO>(0.f);
   }
-  float* dst = nullptr;
-  if constexpr (READ) {
-    if (s == g.nseg - 1 && p.S_out) dst = p.S_out + unit * sq;
-  } else {
+  float* dst = S_out;
+  if constexpr (!READ) {
     dst = p.seg + ((size_t)unit * g.nseg + s + 1) * sq;
     if (sl == 0 && tid == 0) p.seg_total[(size_t)unit * g.nseg + s] = seg_total;
   }
   if (dst) each_state([&](float& x, int r, int c) { if (r < g.d_k && c < cols) dst[(size_t)r * g.d_v + c0 + c] = x; });
 }
 
+size_t split_smem(int d_k, bool read) {
+  auto words = [&](auto c) { constexpr int C = decltype(c)::value; return read ? Tiles<C, true>(d_k).end : Tiles<C, false>(d_k).end; };
+  return (decay::split_tokens(d_k) == 64 ? words(std::integral_constant<int, 64>()) : words(std::integral_constant<int, 32>())) * sizeof(float);
+}
+
 template <typename TI, typename TO, int C, int MI>
 cudaError_t launch_split(const Geom& g, const Ptrs& p, cudaStream_t st) {
   const unsigned units = (unsigned)(g.B * g.H);
   auto go = [&](auto kern, int segments, bool read) {
-    const size_t smem = decay::split_smem(g.d_k, read);
+    const size_t smem = split_smem(g.d_k, read);
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     return tc::launch_overlapped(kern, dim3(segments, g.slices, units), dim3(256), smem, st, g, p);
@@ -377,10 +417,7 @@ cudaError_t launch_width(const Geom& g, const Ptrs& p, cudaStream_t st) {
 
 namespace decay {
 
-size_t split_smem(int d_k, bool read) {
-  auto words = [&](auto c) { constexpr int C = decltype(c)::value; return read ? Tiles<C, true>(d_k).end : Tiles<C, false>(d_k).end; };
-  return (split_tokens(d_k) == 64 ? words(std::integral_constant<int, 64>()) : words(std::integral_constant<int, 32>())) * sizeof(float);
-}
+// (three by registers, two or one by shared memory too)
 int split_blocks(int d_k, bool read) { return d_k <= 64 && !read ? 3 : d_k <= 128 ? 2 : 1; }
 cudaError_t split_launch(const Geom& g, const Ptrs& p, bool bf16_in, bool bf16_out, cudaStream_t st) {
   return bf16_in ? (bf16_out ? launch_width<bf16, bf16>(g, p, st) : launch_width<bf16, float>(g, p, st))

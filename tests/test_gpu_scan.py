@@ -302,3 +302,31 @@ def test_scans_of_two_handles_on_two_streams_at_once(gpu_lib):
         op.status()
         for out in many:
             assert all(torch.equal(out[n], ref[n]) for n in ref)
+
+
+@pytest.mark.parametrize("T", [21, 31, 32, 33, 63, 64, 65, 96, 200])
+@pytest.mark.parametrize("dtype,dk,dv", [("f32", 64, 64), ("f32", 16, 8), ("f32", 63, 31), ("f32", 65, 33), ("f32", 96, 66), ("f32", 128, 128),
+                                         ("f32", 129, 12), ("f32", 256, 64), ("bf16", 160, 64), ("bf16", 131, 70)])
+@pytest.mark.parametrize("state", [False, True])
+def test_scan_split_chunks_at_their_edges(gpu_lib, T, dtype, dk, dv, state):
+    """Chunks of 64 and 32 tokens from split operands: whole, a token less and more, with and without a state to
+    carry on; many units, so that a block takes several chunks."""
+    B = 1 if T < 64 else 80
+    t = _inputs(B, 4, T, dk, dv, dtype, "step" if dk % 2 else "memory", 2, "tokens", state=state, skip=state, seed=T + dk)
+    _check(t, 4, dk, dv, dtype, "f32", 2, "tokens", "heads")
+
+
+def test_scan_split_accuracy(gpu_lib):
+    """Two parts of 11 bits, the first one rounded: 2^-23 of a factor is cut off, 2^-22 of a product left out, 2^-21 of it
+    altogether.  A read-out has two such products in a row, so that sums without cancellation, positive values, come
+    within 2^-20, and another 2^-19 for the weights' products and the sums' roundings."""
+    import torch
+    for dk, T in ((64, 640), (128, 640), (256, 320)):
+        t = _inputs(2, 2, T, dk, 64, "f32", seed=9)
+        for n in ("q", "k", "v", "S0"):
+            t[n].abs_()
+        y, S = _ref(t)
+        out = _op(t, 2, dk, 64, "f32", "f32").forward(t)
+        for got, want in ((out["y"], y), (out["S"], S)):
+            worst = (np.abs(_host(got) - want) / want).max()
+            assert worst <= 2.0 ** -19 + 2.0 ** -20, (dk, worst)

@@ -25,16 +25,28 @@ struct Call {
 // before the current one stay in registers, so x is read once but for the K - 1
 // rows in front of a run, and A rows are in flight at a time.  Taps are a template
 // parameter, not padded with zeros: an infinity K tokens back would meet them.
-// Bound by memory: four channels a thread leave room for four blocks on an SM and
-// their loads (eight: 150 registers, one block, 42 us for 4 x 4096 x 1536 bf16).
+// Bound by issue slots and memory together: 60 instructions for a row's four channels (SiLU's two
+// special functions each among them), 58 % of the slots, at 4.0 TB/s.  Four channels a thread leave room
+// for three blocks on an SM (eight: 150 registers, one block, 42 us for 4 x 4096 x 1536 bf16).
 //
 // The thread of a sequence's first run is the only one that reads the cache (a
 // run is K - 1 tokens at least), and it writes the next one, so that one may be
 // the other.
-template <typename T, int K, int V, int ACT>
-__global__ void __launch_bounds__(256, K <= 4 ? 3 : 2) k_conv(Call c, const T* __restrict__ x, const T* cache,
-                                                              T* __restrict__ y, T* cache_out) {
-  constexpr int A = sizeof(T) == 2 ? 8 : 4;   // 64 bytes of a thread
+// RING: rows come by asynchronous copies, G groups of A ahead, into slots of shared memory
+// that are the thread's own (no barriers): more bytes in flight than registers have
+// room for.  In turn without, in runs of 16, and with: 4 x 4096 x 1536 bf16 26.7 / 25.1 us, fp32
+// 47.7 / 42.6; 8 x 4096 x 1024 of 8 taps 54.8 / 33.5; 1 x 4096 x 2048 12.1 / 11.9.
+constexpr int blocks_of(int K) { return K <= 4 ? 3 : 2; }   // on an SM
+template <typename T>
+constexpr int kAhead = sizeof(T) == 2 ? 8 : 4;   // A: 64 bytes of a thread
+constexpr int kGroups = 4;
+constexpr size_t kRingBytes = 256 * kGroups * 64;   // of a block
+
+template <typename T, int K, int V, int ACT, bool RING>
+__global__ void __launch_bounds__(256, blocks_of(K)) k_conv(Call c, const T* __restrict__ x, const T* cache,
+                                                           T* __restrict__ y, T* cache_out) {
+  constexpr int A = kAhead<T>, BYTES = V * (int)sizeof(T);
+  extern __shared__ __align__(16) uint8_t ring[];
   tc::grid_dependency_wait();
   tc::grid_dependents_launch();
   const size_t item = (size_t)blockIdx.x * 256 + threadIdx.x, rest = item / c.vecs;
@@ -47,6 +59,22 @@ __global__ void __launch_bounds__(256, K <= 4 ? 3 : 2) k_conv(Call c, const T* _
   const T* cb = cache ? cache + b * (K - 1) * c.C + ch : nullptr;
   T* yb = y + (b * c.T + t0) * c.C + ch;
   if (t0 < t_live) {
+    const T* src = xb + (size_t)t0 * c.ld_x;
+    const uint32_t slots = tc::smem_u32(ring) + threadIdx.x * BYTES;
+    // rows t .. t + A - 1 into their slots; a group, if an empty one
+    auto fetch = [&](int t) {
+#pragma unroll
+      for (int a = 0; a < A; ++a)
+        if (t + a < t_live)
+          asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(slots + ((t - t0 + a) % (kGroups * A)) * (256 * BYTES)),
+                       "l"(src + (size_t)(t - t0 + a) * c.ld_x), "n"(BYTES)
+                       : "memory");
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    if constexpr (RING) {
+#pragma unroll
+      for (int i = 0; i < kGroups; ++i) fetch(t0 + i * A);
+    }
     float w[V * K], bias[V], win[K][V];
     load_vec<(V == 1 ? 1 : V * K)>(c.w + (size_t)ch * K, w);
     if constexpr (V == 1) {
@@ -62,48 +90,59 @@ __global__ void __launch_bounds__(256, K <= 4 ? 3 : 2) k_conv(Call c, const T* _
 #pragma unroll
     for (int i = 0; i + 1 < K; ++i) {   // rows t0 - K + 1 + i
       const int t = t0 - K + 1 + i;
-      const T* src = t >= 0 ? xb + (size_t)t * c.ld_x : cb ? cb + (size_t)(t + K - 1) * c.C : nullptr;
-      if (src) {
-        load_vec<V>(src, win[i]);
+      const T* row = t >= 0 ? xb + (size_t)t * c.ld_x : cb ? cb + (size_t)(t + K - 1) * c.C : nullptr;
+      if (row) {
+        load_vec<V>(row, win[i]);
       } else {
 #pragma unroll
         for (int e = 0; e < V; ++e) win[i][e] = 0.f;
       }
     }
-    const T* src = xb + (size_t)t0 * c.ld_x;
     for (int t = t0; t < t_live; t += A) {
       Words<T, V> rows[A];
+      if constexpr (RING) {
+        asm volatile("cp.async.wait_group %0;" ::"n"(kGroups - 1) : "memory");
 #pragma unroll
-      for (int a = 0; a < A; ++a)
-        if (t + a < t_live) rows[a].load(src + a * c.ld_x);
-      src += A * c.ld_x;
+        for (int a = 0; a < A; ++a)
+          rows[a].load(reinterpret_cast<const T*>(ring + ((t - t0 + a) % (kGroups * A)) * (256 * BYTES) + threadIdx.x * BYTES));
+      } else {
 #pragma unroll
-      for (int a = 0; a < A; ++a) {
-        if (t + a >= t_live) break;
-        rows[a].values(win[K - 1]);
-        float o[V];
-        if constexpr (V == 1) {
-          o[0] = bias[0];
-#pragma unroll
-          for (int i = 0; i < K; ++i) o[0] = fmaf(w[i], win[i][0], o[0]);
-        } else {   // pairs of channels, one instruction for two
-#pragma unroll
-          for (int e = 0; e < V; e += 2) {
-            uint64_t s = linear::pack2(bias[e], bias[e + 1]);
-#pragma unroll
-            for (int i = 0; i < K; ++i)
-              s = linear::fma2(linear::pack2(w[e * K + i], w[(e + 1) * K + i]), linear::pack2(win[i][e], win[i][e + 1]), s);
-            linear::unpack2(s, o[e], o[e + 1]);
-          }
-        }
-        linear::act_all<ACT, T, V>(o);
-        store_vec<V>(yb, o);
-        yb += c.C;
-#pragma unroll
-        for (int i = 0; i + 1 < K; ++i)
-#pragma unroll
-          for (int e = 0; e < V; ++e) win[i][e] = win[i + 1][e];
+        for (int a = 0; a < A; ++a)
+          if (t + a < t_live) rows[a].load(src + a * c.ld_x);
+        src += A * c.ld_x;
       }
+      auto group = [&](int rows_on) {   // (A of them, as a rule: no tests then)
+#pragma unroll
+        for (int a = 0; a < A; ++a) {
+          if (a >= rows_on) break;
+          rows[a].values(win[K - 1]);
+          float o[V];
+          if constexpr (V == 1) {
+            o[0] = bias[0];
+#pragma unroll
+            for (int i = 0; i < K; ++i) o[0] = fmaf(w[i], win[i][0], o[0]);
+          } else {   // pairs of channels, one instruction for two
+#pragma unroll
+            for (int e = 0; e < V; e += 2) {
+              uint64_t s = linear::pack2(bias[e], bias[e + 1]);
+#pragma unroll
+              for (int i = 0; i < K; ++i)
+                s = linear::fma2(linear::pack2(w[e * K + i], w[(e + 1) * K + i]), linear::pack2(win[i][e], win[i][e + 1]), s);
+              linear::unpack2(s, o[e], o[e + 1]);
+            }
+          }
+          linear::act_all<ACT, T, V>(o);
+          store_vec<V>(yb, o);
+          yb += c.C;
+#pragma unroll
+          for (int i = 0; i + 1 < K; ++i)
+#pragma unroll
+            for (int e = 0; e < V; ++e) win[i][e] = win[i + 1][e];
+        }
+      };
+      if (t + A <= t_live) group(A);
+      else group(t_live - t);
+      if constexpr (RING) fetch(t + kGroups * A);   // (the slots' values have been used)
     }
   }
   float zero[V] = {};
@@ -128,20 +167,33 @@ template <typename T, int K>
 cudaError_t launch(Call c, const atlas_conv_io& io, bool vec, cudaStream_t st) {
   constexpr int V = 4;
   c.vecs = vec ? c.C / V : c.C;
-  c.run = std::min(c.T, std::max(16, K - 1));
+  // Runs of 16 tokens while those are one wave of blocks; else the ring, and one wave of runs of
+  // up to 128 tokens, or as many waves as it takes (of up to 64, 2 x 16384 x 1024 34.0 us against 30.6; in
+  // one wave however long, 16 x 16384 x 1024 207 against 192).
+  const long long threads = (long long)blocks_of(K) * sm_count() * 256, tokens = (long long)c.B * c.T;
+  const long long per = (tokens * c.vecs + threads - 1) / threads;   // of a thread, in one wave
+  const bool ring = vec && per > 16;
+  c.run = (int)std::min<long long>(c.T, ring ? (per + (per + 127) / 128 - 1) / ((per + 127) / 128) : 16);
   c.nseg = (c.T + c.run - 1) / c.run;
   const size_t blocks = ((size_t)c.B * c.nseg * c.vecs + 255) / 256;
   if (blocks > 0x7fffffffull) return cudaErrorInvalidConfiguration;
   auto go = [&](auto kern) {
-    return tc::launch_overlapped(kern, dim3((unsigned)blocks), dim3(256), 0, st, c, (const T*)io.x, (const T*)io.cache, (T*)io.y,
-                                 (T*)io.cache_out);
+    if (ring) {
+      const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kRingBytes);
+      if (e != cudaSuccess) return e;
+    }
+    return tc::launch_overlapped(kern, dim3((unsigned)blocks), dim3(256), ring ? kRingBytes : 0, st, c, (const T*)io.x,
+                                 (const T*)io.cache, (T*)io.y, (T*)io.cache_out);
   };
-  auto act = [&](auto v) {
+  auto act = [&](auto v, auto r) {
     constexpr int W = decltype(v)::value;
-    return c.act == ATLAS_ACT_SILU ? go(k_conv<T, K, W, ATLAS_ACT_SILU>)
-           : c.act == ATLAS_ACT_GELU ? go(k_conv<T, K, W, ATLAS_ACT_GELU>) : go(k_conv<T, K, W, ATLAS_ACT_NONE>);
+    constexpr bool R = decltype(r)::value;
+    return c.act == ATLAS_ACT_SILU ? go(k_conv<T, K, W, ATLAS_ACT_SILU, R>)
+           : c.act == ATLAS_ACT_GELU ? go(k_conv<T, K, W, ATLAS_ACT_GELU, R>) : go(k_conv<T, K, W, ATLAS_ACT_NONE, R>);
   };
-  return vec ? act(std::integral_constant<int, V>()) : act(std::integral_constant<int, 1>());
+  using Four = std::integral_constant<int, V>;
+  return ring ? act(Four(), std::true_type())
+         : vec ? act(Four(), std::false_type()) : act(std::integral_constant<int, 1>(), std::false_type());
 }
 template <typename T>
 cudaError_t launch_k(const Call& c, const atlas_conv_io& io, int K, bool vec, cudaStream_t st) {

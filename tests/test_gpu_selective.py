@@ -469,3 +469,24 @@ def test_products_of_two_handles_on_two_streams_at_once(gpu_lib):
     for (op, _, ref, _), many in zip(calls, outs):
         op.status()
         assert all(torch.equal(y, ref) for y in many)
+
+
+@pytest.mark.parametrize("B,T,C,K,dtype,extra", [(2, 1501, 2048, 4, "bf16", 8), (3, 777, 2560, 4, "f32", 4), (5, 2000, 1024, 8, "bf16", 0),
+                                                 (4, 1200, 2048, 2, "bf16", 0), (7, 900, 1024, 7, "f32", 0), (2, 3001, 2048, 1, "bf16", 0)])
+def test_conv_long_runs(gpu_lib, B, T, C, K, dtype, extra):
+    """Sizes whose rows go through the ring of copies: runs that end inside a group, ragged lengths (0, 1, 2, .. T), the cache
+    continued in place, NaN behind a length."""
+    import torch
+    from test_learned_neural_gb300.runner import ShortConv
+    t = _conv_case(B, T, C, K, dtype, extra, ragged=True)
+    for b, n in enumerate(t["lens"].tolist()):
+        t["x"][b, n:] = float("nan")
+    t["lens"][-1] = T - 5
+    t["x"][-1] = 0.5
+    ref = {n: a.clone() for n, a in t.items()}
+    op = ShortConv(C, K, "silu", dtype)
+    out = op.alloc_outputs(B, T, "cuda")
+    out["cache"].copy_(t["cache"])
+    t["cache"] = out["cache"]
+    op.forward(t, out=out)
+    _conv_check(ref, out, "silu", dtype)

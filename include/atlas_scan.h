@@ -28,7 +28,9 @@
  *
  * Execution, precision, capture: as in atlas_decay.h.  Products of decays are
  * formed by multiplying the decays themselves, in fp32, so that a decay of 0 (a
- * reset) is exact.
+ * reset) is exact.  Chunks of fp32 q, k, v (and of bf16 ones with d_k > 128) multiply
+ * pairs of tf32 parts: 22 bits of each factor, a product within 2^-21; a value within
+ * 2^-12 of the largest finite one counts as infinite there.
  *
  * Inputs: tokens past lens[b] are never used, whatever they and their gates hold.
  * A NaN or an infinity in a live token (its gates' products among them) reaches
@@ -105,7 +107,7 @@ size_t atlas_scan_workspace_bytes(const atlas_scan_handle* h, int B, int T);
  * outputs of that call are then not valid).  Clears the status word. */
 int atlas_scan_status(atlas_scan_handle* h);
 
-/* How the last forward on h ran: 0 = token by token, 1 = fp32 chunks, 2 =
+/* How the last forward on h ran: 0 = token by token, 1 = chunks of tf32 pairs, 2 =
  * tensor-core chunks, -1 = none yet. */
 int atlas_scan_last_path(const atlas_scan_handle* h);
 

@@ -172,7 +172,7 @@ cudaError_t launch(Call c, const atlas_conv_io& io, bool vec, cudaStream_t st) {
   // one wave however long, 16 x 16384 x 1024 207 against 192).
   const long long threads = (long long)blocks_of(K) * sm_count() * 256, tokens = (long long)c.B * c.T;
   const long long per = (tokens * c.vecs + threads - 1) / threads;   // of a thread, in one wave
-  const bool ring = vec && per > 16;
+  const bool ring = vec && per > 16 && c.T > 16;
   c.run = (int)std::min<long long>(c.T, ring ? (per + (per + 127) / 128 - 1) / ((per + 127) / 128) : 16);
   c.nseg = (c.T + c.run - 1) / c.run;
   const size_t blocks = ((size_t)c.B * c.nseg * c.vecs + 255) / 256;

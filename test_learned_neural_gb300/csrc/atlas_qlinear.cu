@@ -24,6 +24,7 @@
 #include <cuda_fp8.h>
 
 #include <algorithm>
+#include <atomic>
 #include <new>
 #include <type_traits>
 
@@ -37,7 +38,7 @@ namespace {
 constexpr int kWarps = 8, kThreads = 32 * (kWarps + 1);   // eight work, one loads
 constexpr int kCols = 128, kChunk = 128, kCodes = kCols * kChunk / 2;
 constexpr int kRowBytes = 320;   // of a chunk of a row of x in shared memory: 256, and no two rows of a pair in the same banks
-constexpr int kMostStages = 4;
+constexpr int kMostStages = 4, kMostShared = 226 * 1024;   // (227 KB, less the barriers')
 // rows of a call: row blocks are the grid's second dimension
 int most_rows(int x_dtype) { return 65535 * (x_dtype == ATLAS_F32 ? 32 : 64); }
 
@@ -541,8 +542,17 @@ cudaError_t launch(Call c, const atlas_qlinear_io& io, cudaStream_t st) {
   c.stages = std::min(stages, c.turns);
   const size_t smem = std::max(c.stages * stage, sums);
   auto kern = c.s.group == 128 ? k_qlinear<X, MT, NT, 1> : c.s.group == 64 ? k_qlinear<X, MT, NT, 2> : k_qlinear<X, MT, NT, 4>;
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  // The kernel may have as much shared memory as there is; the driver is told once for each device (0.3 us of a call).
+  static std::atomic<uint64_t> told[5];   // by groups of a chunk: a bit for a device
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0ull;
+  if (!(told[c.s.groups()].load(std::memory_order_relaxed) & bit)) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostShared);
+    if (e != cudaSuccess) return e;
+    told[c.s.groups()].fetch_or(bit, std::memory_order_relaxed);
+  }
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
